@@ -395,6 +395,126 @@ PA_API pa_status pa_prefill_step(const pa_cache_desc* desc, const void* q, int64
 PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch, int32_t max_seqlen_q,
                                         int64_t num_tokens, int32_t max_context_len);
 
+/* ---------------------------------------------------------------------------
+ * A cache held in 4 bits.  The calls below stand beside their namesakes above:
+ * desc describes the heads, the pages and the type of q, k, v rows and outputs
+ * (fp32 or bf16); k_cache and v_cache hold 4-bit rows instead, and group_size
+ * (32, 64 or 128, at most head_dim) says how many dims share one scale.
+ *
+ * Values.  Each group of group_size consecutive dims of one (token, kv-head)
+ * keeps two float16 numbers s and c; a code u in 0..15 stands for
+ *     s * (16 + u) + c.
+ * With mn and mx the group's least and largest value (values beyond +-16384
+ * count as +-16384), s = float16((mx - mn) / 15), c = float16(mn - 16 s), and
+ * 16 + u is (x - c) / s rounded half to even and clamped to 16..31 (s = 0:
+ * u = 0).  The quotients are products with the fp32 numbers nearest to 1/15
+ * and 1/s; every step rounds to fp32.  A value so comes back within s / 2 plus
+ * the rounding of s and c (2^-11 of 31 s and of |c|).  A group with a NaN or an
+ * infinity comes back as NaN.
+ *
+ * Layout.  [num_pages, page_size] rows of pa_q4_row_bytes() bytes: head h's
+ * codes at byte h * head_dim / 2, two bytes for four consecutive dims (dim 0 in
+ * bits 6-9, dim 1 in bits 14, 15, 0, 1 from its lowest bit up, dim 2 in bits
+ * 2-5, dim 3 in bits 10-13 of the little-endian half word); then the groups'
+ * words (s in the low, c in the high half), padded to 16 bytes.  In each of the
+ * two parts, within blocks of up to 128 bytes, the 16-byte piece j of the row
+ * in slot t lies at piece j XOR (t mod the block's pieces).  Whole pages can be
+ * copied; a row keeps its meaning only at the same offset in its page, modulo 8.
+ * Caches must be 16-byte aligned and need no initialisation.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of one token's row of a 4-bit K or V cache (a multiple of 16), or 0
+ * when the descriptor or the group size is not supported.  A cache has
+ * num_pages * page_size such rows. */
+PA_API int64_t pa_q4_row_bytes(const pa_cache_desc* desc, int32_t group_size);
+
+/*
+ * pa_kv_write_q4 -- pa_kv_write into a 4-bit cache: row t of k (v) is quantised
+ * into slot slot_mapping[t]; slot -1 stores nothing, other slots outside the
+ * cache are skipped and flagged.  Arguments as pa_kv_write.  A slot must not
+ * occur twice in one call: its row could mix the codes of one token with the
+ * scales of another.
+ */
+PA_API pa_status pa_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* k, int64_t k_row_stride,
+                                const void* v, int64_t v_row_stride, int64_t num_tokens, const int64_t* slot_mapping,
+                                void* k_cache, void* v_cache, pa_stream_t stream);
+
+/*
+ * pa_qk_norm_rope_kv_write_q4, pa_prefill_qk_norm_rope_kv_write_q4 -- the norm /
+ * rotary writes into a 4-bit cache: q_out and the optional outputs are theirs,
+ * and the cache rows are those pa_kv_write_q4 makes of the normed, rotated k
+ * (rounded to the dtype) and of v, bit for bit.  Arguments as
+ * pa_qk_norm_rope_kv_write and pa_prefill_qk_norm_rope_kv_write.
+ */
+PA_API pa_status pa_qk_norm_rope_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q,
+                                             int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                                             int64_t v_row_stride, int64_t num_tokens, const int32_t* positions,
+                                             const void* q_norm_w, const void* k_norm_w, float eps, float rope_theta,
+                                             const int64_t* slot_mapping, void* q_out, void* k_cache, void* v_cache,
+                                             pa_stream_t stream);
+PA_API pa_status pa_prefill_qk_norm_rope_kv_write_q4(
+    const pa_cache_desc* desc, int32_t group_size, const void* q, int64_t q_row_stride, const void* k,
+    int64_t k_row_stride, const void* v, int64_t v_row_stride, int64_t num_tokens, const int32_t* cu_seqlens_q,
+    int32_t batch, const int32_t* context_lens, const int32_t* block_tables, int32_t max_pages_per_seq,
+    const void* q_norm_w, const void* k_norm_w, float eps, float rope_theta, void* q_out, void* k_cache,
+    void* v_cache, int32_t* positions_out, int64_t* slot_mapping_out, pa_stream_t stream);
+
+/*
+ * pa_kv_read_q4 -- read tokens of a 4-bit cache back as rows of desc's dtype
+ * (each value rounded once).
+ *
+ * Request b's rows are cu_rows[b] .. cu_rows[b+1]-1 of k_out and v_out, and
+ * take its tokens starts[b], starts[b] + 1, ... in order.  Rows past the
+ * request's last token (context_lens[b]), rows of a padding request
+ * (context_lens[b] == 0) and rows from cu_rows[batch] on are left as they are.
+ * With cu_rows stepping by whole pages, k_out and v_out are a paged cache of
+ * desc's dtype, request b's pages following each other from cu_rows[b] /
+ * page_size: what pa_prefill_varlen attends to.
+ *
+ *   cu_rows          int32 [batch+1], 0 = cu[0] <= cu[1] <= ...
+ *   starts           int32 [batch], each >= 0, or NULL: every request from token 0.
+ *   num_rows         rows of k_out and v_out (host).
+ *   k_out, v_out     rows at k_row_stride / v_row_stride (elements, >=
+ *                    num_kv_heads*head_dim, multiples of 16 bytes).
+ * A negative start or a length beyond the tables skips the request's rows
+ * (PA_DEVERR_BAD_LENGTH), a bad table entry the rows of its page
+ * (PA_DEVERR_BAD_PAGE).
+ */
+PA_API pa_status pa_kv_read_q4(const pa_cache_desc* desc, int32_t group_size, int32_t batch, const int32_t* cu_rows,
+                               const int32_t* starts, const int32_t* context_lens, const int32_t* block_tables,
+                               int32_t max_pages_per_seq, int64_t num_rows, const void* k_cache, const void* v_cache,
+                               void* k_out, int64_t k_row_stride, void* v_out, int64_t v_row_stride,
+                               pa_stream_t stream);
+
+/* Bytes of device workspace pa_decode_q4 and pa_decode_kv_write_q4 need; as
+ * pa_decode_workspace_size. */
+PA_API size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t group_size, int32_t batch,
+                                          int32_t max_context_len, int32_t max_ctas);
+
+/*
+ * pa_decode_q4 -- pa_decode over a 4-bit cache.  Arguments, padding rows, flags
+ * and the split over CTAs as pa_decode.  q and out are device memory.
+ */
+PA_API pa_status pa_decode_q4(const pa_cache_desc* desc, int32_t group_size, const void* q, int32_t batch,
+                              const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                              int32_t max_pages_per_seq, const int32_t* context_lens, int32_t max_context_len,
+                              float scale, int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes,
+                              pa_stream_t stream);
+
+/*
+ * pa_decode_kv_write_q4 -- pa_decode_kv_write over a 4-bit cache: the new row is
+ * quantised, stored and attended to as stored, by the CTA that ends its
+ * request.  Equal to pa_slot_mapping + pa_kv_write_q4 + pa_decode_q4, bit for
+ * bit in the cache and the output.  Arguments as pa_decode_kv_write.
+ */
+PA_API pa_status pa_decode_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q,
+                                       const void* k_new, int64_t k_row_stride, const void* v_new,
+                                       int64_t v_row_stride, int32_t batch, void* k_cache, void* v_cache,
+                                       const int32_t* block_tables, int32_t max_pages_per_seq,
+                                       const int32_t* context_lens, int32_t max_context_len, float scale,
+                                       int32_t max_ctas, int64_t* slot_mapping, void* out, void* workspace,
+                                       size_t workspace_bytes, pa_stream_t stream);
+
 /*
  * pa_validate_metadata -- opt-in device check of the metadata the other calls
  * trust.  Counts, into *error_count (device int32, overwritten), the requests

@@ -91,6 +91,18 @@ _SIGS = {
     "pa_prefill_step": (_I32, [_DESC, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _I32, _I32, _VP, _I32, _VP, _I32,
                                _VP, _VP, _F32, _F32, _F32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "pa_prefill_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I64, _I32]),
+    "pa_q4_row_bytes": (_I64, [_DESC, _I32]),
+    "pa_kv_write_q4": (_I32, [_DESC, _I32, _VP, _I64, _VP, _I64, _I64, _VP, _VP, _VP, _VP]),
+    "pa_qk_norm_rope_kv_write_q4": (_I32, [_DESC, _I32, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _VP, _VP, _F32,
+                                           _F32, _VP, _VP, _VP, _VP, _VP]),
+    "pa_prefill_qk_norm_rope_kv_write_q4": (_I32, [_DESC, _I32, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _I32, _VP,
+                                                   _VP, _I32, _VP, _VP, _F32, _F32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "pa_kv_read_q4": (_I32, [_DESC, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP]),
+    "pa_decode_q4_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _I32]),
+    "pa_decode_q4": (_I32, [_DESC, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _F32, _I32, _VP, _VP,
+                            ctypes.c_size_t, _VP]),
+    "pa_decode_kv_write_q4": (_I32, [_DESC, _I32, _VP, _VP, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _I32, _VP, _I32,
+                                     _F32, _I32, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "pa_validate_metadata": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP]),
     "pa_selftest_bounded_wait": (_I32, [_I32, _VP]),
     "pa_read_device_errors": (_I32, [ctypes.POINTER(ctypes.c_uint32), _I32]),
@@ -267,6 +279,101 @@ def pa_prefill_step(desc, q, q_row_stride, k, k_row_stride, v, v_row_stride, num
 def pa_prefill_workspace_size(desc, batch, max_seqlen_q, num_tokens, max_context_len) -> int:
     return int(load_library().pa_prefill_workspace_size(ctypes.byref(desc), batch, max_seqlen_q, num_tokens,
                                                         max_context_len))
+
+
+def pa_q4_row_bytes(desc, group_size) -> int:
+    """Bytes of one token's row of a 4-bit K or V cache (0: not supported)."""
+    return int(load_library().pa_q4_row_bytes(ctypes.byref(desc), group_size))
+
+
+def _q4_caches(fn, desc, group_size, *caches):
+    """A 4-bit cache given as a tensor is contiguous uint8 on the current device and holds every row of the
+    descriptor: a cache of the dtype's rows, or one allocated for another group size, is refused here."""
+    row = load_library().pa_q4_row_bytes(ctypes.byref(desc), group_size)
+    need = desc.num_pages * desc.page_size * row
+    for t in caches:
+        if not isinstance(t, torch.Tensor):
+            continue
+        if t.dtype != torch.uint8:
+            raise PagedAttnError(fn, PA_ERR_DTYPE, f"a 4-bit cache is a uint8 tensor, not {t.dtype}")
+        if not t.is_contiguous() or t.numel() < need:
+            raise PagedAttnError(fn, PA_ERR_SHAPE, f"a 4-bit cache is contiguous and has at least {need} bytes")
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise PagedAttnError(fn, PA_ERR_UNSUPPORTED, f"the cache is on {t.device}, not on the current CUDA device")
+
+
+def pa_kv_write_q4(desc, group_size, k, k_row_stride, v, v_row_stride, num_tokens, slot_mapping, k_cache, v_cache,
+                   stream=None):
+    lib = load_library()
+    _q4_caches("pa_kv_write_q4", desc, group_size, k_cache, v_cache)
+    _check("pa_kv_write_q4", lib.pa_kv_write_q4(
+        ctypes.byref(desc), group_size, _ptr(k), k_row_stride, _ptr(v), v_row_stride, num_tokens, _ptr(slot_mapping),
+        _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+
+
+def pa_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens,
+                                positions, q_norm_w, k_norm_w, eps, rope_theta, slot_mapping, q_out, k_cache, v_cache,
+                                stream=None):
+    lib = load_library()
+    _q4_caches("pa_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
+    _check("pa_qk_norm_rope_kv_write_q4", lib.pa_qk_norm_rope_kv_write_q4(
+        ctypes.byref(desc), group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+        num_tokens, _ptr(positions), _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(slot_mapping),
+        _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+
+
+def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride,
+                                        num_tokens, cu_seqlens_q, batch, context_lens, block_tables,
+                                        max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, q_out, k_cache,
+                                        v_cache, positions_out=None, slot_mapping_out=None, stream=None):
+    lib = load_library()
+    _q4_caches("pa_prefill_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
+    _check("pa_prefill_qk_norm_rope_kv_write_q4", lib.pa_prefill_qk_norm_rope_kv_write_q4(
+        ctypes.byref(desc), group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+        num_tokens, _ptr(cu_seqlens_q), batch, _ptr(context_lens), _ptr(block_tables), max_pages_per_seq,
+        _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+        _ptr(positions_out), _ptr(slot_mapping_out), _stream(stream)))
+
+
+def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_tables, max_pages_per_seq, num_rows,
+                  k_cache, v_cache, k_out, k_row_stride, v_out, v_row_stride, stream=None):
+    """Read tokens of a 4-bit cache back as rows of the descriptor's dtype; ``starts`` may be None (token 0)."""
+    lib = load_library()
+    _q4_caches("pa_kv_read_q4", desc, group_size, k_cache, v_cache)
+    _check("pa_kv_read_q4", lib.pa_kv_read_q4(
+        ctypes.byref(desc), group_size, batch, _ptr(cu_rows), _ptr(starts), _ptr(context_lens), _ptr(block_tables),
+        max_pages_per_seq, num_rows, _ptr(k_cache), _ptr(v_cache), _ptr(k_out), k_row_stride, _ptr(v_out),
+        v_row_stride, _stream(stream)))
+
+
+def pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas=0) -> int:
+    return int(load_library().pa_decode_q4_workspace_size(ctypes.byref(desc), group_size, batch, max_context_len,
+                                                          max_ctas))
+
+
+def pa_decode_q4(desc, group_size, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
+                 max_context_len, scale, max_ctas, out, workspace, workspace_bytes=None, stream=None):
+    lib = load_library()
+    _q4_caches("pa_decode_q4", desc, group_size, k_cache, v_cache)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("pa_decode_q4", lib.pa_decode_q4(
+        ctypes.byref(desc), group_size, _ptr(q), batch, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        max_pages_per_seq, _ptr(context_lens), max_context_len, scale, max_ctas, _ptr(out), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row_stride, batch, k_cache, v_cache,
+                          block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas,
+                          slot_mapping, out, workspace, workspace_bytes=None, stream=None):
+    lib = load_library()
+    _q4_caches("pa_decode_kv_write_q4", desc, group_size, k_cache, v_cache)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("pa_decode_kv_write_q4", lib.pa_decode_kv_write_q4(
+        ctypes.byref(desc), group_size, _ptr(q), _ptr(k_new), k_row_stride, _ptr(v_new), v_row_stride, batch,
+        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_pages_per_seq, _ptr(context_lens), max_context_len,
+        scale, max_ctas, _ptr(slot_mapping), _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,

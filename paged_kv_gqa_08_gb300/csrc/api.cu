@@ -287,6 +287,26 @@ pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* 
   return PA_OK;
 }
 
+// The descriptor and group size of a 4-bit cache.
+pa_status check_q4(const pa_cache_desc* d, int32_t group_size) {
+  pa_status st = check_desc(d);
+  if (st != PA_OK) return st;
+  if (group_size != 32 && group_size != 64 && group_size != 128) return PA_ERR_UNSUPPORTED;
+  if (group_size > d->head_dim) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// pa_decode_q4's and pa_decode_kv_write_q4's plan, once their arguments are checked.
+pa_status plan_q4(const pa_cache_desc* desc, int32_t gs, int32_t batch, int32_t max_context_len, int32_t max_ctas,
+                  const void* workspace, size_t workspace_bytes, DecodePlan* pl) {
+  if (!workspace) return PA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_ALIGN;
+  cudaError_t e = plan_decode_q4(*desc, gs, batch, max_context_len, max_ctas, pl);
+  if (e == cudaErrorInvalidValue) return PA_ERR_UNSUPPORTED;
+  if (e != cudaSuccess) return cuda_fail(e);
+  return workspace_bytes < pl->ws_bytes ? PA_ERR_WORKSPACE : PA_OK;
+}
+
 cudaError_t launch_prefill(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
   return d.dtype == PA_BF16 && d.head_dim == 128 ? launch_prefill_tc(d, a, s) : launch_prefill_simt(d, a, s);
 }
@@ -550,6 +570,203 @@ pa_status pa_prefill_step(const pa_cache_desc* desc, const void* q, int64_t q_ro
   a.err = err;
   a.planner_beside_write = true;
   e = launch_prefill(*desc, a, s);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+int64_t pa_q4_row_bytes(const pa_cache_desc* desc, int32_t group_size) {
+  return check_q4(desc, group_size) == PA_OK ? q4_row_bytes(*desc, group_size) : 0;
+}
+
+pa_status pa_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* k, int64_t k_row_stride,
+                         const void* v, int64_t v_row_stride, int64_t num_tokens, const int64_t* slot_mapping,
+                         void* k_cache, void* v_cache, pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  KvWriteParams kp;
+  st = kv_write_params(desc, k, k_row_stride, v, v_row_stride, num_tokens, slot_mapping, k_cache, v_cache, &kp);
+  if (st != PA_OK) return st;
+  Q4WriteParams p{};
+  p.k = kp.k;
+  p.v = kp.v;
+  p.k_stride_bytes = kp.k_stride_bytes;
+  p.v_stride_bytes = kp.v_stride_bytes;
+  p.n_tokens = num_tokens;
+  p.slots = slot_mapping;
+  p.k_cache = kp.k_cache;
+  p.v_cache = kp.v_cache;
+  p.num_slots = kp.num_slots;
+  p.row_bytes = q4_row_bytes(*desc, group_size);
+  p.hkv = desc->num_kv_heads;
+  if ((st = prepare(&p.err)) != PA_OK) return st;
+  cudaError_t e = launch_kv_write_q4(*desc, group_size, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_qk_norm_rope_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q,
+                                      int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                                      int64_t v_row_stride, int64_t num_tokens, const int32_t* positions,
+                                      const void* q_norm_w, const void* k_norm_w, float eps, float rope_theta,
+                                      const int64_t* slot_mapping, void* q_out, void* k_cache, void* v_cache,
+                                      pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  NormRopeParams p;
+  st = norm_rope_params(desc, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens, q_norm_w, k_norm_w, eps,
+                        rope_theta, q_out, k_cache, v_cache, &p);
+  if (st != PA_OK) return st;
+  if (!positions || !slot_mapping) return PA_ERR_NULL;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.q4_group_size = group_size;
+  p.q4_row_bytes = q4_row_bytes(*desc, group_size);
+  if ((st = prepare(&p.err)) != PA_OK) return st;
+  cudaError_t e = launch_norm_rope_kv_write(desc->dtype, desc->head_dim, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_prefill_qk_norm_rope_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q,
+                                              int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                              const void* v, int64_t v_row_stride, int64_t num_tokens,
+                                              const int32_t* cu_seqlens_q, int32_t batch, const int32_t* context_lens,
+                                              const int32_t* block_tables, int32_t max_pages_per_seq,
+                                              const void* q_norm_w, const void* k_norm_w, float eps, float rope_theta,
+                                              void* q_out, void* k_cache, void* v_cache, int32_t* positions_out,
+                                              int64_t* slot_mapping_out, pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || batch < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  NormRopeParams p;
+  st = prefill_norm_params(desc, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens, cu_seqlens_q, batch,
+                           context_lens, block_tables, max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, q_out,
+                           k_cache, v_cache, positions_out, slot_mapping_out, &p);
+  if (st != PA_OK) return st;
+  p.q4_group_size = group_size;
+  p.q4_row_bytes = q4_row_bytes(*desc, group_size);
+  if ((st = prepare(&p.err)) != PA_OK) return st;
+  cudaError_t e = launch_norm_rope_kv_write(desc->dtype, desc->head_dim, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_kv_read_q4(const pa_cache_desc* desc, int32_t group_size, int32_t batch, const int32_t* cu_rows,
+                        const int32_t* starts, const int32_t* context_lens, const int32_t* block_tables,
+                        int32_t max_pages_per_seq, int64_t num_rows, const void* k_cache, const void* v_cache,
+                        void* k_out, int64_t k_row_stride, void* v_out, int64_t v_row_stride, pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  if (batch < 0 || num_rows < 0 || num_rows > 0x7fffffff) return PA_ERR_SHAPE;
+  if (num_rows == 0) return PA_OK;
+  if (batch == 0 || max_pages_per_seq < 1) return PA_ERR_SHAPE;
+  if (!cu_rows || !context_lens || !block_tables || !k_cache || !v_cache || !k_out || !v_out) return PA_ERR_NULL;
+  const int64_t re = row_elems(desc);
+  if (k_row_stride < re || v_row_stride < re) return PA_ERR_SHAPE;
+  if (!stride_ok(desc, k_row_stride, re) || !stride_ok(desc, v_row_stride, re)) return PA_ERR_ALIGN;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out)) return PA_ERR_ALIGN;
+  const int E = elem_bytes(desc->dtype);
+  Q4ReadParams p{};
+  p.cu = cu_rows;
+  p.starts = starts;
+  p.ctx = context_lens;
+  p.bt = block_tables;
+  p.k_cache = static_cast<const char*>(k_cache);
+  p.v_cache = static_cast<const char*>(v_cache);
+  p.k_out = static_cast<char*>(k_out);
+  p.v_out = static_cast<char*>(v_out);
+  p.k_stride_bytes = k_row_stride * E;
+  p.v_stride_bytes = v_row_stride * E;
+  p.num_rows = num_rows;
+  p.num_pages = desc->num_pages;
+  p.batch = batch;
+  p.maxp = max_pages_per_seq;
+  while ((1 << p.log2P) < desc->page_size) ++p.log2P;
+  p.row_bytes = q4_row_bytes(*desc, group_size);
+  p.hkv = desc->num_kv_heads;
+  if ((st = prepare(&p.err)) != PA_OK) return st;
+  cudaError_t e = launch_kv_read_q4(*desc, group_size, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t group_size, int32_t batch,
+                                   int32_t max_context_len, int32_t max_ctas) {
+  if (check_q4(desc, group_size) != PA_OK || batch < 1 || max_context_len < 1 || max_ctas < 0) return 0;
+  DecodePlan pl;
+  if (plan_decode_q4(*desc, group_size, batch, max_context_len, max_ctas, &pl) != cudaSuccess) return 0;
+  return pl.ws_bytes;
+}
+
+pa_status pa_decode_q4(const pa_cache_desc* desc, int32_t group_size, const void* q, int32_t batch,
+                       const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                       int32_t max_pages_per_seq, const int32_t* context_lens, int32_t max_context_len, float scale,
+                       int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  st = check_decode_args(desc, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
+                         max_context_len, scale, max_ctas, out);
+  if (st != PA_OK || batch == 0) return st;
+  DecodePlan pl;
+  st = plan_q4(desc, group_size, batch, max_context_len, max_ctas, workspace, workspace_bytes, &pl);
+  if (st != PA_OK) return st;
+  DecodeArgs a{};
+  if ((st = prepare(&a.err)) != PA_OK) return st;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = out;
+  a.workspace = workspace;
+  a.batch = batch;
+  a.max_pages = max_pages_per_seq;
+  a.max_context_len = max_context_len;
+  a.scale = scale;
+  cudaError_t e = launch_decode_q4(*desc, group_size, pl, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_decode_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q, const void* k_new,
+                                int64_t k_row_stride, const void* v_new, int64_t v_row_stride, int32_t batch,
+                                void* k_cache, void* v_cache, const int32_t* block_tables, int32_t max_pages_per_seq,
+                                const int32_t* context_lens, int32_t max_context_len, float scale, int32_t max_ctas,
+                                int64_t* slot_mapping, void* out, void* workspace, size_t workspace_bytes,
+                                pa_stream_t stream) {
+  pa_status st = check_q4(desc, group_size);
+  if (st != PA_OK) return st;
+  st = check_decode_args(desc, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
+                         max_context_len, scale, max_ctas, out);
+  if (st != PA_OK || batch == 0) return st;
+  if (!k_new || !v_new) return PA_ERR_NULL;
+  const int64_t re = row_elems(desc);
+  if (k_row_stride < re || v_row_stride < re) return PA_ERR_SHAPE;
+  if (!stride_ok(desc, k_row_stride, re) || !stride_ok(desc, v_row_stride, re)) return PA_ERR_ALIGN;
+  if (!aligned16(k_new) || !aligned16(v_new)) return PA_ERR_ALIGN;
+  if (desc->num_pages * desc->page_size >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  DecodePlan pl;
+  st = plan_q4(desc, group_size, batch, max_context_len, max_ctas, workspace, workspace_bytes, &pl);
+  if (st != PA_OK) return st;
+  DecodeArgs a{};
+  if ((st = prepare(&a.err)) != PA_OK) return st;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = out;
+  a.workspace = workspace;
+  a.batch = batch;
+  a.max_pages = max_pages_per_seq;
+  a.max_context_len = max_context_len;
+  a.scale = scale;
+  const int E = elem_bytes(desc->dtype);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_new_stride_bytes = k_row_stride * E;
+  a.v_new_stride_bytes = v_row_stride * E;
+  a.slot_out = slot_mapping;
+  cudaError_t e = launch_decode_q4(*desc, group_size, pl, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,439 @@
+// Batched GQA decode attention over a 4-bit paged cache (sm_103a).
+//
+// The mathematics is decode.cu's with K and V rows that are decoded on the
+// way in (q4_common.cuh): the split of the keys over the CTAs, the partial
+// results and their merge are the same code (decode_shared.cuh).  A chunk is
+// 16 tokens of one page, one contiguous run of 16 rows of K and one of V; a
+// producer warp copies the runs of the cache as they are into a ring in shared
+// memory, and one consumer warp per kv-head decodes its head's part.
+#include "decode_shared.cuh"
+#include "q4_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTok = 16;     // tokens per chunk
+constexpr int kStagesQ4 = 4; // ring depth
+
+struct Q4Params {
+  KParams k;
+  int32_t codes, pars;  // bytes of the two parts of a row
+  int32_t log2gs;
+  uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
+};
+
+// The new token's K and V of kv-head h, quantised by the warp: into the chunk's
+// stage (row n - 1) and into the cache.  Every lane takes eight dims: K in the
+// lower lanes, V behind it.
+template <typename T, int HD>
+PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned char* vst, int b, int n, int slot, int h,
+                             int lane) {
+  constexpr int LPR = HD / 8;
+  const bool isv = (lane / LPR) & 1;
+  const int l = lane % LPR;
+  const char* src = (isv ? p.k.v_new + static_cast<int64_t>(b) * p.k.v_new_stride
+                         : p.k.k_new + static_cast<int64_t>(b) * p.k.k_new_stride) +
+                    (h * HD + l * 8) * sizeof(T);
+  float x[8];
+  q4_load8<T>(src, x);
+  const int gl = 1 << (p.log2gs - 3);
+  uint32_t par;
+  const uint32_t w = q4_quantise8(x, gl, par);
+  if (lane < 2 * LPR) {
+    const uint32_t t = static_cast<uint32_t>(n - 1);  // = slot mod 16
+    unsigned char* row = (isv ? vst : kst) + t * p.k.row_bytes;
+    char* dst = const_cast<char*>(isv ? p.k.v_cache : p.k.k_cache) + static_cast<int64_t>(slot) * p.k.row_bytes;
+    const uint32_t co = q4_swz(h * (HD / 2) + l * 4, p.codes, t);
+    *reinterpret_cast<uint32_t*>(row + co) = w;
+    *reinterpret_cast<uint32_t*>(dst + co) = w;
+    if ((l & (gl - 1)) == 0) {
+      const uint32_t po = p.codes + q4_swz((h * (HD >> p.log2gs) + ((l * 8) >> p.log2gs)) * 4, p.pars, t);
+      *reinterpret_cast<uint32_t*>(row + po) = par;
+      *reinterpret_cast<uint32_t*>(dst + po) = par;
+    }
+  }
+  // the fence orders these stores before the copies that refill the stage later
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core consumer: GP = the group's q-heads rounded up to a power of two.
+// Scores: lane (gq, tq) takes tokens gq and gq + 8 and a quarter of the dims.
+// Products with V: a lane takes HD / 32 dims of every token.
+// ---------------------------------------------------------------------------
+template <typename T, int HD, int GP>
+PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
+                             volatile int* abort_flag, int x0, int x1, int c) {
+  constexpr int QD = HD / 4;
+  constexpr int EL = HD / 32;
+  constexpr int NH = GP > 4 ? 2 : 1;  // heads whose softmax a lane keeps
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = warp, G = p.k.Hq / p.k.Hkv;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int R = p.k.row_bytes, NG = HD >> p.log2gs;
+  float* qs = reinterpret_cast<float*>(smem + p.off_q) + warp * GP * HD;
+  float* p_tile = reinterpret_cast<float*>(smem + p.k.off_p) + warp * kTok * GP;
+  float* alpha_s = reinterpret_cast<float*>(smem + p.k.off_alpha) + warp * 8;
+  float* ml_s = reinterpret_cast<float*>(smem + p.k.off_ml) + warp * 16;
+  float o[GP][EL];
+  float m_run[NH], l_part[NH];
+  for (int x = x0, it = 0; x < x1; ++x, ++it) {
+    const int s = it % kStagesQ4;
+    if (!mbar_wait_bounded(&full[s], (it / kStagesQ4) & 1, abort_flag, p.k.err)) break;
+    const int4 md = meta[s];
+    const int b = md.x, n = md.y, flags = md.z;
+    unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
+    unsigned char* vst = kst + p.k.chunk_bytes;
+    if (flags & 1) {  // first chunk of this CTA's share of request b
+      const T* qb = reinterpret_cast<const T*>(p.k.q) + (static_cast<int64_t>(b) * p.k.Hq + h * G) * HD;
+      __syncwarp();
+      for (int i = lane; i < GP * HD; i += 32)
+        qs[i] = i < G * HD ? static_cast<float>(qb[i]) * p.k.scale_log2 : 0.f;
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < GP; ++g)
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[g][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        m_run[j] = -INFINITY;
+        l_part[j] = 0.f;
+      }
+    }
+    if (md.w >= 0) write_new_row<T, HD>(p, kst, vst, b, n, md.w, h, lane);
+
+    float acc[GP][2];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) acc[g][0] = acc[g][1] = 0.f;
+    float2 sc[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = gq + 8 * u;
+      sc[u] = q4_sc(*reinterpret_cast<const uint32_t*>(
+          kst + t * R + p.codes + q4_swz((h * NG + ((tq * QD) >> p.log2gs)) * 4, p.pars, t)));
+    }
+#pragma unroll
+    for (int c8 = 0; c8 < QD / 8; ++c8) {
+      float xk[2][8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = gq + 8 * u;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(
+            kst + t * R + q4_swz(h * (HD / 2) + tq * (QD / 2) + c8 * 4, p.codes, t));
+        float a[4], bb[4];
+        q4_decode4(w & 0xFFFFu, sc[u].x, sc[u].y, a);
+        q4_decode4(w >> 16, sc[u].x, sc[u].y, bb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          xk[u][e] = a[e];
+          xk[u][4 + e] = bb[e];
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float4 qa = *reinterpret_cast<const float4*>(qs + g * HD + tq * QD + c8 * 8);
+        const float4 qb = *reinterpret_cast<const float4*>(qs + g * HD + tq * QD + c8 * 8 + 4);
+        const float qv[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          acc[g][0] = fmaf(qv[e], xk[0][e], acc[g][0]);
+          acc[g][1] = fmaf(qv[e], xk[1][e], acc[g][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        acc[g][u] += __shfl_xor_sync(0xffffffffu, acc[g][u], 1);
+        acc[g][u] += __shfl_xor_sync(0xffffffffu, acc[g][u], 2);
+      }
+    // online softmax (base 2): lane tq keeps heads tq and tq + 4
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      const int g = tq + 4 * j;
+      float v0 = acc[4 * j][0], v1 = acc[4 * j][1];
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        if (4 * j + k < GP && tq == k) {
+          v0 = acc[(4 * j + k) % GP][0];
+          v1 = acc[(4 * j + k) % GP][1];
+        }
+      v0 = gq < n ? v0 : -INFINITY;
+      v1 = gq + 8 < n ? v1 : -INFINITY;
+      float mx = fmaxf(v0, v1);
+#pragma unroll
+      for (int m = 4; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+      const float m_new = fmaxf(m_run[j], mx);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m_run[j] - m_use);
+      const float p0 = exp2f(v0 - m_use), p1 = exp2f(v1 - m_use);
+      l_part[j] = l_part[j] * alpha + (p0 + p1);
+      m_run[j] = m_new;
+      if (g < GP) {
+        p_tile[gq * GP + g] = p0;
+        p_tile[(gq + 8) * GP + g] = p1;
+        if (gq == 0) alpha_s[g] = alpha;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      const float al = alpha_s[g];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) o[g][e] *= al;
+    }
+    for (int t = 0; t < n; ++t) {
+      const float2 scv = q4_sc(*reinterpret_cast<const uint32_t*>(
+          vst + t * R + p.codes + q4_swz((h * NG + ((lane * EL) >> p.log2gs)) * 4, p.pars, t)));
+      const uint32_t hw = *reinterpret_cast<const uint16_t*>(
+          vst + t * R + q4_swz(h * (HD / 2) + (lane * EL / 4) * 2, p.codes, t));
+      float a[4];
+      q4_decode4(hw, scv.x, scv.y, a);
+      float xv[EL];
+      if constexpr (EL == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xv[e] = a[e];
+      } else {
+        xv[0] = (lane & 1) ? a[2] : a[0];
+        xv[1] = (lane & 1) ? a[3] : a[1];
+      }
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float pv = p_tile[t * GP + g];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[g][e] = fmaf(pv, xv[e], o[g][e]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+
+    if (flags & 2) {  // last chunk of the share: write the result
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        float l = l_part[j];
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
+        if (gq == 0 && tq + 4 * j < GP) {
+          ml_s[2 * (tq + 4 * j)] = m_run[j];
+          ml_s[2 * (tq + 4 * j) + 1] = l;
+        }
+      }
+      __syncwarp();
+      const bool whole = (flags & 4) != 0;
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        if (g < G) {
+          const float mg = ml_s[2 * g], lg = ml_s[2 * g + 1];
+          const float inv = lg > 0.f ? 1.f / lg : 0.f;
+          const int hq = h * G + g;
+          if (whole) {
+            T* dst = reinterpret_cast<T*>(p.k.out) + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD + lane * EL;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) dst[e] = static_cast<T>(o[g][e] * inv);
+          } else {
+            const int64_t slot = static_cast<int64_t>(c) + b;
+            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + lane * EL;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) dst[e] = o[g][e] * inv;
+            if (lane == 0) p.k.lse_part[slot * p.k.Hq + hq] = lg > 0.f ? mg + log2f(lg) : -INFINITY;
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <typename T, int HD, int GP>
+__global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const KParams& k = p.k;
+  const int c = blockIdx.x;
+  const int NW = k.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int32_t* cs;  // [B+1] chunk prefix sums
+  if (k.inline_plan) {
+    int32_t* cs_s = reinterpret_cast<int32_t*>(smem + k.off_cs);
+    plan_in_cta(k, cs_s, cs_s + kInlinePlanMax + 1, c == 0);
+    cs = cs_s;
+  } else {
+    pdl_wait();  // the plan kernel's chunk sums and CTA starts are complete
+    cs = k.cs;
+  }
+  pdl_trigger();  // the merge kernel may start launching; it waits for this grid
+  const int NC = cs[k.B];
+  const int x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
+  const int x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
+  if (x0 >= x1) return;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + k.off_bar);
+  uint64_t* empty = full + kStagesQ4;
+  int4* meta = reinterpret_cast<int4*>(smem + k.off_meta);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + k.off_abort);
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int s = 0; s < kStagesQ4; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NW);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  cta_sync();
+
+  if (warp == NW) {
+    // ------------------------------ producer ------------------------------
+    const uint64_t pol = l2_policy_evict_first();
+    int b = k.inline_plan ? first_request(cs, k.B, x0) : k.cta_seq[c];
+    int issued = 0;
+    bool aborted = false;
+    for (int xg = x0; xg < x1 && !aborted; xg += 32) {
+      const int nvalid = min(32, x1 - xg);
+      const int x = xg + lane;
+      int my_b = b, n = 0, flags = 0, new_slot = -1;
+      long long off = 0;
+      if (lane < nvalid) {
+        while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
+        const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
+        const int jc = x - cb0;
+        const int t0 = jc * kTok;
+        n = min(kTok, k.ctx[my_b] - t0);
+        const int page = k.bt[static_cast<int64_t>(my_b) * k.maxp + (t0 >> k.log2P)];
+        if (page < 0 || page >= k.num_pages) {
+          raise_flag(k.err, PA_DEVERR_BAD_PAGE);
+          n = 0;
+        } else {
+          const long long slot0 = (static_cast<long long>(page) << k.log2P) + (t0 & (k.P - 1));
+          off = slot0 * k.row_bytes;
+          if (k.k_new != nullptr && x == cb1 - 1) new_slot = static_cast<int>(slot0) + n - 1;  // position context_len - 1
+        }
+        flags = ((x == x0 || jc == 0) ? 1 : 0) | ((x == x1 - 1 || x == cb1 - 1) ? 2 : 0) |
+                ((cb0 >= x0 && cb1 <= x1) ? 4 : 0) | ((x == cb1 - 1) ? 8 : 0);
+      }
+      b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
+      for (int u = 0; u < nvalid; ++u) {
+        const int ub = __shfl_sync(0xffffffffu, my_b, u);
+        const int un = __shfl_sync(0xffffffffu, n, u);
+        const int uf = __shfl_sync(0xffffffffu, flags, u);
+        const long long uoff = __shfl_sync(0xffffffffu, off, u);
+        const int uslot = __shfl_sync(0xffffffffu, new_slot, u);
+        int ok = 1;
+        if (lane == 0) {
+          const int it = xg - x0 + u;
+          const int s = it % kStagesQ4;
+          if (!mbar_wait_bounded(&empty[s], ((it / kStagesQ4) & 1) ^ 1, abort_flag, k.err)) {
+            ok = 0;
+          } else {
+            meta[s] = make_int4(ub, un, uf, uslot);
+            // the new token's row is quantised by the consumers
+            const uint32_t rows = static_cast<uint32_t>(un) - (uslot >= 0 ? 1u : 0u);
+            const uint32_t bytes = rows * static_cast<uint32_t>(k.row_bytes);
+            mbar_arrive_expect_tx(&full[s], 2 * bytes);
+            if (bytes) {
+              unsigned char* dst = smem + static_cast<size_t>(s) * 2 * k.chunk_bytes;
+              bulk_g2s_hint(dst, k.k_cache + uoff, bytes, &full[s], pol);
+              bulk_g2s_hint(dst + k.chunk_bytes, k.v_cache + uoff, bytes, &full[s], pol);
+            }
+            if (k.k_new != nullptr && (uf & 8) && k.slot_out) k.slot_out[ub] = uslot;
+            ++issued;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          aborted = true;
+          break;
+        }
+      }
+    }
+    if (aborted && lane == 0) {
+      // Copies already issued may still be landing: wait for them (time only).
+      for (int it = max(0, issued - kStagesQ4); it < issued; ++it)
+        drain_wait(&full[it % kStagesQ4], (it / kStagesQ4) & 1);
+    }
+    return;
+  }
+  simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
+}
+
+struct Fns {
+  const void* main;
+  const void* merge;
+};
+
+template <typename T, int HD>
+Fns fns_for(int G) {
+  const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<T, HD>);
+  if (G == 1) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 1>), merge};
+  if (G == 2) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 2>), merge};
+  if (G <= 4) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 4>), merge};
+  return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
+}
+
+Fns get_fns(int dtype, int hd, int G) {
+  if (dtype == PA_BF16) return hd == 128 ? fns_for<__nv_bfloat16, 128>(G) : fns_for<__nv_bfloat16, 64>(G);
+  return hd == 128 ? fns_for<float, 128>(G) : fns_for<float, 64>(G);
+}
+
+int heads_padded(int G) { return G <= 2 ? G : G <= 4 ? 4 : 8; }
+
+}  // namespace
+
+cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ctx, int max_ctas, DecodePlan* out) {
+  DeviceInfo di;
+  cudaError_t e = current_device_info(&di);
+  if (e != cudaSuccess) return e;
+  const int G = d.num_q_heads / d.num_kv_heads;
+  DecodePlan pl;
+  pl.nw = d.num_kv_heads;
+  pl.tokens_per_chunk = kTok;
+  pl.row_pitch = q4_row_bytes(d, gs);
+  pl.chunk_bytes = kTok * pl.row_pitch;
+  pl.stages = kStagesQ4;
+  size_t off = static_cast<size_t>(kStagesQ4) * 2 * pl.chunk_bytes;
+  pl.off_bar = static_cast<uint32_t>(off);
+  off += 2 * kStagesQ4 * sizeof(uint64_t);
+  pl.off_meta = static_cast<uint32_t>(align_up(off, 16));
+  off = pl.off_meta + kStagesQ4 * 16;
+  pl.off_abort = static_cast<uint32_t>(off);
+  off += 16;
+  pl.off_p = static_cast<uint32_t>(align_up(off, 16));
+  off = pl.off_p + static_cast<size_t>(pl.nw) * kTok * heads_padded(G) * 4;
+  pl.off_alpha = static_cast<uint32_t>(align_up(off, 16));
+  off = pl.off_alpha + static_cast<size_t>(pl.nw) * 8 * 4;
+  pl.off_ml = static_cast<uint32_t>(off);
+  off += static_cast<size_t>(pl.nw) * 16 * 4;
+  off += static_cast<size_t>(pl.nw) * heads_padded(G) * d.head_dim * 4;  // scaled queries, behind off_ml
+  pl.off_cs = static_cast<uint32_t>(align_up(off, 16));
+  off = pl.off_cs + static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4;
+  pl.smem_bytes = align_up(off, 128);
+  if (pl.smem_bytes > static_cast<size_t>(di.max_smem_optin)) return cudaErrorInvalidValue;
+  int occ = 0;
+  e = ctas_per_sm(di, get_fns(d.dtype, d.head_dim, G).main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
+  if (e != cudaSuccess) return e;
+  const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
+  int64_t n = static_cast<int64_t>(occ) * di.sm_count;
+  if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
+  n = std::min<int64_t>(n, std::max<int64_t>(1, chunks_upper));
+  pl.n_ctas = static_cast<int>(std::max<int64_t>(1, n));
+  decode_workspace_layout(d, batch, &pl);
+  *out = pl;
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& pl, const DecodeArgs& a,
+                             cudaStream_t s) {
+  const Fns f = get_fns(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
+  Q4Params p{};
+  p.k = decode_params(d, pl, a, q4_row_bytes(d, gs));
+  p.codes = q4_codes_bytes(d);
+  p.pars = p.k.row_bytes - p.codes;
+  while ((1 << p.log2gs) < gs) ++p.log2gs;
+  p.off_q = pl.off_ml + pl.nw * 16 * 4;
+  void* args[] = {&p};
+  return launch_decode_kernels(f.main, f.merge, pl, p.k, args, s);
+}
+
+}  // namespace pa

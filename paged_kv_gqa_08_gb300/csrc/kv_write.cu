@@ -5,7 +5,7 @@
 
 #include <algorithm>
 
-#include "pa_common.cuh"
+#include "q4_common.cuh"
 
 namespace pa {
 namespace {
@@ -190,6 +190,56 @@ PA_DEVINL void map_token(const NormRopeParams& p, int64_t t, bool report, int& p
   map_token_of(p, t, lo, p.cu[lo], p.cu[lo + 1], p.ctx[lo], report, pos, slot);
 }
 
+// One head's rotated k (four dims of each half per lane, HD / 8 lanes a head),
+// quantised into head h of a 4-bit row.  All 32 lanes take part.
+template <int HD, int GS>
+PA_DEVINL void store_q4_halves(float (&a)[4], float (&b)[4], int l, bool store, char* row, int h, uint32_t codes,
+                               uint32_t pars, uint32_t t) {
+  constexpr bool kWhole = GS == HD;                // one group: both halves
+  constexpr int GL = kWhole ? HD / 8 : GS / 4;     // lanes of a group
+  float mna = INFINITY, mxa = -INFINITY, mnb = INFINITY, mxb = -INFINITY;
+  int bad_a = 0, bad_b = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    bad_a |= q4_bad(a[e]);
+    bad_b |= q4_bad(b[e]);
+    a[e] = q4_clamp(a[e]);
+    b[e] = q4_clamp(b[e]);
+    mna = fminf(mna, a[e]);
+    mxa = fmaxf(mxa, a[e]);
+    mnb = fminf(mnb, b[e]);
+    mxb = fmaxf(mxb, b[e]);
+  }
+  if constexpr (kWhole) {
+    mna = fminf(mna, mnb);
+    mxa = fmaxf(mxa, mxb);
+    bad_a |= bad_b;
+  }
+#pragma unroll
+  for (int m = 1; m < GL; m <<= 1) {
+    mna = fminf(mna, __shfl_xor_sync(0xffffffffu, mna, m));
+    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, m));
+    bad_a |= __shfl_xor_sync(0xffffffffu, bad_a, m);
+    if constexpr (!kWhole) {
+      mnb = fminf(mnb, __shfl_xor_sync(0xffffffffu, mnb, m));
+      mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, m));
+      bad_b |= __shfl_xor_sync(0xffffffffu, bad_b, m);
+    }
+  }
+  const Q4Group ga = q4_group(mna, mxa, bad_a != 0);
+  const Q4Group gb = kWhole ? ga : q4_group(mnb, mxb, bad_b != 0);
+  if (!store) return;
+  const uint32_t o = static_cast<uint32_t>(h * (HD / 2) + l * 2);
+  *reinterpret_cast<uint16_t*>(row + q4_swz(o, codes, t)) = static_cast<uint16_t>(q4_encode4(a, ga));
+  *reinterpret_cast<uint16_t*>(row + q4_swz(o + HD / 4, codes, t)) = static_cast<uint16_t>(q4_encode4(b, gb));
+  if (l % GL == 0) {
+    const uint32_t g = static_cast<uint32_t>(h * (HD / GS) + l / GL);
+    *reinterpret_cast<uint32_t*>(row + codes + q4_swz(g * 4, pars, t)) = ga.word;
+    if constexpr (!kWhole)
+      *reinterpret_cast<uint32_t*>(row + codes + q4_swz((g + HD / GS / 2) * 4, pars, t)) = gb.word;
+  }
+}
+
 constexpr int kNrThreads = 128;
 constexpr int kNrCtasPerSm = 8;
 constexpr int kNrMaxPerCta = 2048;
@@ -208,7 +258,13 @@ __host__ __device__ constexpr int nr_stage_bytes(int hq, int hkv, int hd, int e)
 // casts of the Qwen3 norm and rotary in the nano-vLLM learning note); for
 // bf16 the element arithmetic runs on fp32 pairs (packed multiplies and FMAs,
 // one two-lane conversion per rounding).
-template <typename T, int HD>
+//
+// GS != 0: the cache holds 4-bit rows with groups of GS dims (q4_common.cuh).
+// The rotated k (rounded to the storage type, as a cache of that type would
+// hold it) and the v row are quantised on their way out: a lane's four dims of
+// each half are 16 bits of codes, and GS / 4 neighbouring lanes (both halves
+// together when GS = HD) form a group.
+template <typename T, int HD, int GS>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const NormRopeParams p) {
   constexpr int E = sizeof(T);
   constexpr int PE = 4;
@@ -339,6 +395,9 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       nsn[e] = -sn[e];
     }
     const unsigned char* st = stages + (i & 1) * stage_bytes;
+    [[maybe_unused]] const uint32_t q4_codes = static_cast<uint32_t>(p.hkv) * (HD / 2),
+                                    q4_pars = static_cast<uint32_t>(p.q4_row_bytes) - q4_codes,
+                                    q4_t = static_cast<uint32_t>(slot);
     const int nheads = p.hq + p.hkv;
     for (int hh = warp * HPW + sub; hh - sub < nheads; hh += (kNrThreads / 32) * HPW) {
       const bool active = hh < nheads;
@@ -358,11 +417,15 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       float ss = ss2.x + ss2.y;
 #pragma unroll
       for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (!active) continue;
+      // a 4-bit group's reduction takes the whole warp, heads past the last included
+      if constexpr (GS == 0) {
+        if (!active) continue;
+      }
       const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
       T* dst = isq ? static_cast<T*>(p.q_out) + (t * p.hq + hh) * HD
-                   : static_cast<T*>(p.k_cache) + (slot * p.hkv + (hh - p.hq)) * HD;
-      const bool store = isq || slot_ok;
+                   : GS == 0 ? static_cast<T*>(p.k_cache) + (slot * p.hkv + (hh - p.hq)) * HD : nullptr;
+      const bool store = GS == 0 ? isq || slot_ok : isq && active;
+      [[maybe_unused]] float q4a[PE], q4b[PE];  // the rotated head in the storage type's values
       if constexpr (sizeof(T) == 2) {
         // y_a = n_a cos - n_b sin, y_b = n_b cos + n_a sin on fp32 pairs
         uint32_t wa[PE / 2], wb[PE / 2];
@@ -379,6 +442,13 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           const float2 yb = ffma2(nb, c2, fmul2(na, make_float2(sn[e], sn[e + 1])));
           wa[e2] = pack_bf16x2(ya.x, ya.y);
           wb[e2] = pack_bf16x2(yb.x, yb.y);
+          if constexpr (GS != 0) {
+            const float2 ra = bf16x2_to_float2(wa[e2]), rb = bf16x2_to_float2(wb[e2]);
+            q4a[e] = ra.x;
+            q4a[e + 1] = ra.y;
+            q4b[e] = rb.x;
+            q4b[e + 1] = rb.y;
+          }
         }
         if (store) {
           *reinterpret_cast<uint2*>(dst + l * PE) = make_uint2(wa[0], wa[1]);
@@ -392,14 +462,49 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           const float nb = round_to<T>(round_to<T>(xb[e] * r) * (isq ? wq_b[e] : wk_b[e]));
           ya[e] = round_to<T>(na * cs[e] - nb * sn[e]);
           yb[e] = round_to<T>(nb * cs[e] + na * sn[e]);
+          if constexpr (GS != 0) {
+            q4a[e] = ya[e];
+            q4b[e] = yb[e];
+          }
         }
         if (store) {
           Vec4<T>::store(dst + l * PE, ya);
           Vec4<T>::store(dst + HD / 2 + l * PE, yb);
         }
       }
+      if constexpr (GS != 0) {
+        if (hh - sub + HPW > p.hq)  // the pass holds a k head (the same for the whole warp)
+          store_q4_halves<HD, GS>(q4a, q4b, l, active && !isq && slot_ok,
+                                  static_cast<char*>(p.k_cache) + slot * p.q4_row_bytes, hh - p.hq, q4_codes, q4_pars,
+                                  q4_t);
+      }
     }
-    if (slot_ok) {  // the v row, unchanged, into its slot
+    if constexpr (GS != 0) {  // the v row, quantised, into its slot
+      const unsigned char* vsrc = st + row_q + row_kv;
+      const int units = p.hkv * (HD / 8);  // eight dims each
+      for (int u0 = threadIdx.x & ~31; u0 < units; u0 += kNrThreads) {
+        const int u = u0 + lane;
+        float x[8] = {};
+        if (u < units) {
+          float lo[4], hi[4];
+          Vec4<T>::load(vsrc + u * 8 * E, lo);
+          Vec4<T>::load(vsrc + u * 8 * E + 4 * E, hi);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = lo[e];
+            x[4 + e] = hi[e];
+          }
+        }
+        uint32_t par;
+        const uint32_t w = q4_quantise8(x, GS / 8, par);
+        if (u < units && slot_ok) {
+          char* vr = static_cast<char*>(p.v_cache) + slot * p.q4_row_bytes;
+          *reinterpret_cast<uint32_t*>(vr + q4_swz(u * 4, q4_codes, q4_t)) = w;
+          if (u % (GS / 8) == 0)
+            *reinterpret_cast<uint32_t*>(vr + q4_codes + q4_swz(u / (GS / 8) * 4, q4_pars, q4_t)) = par;
+        }
+      }
+    } else if (slot_ok) {  // the v row, unchanged, into its slot
       const unsigned char* vsrc = st + row_q + row_kv;
       char* vdst = static_cast<char*>(p.v_cache) + slot * row_kv;
       for (int ch = threadIdx.x; ch < row_kv / 16; ch += kNrThreads)
@@ -418,6 +523,16 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       }
     }
   }
+}
+
+// The kernel for rows of the storage type (gs = 0) or 4-bit rows with groups of gs dims.
+template <typename T, int HD>
+const void* norm_rope_fn(int gs) {
+  if (gs == 0) return reinterpret_cast<const void*>(norm_rope_kv_write_kernel<T, HD, 0>);
+  if constexpr (HD == 128)
+    if (gs == 128) return reinterpret_cast<const void*>(norm_rope_kv_write_kernel<T, HD, 128>);
+  return gs == 64 ? reinterpret_cast<const void*>(norm_rope_kv_write_kernel<T, HD, 64>)
+                  : reinterpret_cast<const void*>(norm_rope_kv_write_kernel<T, HD, 32>);
 }
 
 }  // namespace
@@ -454,11 +569,10 @@ cudaError_t launch_norm_rope_kv_write(int dtype, int head_dim, const NormRopePar
   const size_t smem = 2 * static_cast<size_t>(nr_stage_bytes(p.hq, p.hkv, head_dim, es)) + 2 * sizeof(uint64_t) +
                       head_dim * sizeof(float) + (p.positions == nullptr ? per_cta * sizeof(longlong2) : 0);
   if (smem > static_cast<size_t>(di.max_smem_optin)) return cudaErrorInvalidValue;
+  const int gs = p.q4_group_size;
   const void* fn = dtype == PA_BF16
-                       ? (head_dim == 128 ? reinterpret_cast<const void*>(norm_rope_kv_write_kernel<__nv_bfloat16, 128>)
-                                          : reinterpret_cast<const void*>(norm_rope_kv_write_kernel<__nv_bfloat16, 64>))
-                       : (head_dim == 128 ? reinterpret_cast<const void*>(norm_rope_kv_write_kernel<float, 128>)
-                                          : reinterpret_cast<const void*>(norm_rope_kv_write_kernel<float, 64>));
+                       ? (head_dim == 128 ? norm_rope_fn<__nv_bfloat16, 128>(gs) : norm_rope_fn<__nv_bfloat16, 64>(gs))
+                       : (head_dim == 128 ? norm_rope_fn<float, 128>(gs) : norm_rope_fn<float, 64>(gs));
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

@@ -97,8 +97,48 @@ struct NormRopeParams {
   int64_t num_pages;
   int32_t* pos_out;
   int64_t* slots_out;
+  // a 4-bit cache: its group size and row bytes (0: rows of the cache's dtype)
+  int32_t q4_group_size = 0, q4_row_bytes = 0;
 };
 cudaError_t launch_norm_rope_kv_write(int dtype, int head_dim, const NormRopeParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// 4-bit cache rows
+// ---------------------------------------------------------------------------
+inline int q4_codes_bytes(const pa_cache_desc& d) { return d.num_kv_heads * d.head_dim / 2; }
+inline int q4_row_bytes(const pa_cache_desc& d, int gs) {
+  return q4_codes_bytes(d) + (d.num_kv_heads * (d.head_dim / gs) * 4 + 15) / 16 * 16;
+}
+
+struct Q4WriteParams {
+  const char* k;
+  const char* v;
+  int64_t k_stride_bytes, v_stride_bytes;
+  int64_t n_tokens;
+  const int64_t* slots;
+  char* k_cache;
+  char* v_cache;
+  int64_t num_slots;
+  int32_t row_bytes, hkv;
+  unsigned int* err;
+};
+cudaError_t launch_kv_write_q4(const pa_cache_desc& d, int gs, const Q4WriteParams& p, cudaStream_t s);
+
+struct Q4ReadParams {
+  const int32_t* cu;
+  const int32_t* starts;  // first token of each request, or null: 0
+  const int32_t* ctx;
+  const int32_t* bt;
+  const char* k_cache;
+  const char* v_cache;
+  char* k_out;
+  char* v_out;
+  int64_t k_stride_bytes, v_stride_bytes;
+  int64_t num_rows, num_pages;
+  int32_t batch, maxp, log2P, row_bytes, hkv;
+  unsigned int* err;
+};
+cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, const Q4ReadParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // decode
@@ -142,6 +182,11 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const pa_cache_desc& d, const DecodePlan& plan, const DecodeArgs& a,
                           cudaStream_t s);
+// The same over a 4-bit cache with groups of gs dims.
+cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_context_len, int max_ctas,
+                           DecodePlan* out);
+cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& plan, const DecodeArgs& a,
+                             cudaStream_t s);
 
 // Launch `fn` so that it may start while the stream's previous kernel runs
 // (programmatic stream serialisation); the kernel calls pdl_wait() before it
