@@ -12,14 +12,27 @@
 namespace pa {
 namespace {
 
-constexpr int kTok = 16;     // tokens per chunk
-constexpr int kStagesQ4 = 4; // ring depth
+constexpr int kTok = 16;        // tokens per chunk
+constexpr int kMaxStages = 8;   // ring depth, at most
 
 struct Q4Params {
   KParams k;
+  int32_t stages;       // ring depth
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
   uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
+};
+
+// Position in the ring: stage and phase bit of the running chunk.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  PA_DEVINL void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // The new token's K and V of kv-head h, quantised by the warp: into the chunk's
@@ -78,9 +91,10 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
   float* ml_s = reinterpret_cast<float*>(smem + p.k.off_ml) + warp * 16;
   float o[GP][EL];
   float m_run[NH], l_part[NH];
-  for (int x = x0, it = 0; x < x1; ++x, ++it) {
-    const int s = it % kStagesQ4;
-    if (!mbar_wait_bounded(&full[s], (it / kStagesQ4) & 1, abort_flag, p.k.err)) break;
+  Ring ring;
+  for (int x = x0; x < x1; ++x, ring.next(p.stages)) {
+    const int s = ring.s;
+    if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
     const int4 md = meta[s];
     const int b = md.x, n = md.y, flags = md.z;
     unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
@@ -246,8 +260,290 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tensor-core consumer (bf16 queries and outputs, groups of up to 8 q-heads).
+//
+// Per chunk, S^T = K Q^T and O^T += V^T P^T as mma.sync m16n8k16 (float16 in,
+// fp32 out): the chunk's 16 tokens, then 16 of the head's dims, are the rows,
+// and the group's q-heads the 8 columns (heads past G are zero queries), so no
+// row of a product is padding.  With l = 4 gq + tq, a lane holds of A rows gq
+// and gq + 8 at columns 2 tq, 2 tq + 1 (+ 8), of B column gq at rows 2 tq,
+// 2 tq + 1 (+ 8), of C rows gq and gq + 8 at columns 2 tq, 2 tq + 1 (PTX ISA).
+//
+// Neither the order of the dims inside S's sums, nor that of O's rows, nor that
+// of the tokens matters to the result, so each lane's share is chosen to be
+// contiguous in the row: of K the HD / 4 dims from tq * HD / 4 of tokens gq and
+// gq + 8 (a register pairs dims d and d + 4 of one token), of V the HD / 8 dims
+// from gq * HD / 8 of tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (a register
+// pairs one dim of two neighbouring tokens).  A lane so meets one group of each
+// of its tokens, and with the rows' swizzle its loads are free of bank
+// conflicts where a row is a multiple of 128 bytes.
+//
+// A code becomes a float16 in place (q4_common.cuh): mask-or, then one packed
+// multiply-add with (s, c).  That is 11 to 12 instructions for 8 values and the
+// kernel's main cost; the tensor cores make the products nearly free.
+// Values, probabilities and queries are float16 (2^-12 relative, finer than
+// bf16): queries are scaled by a power of two to a largest magnitude in [1, 2)
+// first, so their range does not matter; sums and statistics are fp32.
+// ---------------------------------------------------------------------------
+PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held two to a lane.
+PA_DEVINL uint32_t movm_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+PA_DEVINL uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// s * (16 + u) + c of the two codes in bits 6-9 and 22-25 of w.
+PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t s, uint32_t c) {
+  const uint32_t v = (w & 0x03C003C0u) | 0x4C004C00u;
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(s), "r"(c));
+  return d;
+}
+
+template <int HD>
+PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
+                            volatile int* abort_flag, int x0, int x1, int c) {
+  constexpr int KW = HD / 32;  // words of K codes a lane holds per token
+  constexpr int VW = HD / 64;  // words of V codes a lane holds per token
+  constexpr int MB = HD / 16;  // 16-dim blocks of O
+  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.k.Hq / p.k.Hkv;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int R = p.k.row_bytes, NG = HD >> p.log2gs;
+  // this lane's places in a stage: K codes and parameters of token gq (gq + 8:
+  // 8 rows on), V codes and parameters of tokens 2 tq and 2 tq + 1
+  const uint32_t k_codes = gq * R + q4_swz(h * (HD / 2) + tq * (HD / 8), p.codes, gq);
+  const uint32_t k_pars = gq * R + p.codes + q4_swz((h * NG + ((tq * (HD / 4)) >> p.log2gs)) * 4, p.pars, gq);
+  const uint32_t vo = h * (HD / 2) + gq * (HD / 16), vp = (h * NG + ((gq * (HD / 8)) >> p.log2gs)) * 4;
+  const uint32_t v_codes0 = 2 * tq * R + q4_swz(vo, p.codes, 2 * tq);
+  const uint32_t v_codes1 = (2 * tq + 1) * R + q4_swz(vo, p.codes, 2 * tq + 1);
+  const uint32_t v_pars0 = 2 * tq * R + p.codes + q4_swz(vp, p.pars, 2 * tq);
+  const uint32_t v_pars1 = (2 * tq + 1) * R + p.codes + q4_swz(vp, p.pars, 2 * tq + 1);
+
+  uint32_t qf[MB][2];  // B fragments of the queries
+  float o[MB][4];
+  float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the queries' power of two undone)
+  float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
+  float l[2] = {0.f, 0.f};     // this lane's part of the softmax sums
+  float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
+  int b = 0;
+  Ring ring;
+  for (int x = x0; x < x1; ++x, ring.next(p.stages)) {
+    const int s = ring.s;
+    if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
+    const int4 md = meta[s];
+    b = md.x;
+    const int n = md.y, flags = md.z;
+    unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
+    unsigned char* vst = kst + p.k.chunk_bytes;
+
+    if (flags & 1) {  // first chunk of this CTA's share of request b
+      const char* qrow = p.k.q + ((static_cast<int64_t>(b) * p.k.Hq + h * G + gq) * HD + tq * (HD / 4)) * 2;
+      float qv[HD / 4];
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 32; ++i) {
+        float v8[8] = {};
+        if (gq < G) q4_load8<__nv_bfloat16>(qrow + i * 16, v8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          qv[8 * i + e] = v8[e];
+          mx = fmaxf(mx, fabsf(v8[e]));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^-E of the largest magnitude's exponent E, and 2^E
+      const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+      const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
+#pragma unroll
+      for (int i = 0; i < HD / 32; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          qf[2 * i + (v >> 1)][v & 1] = pack_f16x2(qv[8 * i + v] * down, qv[8 * i + 4 + v] * down);
+      mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq);
+      mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4);
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+      m[0] = m[1] = l[0] = l[1] = 0.f;
+      limit = -INFINITY;
+    }
+    if (md.w >= 0) write_new_row<__nv_bfloat16, HD>(p, kst, vst, b, n, md.w, h, lane);
+
+    // S^T = K Q^T
+    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      uint32_t kw[2][KW], ks[2], kc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const unsigned char* src = kst + k_codes + u * 8 * R;
+        if constexpr (KW == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src);
+          kw[u][0] = w.x; kw[u][1] = w.y; kw[u][2] = w.z; kw[u][3] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(src);
+          kw[u][0] = w.x; kw[u][1] = w.y;
+        }
+        const uint32_t par = *reinterpret_cast<const uint32_t*>(kst + k_pars + u * 8 * R);
+        ks[u] = __byte_perm(par, 0, 0x1010);
+        kc[u] = __byte_perm(par, 0, 0x3232);
+      }
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t w0 = kw[0][i], w1 = kw[1][i];
+        const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
+        mma_f16(sc, q4_pair(w0, ks[0], kc[0]), q4_pair(w1, ks[1], kc[1]), q4_pair(y0, ks[0], kc[0]),
+                q4_pair(y1, ks[1], kc[1]), qf[2 * i][0], qf[2 * i][1]);
+        mma_f16(sc, q4_pair(w0 << 4, ks[0], kc[0]), q4_pair(w1 << 4, ks[1], kc[1]), q4_pair(y0 << 4, ks[0], kc[0]),
+                q4_pair(y1 << 4, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
+      }
+    }
+
+    // softmax: exponents relative to a reference that only moves when a score
+    // passes it by more than 2^8 (probabilities stay below 2^8: a float16)
+    float t0 = fmaf(sc[0], mult[0], -m[0]), t1 = fmaf(sc[1], mult[1], -m[1]);
+    float t2 = fmaf(sc[2], mult[0], -m[0]), t3 = fmaf(sc[3], mult[1], -m[1]);
+    if (n < kTok) {
+      if (gq >= n) t0 = t1 = -INFINITY;
+      if (gq + 8 >= n) t2 = t3 = -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, fmaxf(fmaxf(t0, t2), fmaxf(t1, t3)) > limit)) {
+      float d0 = fmaxf(t0, t2), d1 = fmaxf(t1, t3);
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) {
+        d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, k));
+        d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, k));
+      }
+      if (limit == -INFINITY) {  // the first scores: O and l are zero
+        if (d0 == -INFINITY) d0 = 0.f;
+        if (d1 == -INFINITY) d1 = 0.f;
+      } else {
+        d0 = fmaxf(d0, 0.f);
+        d1 = fmaxf(d1, 0.f);
+        const float a0 = ex2_approx(-d0), a1 = ex2_approx(-d1);
+        l[0] *= a0;
+        l[1] *= a1;
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          o[j][0] *= a0;
+          o[j][1] *= a1;
+          o[j][2] *= a0;
+          o[j][3] *= a1;
+        }
+      }
+      m[0] += d0;
+      m[1] += d1;
+      t0 -= d0;
+      t1 -= d1;
+      t2 -= d0;
+      t3 -= d1;
+      limit = 8.f;
+    }
+    const float p0 = ex2_approx(t0), p1 = ex2_approx(t1), p2 = ex2_approx(t2), p3 = ex2_approx(t3);
+    l[0] += p0 + p2;
+    l[1] += p1 + p3;
+    const uint32_t b0 = movm_trans(pack_f16x2(p0, p1)), b1 = movm_trans(pack_f16x2(p2, p3));
+
+    // O^T += V^T P^T
+    {
+      uint32_t vw[4][VW], vpar[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const unsigned char* src = vst + ((u & 1) ? v_codes1 : v_codes0) + (u >> 1) * 8 * R;
+        if constexpr (VW == 2) {
+          const uint2 w = *reinterpret_cast<const uint2*>(src);
+          vw[u][0] = w.x; vw[u][1] = w.y;
+        } else {
+          vw[u][0] = *reinterpret_cast<const uint32_t*>(src);
+        }
+        vpar[u] = *reinterpret_cast<const uint32_t*>(vst + ((u & 1) ? v_pars1 : v_pars0) + (u >> 1) * 8 * R);
+      }
+      if (n < kTok) {
+        // rows past the context meet probability 0 and must be finite
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (2 * tq + (u & 1) + (u >> 1) * 8 >= n) vpar[u] = 0u;
+      }
+      uint32_t vs[2], vc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        vs[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x5410);
+        vc[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t xx[2], yy[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            xx[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], hf ? 0x7632 : 0x5410);
+            yy[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], hf ? 0x6723 : 0x4501);
+          }
+          mma_f16(o[4 * j + 2 * hf], q4_pair(xx[0], vs[0], vc[0]), q4_pair(yy[0], vs[0], vc[0]),
+                  q4_pair(xx[1], vs[1], vc[1]), q4_pair(yy[1], vs[1], vc[1]), b0, b1);
+          mma_f16(o[4 * j + 2 * hf + 1], q4_pair(xx[0] << 4, vs[0], vc[0]), q4_pair(yy[0] << 4, vs[0], vc[0]),
+                  q4_pair(xx[1] << 4, vs[1], vc[1]), q4_pair(yy[1] << 4, vs[1], vc[1]), b0, b1);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+
+    if (flags & 2) {  // last chunk of the share: write the result
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int g = 2 * tq + e;
+        if (g < G) {
+          const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+          const int hq = h * G + g;
+          if (flags & 4) {
+            char* dst = p.k.out + ((static_cast<int64_t>(b) * p.k.Hq + hq) * HD + gq * (HD / 8)) * 2;
+#pragma unroll
+            for (int j = 0; j < MB; j += 4)
+              stg16(dst + j * 4, make_uint4(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
+                                            pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv),
+                                            pack_bf16x2(o[j + 2][e] * inv, o[j + 2][2 + e] * inv),
+                                            pack_bf16x2(o[j + 3][e] * inv, o[j + 3][2 + e] * inv)));
+          } else {
+            const int64_t slot = static_cast<int64_t>(c) + b;
+            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + gq * (HD / 8);
+#pragma unroll
+            for (int j = 0; j < MB; j += 2)
+              *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[j][e] * inv, o[j][2 + e] * inv,
+                                                                    o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
+            if (gq == 0) p.k.lse_part[slot * p.k.Hq + hq] = l[e] > 0.f ? m[e] + log2f(l[e]) : -INFINITY;
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 template <typename T, int HD, int GP>
-__global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(9 * 32, 2) decode_q4_kernel(const Q4Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const KParams& k = p.k;
   const int c = blockIdx.x;
@@ -270,12 +566,11 @@ __global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
   if (x0 >= x1) return;
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + k.off_bar);
-  uint64_t* empty = full + kStagesQ4;
+  uint64_t* empty = full + kMaxStages;
   int4* meta = reinterpret_cast<int4*>(smem + k.off_meta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + k.off_abort);
   if (threadIdx.x == 0) {
-#pragma unroll
-    for (int s = 0; s < kStagesQ4; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], NW);
     }
@@ -289,6 +584,7 @@ __global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
     const uint64_t pol = l2_policy_evict_first();
     int b = k.inline_plan ? first_request(cs, k.B, x0) : k.cta_seq[c];
     int issued = 0;
+    Ring ring;
     bool aborted = false;
     for (int xg = x0; xg < x1 && !aborted; xg += 32) {
       const int nvalid = min(32, x1 - xg);
@@ -314,7 +610,7 @@ __global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
                 ((cb0 >= x0 && cb1 <= x1) ? 4 : 0) | ((x == cb1 - 1) ? 8 : 0);
       }
       b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
-      for (int u = 0; u < nvalid; ++u) {
+      for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {
         const int ub = __shfl_sync(0xffffffffu, my_b, u);
         const int un = __shfl_sync(0xffffffffu, n, u);
         const int uf = __shfl_sync(0xffffffffu, flags, u);
@@ -322,9 +618,8 @@ __global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
         const int uslot = __shfl_sync(0xffffffffu, new_slot, u);
         int ok = 1;
         if (lane == 0) {
-          const int it = xg - x0 + u;
-          const int s = it % kStagesQ4;
-          if (!mbar_wait_bounded(&empty[s], ((it / kStagesQ4) & 1) ^ 1, abort_flag, k.err)) {
+          const int s = ring.s;
+          if (!mbar_wait_bounded(&empty[s], ring.phase ^ 1, abort_flag, k.err)) {
             ok = 0;
           } else {
             meta[s] = make_int4(ub, un, uf, uslot);
@@ -350,12 +645,15 @@ __global__ void __launch_bounds__(9 * 32) decode_q4_kernel(const Q4Params p) {
     }
     if (aborted && lane == 0) {
       // Copies already issued may still be landing: wait for them (time only).
-      for (int it = max(0, issued - kStagesQ4); it < issued; ++it)
-        drain_wait(&full[it % kStagesQ4], (it / kStagesQ4) & 1);
+      for (int it = max(0, issued - p.stages); it < issued; ++it)
+        drain_wait(&full[it % p.stages], (it / p.stages) & 1);
     }
     return;
   }
-  simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
+  if constexpr (sizeof(T) == 2)
+    mma_consumer<HD>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
+  else
+    simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
 }
 
 struct Fns {
@@ -366,10 +664,15 @@ struct Fns {
 template <typename T, int HD>
 Fns fns_for(int G) {
   const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<T, HD>);
-  if (G == 1) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 1>), merge};
-  if (G == 2) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 2>), merge};
-  if (G <= 4) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 4>), merge};
-  return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
+  // the tensor-core consumer takes any group of up to 8 heads
+  if constexpr (sizeof(T) == 2) {
+    return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
+  } else {
+    if (G == 1) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 1>), merge};
+    if (G == 2) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 2>), merge};
+    if (G <= 4) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 4>), merge};
+    return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
+  }
 }
 
 Fns get_fns(int dtype, int hd, int G) {
@@ -391,24 +694,32 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   pl.tokens_per_chunk = kTok;
   pl.row_pitch = q4_row_bytes(d, gs);
   pl.chunk_bytes = kTok * pl.row_pitch;
-  pl.stages = kStagesQ4;
-  size_t off = static_cast<size_t>(kStagesQ4) * 2 * pl.chunk_bytes;
-  pl.off_bar = static_cast<uint32_t>(off);
-  off += 2 * kStagesQ4 * sizeof(uint64_t);
-  pl.off_meta = static_cast<uint32_t>(align_up(off, 16));
-  off = pl.off_meta + kStagesQ4 * 16;
-  pl.off_abort = static_cast<uint32_t>(off);
-  off += 16;
-  pl.off_p = static_cast<uint32_t>(align_up(off, 16));
-  off = pl.off_p + static_cast<size_t>(pl.nw) * kTok * heads_padded(G) * 4;
-  pl.off_alpha = static_cast<uint32_t>(align_up(off, 16));
-  off = pl.off_alpha + static_cast<size_t>(pl.nw) * 8 * 4;
-  pl.off_ml = static_cast<uint32_t>(off);
-  off += static_cast<size_t>(pl.nw) * 16 * 4;
-  off += static_cast<size_t>(pl.nw) * heads_padded(G) * d.head_dim * 4;  // scaled queries, behind off_ml
-  pl.off_cs = static_cast<uint32_t>(align_up(off, 16));
-  off = pl.off_cs + static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4;
-  pl.smem_bytes = align_up(off, 128);
+  // behind the ring: barriers, chunk descriptors, the batch's prefix sums, and
+  // what the CUDA-core consumer (fp32) keeps in shared memory
+  const bool simt = d.dtype != PA_BF16;
+  size_t off = 0;
+  auto place = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 16);
+    return static_cast<uint32_t>(at);
+  };
+  pl.off_bar = place(2 * kMaxStages * sizeof(uint64_t));
+  pl.off_meta = place(kMaxStages * 16);
+  pl.off_abort = place(16);
+  pl.off_cs = place(static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4);
+  pl.off_p = place(simt ? static_cast<size_t>(pl.nw) * kTok * heads_padded(G) * 4 : 0);
+  pl.off_alpha = place(simt ? static_cast<size_t>(pl.nw) * 8 * 4 : 0);
+  // statistics, then the scaled queries
+  pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4 : 0);
+  // The ring takes what is left of a CTA's share of the SM's shared memory with
+  // 16 consumer warps on an SM (two CTAs at 8 kv-heads): about 5 chunks.
+  const size_t fixed = align_up(off, 128), stage = 2 * static_cast<size_t>(pl.chunk_bytes);
+  const size_t share = static_cast<size_t>(di.max_smem_optin) * pl.nw / 16 - 1024;
+  pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, share > fixed ? (share - fixed) / stage : 0)));
+  const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
+  for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
+    *o += ring;
+  pl.smem_bytes = ring + fixed;
   if (pl.smem_bytes > static_cast<size_t>(di.max_smem_optin)) return cudaErrorInvalidValue;
   int occ = 0;
   e = ctas_per_sm(di, get_fns(d.dtype, d.head_dim, G).main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
@@ -428,6 +739,7 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   const Fns f = get_fns(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
   Q4Params p{};
   p.k = decode_params(d, pl, a, q4_row_bytes(d, gs));
+  p.stages = pl.stages;
   p.codes = q4_codes_bytes(d);
   p.pars = p.k.row_bytes - p.codes;
   while ((1 << p.log2gs) < gs) ++p.log2gs;
