@@ -3,17 +3,25 @@
 // The mathematics is decode.cu's with K and V rows that are decoded on the
 // way in (q4_common.cuh): the split of the keys over the CTAs, the partial
 // results and their merge are the same code (decode_shared.cuh).  A chunk is
-// 16 tokens of one page, one contiguous run of 16 rows of K and one of V; a
-// producer warp copies the runs of the cache as they are into a ring in shared
-// memory, and one consumer warp per kv-head decodes its head's part.
+// 32 tokens, two halves of 16 tokens of one page each; a producer warp copies
+// their rows of K and V as they are into a ring in shared memory (one run of
+// rows where the halves follow each other in a page), and one consumer warp
+// per kv-head decodes its head's part.
 #include "decode_shared.cuh"
 #include "q4_common.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kTok = 16;        // tokens per chunk
+constexpr int kTok = 32;        // tokens per chunk
+constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
+
+// A chunk in the ring: its request, the tokens of its halves (n0 | n1 << 8, 0
+// for one whose page is out of range), flags, and the slot of the request's new
+// token when it is the last of these tokens (else -1).
+//   1 the first chunk of this CTA's share of the request   2 the last
+//   4 the share is the whole request                       8 the request's last chunk
 
 struct Q4Params {
   KParams k;
@@ -35,12 +43,12 @@ struct Ring {
   }
 };
 
-// The new token's K and V of kv-head h, quantised by the warp: into the chunk's
-// stage (row n - 1) and into the cache.  Every lane takes eight dims: K in the
+// The new token's K and V of kv-head h, quantised by the warp: into row t of the
+// chunk's stage and into the cache.  Every lane takes eight dims: K in the
 // lower lanes, V behind it.
 template <typename T, int HD>
-PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned char* vst, int b, int n, int slot, int h,
-                             int lane) {
+PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned char* vst, int b, uint32_t t, int slot,
+                             int h, int lane) {
   constexpr int LPR = HD / 8;
   const bool isv = (lane / LPR) & 1;
   const int l = lane % LPR;
@@ -53,7 +61,6 @@ PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned cha
   uint32_t par;
   const uint32_t w = q4_quantise8(x, gl, par);
   if (lane < 2 * LPR) {
-    const uint32_t t = static_cast<uint32_t>(n - 1);  // = slot mod 16
     unsigned char* row = (isv ? vst : kst) + t * p.k.row_bytes;
     char* dst = const_cast<char*>(isv ? p.k.v_cache : p.k.k_cache) + static_cast<int64_t>(slot) * p.k.row_bytes;
     const uint32_t co = q4_swz(h * (HD / 2) + l * 4, p.codes, t);
@@ -86,7 +93,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
   const int gq = lane >> 2, tq = lane & 3;
   const int R = p.k.row_bytes, NG = HD >> p.log2gs;
   float* qs = reinterpret_cast<float*>(smem + p.off_q) + warp * GP * HD;
-  float* p_tile = reinterpret_cast<float*>(smem + p.k.off_p) + warp * kTok * GP;
+  float* p_tile = reinterpret_cast<float*>(smem + p.k.off_p) + warp * kHalf * GP;
   float* alpha_s = reinterpret_cast<float*>(smem + p.k.off_alpha) + warp * 8;
   float* ml_s = reinterpret_cast<float*>(smem + p.k.off_ml) + warp * 16;
   float o[GP][EL];
@@ -96,7 +103,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
     const int s = ring.s;
     if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
     const int4 md = meta[s];
-    const int b = md.x, n = md.y, flags = md.z;
+    const int b = md.x, n0 = md.y & 255, n1 = md.y >> 8, flags = md.z;
     unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
     unsigned char* vst = kst + p.k.chunk_bytes;
     if (flags & 1) {  // first chunk of this CTA's share of request b
@@ -115,8 +122,11 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
         l_part[j] = 0.f;
       }
     }
-    if (md.w >= 0) write_new_row<T, HD>(p, kst, vst, b, n, md.w, h, lane);
+    if (md.w >= 0) write_new_row<T, HD>(p, kst, vst, b, n1 ? kHalf + n1 - 1 : n0 - 1, md.w, h, lane);
 
+    for (int hf = 0; hf < 2; ++hf, kst += kHalf * R, vst += kHalf * R) {
+    const int n = hf ? n1 : n0;
+    if (n == 0) continue;
     float acc[GP][2];
 #pragma unroll
     for (int g = 0; g < GP; ++g) acc[g][0] = acc[g][1] = 0.f;
@@ -221,6 +231,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
       }
     }
     __syncwarp();
+    }
     if (lane == 0) mbar_arrive(&empty[s]);
 
     if (flags & 2) {  // last chunk of the share: write the result
@@ -287,8 +298,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 // first, so their range does not matter; sums and statistics are fp32.
 // ---------------------------------------------------------------------------
 PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -297,7 +307,7 @@ PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 // Transpose of an 8x8 matrix of 16-bit elements held two to a lane.
 PA_DEVINL uint32_t movm_trans(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -315,6 +325,20 @@ PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t s, uint32_t c) {
   return d;
 }
 
+// Loads from a shared-memory address.  Volatile: they stay between the wait for
+// a stage and its release.
+PA_DEVINL uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+PA_DEVINL void lds64(uint32_t (&r)[2], uint32_t a) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a));
+}
+PA_DEVINL void lds128(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
 template <int HD>
 PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
                             volatile int* abort_flag, int x0, int x1, int c) {
@@ -324,16 +348,22 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
   const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.k.Hq / p.k.Hkv;
   const int gq = lane >> 2, tq = lane & 3;
-  const int R = p.k.row_bytes, NG = HD >> p.log2gs;
-  // this lane's places in a stage: K codes and parameters of token gq (gq + 8:
-  // 8 rows on), V codes and parameters of tokens 2 tq and 2 tq + 1
-  const uint32_t k_codes = gq * R + q4_swz(h * (HD / 2) + tq * (HD / 8), p.codes, gq);
-  const uint32_t k_pars = gq * R + p.codes + q4_swz((h * NG + ((tq * (HD / 4)) >> p.log2gs)) * 4, p.pars, gq);
+  const uint32_t R = p.k.row_bytes, NG = HD >> p.log2gs;
+  // Token of row g of a half: with rows a multiple of 128 bytes apart, odd rows
+  // take the tokens 4 on, so that the tokens which meet in one pass of a load
+  // lie in different banks.
+  const int flip = (R & 127u) == 0 ? 4 : 0;
+  const int kt = gq ^ ((gq & 1) * flip), vt0 = 2 * tq, vt1 = (2 * tq + 1) ^ flip;
+  // this lane's places in a stage: K codes and parameters of its token in row gq
+  // (gq + 8: 8 rows on), V codes and parameters of those in rows 2 tq, 2 tq + 1
+  const uint32_t k_codes = kt * R + q4_swz(h * (HD / 2) + tq * (HD / 8), p.codes, kt);
+  const uint32_t k_pars = kt * R + p.codes + q4_swz((h * NG + ((tq * (HD / 4)) >> p.log2gs)) * 4, p.pars, kt);
   const uint32_t vo = h * (HD / 2) + gq * (HD / 16), vp = (h * NG + ((gq * (HD / 8)) >> p.log2gs)) * 4;
-  const uint32_t v_codes0 = 2 * tq * R + q4_swz(vo, p.codes, 2 * tq);
-  const uint32_t v_codes1 = (2 * tq + 1) * R + q4_swz(vo, p.codes, 2 * tq + 1);
-  const uint32_t v_pars0 = 2 * tq * R + p.codes + q4_swz(vp, p.pars, 2 * tq);
-  const uint32_t v_pars1 = (2 * tq + 1) * R + p.codes + q4_swz(vp, p.pars, 2 * tq + 1);
+  const uint32_t v_codes0 = p.k.chunk_bytes + vt0 * R + q4_swz(vo, p.codes, vt0);
+  const uint32_t v_codes1 = p.k.chunk_bytes + vt1 * R + q4_swz(vo, p.codes, vt1);
+  const uint32_t v_pars0 = p.k.chunk_bytes + vt0 * R + p.codes + q4_swz(vp, p.pars, vt0);
+  const uint32_t v_pars1 = p.k.chunk_bytes + vt1 * R + p.codes + q4_swz(vp, p.pars, vt1);
+  const uint32_t smem0 = smem_u32(smem), meta0 = smem_u32(meta);
 
   uint32_t qf[MB][2];  // B fragments of the queries
   float o[MB][4];
@@ -341,19 +371,18 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
   float l[2] = {0.f, 0.f};     // this lane's part of the softmax sums
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
-  int b = 0;
   Ring ring;
   for (int x = x0; x < x1; ++x, ring.next(p.stages)) {
     const int s = ring.s;
     if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
-    const int4 md = meta[s];
-    b = md.x;
-    const int n = md.y, flags = md.z;
-    unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
-    unsigned char* vst = kst + p.k.chunk_bytes;
+    uint32_t md[4];
+    lds128(md, meta0 + s * 16);
+    const uint32_t nn = md[1], flags = md[2];
+    const uint32_t st = smem0 + s * 2 * p.k.chunk_bytes;
 
-    if (flags & 1) {  // first chunk of this CTA's share of request b
-      const char* qrow = p.k.q + ((static_cast<int64_t>(b) * p.k.Hq + h * G + gq) * HD + tq * (HD / 4)) * 2;
+    if (flags & 1) {  // first chunk of this CTA's share of the request
+      const char* qrow =
+          p.k.q + ((static_cast<int64_t>(md[0]) * p.k.Hq + h * G + gq) * HD + tq * (HD / 4)) * 2;
       float qv[HD / 4];
       float mx = 0.f;
 #pragma unroll
@@ -385,47 +414,59 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
       m[0] = m[1] = l[0] = l[1] = 0.f;
       limit = -INFINITY;
     }
-    if (md.w >= 0) write_new_row<__nv_bfloat16, HD>(p, kst, vst, b, n, md.w, h, lane);
+    if (static_cast<int>(md[3]) >= 0) {
+      unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
+      const uint32_t n0 = nn & 255, n1 = nn >> 8;
+      write_new_row<__nv_bfloat16, HD>(p, kst, kst + p.k.chunk_bytes, md[0], n1 ? kHalf + n1 - 1 : n0 - 1, md[3], h,
+                                       lane);
+    }
 
-    // S^T = K Q^T
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
-    {
+    // S^T = K Q^T of both halves
+    float sc[2][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
       uint32_t kw[2][KW], ks[2], kc[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const unsigned char* src = kst + k_codes + u * 8 * R;
-        if constexpr (KW == 4) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src);
-          kw[u][0] = w.x; kw[u][1] = w.y; kw[u][2] = w.z; kw[u][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(src);
-          kw[u][0] = w.x; kw[u][1] = w.y;
-        }
-        const uint32_t par = *reinterpret_cast<const uint32_t*>(kst + k_pars + u * 8 * R);
+        const uint32_t row = st + (hf * kHalf + u * 8) * R;
+        if constexpr (KW == 4) lds128(kw[u], row + k_codes);
+        else lds64(kw[u], row + k_codes);
+        const uint32_t par = lds32(row + k_pars);
         ks[u] = __byte_perm(par, 0, 0x1010);
         kc[u] = __byte_perm(par, 0, 0x3232);
       }
 #pragma unroll
+      for (int e = 0; e < 4; ++e) sc[hf][e] = 0.f;
+#pragma unroll
       for (int i = 0; i < KW; ++i) {
         const uint32_t w0 = kw[0][i], w1 = kw[1][i];
         const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
-        mma_f16(sc, q4_pair(w0, ks[0], kc[0]), q4_pair(w1, ks[1], kc[1]), q4_pair(y0, ks[0], kc[0]),
+        mma_f16(sc[hf], q4_pair(w0, ks[0], kc[0]), q4_pair(w1, ks[1], kc[1]), q4_pair(y0, ks[0], kc[0]),
                 q4_pair(y1, ks[1], kc[1]), qf[2 * i][0], qf[2 * i][1]);
-        mma_f16(sc, q4_pair(w0 << 4, ks[0], kc[0]), q4_pair(w1 << 4, ks[1], kc[1]), q4_pair(y0 << 4, ks[0], kc[0]),
-                q4_pair(y1 << 4, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
+        mma_f16(sc[hf], q4_pair(w0 << 4, ks[0], kc[0]), q4_pair(w1 << 4, ks[1], kc[1]),
+                q4_pair(y0 << 4, ks[0], kc[0]), q4_pair(y1 << 4, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
       }
     }
 
     // softmax: exponents relative to a reference that only moves when a score
     // passes it by more than 2^8 (probabilities stay below 2^8: a float16)
-    float t0 = fmaf(sc[0], mult[0], -m[0]), t1 = fmaf(sc[1], mult[1], -m[1]);
-    float t2 = fmaf(sc[2], mult[0], -m[0]), t3 = fmaf(sc[3], mult[1], -m[1]);
-    if (n < kTok) {
-      if (gq >= n) t0 = t1 = -INFINITY;
-      if (gq + 8 >= n) t2 = t3 = -INFINITY;
+    float t[2][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[hf][e], mult[e & 1], -m[e & 1]);
+    const bool ragged = nn != (kHalf | kHalf << 8);
+    if (ragged) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int n = hf ? nn >> 8 : nn & 255;
+        if (kt >= n) t[hf][0] = t[hf][1] = -INFINITY;
+        if (kt + 8 >= n) t[hf][2] = t[hf][3] = -INFINITY;
+      }
     }
-    if (__any_sync(0xffffffffu, fmaxf(fmaxf(t0, t2), fmaxf(t1, t3)) > limit)) {
-      float d0 = fmaxf(t0, t2), d1 = fmaxf(t1, t3);
+    float d0 = fmaxf(fmaxf(t[0][0], t[0][2]), fmaxf(t[1][0], t[1][2]));
+    float d1 = fmaxf(fmaxf(t[0][1], t[0][3]), fmaxf(t[1][1], t[1][3]));
+    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > limit)) {
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) {
         d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, k));
@@ -450,36 +491,43 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
       }
       m[0] += d0;
       m[1] += d1;
-      t0 -= d0;
-      t1 -= d1;
-      t2 -= d0;
-      t3 -= d1;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        t[hf][0] -= d0;
+        t[hf][1] -= d1;
+        t[hf][2] -= d0;
+        t[hf][3] -= d1;
+      }
       limit = 8.f;
     }
-    const float p0 = ex2_approx(t0), p1 = ex2_approx(t1), p2 = ex2_approx(t2), p3 = ex2_approx(t3);
-    l[0] += p0 + p2;
-    l[1] += p1 + p3;
-    const uint32_t b0 = movm_trans(pack_f16x2(p0, p1)), b1 = movm_trans(pack_f16x2(p2, p3));
+    uint32_t pb[2][2];  // B fragments of the probabilities
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const float p0 = ex2_approx(t[hf][0]), p1 = ex2_approx(t[hf][1]);
+      const float p2 = ex2_approx(t[hf][2]), p3 = ex2_approx(t[hf][3]);
+      l[0] += p0 + p2;
+      l[1] += p1 + p3;
+      pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
+      pb[hf][1] = movm_trans(pack_f16x2(p2, p3));
+    }
 
     // O^T += V^T P^T
-    {
-      uint32_t vw[4][VW], vpar[4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t vw[4][2], vpar[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const unsigned char* src = vst + ((u & 1) ? v_codes1 : v_codes0) + (u >> 1) * 8 * R;
-        if constexpr (VW == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(src);
-          vw[u][0] = w.x; vw[u][1] = w.y;
-        } else {
-          vw[u][0] = *reinterpret_cast<const uint32_t*>(src);
-        }
-        vpar[u] = *reinterpret_cast<const uint32_t*>(vst + ((u & 1) ? v_pars1 : v_pars0) + (u >> 1) * 8 * R);
+        const uint32_t row = st + (hf * kHalf + (u >> 1) * 8) * R;
+        if constexpr (VW == 2) lds64(vw[u], row + ((u & 1) ? v_codes1 : v_codes0));
+        else vw[u][0] = lds32(row + ((u & 1) ? v_codes1 : v_codes0));
+        vpar[u] = lds32(row + ((u & 1) ? v_pars1 : v_pars0));
       }
-      if (n < kTok) {
+      if (ragged) {
         // rows past the context meet probability 0 and must be finite
+        const int n = hf ? nn >> 8 : nn & 255;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (2 * tq + (u & 1) + (u >> 1) * 8 >= n) vpar[u] = 0u;
+          if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n) vpar[u] = 0u;
       }
       uint32_t vs[2], vc[2];
 #pragma unroll
@@ -490,23 +538,24 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
 #pragma unroll
       for (int j = 0; j < VW; ++j)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t xx[2], yy[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            xx[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], hf ? 0x7632 : 0x5410);
-            yy[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], hf ? 0x6723 : 0x4501);
+            xx[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x7632 : 0x5410);
+            yy[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x6723 : 0x4501);
           }
-          mma_f16(o[4 * j + 2 * hf], q4_pair(xx[0], vs[0], vc[0]), q4_pair(yy[0], vs[0], vc[0]),
-                  q4_pair(xx[1], vs[1], vc[1]), q4_pair(yy[1], vs[1], vc[1]), b0, b1);
-          mma_f16(o[4 * j + 2 * hf + 1], q4_pair(xx[0] << 4, vs[0], vc[0]), q4_pair(yy[0] << 4, vs[0], vc[0]),
-                  q4_pair(xx[1] << 4, vs[1], vc[1]), q4_pair(yy[1] << 4, vs[1], vc[1]), b0, b1);
+          mma_f16(o[4 * j + 2 * q], q4_pair(xx[0], vs[0], vc[0]), q4_pair(yy[0], vs[0], vc[0]),
+                  q4_pair(xx[1], vs[1], vc[1]), q4_pair(yy[1], vs[1], vc[1]), pb[hf][0], pb[hf][1]);
+          mma_f16(o[4 * j + 2 * q + 1], q4_pair(xx[0] << 4, vs[0], vc[0]), q4_pair(yy[0] << 4, vs[0], vc[0]),
+                  q4_pair(xx[1] << 4, vs[1], vc[1]), q4_pair(yy[1] << 4, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
         }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
 
     if (flags & 2) {  // last chunk of the share: write the result
+      const int b = md[0];
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
@@ -587,60 +636,72 @@ __global__ void __launch_bounds__(9 * 32, 2) decode_q4_kernel(const Q4Params p) 
     Ring ring;
     bool aborted = false;
     for (int xg = x0; xg < x1 && !aborted; xg += 32) {
+      // a lane looks up one of the next 32 chunks, then issues its copies in turn
       const int nvalid = min(32, x1 - xg);
       const int x = xg + lane;
-      int my_b = b, n = 0, flags = 0, new_slot = -1;
-      long long off = 0;
+      int my_b = b, n[2] = {0, 0}, flags = 0, new_slot = -1;
+      long long off[2] = {0, 0};
       if (lane < nvalid) {
         while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
         const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
-        const int jc = x - cb0;
-        const int t0 = jc * kTok;
-        n = min(kTok, k.ctx[my_b] - t0);
-        const int page = k.bt[static_cast<int64_t>(my_b) * k.maxp + (t0 >> k.log2P)];
-        if (page < 0 || page >= k.num_pages) {
-          raise_flag(k.err, PA_DEVERR_BAD_PAGE);
-          n = 0;
-        } else {
-          const long long slot0 = (static_cast<long long>(page) << k.log2P) + (t0 & (k.P - 1));
-          off = slot0 * k.row_bytes;
-          if (k.k_new != nullptr && x == cb1 - 1) new_slot = static_cast<int>(slot0) + n - 1;  // position context_len - 1
+        const int t0 = (x - cb0) * kTok;
+        const int left = k.ctx[my_b] - t0;
+        const int32_t* bt = k.bt + static_cast<int64_t>(my_b) * k.maxp;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int th = t0 + hf * kHalf, nh = min(kHalf, left - hf * kHalf);
+          if (nh <= 0) continue;
+          const int page = bt[th >> k.log2P];
+          if (page < 0 || page >= k.num_pages) {
+            raise_flag(k.err, PA_DEVERR_BAD_PAGE);
+            continue;
+          }
+          const long long slot0 = (static_cast<long long>(page) << k.log2P) + (th & (k.P - 1));
+          off[hf] = slot0 * k.row_bytes;
+          n[hf] = nh;
+          if (k.k_new != nullptr && th + nh == t0 + left) new_slot = static_cast<int>(slot0) + nh - 1;  // the last token
         }
-        flags = ((x == x0 || jc == 0) ? 1 : 0) | ((x == x1 - 1 || x == cb1 - 1) ? 2 : 0) |
+        flags = ((x == x0 || x == cb0) ? 1 : 0) | ((x == x1 - 1 || x == cb1 - 1) ? 2 : 0) |
                 ((cb0 >= x0 && cb1 <= x1) ? 4 : 0) | ((x == cb1 - 1) ? 8 : 0);
       }
       b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
       for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {
-        const int ub = __shfl_sync(0xffffffffu, my_b, u);
-        const int un = __shfl_sync(0xffffffffu, n, u);
-        const int uf = __shfl_sync(0xffffffffu, flags, u);
-        const long long uoff = __shfl_sync(0xffffffffu, off, u);
-        const int uslot = __shfl_sync(0xffffffffu, new_slot, u);
         int ok = 1;
-        if (lane == 0) {
+        if (lane == u) {
           const int s = ring.s;
           if (!mbar_wait_bounded(&empty[s], ring.phase ^ 1, abort_flag, k.err)) {
             ok = 0;
           } else {
-            meta[s] = make_int4(ub, un, uf, uslot);
+            meta[s] = make_int4(my_b, n[0] | n[1] << 8, flags, new_slot);
             // the new token's row is quantised by the consumers
-            const uint32_t rows = static_cast<uint32_t>(un) - (uslot >= 0 ? 1u : 0u);
-            const uint32_t bytes = rows * static_cast<uint32_t>(k.row_bytes);
-            mbar_arrive_expect_tx(&full[s], 2 * bytes);
-            if (bytes) {
-              unsigned char* dst = smem + static_cast<size_t>(s) * 2 * k.chunk_bytes;
-              bulk_g2s_hint(dst, k.k_cache + uoff, bytes, &full[s], pol);
-              bulk_g2s_hint(dst + k.chunk_bytes, k.v_cache + uoff, bytes, &full[s], pol);
+            int rows[2] = {n[0], n[1]};
+            if (new_slot >= 0) {
+              if (n[1]) --rows[1];
+              else --rows[0];
             }
-            if (k.k_new != nullptr && (uf & 8) && k.slot_out) k.slot_out[ub] = uslot;
-            ++issued;
+            unsigned char* dst = smem + static_cast<size_t>(s) * 2 * k.chunk_bytes;
+            const uint32_t rb = static_cast<uint32_t>(k.row_bytes);
+            mbar_arrive_expect_tx(&full[s], 2 * rb * static_cast<uint32_t>(rows[0] + rows[1]));
+            if (rows[0] == kHalf && off[1] == off[0] + kHalf * static_cast<long long>(rb)) {  // one run
+              rows[0] += rows[1];
+              rows[1] = 0;
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              if (rows[hf] > 0) {
+                bulk_g2s_hint(dst + hf * kHalf * rb, k.k_cache + off[hf], rows[hf] * rb, &full[s], pol);
+                bulk_g2s_hint(dst + hf * kHalf * rb + k.chunk_bytes, k.v_cache + off[hf], rows[hf] * rb, &full[s],
+                              pol);
+              }
+            if (k.k_new != nullptr && (flags & 8) && k.slot_out) k.slot_out[my_b] = new_slot;
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = __shfl_sync(0xffffffffu, ok, u);
         if (!ok) {
           aborted = true;
           break;
         }
+        ++issued;
       }
     }
     if (aborted && lane == 0) {
@@ -707,7 +768,7 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   pl.off_meta = place(kMaxStages * 16);
   pl.off_abort = place(16);
   pl.off_cs = place(static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4);
-  pl.off_p = place(simt ? static_cast<size_t>(pl.nw) * kTok * heads_padded(G) * 4 : 0);
+  pl.off_p = place(simt ? static_cast<size_t>(pl.nw) * kHalf * heads_padded(G) * 4 : 0);
   pl.off_alpha = place(simt ? static_cast<size_t>(pl.nw) * 8 * 4 : 0);
   // statistics, then the scaled queries
   pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4 : 0);
