@@ -317,12 +317,21 @@ PA_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
-// s * (16 + u) + c of the two codes in bits 6-9 and 22-25 of w.
-PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t s, uint32_t c) {
-  const uint32_t v = (w & 0x03C003C0u) | 0x4C004C00u;
-  uint32_t d;
+// s * (16 + u) + c of the two codes in bits 6-9 and 22-25 of w.  The mask-or is
+// one three-input logic instruction (LUT 0xEA: a & b | c) only when one of its
+// two constants is in a register: `sixteen` is 16 twice, kept there by keep_reg.
+constexpr uint32_t kSixteen = 0x4C004C00u;
+PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t sixteen, uint32_t s, uint32_t c) {
+  uint32_t v, d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(0x03C003C0), "r"(sixteen));
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(s), "r"(c));
   return d;
+}
+
+// A value the compiler takes for unknown, so that it stays in a register.
+PA_DEVINL uint32_t keep_reg(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
 // Loads from a shared-memory address.  Volatile: they stay between the wait for
@@ -364,6 +373,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
   const uint32_t v_pars0 = p.k.chunk_bytes + vt0 * R + p.codes + q4_swz(vp, p.pars, vt0);
   const uint32_t v_pars1 = p.k.chunk_bytes + vt1 * R + p.codes + q4_swz(vp, p.pars, vt1);
   const uint32_t smem0 = smem_u32(smem), meta0 = smem_u32(meta);
+  const uint32_t sixteen = keep_reg(kSixteen);
 
   uint32_t qf[MB][2];  // B fragments of the queries
   float o[MB][4];
@@ -441,10 +451,10 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
       for (int i = 0; i < KW; ++i) {
         const uint32_t w0 = kw[0][i], w1 = kw[1][i];
         const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
-        mma_f16(sc[hf], q4_pair(w0, ks[0], kc[0]), q4_pair(w1, ks[1], kc[1]), q4_pair(y0, ks[0], kc[0]),
-                q4_pair(y1, ks[1], kc[1]), qf[2 * i][0], qf[2 * i][1]);
-        mma_f16(sc[hf], q4_pair(w0 << 4, ks[0], kc[0]), q4_pair(w1 << 4, ks[1], kc[1]),
-                q4_pair(y0 << 4, ks[0], kc[0]), q4_pair(y1 << 4, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
+        mma_f16(sc[hf], q4_pair(w0, sixteen, ks[0], kc[0]), q4_pair(w1, sixteen, ks[1], kc[1]), q4_pair(y0, sixteen, ks[0], kc[0]),
+                q4_pair(y1, sixteen, ks[1], kc[1]), qf[2 * i][0], qf[2 * i][1]);
+        mma_f16(sc[hf], q4_pair(w0 << 4, sixteen, ks[0], kc[0]), q4_pair(w1 << 4, sixteen, ks[1], kc[1]),
+                q4_pair(y0 << 4, sixteen, ks[0], kc[0]), q4_pair(y1 << 4, sixteen, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
       }
     }
 
@@ -545,10 +555,10 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
             xx[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x7632 : 0x5410);
             yy[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x6723 : 0x4501);
           }
-          mma_f16(o[4 * j + 2 * q], q4_pair(xx[0], vs[0], vc[0]), q4_pair(yy[0], vs[0], vc[0]),
-                  q4_pair(xx[1], vs[1], vc[1]), q4_pair(yy[1], vs[1], vc[1]), pb[hf][0], pb[hf][1]);
-          mma_f16(o[4 * j + 2 * q + 1], q4_pair(xx[0] << 4, vs[0], vc[0]), q4_pair(yy[0] << 4, vs[0], vc[0]),
-                  q4_pair(xx[1] << 4, vs[1], vc[1]), q4_pair(yy[1] << 4, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
+          mma_f16(o[4 * j + 2 * q], q4_pair(xx[0], sixteen, vs[0], vc[0]), q4_pair(yy[0], sixteen, vs[0], vc[0]),
+                  q4_pair(xx[1], sixteen, vs[1], vc[1]), q4_pair(yy[1], sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
+          mma_f16(o[4 * j + 2 * q + 1], q4_pair(xx[0] << 4, sixteen, vs[0], vc[0]), q4_pair(yy[0] << 4, sixteen, vs[0], vc[0]),
+                  q4_pair(xx[1] << 4, sixteen, vs[1], vc[1]), q4_pair(yy[1] << 4, sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
         }
     }
     __syncwarp();
