@@ -17,15 +17,25 @@ constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
 
-// A chunk in the ring: its request, the tokens of its halves (n0 | n1 << 8, 0
-// for one whose page is out of range), flags, and the slot of the request's new
-// token when it is the last of these tokens (else -1).
-//   1 the first chunk of this CTA's share of the request   2 the last
-//   4 the share is the whole request                       8 the request's last chunk
+// A chunk in the ring, as the producer describes it to the consumers: its
+// request; the tokens of its halves (n0 | n1 << 8, 0 for a half whose page is
+// out of range) and flags; the share it belongs to; and the slot of the
+// request's new token when it is the last of these tokens (else -1).
+constexpr uint32_t kFirst = 1u << 16;  // the consumer group's first chunk of the request: the queries come with it
+constexpr uint32_t kLast = 1u << 17;   // the share's last chunk of the request: its group writes the result
+constexpr uint32_t kYield = 1u << 18;  // the other group's last chunk of the request: it hands its part over
+constexpr uint32_t kSolo = 1u << 19;   // with kLast: the other group has no part
+constexpr uint32_t kWhole = 1u << 20;  // the share holds the whole request
+constexpr uint32_t kRagged = 1u << 21; // a half has fewer than 16 tokens
+constexpr uint32_t kNew = 1u << 22;    // the request's new token is the last one
+constexpr uint32_t kEnd = 1u << 23;    // no chunk: the CTA's work is done
 
 struct Q4Params {
   KParams k;
   int32_t stages;       // ring depth
+  int32_t stage_bytes;  // K rows, V rows, queries
+  int32_t groups;       // consumer groups: 2 (tensor cores) or 1
+  uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, with its statistics
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
   uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
@@ -84,7 +94,7 @@ PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned cha
 // ---------------------------------------------------------------------------
 template <typename T, int HD, int GP>
 PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
-                             volatile int* abort_flag, int x0, int x1, int c) {
+                             volatile int* abort_flag) {
   constexpr int QD = HD / 4;
   constexpr int EL = HD / 32;
   constexpr int NH = GP > 4 ? 2 : 1;  // heads whose softmax a lane keeps
@@ -98,16 +108,17 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
   float* ml_s = reinterpret_cast<float*>(smem + p.k.off_ml) + warp * 16;
   float o[GP][EL];
   float m_run[NH], l_part[NH];
-  Ring ring;
-  for (int x = x0; x < x1; ++x, ring.next(p.stages)) {
+  for (Ring ring;; ring.next(p.stages)) {
     const int s = ring.s;
     if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
     const int4 md = meta[s];
-    const int b = md.x, n0 = md.y & 255, n1 = md.y >> 8, flags = md.z;
-    unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
+    const uint32_t flags = md.y;
+    if (flags & kEnd) break;
+    const int b = md.x, n0 = flags & 255, n1 = (flags >> 8) & 255;
+    unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
     unsigned char* vst = kst + p.k.chunk_bytes;
-    if (flags & 1) {  // first chunk of this CTA's share of request b
-      const T* qb = reinterpret_cast<const T*>(p.k.q) + (static_cast<int64_t>(b) * p.k.Hq + h * G) * HD;
+    if (flags & kFirst) {
+      const T* qb = reinterpret_cast<const T*>(kst + 2 * p.k.chunk_bytes) + h * G * HD;
       __syncwarp();
       for (int i = lane; i < GP * HD; i += 32)
         qs[i] = i < G * HD ? static_cast<float>(qb[i]) * p.k.scale_log2 : 0.f;
@@ -122,7 +133,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
         l_part[j] = 0.f;
       }
     }
-    if (md.w >= 0) write_new_row<T, HD>(p, kst, vst, b, n1 ? kHalf + n1 - 1 : n0 - 1, md.w, h, lane);
+    if (flags & kNew) write_new_row<T, HD>(p, kst, vst, b, n1 ? kHalf + n1 - 1 : n0 - 1, md.w, h, lane);
 
     for (int hf = 0; hf < 2; ++hf, kst += kHalf * R, vst += kHalf * R) {
     const int n = hf ? n1 : n0;
@@ -234,7 +245,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
     }
     if (lane == 0) mbar_arrive(&empty[s]);
 
-    if (flags & 2) {  // last chunk of the share: write the result
+    if (flags & kLast) {  // write the result
 #pragma unroll
       for (int j = 0; j < NH; ++j) {
         float l = l_part[j];
@@ -246,7 +257,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
         }
       }
       __syncwarp();
-      const bool whole = (flags & 4) != 0;
+      const bool whole = (flags & kWhole) != 0;
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
         if (g < G) {
@@ -258,7 +269,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 #pragma unroll
             for (int e = 0; e < EL; ++e) dst[e] = static_cast<T>(o[g][e] * inv);
           } else {
-            const int64_t slot = static_cast<int64_t>(c) + b;
+            const int64_t slot = static_cast<int64_t>(md.z) + b;
             float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + lane * EL;
 #pragma unroll
             for (int e = 0; e < EL; ++e) dst[e] = o[g][e] * inv;
@@ -349,12 +360,13 @@ PA_DEVINL void lds128(uint32_t (&r)[4], uint32_t a) {
 }
 
 template <int HD>
-PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
-                            volatile int* abort_flag, int x0, int x1, int c) {
+PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty,
+                            uint64_t* handed, uint64_t* taken, const int4* meta, volatile int* abort_flag, int h,
+                            int group) {
   constexpr int KW = HD / 32;  // words of K codes a lane holds per token
   constexpr int VW = HD / 64;  // words of V codes a lane holds per token
   constexpr int MB = HD / 16;  // 16-dim blocks of O
-  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int G = p.k.Hq / p.k.Hkv;
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t R = p.k.row_bytes, NG = HD >> p.log2gs;
@@ -381,28 +393,33 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
   float l[2] = {0.f, 0.f};     // this lane's part of the softmax sums
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
+  uint32_t hand_phase = 0;  // parity of the handovers so far
   Ring ring;
-  for (int x = x0; x < x1; ++x, ring.next(p.stages)) {
+  if (group) ring.next(p.stages);  // group g takes stages g, g + 2, ... of the ring
+  for (;; ring.next(p.stages), ring.next(p.stages)) {
     const int s = ring.s;
     if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
     uint32_t md[4];
     lds128(md, meta0 + s * 16);
-    const uint32_t nn = md[1], flags = md[2];
-    const uint32_t st = smem0 + s * 2 * p.k.chunk_bytes;
+    const uint32_t flags = md[1];
+    const uint32_t st = smem0 + s * p.stage_bytes;
 
-    if (flags & 1) {  // first chunk of this CTA's share of the request
-      const char* qrow =
-          p.k.q + ((static_cast<int64_t>(md[0]) * p.k.Hq + h * G + gq) * HD + tq * (HD / 4)) * 2;
+    if (flags & (kFirst | kNew | kEnd)) {
+    if (flags & kEnd) break;
+    if (flags & kFirst) {
+      const uint32_t qrow = st + 2 * p.k.chunk_bytes + ((h * G + gq) * HD + tq * (HD / 4)) * 2;
       float qv[HD / 4];
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < HD / 32; ++i) {
-        float v8[8] = {};
-        if (gq < G) q4_load8<__nv_bfloat16>(qrow + i * 16, v8);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (gq < G) lds128(w, qrow + i * 16);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          qv[8 * i + e] = v8[e];
-          mx = fmaxf(mx, fabsf(v8[e]));
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = bf16x2_to_float2(w[e]);
+          qv[8 * i + 2 * e] = v.x;
+          qv[8 * i + 2 * e + 1] = v.y;
+          mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
         }
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -424,11 +441,12 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
       m[0] = m[1] = l[0] = l[1] = 0.f;
       limit = -INFINITY;
     }
-    if (static_cast<int>(md[3]) >= 0) {
-      unsigned char* kst = smem + static_cast<size_t>(s) * 2 * p.k.chunk_bytes;
-      const uint32_t n0 = nn & 255, n1 = nn >> 8;
+    if (flags & kNew) {
+      unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
+      const uint32_t n0 = flags & 255, n1 = (flags >> 8) & 255;
       write_new_row<__nv_bfloat16, HD>(p, kst, kst + p.k.chunk_bytes, md[0], n1 ? kHalf + n1 - 1 : n0 - 1, md[3], h,
                                        lane);
+    }
     }
 
     // S^T = K Q^T of both halves
@@ -465,11 +483,10 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[hf][e], mult[e & 1], -m[e & 1]);
-    const bool ragged = nn != (kHalf | kHalf << 8);
-    if (ragged) {
+    if (flags & kRagged) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int n = hf ? nn >> 8 : nn & 255;
+        const int n = (flags >> (8 * hf)) & 255;
         if (kt >= n) t[hf][0] = t[hf][1] = -INFINITY;
         if (kt + 8 >= n) t[hf][2] = t[hf][3] = -INFINITY;
       }
@@ -532,9 +549,9 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
         else vw[u][0] = lds32(row + ((u & 1) ? v_codes1 : v_codes0));
         vpar[u] = lds32(row + ((u & 1) ? v_pars1 : v_pars0));
       }
-      if (ragged) {
+      if (flags & kRagged) {
         // rows past the context meet probability 0 and must be finite
-        const int n = hf ? nn >> 8 : nn & 255;
+        const int n = (flags >> (8 * hf)) & 255;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n) vpar[u] = 0u;
@@ -564,12 +581,60 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
 
-    if (flags & 2) {  // last chunk of the share: write the result
+    if (flags & (kLast | kYield)) {
       const int b = md[0];
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
         l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+      }
+      if (flags & kYield) {
+        // hand this group's part over: once the previous one has been taken
+        if (!mbar_wait_bounded(&taken[h], hand_phase ^ 1, abort_flag, p.k.err)) break;
+        hand_phase ^= 1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int g = 2 * tq + e;
+          if (g < G) {
+            float* dst = reinterpret_cast<float*>(smem + p.off_hand) + (h * G + g) * (HD + 4);
+#pragma unroll
+            for (int j = 0; j < MB; j += 2)
+              *reinterpret_cast<float4*>(dst + gq * (HD / 8) + 2 * j) =
+                  make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
+            if (gq == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(m[e], l[e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&handed[h]);
+        continue;
+      }
+      if (!(flags & kSolo)) {
+        // add the other group's part
+        if (!mbar_wait_bounded(&handed[h], hand_phase, abort_flag, p.k.err)) break;
+        hand_phase ^= 1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int g = 2 * tq + e;
+          if (g < G) {
+            const float* src = reinterpret_cast<const float*>(smem + p.off_hand) + (h * G + g) * (HD + 4);
+            const float2 ml = *reinterpret_cast<const float2*>(src + HD);
+            // a part without tokens (bad pages) has sum 0 and no say in the reference
+            const float mm = ml.y == 0.f ? m[e] : l[e] == 0.f ? ml.x : fmaxf(m[e], ml.x);
+            const float wa = l[e] == 0.f ? 0.f : ex2_approx(m[e] - mm), wb = ml.y == 0.f ? 0.f : ex2_approx(ml.x - mm);
+            m[e] = mm;
+            l[e] = l[e] * wa + ml.y * wb;
+#pragma unroll
+            for (int j = 0; j < MB; j += 2) {
+              const float4 v = *reinterpret_cast<const float4*>(src + gq * (HD / 8) + 2 * j);
+              o[j][e] = o[j][e] * wa + v.x * wb;
+              o[j][2 + e] = o[j][2 + e] * wa + v.y * wb;
+              o[j + 1][e] = o[j + 1][e] * wa + v.z * wb;
+              o[j + 1][2 + e] = o[j + 1][2 + e] * wa + v.w * wb;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[h]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -577,7 +642,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
         if (g < G) {
           const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
           const int hq = h * G + g;
-          if (flags & 4) {
+          if (flags & kWhole) {
             char* dst = p.k.out + ((static_cast<int64_t>(b) * p.k.Hq + hq) * HD + gq * (HD / 8)) * 2;
 #pragma unroll
             for (int j = 0; j < MB; j += 4)
@@ -586,7 +651,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
                                             pack_bf16x2(o[j + 2][e] * inv, o[j + 2][2 + e] * inv),
                                             pack_bf16x2(o[j + 3][e] * inv, o[j + 3][2 + e] * inv)));
           } else {
-            const int64_t slot = static_cast<int64_t>(c) + b;
+            const int64_t slot = static_cast<int64_t>(md[2]) + b;
             float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + gq * (HD / 8);
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
@@ -601,31 +666,181 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
   }
 }
 
-template <typename T, int HD, int GP>
-__global__ void __launch_bounds__(9 * 32, 2) decode_q4_kernel(const Q4Params p) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  const KParams& k = p.k;
-  const int c = blockIdx.x;
-  const int NW = k.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// ---------------------------------------------------------------------------
+// producer warp
+// ---------------------------------------------------------------------------
+// The chunk prefix sums of up to kInlinePlanMax requests, by one warp into
+// shared memory: each lane sums a run of consecutive requests, so one round
+// trip of loads and one warp scan.  `first` (the warp of share 0) also does the
+// plan's side work, as plan_in_cta.
+PA_DEVINL int plan_in_warp(const KParams& k, int32_t* cs_s, bool first, int lane) {
+  const int cap = static_cast<int>(min(static_cast<int64_t>(k.max_ctx), static_cast<int64_t>(k.maxp) << k.log2P));
+  const int per = (k.B + 31) / 32;
+  const int b0 = min(k.B, lane * per), b1 = min(k.B, b0 + per);
+  int sum = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
+    const int L = k.ctx[b];
+    int cnt = 0;
+    if (L >= 1 && L <= cap) {
+      cnt = (L + kTok - 1) / kTok;
+    } else if (first) {
+      // length 0 is a padding row: nothing is read, stored or written for it
+      if (L != 0) raise_flag(k.err, PA_DEVERR_BAD_LENGTH);
+      if (k.k_new != nullptr && k.slot_out) k.slot_out[b] = -1;
+    }
+    cs_s[b + 1] = cnt;
+    sum += cnt;
+  }
+  int x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  int run = x - sum;
+  for (int b = b0; b < b1; ++b) {
+    run += cs_s[b + 1];
+    cs_s[b + 1] = run;
+  }
+  if (lane == 0) cs_s[0] = 0;
+  __syncwarp();
+  if (first)
+    for (int b = lane; b <= k.B; b += 32) k.cs[b] = cs_s[b];
+  return __shfl_sync(0xffffffffu, x, 31);
+}
 
-  const int32_t* cs;  // [B+1] chunk prefix sums
+// Fills the ring with the chunks of this CTA's share.
+PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, int4* meta,
+                       volatile int* abort_flag, int lane) {
+  const KParams& k = p.k;
+  const uint64_t pol = l2_policy_evict_first();
+  const int32_t* cs;
+  int NC;
   if (k.inline_plan) {
     int32_t* cs_s = reinterpret_cast<int32_t*>(smem + k.off_cs);
-    plan_in_cta(k, cs_s, cs_s + kInlinePlanMax + 1, c == 0);
+    NC = plan_in_warp(k, cs_s, blockIdx.x == 0, lane);
     cs = cs_s;
   } else {
-    pdl_wait();  // the plan kernel's chunk sums and CTA starts are complete
+    pdl_wait();  // the plan kernel's chunk sums are complete
     cs = k.cs;
+    NC = cs[k.B];
   }
-  pdl_trigger();  // the merge kernel may start launching; it waits for this grid
-  const int NC = cs[k.B];
+  const int c = blockIdx.x;
   const int x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
   const int x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
-  if (x0 >= x1) return;
+  const uint32_t rb = static_cast<uint32_t>(k.row_bytes), q_bytes = p.stage_bytes - 2 * k.chunk_bytes;
+  int b = x0 < x1 ? first_request(cs, k.B, x0) : 0;
+  int issued = 0;
+  Ring ring;
+  bool aborted = false;
+  for (int xg = x0; xg < x1 && !aborted; xg += 32) {
+    // a lane looks up one of the next 32 chunks, then issues its copies in turn
+    const int nvalid = min(32, x1 - xg);
+    const int x = xg + lane;
+    int my_b = b, n[2] = {0, 0}, new_slot = -1;
+    uint32_t flags = 0;
+    bool ends = false;
+    long long off[2] = {0, 0};
+    if (lane < nvalid) {
+      while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
+      const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
+      const int t0 = (x - cb0) * kTok;
+      const int left = k.ctx[my_b] - t0;
+      const int32_t* bt = k.bt + static_cast<int64_t>(my_b) * k.maxp;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int th = t0 + hf * kHalf, nh = min(kHalf, left - hf * kHalf);
+        if (nh <= 0) continue;
+        const int page = bt[th >> k.log2P];
+        if (page < 0 || page >= k.num_pages) {
+          raise_flag(k.err, PA_DEVERR_BAD_PAGE);
+          continue;
+        }
+        const long long slot0 = (static_cast<long long>(page) << k.log2P) + (th & (k.P - 1));
+        off[hf] = slot0 * k.row_bytes;
+        n[hf] = nh;
+        if (k.k_new != nullptr && th + nh == t0 + left) new_slot = static_cast<int>(slot0) + nh - 1;  // the last token
+      }
+      ends = x == cb1 - 1;
+      const int xa = max(x0, cb0), xb = min(x1, cb1);  // the request's chunks in this share
+      flags = (x < xa + p.groups ? kFirst : 0u) | (x == xb - 1 ? kLast : 0u) |
+              (p.groups == 2 && x == xb - 2 ? kYield : 0u) | (p.groups == 1 || xb - xa == 1 ? kSolo : 0u) |
+              (cb0 >= x0 && cb1 <= x1 ? kWhole : 0u) | (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) |
+              (new_slot >= 0 ? kNew : 0u);
+    }
+    b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
+    for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {
+      int ok = 1;
+      if (lane == u) {
+        const int s = ring.s;
+        if (!mbar_wait_bounded(&empty[s], ring.phase ^ 1, abort_flag, k.err)) {
+          ok = 0;
+        } else {
+          meta[s] = make_int4(my_b, n[0] | n[1] << 8 | static_cast<int>(flags), c, new_slot);
+          // the new token's row is quantised by the consumers
+          int rows0 = n[0], rows1 = n[1];
+          if (new_slot >= 0) {
+            if (rows1) --rows1;
+            else --rows0;
+          }
+          const uint32_t qb = (flags & kFirst) ? q_bytes : 0u;
+          unsigned char* dst = smem + static_cast<size_t>(s) * p.stage_bytes;
+          mbar_arrive_expect_tx(&full[s], 2 * rb * static_cast<uint32_t>(rows0 + rows1) + qb);
+          if (rows0 == kHalf && off[1] == off[0] + kHalf * static_cast<long long>(rb)) {  // one run
+            rows0 += rows1;
+            rows1 = 0;
+          }
+          if (qb) bulk_g2s(dst + 2 * k.chunk_bytes, k.q + static_cast<int64_t>(my_b) * q_bytes, qb, &full[s]);
+          if (rows0 > 0) {
+            bulk_g2s_hint(dst, k.k_cache + off[0], rows0 * rb, &full[s], pol);
+            bulk_g2s_hint(dst + k.chunk_bytes, k.v_cache + off[0], rows0 * rb, &full[s], pol);
+          }
+          if (rows1 > 0) {
+            bulk_g2s_hint(dst + kHalf * rb, k.k_cache + off[1], rows1 * rb, &full[s], pol);
+            bulk_g2s_hint(dst + k.chunk_bytes + kHalf * rb, k.v_cache + off[1], rows1 * rb, &full[s], pol);
+          }
+          if (k.k_new != nullptr && ends && k.slot_out) k.slot_out[my_b] = new_slot;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, u);
+      if (!ok) {
+        aborted = true;
+        break;
+      }
+      ++issued;
+    }
+  }
+  if (lane == 0) {
+    if (aborted) {
+      // Copies already issued may still be landing: wait for them (time only).
+      for (int it = max(0, issued - p.stages); it < issued; ++it)
+        drain_wait(&full[it % p.stages], (it / p.stages) & 1);
+    } else {
+      for (int g = 0; g < p.groups; ++g, ring.next(p.stages)) {  // one end for each group
+        if (!mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, abort_flag, k.err)) break;
+        meta[ring.s] = make_int4(0, static_cast<int>(kEnd), 0, -1);
+        mbar_arrive(&full[ring.s]);
+      }
+    }
+  }
+}
 
+// bf16: two groups of one consumer warp per kv-head, which take the chunks in
+// turn from one ring, and the producer; fp32: one group.
+template <typename T, int HD, int GP>
+constexpr int kMaxThreads = sizeof(T) == 2 ? 17 * 32 : 9 * 32;
+
+template <typename T, int HD, int GP>
+__global__ void __launch_bounds__(kMaxThreads<T, HD, GP>, sizeof(T) == 2 ? 1 : 2) decode_q4_kernel(const Q4Params p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const KParams& k = p.k;
+  const int NW = k.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + k.off_bar);
   uint64_t* empty = full + kMaxStages;
+  uint64_t* handed = empty + kMaxStages;  // [8] per kv-head: a part is in its place
+  uint64_t* taken = handed + 8;           // [8] it has been added
   int4* meta = reinterpret_cast<int4*>(smem + k.off_meta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + k.off_abort);
   if (threadIdx.x == 0) {
@@ -633,98 +848,26 @@ __global__ void __launch_bounds__(9 * 32, 2) decode_q4_kernel(const Q4Params p) 
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], NW);
     }
+    for (int h = 0; h < NW; ++h) {
+      mbar_init(&handed[h], 1);
+      mbar_init(&taken[h], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   cta_sync();
+  pdl_trigger();  // the merge kernel may start launching; it waits for this grid
 
-  if (warp == NW) {
-    // ------------------------------ producer ------------------------------
-    const uint64_t pol = l2_policy_evict_first();
-    int b = k.inline_plan ? first_request(cs, k.B, x0) : k.cta_seq[c];
-    int issued = 0;
-    Ring ring;
-    bool aborted = false;
-    for (int xg = x0; xg < x1 && !aborted; xg += 32) {
-      // a lane looks up one of the next 32 chunks, then issues its copies in turn
-      const int nvalid = min(32, x1 - xg);
-      const int x = xg + lane;
-      int my_b = b, n[2] = {0, 0}, flags = 0, new_slot = -1;
-      long long off[2] = {0, 0};
-      if (lane < nvalid) {
-        while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
-        const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
-        const int t0 = (x - cb0) * kTok;
-        const int left = k.ctx[my_b] - t0;
-        const int32_t* bt = k.bt + static_cast<int64_t>(my_b) * k.maxp;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int th = t0 + hf * kHalf, nh = min(kHalf, left - hf * kHalf);
-          if (nh <= 0) continue;
-          const int page = bt[th >> k.log2P];
-          if (page < 0 || page >= k.num_pages) {
-            raise_flag(k.err, PA_DEVERR_BAD_PAGE);
-            continue;
-          }
-          const long long slot0 = (static_cast<long long>(page) << k.log2P) + (th & (k.P - 1));
-          off[hf] = slot0 * k.row_bytes;
-          n[hf] = nh;
-          if (k.k_new != nullptr && th + nh == t0 + left) new_slot = static_cast<int>(slot0) + nh - 1;  // the last token
-        }
-        flags = ((x == x0 || x == cb0) ? 1 : 0) | ((x == x1 - 1 || x == cb1 - 1) ? 2 : 0) |
-                ((cb0 >= x0 && cb1 <= x1) ? 4 : 0) | ((x == cb1 - 1) ? 8 : 0);
-      }
-      b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
-      for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {
-        int ok = 1;
-        if (lane == u) {
-          const int s = ring.s;
-          if (!mbar_wait_bounded(&empty[s], ring.phase ^ 1, abort_flag, k.err)) {
-            ok = 0;
-          } else {
-            meta[s] = make_int4(my_b, n[0] | n[1] << 8, flags, new_slot);
-            // the new token's row is quantised by the consumers
-            int rows[2] = {n[0], n[1]};
-            if (new_slot >= 0) {
-              if (n[1]) --rows[1];
-              else --rows[0];
-            }
-            unsigned char* dst = smem + static_cast<size_t>(s) * 2 * k.chunk_bytes;
-            const uint32_t rb = static_cast<uint32_t>(k.row_bytes);
-            mbar_arrive_expect_tx(&full[s], 2 * rb * static_cast<uint32_t>(rows[0] + rows[1]));
-            if (rows[0] == kHalf && off[1] == off[0] + kHalf * static_cast<long long>(rb)) {  // one run
-              rows[0] += rows[1];
-              rows[1] = 0;
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              if (rows[hf] > 0) {
-                bulk_g2s_hint(dst + hf * kHalf * rb, k.k_cache + off[hf], rows[hf] * rb, &full[s], pol);
-                bulk_g2s_hint(dst + hf * kHalf * rb + k.chunk_bytes, k.v_cache + off[hf], rows[hf] * rb, &full[s],
-                              pol);
-              }
-            if (k.k_new != nullptr && (flags & 8) && k.slot_out) k.slot_out[my_b] = new_slot;
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, u);
-        if (!ok) {
-          aborted = true;
-          break;
-        }
-        ++issued;
-      }
-    }
-    if (aborted && lane == 0) {
-      // Copies already issued may still be landing: wait for them (time only).
-      for (int it = max(0, issued - p.stages); it < issued; ++it)
-        drain_wait(&full[it % p.stages], (it / p.stages) & 1);
-    }
+  if (warp == NW * p.groups) {
+    produce(p, smem, full, empty, meta, abort_flag, lane);
     return;
   }
-  if constexpr (sizeof(T) == 2)
-    mma_consumer<HD>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
-  else
-    simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag, x0, x1, c);
+  if constexpr (sizeof(T) == 2) {
+    const int group = warp >= NW;
+    mma_consumer<HD>(p, smem, full, empty, handed, taken, meta, abort_flag, warp - group * NW, group);
+  } else {
+    simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag);
+  }
 }
 
 struct Fns {
@@ -751,6 +894,14 @@ Fns get_fns(int dtype, int hd, int G) {
   return hd == 128 ? fns_for<float, 128>(G) : fns_for<float, 64>(G);
 }
 
+// Bytes of a ring stage: a chunk's rows of K and V, and a request's queries.
+size_t q4_stage_bytes(const pa_cache_desc& d, const DecodePlan& pl) {
+  return 2 * static_cast<size_t>(pl.chunk_bytes) +
+         static_cast<size_t>(d.num_q_heads) * d.head_dim * elem_bytes(d.dtype);
+}
+
+int q4_groups(const pa_cache_desc& d) { return d.dtype == PA_BF16 ? 2 : 1; }
+
 int heads_padded(int G) { return G <= 2 ? G : G <= 4 ? 4 : 8; }
 
 }  // namespace
@@ -761,7 +912,7 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   if (e != cudaSuccess) return e;
   const int G = d.num_q_heads / d.num_kv_heads;
   DecodePlan pl;
-  pl.nw = d.num_kv_heads;
+  pl.nw = d.num_kv_heads * q4_groups(d);  // consumer warps
   pl.tokens_per_chunk = kTok;
   pl.row_pitch = q4_row_bytes(d, gs);
   pl.chunk_bytes = kTok * pl.row_pitch;
@@ -774,18 +925,19 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
     off = align_up(off + bytes, 16);
     return static_cast<uint32_t>(at);
   };
-  pl.off_bar = place(2 * kMaxStages * sizeof(uint64_t));
+  pl.off_bar = place((2 * kMaxStages + 16) * sizeof(uint64_t));
   pl.off_meta = place(kMaxStages * 16);
   pl.off_abort = place(16);
   pl.off_cs = place(static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4);
   pl.off_p = place(simt ? static_cast<size_t>(pl.nw) * kHalf * heads_padded(G) * 4 : 0);
   pl.off_alpha = place(simt ? static_cast<size_t>(pl.nw) * 8 * 4 : 0);
   // statistics, then the scaled queries
-  pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4 : 0);
+  pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4
+                         : static_cast<size_t>(d.num_q_heads) * (d.head_dim + 4) * 4);  // or the handed-over part
   // The ring takes what is left of a CTA's share of the SM's shared memory with
-  // 16 consumer warps on an SM (two CTAs at 8 kv-heads): about 5 chunks.
-  const size_t fixed = align_up(off, 128), stage = 2 * static_cast<size_t>(pl.chunk_bytes);
-  const size_t share = static_cast<size_t>(di.max_smem_optin) * pl.nw / 16 - 1024;
+  // 16 consumer warps on an SM: four or more chunks.
+  const size_t fixed = align_up(off, 128), stage = q4_stage_bytes(d, pl);
+  const size_t share = static_cast<size_t>(di.max_smem_optin) * std::min(pl.nw, 16) / 16 - 1024;
   pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, share > fixed ? (share - fixed) / stage : 0)));
   const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
   for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
@@ -811,10 +963,13 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   Q4Params p{};
   p.k = decode_params(d, pl, a, q4_row_bytes(d, gs));
   p.stages = pl.stages;
+  p.stage_bytes = static_cast<int32_t>(q4_stage_bytes(d, pl));
   p.codes = q4_codes_bytes(d);
   p.pars = p.k.row_bytes - p.codes;
   while ((1 << p.log2gs) < gs) ++p.log2gs;
+  p.groups = q4_groups(d);
   p.off_q = pl.off_ml + pl.nw * 16 * 4;
+  p.off_hand = pl.off_ml;
   void* args[] = {&p};
   return launch_decode_kernels(f.main, f.merge, pl, p.k, args, s);
 }
