@@ -151,9 +151,28 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+# The current device's index and its current stream's handle, as torch.cuda.current_device() and
+# current_stream().cuda_stream give them, without their layers of checks: those took 4 us of a call's 14.
+_current_device = None
+_raw_stream = None
+
+
+def _find_cuda() -> bool:
+    """Whether there is a CUDA device; sets up the two lookups above once there is."""
+    global _current_device, _raw_stream
+    if not torch.cuda.is_available():
+        return False
+    torch.cuda.init()
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _current_device = torch._C._cuda_getDevice
+    return True
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if _current_device is None and not _find_cuda():
+            return None
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -283,22 +302,21 @@ def pa_prefill_workspace_size(desc, batch, max_seqlen_q, num_tokens, max_context
 
 def pa_q4_row_bytes(desc, group_size) -> int:
     """Bytes of one token's row of a 4-bit K or V cache (0: not supported)."""
-    return int(load_library().pa_q4_row_bytes(ctypes.byref(desc), group_size))
+    return int(load_library().pa_q4_row_bytes(desc, group_size))
 
 
-def _q4_caches(fn, desc, group_size, *caches):
+def _q4_caches(fn, desc, group_size, k_cache, v_cache):
     """A 4-bit cache given as a tensor is contiguous uint8 on the current device and holds every row of the
     descriptor: a cache of the dtype's rows, or one allocated for another group size, is refused here."""
-    row = load_library().pa_q4_row_bytes(ctypes.byref(desc), group_size)
-    need = desc.num_pages * desc.page_size * row
-    for t in caches:
+    need = desc.num_pages * desc.page_size * load_library().pa_q4_row_bytes(desc, group_size)
+    for t in (k_cache, v_cache):
         if not isinstance(t, torch.Tensor):
             continue
-        if t.dtype != torch.uint8:
+        if t.dtype is not torch.uint8:
             raise PagedAttnError(fn, PA_ERR_DTYPE, f"a 4-bit cache is a uint8 tensor, not {t.dtype}")
-        if not t.is_contiguous() or t.numel() < need:
+        if t.numel() < need or not t.is_contiguous():
             raise PagedAttnError(fn, PA_ERR_SHAPE, f"a 4-bit cache is contiguous and has at least {need} bytes")
-        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        if (_current_device is None and not _find_cuda()) or t.get_device() != _current_device():
             raise PagedAttnError(fn, PA_ERR_UNSUPPORTED, f"the cache is on {t.device}, not on the current CUDA device")
 
 
@@ -307,7 +325,7 @@ def pa_kv_write_q4(desc, group_size, k, k_row_stride, v, v_row_stride, num_token
     lib = load_library()
     _q4_caches("pa_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_kv_write_q4", lib.pa_kv_write_q4(
-        ctypes.byref(desc), group_size, _ptr(k), k_row_stride, _ptr(v), v_row_stride, num_tokens, _ptr(slot_mapping),
+        desc, group_size, _ptr(k), k_row_stride, _ptr(v), v_row_stride, num_tokens, _ptr(slot_mapping),
         _ptr(k_cache), _ptr(v_cache), _stream(stream)))
 
 
@@ -317,7 +335,7 @@ def pa_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stri
     lib = load_library()
     _q4_caches("pa_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_qk_norm_rope_kv_write_q4", lib.pa_qk_norm_rope_kv_write_q4(
-        ctypes.byref(desc), group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+        desc, group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
         num_tokens, _ptr(positions), _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(slot_mapping),
         _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _stream(stream)))
 
@@ -329,7 +347,7 @@ def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_
     lib = load_library()
     _q4_caches("pa_prefill_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_prefill_qk_norm_rope_kv_write_q4", lib.pa_prefill_qk_norm_rope_kv_write_q4(
-        ctypes.byref(desc), group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+        desc, group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
         num_tokens, _ptr(cu_seqlens_q), batch, _ptr(context_lens), _ptr(block_tables), max_pages_per_seq,
         _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
         _ptr(positions_out), _ptr(slot_mapping_out), _stream(stream)))
@@ -341,13 +359,13 @@ def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_
     lib = load_library()
     _q4_caches("pa_kv_read_q4", desc, group_size, k_cache, v_cache)
     _check("pa_kv_read_q4", lib.pa_kv_read_q4(
-        ctypes.byref(desc), group_size, batch, _ptr(cu_rows), _ptr(starts), _ptr(context_lens), _ptr(block_tables),
+        desc, group_size, batch, _ptr(cu_rows), _ptr(starts), _ptr(context_lens), _ptr(block_tables),
         max_pages_per_seq, num_rows, _ptr(k_cache), _ptr(v_cache), _ptr(k_out), k_row_stride, _ptr(v_out),
         v_row_stride, _stream(stream)))
 
 
 def pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas=0) -> int:
-    return int(load_library().pa_decode_q4_workspace_size(ctypes.byref(desc), group_size, batch, max_context_len,
+    return int(load_library().pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len,
                                                           max_ctas))
 
 
@@ -358,7 +376,7 @@ def pa_decode_q4(desc, group_size, q, batch, k_cache, v_cache, block_tables, max
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("pa_decode_q4", lib.pa_decode_q4(
-        ctypes.byref(desc), group_size, _ptr(q), batch, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        desc, group_size, _ptr(q), batch, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
         max_pages_per_seq, _ptr(context_lens), max_context_len, scale, max_ctas, _ptr(out), _ptr(workspace),
         workspace_bytes, _stream(stream)))
 
@@ -371,7 +389,7 @@ def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("pa_decode_kv_write_q4", lib.pa_decode_kv_write_q4(
-        ctypes.byref(desc), group_size, _ptr(q), _ptr(k_new), k_row_stride, _ptr(v_new), v_row_stride, batch,
+        desc, group_size, _ptr(q), _ptr(k_new), k_row_stride, _ptr(v_new), v_row_stride, batch,
         _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_pages_per_seq, _ptr(context_lens), max_context_len,
         scale, max_ctas, _ptr(slot_mapping), _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
 
