@@ -65,11 +65,11 @@ PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned cha
   const char* src = (isv ? p.k.v_new + static_cast<int64_t>(b) * p.k.v_new_stride
                          : p.k.k_new + static_cast<int64_t>(b) * p.k.k_new_stride) +
                     (h * HD + l * 8) * sizeof(T);
-  float x[8];
-  q4_load8<T>(src, x);
+  uint32_t words[kQ4Words<T>];
+  q4_load8<T>(src, words);
   const int gl = 1 << (p.log2gs - 3);
   uint32_t par;
-  const uint32_t w = q4_quantise8(x, gl, par);
+  const uint32_t w = q4_quantise8<T>(words, gl, par);
   if (lane < 2 * LPR) {
     unsigned char* row = (isv ? vst : kst) + t * p.k.row_bytes;
     char* dst = const_cast<char*>(isv ? p.k.v_cache : p.k.k_cache) + static_cast<int64_t>(slot) * p.k.row_bytes;
@@ -156,14 +156,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
         const int t = gq + 8 * u;
         const uint32_t w = *reinterpret_cast<const uint32_t*>(
             kst + t * R + q4_swz(h * (HD / 2) + tq * (QD / 2) + c8 * 4, p.codes, t));
-        float a[4], bb[4];
-        q4_decode4(w & 0xFFFFu, sc[u].x, sc[u].y, a);
-        q4_decode4(w >> 16, sc[u].x, sc[u].y, bb);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xk[u][e] = a[e];
-          xk[u][4 + e] = bb[e];
-        }
+        q4_decode8(w, sc[u].x, sc[u].y, xk[u]);
       }
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
@@ -224,8 +217,8 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
           vst + t * R + p.codes + q4_swz((h * NG + ((lane * EL) >> p.log2gs)) * 4, p.pars, t)));
       const uint32_t hw = *reinterpret_cast<const uint16_t*>(
           vst + t * R + q4_swz(h * (HD / 2) + (lane * EL / 4) * 2, p.codes, t));
-      float a[4];
-      q4_decode4(hw, scv.x, scv.y, a);
+      float a[8];
+      q4_decode8(hw, scv.x, scv.y, a);
       float xv[EL];
       if constexpr (EL == 4) {
 #pragma unroll

@@ -190,48 +190,32 @@ PA_DEVINL void map_token(const NormRopeParams& p, int64_t t, bool report, int& p
   map_token_of(p, t, lo, p.cu[lo], p.cu[lo + 1], p.ctx[lo], report, pos, slot);
 }
 
-// One head's rotated k (four dims of each half per lane, HD / 8 lanes a head),
-// quantised into head h of a 4-bit row.  All 32 lanes take part.
-template <int HD, int GS>
-PA_DEVINL void store_q4_halves(float (&a)[4], float (&b)[4], int l, bool store, char* row, int h, uint32_t codes,
-                               uint32_t pars, uint32_t t) {
+// One head's rotated k (words of four dims of each half per lane, HD / 8 lanes
+// a head), quantised into head h of a 4-bit row.  All 32 lanes take part.
+template <typename T, int HD, int GS>
+PA_DEVINL void store_q4_halves(const uint32_t (&wa)[sizeof(T)], const uint32_t (&wb)[sizeof(T)], int l, bool store,
+                               char* row, int h, uint32_t codes, uint32_t pars, uint32_t t) {
   constexpr bool kWhole = GS == HD;                // one group: both halves
   constexpr int GL = kWhole ? HD / 8 : GS / 4;     // lanes of a group
-  float mna = INFINITY, mxa = -INFINITY, mnb = INFINITY, mxb = -INFINITY;
-  int bad_a = 0, bad_b = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bad_a |= q4_bad(a[e]);
-    bad_b |= q4_bad(b[e]);
-    a[e] = q4_clamp(a[e]);
-    b[e] = q4_clamp(b[e]);
-    mna = fminf(mna, a[e]);
-    mxa = fmaxf(mxa, a[e]);
-    mnb = fminf(mnb, b[e]);
-    mxb = fmaxf(mxb, b[e]);
-  }
-  if constexpr (kWhole) {
-    mna = fminf(mna, mnb);
-    mxa = fmaxf(mxa, mxb);
-    bad_a |= bad_b;
-  }
+  Q4Range<T> ra, rb;
+  ra.of_words(wa);
+  rb.of_words(wb);
+  if constexpr (kWhole) ra.join(rb);
 #pragma unroll
   for (int m = 1; m < GL; m <<= 1) {
-    mna = fminf(mna, __shfl_xor_sync(0xffffffffu, mna, m));
-    mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, m));
-    bad_a |= __shfl_xor_sync(0xffffffffu, bad_a, m);
-    if constexpr (!kWhole) {
-      mnb = fminf(mnb, __shfl_xor_sync(0xffffffffu, mnb, m));
-      mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, m));
-      bad_b |= __shfl_xor_sync(0xffffffffu, bad_b, m);
-    }
+    ra.reduce(m);
+    if constexpr (!kWhole) rb.reduce(m);
   }
-  const Q4Group ga = q4_group(mna, mxa, bad_a != 0);
-  const Q4Group gb = kWhole ? ga : q4_group(mnb, mxb, bad_b != 0);
+  const Q4Group ga = ra.group();
+  const Q4Group gb = kWhole ? ga : rb.group();
   if (!store) return;
+  float a[4], b[4];
+  q4_widen<T>(wa, a);
+  q4_widen<T>(wb, b);
+  const uint32_t w = q4_encode8(a, ga, b, gb);
   const uint32_t o = static_cast<uint32_t>(h * (HD / 2) + l * 2);
-  *reinterpret_cast<uint16_t*>(row + q4_swz(o, codes, t)) = static_cast<uint16_t>(q4_encode4(a, ga));
-  *reinterpret_cast<uint16_t*>(row + q4_swz(o + HD / 4, codes, t)) = static_cast<uint16_t>(q4_encode4(b, gb));
+  *reinterpret_cast<uint16_t*>(row + q4_swz(o, codes, t)) = static_cast<uint16_t>(w);
+  *reinterpret_cast<uint16_t*>(row + q4_swz(o + HD / 4, codes, t)) = static_cast<uint16_t>(w >> 16);
   if (l % GL == 0) {
     const uint32_t g = static_cast<uint32_t>(h * (HD / GS) + l / GL);
     *reinterpret_cast<uint32_t*>(row + codes + q4_swz(g * 4, pars, t)) = ga.word;
@@ -425,7 +409,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       T* dst = isq ? static_cast<T*>(p.q_out) + (t * p.hq + hh) * HD
                    : GS == 0 ? static_cast<T*>(p.k_cache) + (slot * p.hkv + (hh - p.hq)) * HD : nullptr;
       const bool store = GS == 0 ? isq || slot_ok : isq && active;
-      [[maybe_unused]] float q4a[PE], q4b[PE];  // the rotated head in the storage type's values
+      [[maybe_unused]] uint32_t q4a[E], q4b[E];  // the rotated head in the storage type
       if constexpr (sizeof(T) == 2) {
         // y_a = n_a cos - n_b sin, y_b = n_b cos + n_a sin on fp32 pairs
         uint32_t wa[PE / 2], wb[PE / 2];
@@ -443,11 +427,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           wa[e2] = pack_bf16x2(ya.x, ya.y);
           wb[e2] = pack_bf16x2(yb.x, yb.y);
           if constexpr (GS != 0) {
-            const float2 ra = bf16x2_to_float2(wa[e2]), rb = bf16x2_to_float2(wb[e2]);
-            q4a[e] = ra.x;
-            q4a[e + 1] = ra.y;
-            q4b[e] = rb.x;
-            q4b[e + 1] = rb.y;
+            q4a[e2] = wa[e2];
+            q4b[e2] = wb[e2];
           }
         }
         if (store) {
@@ -463,8 +444,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           ya[e] = round_to<T>(na * cs[e] - nb * sn[e]);
           yb[e] = round_to<T>(nb * cs[e] + na * sn[e]);
           if constexpr (GS != 0) {
-            q4a[e] = ya[e];
-            q4b[e] = yb[e];
+            q4a[e] = __float_as_uint(ya[e]);
+            q4b[e] = __float_as_uint(yb[e]);
           }
         }
         if (store) {
@@ -474,7 +455,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       }
       if constexpr (GS != 0) {
         if (hh - sub + HPW > p.hq)  // the pass holds a k head (the same for the whole warp)
-          store_q4_halves<HD, GS>(q4a, q4b, l, active && !isq && slot_ok,
+          store_q4_halves<T, HD, GS>(q4a, q4b, l, active && !isq && slot_ok,
                                   static_cast<char*>(p.k_cache) + slot * p.q4_row_bytes, hh - p.hq, q4_codes, q4_pars,
                                   q4_t);
       }
@@ -484,19 +465,19 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       const int units = p.hkv * (HD / 8);  // eight dims each
       for (int u0 = threadIdx.x & ~31; u0 < units; u0 += kNrThreads) {
         const int u = u0 + lane;
-        float x[8] = {};
+        uint32_t words[kQ4Words<T>] = {};
         if (u < units) {
-          float lo[4], hi[4];
-          Vec4<T>::load(vsrc + u * 8 * E, lo);
-          Vec4<T>::load(vsrc + u * 8 * E + 4 * E, hi);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = lo[e];
-            x[4 + e] = hi[e];
+          for (int e = 0; e < kQ4Words<T>; e += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vsrc + u * 8 * E + e * 4);
+            words[e] = v.x;
+            words[e + 1] = v.y;
+            words[e + 2] = v.z;
+            words[e + 3] = v.w;
           }
         }
         uint32_t par;
-        const uint32_t w = q4_quantise8(x, GS / 8, par);
+        const uint32_t w = q4_quantise8<T>(words, GS / 8, par);
         if (u < units && slot_ok) {
           char* vr = static_cast<char*>(p.v_cache) + slot * p.q4_row_bytes;
           *reinterpret_cast<uint32_t*>(vr + q4_swz(u * 4, q4_codes, q4_t)) = w;

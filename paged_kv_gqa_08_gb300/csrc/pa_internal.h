@@ -136,9 +136,10 @@ struct Q4ReadParams {
   int64_t k_stride_bytes, v_stride_bytes;
   int64_t num_rows, num_pages;
   int32_t batch, maxp, log2P, row_bytes, hkv;
+  int32_t rows_per_cta;  // chosen by the launch
   unsigned int* err;
 };
-cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, const Q4ReadParams& p, cudaStream_t s);
+cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, Q4ReadParams p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // decode

@@ -25,69 +25,89 @@ PA_DEVINL void store8(char* p, const float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// write: a thread takes eight dims of one (token, kv-head), K and V
+// write: a thread takes eight dims of one kv-head, K and V, of every kQ4Threads /
+// (threads of a token)-th token; the loads of two tokens are in flight together
 // ---------------------------------------------------------------------------
 template <typename T, int HD, int GS>
 __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WriteParams p) {
-  constexpr int LPR = HD / 8;   // lanes per head row
-  constexpr int NG = HD / GS;   // groups per head row
   pdl_trigger();                // as in kv_write_kernel
-  const uint32_t per_tok = static_cast<uint32_t>(p.hkv) * LPR;
+  const uint32_t per_tok = static_cast<uint32_t>(p.hkv) * (HD / 8);  // threads of a token: a power of two, 8 to 128
   const uint32_t codes = static_cast<uint32_t>(p.hkv) * (HD / 2), pars = static_cast<uint32_t>(p.row_bytes) - codes;
-  const int64_t total = p.n_tokens * per_tok;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  // whole warps go round together (the groups' reductions are warp shuffles)
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31u); i0 < total; i0 += step) {
-    const int64_t i = i0 + (threadIdx.x & 31u);
-    const int64_t t = i / per_tok;
-    const uint32_t r = static_cast<uint32_t>(i - t * per_tok), h = r / LPR, l = r % LPR;
-    int64_t slot = -1;
-    if (i < total) {
-      slot = p.slots[t];
-      if (slot < 0 || slot >= p.num_slots) {
-        if (slot != -1 && r == 0) raise_flag(p.err, PA_DEVERR_BAD_SLOT);
-        slot = -1;
+  const uint32_t r = threadIdx.x & (per_tok - 1);
+  const uint32_t sub = threadIdx.x >> (31 - __clz(per_tok)), tpc = kQ4Threads >> (31 - __clz(per_tok));  // tokens per CTA
+  const uint32_t co = r * 4, po = r / (GS / 8) * 4;
+  const bool leads = r % (GS / 8) == 0;  // stores its group's parameters
+  const int64_t step = static_cast<int64_t>(gridDim.x) * tpc;
+  // whole CTAs go round together (the groups' reductions are warp shuffles)
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpc; t0 < p.n_tokens; t0 += 2 * step) {
+    uint32_t kw[2][kQ4Words<T>], vw[2][kQ4Words<T>];
+    int64_t slot[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t t = t0 + u * step + sub;
+      slot[u] = -1;
+      if (t < p.n_tokens) {
+        slot[u] = p.slots[t];
+        if (slot[u] < 0 || slot[u] >= p.num_slots) {
+          if (slot[u] != -1 && r == 0) raise_flag(p.err, PA_DEVERR_BAD_SLOT);
+          slot[u] = -1;
+        }
+        // a token that is not stored is read all the same: its loads need not wait for its slot
+        q4_load8<T>(p.k + t * p.k_stride_bytes + r * (8 * sizeof(T)), kw[u]);
+        q4_load8<T>(p.v + t * p.v_stride_bytes + r * (8 * sizeof(T)), vw[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kQ4Words<T>; ++e) kw[u][e] = vw[u][e] = 0u;
       }
     }
-    float k[8] = {}, v[8] = {};
-    if (slot >= 0) {
-      q4_load8<T>(p.k + t * p.k_stride_bytes + r * (8 * sizeof(T)), k);
-      q4_load8<T>(p.v + t * p.v_stride_bytes + r * (8 * sizeof(T)), v);
-    }
-    uint32_t kp, vp;
-    const uint32_t kw = q4_quantise8(k, GS / 8, kp), vw = q4_quantise8(v, GS / 8, vp);
-    if (slot >= 0) {
-      const uint32_t tt = static_cast<uint32_t>(slot);
-      const uint32_t co = q4_swz(r * 4, codes, tt);
-      char* kr = p.k_cache + slot * p.row_bytes;
-      char* vr = p.v_cache + slot * p.row_bytes;
-      *reinterpret_cast<uint32_t*>(kr + co) = kw;
-      *reinterpret_cast<uint32_t*>(vr + co) = vw;
-      if (l % (GS / 8) == 0) {
-        const uint32_t po = codes + q4_swz((h * NG + l / (GS / 8)) * 4, pars, tt);
-        *reinterpret_cast<uint32_t*>(kr + po) = kp;
-        *reinterpret_cast<uint32_t*>(vr + po) = vp;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u == 1 && t0 + step >= p.n_tokens) break;  // the same for the whole CTA
+      uint32_t kp, vp;
+      const uint32_t kc = q4_quantise8<T>(kw[u], GS / 8, kp), vc = q4_quantise8<T>(vw[u], GS / 8, vp);
+      if (slot[u] >= 0) {
+        const uint32_t tt = static_cast<uint32_t>(slot[u]);
+        char* kr = p.k_cache + slot[u] * p.row_bytes;
+        char* vr = p.v_cache + slot[u] * p.row_bytes;
+        *reinterpret_cast<uint32_t*>(kr + q4_swz(co, codes, tt)) = kc;
+        *reinterpret_cast<uint32_t*>(vr + q4_swz(co, codes, tt)) = vc;
+        if (leads) {
+          *reinterpret_cast<uint32_t*>(kr + codes + q4_swz(po, pars, tt)) = kp;
+          *reinterpret_cast<uint32_t*>(vr + codes + q4_swz(po, pars, tt)) = vp;
+        }
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// read back: a CTA takes kReadRows consecutive output rows; their slots are
-// looked up first (one thread a row), then a thread takes eight dims of a row
+// read back: a CTA takes `rows_per_cta` consecutive output rows.  Their slots are
+// looked up first; then a thread takes eight dims of every row of its share, the
+// loads of kReadRows rows in flight together.
 // ---------------------------------------------------------------------------
-constexpr int kReadRows = 16;
+constexpr int kMaxReadRows = 32;
+constexpr int kReadRows = 4;
+
+// The number of requests whose rows start at or before row r, by the whole CTA.
+PA_DEVINL int requests_from(const Q4ReadParams& p, int64_t r) {
+  int n = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kQ4Threads) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    n += __syncthreads_count(b < p.batch && p.cu[b] <= r);
+  }
+  return n;
+}
 
 template <typename T, int HD, int GS>
 __global__ void __launch_bounds__(kQ4Threads) kv_read_q4_kernel(const Q4ReadParams p) {
-  constexpr int LPR = HD / 8;
-  constexpr int NG = HD / GS;
-  __shared__ int64_t slot_s[kReadRows];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kReadRows), p.num_rows - row0));
+  __shared__ int64_t slot_s[kMaxReadRows];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows_per_cta), p.num_rows - row0));
+  // requests of the first and the last row (cu_rows does not fall), then each row's between them
+  const int first = max(requests_from(p, row0) - 1, 0), last = max(requests_from(p, row0 + rows - 1) - 1, first);
   if (threadIdx.x < rows) {
     const int64_t r = row0 + threadIdx.x;
-    int lo = 0, hi = p.batch - 1;  // the last request whose rows start at or before r
+    int lo = first, hi = last;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.cu[mid] <= r) lo = mid;
@@ -118,28 +138,42 @@ __global__ void __launch_bounds__(kQ4Threads) kv_read_q4_kernel(const Q4ReadPara
     slot_s[threadIdx.x] = slot;
   }
   cta_sync();
-  const uint32_t per_row = static_cast<uint32_t>(p.hkv) * LPR;
+  const uint32_t per_row = static_cast<uint32_t>(p.hkv) * (HD / 8);  // threads of a row: a power of two, 8 to 128
   const uint32_t codes = static_cast<uint32_t>(p.hkv) * (HD / 2), pars = static_cast<uint32_t>(p.row_bytes) - codes;
-  const uint32_t total = rows * per_row;
-#pragma unroll 4
-  for (uint32_t i = threadIdx.x; i < total; i += kQ4Threads) {
-    const uint32_t rr = i / per_row, r = i - rr * per_row, h = r / LPR, l = r % LPR;
-    const int64_t slot = slot_s[rr];
-    if (slot < 0) continue;
-    const uint32_t tt = static_cast<uint32_t>(slot);
-    const uint32_t co = q4_swz(r * 4, codes, tt);
-    const uint32_t po = codes + q4_swz((h * NG + l / (GS / 8)) * 4, pars, tt);
+  const uint32_t r = threadIdx.x & (per_row - 1);
+  const int sub = threadIdx.x >> (31 - __clz(per_row)), step = kQ4Threads >> (31 - __clz(per_row));
+  const uint32_t co = r * 4, po = r / (GS / 8) * 4;
+  char* k_out = p.k_out + row0 * p.k_stride_bytes + r * (8 * sizeof(T));
+  char* v_out = p.v_out + row0 * p.v_stride_bytes + r * (8 * sizeof(T));
+  for (int r0 = sub; r0 < rows; r0 += kReadRows * step) {
+    uint32_t w[kReadRows][2], sc[kReadRows][2];
+    bool live[kReadRows];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const char* src = (part ? p.v_cache : p.k_cache) + slot * p.row_bytes;
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src + co));
-      const float2 sc = q4_sc(__ldg(reinterpret_cast<const uint32_t*>(src + po)));
-      float a[4], b[4];
-      q4_decode4(w & 0xFFFFu, sc.x, sc.y, a);
-      q4_decode4(w >> 16, sc.x, sc.y, b);
-      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      char* dst = part ? p.v_out + (row0 + rr) * p.v_stride_bytes : p.k_out + (row0 + rr) * p.k_stride_bytes;
-      store8<T>(dst + r * (8 * sizeof(T)), x);
+    for (int u = 0; u < kReadRows; ++u) {
+      const int rr = r0 + u * step;
+      int64_t slot = rr < rows ? slot_s[rr] : -1;
+      live[u] = slot >= 0;
+      slot = max(slot, static_cast<int64_t>(0));  // (a row that is not read loads slot 0: no branch between the loads)
+      const uint32_t tt = static_cast<uint32_t>(slot);
+      const char* kr = p.k_cache + slot * p.row_bytes;
+      const char* vr = p.v_cache + slot * p.row_bytes;
+      const uint32_t c = q4_swz(co, codes, tt), q = codes + q4_swz(po, pars, tt);
+      w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(kr + c));
+      w[u][1] = __ldg(reinterpret_cast<const uint32_t*>(vr + c));
+      sc[u][0] = __ldg(reinterpret_cast<const uint32_t*>(kr + q));
+      sc[u][1] = __ldg(reinterpret_cast<const uint32_t*>(vr + q));
+    }
+#pragma unroll
+    for (int u = 0; u < kReadRows; ++u) {
+      if (!live[u]) continue;
+      const int64_t rr = r0 + u * step;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const float2 g = q4_sc(sc[u][part]);
+        float x[8];
+        q4_decode8(w[u][part], g.x, g.y, x);
+        store8<T>(part ? v_out + rr * p.v_stride_bytes : k_out + rr * p.k_stride_bytes, x);
+      }
     }
   }
 }
@@ -169,21 +203,29 @@ cudaError_t launch_kv_write_q4(const pa_cache_desc& d, int gs, const Q4WritePara
   const void* fn = d.dtype == PA_BF16
                        ? (d.head_dim == 128 ? write_fn<__nv_bfloat16, 128>(gs) : write_fn<__nv_bfloat16, 64>(gs))
                        : (d.head_dim == 128 ? write_fn<float, 128>(gs) : write_fn<float, 64>(gs));
-  const int64_t total = p.n_tokens * p.hkv * (d.head_dim / 8);
-  const int64_t blocks =
-      std::min<int64_t>((total + kQ4Threads - 1) / kQ4Threads, static_cast<int64_t>(di.sm_count) * 8);
+  const int tpc = kQ4Threads / (p.hkv * (d.head_dim / 8));  // tokens a CTA takes at a time
+  const int64_t blocks = std::min<int64_t>((p.n_tokens + tpc - 1) / tpc, static_cast<int64_t>(di.sm_count) * 8);
   void* args[] = {const_cast<Q4WriteParams*>(&p)};
   e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kQ4Threads), args, 0, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, const Q4ReadParams& p, cudaStream_t s) {
+cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, Q4ReadParams p, cudaStream_t s) {
+  DeviceInfo di;
+  cudaError_t e = current_device_info(&di);
+  if (e != cudaSuccess) return e;
   const void* fn = d.dtype == PA_BF16
                        ? (d.head_dim == 128 ? read_fn<__nv_bfloat16, 128>(gs) : read_fn<__nv_bfloat16, 64>(gs))
                        : (d.head_dim == 128 ? read_fn<float, 128>(gs) : read_fn<float, 64>(gs));
-  const unsigned blocks = static_cast<unsigned>((p.num_rows + kReadRows - 1) / kReadRows);
-  void* args[] = {const_cast<Q4ReadParams*>(&p)};
-  cudaError_t e = cudaLaunchKernel(fn, dim3(blocks), dim3(kQ4Threads), args, 0, s);
+  // Rows per CTA: what its threads take in one go (several rows each), unless
+  // that leaves SMs without work; then down to one row a thread.
+  const int at_once = kQ4Threads / (p.hkv * (d.head_dim / 8));
+  int64_t rows = std::min<int64_t>(kMaxReadRows, static_cast<int64_t>(at_once) * kReadRows);
+  while (rows > at_once && (p.num_rows + rows - 1) / rows < 2 * di.sm_count) rows /= 2;
+  p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(rows, kMaxReadRows));
+  const unsigned blocks = static_cast<unsigned>((p.num_rows + p.rows_per_cta - 1) / p.rows_per_cta);
+  void* args[] = {&p};
+  e = cudaLaunchKernel(fn, dim3(blocks), dim3(kQ4Threads), args, 0, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

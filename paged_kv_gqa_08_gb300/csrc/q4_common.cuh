@@ -57,78 +57,170 @@ PA_DEVINL Q4Group q4_group(float mn, float mx, bool bad) {
   return g;
 }
 
-// The code of one clamped value: rint((x - c) / s) - 16 within 0..15.
-PA_DEVINL uint32_t q4_code(float x, const Q4Group& g) {
-  float t = __fmul_rn(__fsub_rn(x, g.c), g.r);
-  t = fminf(fmaxf(t, 16.f), 31.f);
-  // adding 1.5 * 2^23 rounds to an integer (half to even) in the low bits
-  return __float_as_uint(__fadd_rn(t, 12582912.f)) & 15u;
+// rint((x - c) / s), clamped to 16..31, in the low bits of an integer whose
+// other bits are those of 1.5 * 2^23: adding that number rounds half to even.
+// Values beyond +-kQ4Max need no clamp of their own: the group's range ends
+// there, so they meet the ends of 16..31.
+PA_DEVINL uint32_t q4_step(float x, const Q4Group& g) {
+  const float t = __fmul_rn(__fsub_rn(x, g.c), g.r);
+  return __float_as_uint(__fadd_rn(fminf(fmaxf(t, 16.f), 31.f), 12582912.f));
 }
 
-// Four consecutive dims' codes in their 16 bits.
-PA_DEVINL uint32_t q4_pack4(uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
-  return (u0 << 6) | (u2 << 2) | (u3 << 10) | ((u1 & 3u) << 14) | (u1 >> 2);
+// Eight dims' codes, four in each half of the word.  Dims 0, 2, 3 are shifted
+// and added with their upper bits (each is 0x4B400010 + u), whose sum is taken
+// off again; dim 1 is turned round the half word's end.
+PA_DEVINL uint32_t q4_encode8(const float (&a)[4], const Q4Group& ga, const float (&b)[4], const Q4Group& gb) {
+  constexpr uint32_t kBase = 0x4B400010u;
+  constexpr uint32_t kBases = (kBase << 6) + (kBase << 2) + (kBase << 10) + (kBase << 22) + (kBase << 18) + (kBase << 26);
+  const uint32_t u = (q4_step(a[0], ga) << 6) + (q4_step(a[2], ga) << 2) + (q4_step(a[3], ga) << 10) +
+                     (q4_step(b[0], gb) << 22) + (q4_step(b[2], gb) << 18) + (q4_step(b[3], gb) << 26) - kBases;
+  const uint32_t v = (q4_step(a[1], ga) & 15u) | (q4_step(b[1], gb) << 16);  // (b's upper bits leave the word)
+  return u | ((v << 14) & 0xC000C000u) | ((v >> 2) & 0x00030003u);
 }
 
-PA_DEVINL uint32_t q4_encode4(const float (&x)[4], const Q4Group& g) {
-  return q4_pack4(q4_code(x[0], g), q4_code(x[1], g), q4_code(x[2], g), q4_code(x[3], g));
-}
-
-PA_DEVINL float q4_clamp(float x) { return fminf(fmaxf(x, -kQ4Max), kQ4Max); }
 PA_DEVINL bool q4_bad(float x) { return !(fabsf(x) <= FLT_MAX); }
 
-// Eight elements of the storage type as fp32.
+// ----------------------------------------------------------------------------
+// minimum and maximum of a group.  bf16: on packed pairs, as {min, -max}, with
+// NaN passed on, so that one shuffle and one instruction take a step of the
+// reduction; fp32: apart, with a flag for values that are not finite.
+// ----------------------------------------------------------------------------
+PA_DEVINL uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+PA_DEVINL uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 template <typename T>
-PA_DEVINL void q4_load8(const char* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 w = ldg16(p);
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y), c = bf16x2_to_float2(w.z),
-                 d = bf16x2_to_float2(w.w);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-    x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
-  } else {
-    const uint4 w = ldg16(p), v = ldg16(p + 16);
-    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-    x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y); x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
+struct Q4Range;
+
+template <>
+struct Q4Range<__nv_bfloat16> {
+  uint32_t r;  // {min, -max}
+  template <int N>
+  PA_DEVINL void of_words(const uint32_t (&w)[N]) {
+    uint32_t mn = w[0], mx = w[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+      mn = min_bf16x2(mn, w[i]);
+      mx = max_bf16x2(mx, w[i]);
+    }
+    mx ^= 0x80008000u;
+    r = min_bf16x2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+  }
+  PA_DEVINL void join(const Q4Range& o) { r = min_bf16x2(r, o.r); }
+  PA_DEVINL void reduce(int m) { r = min_bf16x2(r, __shfl_xor_sync(0xffffffffu, r, m)); }
+  PA_DEVINL Q4Group group() const {
+    const float mn = __uint_as_float(r << 16), mx = -__uint_as_float(r & 0xFFFF0000u);
+    return q4_group(fminf(fmaxf(mn, -kQ4Max), kQ4Max), fmaxf(fminf(mx, kQ4Max), -kQ4Max), q4_bad(mn) || q4_bad(mx));
+  }
+};
+
+template <>
+struct Q4Range<float> {
+  float mn, mx;
+  int bad;
+  template <int N>
+  PA_DEVINL void of_words(const uint32_t (&w)[N]) {
+    mn = INFINITY;
+    mx = -INFINITY;
+    bad = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = __uint_as_float(w[i]);
+      bad |= q4_bad(x);
+      mn = fminf(mn, x);
+      mx = fmaxf(mx, x);
+    }
+  }
+  PA_DEVINL void join(const Q4Range& o) {
+    mn = fminf(mn, o.mn);
+    mx = fmaxf(mx, o.mx);
+    bad |= o.bad;
+  }
+  PA_DEVINL void reduce(int m) {
+    Q4Range o;
+    o.mn = __shfl_xor_sync(0xffffffffu, mn, m);
+    o.mx = __shfl_xor_sync(0xffffffffu, mx, m);
+    o.bad = __shfl_xor_sync(0xffffffffu, bad, m);
+    join(o);
+  }
+  PA_DEVINL Q4Group group() const {
+    return q4_group(fminf(fmaxf(mn, -kQ4Max), kQ4Max), fmaxf(fminf(mx, kQ4Max), -kQ4Max), bad != 0);
+  }
+};
+
+// N words of the storage type as fp32 (bf16: two values a word).
+template <typename T, int N, int M>
+PA_DEVINL void q4_widen(const uint32_t (&w)[N], float (&x)[M]) {
+  static_assert(N * 4 == M * static_cast<int>(sizeof(T)), "");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const float2 f = bf16x2_to_float2(w[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// Words of eight elements of the storage type.
+template <typename T>
+constexpr int kQ4Words = 2 * sizeof(T);
+
+template <typename T>
+PA_DEVINL void q4_load8(const char* p, uint32_t (&w)[kQ4Words<T>]) {
+#pragma unroll
+  for (int i = 0; i < kQ4Words<T>; i += 4) {
+    const uint4 v = ldg16(p + 4 * i);
+    w[i] = v.x;
+    w[i + 1] = v.y;
+    w[i + 2] = v.z;
+    w[i + 3] = v.w;
   }
 }
 
 // Eight consecutive dims of a group spread over `lanes` (a power of two)
 // neighbouring lanes, all 32 lanes taking part: the word of codes, and the
 // group's parameters.
-PA_DEVINL uint32_t q4_quantise8(float (&x)[8], int lanes, uint32_t& params) {
-  bool bad = false;
+template <typename T>
+PA_DEVINL uint32_t q4_quantise8(const uint32_t (&w)[kQ4Words<T>], int lanes, uint32_t& params) {
+  Q4Range<T> range;
+  range.of_words(w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    bad |= q4_bad(x[e]);
-    x[e] = q4_clamp(x[e]);
-  }
-  float mn = x[0], mx = x[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    mn = fminf(mn, x[e]);
-    mx = fmaxf(mx, x[e]);
-  }
-#pragma unroll
-  for (int m = 1; m < lanes; m <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, m));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-    bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), m) != 0;
-  }
-  const Q4Group g = q4_group(mn, mx, bad);
+  for (int m = 1; m < lanes; m <<= 1) range.reduce(m);
+  const Q4Group g = range.group();
   params = g.word;
+  float x[8];
+  q4_widen<T>(w, x);
   const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-  return q4_encode4(a, g) | (q4_encode4(b, g) << 16);
+  return q4_encode8(a, g, b, g);
 }
 
-// The value of one code of a group (one fp32 rounding: s * (16 + u) is exact).
-PA_DEVINL float q4_value(uint32_t u, float s, float c) { return fmaf(s, static_cast<float>(16u + u), c); }
+// The value of a code in bits 19-22, with one fp32 rounding (s * (16 + u) is
+// exact): 16 + u is the fp32 number with u in bits 19-22 over 16's bits.
+PA_DEVINL float q4_value(uint32_t code_at_19, float s, float c) {
+  return fmaf(s, __uint_as_float((code_at_19 & 0x00780000u) | 0x41800000u), c);
+}
 
-PA_DEVINL void q4_decode4(uint32_t h, float s, float c, float (&x)[4]) {
-  x[0] = q4_value((h >> 6) & 15u, s, c);
-  x[1] = q4_value(((h >> 14) & 3u) | ((h & 3u) << 2), s, c);
-  x[2] = q4_value((h >> 2) & 15u, s, c);
-  x[3] = q4_value((h >> 10) & 15u, s, c);
+// The eight values of a word of codes.
+PA_DEVINL void q4_decode8(uint32_t w, float s, float c, float (&x)[8]) {
+  const uint32_t lo = __byte_perm(w, 0, 0x1010), hi = __byte_perm(w, 0, 0x3232);  // a half twice: dim 1 in bits 14-17
+  x[0] = q4_value(w << 13, s, c);
+  x[1] = q4_value(lo << 5, s, c);
+  x[2] = q4_value(w << 17, s, c);
+  x[3] = q4_value(w << 9, s, c);
+  x[4] = q4_value(w >> 3, s, c);
+  x[5] = q4_value(hi << 5, s, c);
+  x[6] = q4_value(w << 1, s, c);
+  x[7] = q4_value(w >> 7, s, c);
 }
 
 PA_DEVINL float2 q4_sc(uint32_t word) {
