@@ -151,6 +151,14 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+def _at(t) -> Optional[int]:
+    """_ptr for the short calls: a tensor's address, whatever its size (the library looks at the sizes it is given)."""
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return None if t is None else int(t)
+
+
 # The current device's index and its current stream's handle, as torch.cuda.current_device() and
 # current_stream().cuda_stream give them, without their layers of checks: those took 4 us of a call's 14.
 _current_device = None
@@ -325,8 +333,8 @@ def pa_kv_write_q4(desc, group_size, k, k_row_stride, v, v_row_stride, num_token
     lib = load_library()
     _q4_caches("pa_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_kv_write_q4", lib.pa_kv_write_q4(
-        desc, group_size, _ptr(k), k_row_stride, _ptr(v), v_row_stride, num_tokens, _ptr(slot_mapping),
-        _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+        desc, group_size, _at(k), k_row_stride, _at(v), v_row_stride, num_tokens, _at(slot_mapping),
+        _at(k_cache), _at(v_cache), _stream(stream)))
 
 
 def pa_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens,
@@ -335,9 +343,9 @@ def pa_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stri
     lib = load_library()
     _q4_caches("pa_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_qk_norm_rope_kv_write_q4", lib.pa_qk_norm_rope_kv_write_q4(
-        desc, group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
-        num_tokens, _ptr(positions), _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(slot_mapping),
-        _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+        desc, group_size, _at(q), q_row_stride, _at(k), k_row_stride, _at(v), v_row_stride,
+        num_tokens, _at(positions), _at(q_norm_w), _at(k_norm_w), eps, rope_theta, _at(slot_mapping),
+        _at(q_out), _at(k_cache), _at(v_cache), _stream(stream)))
 
 
 def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride,
@@ -347,10 +355,10 @@ def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_
     lib = load_library()
     _q4_caches("pa_prefill_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
     _check("pa_prefill_qk_norm_rope_kv_write_q4", lib.pa_prefill_qk_norm_rope_kv_write_q4(
-        desc, group_size, _ptr(q), q_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
-        num_tokens, _ptr(cu_seqlens_q), batch, _ptr(context_lens), _ptr(block_tables), max_pages_per_seq,
-        _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_theta, _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-        _ptr(positions_out), _ptr(slot_mapping_out), _stream(stream)))
+        desc, group_size, _at(q), q_row_stride, _at(k), k_row_stride, _at(v), v_row_stride,
+        num_tokens, _at(cu_seqlens_q), batch, _at(context_lens), _at(block_tables), max_pages_per_seq,
+        _at(q_norm_w), _at(k_norm_w), eps, rope_theta, _at(q_out), _at(k_cache), _at(v_cache),
+        _at(positions_out), _at(slot_mapping_out), _stream(stream)))
 
 
 def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_tables, max_pages_per_seq, num_rows,
@@ -359,8 +367,8 @@ def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_
     lib = load_library()
     _q4_caches("pa_kv_read_q4", desc, group_size, k_cache, v_cache)
     _check("pa_kv_read_q4", lib.pa_kv_read_q4(
-        desc, group_size, batch, _ptr(cu_rows), _ptr(starts), _ptr(context_lens), _ptr(block_tables),
-        max_pages_per_seq, num_rows, _ptr(k_cache), _ptr(v_cache), _ptr(k_out), k_row_stride, _ptr(v_out),
+        desc, group_size, batch, _at(cu_rows), _at(starts), _at(context_lens), _at(block_tables),
+        max_pages_per_seq, num_rows, _at(k_cache), _at(v_cache), _at(k_out), k_row_stride, _at(v_out),
         v_row_stride, _stream(stream)))
 
 
@@ -376,8 +384,8 @@ def pa_decode_q4(desc, group_size, q, batch, k_cache, v_cache, block_tables, max
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("pa_decode_q4", lib.pa_decode_q4(
-        desc, group_size, _ptr(q), batch, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-        max_pages_per_seq, _ptr(context_lens), max_context_len, scale, max_ctas, _ptr(out), _ptr(workspace),
+        desc, group_size, _at(q), batch, _at(k_cache), _at(v_cache), _at(block_tables),
+        max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas, _at(out), _at(workspace),
         workspace_bytes, _stream(stream)))
 
 
@@ -389,9 +397,9 @@ def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("pa_decode_kv_write_q4", lib.pa_decode_kv_write_q4(
-        desc, group_size, _ptr(q), _ptr(k_new), k_row_stride, _ptr(v_new), v_row_stride, batch,
-        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_pages_per_seq, _ptr(context_lens), max_context_len,
-        scale, max_ctas, _ptr(slot_mapping), _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+        desc, group_size, _at(q), _at(k_new), k_row_stride, _at(v_new), v_row_stride, batch,
+        _at(k_cache), _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len,
+        scale, max_ctas, _at(slot_mapping), _at(out), _at(workspace), workspace_bytes, _stream(stream)))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,

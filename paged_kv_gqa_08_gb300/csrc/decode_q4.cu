@@ -16,6 +16,7 @@ namespace {
 constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
+constexpr int kWholeTokens = 256;  // requests of at most this many tokens are not split where a CTA each fits
 
 // A chunk in the ring, as the producer describes it to the consumers: its
 // request; the tokens of its halves (n0 | n1 << 8, 0 for a half whose page is
@@ -35,6 +36,7 @@ struct Q4Params {
   int32_t stages;       // ring depth
   int32_t stage_bytes;  // K rows, V rows, queries
   int32_t groups;       // consumer groups: 2 (tensor cores) or 1
+  int32_t by_request;   // 1: CTA b takes request b, whole (nothing to merge)
   uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, with its statistics
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
@@ -720,10 +722,10 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
     NC = cs[k.B];
   }
   const int c = blockIdx.x;
-  const int x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
-  const int x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
+  const int x0 = p.by_request ? cs[c] : static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
+  const int x1 = p.by_request ? cs[c + 1] : static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
   const uint32_t rb = static_cast<uint32_t>(k.row_bytes), q_bytes = p.stage_bytes - 2 * k.chunk_bytes;
-  int b = x0 < x1 ? first_request(cs, k.B, x0) : 0;
+  int b = p.by_request ? c : x0 < x1 ? first_request(cs, k.B, x0) : 0;
   int issued = 0;
   Ring ring;
   bool aborted = false;
@@ -943,8 +945,11 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
   int64_t n = static_cast<int64_t>(occ) * di.sm_count;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
+  // Short requests that fit the GPU at once: a CTA each, no partial results
+  // and no merge kernel.
+  if (n >= batch && batch <= kInlinePlanMax && max_ctx <= kWholeTokens) pl.by_request = true;
   n = std::min<int64_t>(n, std::max<int64_t>(1, chunks_upper));
-  pl.n_ctas = static_cast<int>(std::max<int64_t>(1, n));
+  pl.n_ctas = pl.by_request ? batch : static_cast<int>(std::max<int64_t>(1, n));
   decode_workspace_layout(d, batch, &pl);
   *out = pl;
   return cudaSuccess;
@@ -961,6 +966,7 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   p.pars = p.k.row_bytes - p.codes;
   while ((1 << p.log2gs) < gs) ++p.log2gs;
   p.groups = q4_groups(d);
+  p.by_request = pl.by_request;
   p.off_q = pl.off_ml + pl.nw * 16 * 4;
   p.off_hand = pl.off_ml;
   void* args[] = {&p};

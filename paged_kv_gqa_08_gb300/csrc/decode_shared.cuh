@@ -433,7 +433,7 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
     e = launch_after_previous(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), pl.smem_bytes, s, main_args);
   }
   if (e != cudaSuccess) return e;
-  if (pl.n_ctas > 1) {
+  if (pl.n_ctas > 1 && !pl.by_request) {
     // warps per (request, q-head): about one per 8 partials of a request when
     // the requests are equally long (CTAs per request / 8), at most 4
     const int per_req = pl.n_ctas / std::max(1, p.B);

@@ -190,42 +190,11 @@ PA_DEVINL void map_token(const NormRopeParams& p, int64_t t, bool report, int& p
   map_token_of(p, t, lo, p.cu[lo], p.cu[lo + 1], p.ctx[lo], report, pos, slot);
 }
 
-// One head's rotated k (words of four dims of each half per lane, HD / 8 lanes
-// a head), quantised into head h of a 4-bit row.  All 32 lanes take part.
-template <typename T, int HD, int GS>
-PA_DEVINL void store_q4_halves(const uint32_t (&wa)[sizeof(T)], const uint32_t (&wb)[sizeof(T)], int l, bool store,
-                               char* row, int h, uint32_t codes, uint32_t pars, uint32_t t) {
-  constexpr bool kWhole = GS == HD;                // one group: both halves
-  constexpr int GL = kWhole ? HD / 8 : GS / 4;     // lanes of a group
-  Q4Range<T> ra, rb;
-  ra.of_words(wa);
-  rb.of_words(wb);
-  if constexpr (kWhole) ra.join(rb);
-#pragma unroll
-  for (int m = 1; m < GL; m <<= 1) {
-    ra.reduce(m);
-    if constexpr (!kWhole) rb.reduce(m);
-  }
-  const Q4Group ga = ra.group();
-  const Q4Group gb = kWhole ? ga : rb.group();
-  if (!store) return;
-  float a[4], b[4];
-  q4_widen<T>(wa, a);
-  q4_widen<T>(wb, b);
-  const uint32_t w = q4_encode8(a, ga, b, gb);
-  const uint32_t o = static_cast<uint32_t>(h * (HD / 2) + l * 2);
-  *reinterpret_cast<uint16_t*>(row + q4_swz(o, codes, t)) = static_cast<uint16_t>(w);
-  *reinterpret_cast<uint16_t*>(row + q4_swz(o + HD / 4, codes, t)) = static_cast<uint16_t>(w >> 16);
-  if (l % GL == 0) {
-    const uint32_t g = static_cast<uint32_t>(h * (HD / GS) + l / GL);
-    *reinterpret_cast<uint32_t*>(row + codes + q4_swz(g * 4, pars, t)) = ga.word;
-    if constexpr (!kWhole)
-      *reinterpret_cast<uint32_t*>(row + codes + q4_swz((g + HD / GS / 2) * 4, pars, t)) = gb.word;
-  }
-}
-
 constexpr int kNrThreads = 128;
 constexpr int kNrCtasPerSm = 8;
+// 4-bit rows take more registers: 80 without recomputing values, so 5 CTAs
+// (16384 tokens: 60.8 us; 6, 7, 8 CTAs at 64 registers 62.9, 64.9, 66.3 us).
+constexpr int kNrCtasPerSmQ4 = 5;
 constexpr int kNrMaxPerCta = 2048;
 
 // Shared-memory bytes of one token's stage: its q, k and v rows.
@@ -245,11 +214,14 @@ __host__ __device__ constexpr int nr_stage_bytes(int hq, int hkv, int hd, int e)
 //
 // GS != 0: the cache holds 4-bit rows with groups of GS dims (q4_common.cuh).
 // The rotated k (rounded to the storage type, as a cache of that type would
-// hold it) and the v row are quantised on their way out: a lane's four dims of
-// each half are 16 bits of codes, and GS / 4 neighbouring lanes (both halves
-// together when GS = HD) form a group.
+// hold it) goes back into the stage in place of the k it came from; the warp
+// then takes eight consecutive dims a lane of these heads' k and v rows and
+// quantises the two together, which shares the work on the groups' parameters
+// (quantising k from the rotation's registers and v apart took 3240 instructions
+// a token instead of 2900).
 template <typename T, int HD, int GS>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
+    norm_rope_kv_write_kernel(const NormRopeParams p) {
   constexpr int E = sizeof(T);
   constexpr int PE = 4;
   constexpr int LPH = HD / (2 * PE);  // lanes per head
@@ -378,7 +350,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       sn[e] = sn_s[l * PE + e];
       nsn[e] = -sn[e];
     }
-    const unsigned char* st = stages + (i & 1) * stage_bytes;
+    unsigned char* st = stages + (i & 1) * stage_bytes;
     [[maybe_unused]] const uint32_t q4_codes = static_cast<uint32_t>(p.hkv) * (HD / 2),
                                     q4_pars = static_cast<uint32_t>(p.q4_row_bytes) - q4_codes,
                                     q4_t = static_cast<uint32_t>(slot);
@@ -407,9 +379,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
       }
       const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
       T* dst = isq ? static_cast<T*>(p.q_out) + (t * p.hq + hh) * HD
-                   : GS == 0 ? static_cast<T*>(p.k_cache) + (slot * p.hkv + (hh - p.hq)) * HD : nullptr;
-      const bool store = GS == 0 ? isq || slot_ok : isq && active;
-      [[maybe_unused]] uint32_t q4a[E], q4b[E];  // the rotated head in the storage type
+                   : GS == 0 ? static_cast<T*>(p.k_cache) + (slot * p.hkv + (hh - p.hq)) * HD : const_cast<T*>(src);
+      const bool store = GS == 0 ? isq || slot_ok : active;  // (4-bit: k into the stage)
       if constexpr (sizeof(T) == 2) {
         // y_a = n_a cos - n_b sin, y_b = n_b cos + n_a sin on fp32 pairs
         uint32_t wa[PE / 2], wb[PE / 2];
@@ -426,10 +397,6 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           const float2 yb = ffma2(nb, c2, fmul2(na, make_float2(sn[e], sn[e + 1])));
           wa[e2] = pack_bf16x2(ya.x, ya.y);
           wb[e2] = pack_bf16x2(yb.x, yb.y);
-          if constexpr (GS != 0) {
-            q4a[e2] = wa[e2];
-            q4b[e2] = wb[e2];
-          }
         }
         if (store) {
           *reinterpret_cast<uint2*>(dst + l * PE) = make_uint2(wa[0], wa[1]);
@@ -443,10 +410,6 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
           const float nb = round_to<T>(round_to<T>(xb[e] * r) * (isq ? wq_b[e] : wk_b[e]));
           ya[e] = round_to<T>(na * cs[e] - nb * sn[e]);
           yb[e] = round_to<T>(nb * cs[e] + na * sn[e]);
-          if constexpr (GS != 0) {
-            q4a[e] = __float_as_uint(ya[e]);
-            q4b[e] = __float_as_uint(yb[e]);
-          }
         }
         if (store) {
           Vec4<T>::store(dst + l * PE, ya);
@@ -454,37 +417,41 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kv_write_kernel(const No
         }
       }
       if constexpr (GS != 0) {
-        if (hh - sub + HPW > p.hq)  // the pass holds a k head (the same for the whole warp)
-          store_q4_halves<T, HD, GS>(q4a, q4b, l, active && !isq && slot_ok,
-                                  static_cast<char*>(p.k_cache) + slot * p.q4_row_bytes, hh - p.hq, q4_codes, q4_pars,
-                                  q4_t);
+        if (hh - sub + HPW > p.hq) {  // the pass holds a k head (the same for the whole warp)
+          __syncwarp();               // its rotated k is in the stage
+          const int h = hh - p.hq;
+          const bool mine = active && !isq;
+          uint32_t kw[kQ4Words<T>] = {}, vw[kQ4Words<T>] = {};
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < kQ4Words<T>; e += 4) {
+              const uint4 a = *reinterpret_cast<const uint4*>(st + row_q + (h * HD + l * 8) * E + e * 4);
+              const uint4 b = *reinterpret_cast<const uint4*>(st + row_q + row_kv + (h * HD + l * 8) * E + e * 4);
+              kw[e] = a.x; kw[e + 1] = a.y; kw[e + 2] = a.z; kw[e + 3] = a.w;
+              vw[e] = b.x; vw[e + 1] = b.y; vw[e + 2] = b.z; vw[e + 3] = b.w;
+            }
+          }
+          uint32_t kc, vc, kp, vp;
+          q4_quantise8_pair<T>(kw, vw, GS / 8, kc, vc, kp, vp);
+          if (mine && slot_ok) {
+            char* kr = static_cast<char*>(p.k_cache) + slot * p.q4_row_bytes;
+            char* vr = static_cast<char*>(p.v_cache) + slot * p.q4_row_bytes;
+            const uint32_t co = q4_swz((h * (HD / 8) + l) * 4, q4_codes, q4_t);
+            *reinterpret_cast<uint32_t*>(kr + co) = kc;
+            *reinterpret_cast<uint32_t*>(vr + co) = vc;
+            if (l % (GS / 8) == 0) {
+              const uint32_t po = q4_codes + q4_swz((h * (HD / GS) + l / (GS / 8)) * 4, q4_pars, q4_t);
+              *reinterpret_cast<uint32_t*>(kr + po) = kp;
+              *reinterpret_cast<uint32_t*>(vr + po) = vp;
+            }
+          }
+          // the rotated k's stores come before the copies that refill the stage
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
       }
     }
-    if constexpr (GS != 0) {  // the v row, quantised, into its slot
-      const unsigned char* vsrc = st + row_q + row_kv;
-      const int units = p.hkv * (HD / 8);  // eight dims each
-      for (int u0 = threadIdx.x & ~31; u0 < units; u0 += kNrThreads) {
-        const int u = u0 + lane;
-        uint32_t words[kQ4Words<T>] = {};
-        if (u < units) {
-#pragma unroll
-          for (int e = 0; e < kQ4Words<T>; e += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(vsrc + u * 8 * E + e * 4);
-            words[e] = v.x;
-            words[e + 1] = v.y;
-            words[e + 2] = v.z;
-            words[e + 3] = v.w;
-          }
-        }
-        uint32_t par;
-        const uint32_t w = q4_quantise8<T>(words, GS / 8, par);
-        if (u < units && slot_ok) {
-          char* vr = static_cast<char*>(p.v_cache) + slot * p.q4_row_bytes;
-          *reinterpret_cast<uint32_t*>(vr + q4_swz(u * 4, q4_codes, q4_t)) = w;
-          if (u % (GS / 8) == 0)
-            *reinterpret_cast<uint32_t*>(vr + q4_codes + q4_swz(u / (GS / 8) * 4, q4_pars, q4_t)) = par;
-        }
-      }
+    if constexpr (GS != 0) {
+      // (the v row is written with its k heads)
     } else if (slot_ok) {  // the v row, unchanged, into its slot
       const unsigned char* vsrc = st + row_q + row_kv;
       char* vdst = static_cast<char*>(p.v_cache) + slot * row_kv;
@@ -543,7 +510,7 @@ cudaError_t launch_norm_rope_kv_write(int dtype, int head_dim, const NormRopePar
   const int es = dtype == PA_BF16 ? 2 : 4;
   // one wave of CTAs walking the tokens, with at most kNrMaxPerCta tokens
   // each (the mapped tokens' positions and slots are kept in shared memory)
-  const int64_t wave = static_cast<int64_t>(di.sm_count) * kNrCtasPerSm;
+  const int64_t wave = static_cast<int64_t>(di.sm_count) * (p.q4_group_size ? kNrCtasPerSmQ4 : kNrCtasPerSm);
   const unsigned grid = static_cast<unsigned>(
       std::max(std::min<int64_t>(p.n_tokens, wave), (p.n_tokens + kNrMaxPerCta - 1) / kNrMaxPerCta));
   const int64_t per_cta = (p.n_tokens + grid - 1) / grid;  // tokens of the busiest CTA

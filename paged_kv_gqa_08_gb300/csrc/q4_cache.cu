@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WritePa
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (u == 1 && t0 + step >= p.n_tokens) break;  // the same for the whole CTA
-      uint32_t kp, vp;
-      const uint32_t kc = q4_quantise8<T>(kw[u], GS / 8, kp), vc = q4_quantise8<T>(vw[u], GS / 8, vp);
+      uint32_t kp, vp, kc, vc;
+      q4_quantise8_pair<T>(kw[u], vw[u], GS / 8, kc, vc, kp, vp);
       if (slot[u] >= 0) {
         const uint32_t tt = static_cast<uint32_t>(slot[u]);
         char* kr = p.k_cache + slot[u] * p.row_bytes;
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kQ4Threads) kv_write_q4_kernel(const Q4WritePa
 // looked up first; then a thread takes eight dims of every row of its share, the
 // loads of kReadRows rows in flight together.
 // ---------------------------------------------------------------------------
-constexpr int kMaxReadRows = 32;
+constexpr int kMaxReadRows = kQ4Threads;  // a thread looks up one row
 constexpr int kReadRows = 4;
 
 // The number of requests whose rows start at or before row r, by the whole CTA.
@@ -217,11 +217,14 @@ cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, Q4ReadParams p, cu
   const void* fn = d.dtype == PA_BF16
                        ? (d.head_dim == 128 ? read_fn<__nv_bfloat16, 128>(gs) : read_fn<__nv_bfloat16, 64>(gs))
                        : (d.head_dim == 128 ? read_fn<float, 128>(gs) : read_fn<float, 64>(gs));
-  // Rows per CTA: what its threads take in one go (several rows each), unless
-  // that leaves SMs without work; then down to one row a thread.
-  const int at_once = kQ4Threads / (p.hkv * (d.head_dim / 8));
-  int64_t rows = std::min<int64_t>(kMaxReadRows, static_cast<int64_t>(at_once) * kReadRows);
-  while (rows > at_once && (p.num_rows + rows - 1) / rows < 2 * di.sm_count) rows /= 2;
+  // Rows per CTA: what its threads take in one go (kReadRows each); twice that
+  // where it still leaves 12 CTAs an SM (the look-up of the rows' slots, about
+  // 2 us, is paid half as often: 89.6k rows 77.9 -> 74.6 us, but 16.4k rows
+  // 18.8 -> 19.5 us); less where SMs would have no work.
+  const int64_t at_once = kQ4Threads / (p.hkv * (d.head_dim / 8));
+  int64_t rows = at_once * kReadRows;
+  if (p.num_rows / (2 * rows) >= 12 * di.sm_count) rows *= 2;
+  while (rows > at_once && p.num_rows / rows < 2 * di.sm_count) rows /= 2;
   p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(rows, kMaxReadRows));
   const unsigned blocks = static_cast<unsigned>((p.num_rows + p.rows_per_cta - 1) / p.rows_per_cta);
   void* args[] = {&p};

@@ -41,6 +41,7 @@ PA_DEVINL uint32_t q4_swz(uint32_t o, uint32_t size, uint32_t t) {
 struct Q4Group {  // a group's parameters, as stored and as fp32
   uint32_t word;  // s | c << 16
   float c, r;     // r = 1 / s, or 0
+  bool clamp;     // (x - c) / s may round beyond 16..31
 };
 
 // Parameters of a group with minimum mn and maximum mx (clamped values), or of
@@ -54,28 +55,63 @@ PA_DEVINL Q4Group q4_group(float mn, float mx, bool bad) {
                : static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(ch)) << 16);
   g.c = __half2float(ch);
   g.r = s > 0.f && !bad ? __frcp_rn(s) : 0.f;
+  // With s a normal float16 (off by 2^-11 of itself at most) and |c| <= 512 s
+  // (off by s / 4 at most), (x - c) / s lies within 16 - 0.26 .. 31 + 0.27 for
+  // every x of the group, unless the range was clamped: no need to clamp.
+  g.clamp = !(s >= 6.103515625e-5f && fabsf(g.c) <= 512.f * s && !bad && mn > -kQ4Max && mx < kQ4Max);
   return g;
+}
+
+// Two groups' parameters, each found by every second lane (lanes 2 i and 2 i + 1
+// hold the same two ranges) and exchanged.
+template <typename R>
+PA_DEVINL void q4_group_pair(const R& a, const R& b, Q4Group& ga, Q4Group& gb) {
+  const bool odd = threadIdx.x & 1;
+  const Q4Group mine = R::select(odd, b, a).group();
+  Q4Group other;
+  other.word = __shfl_xor_sync(0xffffffffu, mine.word, 1);
+  other.r = __shfl_xor_sync(0xffffffffu, mine.clamp ? -mine.r : mine.r, 1);  // (the flag in the sign)
+  other.clamp = signbit(other.r);
+  other.r = fabsf(other.r);
+  other.c = __half2float(__ushort_as_half(static_cast<uint16_t>(other.word >> 16)));
+  ga.word = odd ? other.word : mine.word;
+  gb.word = odd ? mine.word : other.word;
+  ga.r = odd ? other.r : mine.r;
+  gb.r = odd ? mine.r : other.r;
+  ga.c = odd ? other.c : mine.c;
+  gb.c = odd ? mine.c : other.c;
+  ga.clamp = odd ? other.clamp : mine.clamp;
+  gb.clamp = odd ? mine.clamp : other.clamp;
 }
 
 // rint((x - c) / s), clamped to 16..31, in the low bits of an integer whose
 // other bits are those of 1.5 * 2^23: adding that number rounds half to even.
 // Values beyond +-kQ4Max need no clamp of their own: the group's range ends
 // there, so they meet the ends of 16..31.
+template <bool kClamp>
 PA_DEVINL uint32_t q4_step(float x, const Q4Group& g) {
   const float t = __fmul_rn(__fsub_rn(x, g.c), g.r);
-  return __float_as_uint(__fadd_rn(fminf(fmaxf(t, 16.f), 31.f), 12582912.f));
+  return __float_as_uint(__fadd_rn(kClamp ? fminf(fmaxf(t, 16.f), 31.f) : t, 12582912.f));
 }
 
 // Eight dims' codes, four in each half of the word.  Dims 0, 2, 3 are shifted
 // and added with their upper bits (each is 0x4B400010 + u), whose sum is taken
 // off again; dim 1 is turned round the half word's end.
-PA_DEVINL uint32_t q4_encode8(const float (&a)[4], const Q4Group& ga, const float (&b)[4], const Q4Group& gb) {
+template <bool kClamp>
+PA_DEVINL uint32_t q4_encode8_as(const float (&a)[4], const Q4Group& ga, const float (&b)[4], const Q4Group& gb) {
   constexpr uint32_t kBase = 0x4B400010u;
   constexpr uint32_t kBases = (kBase << 6) + (kBase << 2) + (kBase << 10) + (kBase << 22) + (kBase << 18) + (kBase << 26);
-  const uint32_t u = (q4_step(a[0], ga) << 6) + (q4_step(a[2], ga) << 2) + (q4_step(a[3], ga) << 10) +
-                     (q4_step(b[0], gb) << 22) + (q4_step(b[2], gb) << 18) + (q4_step(b[3], gb) << 26) - kBases;
-  const uint32_t v = (q4_step(a[1], ga) & 15u) | (q4_step(b[1], gb) << 16);  // (b's upper bits leave the word)
+  const uint32_t u = (q4_step<kClamp>(a[0], ga) << 6) + (q4_step<kClamp>(a[2], ga) << 2) +
+                     (q4_step<kClamp>(a[3], ga) << 10) + (q4_step<kClamp>(b[0], gb) << 22) +
+                     (q4_step<kClamp>(b[2], gb) << 18) + (q4_step<kClamp>(b[3], gb) << 26) - kBases;
+  const uint32_t v = (q4_step<kClamp>(a[1], ga) & 15u) | (q4_step<kClamp>(b[1], gb) << 16);  // (b's upper bits leave)
   return u | ((v << 14) & 0xC000C000u) | ((v >> 2) & 0x00030003u);
+}
+
+// All 32 lanes take part.
+PA_DEVINL uint32_t q4_encode8(const float (&a)[4], const Q4Group& ga, const float (&b)[4], const Q4Group& gb) {
+  return __any_sync(0xffffffffu, ga.clamp || gb.clamp) ? q4_encode8_as<true>(a, ga, b, gb)
+                                                       : q4_encode8_as<false>(a, ga, b, gb);
 }
 
 PA_DEVINL bool q4_bad(float x) { return !(fabsf(x) <= FLT_MAX); }
@@ -114,6 +150,7 @@ struct Q4Range<__nv_bfloat16> {
     r = min_bf16x2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
   }
   PA_DEVINL void join(const Q4Range& o) { r = min_bf16x2(r, o.r); }
+  static PA_DEVINL Q4Range select(bool second, const Q4Range& b, const Q4Range& a) { return second ? b : a; }
   PA_DEVINL void reduce(int m) { r = min_bf16x2(r, __shfl_xor_sync(0xffffffffu, r, m)); }
   PA_DEVINL Q4Group group() const {
     const float mn = __uint_as_float(r << 16), mx = -__uint_as_float(r & 0xFFFF0000u);
@@ -142,6 +179,13 @@ struct Q4Range<float> {
     mn = fminf(mn, o.mn);
     mx = fmaxf(mx, o.mx);
     bad |= o.bad;
+  }
+  static PA_DEVINL Q4Range select(bool second, const Q4Range& b, const Q4Range& a) {
+    Q4Range o;
+    o.mn = second ? b.mn : a.mn;
+    o.mx = second ? b.mx : a.mx;
+    o.bad = second ? b.bad : a.bad;
+    return o;
   }
   PA_DEVINL void reduce(int m) {
     Q4Range o;
@@ -187,9 +231,9 @@ PA_DEVINL void q4_load8(const char* p, uint32_t (&w)[kQ4Words<T>]) {
   }
 }
 
-// Eight consecutive dims of a group spread over `lanes` (a power of two)
-// neighbouring lanes, all 32 lanes taking part: the word of codes, and the
-// group's parameters.
+// Eight consecutive dims of a group spread over `lanes` (a power of two, at
+// least 4) neighbouring lanes, all 32 lanes taking part: the word of codes, and
+// the group's parameters.
 template <typename T>
 PA_DEVINL uint32_t q4_quantise8(const uint32_t (&w)[kQ4Words<T>], int lanes, uint32_t& params) {
   Q4Range<T> range;
@@ -202,6 +246,36 @@ PA_DEVINL uint32_t q4_quantise8(const uint32_t (&w)[kQ4Words<T>], int lanes, uin
   q4_widen<T>(w, x);
   const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
   return q4_encode8(a, g, b, g);
+}
+
+// The same of two rows (K and V).
+template <typename T>
+PA_DEVINL void q4_quantise8_pair(const uint32_t (&k)[kQ4Words<T>], const uint32_t (&v)[kQ4Words<T>], int lanes,
+                                 uint32_t& k_codes, uint32_t& v_codes, uint32_t& k_params, uint32_t& v_params) {
+  Q4Range<T> rk, rv;
+  rk.of_words(k);
+  rv.of_words(v);
+#pragma unroll
+  for (int m = 1; m < lanes; m <<= 1) {
+    rk.reduce(m);
+    rv.reduce(m);
+  }
+  Q4Group gk, gv;
+  q4_group_pair(rk, rv, gk, gv);
+  k_params = gk.word;
+  v_params = gv.word;
+  float x[8], y[8];
+  q4_widen<T>(k, x);
+  q4_widen<T>(v, y);
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  const float c[4] = {y[0], y[1], y[2], y[3]}, d[4] = {y[4], y[5], y[6], y[7]};
+  if (__any_sync(0xffffffffu, gk.clamp || gv.clamp)) {
+    k_codes = q4_encode8_as<true>(a, gk, b, gk);
+    v_codes = q4_encode8_as<true>(c, gv, d, gv);
+  } else {
+    k_codes = q4_encode8_as<false>(a, gk, b, gk);
+    v_codes = q4_encode8_as<false>(c, gv, d, gv);
+  }
 }
 
 // The value of a code in bits 19-22, with one fp32 rounding (s * (16 + u) is
