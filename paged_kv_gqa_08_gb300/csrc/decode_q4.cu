@@ -37,10 +37,19 @@ struct Q4Params {
   int32_t stage_bytes;  // K rows, V rows, queries
   int32_t groups;       // consumer groups: 2 (tensor cores) or 1
   int32_t by_request;   // 1: CTA b takes request b, whole (nothing to merge)
+  uint32_t off_places;  // [vectors][Hkv][32 lanes] of 16 bytes: the lanes' places in a stage
   uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, with its statistics
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
   uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
+};
+
+// The row of a 4-bit cache.
+template <int HD, int NG, int HKV>
+struct Q4Row {
+  static constexpr uint32_t kCodes = HKV * HD / 2;
+  static constexpr uint32_t kPars = (HKV * NG * 4 + 15) / 16 * 16;
+  static constexpr uint32_t kBytes = kCodes + kPars;
 };
 
 // Position in the ring: stage and phase bit of the running chunk.
@@ -281,33 +290,62 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 // Tensor-core consumer (bf16 queries and outputs, groups of up to 8 q-heads).
 //
 // Per chunk, S^T = K Q^T and O^T += V^T P^T as mma.sync m16n8k16 (float16 in,
-// fp32 out): the chunk's 16 tokens, then 16 of the head's dims, are the rows,
-// and the group's q-heads the 8 columns (heads past G are zero queries), so no
-// row of a product is padding.  With l = 4 gq + tq, a lane holds of A rows gq
-// and gq + 8 at columns 2 tq, 2 tq + 1 (+ 8), of B column gq at rows 2 tq,
-// 2 tq + 1 (+ 8), of C rows gq and gq + 8 at columns 2 tq, 2 tq + 1 (PTX ISA).
+// fp32 out): 16 tokens, then 16 of the head's dims, are the rows, and the
+// group's q-heads the 8 columns (heads past G are zero queries), so no row of a
+// product is padding.  With l = 4 gq + tq, a lane holds of A rows gq and gq + 8
+// at columns 2 tq, 2 tq + 1 (+ 8), of B column gq at rows 2 tq, 2 tq + 1 (+ 8),
+// of C rows gq and gq + 8 at columns 2 tq, 2 tq + 1 (PTX ISA).
 //
-// Neither the order of the dims inside S's sums, nor that of O's rows, nor that
-// of the tokens matters to the result, so each lane's share is chosen to be
-// contiguous in the row: of K the HD / 4 dims from tq * HD / 4 of tokens gq and
-// gq + 8 (a register pairs dims d and d + 4 of one token), of V the HD / 8 dims
-// from gq * HD / 8 of tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (a register
-// pairs one dim of two neighbouring tokens).  A lane so meets one group of each
-// of its tokens, and with the rows' swizzle its loads are free of bank
-// conflicts where a row is a multiple of 128 bytes.
+// Neither the order of the dims inside a sum, nor that of O's rows, nor that of
+// the tokens matters to the result, so a lane's share is what it can load in
+// one piece: of K, for each group of GS dims, GS / 4 consecutive dims of tokens
+// gq and gq + 8 (a register pairs dims d and d + 4 of one token); of V some
+// consecutive dims of tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (a register
+// pairs one dim of two tokens).
 //
-// A code becomes a float16 in place (q4_common.cuh): mask-or, then one packed
-// multiply-add with (s, c).  That is 11 to 12 instructions for 8 values and the
-// kernel's main cost; the tensor cores make the products nearly free.
-// Values, probabilities and queries are float16 (2^-12 relative, finer than
-// bf16): queries are scaled by a power of two to a largest magnitude in [1, 2)
-// first, so their range does not matter; sums and statistics are fp32.
+// The kernel is bound by instructions, not bytes, until decoding is cheap, so
+// codes enter the products undecoded where they can: u in bits 6-9 (2-5) of a
+// half word is the subnormal float16 u * 2^-18 (2^-22), exact, one mask.  With
+// m = 16 s + c the value is s u + m, so
+//   S = sum over groups of s (sum q u) + m (sum q):  the sums of q u are scaled
+//       by s as they leave the tensor cores, the second term is one m16n8k8
+//       product of the parameter words (s, c) with (16 sum q, sum q);
+//   O = sum over tokens of (p s) u + p m:  p s replaces p as the B operand, and
+//       the second term is one product of the words' halves with p.
+// The last needs rows of one product (16 dims) to lie in one group and a lane's
+// dims to come in whole words, so groups of 64 and 128; with groups of 32, V is
+// decoded in registers: mask-or to the float16 16 + u, one multiply-add.
+// Decoding both K and V that way took 309 instructions for 16 tokens of a head;
+// this takes FIXME.
+//
+// Ranges.  Queries are scaled by a power of two to a largest magnitude in
+// [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
+// when a score passes it by more).  p s is kept in float16's range by a power of
+// two 2^-E that follows the largest s seen.  Each rounding to float16 is 2^-12
+// relative, finer than the bf16 of queries and outputs; sums and statistics are
+// fp32.
 // ---------------------------------------------------------------------------
 PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Rows 0-7 alone (a1 = a3 = 0): two accumulators.
+PA_DEVINL void mma_f16_top(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  [[maybe_unused]] float x2, x3;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
+      "{%0, %1, %9, %9};"
+      : "+f"(d[0]), "+f"(d[1]), "=f"(x2), "=f"(x3)
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// d = A B with 8 columns of A.
+PA_DEVINL void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held two to a lane.
@@ -323,10 +361,19 @@ PA_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+PA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+PA_DEVINL float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w & 0xFFFFu))); }
+
 // s * (16 + u) + c of the two codes in bits 6-9 and 22-25 of w.  The mask-or is
 // one three-input logic instruction (LUT 0xEA: a & b | c) only when one of its
 // two constants is in a register: `sixteen` is 16 twice, kept there by keep_reg.
 constexpr uint32_t kSixteen = 0x4C004C00u;
+constexpr uint32_t kOnes = 0x3C003C00u;
 PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t sixteen, uint32_t s, uint32_t c) {
   uint32_t v, d;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(0x03C003C0), "r"(sixteen));
@@ -340,6 +387,50 @@ PA_DEVINL uint32_t keep_reg(uint32_t v) {
   return v;
 }
 
+// u * 2^-18 of the codes in bits 6-9, u * 2^-22 of those in bits 2-5.
+PA_DEVINL uint32_t raw_hi(uint32_t w) { return w & 0x03C003C0u; }
+PA_DEVINL uint32_t raw_lo(uint32_t w) { return w & 0x003C003Cu; }
+
+// mbarriers by their shared-memory address: the consumers' registers are scarce,
+// and 64-bit pointers to them would take a dozen.
+PA_DEVINL bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// As mbar_wait_bounded, with the abort flag at a shared-memory address.
+PA_DEVINL bool bar_wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, unsigned int* err) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      uint32_t gone;
+      asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+      if (gone) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+        raise_flag(err, PA_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+PA_DEVINL bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort, unsigned int* err) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity, abort, err);
+}
+
+PA_DEVINL void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Loads from a shared-memory address.  Volatile: they stay between the wait for
 // a stage and its release.
 PA_DEVINL uint32_t lds32(uint32_t a) {
@@ -347,137 +438,226 @@ PA_DEVINL uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
-PA_DEVINL void lds64(uint32_t (&r)[2], uint32_t a) {
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a));
-}
 PA_DEVINL void lds128(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
+// N consecutive words.
+template <int N>
+PA_DEVINL void lds_words(uint32_t* r, uint32_t a) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 1) {
+    r[0] = lds32(a);
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a));
+  } else {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  }
+}
 
-template <int HD>
-PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty,
-                            uint64_t* handed, uint64_t* taken, const int4* meta, volatile int* abort_flag, int h,
-                            int group) {
-  constexpr int KW = HD / 32;  // words of K codes a lane holds per token
-  constexpr int VW = HD / 64;  // words of V codes a lane holds per token
-  constexpr int MB = HD / 16;  // 16-dim blocks of O
+template <int HD, int NG, int HKV>
+PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int group) {
+  constexpr int GS = HD / NG;
+  constexpr int KW = GS / 32;          // words of K codes a lane holds of a token's group
+  constexpr int MB = HD / 16;          // 16-dim blocks of O: four to a word of V codes
+  constexpr int VW = MB / 4;           // words of V codes a lane holds of a token
+  constexpr bool kRawV = GS >= 64;     // V codes enter the products undecoded
+  constexpr int VL = kRawV ? GS / 64 : VW;  // of them, one load's
+  constexpr int NL = VW / VL;          // loads of V codes a token
+  using Row = Q4Row<HD, NG, HKV>;
+  constexpr uint32_t R = Row::kBytes, kChunk = kTok * R;
   const int lane = threadIdx.x & 31;
-  const int G = p.k.Hq / p.k.Hkv;
+  const int G = p.k.Hq / HKV;
   const int gq = lane >> 2, tq = lane & 3;
-  const uint32_t R = p.k.row_bytes, NG = HD >> p.log2gs;
   // Token of row g of a half: with rows a multiple of 128 bytes apart, odd rows
   // take the tokens 4 on, so that the tokens which meet in one pass of a load
   // lie in different banks.
-  const int flip = (R & 127u) == 0 ? 4 : 0;
+  constexpr int flip = R % 128 == 0 ? 4 : 0;
   const int kt = gq ^ ((gq & 1) * flip), vt0 = 2 * tq, vt1 = (2 * tq + 1) ^ flip;
-  // this lane's places in a stage: K codes and parameters of its token in row gq
-  // (gq + 8: 8 rows on), V codes and parameters of those in rows 2 tq, 2 tq + 1
-  const uint32_t k_codes = kt * R + q4_swz(h * (HD / 2) + tq * (HD / 8), p.codes, kt);
-  const uint32_t k_pars = kt * R + p.codes + q4_swz((h * NG + ((tq * (HD / 4)) >> p.log2gs)) * 4, p.pars, kt);
-  const uint32_t vo = h * (HD / 2) + gq * (HD / 16), vp = (h * NG + ((gq * (HD / 8)) >> p.log2gs)) * 4;
-  const uint32_t v_codes0 = p.k.chunk_bytes + vt0 * R + q4_swz(vo, p.codes, vt0);
-  const uint32_t v_codes1 = p.k.chunk_bytes + vt1 * R + q4_swz(vo, p.codes, vt1);
-  const uint32_t v_pars0 = p.k.chunk_bytes + vt0 * R + p.codes + q4_swz(vp, p.pars, vt0);
-  const uint32_t v_pars1 = p.k.chunk_bytes + vt1 * R + p.codes + q4_swz(vp, p.pars, vt1);
-  const uint32_t smem0 = smem_u32(smem), meta0 = smem_u32(meta);
-  const uint32_t sixteen = keep_reg(kSixteen);
+  // This lane's places in a stage: K codes (for each group) and parameters of its
+  // token in row gq (gq + 8: 8 rows on), V codes and parameters of those in rows
+  // 2 tq and 2 tq + 1.  They are kept in shared memory, in vectors of four for
+  // the lane to load when it needs them: as registers they made the loop spill.
+  constexpr int KV = (NG + 4) / 4, VV = (2 * NL + 5) / 4;  // vectors of K's places (NG + 1) and V's (2 NL + 2)
+  const uint32_t places = smem_u32(smem) + p.off_places + (h * 32 + lane) * 16;  // vector i: i * Hkv * 512 on
+  constexpr uint32_t vector = HKV * 512;
+  {
+    uint32_t at[4 * (KV + VV)] = {};
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      at[g] = kt * R + q4_swz(h * (HD / 2) + g * (GS / 2) + tq * (KW * 4), Row::kCodes, kt);
+    at[NG] = kt * R + Row::kCodes + q4_swz(h * NG * 4, Row::kPars, kt);
+    const uint32_t v_group = kRawV ? 0u : ((gq * (HD / 8)) / GS) * 4u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t vt = u ? vt1 : vt0, row = kChunk + vt * R;
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        at[4 * KV + 2 * i + u] = row + q4_swz(h * (HD / 2) + i * (GS / 2) + gq * (VL * 4), Row::kCodes, vt);
+      at[4 * KV + 2 * NL + u] = row + Row::kCodes + q4_swz(h * NG * 4 + v_group, Row::kPars, vt);
+    }
+#pragma unroll
+    for (int i = 0; i < KV + VV; ++i)  // (the other group's warp stores the same)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(places + i * vector), "r"(at[4 * i]),
+                   "r"(at[4 * i + 1]), "r"(at[4 * i + 2]), "r"(at[4 * i + 3])
+                   : "memory");
+  }
+  // first dim of this lane's w-th word of V codes
+  auto v_dim = [&](int w) { return kRawV ? (w / VL) * GS + (gq * VL + w % VL) * 8 : gq * (HD / 8) + w * 8; };
+  const uint32_t smem0 = smem_u32(smem);
+  // the barriers of the table in the kernel below
+  auto full = [&](int s) { return smem0 + p.k.off_bar + 8 * s; };
+  auto empty = [&](int s) { return smem0 + p.k.off_bar + 8 * (kMaxStages + s); };
+  auto handed = [&] { return smem0 + p.k.off_bar + 8 * (2 * kMaxStages + h); };
+  auto taken = [&] { return smem0 + p.k.off_bar + 8 * (2 * kMaxStages + 8 + h); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, smem0 + p.k.off_abort, p.k.err); };
+  [[maybe_unused]] const uint32_t sixteen = keep_reg(kSixteen);
+  [[maybe_unused]] const uint32_t par_half = (gq & 1) ? 0x7632 : 0x5410;  // c or s of two words
 
-  uint32_t qf[MB][2];  // B fragments of the queries
+  uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
+  uint32_t qm = 0u;    // 2^-10 (16 sum q, sum q) over the dims of group tq
   float o[MB][4];
-  float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the queries' power of two undone)
+  // Sums over the tokens: of p s and p c (row gq < 4: group gq / 2's s or, odd,
+  // c; only where V's codes are raw), and of p (the other rows).
+  float om[2] = {0.f, 0.f};
+  [[maybe_unused]] int s_bits = 0;  // exponent bits of the largest s seen: E = max(s_bits - 21, -15); 0: none above 0 yet
+  float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone)
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
-  float l[2] = {0.f, 0.f};     // this lane's part of the softmax sums
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
-  uint32_t hand_phase = 0;  // parity of the handovers so far
+  uint32_t hand_phase = 0;     // parity of the handovers so far
   Ring ring;
   if (group) ring.next(p.stages);  // group g takes stages g, g + 2, ... of the ring
   for (;; ring.next(p.stages), ring.next(p.stages)) {
     const int s = ring.s;
-    if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
-    uint32_t md[4];
-    lds128(md, meta0 + s * 16);
-    const uint32_t flags = md[1];
+    if (!wait(full(s), ring.phase)) break;
+    const uint32_t md = smem0 + p.k.off_meta + s * 16;  // {request, tokens and flags, share, slot}
+    const uint32_t flags = lds32(md + 4);
     const uint32_t st = smem0 + s * p.stage_bytes;
 
     if (flags & (kFirst | kNew | kEnd)) {
-    if (flags & kEnd) break;
-    if (flags & kFirst) {
-      const uint32_t qrow = st + 2 * p.k.chunk_bytes + ((h * G + gq) * HD + tq * (HD / 4)) * 2;
-      float qv[HD / 4];
-      float mx = 0.f;
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        const uint32_t qrow = st + 2 * kChunk + (h * G + gq) * HD * 2;
+        uint32_t qw[NG][KW * 4];  // bf16 pairs
+        float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (gq < G) lds128(w, qrow + i * 16);
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = bf16x2_to_float2(w[e]);
-          qv[8 * i + 2 * e] = v.x;
-          qv[8 * i + 2 * e + 1] = v.y;
-          mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+          for (int i = 0; i < KW; ++i) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (gq < G) lds128(w, qrow + (g * GS + tq * (GS / 4) + i * 8) * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              qw[g][4 * i + e] = w[e];
+              const float2 v = bf16x2_to_float2(w[e]);
+              mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // 2^-E of the largest magnitude's exponent E, and 2^E
+        const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+        const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          sum[g] = 0.f;
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {
+            float q[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = bf16x2_to_float2(qw[g][4 * i + e]);
+              q[2 * e] = v.x * down * 256.f;
+              q[2 * e + 1] = v.y * down * 256.f;
+            }
+            // as they are rounded: the second term's sum has to be that of the first's queries
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              q[e] = __half2float(__float2half_rn(q[e]));
+              sum[g] += q[e];
+            }
+            const int k = 2 * (g * KW + i);
+            qf[k][0] = pack_f16x2(q[0], q[4]);
+            qf[k][1] = pack_f16x2(q[1], q[5]);
+            qf[k + 1][0] = pack_f16x2(q[2] * 16.f, q[6] * 16.f);
+            qf[k + 1][1] = pack_f16x2(q[3] * 16.f, q[7] * 16.f);
+          }
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
         }
+        qm = 0u;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (tq == g) {
+            const float r = __half2float(__float2half_rn(sum[g] * 0x1p-18f));
+            qm = pack_f16x2(r * 16.f, r);
+          }
+        mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
+        mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        m[0] = m[1] = 0.f;
+        limit = -INFINITY;
+        om[0] = om[1] = 0.f;
+        s_bits = 0;
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 2^-E of the largest magnitude's exponent E, and 2^E
-      const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-      const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
-#pragma unroll
-      for (int i = 0; i < HD / 32; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          qf[2 * i + (v >> 1)][v & 1] = pack_f16x2(qv[8 * i + v] * down, qv[8 * i + 4 + v] * down);
-      mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq);
-      mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4);
-#pragma unroll
-      for (int j = 0; j < MB; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-      m[0] = m[1] = l[0] = l[1] = 0.f;
-      limit = -INFINITY;
-    }
-    if (flags & kNew) {
-      unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
-      const uint32_t n0 = flags & 255, n1 = (flags >> 8) & 255;
-      write_new_row<__nv_bfloat16, HD>(p, kst, kst + p.k.chunk_bytes, md[0], n1 ? kHalf + n1 - 1 : n0 - 1, md[3], h,
-                                       lane);
-    }
+      if (flags & kNew) {
+        unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
+        const uint32_t n0 = flags & 255, n1 = (flags >> 8) & 255;
+        write_new_row<__nv_bfloat16, HD>(p, kst, kst + kChunk, lds32(md), n1 ? kHalf + n1 - 1 : n0 - 1,
+                                         lds32(md + 12), h, lane);
+      }
     }
 
     // S^T = K Q^T of both halves
-    float sc[2][4];
+    float t[2][4];
+    uint32_t k_at[4 * KV];  // k_codes[NG], k_pars
+#pragma unroll
+    for (int i = 0; i < KV; ++i) lds_words<4>(k_at + 4 * i, places + i * vector);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      uint32_t kw[2][KW], ks[2], kc[2];
+      uint32_t kw[2][NG][KW], par[2][NG];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t row = st + (hf * kHalf + u * 8) * R;
-        if constexpr (KW == 4) lds128(kw[u], row + k_codes);
-        else lds64(kw[u], row + k_codes);
-        const uint32_t par = lds32(row + k_pars);
-        ks[u] = __byte_perm(par, 0, 0x1010);
-        kc[u] = __byte_perm(par, 0, 0x3232);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) lds_words<KW>(kw[u][g], row + k_at[g]);
+        lds_words<NG>(par[u], row + k_at[NG]);
+      }
+      uint32_t pm[2];  // the parameters of group tq (of any where there is none: its queries' sum is 0)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        pm[u] = par[u][0];
+        if constexpr (NG == 2) pm[u] = (tq & 1) ? par[u][1] : par[u][0];
+        if constexpr (NG == 4) pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
+      }
+      float sc[4];
+      mma_f16_k8(sc, pm[0], pm[1], qm);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const uint32_t w0 = kw[0][g][i], w1 = kw[1][g][i];
+          const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
+          const int k = 2 * (g * KW + i);
+          mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), qf[k][0], qf[k][1]);
+          mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), qf[k + 1][0], qf[k + 1][1]);
+        }
+        const float s0 = f16_lo(par[0][g]), s1 = f16_lo(par[1][g]);
+        sc[0] = fmaf(d[0], s0, sc[0]);
+        sc[1] = fmaf(d[1], s0, sc[1]);
+        sc[2] = fmaf(d[2], s1, sc[2]);
+        sc[3] = fmaf(d[3], s1, sc[3]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[hf][e] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const uint32_t w0 = kw[0][i], w1 = kw[1][i];
-        const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
-        mma_f16(sc[hf], q4_pair(w0, sixteen, ks[0], kc[0]), q4_pair(w1, sixteen, ks[1], kc[1]), q4_pair(y0, sixteen, ks[0], kc[0]),
-                q4_pair(y1, sixteen, ks[1], kc[1]), qf[2 * i][0], qf[2 * i][1]);
-        mma_f16(sc[hf], q4_pair(w0 << 4, sixteen, ks[0], kc[0]), q4_pair(w1 << 4, sixteen, ks[1], kc[1]),
-                q4_pair(y0 << 4, sixteen, ks[0], kc[0]), q4_pair(y1 << 4, sixteen, ks[1], kc[1]), qf[2 * i + 1][0], qf[2 * i + 1][1]);
-      }
+      for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[e], mult[e & 1], -m[e & 1]);
     }
 
     // softmax: exponents relative to a reference that only moves when a score
     // passes it by more than 2^8 (probabilities stay below 2^8: a float16)
-    float t[2][4];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[hf][e], mult[e & 1], -m[e & 1]);
     if (flags & kRagged) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -501,8 +681,8 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
         d0 = fmaxf(d0, 0.f);
         d1 = fmaxf(d1, 0.f);
         const float a0 = ex2_approx(-d0), a1 = ex2_approx(-d1);
-        l[0] *= a0;
-        l[1] *= a1;
+        om[0] *= a0;
+        om[1] *= a1;
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           o[j][0] *= a0;
@@ -527,65 +707,164 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
     for (int hf = 0; hf < 2; ++hf) {
       const float p0 = ex2_approx(t[hf][0]), p1 = ex2_approx(t[hf][1]);
       const float p2 = ex2_approx(t[hf][2]), p3 = ex2_approx(t[hf][3]);
-      l[0] += p0 + p2;
-      l[1] += p1 + p3;
       pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
       pb[hf][1] = movm_trans(pack_f16x2(p2, p3));
+      if constexpr (!kRawV) mma_f16_top(om, kOnes, kOnes, pb[hf][0], pb[hf][1]);
     }
 
     // O^T += V^T P^T
+    uint32_t v_at[4 * VV];  // v_codes[NL][2], v_pars[2]
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t vw[4][2], vpar[4];
+    for (int i = 0; i < VV; ++i) lds_words<4>(v_at + 4 * i, places + (KV + i) * vector);
+    if constexpr (kRawV) {
+      uint32_t vs[2][NG][2], vm[2][2];  // s of two tokens; the rows of the second term
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t row = st + (hf * kHalf + (u >> 1) * 8) * R;
-        if constexpr (VW == 2) lds64(vw[u], row + ((u & 1) ? v_codes1 : v_codes0));
-        else vw[u][0] = lds32(row + ((u & 1) ? v_codes1 : v_codes0));
-        vpar[u] = lds32(row + ((u & 1) ? v_pars1 : v_pars0));
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t par[4][NG];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          lds_words<NG>(par[u], st + (hf * kHalf + (u >> 1) * 8) * R + v_at[2 * NL + (u & 1)]);
+          if (flags & kRagged) {
+            // rows past the context meet probability 0 and must be finite
+            const int n = (flags >> (8 * hf)) & 255;
+            if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n)
+#pragma unroll
+              for (int g = 0; g < NG; ++g) par[u][g] = 0u;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int g = 0; g < NG; ++g) vs[hf][g][u] = __byte_perm(par[2 * u][g], par[2 * u + 1][g], 0x5410);
+          uint32_t w0 = par[2 * u][0], w1 = par[2 * u + 1][0];
+          if constexpr (NG == 2) {
+            w0 = (gq & 2) ? par[2 * u][1] : w0;
+            w1 = (gq & 2) ? par[2 * u + 1][1] : w1;
+          }
+          vm[hf][u] = gq < 4 ? __byte_perm(w0, w1, par_half) : kOnes;
+        }
       }
-      if (flags & kRagged) {
-        // rows past the context meet probability 0 and must be finite
-        const int n = (flags >> (8 * hf)) & 255;
+      // a larger s than the scale was made for: scale anew (s is never negative,
+      // so its bits compare as integers)
+      uint32_t top = 0u;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) top = __vmaxu2(top, vs[hf][g][u]);
+      const uint32_t most = s_bits ? ((s_bits + 1) << 10) - 1 : 0u;  // the largest s that the scale is made for
+      if (__any_sync(0xffffffffu, __vmaxu2(top, most * 0x00010001u) != most * 0x00010001u)) {
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+        const int now = max(static_cast<int>(bits >> 10), 1);
+        if (s_bits != 0) {
+          const float a = __uint_as_float(static_cast<uint32_t>(127 + max(s_bits, 6) - max(now, 6)) << 23);
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] *= a;
+        }
+        s_bits = now;
+      }
+      // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
+      const uint32_t s_scale = static_cast<uint32_t>(36 - max(s_bits, 6)) * (0x00010001u << 10);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        mma_f16_top(om, vm[hf][0], vm[hf][1], pb[hf][0], pb[hf][1]);
+        uint32_t vw[4][VW];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n) vpar[u] = 0u;
-      }
-      uint32_t vs[2], vc[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        vs[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x5410);
-        vc[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x7632);
-      }
+          for (int i = 0; i < NL; ++i)
+            lds_words<VL>(&vw[u][i * VL], st + (hf * kHalf + (u >> 1) * 8) * R + v_at[2 * i + (u & 1)]);
 #pragma unroll
-      for (int j = 0; j < VW; ++j)
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t b0 = mul_f16x2(pb[hf][0], mul_f16x2(vs[hf][w / VL][0], s_scale));
+          const uint32_t b1 = mul_f16x2(pb[hf][1], mul_f16x2(vs[hf][w / VL][1], s_scale));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t xx[2], yy[2];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t xx[2], yy[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            xx[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x7632 : 0x5410);
-            yy[u] = __byte_perm(vw[2 * u][j], vw[2 * u + 1][j], q ? 0x6723 : 0x4501);
+            for (int u = 0; u < 2; ++u) {
+              xx[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x7632 : 0x5410);
+              yy[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x6723 : 0x4501);
+            }
+            mma_f16(o[4 * w + 2 * q], raw_hi(xx[0]), raw_hi(yy[0]), raw_hi(xx[1]), raw_hi(yy[1]), b0, b1);
+            mma_f16(o[4 * w + 2 * q + 1], raw_lo(xx[0]), raw_lo(yy[0]), raw_lo(xx[1]), raw_lo(yy[1]), b0, b1);
           }
-          mma_f16(o[4 * j + 2 * q], q4_pair(xx[0], sixteen, vs[0], vc[0]), q4_pair(yy[0], sixteen, vs[0], vc[0]),
-                  q4_pair(xx[1], sixteen, vs[1], vc[1]), q4_pair(yy[1], sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
-          mma_f16(o[4 * j + 2 * q + 1], q4_pair(xx[0] << 4, sixteen, vs[0], vc[0]), q4_pair(yy[0] << 4, sixteen, vs[0], vc[0]),
-                  q4_pair(xx[1] << 4, sixteen, vs[1], vc[1]), q4_pair(yy[1] << 4, sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
         }
+      }
+    } else {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t vw[4][VW], vpar[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t row = st + (hf * kHalf + (u >> 1) * 8) * R;
+          lds_words<VW>(vw[u], row + v_at[u & 1]);
+          vpar[u] = lds32(row + v_at[2 * NL + (u & 1)]);
+        }
+        if (flags & kRagged) {
+          // rows past the context meet probability 0 and must be finite
+          const int n = (flags >> (8 * hf)) & 255;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n) vpar[u] = 0u;
+        }
+        uint32_t vs[2], vc[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          vs[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x5410);
+          vc[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x7632);
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t xx[2], yy[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              xx[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x7632 : 0x5410);
+              yy[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x6723 : 0x4501);
+            }
+            mma_f16(o[4 * w + 2 * q], q4_pair(xx[0], sixteen, vs[0], vc[0]), q4_pair(yy[0], sixteen, vs[0], vc[0]),
+                    q4_pair(xx[1], sixteen, vs[1], vc[1]), q4_pair(yy[1], sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
+            mma_f16(o[4 * w + 2 * q + 1], q4_pair(xx[0] << 4, sixteen, vs[0], vc[0]),
+                    q4_pair(yy[0] << 4, sixteen, vs[0], vc[0]), q4_pair(xx[1] << 4, sixteen, vs[1], vc[1]),
+                    q4_pair(yy[1] << 4, sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
+          }
+      }
+    }
+    uint32_t b = 0, share = 0;
+    if (flags & kLast) {
+      b = lds32(md);
+      share = lds32(md + 8);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
+    if (lane == 0) bar_arrive(empty(s));
 
     if (flags & (kLast | kYield)) {
-      const int b = md[0];
+      float l[2];  // the softmax sums
+      l[0] = __shfl_sync(0xffffffffu, om[0], 16 + tq);
+      l[1] = __shfl_sync(0xffffffffu, om[1], 16 + tq);
+      if constexpr (kRawV) {
+        // the powers of two undone, the second term added
+        const float hi = __uint_as_float(static_cast<uint32_t>(127 + 18 - 21 + max(s_bits, 6)) << 23), lo = hi * 16.f;
 #pragma unroll
-      for (int k = 4; k < 32; k <<= 1) {
-        l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
-        l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+        for (int g = 0; g < NG; ++g) {
+          float add[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], 8 * g + tq), __shfl_sync(0xffffffffu, om[e], 8 * g + 4 + tq));
+#pragma unroll
+          for (int j = g * 4 * VL; j < (g + 1) * 4 * VL; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
+        }
       }
       if (flags & kYield) {
         // hand this group's part over: once the previous one has been taken
-        if (!mbar_wait_bounded(&taken[h], hand_phase ^ 1, abort_flag, p.k.err)) break;
+        if (!wait(taken(), hand_phase ^ 1)) break;
         hand_phase ^= 1;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -594,18 +873,18 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
             float* dst = reinterpret_cast<float*>(smem + p.off_hand) + (h * G + g) * (HD + 4);
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
-              *reinterpret_cast<float4*>(dst + gq * (HD / 8) + 2 * j) =
+              *reinterpret_cast<float4*>(dst + v_dim(j / 4) + (j & 2) * 2) =
                   make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
             if (gq == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(m[e], l[e]);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&handed[h]);
+        if (lane == 0) bar_arrive(handed());
         continue;
       }
       if (!(flags & kSolo)) {
         // add the other group's part
-        if (!mbar_wait_bounded(&handed[h], hand_phase, abort_flag, p.k.err)) break;
+        if (!wait(handed(), hand_phase)) break;
         hand_phase ^= 1;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -620,7 +899,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
             l[e] = l[e] * wa + ml.y * wb;
 #pragma unroll
             for (int j = 0; j < MB; j += 2) {
-              const float4 v = *reinterpret_cast<const float4*>(src + gq * (HD / 8) + 2 * j);
+              const float4 v = *reinterpret_cast<const float4*>(src + v_dim(j / 4) + (j & 2) * 2);
               o[j][e] = o[j][e] * wa + v.x * wb;
               o[j][2 + e] = o[j][2 + e] * wa + v.y * wb;
               o[j + 1][e] = o[j + 1][e] * wa + v.z * wb;
@@ -629,7 +908,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[h]);
+        if (lane == 0) bar_arrive(taken());
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -638,20 +917,20 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, uint64_t* fu
           const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
           const int hq = h * G + g;
           if (flags & kWhole) {
-            char* dst = p.k.out + ((static_cast<int64_t>(b) * p.k.Hq + hq) * HD + gq * (HD / 8)) * 2;
+            char* dst = p.k.out + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD * 2;
 #pragma unroll
             for (int j = 0; j < MB; j += 4)
-              stg16(dst + j * 4, make_uint4(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
-                                            pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv),
-                                            pack_bf16x2(o[j + 2][e] * inv, o[j + 2][2 + e] * inv),
-                                            pack_bf16x2(o[j + 3][e] * inv, o[j + 3][2 + e] * inv)));
+              stg16(dst + v_dim(j / 4) * 2, make_uint4(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
+                                                       pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv),
+                                                       pack_bf16x2(o[j + 2][e] * inv, o[j + 2][2 + e] * inv),
+                                                       pack_bf16x2(o[j + 3][e] * inv, o[j + 3][2 + e] * inv)));
           } else {
-            const int64_t slot = static_cast<int64_t>(md[2]) + b;
-            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + gq * (HD / 8);
+            const int64_t slot = static_cast<int64_t>(share) + b;
+            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD;
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
-              *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[j][e] * inv, o[j][2 + e] * inv,
-                                                                    o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
+              *reinterpret_cast<float4*>(dst + v_dim(j / 4) + (j & 2) * 2) =
+                  make_float4(o[j][e] * inv, o[j][2 + e] * inv, o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
             if (gq == 0) p.k.lse_part[slot * p.k.Hq + hq] = l[e] > 0.f ? m[e] + log2f(l[e]) : -INFINITY;
           }
         }
@@ -823,11 +1102,12 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
 
 // bf16: two groups of one consumer warp per kv-head, which take the chunks in
 // turn from one ring, and the producer; fp32: one group.
-template <typename T, int HD, int GP>
-constexpr int kMaxThreads = sizeof(T) == 2 ? 17 * 32 : 9 * 32;
-
-template <typename T, int HD, int GP>
-__global__ void __launch_bounds__(kMaxThreads<T, HD, GP>, sizeof(T) == 2 ? 1 : 2) decode_q4_kernel(const Q4Params p) {
+// V: of fp32, the group's q-heads rounded up to a power of two; of bf16, the
+// groups of a head row, for HKV kv-heads (a row's layout in the instructions:
+// 27 address additions a chunk less).
+template <typename T, int HD, int V, int HKV>
+__global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) == 2 ? 1 : 2)
+    decode_q4_kernel(const Q4Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const KParams& k = p.k;
   const int NW = k.Hkv;
@@ -859,9 +1139,9 @@ __global__ void __launch_bounds__(kMaxThreads<T, HD, GP>, sizeof(T) == 2 ? 1 : 2
   }
   if constexpr (sizeof(T) == 2) {
     const int group = warp >= NW;
-    mma_consumer<HD>(p, smem, full, empty, handed, taken, meta, abort_flag, warp - group * NW, group);
+    mma_consumer<HD, V, HKV>(p, smem, warp - group * NW, group);
   } else {
-    simt_consumer<T, HD, GP>(p, smem, full, empty, meta, abort_flag);
+    simt_consumer<T, HD, V>(p, smem, full, empty, meta, abort_flag);
   }
 }
 
@@ -870,24 +1150,36 @@ struct Fns {
   const void* merge;
 };
 
-template <typename T, int HD>
-Fns fns_for(int G) {
-  const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<T, HD>);
-  // the tensor-core consumer takes any group of up to 8 heads
-  if constexpr (sizeof(T) == 2) {
-    return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
-  } else {
-    if (G == 1) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 1>), merge};
-    if (G == 2) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 2>), merge};
-    if (G <= 4) return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 4>), merge};
-    return {reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 8>), merge};
+template <int HD, int HKV>
+const void* mma_fn(int gs) {
+  if constexpr (HD == 128)
+    if (gs == 32) return reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 4, HKV>);
+  return HD == 2 * gs ? reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 2, HKV>)
+                      : reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 1, HKV>);
+}
+
+template <int HD>
+const void* simt_fn(int G) {
+  if (G == 1) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 1, 0>);
+  if (G == 2) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 2, 0>);
+  if (G <= 4) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 4, 0>);
+  return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 8, 0>);
+}
+
+template <int HD>
+Fns fns_for(const pa_cache_desc& d, int gs) {
+  if (d.dtype != PA_BF16)
+    return {simt_fn<HD>(d.num_q_heads / d.num_kv_heads), reinterpret_cast<const void*>(decode_merge_kernel<float, HD>)};
+  const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<__nv_bfloat16, HD>);
+  switch (d.num_kv_heads) {
+    case 1: return {mma_fn<HD, 1>(gs), merge};
+    case 2: return {mma_fn<HD, 2>(gs), merge};
+    case 4: return {mma_fn<HD, 4>(gs), merge};
+    default: return {mma_fn<HD, 8>(gs), merge};
   }
 }
 
-Fns get_fns(int dtype, int hd, int G) {
-  if (dtype == PA_BF16) return hd == 128 ? fns_for<__nv_bfloat16, 128>(G) : fns_for<__nv_bfloat16, 64>(G);
-  return hd == 128 ? fns_for<float, 128>(G) : fns_for<float, 64>(G);
-}
+Fns get_fns(const pa_cache_desc& d, int gs) { return d.head_dim == 128 ? fns_for<128>(d, gs) : fns_for<64>(d, gs); }
 
 // Bytes of a ring stage: a chunk's rows of K and V, and a request's queries.
 size_t q4_stage_bytes(const pa_cache_desc& d, const DecodePlan& pl) {
@@ -929,18 +1221,20 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // statistics, then the scaled queries
   pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4
                          : static_cast<size_t>(d.num_q_heads) * (d.head_dim + 4) * 4);  // or the handed-over part
+  const uint32_t off_places = place(simt ? 0 : static_cast<size_t>(4) * d.num_kv_heads * 512);
   // The ring takes what is left of a CTA's share of the SM's shared memory with
   // 16 consumer warps on an SM: four or more chunks.
   const size_t fixed = align_up(off, 128), stage = q4_stage_bytes(d, pl);
   const size_t share = static_cast<size_t>(di.max_smem_optin) * std::min(pl.nw, 16) / 16 - 1024;
   pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, share > fixed ? (share - fixed) / stage : 0)));
   const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
+  pl.off_places = off_places + ring;
   for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
     *o += ring;
   pl.smem_bytes = ring + fixed;
   if (pl.smem_bytes > static_cast<size_t>(di.max_smem_optin)) return cudaErrorInvalidValue;
   int occ = 0;
-  e = ctas_per_sm(di, get_fns(d.dtype, d.head_dim, G).main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
+  e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
   if (e != cudaSuccess) return e;
   const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
   int64_t n = static_cast<int64_t>(occ) * di.sm_count;
@@ -957,7 +1251,7 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
 
 cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& pl, const DecodeArgs& a,
                              cudaStream_t s) {
-  const Fns f = get_fns(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
+  const Fns f = get_fns(d, gs);
   Q4Params p{};
   p.k = decode_params(d, pl, a, q4_row_bytes(d, gs));
   p.stages = pl.stages;
@@ -969,6 +1263,7 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   p.by_request = pl.by_request;
   p.off_q = pl.off_ml + pl.nw * 16 * 4;
   p.off_hand = pl.off_ml;
+  p.off_places = pl.off_places;
   void* args[] = {&p};
   return launch_decode_kernels(f.main, f.merge, pl, p.k, args, s);
 }
