@@ -5,6 +5,10 @@ Attention.forward listings): positions and slots of the step's new tokens,
 optional per-head q/k RMSNorm + rotary, the KV write, then decode or
 chunked-prefill attention over the cache.  This module only allocates buffers
 and sequences calls; every value is computed by libpagedattn's kernels.
+
+Buffers allocated with a ``group_size`` step over a 4-bit cache: the writes
+quantise, decode attends to the codes, and prefill reads the contexts back into
+a staging cache of the descriptor's dtype and attends to that.
 """
 from __future__ import annotations
 
@@ -13,8 +17,22 @@ from typing import Optional
 
 import torch
 
-from . import (pa_decode, pa_decode_workspace_size, pa_kv_write, pa_prefill_qk_norm_rope_kv_write, pa_prefill_step,
-               pa_prefill_workspace_size, pa_slot_mapping)
+from . import (cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
+               pa_kv_read_q4, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
+               pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step, pa_prefill_varlen, pa_prefill_workspace_size,
+               pa_slot_mapping)
+
+
+@dataclasses.dataclass
+class Staging:
+    """Where a prefill step over a 4-bit cache reads the contexts back to: a paged cache of the descriptor's dtype
+    in which request b has the ``max_pages`` pages from ``b * max_pages`` on."""
+    desc: object                       # the staging cache's descriptor
+    max_pages: int
+    cu_rows: torch.Tensor              # int32 [batch + 1]
+    block_tables: torch.Tensor         # int32 [batch, max_pages]
+    k: torch.Tensor                    # [batch * max_pages, page_size, Hkv, hd]
+    v: torch.Tensor
 
 
 @dataclasses.dataclass
@@ -25,6 +43,8 @@ class StepBuffers:
     q_out: Optional[torch.Tensor]      # [N, Hq, hd] normed + rotated q (when norm weights are used)
     workspace: Optional[torch.Tensor]  # decode split-KV / planned-prefill workspace (bytes)
     max_ctas: int = 0
+    group_size: int = 0                # dims that share a scale in a 4-bit cache; 0: a cache of the dtype's rows
+    staging: Optional[Staging] = None  # prefill over a 4-bit cache
 
 
 def torch_dtype(desc) -> torch.dtype:
@@ -33,10 +53,12 @@ def torch_dtype(desc) -> torch.dtype:
 
 def alloc_step_buffers(desc, kind: str, num_tokens: int, batch: int, max_context_len: int, device,
                        norm: bool = False, max_ctas: int = 0, max_seqlen_q: Optional[int] = None,
-                       plan_prefill: bool = True) -> StepBuffers:
+                       plan_prefill: bool = True, group_size: int = 0) -> StepBuffers:
     """Buffers of one step.  A prefill step gets the planned-launch workspace
     unless ``plan_prefill`` is False (or the shape is never planned); it is
-    sized for chunks up to ``max_seqlen_q`` tokens (default: ``num_tokens``)."""
+    sized for chunks up to ``max_seqlen_q`` tokens (default: ``num_tokens``).
+    ``group_size`` (32, 64 or 128) is that of a 4-bit cache; a prefill step over
+    one gets a staging cache for ``batch`` contexts of ``max_context_len``."""
     dt = torch_dtype(desc)
     n = max(num_tokens, 1)
     positions = torch.empty(n, dtype=torch.int32, device=device)
@@ -45,21 +67,36 @@ def alloc_step_buffers(desc, kind: str, num_tokens: int, batch: int, max_context
     q_out = torch.empty_like(out) if norm else None
     ws = None
     if kind == "decode":
-        nbytes = pa_decode_workspace_size(desc, batch, max_context_len, max_ctas)
+        fn = "pa_decode_q4_workspace_size" if group_size else "pa_decode_workspace_size"
+        nbytes = (pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas) if group_size
+                  else pa_decode_workspace_size(desc, batch, max_context_len, max_ctas))
         if nbytes == 0:
-            raise RuntimeError("pa_decode_workspace_size returned 0 (unsupported shape or no device)")
+            raise RuntimeError(fn + " returned 0 (unsupported shape or no device)")
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif plan_prefill and num_tokens > 0:
         nbytes = pa_prefill_workspace_size(desc, batch, max_seqlen_q or num_tokens, num_tokens, max_context_len)
         if nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return StepBuffers(positions, slots, out, q_out, ws, max_ctas)
+    staging = None
+    if group_size and kind != "decode":
+        P = desc.page_size
+        max_pages = max(-(-max_context_len // P), 1)
+        pages = max(batch, 1) * max_pages
+        if pages * P >= 2 ** 31:
+            raise ValueError("the staged contexts have more than 2^31 - 1 rows")
+        shape = (pages, P, desc.num_kv_heads, desc.head_dim)
+        staging = Staging(cache_desc(desc.num_q_heads, desc.num_kv_heads, desc.head_dim, P, pages, dt), max_pages,
+                          torch.arange(0, pages * P + 1, max_pages * P, dtype=torch.int32, device=device),
+                          torch.arange(pages, dtype=torch.int32, device=device).view(-1, max_pages),
+                          torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device))
+    return StepBuffers(positions, slots, out, q_out, ws, max_ctas, group_size, staging)
 
 
 def write_rows(desc, k_rows, v_rows, cu_rows, lens, block_tables, max_pages_per_seq, bufs_positions, bufs_slots,
-               k_cache, v_cache, stream=None):
+               k_cache, v_cache, stream=None, group_size: int = 0):
     """Store already-computed K/V rows (the last ``cu_rows`` segment of each of
-    ``lens[b]`` tokens) into their slots: slot mapping then KV write."""
+    ``lens[b]`` tokens) into their slots: slot mapping then KV write.
+    ``group_size``: that of a 4-bit cache."""
     n = k_rows.shape[0]
     batch = lens.shape[0]
     if n == 0:
@@ -67,6 +104,9 @@ def write_rows(desc, k_rows, v_rows, cu_rows, lens, block_tables, max_pages_per_
     pa_slot_mapping(desc, batch, cu_rows, lens, block_tables, max_pages_per_seq, n, bufs_positions, bufs_slots,
                     stream)
     row = desc.num_kv_heads * desc.head_dim
+    if group_size:
+        pa_kv_write_q4(desc, group_size, k_rows, row, v_rows, row, n, bufs_slots, k_cache, v_cache, stream)
+        return
     pa_kv_write(desc, k_rows, row, v_rows, row, n, bufs_slots, k_cache, v_cache, stream)
 
 
@@ -76,6 +116,10 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
     """Run one step; returns ``bufs.out`` (the attention output of the new tokens)."""
     n = q.shape[0]
     batch = context_lens.shape[0]
+    if bufs.group_size:
+        return _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
+                            scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps,
+                            rope_theta, stream)
     if kind != "decode":
         # the write part and the attention in one call, whose attention planner
         # runs beside the write kernel
@@ -98,4 +142,34 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
         qa = q
     pa_decode(desc, qa, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len,
               scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
+    return bufs.out
+
+
+def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, scale,
+                 max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps, rope_theta, stream):
+    """The step over a 4-bit cache.  A prefill step whose metadata is flagged as bad (``pa_read_device_errors``)
+    attends, where a page was skipped, to what the staging cache held there before."""
+    n, batch, gs = q.shape[0], context_lens.shape[0], bufs.group_size
+    if q_norm_w is not None:
+        pa_prefill_qk_norm_rope_kv_write_q4(desc, gs, q, q.stride(0), k, k.stride(0), v, v.stride(0), n,
+                                            cu_seqlens_q, batch, context_lens, block_tables, max_pages_per_seq,
+                                            q_norm_w, k_norm_w, eps, rope_theta, bufs.q_out, k_cache, v_cache,
+                                            bufs.positions, bufs.slots, stream)
+        q = bufs.q_out
+    else:
+        pa_slot_mapping(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq, n, bufs.positions,
+                        bufs.slots, stream)
+        pa_kv_write_q4(desc, gs, k, k.stride(0), v, v.stride(0), n, bufs.slots, k_cache, v_cache, stream)
+    if kind == "decode":
+        pa_decode_q4(desc, gs, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
+                     max_context_len, scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
+        return bufs.out
+    st = bufs.staging
+    if batch > st.block_tables.shape[0] or max_context_len > st.max_pages * desc.page_size:
+        raise ValueError("the step's batch or max_context_len is beyond what the buffers were allocated for")
+    row = desc.num_kv_heads * desc.head_dim
+    pa_kv_read_q4(desc, gs, batch, st.cu_rows, None, context_lens, block_tables, max_pages_per_seq,
+                  batch * st.max_pages * desc.page_size, k_cache, v_cache, st.k, row, st.v, row, stream)
+    pa_prefill_varlen(st.desc, q, cu_seqlens_q, batch, max_seqlen_q, n, st.k, st.v, st.block_tables, st.max_pages,
+                      context_lens, max_context_len, scale, bufs.out, bufs.workspace, None, stream)
     return bufs.out

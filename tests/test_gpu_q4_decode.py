@@ -78,9 +78,9 @@ class Case:
 
     def check(self, out, ref=None):
         """Tolerance.  fp32: the products and sums are fp32, so an output is off by a few 2^-24 of the values'
-        magnitude per step: 1e-5 of it.  bf16: queries, values and probabilities enter the products as 16-bit floats
-        (at most 2^-9 of each, the error of the scores scaled by their size of a few units) and the output is rounded to
-        bf16 (2^-9): 1e-2 of the largest output."""
+        magnitude per step: 1e-5 of it.  bf16: queries, values and probabilities enter the products as float16
+        (2^-11 of each, the error of the scores scaled by their size of a few units) and the output is rounded to
+        bf16 (2^-8 of it): 1e-2 of the largest output."""
         ref = self.reference() if ref is None else ref
         live = self.lens > 0
         got = out.double().cpu().numpy()
