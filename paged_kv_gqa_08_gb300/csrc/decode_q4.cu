@@ -37,7 +37,6 @@ struct Q4Params {
   int32_t stage_bytes;  // K rows, V rows, queries
   int32_t groups;       // consumer groups: 2 (tensor cores) or 1
   int32_t by_request;   // 1: CTA b takes request b, whole (nothing to merge)
-  uint32_t off_places;  // [vectors][Hkv][32 lanes] of 16 bytes: the lanes' places in a stage
   uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, with its statistics
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
@@ -296,27 +295,27 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 // at columns 2 tq, 2 tq + 1 (+ 8), of B column gq at rows 2 tq, 2 tq + 1 (+ 8),
 // of C rows gq and gq + 8 at columns 2 tq, 2 tq + 1 (PTX ISA).
 //
-// Neither the order of the dims inside a sum, nor that of O's rows, nor that of
-// the tokens matters to the result, so a lane's share is what it can load in
-// one piece: of K, for each group of GS dims, GS / 4 consecutive dims of tokens
-// gq and gq + 8 (a register pairs dims d and d + 4 of one token); of V some
-// consecutive dims of tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (a register
-// pairs one dim of two tokens).
+// Neither the order of the dims inside a sum nor that of O's rows matters to the
+// result, so a lane's share is what ldmatrix hands it of 16-byte pieces, 32 dims
+// of a token each (the pieces of eight consecutive tokens lie in different banks,
+// whatever the row's size): of K, word tq of tokens gq and gq + 8, eight dims of
+// which a register pairs d and d + 4; of V, transposed, half word gq of tokens
+// 2 tq, 2 tq + 1 (+ 8), four dims that each pair two tokens in a register.
 //
 // The kernel is bound by instructions, not bytes, until decoding is cheap, so
-// codes enter the products undecoded where they can: u in bits 6-9 (2-5) of a
-// half word is the subnormal float16 u * 2^-18 (2^-22), exact, one mask.  With
-// m = 16 s + c the value is s u + m, so
+// codes enter the products undecoded: u in bits 6-9 (2-5) of a half word is the
+// subnormal float16 u * 2^-18 (2^-22), exact, one mask.  With m = 16 s + c the
+// value is s u + m, so
 //   S = sum over groups of s (sum q u) + m (sum q):  the sums of q u are scaled
 //       by s as they leave the tensor cores, the second term is one m16n8k8
 //       product of the parameter words (s, c) with (16 sum q, sum q);
 //   O = sum over tokens of (p s) u + p m:  p s replaces p as the B operand, and
-//       the second term is one product of the words' halves with p.
-// The last needs rows of one product (16 dims) to lie in one group and a lane's
-// dims to come in whole words, so groups of 64 and 128; with groups of 32, V is
-// decoded in registers: mask-or to the float16 16 + u, one multiply-add.
-// Decoding both K and V that way took 309 instructions for 16 tokens of a head;
-// this takes FIXME.
+//       the second term is one product of the transposed parameter piece, whose
+//       rows are its groups' s and c, with p.  The product's other eight rows
+//       are ones: the softmax sum.
+// 16 tokens of a head take 201 instructions with groups of 128, 111 of them on
+// the integer pipe (two cycles each); 309 with K and V decoded to float16 in
+// registers, 228 with raw codes loaded as words and paired by byte permutes.
 //
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
 // [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
@@ -330,15 +329,6 @@ PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Rows 0-7 alone (a1 = a3 = 0): two accumulators.
-PA_DEVINL void mma_f16_top(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  [[maybe_unused]] float x2, x3;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
-      "{%0, %1, %9, %9};"
-      : "+f"(d[0]), "+f"(d[1]), "=f"(x2), "=f"(x3)
-      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // d = A B with 8 columns of A.
@@ -369,23 +359,7 @@ PA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 PA_DEVINL float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w & 0xFFFFu))); }
 
-// s * (16 + u) + c of the two codes in bits 6-9 and 22-25 of w.  The mask-or is
-// one three-input logic instruction (LUT 0xEA: a & b | c) only when one of its
-// two constants is in a register: `sixteen` is 16 twice, kept there by keep_reg.
-constexpr uint32_t kSixteen = 0x4C004C00u;
 constexpr uint32_t kOnes = 0x3C003C00u;
-PA_DEVINL uint32_t q4_pair(uint32_t w, uint32_t sixteen, uint32_t s, uint32_t c) {
-  uint32_t v, d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(0x03C003C0), "r"(sixteen));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(s), "r"(c));
-  return d;
-}
-
-// A value the compiler takes for unknown, so that it stays in a register.
-PA_DEVINL uint32_t keep_reg(uint32_t v) {
-  asm volatile("" : "+r"(v));
-  return v;
-}
 
 // u * 2^-18 of the codes in bits 6-9, u * 2^-22 of those in bits 2-5.
 PA_DEVINL uint32_t raw_hi(uint32_t w) { return w & 0x03C003C0u; }
@@ -454,55 +428,42 @@ PA_DEVINL void lds_words(uint32_t* r, uint32_t a) {
   }
 }
 
+// Four 8x8 matrices of 16-bit elements, lane i's address that of row i % 8 of
+// matrix i / 8: two elements of row lane / 4 each, or (trans) of column lane / 4.
+PA_DEVINL void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+PA_DEVINL void ldsm4_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+
 template <int HD, int NG, int HKV>
 PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int group) {
-  constexpr int GS = HD / NG;
-  constexpr int KW = GS / 32;          // words of K codes a lane holds of a token's group
-  constexpr int MB = HD / 16;          // 16-dim blocks of O: four to a word of V codes
-  constexpr int VW = MB / 4;           // words of V codes a lane holds of a token
-  constexpr bool kRawV = GS >= 64;     // V codes enter the products undecoded
-  constexpr int VL = kRawV ? GS / 64 : VW;  // of them, one load's
-  constexpr int NL = VW / VL;          // loads of V codes a token
+  constexpr int NP = HD / 32;          // pieces of a head's codes in a row: 32 dims each
+  constexpr int PG = NP / NG;          // of them, a group's
+  constexpr int MB = HD / 16;          // 16-dim blocks of O: two to a piece
   using Row = Q4Row<HD, NG, HKV>;
   constexpr uint32_t R = Row::kBytes, kChunk = kTok * R;
   const int lane = threadIdx.x & 31;
   const int G = p.k.Hq / HKV;
   const int gq = lane >> 2, tq = lane & 3;
-  // Token of row g of a half: with rows a multiple of 128 bytes apart, odd rows
-  // take the tokens 4 on, so that the tokens which meet in one pass of a load
-  // lie in different banks.
-  constexpr int flip = R % 128 == 0 ? 4 : 0;
-  const int kt = gq ^ ((gq & 1) * flip), vt0 = 2 * tq, vt1 = (2 * tq + 1) ^ flip;
-  // This lane's places in a stage: K codes (for each group) and parameters of its
-  // token in row gq (gq + 8: 8 rows on), V codes and parameters of those in rows
-  // 2 tq and 2 tq + 1.  They are kept in shared memory, in vectors of four for
-  // the lane to load when it needs them: as registers they made the loop spill.
-  constexpr int KV = (NG + 4) / 4, VV = (2 * NL + 5) / 4;  // vectors of K's places (NG + 1) and V's (2 NL + 2)
-  const uint32_t places = smem_u32(smem) + p.off_places + (h * 32 + lane) * 16;  // vector i: i * Hkv * 512 on
-  constexpr uint32_t vector = HKV * 512;
-  {
-    uint32_t at[4 * (KV + VV)] = {};
+  // Places in a stage.  Codes: this lane's row of the matrices that one load
+  // takes, tokens 0-7 and 8-15 of pieces i, i + 1 (K's; V's are kChunk on).
+  uint32_t c_at[NP / 2];
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-      at[g] = kt * R + q4_swz(h * (HD / 2) + g * (GS / 2) + tq * (KW * 4), Row::kCodes, kt);
-    at[NG] = kt * R + Row::kCodes + q4_swz(h * NG * 4, Row::kPars, kt);
-    const uint32_t v_group = kRawV ? 0u : ((gq * (HD / 8)) / GS) * 4u;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t vt = u ? vt1 : vt0, row = kChunk + vt * R;
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        at[4 * KV + 2 * i + u] = row + q4_swz(h * (HD / 2) + i * (GS / 2) + gq * (VL * 4), Row::kCodes, vt);
-      at[4 * KV + 2 * NL + u] = row + Row::kCodes + q4_swz(h * NG * 4 + v_group, Row::kPars, vt);
-    }
-#pragma unroll
-    for (int i = 0; i < KV + VV; ++i)  // (the other group's warp stores the same)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(places + i * vector), "r"(at[4 * i]),
-                   "r"(at[4 * i + 1]), "r"(at[4 * i + 2]), "r"(at[4 * i + 3])
-                   : "memory");
-  }
-  // first dim of this lane's w-th word of V codes
-  auto v_dim = [&](int w) { return kRawV ? (w / VL) * GS + (gq * VL + w % VL) * 8 : gq * (HD / 8) + w * 8; };
+  for (int i = 0; i < NP / 2; ++i)
+    c_at[i] = (lane & 15) * R + q4_swz(h * (HD / 2) + (2 * i + (lane >> 4)) * 16, Row::kCodes, lane);
+  // K's parameters of token gq, and the piece with the head's V parameters of token `lane`
+  const uint32_t kp_at = gq * R + Row::kCodes + q4_swz(h * NG * 4, Row::kPars, gq);
+  const uint32_t vp_at = kChunk + lane * R + Row::kCodes + q4_swz(h * NG * 4 & ~15, Row::kPars, lane);
+  // The piece's half words, rows of the transposed matrix: those of this head from
+  // 2 (h NG mod 4) on, s and c of each group.  s of group g is with lanes s_lane + 8 g.
+  const int s_row = h * NG % 4 * 2, s_lane = s_row * 4 + tq;
+  const uint32_t s_mask = gq >= s_row && gq < s_row + 2 * NG && gq % 2 == 0 ? 0xFFFFFFFFu : 0u;
   const uint32_t smem0 = smem_u32(smem);
   // the barriers of the table in the kernel below
   auto full = [&](int s) { return smem0 + p.k.off_bar + 8 * s; };
@@ -510,16 +471,14 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
   auto handed = [&] { return smem0 + p.k.off_bar + 8 * (2 * kMaxStages + h); };
   auto taken = [&] { return smem0 + p.k.off_bar + 8 * (2 * kMaxStages + 8 + h); };
   auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, smem0 + p.k.off_abort, p.k.err); };
-  [[maybe_unused]] const uint32_t sixteen = keep_reg(kSixteen);
-  [[maybe_unused]] const uint32_t par_half = (gq & 1) ? 0x7632 : 0x5410;  // c or s of two words
 
   uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
   uint32_t qm = 0u;    // 2^-10 (16 sum q, sum q) over the dims of group tq
   float o[MB][4];
-  // Sums over the tokens: of p s and p c (row gq < 4: group gq / 2's s or, odd,
-  // c; only where V's codes are raw), and of p (the other rows).
-  float om[2] = {0.f, 0.f};
-  [[maybe_unused]] int s_bits = 0;  // exponent bits of the largest s seen: E = max(s_bits - 21, -15); 0: none above 0 yet
+  // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
+  // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
+  float om[4] = {0.f, 0.f, 0.f, 0.f};
+  int s_bits = 0;  // exponent bits of the largest s seen: E = max(s_bits - 21, -15); 0: none above 0 yet
   float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone)
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
@@ -537,36 +496,33 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
       if (flags & kEnd) break;
       if (flags & kFirst) {
         const uint32_t qrow = st + 2 * kChunk + (h * G + gq) * HD * 2;
-        uint32_t qw[NG][KW * 4];  // bf16 pairs
+        uint32_t qw[NP][4];  // bf16 pairs: eight dims of each piece
         float mx = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+        for (int i = 0; i < NP; ++i) {
+          qw[i][0] = qw[i][1] = qw[i][2] = qw[i][3] = 0u;
+          if (gq < G) lds128(qw[i], qrow + (i * 32 + tq * 8) * 2);
 #pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            if (gq < G) lds128(w, qrow + (g * GS + tq * (GS / 4) + i * 8) * 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              qw[g][4 * i + e] = w[e];
-              const float2 v = bf16x2_to_float2(w[e]);
-              mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = bf16x2_to_float2(qw[i][e]);
+            mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
           }
+        }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // 2^-E of the largest magnitude's exponent E, and 2^E
         const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
         const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
-        float sum[NG];
+        qm = 0u;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          sum[g] = 0.f;
+          float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < KW; ++i) {
+          for (int i = g * PG; i < (g + 1) * PG; ++i) {
             float q[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 v = bf16x2_to_float2(qw[g][4 * i + e]);
+              const float2 v = bf16x2_to_float2(qw[i][e]);
               q[2 * e] = v.x * down * 256.f;
               q[2 * e + 1] = v.y * down * 256.f;
             }
@@ -574,24 +530,18 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               q[e] = __half2float(__float2half_rn(q[e]));
-              sum[g] += q[e];
+              sum += q[e];
             }
-            const int k = 2 * (g * KW + i);
-            qf[k][0] = pack_f16x2(q[0], q[4]);
-            qf[k][1] = pack_f16x2(q[1], q[5]);
-            qf[k + 1][0] = pack_f16x2(q[2] * 16.f, q[6] * 16.f);
-            qf[k + 1][1] = pack_f16x2(q[3] * 16.f, q[7] * 16.f);
+            qf[2 * i][0] = pack_f16x2(q[0], q[4]);
+            qf[2 * i][1] = pack_f16x2(q[1], q[5]);
+            qf[2 * i + 1][0] = pack_f16x2(q[2] * 16.f, q[6] * 16.f);
+            qf[2 * i + 1][1] = pack_f16x2(q[3] * 16.f, q[7] * 16.f);
           }
-          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
+          if (tq == g) qm = pack_f16x2(r * 16.f, r);
         }
-        qm = 0u;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          if (tq == g) {
-            const float r = __half2float(__float2half_rn(sum[g] * 0x1p-18f));
-            qm = pack_f16x2(r * 16.f, r);
-          }
         mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
         mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
 #pragma unroll
@@ -600,7 +550,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
           for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         m[0] = m[1] = 0.f;
         limit = -INFINITY;
-        om[0] = om[1] = 0.f;
+        om[0] = om[1] = om[2] = om[3] = 0.f;
         s_bits = 0;
       }
       if (flags & kNew) {
@@ -613,44 +563,35 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
 
     // S^T = K Q^T of both halves
     float t[2][4];
-    uint32_t k_at[4 * KV];  // k_codes[NG], k_pars
-#pragma unroll
-    for (int i = 0; i < KV; ++i) lds_words<4>(k_at + 4 * i, places + i * vector);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      uint32_t kw[2][NG][KW], par[2][NG];
+      const uint32_t half = st + hf * kHalf * R;
+      uint32_t par[2][NG], pm[2];  // parameters of tokens gq, gq + 8; of their group tq
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t row = st + (hf * kHalf + u * 8) * R;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) lds_words<KW>(kw[u][g], row + k_at[g]);
-        lds_words<NG>(par[u], row + k_at[NG]);
-      }
-      uint32_t pm[2];  // the parameters of group tq (of any where there is none: its queries' sum is 0)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        pm[u] = par[u][0];
+        lds_words<NG>(par[u], half + u * 8 * R + kp_at);
+        pm[u] = par[u][0];  // (any where there is no group tq: its queries' sum is 0)
         if constexpr (NG == 2) pm[u] = (tq & 1) ? par[u][1] : par[u][0];
         if constexpr (NG == 4) pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
       }
-      float sc[4];
+      float sc[4], d[4];
       mma_f16_k8(sc, pm[0], pm[1], qm);
+      uint32_t w[4];  // of two pieces: the words of tokens gq and gq + 8
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const uint32_t w0 = kw[0][g][i], w1 = kw[1][g][i];
-          const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
-          const int k = 2 * (g * KW + i);
-          mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), qf[k][0], qf[k][1]);
-          mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), qf[k + 1][0], qf[k + 1][1]);
+      for (int i = 0; i < NP; ++i) {
+        if (i % 2 == 0) ldsm4(w, half + c_at[i / 2]);
+        const uint32_t w0 = i % 2 == 0 ? w[0] : w[2], w1 = i % 2 == 0 ? w[1] : w[3];
+        const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
+        if (i % PG == 0) d[0] = d[1] = d[2] = d[3] = 0.f;
+        mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), qf[2 * i][0], qf[2 * i][1]);
+        mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), qf[2 * i + 1][0], qf[2 * i + 1][1]);
+        if (i % PG == PG - 1) {
+          const float s0 = f16_lo(par[0][i / PG]), s1 = f16_lo(par[1][i / PG]);
+          sc[0] = fmaf(d[0], s0, sc[0]);
+          sc[1] = fmaf(d[1], s0, sc[1]);
+          sc[2] = fmaf(d[2], s1, sc[2]);
+          sc[3] = fmaf(d[3], s1, sc[3]);
         }
-        const float s0 = f16_lo(par[0][g]), s1 = f16_lo(par[1][g]);
-        sc[0] = fmaf(d[0], s0, sc[0]);
-        sc[1] = fmaf(d[1], s0, sc[1]);
-        sc[2] = fmaf(d[2], s1, sc[2]);
-        sc[3] = fmaf(d[3], s1, sc[3]);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[e], mult[e & 1], -m[e & 1]);
@@ -662,8 +603,8 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int n = (flags >> (8 * hf)) & 255;
-        if (kt >= n) t[hf][0] = t[hf][1] = -INFINITY;
-        if (kt + 8 >= n) t[hf][2] = t[hf][3] = -INFINITY;
+        if (gq >= n) t[hf][0] = t[hf][1] = -INFINITY;
+        if (gq + 8 >= n) t[hf][2] = t[hf][3] = -INFINITY;
       }
     }
     float d0 = fmaxf(fmaxf(t[0][0], t[0][2]), fmaxf(t[1][0], t[1][2]));
@@ -683,6 +624,8 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
         const float a0 = ex2_approx(-d0), a1 = ex2_approx(-d1);
         om[0] *= a0;
         om[1] *= a1;
+        om[2] *= a0;
+        om[3] *= a1;
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           o[j][0] *= a0;
@@ -709,130 +652,54 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
       const float p2 = ex2_approx(t[hf][2]), p3 = ex2_approx(t[hf][3]);
       pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
       pb[hf][1] = movm_trans(pack_f16x2(p2, p3));
-      if constexpr (!kRawV) mma_f16_top(om, kOnes, kOnes, pb[hf][0], pb[hf][1]);
     }
 
     // O^T += V^T P^T
-    uint32_t v_at[4 * VV];  // v_codes[NL][2], v_pars[2]
+    uint32_t vm[4];  // row gq of the parameter piece: tokens 2 tq, 2 tq + 1 (+ 8, + 16, + 24)
+    ldsm4_trans(vm, st + vp_at);
+    if (flags & kRagged) {
+      // rows past the context meet probability 0 and must be finite
 #pragma unroll
-    for (int i = 0; i < VV; ++i) lds_words<4>(v_at + 4 * i, places + (KV + i) * vector);
-    if constexpr (kRawV) {
-      uint32_t vs[2][NG][2], vm[2][2];  // s of two tokens; the rows of the second term
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t par[4][NG];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          lds_words<NG>(par[u], st + (hf * kHalf + (u >> 1) * 8) * R + v_at[2 * NL + (u & 1)]);
-          if (flags & kRagged) {
-            // rows past the context meet probability 0 and must be finite
-            const int n = (flags >> (8 * hf)) & 255;
-            if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n)
-#pragma unroll
-              for (int g = 0; g < NG; ++g) par[u][g] = 0u;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g) vs[hf][g][u] = __byte_perm(par[2 * u][g], par[2 * u + 1][g], 0x5410);
-          uint32_t w0 = par[2 * u][0], w1 = par[2 * u + 1][0];
-          if constexpr (NG == 2) {
-            w0 = (gq & 2) ? par[2 * u][1] : w0;
-            w1 = (gq & 2) ? par[2 * u + 1][1] : w1;
-          }
-          vm[hf][u] = gq < 4 ? __byte_perm(w0, w1, par_half) : kOnes;
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int n = static_cast<int>((flags >> (u / 2 * 8)) & 255) - (u & 1) * 8;
+        vm[u] &= (2 * tq < n ? 0xFFFFu : 0u) | (2 * tq + 1 < n ? 0xFFFF0000u : 0u);
       }
-      // a larger s than the scale was made for: scale anew (s is never negative,
-      // so its bits compare as integers)
-      uint32_t top = 0u;
+    }
+    // A larger s than the scale was made for: scale anew (s is never negative, so
+    // its bits compare as integers).
+    const uint32_t top = __vmaxu2(__vmaxu2(vm[0], vm[1]), __vmaxu2(vm[2], vm[3])) & s_mask;
+    const uint32_t most = (s_bits ? ((s_bits + 1) << 10) - 1 : 0u) * 0x00010001u;  // the largest the scale is made for
+    if (__any_sync(0xffffffffu, __vmaxu2(top, most) != most)) {
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+      const int now = max(static_cast<int>(bits >> 10), 1);
+      if (s_bits != 0) {
+        const float a = __uint_as_float(static_cast<uint32_t>(127 + max(s_bits, 6) - max(now, 6)) << 23);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) top = __vmaxu2(top, vs[hf][g][u]);
-      const uint32_t most = s_bits ? ((s_bits + 1) << 10) - 1 : 0u;  // the largest s that the scale is made for
-      if (__any_sync(0xffffffffu, __vmaxu2(top, most * 0x00010001u) != most * 0x00010001u)) {
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-        const int now = max(static_cast<int>(bits >> 10), 1);
-        if (s_bits != 0) {
-          const float a = __uint_as_float(static_cast<uint32_t>(127 + max(s_bits, 6) - max(now, 6)) << 23);
-#pragma unroll
-          for (int j = 0; j < MB; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] *= a;
-        }
-        s_bits = now;
+          for (int i = 0; i < 4; ++i) o[j][i] *= a;
       }
-      // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
-      const uint32_t s_scale = static_cast<uint32_t>(36 - max(s_bits, 6)) * (0x00010001u << 10);
+      s_bits = now;
+    }
+    // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
+    const uint32_t s_scale = static_cast<uint32_t>(36 - max(s_bits, 6)) * (0x00010001u << 10);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        mma_f16_top(om, vm[hf][0], vm[hf][1], pb[hf][0], pb[hf][1]);
-        uint32_t vw[4][VW];
+    for (int hf = 0; hf < 2; ++hf) {
+      mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
+      uint32_t x[4];  // of two pieces: half word gq of tokens 2 tq, 2 tq + 1 and of those 8 on
+      uint32_t b0, b1;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < NL; ++i)
-            lds_words<VL>(&vw[u][i * VL], st + (hf * kHalf + (u >> 1) * 8) * R + v_at[2 * i + (u & 1)]);
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          const uint32_t b0 = mul_f16x2(pb[hf][0], mul_f16x2(vs[hf][w / VL][0], s_scale));
-          const uint32_t b1 = mul_f16x2(pb[hf][1], mul_f16x2(vs[hf][w / VL][1], s_scale));
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t xx[2], yy[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              xx[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x7632 : 0x5410);
-              yy[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x6723 : 0x4501);
-            }
-            mma_f16(o[4 * w + 2 * q], raw_hi(xx[0]), raw_hi(yy[0]), raw_hi(xx[1]), raw_hi(yy[1]), b0, b1);
-            mma_f16(o[4 * w + 2 * q + 1], raw_lo(xx[0]), raw_lo(yy[0]), raw_lo(xx[1]), raw_lo(yy[1]), b0, b1);
-          }
+      for (int i = 0; i < NP; ++i) {
+        if (i % 2 == 0) ldsm4_trans(x, st + kChunk + hf * kHalf * R + c_at[i / 2]);
+        if (i % PG == 0) {  // p s of the group
+          const int from = s_lane + i / PG * 8;
+          b0 = mul_f16x2(pb[hf][0], mul_f16x2(__shfl_sync(0xffffffffu, vm[2 * hf], from), s_scale));
+          b1 = mul_f16x2(pb[hf][1], mul_f16x2(__shfl_sync(0xffffffffu, vm[2 * hf + 1], from), s_scale));
         }
-      }
-    } else {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t vw[4][VW], vpar[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t row = st + (hf * kHalf + (u >> 1) * 8) * R;
-          lds_words<VW>(vw[u], row + v_at[u & 1]);
-          vpar[u] = lds32(row + v_at[2 * NL + (u & 1)]);
-        }
-        if (flags & kRagged) {
-          // rows past the context meet probability 0 and must be finite
-          const int n = (flags >> (8 * hf)) & 255;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (((u & 1) ? vt1 : vt0) + (u >> 1) * 8 >= n) vpar[u] = 0u;
-        }
-        uint32_t vs[2], vc[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          vs[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x5410);
-          vc[u] = __byte_perm(vpar[2 * u], vpar[2 * u + 1], 0x7632);
-        }
-#pragma unroll
-        for (int w = 0; w < VW; ++w)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t xx[2], yy[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              xx[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x7632 : 0x5410);
-              yy[u] = __byte_perm(vw[2 * u][w], vw[2 * u + 1][w], q ? 0x6723 : 0x4501);
-            }
-            mma_f16(o[4 * w + 2 * q], q4_pair(xx[0], sixteen, vs[0], vc[0]), q4_pair(yy[0], sixteen, vs[0], vc[0]),
-                    q4_pair(xx[1], sixteen, vs[1], vc[1]), q4_pair(yy[1], sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
-            mma_f16(o[4 * w + 2 * q + 1], q4_pair(xx[0] << 4, sixteen, vs[0], vc[0]),
-                    q4_pair(yy[0] << 4, sixteen, vs[0], vc[0]), q4_pair(xx[1] << 4, sixteen, vs[1], vc[1]),
-                    q4_pair(yy[1] << 4, sixteen, vs[1], vc[1]), pb[hf][0], pb[hf][1]);
-          }
+        const uint32_t x0 = i % 2 == 0 ? x[0] : x[2], x1 = i % 2 == 0 ? x[1] : x[3];
+        const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
+        mma_f16(o[2 * i], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
+        mma_f16(o[2 * i + 1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
       }
     }
     uint32_t b = 0, share = 0;
@@ -844,23 +711,20 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
     if (lane == 0) bar_arrive(empty(s));
 
     if (flags & (kLast | kYield)) {
-      float l[2];  // the softmax sums
-      l[0] = __shfl_sync(0xffffffffu, om[0], 16 + tq);
-      l[1] = __shfl_sync(0xffffffffu, om[1], 16 + tq);
-      if constexpr (kRawV) {
-        // the powers of two undone, the second term added
-        const float hi = __uint_as_float(static_cast<uint32_t>(127 + 18 - 21 + max(s_bits, 6)) << 23), lo = hi * 16.f;
+      float l[2] = {om[2], om[3]};  // the softmax sums
+      // the powers of two undone, the second term added
+      const float hi = __uint_as_float(static_cast<uint32_t>(127 + 18 - 21 + max(s_bits, 6)) << 23), lo = hi * 16.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float add[2];
+      for (int g = 0; g < NG; ++g) {
+        float add[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], 8 * g + tq), __shfl_sync(0xffffffffu, om[e], 8 * g + 4 + tq));
+        for (int e = 0; e < 2; ++e)
+          add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
+                        __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
 #pragma unroll
-          for (int j = g * 4 * VL; j < (g + 1) * 4 * VL; ++j)
+        for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
-        }
+          for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
       }
       if (flags & kYield) {
         // hand this group's part over: once the previous one has been taken
@@ -873,7 +737,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
             float* dst = reinterpret_cast<float*>(smem + p.off_hand) + (h * G + g) * (HD + 4);
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
-              *reinterpret_cast<float4*>(dst + v_dim(j / 4) + (j & 2) * 2) =
+              *reinterpret_cast<float4*>(dst + j * 16 + gq * 4) =
                   make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
             if (gq == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(m[e], l[e]);
           }
@@ -899,7 +763,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
             l[e] = l[e] * wa + ml.y * wb;
 #pragma unroll
             for (int j = 0; j < MB; j += 2) {
-              const float4 v = *reinterpret_cast<const float4*>(src + v_dim(j / 4) + (j & 2) * 2);
+              const float4 v = *reinterpret_cast<const float4*>(src + j * 16 + gq * 4);
               o[j][e] = o[j][e] * wa + v.x * wb;
               o[j][2 + e] = o[j][2 + e] * wa + v.y * wb;
               o[j + 1][e] = o[j + 1][e] * wa + v.z * wb;
@@ -919,17 +783,16 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
           if (flags & kWhole) {
             char* dst = p.k.out + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD * 2;
 #pragma unroll
-            for (int j = 0; j < MB; j += 4)
-              stg16(dst + v_dim(j / 4) * 2, make_uint4(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
-                                                       pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv),
-                                                       pack_bf16x2(o[j + 2][e] * inv, o[j + 2][2 + e] * inv),
-                                                       pack_bf16x2(o[j + 3][e] * inv, o[j + 3][2 + e] * inv)));
+            for (int j = 0; j < MB; j += 2)
+              *reinterpret_cast<uint2*>(dst + (j * 16 + gq * 4) * 2) =
+                  make_uint2(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
+                             pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv));
           } else {
             const int64_t slot = static_cast<int64_t>(share) + b;
             float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD;
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
-              *reinterpret_cast<float4*>(dst + v_dim(j / 4) + (j & 2) * 2) =
+              *reinterpret_cast<float4*>(dst + j * 16 + gq * 4) =
                   make_float4(o[j][e] * inv, o[j][2 + e] * inv, o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
             if (gq == 0) p.k.lse_part[slot * p.k.Hq + hq] = l[e] > 0.f ? m[e] + log2f(l[e]) : -INFINITY;
           }
@@ -1221,14 +1084,12 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // statistics, then the scaled queries
   pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4
                          : static_cast<size_t>(d.num_q_heads) * (d.head_dim + 4) * 4);  // or the handed-over part
-  const uint32_t off_places = place(simt ? 0 : static_cast<size_t>(4) * d.num_kv_heads * 512);
   // The ring takes what is left of a CTA's share of the SM's shared memory with
   // 16 consumer warps on an SM: four or more chunks.
   const size_t fixed = align_up(off, 128), stage = q4_stage_bytes(d, pl);
   const size_t share = static_cast<size_t>(di.max_smem_optin) * std::min(pl.nw, 16) / 16 - 1024;
   pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, share > fixed ? (share - fixed) / stage : 0)));
   const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
-  pl.off_places = off_places + ring;
   for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
     *o += ring;
   pl.smem_bytes = ring + fixed;
@@ -1263,7 +1124,6 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   p.by_request = pl.by_request;
   p.off_q = pl.off_ml + pl.nw * 16 * 4;
   p.off_hand = pl.off_ml;
-  p.off_places = pl.off_places;
   void* args[] = {&p};
   return launch_decode_kernels(f.main, f.merge, pl, p.k, args, s);
 }
