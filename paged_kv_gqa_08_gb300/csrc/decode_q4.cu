@@ -61,6 +61,13 @@ struct Ring {
       phase ^= 1;
     }
   }
+  PA_DEVINL void next2(int stages) {
+    s += 2;
+    if (s >= stages) {
+      s -= stages;
+      phase ^= 1;
+    }
+  }
 };
 
 // The new token's K and V of kv-head h, quantised by the warp: into row t of the
@@ -313,7 +320,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 //       the second term is one product of the transposed parameter piece, whose
 //       rows are its groups' s and c, with p.  The product's other eight rows
 //       are ones: the softmax sum.
-// 16 tokens of a head take 201 instructions with groups of 128, 111 of them on
+// 16 tokens of a head take 197 instructions with groups of 128, 109 of them on
 // the integer pipe (two cycles each); 309 with K and V decoded to float16 in
 // registers, 228 with raw codes loaded as words and paired by byte permutes.
 //
@@ -359,7 +366,8 @@ PA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 PA_DEVINL float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w & 0xFFFFu))); }
 
-constexpr uint32_t kOnes = 0x3C003C00u;
+constexpr uint32_t kOnes = 0x3C003C00u;      // 1 twice
+constexpr uint32_t kExponent = 0x04000400u;  // the lowest exponent bit of a float16, twice
 
 // u * 2^-18 of the codes in bits 6-9, u * 2^-22 of those in bits 2-5.
 PA_DEVINL uint32_t raw_hi(uint32_t w) { return w & 0x03C003C0u; }
@@ -478,14 +486,16 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
   // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
   // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
   float om[4] = {0.f, 0.f, 0.f, 0.f};
-  int s_bits = 0;  // exponent bits of the largest s seen: E = max(s_bits - 21, -15); 0: none above 0 yet
+  // The largest s with the exponent of the largest seen, twice (0: none above 0
+  // yet).  With that exponent's bits x, E = max(x - 21, -15).
+  uint32_t s_most = 0u;
   float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone)
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
   uint32_t hand_phase = 0;     // parity of the handovers so far
   Ring ring;
   if (group) ring.next(p.stages);  // group g takes stages g, g + 2, ... of the ring
-  for (;; ring.next(p.stages), ring.next(p.stages)) {
+  for (;; ring.next2(p.stages)) {
     const int s = ring.s;
     if (!wait(full(s), ring.phase)) break;
     const uint32_t md = smem0 + p.k.off_meta + s * 16;  // {request, tokens and flags, share, slot}
@@ -551,7 +561,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
         m[0] = m[1] = 0.f;
         limit = -INFINITY;
         om[0] = om[1] = om[2] = om[3] = 0.f;
-        s_bits = 0;
+        s_most = 0u;
       }
       if (flags & kNew) {
         unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
@@ -668,21 +678,19 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
     // A larger s than the scale was made for: scale anew (s is never negative, so
     // its bits compare as integers).
     const uint32_t top = __vmaxu2(__vmaxu2(vm[0], vm[1]), __vmaxu2(vm[2], vm[3])) & s_mask;
-    const uint32_t most = (s_bits ? ((s_bits + 1) << 10) - 1 : 0u) * 0x00010001u;  // the largest the scale is made for
-    if (__any_sync(0xffffffffu, __vmaxu2(top, most) != most)) {
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-      const int now = max(static_cast<int>(bits >> 10), 1);
-      if (s_bits != 0) {
-        const float a = __uint_as_float(static_cast<uint32_t>(127 + max(s_bits, 6) - max(now, 6)) << 23);
+    if (__any_sync(0xffffffffu, __vmaxu2(top, s_most) != s_most)) {
+      const uint32_t bits = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 10, 1u);
+      if (s_most != 0u) {
+        const float a = __uint_as_float((127u + max(s_most >> 26, 6u) - max(bits, 6u)) << 23);
 #pragma unroll
         for (int j = 0; j < MB; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][i] *= a;
       }
-      s_bits = now;
+      s_most = (((bits + 1) << 10) - 1) * 0x00010001u;
     }
     // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
-    const uint32_t s_scale = static_cast<uint32_t>(36 - max(s_bits, 6)) * (0x00010001u << 10);
+    const uint32_t s_scale = 36u * kExponent - max(s_most & 0x7C007C00u, 6u * kExponent);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
@@ -713,7 +721,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
     if (flags & (kLast | kYield)) {
       float l[2] = {om[2], om[3]};  // the softmax sums
       // the powers of two undone, the second term added
-      const float hi = __uint_as_float(static_cast<uint32_t>(127 + 18 - 21 + max(s_bits, 6)) << 23), lo = hi * 16.f;
+      const float hi = __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23), lo = hi * 16.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float add[2];
