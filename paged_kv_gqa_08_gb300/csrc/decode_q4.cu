@@ -16,7 +16,12 @@ namespace {
 constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
-constexpr int kWholeTokens = 256;  // requests of at most this many tokens are not split where a CTA each fits
+constexpr int kMaxCluster = 8;  // CTAs of a cluster that shares a request, at most
+// Tokens of a request that a CTA alone takes, or (of 128 dims; of 64 twice as
+// many) each of a cluster's CTAs, where all requests' CTAs fit at once: more, and
+// it pays to split the batch's keys evenly over the GPU and to merge partial
+// results by another kernel.
+constexpr int kWholeTokens = 256, kClusterTokens = 384;
 
 // A chunk in the ring, as the producer describes it to the consumers: its
 // request; the tokens of its halves (n0 | n1 << 8, 0 for a half whose page is
@@ -36,8 +41,8 @@ struct Q4Params {
   int32_t stages;       // ring depth
   int32_t stage_bytes;  // K rows, V rows, queries
   int32_t groups;       // consumer groups: 2 (tensor cores) or 1
-  int32_t by_request;   // 1: CTA b takes request b, whole (nothing to merge)
-  uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, with its statistics
+  int32_t cluster;      // CTAs of each request; 0: the CTAs share the batch's chunks evenly
+  uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, or a CTA to its cluster
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
   uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
@@ -103,6 +108,10 @@ PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned cha
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
 }
+
+// log2-sum-exp of a partial result.  One without tokens (all on bad pages) has no
+// weight in a merge; one that is not a number has all of it.
+PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; }
 
 // ---------------------------------------------------------------------------
 // CUDA-core consumer: GP = the group's q-heads rounded up to a power of two.
@@ -283,7 +292,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
             float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + lane * EL;
 #pragma unroll
             for (int e = 0; e < EL; ++e) dst[e] = o[g][e] * inv;
-            if (lane == 0) p.k.lse_part[slot * p.k.Hq + hq] = lg > 0.f ? mg + log2f(lg) : -INFINITY;
+            if (lane == 0) p.k.lse_part[slot * p.k.Hq + hq] = partial_lse(mg, lg);
           }
         }
       }
@@ -796,13 +805,19 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
                   make_uint2(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
                              pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv));
           } else {
-            const int64_t slot = static_cast<int64_t>(share) + b;
-            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD;
+            // a partial result: for the merge kernel, or (generic addresses) for the cluster
+            const int64_t part = (static_cast<int64_t>(share) + b) * p.k.Hq + hq;
+            float* dst = p.k.o_part + part * HD;
+            float* lse = p.k.lse_part + part;
+            if (p.cluster) {
+              dst = reinterpret_cast<float*>(smem + p.off_hand) + hq * (HD + 4);
+              lse = dst + HD;
+            }
 #pragma unroll
             for (int j = 0; j < MB; j += 2)
               *reinterpret_cast<float4*>(dst + j * 16 + gq * 4) =
                   make_float4(o[j][e] * inv, o[j][2 + e] * inv, o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
-            if (gq == 0) p.k.lse_part[slot * p.k.Hq + hq] = l[e] > 0.f ? m[e] + log2f(l[e]) : -INFINITY;
+            if (gq == 0) *lse = partial_lse(m[e], l[e]);
           }
         }
       }
@@ -872,10 +887,19 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
     NC = cs[k.B];
   }
   const int c = blockIdx.x;
-  const int x0 = p.by_request ? cs[c] : static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
-  const int x1 = p.by_request ? cs[c + 1] : static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
+  // its share: of its cluster's request, or of the batch
+  int b, x0, x1;
+  if (p.cluster) {
+    b = c / p.cluster;
+    const int part = c - b * p.cluster, count = cs[b + 1] - cs[b];
+    x0 = cs[b] + part * count / p.cluster;
+    x1 = cs[b] + (part + 1) * count / p.cluster;
+  } else {
+    x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / k.n_ctas);
+    x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / k.n_ctas);
+    b = x0 < x1 ? first_request(cs, k.B, x0) : 0;
+  }
   const uint32_t rb = static_cast<uint32_t>(k.row_bytes), q_bytes = p.stage_bytes - 2 * k.chunk_bytes;
-  int b = p.by_request ? c : x0 < x1 ? first_request(cs, k.B, x0) : 0;
   int issued = 0;
   Ring ring;
   bool aborted = false;
@@ -911,7 +935,7 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
       const int xa = max(x0, cb0), xb = min(x1, cb1);  // the request's chunks in this share
       flags = (x < xa + p.groups ? kFirst : 0u) | (x == xb - 1 ? kLast : 0u) |
               (p.groups == 2 && x == xb - 2 ? kYield : 0u) | (p.groups == 1 || xb - xa == 1 ? kSolo : 0u) |
-              (cb0 >= x0 && cb1 <= x1 ? kWhole : 0u) | (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) |
+              (cb0 >= x0 && cb1 <= x1 && p.cluster <= 1 ? kWhole : 0u) | (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) |
               (new_slot >= 0 ? kNew : 0u);
     }
     b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
@@ -971,6 +995,72 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
   }
 }
 
+// ---------------------------------------------------------------------------
+// The partial results of a cluster's request, which its CTAs left in their shared
+// memory (off_hand, with the log2-sum-exp behind the outputs; -infinity where a
+// CTA had no chunk): a warp takes a q-head and adds them in the order of the CTAs.
+// ---------------------------------------------------------------------------
+PA_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+PA_DEVINL uint32_t peer_addr(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+template <int HD>
+PA_DEVINL void cluster_merge(const Q4Params& p, unsigned char* smem, int warp, int lane) {
+  constexpr int EL = HD / 32;
+  cluster_sync();  // every part is in its place
+  const int b = blockIdx.x / p.cluster, rank = blockIdx.x - b * p.cluster;
+  const int32_t* cs = reinterpret_cast<const int32_t*>(smem + p.k.off_cs);
+  if (cs[b] < cs[b + 1]) {  // (a padding row keeps its output)
+    const int nw = blockDim.x / 32;
+    for (int hq = rank * nw + warp; hq < p.k.Hq; hq += p.cluster * nw) {
+      const uint32_t at = smem_u32(smem) + p.off_hand + hq * (HD + 4) * 4;
+      float lse = -INFINITY;  // lane r: CTA r's
+      if (lane < p.cluster)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lse) : "r"(peer_addr(at + HD * 4, lane)));
+      float v[kMaxCluster][EL];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= p.cluster) break;
+        const uint32_t src = peer_addr(at + lane * EL * 4, r);
+        if constexpr (EL == 4)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[r][0]), "=f"(v[r][1]), "=f"(v[r][2]), "=f"(v[r][3])
+                       : "r"(src));
+        else
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[r][0]), "=f"(v[r][1]) : "r"(src));
+      }
+      float top = lse;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float w = lse == -INFINITY ? 0.f : ex2_approx(lse - top);
+      float sum = w;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = __shfl_sync(0xffffffffu, sum, 0);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      float acc[EL] = {};
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= p.cluster) break;
+        const float wr = __shfl_sync(0xffffffffu, w, r);
+        if (wr != 0.f)  // (a CTA without a chunk left nothing)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) acc[e] = fmaf(wr, v[r][e], acc[e]);
+      }
+      char* dst = p.k.out + ((static_cast<int64_t>(b) * p.k.Hq + hq) * HD + lane * EL) * 2;
+#pragma unroll
+      for (int e = 0; e < EL; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e * 2) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+  }
+  cluster_sync();  // no CTA leaves while its part is read
+}
+
 // bf16: two groups of one consumer warp per kv-head, which take the chunks in
 // turn from one ring, and the producer; fp32: one group.
 // V: of fp32, the group's q-heads rounded up to a power of two; of bf16, the
@@ -989,6 +1079,9 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) =
   uint64_t* taken = handed + 8;           // [8] it has been added
   int4* meta = reinterpret_cast<int4*>(smem + k.off_meta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + k.off_abort);
+  if (sizeof(T) == 2 && p.cluster > 1)
+    for (int hq = threadIdx.x; hq < k.Hq; hq += blockDim.x)
+      *reinterpret_cast<float*>(smem + p.off_hand + (hq * (HD + 4) + HD) * 4) = -INFINITY;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -1006,13 +1099,15 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) =
 
   if (warp == NW * p.groups) {
     produce(p, smem, full, empty, meta, abort_flag, lane);
-    return;
-  }
-  if constexpr (sizeof(T) == 2) {
+  } else if constexpr (sizeof(T) == 2) {
     const int group = warp >= NW;
     mma_consumer<HD, V, HKV>(p, smem, warp - group * NW, group);
   } else {
     simt_consumer<T, HD, V>(p, smem, full, empty, meta, abort_flag);
+  }
+  if constexpr (sizeof(T) == 2) {
+    __syncwarp();
+    if (p.cluster > 1) cluster_merge<HD>(p, smem, warp, lane);
   }
 }
 
@@ -1108,12 +1203,30 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
   int64_t n = static_cast<int64_t>(occ) * di.sm_count;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
-  // Short requests that fit the GPU at once: a CTA each, no partial results
-  // and no merge kernel.
-  if (n >= batch && batch <= kInlinePlanMax && max_ctx <= kWholeTokens) pl.by_request = true;
+  // Short requests that fit the GPU at once: a CTA or a cluster each, and no
+  // merge kernel, whose 4 to 7 us are most of such a call.  With 32 q-heads over
+  // 8, groups of 64 and the clusters that fit, against the even split: 8 requests
+  // of 300-1000 tokens 12.3 us (15.5), 37 of them 18.5 (20.9), 16 of 2000 18.9
+  // (22.7); where a CTA's part is longer the even split wins: 8 requests of 4000
+  // tokens 22.5 (20.7), 64 of 300-2000 34.1 (30.0).  37 of 100-2900 with 24
+  // q-heads over 4 of 64 dims 17.7 (22.3).  One request alone is faster
+  // over all SMs (1000 tokens: 10.9 us, by a cluster 12.1).
+  if (n >= batch && batch <= kInlinePlanMax && max_ctx <= kWholeTokens) pl.cluster = 1;
+  if (!simt && batch > 1 && batch <= kInlinePlanMax && pl.cluster == 0) {
+    int c = static_cast<int>(std::min<int64_t>({kMaxCluster, n / batch, (max_ctx + kTok - 1) / kTok}));
+    for (; c > 1 && static_cast<int64_t>(max_ctx) * d.head_dim <= static_cast<int64_t>(c) * kClusterTokens * 128; --c) {
+      int fit = 0;
+      e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &fit, c);
+      if (e != cudaSuccess) return e;
+      if (fit < batch) continue;
+      pl.cluster = c;
+      break;
+    }
+  }
   n = std::min<int64_t>(n, std::max<int64_t>(1, chunks_upper));
-  pl.n_ctas = pl.by_request ? batch : static_cast<int>(std::max<int64_t>(1, n));
-  decode_workspace_layout(d, batch, &pl);
+  pl.n_ctas = static_cast<int>(std::max<int64_t>(1, n));
+  decode_workspace_layout(d, batch, &pl);  // (the same for both forms: it grows with the bounds)
+  if (pl.cluster) pl.n_ctas = batch * pl.cluster;
   *out = pl;
   return cudaSuccess;
 }
@@ -1129,7 +1242,7 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   p.pars = p.k.row_bytes - p.codes;
   while ((1 << p.log2gs) < gs) ++p.log2gs;
   p.groups = q4_groups(d);
-  p.by_request = pl.by_request;
+  p.cluster = pl.cluster;
   p.off_q = pl.off_ml + pl.nw * 16 * 4;
   p.off_hand = pl.off_ml;
   void* args[] = {&p};

@@ -303,24 +303,43 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// CTAs of one kernel instance that fit on an SM, cached per (device, kernel, smem).
+inline cudaLaunchConfig_t cluster_config(int ctas, int threads, size_t smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  return cfg;
+}
+inline cudaLaunchAttribute cluster_attribute(int cluster) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  return attr;
+}
+
+// CTAs of one kernel instance that fit on an SM, or (cluster > 1) clusters of
+// that many CTAs that fit on the GPU; cached per (device, kernel, smem, cluster).
 struct OccKey {
   int device;
   const void* fn;
   int threads;
   size_t smem;
+  int cluster;
 };
+constexpr int kOccKeys = 256;
 std::mutex g_occ_mu;
-OccKey g_occ_keys[64];
-int g_occ_vals[64];
+OccKey g_occ_keys[kOccKeys];
+int g_occ_vals[kOccKeys];
 int g_occ_n = 0;
 
-inline cudaError_t ctas_per_sm(const DeviceInfo& di, const void* fn, int threads, size_t smem, int* out) {
+inline cudaError_t ctas_per_sm(const DeviceInfo& di, const void* fn, int threads, size_t smem, int* out,
+                               int cluster = 0) {
   {
     std::lock_guard<std::mutex> lk(g_occ_mu);
     for (int i = 0; i < g_occ_n; ++i) {
       const OccKey& k = g_occ_keys[i];
-      if (k.device == di.device && k.fn == fn && k.threads == threads && k.smem == smem) {
+      if (k.device == di.device && k.fn == fn && k.threads == threads && k.smem == smem && k.cluster == cluster) {
         *out = g_occ_vals[i];
         return cudaSuccess;
       }
@@ -335,12 +354,21 @@ inline cudaError_t ctas_per_sm(const DeviceInfo& di, const void* fn, int threads
   e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem);
-  if (e != cudaSuccess) return e;
-  if (n < 1) return cudaErrorInvalidConfiguration;
+  if (cluster > 1) {
+    cudaLaunchConfig_t cfg = cluster_config(cluster, threads, smem);
+    cudaLaunchAttribute attr = cluster_attribute(cluster);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    if (e != cudaSuccess) return e;
+  } else {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+  }
   std::lock_guard<std::mutex> lk(g_occ_mu);
-  if (g_occ_n < 64) {
-    g_occ_keys[g_occ_n] = {di.device, fn, threads, smem};
+  if (g_occ_n < kOccKeys) {
+    g_occ_keys[g_occ_n] = {di.device, fn, threads, smem, cluster};
     g_occ_vals[g_occ_n] = n;
     ++g_occ_n;
   }
@@ -424,7 +452,14 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
   // The kernels after the first are launched to overlap their launch with the
   // kernel before them (each waits for it before reading its output).
   cudaError_t e;
-  if (p.inline_plan) {
+  if (pl.cluster > 1) {
+    cudaLaunchConfig_t cfg = cluster_config(pl.n_ctas, (pl.nw + 1) * 32, pl.smem_bytes);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = cluster_attribute(pl.cluster);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelExC(&cfg, main_fn, main_args);
+  } else if (p.inline_plan) {
     e = cudaLaunchKernel(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), main_args, pl.smem_bytes, s);
   } else {
     decode_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
@@ -433,7 +468,7 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
     e = launch_after_previous(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), pl.smem_bytes, s, main_args);
   }
   if (e != cudaSuccess) return e;
-  if (pl.n_ctas > 1 && !pl.by_request) {
+  if (pl.n_ctas > 1 && pl.cluster == 0) {
     // warps per (request, q-head): about one per 8 partials of a request when
     // the requests are equally long (CTAs per request / 8), at most 4
     const int per_req = pl.n_ctas / std::max(1, p.B);

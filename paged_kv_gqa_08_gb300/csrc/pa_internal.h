@@ -151,7 +151,7 @@ struct DecodePlan {
   int row_pitch = 0;     // shared-memory bytes per token row of a chunk
   int stages = 0;
   int n_ctas = 0;        // partitions of the key space
-  bool by_request = false;  // 4-bit caches: a partition is a request (no merge)
+  int cluster = 0;       // 4-bit caches: CTAs of each request, a cluster (0: CTAs share the batch's keys evenly)
   size_t smem_bytes = 0;
   // workspace layout (byte offsets)
   size_t ws_cs = 0, ws_cta_seq = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;

@@ -348,3 +348,83 @@ def test_prefill_attends_to_the_read_back(hd):
         ref = oracle.attend(q[s0: s0 + m].double().numpy(), K, V, np.arange(L - m, L), c.scale)[0]
         assert np.abs(got[s0: s0 + m] - ref).max() <= 1e-2 * np.abs(ref).max()
     assert pa.pa_read_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("batch", [2, 5, 18, 19, 20, 25, 30, 37, 50, 76, 77, 152, 153])
+def test_requests_by_clusters_of_every_size(batch):
+    """Short requests take a cluster of CTAs each while these fit the GPU (8 CTAs down to 1 as the batch grows): lengths
+    below and above a cluster's CTAs, padding rows, a bad length and a bad page."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(1, 300, batch)
+    lens[0], lens[-1] = 600, 33
+    if batch > 4:
+        lens[1:4] = 0, 1, 257
+    c = Case("bf16", 16, 8, 128, 64, 16, lens, seed=batch)
+    ref = c.reference()
+    c.check(c.decode(), ref)
+    c.check(c.decode(max_ctas=1), ref)          # the same by one CTA
+    assert pa.pa_read_device_errors(reset=True) == 0
+    if batch > 4:
+        c.ctx[4] = c.maxp * c.P + 1
+        want = c.decode(max_ctas=1)
+        got = c.decode()
+        assert (got[4] == 7.0).all() and (want[4] == 7.0).all()
+        keep = [i for i in range(batch) if i != 4]
+        c2 = got[keep].double().cpu().numpy()
+        live = lens[keep] > 0
+        assert np.abs(c2[live] - ref[keep][live]).max() <= 1e-2 * np.nanmax(np.abs(ref))
+        assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_LENGTH
+        c.ctx[4] = int(lens[4])
+    c.btd[0, :] = c.pages + 5                   # every page of a request: its output is zero
+    out = c.decode()
+    assert (out[0] == 0).all() and pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_PAGE
+    got = out.double().cpu().numpy()
+    live = np.arange(batch) > 0
+    live &= lens > 0
+    assert np.abs(got[live] - ref[live]).max() <= 1e-2 * np.abs(ref[live]).max()
+
+
+@pytest.mark.parametrize("hq,hkv,hd,gs", [(64, 8, 128, 32), (5, 1, 64, 32), (14, 2, 128, 128), (12, 4, 64, 64)])
+def test_the_fused_step_by_clusters_and_by_even_shares(hq, hkv, hd, gs):
+    """The new token's row written by the cluster's last CTA, and by one CTA of an even split: the same bytes and the
+    output of the separate calls."""
+    lens = [1, 2, 33, 300, 0, 257, 64]
+    for max_ctas in (0, 3):
+        c = Case("bf16", hq, hkv, hd, gs, 16, lens, seed=3)
+        B = len(lens)
+        g = torch.Generator().manual_seed(5)
+        k, v = (torch.randn(B, hkv, hd, generator=g).bfloat16().cuda() for _ in range(2))
+        row = hkv * hd
+        other = [x.clone() for x in c.cache]
+        out = torch.full_like(c.q, 7.0)
+        slots = torch.full((B,), -9, dtype=torch.int64, device="cuda")
+        pa.pa_decode_kv_write_q4(c.desc, gs, c.q, k, row, v, row, B, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx, c.scale,
+                                 max_ctas, slots, out, c.ws(max_ctas))
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        pos = torch.empty(B, dtype=torch.int32, device="cuda")
+        s2 = torch.empty(B, dtype=torch.int64, device="cuda")
+        pa.pa_slot_mapping(c.desc, B, cu, c.ctx, c.btd, c.maxp, B, pos, s2)
+        pa.pa_kv_write_q4(c.desc, gs, k, row, v, row, B, s2, *other)
+        assert (slots == s2).all()
+        for a, b in zip(c.cache, other):
+            assert (a == b).all()
+        c.cache = other
+        assert (c.decode(max_ctas) == out).all()
+    assert pa.pa_read_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_key_that_is_not_a_number_makes_its_heads_outputs_nan_however_they_are_split(dtype):
+    c = Case(dtype, 8, 4, 128, 32, 16, [900, 700], seed=6)
+    ref = c.reference()
+    slot = int(c.bt[0, 20]) * 16 + 3
+    u, s, p = q4.unpack_rows(c.cache[0][slot].cpu().numpy()[None], [slot], 4, 128, 32)
+    s[0, 2, 1], p[0, 2, 1] = 0, np.float16(np.nan)
+    c.cache[0][slot] = torch.from_numpy(q4.pack_rows(u, s, p, [slot])[0]).cuda()
+    want = torch.zeros(2, 8, 128, dtype=torch.bool)
+    want[0, 4:6] = True                         # the two q-heads of kv-head 2
+    for max_ctas in (0, 1, 2, 9):
+        out = c.decode(max_ctas)
+        assert torch.equal(torch.isnan(out).cpu(), want)
+        ok = ~want.numpy()
+        assert np.abs(out.double().cpu().numpy() - ref)[ok].max() <= (1e-5 if dtype == "f32" else 1e-2) * np.abs(ref).max()
