@@ -441,9 +441,13 @@ PA_API pa_status pa_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, c
 
 /*
  * pa_qk_norm_rope_kv_write_q4, pa_prefill_qk_norm_rope_kv_write_q4 -- the norm /
- * rotary writes into a 4-bit cache: q_out and the optional outputs are theirs,
- * and the cache rows are those pa_kv_write_q4 makes of the normed, rotated k
- * (rounded to the dtype) and of v, bit for bit.  Arguments as
+ * rotary writes into a 4-bit cache: the cache rows are those pa_kv_write_q4 makes
+ * of the normed, rotated k (rounded to the dtype) and of v, bit for bit.  A code
+ * moves by a whole step where its value crosses a border by an ulp, so the norm
+ * and the rotation are the plain formulas evaluated operation by operation in
+ * fp32 (the squares 32 elements apart added first, then neighbours in pairs;
+ * sines and cosines of the 64-bit angle, rounded): q_out may differ in the last
+ * bit from that of the namesakes, whose angles are coarser.  Arguments as
  * pa_qk_norm_rope_kv_write and pa_prefill_qk_norm_rope_kv_write.
  */
 PA_API pa_status pa_qk_norm_rope_kv_write_q4(const pa_cache_desc* desc, int32_t group_size, const void* q,

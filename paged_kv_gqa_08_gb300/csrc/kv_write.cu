@@ -114,6 +114,17 @@ struct Vec4<__nv_bfloat16> {
   }
 };
 
+PA_DEVINL void load_two(const float* p, float& x, float& y) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  x = v.x;
+  y = v.y;
+}
+PA_DEVINL void load_two(const __nv_bfloat16* p, float& x, float& y) {
+  const float2 v = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(p));
+  x = v.x;
+  y = v.y;
+}
+
 // 2*pi as the float nearest to it plus the float nearest to the remainder
 // (Cody and Waite's additive reduction, 1980), and the float nearest to 1/(2*pi).
 constexpr float kTwoPiF1 = 6.28318548202514648f;
@@ -136,6 +147,52 @@ PA_DEVINL float reduce_angle(int pos, float fh, float fl) {
   const float k = rintf(p1 * kInvTwoPiF);
   const float r = fmaf(-k, kTwoPiF2, fmaf(-k, kTwoPiF1, p1));
   return r + (e1 + e2);
+}
+
+// a + b = s + e exactly (Knuth).
+PA_DEVINL void two_sum(float a, float b, float& s, float& e) {
+  s = a + b;
+  const float bb = s - a;
+  e = (a - (s - bb)) + (b - bb);
+}
+
+// Sine and cosine of pos * (fh + fl), rounded to fp32 from about 2^-35 of their
+// value (0.06% of them differ from the rounded double result, by one ulp; for
+// positions up to 140000).  The angle is a float pair, reduced by multiples of
+// pi/2 in three floats (p - k C1 is exact: both are multiples of the result's
+// last place); the Taylor series' first correction (-r^3/6, r^4/24) is a float
+// pair too, the rest of either series too small to need one.
+PA_DEVINL void sincos_pair(int pos, float fh, float fl, float& sn, float& cs) {
+  const float pf = static_cast<float>(pos);
+  const float p = __fmul_rn(pf, fh), lo = fmaf(pf, fl, fmaf(pf, fh, -p));
+  const float k = rintf(p * 0.636619772f);
+  const float h = __fmul_rn(k, -4.37113883e-8f), l = fmaf(k, -1.71512451e-15f, fmaf(k, -4.37113883e-8f, -h));
+  float s1, e1, s2, e2, r, rl;
+  two_sum(fmaf(-k, 1.57079637f, p), lo, s1, e1);
+  two_sum(s1, -h, s2, e2);
+  two_sum(s2, (e1 + e2) - l, r, rl);
+  const float z = __fmul_rn(r, r), zl = fmaf(r, r, -z);
+  // sin: r - r^3 / 6 + ...
+  const float a = __fmul_rn(r, z), al = fmaf(r, zl, fmaf(r, z, -a));
+  float w = __fmul_rn(a, -0.166666672f);
+  float wl = fmaf(al, -0.166666672f, fmaf(a, 4.967054e-9f, fmaf(a, -0.166666672f, -w)));
+  float tail = a * z * fmaf(z, fmaf(z, fmaf(z, -2.50521084e-8f, 2.75573192e-6f), -1.98412698e-4f), 8.33333333e-3f);
+  float s = r + w;
+  const float S = s + ((w - (s - r)) + (wl + tail + rl * fmaf(-0.5f, z, 1.f)));
+  // cos: 1 - r^2 / 2 + r^4 / 24 - ...
+  const float z2 = fmaf(2.f * r, rl, zl);
+  const float b = __fmul_rn(z, z), bl = fmaf(2.f * z, z2, fmaf(z, z, -b));
+  w = __fmul_rn(b, 0.0416666679f);
+  wl = fmaf(bl, 0.0416666679f, fmaf(b, -1.2417635e-9f, fmaf(b, 0.0416666679f, -w)));
+  tail = b * z * fmaf(z, fmaf(z, fmaf(z, 2.08767570e-9f, -2.75573192e-7f), 2.48015873e-5f), -1.38888889e-3f);
+  s = fmaf(-0.5f, z, 1.f);
+  const float c = s + w;
+  const float C = c + ((w - (c - s)) + (fmaf(-0.5f, z, 1.f - s) + fmaf(-0.5f, z2, wl + tail)));
+  const int q = static_cast<int>(k);
+  sn = (q & 1) ? C : S;
+  cs = (q & 1) ? S : C;
+  if (q & 2) sn = -sn;
+  if ((q + 1) & 2) cs = -cs;
 }
 
 // Two bf16 products, each rounded once to bf16 (the exact product of two
@@ -218,7 +275,12 @@ __host__ __device__ constexpr int nr_stage_bytes(int hq, int hkv, int hd, int e)
 // then takes eight consecutive dims a lane of these heads' k and v rows and
 // quantises the two together, which shares the work on the groups' parameters
 // (quantising k from the rotation's registers and v apart took 3240 instructions
-// a token instead of 2900).
+// a token instead of 2900).  A code moves by a whole step when its value crosses
+// a border by an ulp, so here the norm and the rotation are the plain formulas,
+// operation by operation in fp32: squares rounded and added in a fixed order
+// (32 elements apart, then pairwise), products and sums of the rotation rounded
+// each, sines and cosines rounded from a float pair.  A lane's pairs lie so that
+// it holds the elements that are added first.
 template <typename T, int HD, int GS>
 __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     norm_rope_kv_write_kernel(const NormRopeParams p) {
@@ -259,11 +321,25 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     if (n_mine > 1) issue(1);
   }
 
+  // The lane's rotation pairs i: elements i and HD / 2 + i of a head.
+  constexpr bool kSplit = GS != 0 && HD == 128;  // i = 2l, 2l + 1, 32 + 2l, 33 + 2l; else 4l ... 4l + 3
+  auto load_pairs = [&](const T* row, float (&x)[PE]) {
+    if constexpr (kSplit) {
+      load_two(row + 2 * l, x[0], x[1]);
+      load_two(row + 32 + 2 * l, x[2], x[3]);
+    } else {
+      Vec4<T>::load(row + l * PE, x);
+    }
+  };
+  // a + b where a or b is a product: an addition would be contracted with it, a
+  // multiply-add by a 1 that the compiler does not know (theta^0) is not.
+  [[maybe_unused]] const float2 one = make_float2(p.inv_freq_hi[0], p.inv_freq_hi[0]);
+  [[maybe_unused]] auto plus = [&](float2 a, float2 b) { return ffma2(a, one, b); };
   float wq_a[PE], wq_b[PE], wk_a[PE], wk_b[PE];
-  Vec4<T>::load(static_cast<const T*>(p.wq) + l * PE, wq_a);
-  Vec4<T>::load(static_cast<const T*>(p.wq) + HD / 2 + l * PE, wq_b);
-  Vec4<T>::load(static_cast<const T*>(p.wk) + l * PE, wk_a);
-  Vec4<T>::load(static_cast<const T*>(p.wk) + HD / 2 + l * PE, wk_b);
+  load_pairs(static_cast<const T*>(p.wq), wq_a);
+  load_pairs(static_cast<const T*>(p.wq) + HD / 2, wq_b);
+  load_pairs(static_cast<const T*>(p.wk), wk_a);
+  load_pairs(static_cast<const T*>(p.wk) + HD / 2, wk_b);
   // bf16: the weights as bf16 pairs for the packed multiply
   uint32_t wq_a2[PE / 2], wq_b2[PE / 2], wk_a2[PE / 2], wk_b2[PE / 2];
 #pragma unroll
@@ -335,9 +411,13 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     // angle pos * theta^(-2i/HD) formed and reduced modulo 2*pi in two-float
     // arithmetic, then evaluated by the special-function unit
     if (threadIdx.x < HD / 2) {
-      const float r = reduce_angle(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x]);
       float sv, cv;
-      __sincosf(r, &sv, &cv);
+      if constexpr (GS == 0) {
+        const float r = reduce_angle(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x]);
+        __sincosf(r, &sv, &cv);
+      } else {
+        sincos_pair(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x], sv, cv);
+      }
       cs_s[threadIdx.x] = cv;
       sn_s[threadIdx.x] = sv;
     }
@@ -346,8 +426,9 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     float cs[PE], sn[PE], nsn[PE];
 #pragma unroll
     for (int e = 0; e < PE; ++e) {
-      cs[e] = cs_s[l * PE + e];
-      sn[e] = sn_s[l * PE + e];
+      const int i = kSplit ? e / 2 * 32 + 2 * l + e % 2 : l * PE + e;
+      cs[e] = cs_s[i];
+      sn[e] = sn_s[i];
       nsn[e] = -sn[e];
     }
     unsigned char* st = stages + (i & 1) * stage_bytes;
@@ -361,18 +442,39 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
       const T* src = reinterpret_cast<const T*>(st) + static_cast<int64_t>(active ? hh : 0) * HD;
       float xa[PE] = {0.f, 0.f, 0.f, 0.f}, xb[PE] = {0.f, 0.f, 0.f, 0.f};
       if (active) {
-        Vec4<T>::load(src + l * PE, xa);
-        Vec4<T>::load(src + HD / 2 + l * PE, xb);
+        load_pairs(src, xa);
+        load_pairs(src + HD / 2, xb);
       }
-      float2 ss2 = make_float2(0.f, 0.f);
+      float ss;
+      if constexpr (GS == 0) {
+        float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < PE; e += 2) {
-        ss2 = ffma2(make_float2(xa[e], xa[e + 1]), make_float2(xa[e], xa[e + 1]), ss2);
-        ss2 = ffma2(make_float2(xb[e], xb[e + 1]), make_float2(xb[e], xb[e + 1]), ss2);
+        for (int e = 0; e < PE; e += 2) {
+          ss2 = ffma2(make_float2(xa[e], xa[e + 1]), make_float2(xa[e], xa[e + 1]), ss2);
+          ss2 = ffma2(make_float2(xb[e], xb[e + 1]), make_float2(xb[e], xb[e + 1]), ss2);
+        }
+        ss = ss2.x + ss2.y;
+#pragma unroll
+        for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      } else {
+        // t + x^2, the square rounded (a bf16's is exact)
+        auto add_square = [&](float2 t, float x, float y) {
+          const float2 v = make_float2(x, y);
+          return sizeof(T) == 2 ? ffma2(v, v, t) : plus(fmul2(v, v), t);
+        };
+        const float2 zero = make_float2(0.f, 0.f);
+        float2 t0 = add_square(zero, xa[0], xa[1]);
+        if constexpr (HD == 128) {  // elements j, j + 32, j + 64, j + 96
+          t0 = add_square(add_square(add_square(t0, xa[2], xa[3]), xb[0], xb[1]), xb[2], xb[3]);
+          ss = t0.x + t0.y;
+        } else {                    // j, j + 32
+          t0 = add_square(t0, xb[0], xb[1]);
+          const float2 t1 = add_square(add_square(zero, xa[2], xa[3]), xb[2], xb[3]);
+          ss = (t0.x + t0.y) + (t1.x + t1.y);
+        }
+#pragma unroll
+        for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       }
-      float ss = ss2.x + ss2.y;
-#pragma unroll
-      for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       // a 4-bit group's reduction takes the whole warp, heads past the last included
       if constexpr (GS == 0) {
         if (!active) continue;
@@ -393,14 +495,23 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
           const float2 na = bf16x2_to_float2(mul_bf16x2(pack_bf16x2(ta.x, ta.y), isq ? wq_a2[e2] : wk_a2[e2]));
           const float2 nb = bf16x2_to_float2(mul_bf16x2(pack_bf16x2(tb.x, tb.y), isq ? wq_b2[e2] : wk_b2[e2]));
           const float2 c2 = make_float2(cs[e], cs[e + 1]);
-          const float2 ya = ffma2(nb, make_float2(nsn[e], nsn[e + 1]), fmul2(na, c2));
-          const float2 yb = ffma2(nb, c2, fmul2(na, make_float2(sn[e], sn[e + 1])));
+          const float2 s2 = make_float2(sn[e], sn[e + 1]), ns2 = make_float2(nsn[e], nsn[e + 1]);
+          const float2 ya = GS == 0 ? ffma2(nb, ns2, fmul2(na, c2)) : plus(fmul2(na, c2), fmul2(nb, ns2));
+          const float2 yb = GS == 0 ? ffma2(nb, c2, fmul2(na, s2)) : plus(fmul2(nb, c2), fmul2(na, s2));
           wa[e2] = pack_bf16x2(ya.x, ya.y);
           wb[e2] = pack_bf16x2(yb.x, yb.y);
         }
         if (store) {
-          *reinterpret_cast<uint2*>(dst + l * PE) = make_uint2(wa[0], wa[1]);
-          *reinterpret_cast<uint2*>(dst + HD / 2 + l * PE) = make_uint2(wb[0], wb[1]);
+          if constexpr (kSplit) {
+#pragma unroll
+            for (int e2 = 0; e2 < PE / 2; ++e2) {
+              *reinterpret_cast<uint32_t*>(dst + e2 * 32 + 2 * l) = wa[e2];
+              *reinterpret_cast<uint32_t*>(dst + HD / 2 + e2 * 32 + 2 * l) = wb[e2];
+            }
+          } else {
+            *reinterpret_cast<uint2*>(dst + l * PE) = make_uint2(wa[0], wa[1]);
+            *reinterpret_cast<uint2*>(dst + HD / 2 + l * PE) = make_uint2(wb[0], wb[1]);
+          }
         }
       } else {
         float ya[PE], yb[PE];
@@ -408,12 +519,22 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
         for (int e = 0; e < PE; ++e) {
           const float na = round_to<T>(round_to<T>(xa[e] * r) * (isq ? wq_a[e] : wk_a[e]));
           const float nb = round_to<T>(round_to<T>(xb[e] * r) * (isq ? wq_b[e] : wk_b[e]));
-          ya[e] = round_to<T>(na * cs[e] - nb * sn[e]);
-          yb[e] = round_to<T>(nb * cs[e] + na * sn[e]);
+          ya[e] = GS == 0 ? round_to<T>(na * cs[e] - nb * sn[e])
+                          : round_to<T>(__fmul_rn(na, cs[e]) + __fmul_rn(nb, nsn[e]));
+          yb[e] = GS == 0 ? round_to<T>(nb * cs[e] + na * sn[e])
+                          : round_to<T>(__fmul_rn(nb, cs[e]) + __fmul_rn(na, sn[e]));
         }
         if (store) {
-          Vec4<T>::store(dst + l * PE, ya);
-          Vec4<T>::store(dst + HD / 2 + l * PE, yb);
+          if constexpr (kSplit) {
+#pragma unroll
+            for (int e = 0; e < PE; e += 2) {
+              *reinterpret_cast<float2*>(dst + e * 16 + 2 * l) = make_float2(ya[e], ya[e + 1]);
+              *reinterpret_cast<float2*>(dst + HD / 2 + e * 16 + 2 * l) = make_float2(yb[e], yb[e + 1]);
+            }
+          } else {
+            Vec4<T>::store(dst + l * PE, ya);
+            Vec4<T>::store(dst + HD / 2 + l * PE, yb);
+          }
         }
       }
       if constexpr (GS != 0) {

@@ -141,9 +141,9 @@ def test_bad_slots_are_skipped_and_flagged():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hq,hkv,hd,gs", [(16, 8, 128, 32), (8, 8, 128, 64), (10, 2, 128, 128), (3, 1, 128, 32),
                                           (8, 4, 64, 32), (7, 1, 64, 64), (6, 2, 64, 32)])
-def test_norm_rope_write_is_the_norm_rope_row_quantised(dtype, hq, hkv, hd, gs):
-    """The rows of pa_qk_norm_rope_kv_write, read from a cache of the dtype and quantised by pa_kv_write_q4, are the
-    fused call's rows, bit for bit; so are q_out and the variant that maps the slots itself."""
+def test_norm_rope_write_quantises_the_rows_of_the_plain_formula(dtype, hq, hkv, hd, gs):
+    """q_out is the norm and rotary evaluated operation by operation in fp32, the cache rows those that pa_kv_write_q4
+    makes of k so treated, bit for bit; so is the variant that maps the slots itself."""
     n, P, pages = 37, 16, 8
     dt = DT[dtype]
     desc = pa.cache_desc(hq, hkv, hd, P, pages, dt)
@@ -157,28 +157,79 @@ def test_norm_rope_write_is_the_norm_rope_row_quantised(dtype, hq, hkv, hd, gs):
     slots = torch.empty(n, dtype=torch.int64, device="cuda")
     pa.pa_slot_mapping(desc, 3, cu, ctx, bt, 4, n, pos, slots)
     row = hkv * hd
-    kd, vd = (torch.zeros(pages, P, hkv, hd, dtype=dt, device="cuda") for _ in range(2))
-    qo = torch.zeros(n, hq, hd, dtype=dt, device="cuda")
-    pa.pa_qk_norm_rope_kv_write(desc, q, hq * hd, k, row, v, row, n, pos, wq, wk, 1e-6, 1e6, slots, qo, kd, vd)
     R = pa.pa_q4_row_bytes(desc, gs)
-    want = [torch.full((pages * P, R), FILL, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    live = slots >= 0
-    pa.pa_kv_write_q4(desc, gs, kd.reshape(-1, row)[slots.clamp(min=0)].contiguous(), row, v, row, n, slots, *want)
+    blank = lambda: [torch.full((pages * P, R), FILL, dtype=torch.uint8, device="cuda") for _ in range(2)]  # noqa: E731
+    # k through q's place: its rows as the call norms and rotates them
+    same = pa.cache_desc(hkv, hkv, hd, P, pages, dt)
+    kn = torch.zeros_like(k)
+    pa.pa_qk_norm_rope_kv_write_q4(same, gs, k, row, k, row, v, row, n, pos, wk, wk, 1e-6, 1e6, slots, kn, *blank())
+    want = blank()
+    pa.pa_kv_write_q4(desc, gs, kn, row, v, row, n, slots, *want)
     for mapped in (False, True):
-        got = [torch.full((pages * P, R), FILL, dtype=torch.uint8, device="cuda") for _ in range(2)]
-        qo2 = torch.zeros_like(qo)
+        got = blank()
+        qo = torch.zeros_like(q)
         if mapped:
             p2, s2 = torch.empty_like(pos), torch.empty_like(slots)
             pa.pa_prefill_qk_norm_rope_kv_write_q4(desc, gs, q, hq * hd, k, row, v, row, n, cu, 3, ctx, bt, 4, wq, wk,
-                                                   1e-6, 1e6, qo2, *got, p2, s2)
+                                                   1e-6, 1e6, qo, *got, p2, s2)
             assert torch.equal(p2, pos) and torch.equal(s2, slots)
         else:
             pa.pa_qk_norm_rope_kv_write_q4(desc, gs, q, hq * hd, k, row, v, row, n, pos, wq, wk, 1e-6, 1e6, slots,
-                                           qo2, *got)
-        assert torch.equal(qo2, qo)
+                                           qo, *got)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    assert int(live.sum()) == 34
+        check_norm_rope(qo, plain_norm_rope(q, wq, pos, 1e-6, 1e6), dtype)
+    check_norm_rope(kn, plain_norm_rope(k, wk, pos, 1e-6, 1e6), dtype)
+    assert int((slots >= 0).sum()) == 34
     assert pa.pa_read_device_errors(reset=True) == 0
+
+
+def plain_norm_rope(x, w, pos, eps, theta):
+    """RMSNorm and rotary one fp32 operation at a time: squares 32 elements apart added first, then neighbours in pairs;
+    sines and cosines those of the 64-bit angle, rounded."""
+    dt, hd = x.dtype, x.shape[-1]
+    x = x.float()
+    t = (x * x).unflatten(-1, (hd // 32, 32))
+    ss = t[..., 0, :]
+    for i in range(1, hd // 32):
+        ss = ss + t[..., i, :]
+    while ss.shape[-1] > 1:
+        ss = ss[..., 0::2] + ss[..., 1::2]
+    r = torch.rsqrt(ss / hd + eps)
+    x = ((x * r).to(dt).float() * w.float()).to(dt).float()
+    f = theta ** (-2.0 * torch.arange(hd // 2, device=x.device, dtype=torch.float64) / hd)
+    ang = pos.double()[:, None, None] * f
+    c, s = torch.cos(ang).float(), torch.sin(ang).float()
+    a, b = x[..., : hd // 2], x[..., hd // 2:]
+    return torch.cat([a * c - b * s, b * c + a * s], -1).to(dt)
+
+
+def check_norm_rope(got, want, dtype):
+    """Equal but for the sines and cosines that round to the other neighbour: fewer than one in a thousand, and a value
+    takes one of each (the bound: 1 in 100).  Those move a value by an ulp of its pair's size: 2^-23 of it in fp32, a
+    rounding border crossed in bf16 (2^-7 of the value)."""
+    g, w = got.float(), want.float()
+    assert (g != w).float().mean() <= 0.01
+    h = w.shape[-1] // 2
+    size = torch.hypot(w[..., :h], w[..., h:])
+    size = torch.cat([size, size], -1)
+    assert ((g - w).abs() <= size * (2.0 ** -7 if dtype == "bf16" else 2.0 ** -22)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_norm_rope_write_at_far_positions(dtype, hd):
+    n, heads = 600, 4
+    dt = DT[dtype]
+    desc = pa.cache_desc(heads, heads, hd, 16, 40, dt)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = torch.randn(n, heads, hd, generator=g, device="cuda").to(dt), torch.ones(hd, dtype=dt, device="cuda")
+    pos = torch.randint(0, 131072, (n,), generator=g, device="cuda", dtype=torch.int32)
+    pos[:4] = torch.tensor([0, 1, 131071, 65536], dtype=torch.int32)
+    slots = torch.arange(n, dtype=torch.int64, device="cuda")
+    out, row = torch.zeros_like(x), heads * hd
+    caches = [torch.zeros(40 * 16, pa.pa_q4_row_bytes(desc, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pa.pa_qk_norm_rope_kv_write_q4(desc, 64, x, row, x, row, x, row, n, pos, w, w, 1e-6, 1e4, slots, out, *caches)
+    check_norm_rope(out, plain_norm_rope(x, w, pos, 1e-6, 1e4), dtype)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
