@@ -1,8 +1,11 @@
 // Writing rows into a 4-bit cache and reading them back (sm_103a).
 //
-// Both are one pass over the data and HBM-bound: writing a token reads
-// 2 * Hkv * HD elements and writes 2 rows of (HD / 2 + 4 HD / GS) * Hkv bytes,
-// reading does the reverse.
+// Both are one pass over the data: writing a token reads 2 * Hkv * HD elements and
+// writes 2 rows of (HD / 2 + 4 HD / GS) * Hkv bytes, reading does the reverse.
+// Measured (8 heads of 128 dims, bf16): writing 16384 tokens 22.4 us, 3.9 TB/s,
+// bound by its 1043 warp instructions a token (72% issue active) once K and V share
+// the work on their groups' parameters; reading 32768 rows 31 us and 89554 rows
+// 74.3 us, 5.5 and 6.2 TB/s of a copy's 6.7.
 #include <algorithm>
 
 #include "q4_common.cuh"
