@@ -343,7 +343,7 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
 // [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
 // when a score passes it by more).  p s is kept in float16's range by a power of
-// two 2^-E that follows the largest s seen.  Each rounding to float16 is 2^-12
+// two 2^-E that follows the largest s seen.  Each rounding to float16 is 2^-11
 // relative, finer than the bf16 of queries and outputs; sums and statistics are
 // fp32.
 // ---------------------------------------------------------------------------
@@ -598,7 +598,8 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
         lds_words<NG>(par[u], half + u * 8 * R + kp_at);
         pm[u] = par[u][0];  // (any where there is no group tq: its queries' sum is 0)
         if constexpr (NG == 2) pm[u] = (tq & 1) ? par[u][1] : par[u][0];
-        if constexpr (NG == 4) pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
+        if constexpr (NG == 4)
+          pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
       }
       float sc[4], d[4];
       mma_f16_k8(sc, pm[0], pm[1], qm);
@@ -1198,7 +1199,8 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // 16 consumer warps on an SM: four or more chunks.
   const size_t fixed = align_up(off, 128), stage = q4_stage_bytes(d, pl);
   const size_t share = static_cast<size_t>(di.max_smem_optin) * std::min(pl.nw, 16) / 16 - 1024;
-  pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, share > fixed ? (share - fixed) / stage : 0)));
+  const size_t room = share > fixed ? (share - fixed) / stage : 0;
+  pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, room)));
   const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
   for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
     *o += ring;
@@ -1220,7 +1222,7 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // over all SMs (1000 tokens: 10.9 us, by a cluster 12.1).
   if (n >= batch && batch <= kInlinePlanMax && max_ctx <= kWholeTokens) pl.cluster = 1;
   if (!simt && batch > 1 && batch <= kInlinePlanMax && pl.cluster == 0) {
-    int c = static_cast<int>(std::min<int64_t>({kMaxCluster, n / batch, (max_ctx + kTok - 1) / kTok}));
+    int c = static_cast<int>(std::min<int64_t>({kMaxCluster, n / batch, chunks_upper / batch}));
     for (; c > 1 && static_cast<int64_t>(max_ctx) * d.head_dim <= static_cast<int64_t>(c) * kClusterTokens * 128; --c) {
       int fit = 0;
       e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &fit, c);

@@ -244,20 +244,22 @@ def test_the_fused_step_equals_the_separate_calls(dtype, hq, hkv, hd, gs, P):
     assert pa.pa_read_device_errors(reset=True) == 0
 
 
-def test_two_graphs_share_a_workspace_and_replay_with_new_inputs():
+@pytest.mark.parametrize("max_ctas", [0, 5])    # clusters; even shares and the merge kernel
+def test_two_graphs_share_a_workspace_and_replay_with_new_inputs(max_ctas):
     """A captured step of each kind over one workspace, replayed in turn with other lengths, against fresh calls."""
     c = Case("bf16", 16, 8, 128, 32, 16, [300, 300, 300], seed=31)
     kn, vn = (torch.randn(3, 1024, device="cuda").bfloat16() for _ in range(2))
-    ws = c.ws()
+    ws = c.ws(max_ctas)
     outs = [torch.zeros_like(c.q) for _ in range(2)]
     slots = torch.zeros(3, dtype=torch.int64, device="cuda")
 
     def plain():
-        pa.pa_decode_q4(c.desc, 32, c.q, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx, c.scale, 0, outs[0], ws)
+        pa.pa_decode_q4(c.desc, 32, c.q, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx, c.scale, max_ctas, outs[0],
+                        ws)
 
     def step():
         pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
-                                 c.scale, 0, slots, outs[1], ws)
+                                 c.scale, max_ctas, slots, outs[1], ws)
 
     plain()
     torch.cuda.synchronize()
@@ -282,11 +284,11 @@ def test_two_graphs_share_a_workspace_and_replay_with_new_inputs():
         torch.cuda.synchronize()
         after = c.cache
         c.cache = before
-        want0 = c.decode()
+        want0 = c.decode(max_ctas)
         assert torch.equal(outs[0].view(torch.uint8), want0.view(torch.uint8))
         want1 = torch.full_like(want0, 7.0)
         pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
-                                 c.scale, 0, None, want1, c.ws())
+                                 c.scale, max_ctas, None, want1, c.ws(max_ctas))
         torch.cuda.synchronize()
         assert torch.equal(outs[1].view(torch.uint8), want1.view(torch.uint8))
         assert torch.equal(after[0], c.cache[0]) and torch.equal(after[1], c.cache[1])
@@ -428,3 +430,75 @@ def test_a_key_that_is_not_a_number_makes_its_heads_outputs_nan_however_they_are
         assert torch.equal(torch.isnan(out).cpu(), want)
         ok = ~want.numpy()
         assert np.abs(out.double().cpu().numpy() - ref)[ok].max() <= (1e-5 if dtype == "f32" else 1e-2) * np.abs(ref).max()
+
+
+@pytest.mark.parametrize("gs", [32, 64, 128])
+@pytest.mark.parametrize("order", ["growing", "falling", "one"])
+def test_scales_that_change_along_the_context(gs, order):
+    """V's magnitude rises or falls by 2^40 along the context, or is 2^20 times the others' in one token that no query
+    looks at: the powers of two that keep p s in float16's range follow the largest scale."""
+    c = Case("bf16", 4, 4, 128, gs, 16, [700, 90], seed=8)
+    rng = np.random.default_rng(1)
+    for b, L in enumerate(c.lens):
+        slots = c.bt[b, np.arange(L) // 16].astype(np.int64) * 16 + np.arange(L) % 16
+        x = rng.standard_normal((L, 4, 128))
+        e = np.linspace(-28, 12, L)
+        if order == "falling":
+            e = e[::-1]
+        if order == "one":
+            e = np.full(L, -8.0)
+            e[L // 2] = 12.0
+            k = rng.standard_normal((1, 4, 128)) * 0.01 - 4 * c.q64[b][None]     # scores far below the others'
+            c.cache[0][slots[L // 2]] = torch.from_numpy(q4.pack_rows(*q4.quantise(k.astype(np.float32), gs),
+                                                                      slots[L // 2:L // 2 + 1])[0]).cuda()
+            c.vals[0][slots[L // 2]] = q4.values(*q4.quantise(k.astype(np.float32), gs), gs)[0]
+        x = (x * np.exp2(e)[:, None, None]).astype(np.float32)
+        u, sc, off = q4.quantise(x, gs)
+        c.cache[1][torch.from_numpy(slots).cuda()] = torch.from_numpy(q4.pack_rows(u, sc, off, slots)).cuda()
+        c.vals[1][slots] = q4.values(u, sc, off, gs)
+    ref = c.reference()
+    for max_ctas in (0, 1, 2, 20):
+        c.check(c.decode(max_ctas), ref)
+
+
+def test_two_streams_at_once_and_the_same_bits_every_time():
+    """A clustered and a split decode, each on a stream and a workspace of its own, over and over side by side."""
+    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0], seed=21)
+    b = Case("bf16", 24, 4, 128, 32, 16, [3000, 5, 641], seed=22)
+    wa, wb = a.decode(), b.decode(60)
+    a.check(wa)
+    b.check(wb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = [a.ws(), b.ws(60)]
+    outs = [[torch.full_like(x.q, 7.0) for _ in range(40)] for x in (a, b)]
+    torch.cuda.synchronize()
+    for i in range(40):
+        pa.pa_decode_q4(a.desc, a.gs, a.q, 4, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, outs[0][i], ws[0],
+                        stream=sa)
+        pa.pa_decode_q4(b.desc, b.gs, b.q, 3, *b.cache, b.btd, b.maxp, b.ctx, b.max_ctx, b.scale, 60, outs[1][i], ws[1],
+                        stream=sb)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, wa) for o in outs[0]) and all(torch.equal(o, wb) for o in outs[1])
+
+
+def test_a_fork_and_join_in_one_graph():
+    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0], seed=21)
+    b = Case("f32", 8, 4, 64, 32, 16, [3000, 5, 641], seed=22)
+    wa, wb = a.decode(), b.decode()
+    oa, ob, ws = torch.full_like(a.q, 7.0), torch.full_like(b.q, 7.0), [a.ws(), b.ws()]
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        pa.pa_decode_q4(a.desc, a.gs, a.q, 4, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, oa, ws[0])
+        pa.pa_decode_q4(b.desc, b.gs, b.q, 3, *b.cache, b.btd, b.maxp, b.ctx, b.max_ctx, b.scale, 0, ob, ws[1],
+                        stream=side)
+        main.wait_stream(side)
+    for _ in range(3):
+        oa.fill_(7.0)
+        ob.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa, wa) and torch.equal(ob, wb)
