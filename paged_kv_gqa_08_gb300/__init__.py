@@ -159,6 +159,8 @@ def _at(t) -> Optional[int]:
         return None if t is None else int(t)
 
 
+_Tensor, _uint8 = torch.Tensor, torch.uint8
+
 # The current device's index and its current stream's handle, as torch.cuda.current_device() and
 # current_stream().cuda_stream give them, without their layers of checks: those took 4 us of a call's 14.
 _current_device = None
@@ -328,24 +330,41 @@ def _q4_caches(fn, desc, group_size, k_cache, v_cache):
             raise PagedAttnError(fn, PA_ERR_UNSUPPORTED, f"the cache is on {t.device}, not on the current CUDA device")
 
 
+def _q4_args(fn, desc, group_size, k_cache, v_cache, stream, *tensors):
+    """The addresses of ``tensors`` and of the checked caches, and the stream: what every call over a 4-bit cache
+    passes on.  The calls are short, so the usual case (tensors, the current stream) takes the fewest steps."""
+    at = [t.data_ptr() if t.__class__ is _Tensor else _at(t) for t in tensors]
+    if k_cache.__class__ is _Tensor and v_cache.__class__ is _Tensor and _current_device is not None:
+        device = _current_device()
+        need = desc.num_pages * desc.page_size * _lib.pa_q4_row_bytes(desc, group_size)
+        if (k_cache.dtype is _uint8 and k_cache.numel() >= need and k_cache.is_contiguous()
+                and k_cache.get_device() == device and v_cache.dtype is _uint8 and v_cache.numel() >= need
+                and v_cache.is_contiguous() and v_cache.get_device() == device):
+            return at, k_cache.data_ptr(), v_cache.data_ptr(), (_raw_stream(device) if stream is None
+                                                                else _stream(stream))
+    _q4_caches(fn, desc, group_size, k_cache, v_cache)
+    return at, _at(k_cache), _at(v_cache), _stream(stream)
+
+
 def pa_kv_write_q4(desc, group_size, k, k_row_stride, v, v_row_stride, num_tokens, slot_mapping, k_cache, v_cache,
                    stream=None):
     lib = load_library()
-    _q4_caches("pa_kv_write_q4", desc, group_size, k_cache, v_cache)
-    _check("pa_kv_write_q4", lib.pa_kv_write_q4(
-        desc, group_size, _at(k), k_row_stride, _at(v), v_row_stride, num_tokens, _at(slot_mapping),
-        _at(k_cache), _at(v_cache), _stream(stream)))
+    (k, v, slots), kc, vc, st = _q4_args("pa_kv_write_q4", desc, group_size, k_cache, v_cache, stream, k, v,
+                                         slot_mapping)
+    _check("pa_kv_write_q4", lib.pa_kv_write_q4(desc, group_size, k, k_row_stride, v, v_row_stride, num_tokens, slots,
+                                                kc, vc, st))
 
 
 def pa_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens,
                                 positions, q_norm_w, k_norm_w, eps, rope_theta, slot_mapping, q_out, k_cache, v_cache,
                                 stream=None):
     lib = load_library()
-    _q4_caches("pa_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
+    (q, k, v, pos, wq, wk, slots, qo), kc, vc, st = _q4_args(
+        "pa_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache, stream, q, k, v, positions, q_norm_w,
+        k_norm_w, slot_mapping, q_out)
     _check("pa_qk_norm_rope_kv_write_q4", lib.pa_qk_norm_rope_kv_write_q4(
-        desc, group_size, _at(q), q_row_stride, _at(k), k_row_stride, _at(v), v_row_stride,
-        num_tokens, _at(positions), _at(q_norm_w), _at(k_norm_w), eps, rope_theta, _at(slot_mapping),
-        _at(q_out), _at(k_cache), _at(v_cache), _stream(stream)))
+        desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens, pos, wq, wk, eps, rope_theta,
+        slots, qo, kc, vc, st))
 
 
 def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride,
@@ -353,23 +372,24 @@ def pa_prefill_qk_norm_rope_kv_write_q4(desc, group_size, q, q_row_stride, k, k_
                                         max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, q_out, k_cache,
                                         v_cache, positions_out=None, slot_mapping_out=None, stream=None):
     lib = load_library()
-    _q4_caches("pa_prefill_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache)
+    (q, k, v, cu, ctx, bt, wq, wk, qo, pos, slots), kc, vc, st = _q4_args(
+        "pa_prefill_qk_norm_rope_kv_write_q4", desc, group_size, k_cache, v_cache, stream, q, k, v, cu_seqlens_q,
+        context_lens, block_tables, q_norm_w, k_norm_w, q_out, positions_out, slot_mapping_out)
     _check("pa_prefill_qk_norm_rope_kv_write_q4", lib.pa_prefill_qk_norm_rope_kv_write_q4(
-        desc, group_size, _at(q), q_row_stride, _at(k), k_row_stride, _at(v), v_row_stride,
-        num_tokens, _at(cu_seqlens_q), batch, _at(context_lens), _at(block_tables), max_pages_per_seq,
-        _at(q_norm_w), _at(k_norm_w), eps, rope_theta, _at(q_out), _at(k_cache), _at(v_cache),
-        _at(positions_out), _at(slot_mapping_out), _stream(stream)))
+        desc, group_size, q, q_row_stride, k, k_row_stride, v, v_row_stride, num_tokens, cu, batch, ctx, bt,
+        max_pages_per_seq, wq, wk, eps, rope_theta, qo, kc, vc, pos, slots, st))
 
 
 def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_tables, max_pages_per_seq, num_rows,
                   k_cache, v_cache, k_out, k_row_stride, v_out, v_row_stride, stream=None):
     """Read tokens of a 4-bit cache back as rows of the descriptor's dtype; ``starts`` may be None (token 0)."""
     lib = load_library()
-    _q4_caches("pa_kv_read_q4", desc, group_size, k_cache, v_cache)
+    (cu, starts, ctx, bt, ko, vo), kc, vc, st = _q4_args(
+        "pa_kv_read_q4", desc, group_size, k_cache, v_cache, stream, cu_rows, starts, context_lens, block_tables,
+        k_out, v_out)
     _check("pa_kv_read_q4", lib.pa_kv_read_q4(
-        desc, group_size, batch, _at(cu_rows), _at(starts), _at(context_lens), _at(block_tables),
-        max_pages_per_seq, num_rows, _at(k_cache), _at(v_cache), _at(k_out), k_row_stride, _at(v_out),
-        v_row_stride, _stream(stream)))
+        desc, group_size, batch, cu, starts, ctx, bt, max_pages_per_seq, num_rows, kc, vc, ko, k_row_stride, vo,
+        v_row_stride, st))
 
 
 def pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas=0) -> int:
@@ -380,26 +400,27 @@ def pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ct
 def pa_decode_q4(desc, group_size, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
                  max_context_len, scale, max_ctas, out, workspace, workspace_bytes=None, stream=None):
     lib = load_library()
-    _q4_caches("pa_decode_q4", desc, group_size, k_cache, v_cache)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    (q, bt, ctx, out, ws), kc, vc, st = _q4_args("pa_decode_q4", desc, group_size, k_cache, v_cache, stream, q,
+                                                 block_tables, context_lens, out, workspace)
     _check("pa_decode_q4", lib.pa_decode_q4(
-        desc, group_size, _at(q), batch, _at(k_cache), _at(v_cache), _at(block_tables),
-        max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas, _at(out), _at(workspace),
-        workspace_bytes, _stream(stream)))
+        desc, group_size, q, batch, kc, vc, bt, max_pages_per_seq, ctx, max_context_len, scale, max_ctas, out, ws,
+        workspace_bytes, st))
 
 
 def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row_stride, batch, k_cache, v_cache,
                           block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas,
                           slot_mapping, out, workspace, workspace_bytes=None, stream=None):
     lib = load_library()
-    _q4_caches("pa_decode_kv_write_q4", desc, group_size, k_cache, v_cache)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    (q, k, v, bt, ctx, slots, out, ws), kc, vc, st = _q4_args(
+        "pa_decode_kv_write_q4", desc, group_size, k_cache, v_cache, stream, q, k_new, v_new, block_tables,
+        context_lens, slot_mapping, out, workspace)
     _check("pa_decode_kv_write_q4", lib.pa_decode_kv_write_q4(
-        desc, group_size, _at(q), _at(k_new), k_row_stride, _at(v_new), v_row_stride, batch,
-        _at(k_cache), _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len,
-        scale, max_ctas, _at(slot_mapping), _at(out), _at(workspace), workspace_bytes, _stream(stream)))
+        desc, group_size, q, k, k_row_stride, v, v_row_stride, batch, kc, vc, bt, max_pages_per_seq, ctx,
+        max_context_len, scale, max_ctas, slots, out, ws, workspace_bytes, st))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,
