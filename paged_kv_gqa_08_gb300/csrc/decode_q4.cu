@@ -846,7 +846,7 @@ PA_DEVINL int plan_in_warp(const KParams& k, int32_t* cs_s, bool first, int lane
   const int per = (k.B + 31) / 32;
   const int b0 = min(k.B, lane * per), b1 = min(k.B, b0 + per);
   int sum = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int b = b0; b < b1; ++b) {
     const int L = k.ctx[b];
     int cnt = 0;
@@ -873,8 +873,6 @@ PA_DEVINL int plan_in_warp(const KParams& k, int32_t* cs_s, bool first, int lane
   }
   if (lane == 0) cs_s[0] = 0;
   __syncwarp();
-  if (first)
-    for (int b = lane; b <= k.B; b += 32) k.cs[b] = cs_s[b];
   return __shfl_sync(0xffffffffu, x, 31);
 }
 

@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const KParams
 // its shared memory (B <= kInlinePlanMax): each thread sums the chunk counts
 // of a run of consecutive requests, the runs' totals are scanned across the
 // CTA, then each thread writes its run's prefix sums.  CTA 0 also does the
-// plan kernel's side work: it publishes the sums for the merge kernel, flags
-// bad lengths and marks the slots of rows it skips.
+// plan kernel's side work: it flags bad lengths and marks the slots of rows it
+// skips.  (The merge kernel works the sums out for itself.)
 __device__ __forceinline__ void plan_in_cta(const KParams& p, int32_t* cs_s, int32_t* warp_tot, bool first) {
   const int nthr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int T = 1 << p.log2T;
@@ -169,8 +169,6 @@ __device__ __forceinline__ void plan_in_cta(const KParams& p, int32_t* cs_s, int
   }
   if (tid == 0) cs_s[0] = 0;
   cta_sync();
-  if (first)
-    for (int b = tid; b <= p.B; b += nthr) p.cs[b] = cs_s[b];
 }
 
 // Time-only bounded wait used when draining copies after an abort.
@@ -191,36 +189,53 @@ PA_DEVINL float ex2_approx(float x) {
 // ---------------------------------------------------------------------------
 // log-sum-exp merge of the partials of requests cut across CTAs.  merge_w
 // warps per (request, q-head): each takes a contiguous range of the partials,
-// a lane owns HD/32 elements of the head, the partials' weights are computed
-// one per lane and eight partials' loads are in flight together; the warps'
-// sums meet in shared memory and are added in a fixed order.
+// a lane owns HD/32 elements of the head, eight partials' loads are in flight
+// together, the first ones with their log-sum-exps'; the warps' sums meet in
+// shared memory and are added in a fixed order.
 // ---------------------------------------------------------------------------
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KParams p) {
   constexpr int EL = HD / 32;  // elements per lane
   constexpr int NWARP = kMergeThreads / 32;
   __shared__ float red[NWARP][32][EL + 1];
-  pdl_wait();                  // every partial of the decode grid is written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.merge_w, item = warp / W, sub = warp - item * W;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * (NWARP / W) + item;
   // The W warps of an item decide together; no warp leaves before the CTA
   // barrier below (merge_w, and so the barrier, is the same for every CTA).
-  int b = 0, hq = 0, c0 = 0, parts = 0, NC = 0;
+  int b = 0, hq = 0, c0 = 0, parts = 0, NC = 0, cb0 = 0, cb1 = 0;
   bool active = u < static_cast<int64_t>(p.B) * p.Hq;
   if (active) {
     b = static_cast<int>(u / p.Hq);
     hq = static_cast<int>(u - static_cast<int64_t>(b) * p.Hq);
-    NC = p.cs[p.B];
-    const int cb0 = p.cs[b], cb1 = p.cs[b + 1];
-    if (cb1 <= cb0) {
-      active = false;
-    } else {
-      c0 = static_cast<int>(((static_cast<int64_t>(cb0) + 1) * p.n_ctas + NC - 1) / NC) - 1;
-      const int c1 = static_cast<int>(((static_cast<int64_t>(cb1)) * p.n_ctas + NC - 1) / NC) - 1;
-      parts = c1 - c0 + 1;
-      active = c0 != c1;  // one CTA wrote the request whole
+  }
+  if (p.inline_plan) {
+    // the plan's sums anew, from the lengths: while the decode grid still runs
+    const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
+    int below = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      const int L = p.ctx[i];
+      const int n = L >= 1 && L <= cap ? (L + (1 << p.log2T) - 1) >> p.log2T : 0;
+      NC += n;
+      below += i < b ? n : 0;
+      cb1 += i <= b ? n : 0;
     }
+    NC = __reduce_add_sync(0xffffffffu, NC);
+    cb0 = __reduce_add_sync(0xffffffffu, below);
+    cb1 = __reduce_add_sync(0xffffffffu, cb1);
+    pdl_wait();  // every partial of the decode grid is written
+  } else {
+    pdl_wait();
+    NC = p.cs[p.B];
+    cb0 = p.cs[b];
+    cb1 = p.cs[b + 1];
+  }
+  if (cb1 <= cb0) active = false;
+  if (active) {
+    c0 = static_cast<int>(((static_cast<int64_t>(cb0) + 1) * p.n_ctas + NC - 1) / NC) - 1;
+    const int c1 = static_cast<int>(((static_cast<int64_t>(cb1)) * p.n_ctas + NC - 1) / NC) - 1;
+    parts = c1 - c0 + 1;
+    active = c0 != c1;  // one CTA wrote the request whole
   }
   // With more CTAs than chunks some CTAs between c0 and c1 own no chunk and
   // wrote no partial: only CTAs with a non-empty range take part.  With at
@@ -234,35 +249,43 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
   for (int e = 0; e < EL; ++e) acc[e] = 0.f;
   float wsum = 0.f;
   if (active) {
+    const int per = (parts + W - 1) / W;
+    const int k_begin = sub * per, k_end = min(parts, k_begin + per);
+    // the first partials' loads do not wait for the weights'
+    float v[8][EL];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (k0 + i < k_end) {
+          const int64_t slot = static_cast<int64_t>(c0 + k0 + i) + b;
+          const float* src = p.o_part + (slot * p.Hq + hq) * HD + lane * EL;
+          if constexpr (EL == 4) {
+            const float4 ov = *reinterpret_cast<const float4*>(src);
+            v[i][0] = ov.x, v[i][1] = ov.y, v[i][2] = ov.z, v[i][3] = ov.w;
+          } else {
+            const float2 ov = *reinterpret_cast<const float2*>(src);
+            v[i][0] = ov.x, v[i][1] = ov.y;
+          }
+        }
+      }
+    };
+    load(k_begin);
     float M = -INFINITY;
     for (int k = lane; k < parts; k += 32)
       if (busy(c0 + k)) M = fmaxf(M, lse_of(k));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int per = (parts + W - 1) / W;
-    const int k_begin = sub * per, k_end = min(parts, k_begin + per);
     if (M != -INFINITY) {
-      for (int k0 = k_begin; k0 < k_end; k0 += 32) {
+      for (int k0 = k_begin; k0 < k_end; k0 += 8) {
+        if (k0 != k_begin) load(k0);
         const int k = k0 + lane;
-        const float w_mine = k < k_end && busy(c0 + k) ? exp2f(lse_of(k) - M) : 0.f;
-        const int kn = min(32, k_end - k0);
-#pragma unroll 8
-        for (int i = 0; i < kn; ++i) {
+        const float w_mine = lane < 8 && k < k_end && busy(c0 + k) ? exp2f(lse_of(k) - M) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           const float w = __shfl_sync(0xffffffffu, w_mine, i);
-          const int64_t slot = static_cast<int64_t>(c0 + k0 + i) + b;
-          const float* src = p.o_part + (slot * p.Hq + hq) * HD + lane * EL;
-          if (w != 0.f) {
-            if constexpr (EL == 4) {
-              const float4 ov = *reinterpret_cast<const float4*>(src);
-              acc[0] += w * ov.x;
-              acc[1] += w * ov.y;
-              acc[2] += w * ov.z;
-              acc[3] += w * ov.w;
-            } else {
-              const float2 ov = *reinterpret_cast<const float2*>(src);
-              acc[0] += w * ov.x;
-              acc[1] += w * ov.y;
-            }
+          if (w != 0.f) {  // (an idle CTA wrote no partial)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) acc[e] += w * v[i][e];
             wsum += w;
           }
         }
