@@ -24,11 +24,10 @@ constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
 constexpr int kMaxCluster = 8;  // CTAs of a cluster that shares a request, at most
-// Tokens of a request that a CTA alone takes, or (of 128 dims; of 64 twice as
-// many) each of a cluster's CTAs, where all requests' CTAs fit at once: more, and
-// it pays to split the batch's keys evenly over the GPU and to merge partial
-// results by another kernel.
-constexpr int kWholeTokens = 256, kClusterTokens = 384;
+// Tokens of 128 dims (of 64 twice as many) of a request that a CTA takes, alone or
+// with its cluster, where a CTA or a cluster per request comes to at least 2/5 of
+// the SMs; that a CTA alone takes in any batch; and that in fp32.
+constexpr int kPartTokens = 256, kAloneTokens = 64, kAloneTokensF32 = 32;
 
 // A chunk in the ring, as the producer describes it to the consumers: its
 // request; the tokens of its halves (n0 | n1 << 8, 0 for a half whose page is
@@ -941,8 +940,8 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
       const int xa = max(x0, cb0), xb = min(x1, cb1);  // the request's chunks in this share
       flags = (x < xa + p.groups ? kFirst : 0u) | (x == xb - 1 ? kLast : 0u) |
               (p.groups == 2 && x == xb - 2 ? kYield : 0u) | (p.groups == 1 || xb - xa == 1 ? kSolo : 0u) |
-              (cb0 >= x0 && cb1 <= x1 && p.cluster <= 1 ? kWhole : 0u) | (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) |
-              (new_slot >= 0 ? kNew : 0u);
+              (cb0 >= x0 && cb1 <= x1 && p.cluster <= 1 ? kWhole : 0u) |
+              (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) | (new_slot >= 0 ? kNew : 0u);
     }
     b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
     for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {
@@ -1210,21 +1209,27 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
   int64_t n = static_cast<int64_t>(occ) * di.sm_count;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
-  // Short requests that fit the GPU at once: a CTA or a cluster each, and no
-  // merge kernel, whose 4 to 7 us are most of such a call.  With 32 q-heads over
-  // 8, groups of 64 and the clusters that fit, against the even split: 8 requests
-  // of 300-1000 tokens 12.3 us (15.5), 37 of them 18.5 (20.9), 16 of 2000 18.9
-  // (22.7); where a CTA's part is longer the even split wins: 8 requests of 4000
-  // tokens 22.5 (20.7), 64 of 300-2000 34.1 (30.0).  37 of 100-2900 with 24
-  // q-heads over 4 of 64 dims 17.7 (22.3).  One request alone is faster
-  // over all SMs (1000 tokens: 10.9 us, by a cluster 12.1).
-  if (n >= batch && batch <= kInlinePlanMax && max_ctx <= kWholeTokens) pl.cluster = 1;
-  if (!simt && batch > 1 && batch <= kInlinePlanMax && pl.cluster == 0) {
-    int c = static_cast<int>(std::min<int64_t>({kMaxCluster, n / batch, chunks_upper / batch}));
-    for (; c > 1 && static_cast<int64_t>(max_ctx) * d.head_dim <= static_cast<int64_t>(c) * kClusterTokens * 128; --c) {
-      int fit = 0;
-      e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &fit, c);
-      if (e != cudaSuccess) return e;
+  // Short requests that fit the GPU at once: a CTA or a cluster each and no merge
+  // kernel, 2 to 4 us of such a call; against them the GPU's other SMs.  With 32
+  // q-heads over 8 of 128 dims, in us (the even split): 16 requests of 300-1000
+  // tokens by clusters of 8 13.7 (15.6), 37 of 64-512 by 4 13.3 (14.6), 64 by 2
+  // 16.0 (17.5), 100 of 64-256 by one CTA each 15.0 (18.4), 4 of 5-64 7.6 (8.6).
+  // Longer parts: 64 of 300-2000 33.8 (27.2).  Too few: 2 of 1000 by 8 12.1 (9.0),
+  // 4 of 256 by one 12.3 (8.8).  fp32's CUDA cores take a chunk four to eight
+  // times as long: 4 of 5-64 tokens of 64 dims 7.6 (8.0), of 128 dims 13.4 (11.3).
+  if (batch >= 1 && batch <= kInlinePlanMax && n >= batch) {
+    const int64_t work = static_cast<int64_t>(max_ctx) * d.head_dim;
+    const int alone = simt ? kAloneTokensF32 : kAloneTokens;
+    const int64_t most = std::min<int64_t>({kMaxCluster, n / batch, chunks_upper / batch});
+    int c = simt || work <= alone * 128 ? 1 : static_cast<int>(most);
+    for (; c >= 1; --c) {
+      const bool fills = !simt && 5 * static_cast<int64_t>(batch) * c >= 2 * di.sm_count;
+      if (work > (fills ? c * kPartTokens : c == 1 ? alone : 0) * 128) continue;
+      int fit = batch;
+      if (c > 1) {
+        e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &fit, c);
+        if (e != cudaSuccess) return e;
+      }
       if (fit < batch) continue;
       pl.cluster = c;
       break;

@@ -247,18 +247,18 @@ def test_the_fused_step_equals_the_separate_calls(dtype, hq, hkv, hd, gs, P):
 @pytest.mark.parametrize("max_ctas", [0, 5])    # clusters; even shares and the merge kernel
 def test_two_graphs_share_a_workspace_and_replay_with_new_inputs(max_ctas):
     """A captured step of each kind over one workspace, replayed in turn with other lengths, against fresh calls."""
-    c = Case("bf16", 16, 8, 128, 32, 16, [300, 300, 300], seed=31)
-    kn, vn = (torch.randn(3, 1024, device="cuda").bfloat16() for _ in range(2))
+    c = Case("bf16", 16, 8, 128, 32, 16, [300] * 21, seed=31)
+    kn, vn = (torch.randn(21, 1024, device="cuda").bfloat16() for _ in range(2))
     ws = c.ws(max_ctas)
     outs = [torch.zeros_like(c.q) for _ in range(2)]
-    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    slots = torch.zeros(21, dtype=torch.int64, device="cuda")
 
     def plain():
-        pa.pa_decode_q4(c.desc, 32, c.q, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx, c.scale, max_ctas, outs[0],
+        pa.pa_decode_q4(c.desc, 32, c.q, 21, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx, c.scale, max_ctas, outs[0],
                         ws)
 
     def step():
-        pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
+        pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 21, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
                                  c.scale, max_ctas, slots, outs[1], ws)
 
     plain()
@@ -272,7 +272,7 @@ def test_two_graphs_share_a_workspace_and_replay_with_new_inputs(max_ctas):
                 f()
             graphs.append(g)
     torch.cuda.synchronize()
-    for lens in ([300, 20, 150], [7, 0, 299], [1, 300, 17]):
+    for lens in ([300, 20, 150] * 7, [7, 0, 299] * 7, [1, 300, 17, 0, 33, 32, 256] * 3):
         c.ctx.copy_(torch.tensor(lens, dtype=torch.int32))
         c.q.copy_(torch.randn(c.q.shape, device="cuda"))
         live = torch.tensor([x > 0 for x in lens])
@@ -287,7 +287,7 @@ def test_two_graphs_share_a_workspace_and_replay_with_new_inputs(max_ctas):
         want0 = c.decode(max_ctas)
         assert torch.equal(outs[0].view(torch.uint8), want0.view(torch.uint8))
         want1 = torch.full_like(want0, 7.0)
-        pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 3, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
+        pa.pa_decode_kv_write_q4(c.desc, 32, c.q, kn, 1024, vn, 1024, 21, *c.cache, c.btd, c.maxp, c.ctx, c.max_ctx,
                                  c.scale, max_ctas, None, want1, c.ws(max_ctas))
         torch.cuda.synchronize()
         assert torch.equal(outs[1].view(torch.uint8), want1.view(torch.uint8))
@@ -352,15 +352,17 @@ def test_prefill_attends_to_the_read_back(hd):
     assert pa.pa_read_device_errors(reset=True) == 0
 
 
-@pytest.mark.parametrize("batch", [2, 5, 18, 19, 20, 25, 30, 37, 50, 76, 77, 152, 153])
-def test_requests_by_clusters_of_every_size(batch):
-    """Short requests take a cluster of CTAs each while these fit the GPU (8 CTAs down to 1 as the batch grows): lengths
-    below and above a cluster's CTAs, padding rows, a bad length and a bad page."""
+@pytest.mark.parametrize("batch,longest", [(2, 600), (5, 600), (8, 600), (18, 600), (19, 600), (20, 600), (25, 600),
+                                           (30, 600), (37, 600), (50, 600), (76, 500), (77, 256), (152, 256),
+                                           (153, 256), (6, 64)])
+def test_requests_by_clusters_of_every_size(batch, longest):
+    """Short requests take a cluster of CTAs each where these fit the GPU and fill a good part of it (8 CTAs down to 1 as
+    the batch grows): lengths below and above a cluster's CTAs, padding rows, a bad length and a bad page."""
     rng = np.random.default_rng(batch)
-    lens = rng.integers(1, 300, batch)
-    lens[0], lens[-1] = 600, 33
+    lens = rng.integers(1, longest // 2, batch)
+    lens[0], lens[-1] = longest, 33
     if batch > 4:
-        lens[1:4] = 0, 1, 257
+        lens[1:4] = 0, 1, longest // 2 + 1
     c = Case("bf16", 16, 8, 128, 64, 16, lens, seed=batch)
     ref = c.reference()
     c.check(c.decode(), ref)
@@ -390,7 +392,7 @@ def test_requests_by_clusters_of_every_size(batch):
 def test_the_fused_step_by_clusters_and_by_even_shares(hq, hkv, hd, gs):
     """The new token's row written by the cluster's last CTA, and by one CTA of an even split: the same bytes and the
     output of the separate calls."""
-    lens = [1, 2, 33, 300, 0, 257, 64]
+    lens = [1, 2, 33, 300, 0, 257, 64] * 3
     for max_ctas in (0, 3):
         c = Case("bf16", hq, hkv, hd, gs, 16, lens, seed=3)
         B = len(lens)
@@ -417,19 +419,20 @@ def test_the_fused_step_by_clusters_and_by_even_shares(hq, hkv, hd, gs):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_key_that_is_not_a_number_makes_its_heads_outputs_nan_however_they_are_split(dtype):
-    c = Case(dtype, 8, 4, 128, 32, 16, [900, 700], seed=6)
+    c = Case(dtype, 8, 4, 128, 32, 16, [900, 700] * 12, seed=6)
     ref = c.reference()
     slot = int(c.bt[0, 20]) * 16 + 3
     u, s, p = q4.unpack_rows(c.cache[0][slot].cpu().numpy()[None], [slot], 4, 128, 32)
     s[0, 2, 1], p[0, 2, 1] = 0, np.float16(np.nan)
     c.cache[0][slot] = torch.from_numpy(q4.pack_rows(u, s, p, [slot])[0]).cuda()
-    want = torch.zeros(2, 8, 128, dtype=torch.bool)
+    want = torch.zeros(24, 8, 128, dtype=torch.bool)
     want[0, 4:6] = True                         # the two q-heads of kv-head 2
-    for max_ctas in (0, 1, 2, 9):
+    for max_ctas in (0, 1, 24, 61):
         out = c.decode(max_ctas)
         assert torch.equal(torch.isnan(out).cpu(), want)
         ok = ~want.numpy()
-        assert np.abs(out.double().cpu().numpy() - ref)[ok].max() <= (1e-5 if dtype == "f32" else 1e-2) * np.abs(ref).max()
+        err = np.abs(out.double().cpu().numpy() - ref)[ok].max()
+        assert err <= (1e-5 if dtype == "f32" else 1e-2) * np.abs(ref).max()
 
 
 @pytest.mark.parametrize("gs", [32, 64, 128])
@@ -437,7 +440,7 @@ def test_a_key_that_is_not_a_number_makes_its_heads_outputs_nan_however_they_are
 def test_scales_that_change_along_the_context(gs, order):
     """V's magnitude rises or falls by 2^40 along the context, or is 2^20 times the others' in one token that no query
     looks at: the powers of two that keep p s in float16's range follow the largest scale."""
-    c = Case("bf16", 4, 4, 128, gs, 16, [700, 90], seed=8)
+    c = Case("bf16", 4, 4, 128, gs, 16, [700, 90] * 8, seed=8)
     rng = np.random.default_rng(1)
     for b, L in enumerate(c.lens):
         slots = c.bt[b, np.arange(L) // 16].astype(np.int64) * 16 + np.arange(L) % 16
@@ -463,7 +466,7 @@ def test_scales_that_change_along_the_context(gs, order):
 
 def test_two_streams_at_once_and_the_same_bits_every_time():
     """A clustered and a split decode, each on a stream and a workspace of its own, over and over side by side."""
-    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0], seed=21)
+    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0] * 4, seed=21)
     b = Case("bf16", 24, 4, 128, 32, 16, [3000, 5, 641], seed=22)
     wa, wb = a.decode(), b.decode(60)
     a.check(wa)
@@ -473,7 +476,7 @@ def test_two_streams_at_once_and_the_same_bits_every_time():
     outs = [[torch.full_like(x.q, 7.0) for _ in range(40)] for x in (a, b)]
     torch.cuda.synchronize()
     for i in range(40):
-        pa.pa_decode_q4(a.desc, a.gs, a.q, 4, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, outs[0][i], ws[0],
+        pa.pa_decode_q4(a.desc, a.gs, a.q, 16, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, outs[0][i], ws[0],
                         stream=sa)
         pa.pa_decode_q4(b.desc, b.gs, b.q, 3, *b.cache, b.btd, b.maxp, b.ctx, b.max_ctx, b.scale, 60, outs[1][i], ws[1],
                         stream=sb)
@@ -482,7 +485,7 @@ def test_two_streams_at_once_and_the_same_bits_every_time():
 
 
 def test_a_fork_and_join_in_one_graph():
-    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0], seed=21)
+    a = Case("bf16", 16, 8, 128, 64, 16, [300, 17, 1000, 0] * 4, seed=21)
     b = Case("f32", 8, 4, 64, 32, 16, [3000, 5, 641], seed=22)
     wa, wb = a.decode(), b.decode()
     oa, ob, ws = torch.full_like(a.q, 7.0), torch.full_like(b.q, 7.0), [a.ws(), b.ws()]
@@ -492,7 +495,7 @@ def test_a_fork_and_join_in_one_graph():
     with torch.cuda.graph(g):
         main = torch.cuda.current_stream()
         side.wait_stream(main)
-        pa.pa_decode_q4(a.desc, a.gs, a.q, 4, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, oa, ws[0])
+        pa.pa_decode_q4(a.desc, a.gs, a.q, 16, *a.cache, a.btd, a.maxp, a.ctx, a.max_ctx, a.scale, 0, oa, ws[0])
         pa.pa_decode_q4(b.desc, b.gs, b.q, 3, *b.cache, b.btd, b.maxp, b.ctx, b.max_ctx, b.scale, 0, ob, ws[1],
                         stream=side)
         main.wait_stream(side)
