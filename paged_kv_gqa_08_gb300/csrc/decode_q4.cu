@@ -10,17 +10,17 @@
 //
 // Bound by HBM at its floor.  Measured (16-bit queries, 8 kv-heads of 128 dims; the
 // call with its merge, replayed from a graph): 256 requests of 128-2048 tokens,
-// groups of 32, 71.0 us for 347 MB; 64 of 1024-8192, groups of 64, 69.0 us for
-// 355 MB; 8 of 32768, groups of 128, 58.1 us for 285 MB: 4.9 to 5.1 TB/s of a
-// copy's 6.7.  The copies alone take 65.5, 65.2 and 54.8 us, of which the start
-// (plan, page look-up, first chunk) 6 to 7 and the merge 4 to 6.
+// groups of 32, 70.7 us for 347 MB; 64 of 1024-8192, groups of 64, 66.2 us for
+// 355 MB; 8 of 32768, groups of 128, 55.9 us for 285 MB: 4.9 to 5.4 TB/s of a
+// copy's 6.7.  Of these the start (plan, page look-up, first chunk) takes 6 to 7
+// and the merge 2 to 4 us.
 #include "decode_shared.cuh"
 #include "q4_common.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kTok = 32;        // tokens per chunk
+constexpr int kTok = 32;        // tokens per chunk (fp32: 16)
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
 constexpr int kMaxCluster = 8;  // CTAs of a cluster that shares a request, at most
@@ -850,7 +850,7 @@ PA_DEVINL int plan_in_warp(const KParams& k, int32_t* cs_s, bool first, int lane
     const int L = k.ctx[b];
     int cnt = 0;
     if (L >= 1 && L <= cap) {
-      cnt = (L + kTok - 1) / kTok;
+      cnt = (L + (1 << k.log2T) - 1) >> k.log2T;
     } else if (first) {
       // length 0 is a padding row: nothing is read, stored or written for it
       if (L != 0) raise_flag(k.err, PA_DEVERR_BAD_LENGTH);
@@ -919,13 +919,13 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
     if (lane < nvalid) {
       while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
       const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
-      const int t0 = (x - cb0) * kTok;
+      const int t0 = (x - cb0) << k.log2T;
       const int left = k.ctx[my_b] - t0;
       const int32_t* bt = k.bt + static_cast<int64_t>(my_b) * k.maxp;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int th = t0 + hf * kHalf, nh = min(kHalf, left - hf * kHalf);
-        if (nh <= 0) continue;
+        if (nh <= 0 || hf >= 1 << k.log2T >> 4) continue;
         const int page = bt[th >> k.log2P];
         if (page < 0 || page >= k.num_pages) {
           raise_flag(k.err, PA_DEVERR_BAD_PAGE);
@@ -1171,9 +1171,12 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   const int G = d.num_q_heads / d.num_kv_heads;
   DecodePlan pl;
   pl.nw = d.num_kv_heads * q4_groups(d);  // consumer warps
-  pl.tokens_per_chunk = kTok;
+  // fp32's CUDA cores are slow enough for 16 tokens to be a chunk: short requests
+  // then spread over twice the CTAs (one of 5-64 tokens, 16 q-heads over 8 of 128
+  // dims: 10.7 -> 8.5 us; long batches within 5%)
+  pl.tokens_per_chunk = d.dtype == PA_BF16 ? kTok : kHalf;
   pl.row_pitch = q4_row_bytes(d, gs);
-  pl.chunk_bytes = kTok * pl.row_pitch;
+  pl.chunk_bytes = pl.tokens_per_chunk * pl.row_pitch;
   // behind the ring: barriers, chunk descriptors, the batch's prefix sums, and
   // what the CUDA-core consumer (fp32) keeps in shared memory
   const bool simt = d.dtype != PA_BF16;
@@ -1206,7 +1209,8 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   int occ = 0;
   e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
   if (e != cudaSuccess) return e;
-  const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + kTok - 1) / kTok);
+  const int T = pl.tokens_per_chunk;
+  const int64_t chunks_upper = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_ctx) + T - 1) / T);
   int64_t n = static_cast<int64_t>(occ) * di.sm_count;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
   // Short requests that fit the GPU at once: a CTA or a cluster each and no merge
@@ -1216,7 +1220,7 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // 16.0 (17.5), 100 of 64-256 by one CTA each 15.0 (18.4), 4 of 5-64 7.6 (8.6).
   // Longer parts: 64 of 300-2000 33.8 (27.2).  Too few: 2 of 1000 by 8 12.1 (9.0),
   // 4 of 256 by one 12.3 (8.8).  fp32's CUDA cores take a chunk four to eight
-  // times as long: 4 of 5-64 tokens of 64 dims 7.6 (8.0), of 128 dims 13.4 (11.3).
+  // times as long: 4 of 256 tokens of 64 dims by one 18.9 (8.0).
   if (batch >= 1 && batch <= kInlinePlanMax && n >= batch) {
     const int64_t work = static_cast<int64_t>(max_ctx) * d.head_dim;
     const int alone = simt ? kAloneTokensF32 : kAloneTokens;
