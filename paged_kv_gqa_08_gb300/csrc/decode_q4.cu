@@ -20,14 +20,14 @@
 namespace pa {
 namespace {
 
-constexpr int kTok = 32;        // tokens per chunk (fp32: 16)
+constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
 constexpr int kMaxCluster = 8;  // CTAs of a cluster that shares a request, at most
 // Tokens of 128 dims (of 64 twice as many) of a request that a CTA takes, alone or
 // with its cluster, where a CTA or a cluster per request comes to at least 2/5 of
-// the SMs; that a CTA alone takes in any batch; and that in fp32.
-constexpr int kPartTokens = 256, kAloneTokens = 64, kAloneTokensF32 = 32;
+// the SMs; and that a CTA alone takes in any batch.
+constexpr int kPartTokens = 256, kAloneTokens = 64;
 
 // A chunk in the ring, as the producer describes it to the consumers: its
 // request; the tokens of its halves (n0 | n1 << 8, 0 for a half whose page is
@@ -51,7 +51,6 @@ struct Q4Params {
   uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, or a CTA to its cluster
   int32_t codes, pars;  // bytes of the two parts of a row
   int32_t log2gs;
-  uint32_t off_q;       // [Hkv][GP][HD] fp32: the request's scaled queries (CUDA-core consumer)
 };
 
 // The row of a 4-bit cache.
@@ -120,195 +119,7 @@ PA_DEVINL void write_new_row(const Q4Params& p, unsigned char* kst, unsigned cha
 PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : INFINITY; }
 
 // ---------------------------------------------------------------------------
-// CUDA-core consumer: GP = the group's q-heads rounded up to a power of two.
-// Scores: lane (gq, tq) takes tokens gq and gq + 8 and a quarter of the dims.
-// Products with V: a lane takes HD / 32 dims of every token.
-// ---------------------------------------------------------------------------
-template <typename T, int HD, int GP>
-PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* full, uint64_t* empty, const int4* meta,
-                             volatile int* abort_flag) {
-  constexpr int QD = HD / 4;
-  constexpr int EL = HD / 32;
-  constexpr int NH = GP > 4 ? 2 : 1;  // heads whose softmax a lane keeps
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = warp, G = p.k.Hq / p.k.Hkv;
-  const int gq = lane >> 2, tq = lane & 3;
-  const int R = p.k.row_bytes, NG = HD >> p.log2gs;
-  float* qs = reinterpret_cast<float*>(smem + p.off_q) + warp * GP * HD;
-  float* p_tile = reinterpret_cast<float*>(smem + p.k.off_p) + warp * kHalf * GP;
-  float* alpha_s = reinterpret_cast<float*>(smem + p.k.off_alpha) + warp * 8;
-  float* ml_s = reinterpret_cast<float*>(smem + p.k.off_ml) + warp * 16;
-  float o[GP][EL];
-  float m_run[NH], l_part[NH];
-  for (Ring ring;; ring.next(p.stages)) {
-    const int s = ring.s;
-    if (!mbar_wait_bounded(&full[s], ring.phase, abort_flag, p.k.err)) break;
-    const int4 md = meta[s];
-    const uint32_t flags = md.y;
-    if (flags & kEnd) break;
-    const int b = md.x, n0 = flags & 255, n1 = (flags >> 8) & 255;
-    unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
-    unsigned char* vst = kst + p.k.chunk_bytes;
-    if (flags & kFirst) {
-      const T* qb = reinterpret_cast<const T*>(kst + 2 * p.k.chunk_bytes) + h * G * HD;
-      __syncwarp();
-      for (int i = lane; i < GP * HD; i += 32)
-        qs[i] = i < G * HD ? static_cast<float>(qb[i]) * p.k.scale_log2 : 0.f;
-      __syncwarp();
-#pragma unroll
-      for (int g = 0; g < GP; ++g)
-#pragma unroll
-        for (int e = 0; e < EL; ++e) o[g][e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        m_run[j] = -INFINITY;
-        l_part[j] = 0.f;
-      }
-    }
-    if (flags & kNew) write_new_row<T, HD>(p, kst, vst, b, n1 ? kHalf + n1 - 1 : n0 - 1, md.w, h, lane);
-
-    for (int hf = 0; hf < 2; ++hf, kst += kHalf * R, vst += kHalf * R) {
-    const int n = hf ? n1 : n0;
-    if (n == 0) continue;
-    float acc[GP][2];
-#pragma unroll
-    for (int g = 0; g < GP; ++g) acc[g][0] = acc[g][1] = 0.f;
-    float2 sc[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int t = gq + 8 * u;
-      sc[u] = q4_sc(*reinterpret_cast<const uint32_t*>(
-          kst + t * R + p.codes + q4_swz((h * NG + ((tq * QD) >> p.log2gs)) * 4, p.pars, t)));
-    }
-#pragma unroll
-    for (int c8 = 0; c8 < QD / 8; ++c8) {
-      float xk[2][8];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = gq + 8 * u;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-            kst + t * R + q4_swz(h * (HD / 2) + tq * (QD / 2) + c8 * 4, p.codes, t));
-        q4_decode8(w, sc[u].x, sc[u].y, xk[u]);
-      }
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float4 qa = *reinterpret_cast<const float4*>(qs + g * HD + tq * QD + c8 * 8);
-        const float4 qb = *reinterpret_cast<const float4*>(qs + g * HD + tq * QD + c8 * 8 + 4);
-        const float qv[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          acc[g][0] = fmaf(qv[e], xk[0][e], acc[g][0]);
-          acc[g][1] = fmaf(qv[e], xk[1][e], acc[g][1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < GP; ++g)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        acc[g][u] += __shfl_xor_sync(0xffffffffu, acc[g][u], 1);
-        acc[g][u] += __shfl_xor_sync(0xffffffffu, acc[g][u], 2);
-      }
-    // online softmax (base 2): lane tq keeps heads tq and tq + 4
-#pragma unroll
-    for (int j = 0; j < NH; ++j) {
-      const int g = tq + 4 * j;
-      float v0 = acc[4 * j][0], v1 = acc[4 * j][1];
-#pragma unroll
-      for (int k = 1; k < 4; ++k)
-        if (4 * j + k < GP && tq == k) {
-          v0 = acc[(4 * j + k) % GP][0];
-          v1 = acc[(4 * j + k) % GP][1];
-        }
-      v0 = gq < n ? v0 : -INFINITY;
-      v1 = gq + 8 < n ? v1 : -INFINITY;
-      float mx = fmaxf(v0, v1);
-#pragma unroll
-      for (int m = 4; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-      const float m_new = fmaxf(m_run[j], mx);
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2f(m_run[j] - m_use);
-      const float p0 = exp2f(v0 - m_use), p1 = exp2f(v1 - m_use);
-      l_part[j] = l_part[j] * alpha + (p0 + p1);
-      m_run[j] = m_new;
-      if (g < GP) {
-        p_tile[gq * GP + g] = p0;
-        p_tile[(gq + 8) * GP + g] = p1;
-        if (gq == 0) alpha_s[g] = alpha;
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int g = 0; g < GP; ++g) {
-      const float al = alpha_s[g];
-#pragma unroll
-      for (int e = 0; e < EL; ++e) o[g][e] *= al;
-    }
-    for (int t = 0; t < n; ++t) {
-      const float2 scv = q4_sc(*reinterpret_cast<const uint32_t*>(
-          vst + t * R + p.codes + q4_swz((h * NG + ((lane * EL) >> p.log2gs)) * 4, p.pars, t)));
-      const uint32_t hw = *reinterpret_cast<const uint16_t*>(
-          vst + t * R + q4_swz(h * (HD / 2) + (lane * EL / 4) * 2, p.codes, t));
-      float a[8];
-      q4_decode8(hw, scv.x, scv.y, a);
-      float xv[EL];
-      if constexpr (EL == 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xv[e] = a[e];
-      } else {
-        xv[0] = (lane & 1) ? a[2] : a[0];
-        xv[1] = (lane & 1) ? a[3] : a[1];
-      }
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float pv = p_tile[t * GP + g];
-#pragma unroll
-        for (int e = 0; e < EL; ++e) o[g][e] = fmaf(pv, xv[e], o[g][e]);
-      }
-    }
-    __syncwarp();
-    }
-    if (lane == 0) mbar_arrive(&empty[s]);
-
-    if (flags & kLast) {  // write the result
-#pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        float l = l_part[j];
-#pragma unroll
-        for (int m = 4; m < 32; m <<= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
-        if (gq == 0 && tq + 4 * j < GP) {
-          ml_s[2 * (tq + 4 * j)] = m_run[j];
-          ml_s[2 * (tq + 4 * j) + 1] = l;
-        }
-      }
-      __syncwarp();
-      const bool whole = (flags & kWhole) != 0;
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        if (g < G) {
-          const float mg = ml_s[2 * g], lg = ml_s[2 * g + 1];
-          const float inv = lg > 0.f ? 1.f / lg : 0.f;
-          const int hq = h * G + g;
-          if (whole) {
-            T* dst = reinterpret_cast<T*>(p.k.out) + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD + lane * EL;
-#pragma unroll
-            for (int e = 0; e < EL; ++e) dst[e] = static_cast<T>(o[g][e] * inv);
-          } else {
-            const int64_t slot = static_cast<int64_t>(md.z) + b;
-            float* dst = p.k.o_part + (slot * p.k.Hq + hq) * HD + lane * EL;
-#pragma unroll
-            for (int e = 0; e < EL; ++e) dst[e] = o[g][e] * inv;
-            if (lane == 0) p.k.lse_part[slot * p.k.Hq + hq] = partial_lse(mg, lg);
-          }
-        }
-      }
-      __syncwarp();
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Tensor-core consumer (bf16 queries and outputs, groups of up to 8 q-heads).
+// Consumer (groups of up to 8 q-heads).
 //
 // Per chunk, S^T = K Q^T and O^T += V^T P^T as mma.sync m16n8k16 (float16 in,
 // fp32 out): 16 tokens, then 16 of the head's dims, are the rows, and the
@@ -338,6 +149,11 @@ PA_DEVINL void simt_consumer(const Q4Params& p, unsigned char* smem, uint64_t* f
 // 16 tokens of a head take 197 instructions with groups of 128, 109 of them on
 // the integer pipe (two cycles each); 309 with K and V decoded to float16 in
 // registers, 228 with raw codes loaded as words and paired by byte permutes.
+//
+// fp32 queries and outputs: queries, p s and p as two float16 numbers each, the
+// rounded value and what it lacks (22 bits in all), so twice the products; those of
+// O are added up in fp32 every 16 tokens (a tensor core's additions cut off).  One
+// consumer group, whose warps may have 168 registers.
 //
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
 // [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
@@ -435,9 +251,6 @@ PA_DEVINL uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
-PA_DEVINL void lds128(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
 // N consecutive words.
 template <int N>
 PA_DEVINL void lds_words(uint32_t* r, uint32_t a) {
@@ -464,11 +277,18 @@ PA_DEVINL void ldsm4_trans(uint32_t (&r)[4], uint32_t a) {
                : "r"(a));
 }
 
-template <int HD, int NG, int HKV>
-PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int group) {
+// Two numbers as float16 numbers, and what these lack.
+PA_DEVINL void split_f16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2(x, y);
+  lo = pack_f16x2(x - f16_lo(hi), y - f16_lo(hi >> 16));
+}
+
+template <typename T, int HD, int NG, int HKV>
+PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group) {
   constexpr int NP = HD / 32;          // pieces of a head's codes in a row: 32 dims each
   constexpr int PG = NP / NG;          // of them, a group's
   constexpr int MB = HD / 16;          // 16-dim blocks of O: two to a piece
+  constexpr bool kF32 = sizeof(T) == 4;
   using Row = Q4Row<HD, NG, HKV>;
   constexpr uint32_t R = Row::kBytes, kChunk = kTok * R;
   const int lane = threadIdx.x & 31;
@@ -496,7 +316,9 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
   auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, smem0 + p.k.off_abort, p.k.err); };
 
   uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
-  uint32_t qm = 0u;    // 2^-10 (16 sum q, sum q) over the dims of group tq
+  uint32_t qm = 0u;    // 2^-10 (16 sum q, sum q) over the dims of group tq; fp32: 2^-2, with ...
+  [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // what qf lacks
+  [[maybe_unused]] uint32_t qm_lo = 0u;            // what qm lacks (up to two groups: with the lanes tq + 2 or tq + 1)
   float o[MB][4];
   // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
   // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
@@ -510,7 +332,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
   uint32_t hand_phase = 0;     // parity of the handovers so far
   Ring ring;
   if (group) ring.next(p.stages);  // group g takes stages g, g + 2, ... of the ring
-  for (;; ring.next2(p.stages)) {
+  for (;; kF32 ? ring.next(p.stages) : ring.next2(p.stages)) {
     const int s = ring.s;
     if (!wait(full(s), ring.phase)) break;
     const uint32_t md = smem0 + p.k.off_meta + s * 16;  // {request, tokens and flags, share, slot}
@@ -520,17 +342,28 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
     if (flags & (kFirst | kNew | kEnd)) {
       if (flags & kEnd) break;
       if (flags & kFirst) {
-        const uint32_t qrow = st + 2 * kChunk + (h * G + gq) * HD * 2;
-        uint32_t qw[NP][4];  // bf16 pairs: eight dims of each piece
+        const uint32_t qrow = st + 2 * kChunk + (h * G + gq) * HD * sizeof(T);
+        float qv[NP][8];  // eight dims of each piece
         float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          qw[i][0] = qw[i][1] = qw[i][2] = qw[i][3] = 0u;
-          if (gq < G) lds128(qw[i], qrow + (i * 32 + tq * 8) * 2);
+          uint32_t w[8] = {};
+          const uint32_t at = qrow + (i * 32 + tq * 8) * sizeof(T);
+          if (gq < G) {
+            lds_words<4>(w, at);
+            if constexpr (kF32) lds_words<4>(w + 4, at + 16);
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = bf16x2_to_float2(qw[i][e]);
-            mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+          for (int e = 0; e < 8; e += 2) {
+            if constexpr (kF32) {
+              qv[i][e] = __uint_as_float(w[e]);
+              qv[i][e + 1] = __uint_as_float(w[e + 1]);
+            } else {
+              const float2 v = bf16x2_to_float2(w[e / 2]);
+              qv[i][e] = v.x;
+              qv[i][e + 1] = v.y;
+            }
+            mx = fmaxf(mx, fmaxf(fabsf(qv[i][e]), fabsf(qv[i][e + 1])));
           }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -538,34 +371,47 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
         // 2^-E of the largest magnitude's exponent E, and 2^E
         const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
         const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
-        qm = 0u;
+        qm = qm_lo = 0u;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float sum = 0.f;
 #pragma unroll
           for (int i = g * PG; i < (g + 1) * PG; ++i) {
-            float q[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 v = bf16x2_to_float2(qw[i][e]);
-              q[2 * e] = v.x * down * 256.f;
-              q[2 * e + 1] = v.y * down * 256.f;
-            }
+            float (&q)[8] = qv[i];
+            [[maybe_unused]] float l[8];
             // as they are rounded: the second term's sum has to be that of the first's queries
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              q[e] = __half2float(__float2half_rn(q[e]));
+              const float x = q[e] * down * 256.f;
+              q[e] = __half2float(__float2half_rn(x));
               sum += q[e];
+              if constexpr (kF32) {
+                l[e] = __half2float(__float2half_rn(x - q[e]));
+                sum += l[e];
+              }
             }
             qf[2 * i][0] = pack_f16x2(q[0], q[4]);
             qf[2 * i][1] = pack_f16x2(q[1], q[5]);
             qf[2 * i + 1][0] = pack_f16x2(q[2] * 16.f, q[6] * 16.f);
             qf[2 * i + 1][1] = pack_f16x2(q[3] * 16.f, q[7] * 16.f);
+            if constexpr (kF32) {
+              ql[2 * i][0] = pack_f16x2(l[0], l[4]);
+              ql[2 * i][1] = pack_f16x2(l[1], l[5]);
+              ql[2 * i + 1][0] = pack_f16x2(l[2] * 16.f, l[6] * 16.f);
+              ql[2 * i + 1][1] = pack_f16x2(l[3] * 16.f, l[7] * 16.f);
+            }
           }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
-          if (tq == g) qm = pack_f16x2(r * 16.f, r);
+          if constexpr (kF32) {
+            const float r = sum * 0x1p-10f, rh = __half2float(__float2half_rn(r));
+            const float rl = __half2float(__float2half_rn(r - rh));
+            if (tq == g) qm = pack_f16x2(rh * 16.f, rh);
+            if (NG == 4 ? tq == g : tq == g + NG) (NG == 4 ? qm_lo : qm) = pack_f16x2(rl * 16.f, rl);
+          } else {
+            const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
+            if (tq == g) qm = pack_f16x2(r * 16.f, r);
+          }
         }
         mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
         mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
@@ -581,7 +427,7 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
       if (flags & kNew) {
         unsigned char* kst = smem + static_cast<size_t>(s) * p.stage_bytes;
         const uint32_t n0 = flags & 255, n1 = (flags >> 8) & 255;
-        write_new_row<__nv_bfloat16, HD>(p, kst, kst + kChunk, lds32(md), n1 ? kHalf + n1 - 1 : n0 - 1,
+        write_new_row<T, HD>(p, kst, kst + kChunk, lds32(md), n1 ? kHalf + n1 - 1 : n0 - 1,
                                          lds32(md + 12), h, lane);
       }
     }
@@ -602,6 +448,15 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
       }
       float sc[4], d[4];
       mma_f16_k8(sc, pm[0], pm[1], qm);
+      if constexpr (kF32) {
+        if constexpr (NG == 4) {
+          mma_f16_k8(d, pm[0], pm[1], qm_lo);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[e] += d[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] *= 0x1p-8f;
+      }
       uint32_t w[4];  // of two pieces: the words of tokens gq and gq + 8
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -609,6 +464,10 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
         const uint32_t w0 = i % 2 == 0 ? w[0] : w[2], w1 = i % 2 == 0 ? w[1] : w[3];
         const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
         if (i % PG == 0) d[0] = d[1] = d[2] = d[3] = 0.f;
+        if constexpr (kF32) {
+          mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), ql[2 * i][0], ql[2 * i][1]);
+          mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), ql[2 * i + 1][0], ql[2 * i + 1][1]);
+        }
         mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), qf[2 * i][0], qf[2 * i][1]);
         mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), qf[2 * i + 1][0], qf[2 * i + 1][1]);
         if (i % PG == PG - 1) {
@@ -672,12 +531,25 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
       limit = 8.f;
     }
     uint32_t pb[2][2];  // B fragments of the probabilities
+    [[maybe_unused]] uint32_t pl[2][2];  // fp32: of what these lack (t: the probabilities)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const float p0 = ex2_approx(t[hf][0]), p1 = ex2_approx(t[hf][1]);
       const float p2 = ex2_approx(t[hf][2]), p3 = ex2_approx(t[hf][3]);
-      pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
-      pb[hf][1] = movm_trans(pack_f16x2(p2, p3));
+      if constexpr (kF32) {
+        uint32_t hi[2], lo[2];
+        split_f16x2(p0, p1, hi[0], lo[0]);
+        split_f16x2(p2, p3, hi[1], lo[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          pb[hf][u] = movm_trans(hi[u]);
+          pl[hf][u] = movm_trans(lo[u]);
+        }
+        t[hf][0] = p0, t[hf][1] = p1, t[hf][2] = p2, t[hf][3] = p3;
+      } else {
+        pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
+        pb[hf][1] = movm_trans(pack_f16x2(p2, p3));
+      }
     }
 
     // O^T += V^T P^T
@@ -709,21 +581,58 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
     const uint32_t s_scale = 36u * kExponent - max(s_most & 0x7C007C00u, 6u * kExponent);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
+      [[maybe_unused]] float s_of[2][NG];  // fp32: 2^-E s of tokens gq and gq + 8
+      if constexpr (kF32) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(d, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pl[hf][0], pl[hf][1]);
+        mma_f16(d, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) om[e] += d[e];
+        const float scale = __uint_as_float((127u + 21 - max(s_most >> 26, 6u)) << 23);
+        const int n = static_cast<int>((flags >> (8 * hf)) & 255);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t par[NG];
+          lds_words<NG>(par, st + kChunk + (hf * kHalf + u * 8) * R + kp_at);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) s_of[u][g] = gq + u * 8 < n ? f16_lo(par[g]) * scale : 0.f;
+        }
+      } else {
+        mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
+      }
       uint32_t x[4];  // of two pieces: half word gq of tokens 2 tq, 2 tq + 1 and of those 8 on
       uint32_t b0, b1;
+      [[maybe_unused]] uint32_t l0, l1;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (i % 2 == 0) ldsm4_trans(x, st + kChunk + hf * kHalf * R + c_at[i / 2]);
-        if (i % PG == 0) {  // p s of the group
+        if (i % PG == 0 && kF32) {  // p s of the group
+          const float s0 = s_of[0][i / PG], s1 = s_of[1][i / PG];
+          split_f16x2(t[hf][0] * s0, t[hf][1] * s0, b0, l0);
+          split_f16x2(t[hf][2] * s1, t[hf][3] * s1, b1, l1);
+          b0 = movm_trans(b0), b1 = movm_trans(b1), l0 = movm_trans(l0), l1 = movm_trans(l1);
+        } else if (i % PG == 0) {
           const int from = s_lane + i / PG * 8;
           b0 = mul_f16x2(pb[hf][0], mul_f16x2(__shfl_sync(0xffffffffu, vm[2 * hf], from), s_scale));
           b1 = mul_f16x2(pb[hf][1], mul_f16x2(__shfl_sync(0xffffffffu, vm[2 * hf + 1], from), s_scale));
         }
         const uint32_t x0 = i % 2 == 0 ? x[0] : x[2], x1 = i % 2 == 0 ? x[1] : x[3];
         const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
-        mma_f16(o[2 * i], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
-        mma_f16(o[2 * i + 1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
+        if constexpr (kF32) {
+          float d[2][4] = {};
+          mma_f16(d[0], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), l0, l1);
+          mma_f16(d[0], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
+          mma_f16(d[1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), l0, l1);
+          mma_f16(d[1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * i][e] += d[0][e];
+            o[2 * i + 1][e] += d[1][e];
+          }
+        } else {
+          mma_f16(o[2 * i], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
+          mma_f16(o[2 * i + 1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
+        }
       }
     }
     uint32_t b = 0, share = 0;
@@ -805,12 +714,17 @@ PA_DEVINL void mma_consumer(const Q4Params& p, unsigned char* smem, int h, int g
           const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
           const int hq = h * G + g;
           if (flags & kWhole) {
-            char* dst = p.k.out + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD * 2;
+            char* dst = p.k.out + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD * sizeof(T);
 #pragma unroll
-            for (int j = 0; j < MB; j += 2)
-              *reinterpret_cast<uint2*>(dst + (j * 16 + gq * 4) * 2) =
-                  make_uint2(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
-                             pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv));
+            for (int j = 0; j < MB; j += 2) {
+              char* at = dst + (j * 16 + gq * 4) * sizeof(T);
+              if constexpr (kF32)
+                *reinterpret_cast<float4*>(at) =
+                    make_float4(o[j][e] * inv, o[j][2 + e] * inv, o[j + 1][e] * inv, o[j + 1][2 + e] * inv);
+              else
+                *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(o[j][e] * inv, o[j][2 + e] * inv),
+                                                           pack_bf16x2(o[j + 1][e] * inv, o[j + 1][2 + e] * inv));
+            }
           } else {
             // a partial result: for the merge kernel, or (generic addresses) for the cluster
             const int64_t part = (static_cast<int64_t>(share) + b) * p.k.Hq + hq;
@@ -850,7 +764,7 @@ PA_DEVINL int plan_in_warp(const KParams& k, int32_t* cs_s, bool first, int lane
     const int L = k.ctx[b];
     int cnt = 0;
     if (L >= 1 && L <= cap) {
-      cnt = (L + (1 << k.log2T) - 1) >> k.log2T;
+      cnt = (L + kTok - 1) / kTok;
     } else if (first) {
       // length 0 is a padding row: nothing is read, stored or written for it
       if (L != 0) raise_flag(k.err, PA_DEVERR_BAD_LENGTH);
@@ -919,13 +833,13 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
     if (lane < nvalid) {
       while (my_b < k.B - 1 && cs[my_b + 1] <= x) ++my_b;
       const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
-      const int t0 = (x - cb0) << k.log2T;
+      const int t0 = (x - cb0) * kTok;
       const int left = k.ctx[my_b] - t0;
       const int32_t* bt = k.bt + static_cast<int64_t>(my_b) * k.maxp;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int th = t0 + hf * kHalf, nh = min(kHalf, left - hf * kHalf);
-        if (nh <= 0 || hf >= 1 << k.log2T >> 4) continue;
+        if (nh <= 0) continue;
         const int page = bt[th >> k.log2P];
         if (page < 0 || page >= k.num_pages) {
           raise_flag(k.err, PA_DEVERR_BAD_PAGE);
@@ -1014,7 +928,7 @@ PA_DEVINL uint32_t peer_addr(uint32_t a, int rank) {
   return r;
 }
 
-template <int HD>
+template <typename T, int HD>
 PA_DEVINL void cluster_merge(const Q4Params& p, unsigned char* smem, int warp, int lane) {
   constexpr int EL = HD / 32;
   cluster_sync();  // every part is in its place
@@ -1057,22 +971,25 @@ PA_DEVINL void cluster_merge(const Q4Params& p, unsigned char* smem, int warp, i
 #pragma unroll
           for (int e = 0; e < EL; ++e) acc[e] = fmaf(wr, v[r][e], acc[e]);
       }
-      char* dst = p.k.out + ((static_cast<int64_t>(b) * p.k.Hq + hq) * HD + lane * EL) * 2;
+      T* dst = reinterpret_cast<T*>(p.k.out) + (static_cast<int64_t>(b) * p.k.Hq + hq) * HD + lane * EL;
 #pragma unroll
-      for (int e = 0; e < EL; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e * 2) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      for (int e = 0; e < EL; e += 2) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float2*>(dst + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+        else
+          *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      }
     }
   }
   cluster_sync();  // no CTA leaves while its part is read
 }
 
 // bf16: two groups of one consumer warp per kv-head, which take the chunks in
-// turn from one ring, and the producer; fp32: one group.
-// V: of fp32, the group's q-heads rounded up to a power of two; of bf16, the
-// groups of a head row, for HKV kv-heads (a row's layout in the instructions:
-// 27 address additions a chunk less).
-template <typename T, int HD, int V, int HKV>
-__global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) == 2 ? 1 : 2)
+// turn from one ring, and the producer; fp32: one group.  NG: the groups of a
+// head's row, HKV: kv-heads (a row's layout in the instructions: 27 address
+// additions a chunk less).
+template <typename T, int HD, int NG, int HKV>
+__global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, 1)
     decode_q4_kernel(const Q4Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const KParams& k = p.k;
@@ -1084,7 +1001,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) =
   uint64_t* taken = handed + 8;           // [8] it has been added
   int4* meta = reinterpret_cast<int4*>(smem + k.off_meta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + k.off_abort);
-  if (sizeof(T) == 2 && p.cluster > 1)
+  if (p.cluster > 1)
     for (int hq = threadIdx.x; hq < k.Hq; hq += blockDim.x)
       *reinterpret_cast<float*>(smem + p.off_hand + (hq * (HD + 4) + HD) * 4) = -INFINITY;
   if (threadIdx.x == 0) {
@@ -1104,16 +1021,12 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? 17 * 32 : 9 * 32, sizeof(T) =
 
   if (warp == NW * p.groups) {
     produce(p, smem, full, empty, meta, abort_flag, lane);
-  } else if constexpr (sizeof(T) == 2) {
-    const int group = warp >= NW;
-    mma_consumer<HD, V, HKV>(p, smem, warp - group * NW, group);
   } else {
-    simt_consumer<T, HD, V>(p, smem, full, empty, meta, abort_flag);
+    const int group = warp >= NW;
+    consume<T, HD, NG, HKV>(p, smem, warp - group * NW, group);
   }
-  if constexpr (sizeof(T) == 2) {
-    __syncwarp();
-    if (p.cluster > 1) cluster_merge<HD>(p, smem, warp, lane);
-  }
+  __syncwarp();
+  if (p.cluster > 1) cluster_merge<T, HD>(p, smem, warp, lane);
 }
 
 struct Fns {
@@ -1121,36 +1034,31 @@ struct Fns {
   const void* merge;
 };
 
-template <int HD, int HKV>
-const void* mma_fn(int gs) {
+template <typename T, int HD, int HKV>
+const void* main_fn(int gs) {
   if constexpr (HD == 128)
-    if (gs == 32) return reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 4, HKV>);
-  return HD == 2 * gs ? reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 2, HKV>)
-                      : reinterpret_cast<const void*>(decode_q4_kernel<__nv_bfloat16, HD, 1, HKV>);
+    if (gs == 32) return reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 4, HKV>);
+  return HD == 2 * gs ? reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 2, HKV>)
+                      : reinterpret_cast<const void*>(decode_q4_kernel<T, HD, 1, HKV>);
 }
 
-template <int HD>
-const void* simt_fn(int G) {
-  if (G == 1) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 1, 0>);
-  if (G == 2) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 2, 0>);
-  if (G <= 4) return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 4, 0>);
-  return reinterpret_cast<const void*>(decode_q4_kernel<float, HD, 8, 0>);
-}
-
-template <int HD>
-Fns fns_for(const pa_cache_desc& d, int gs) {
-  if (d.dtype != PA_BF16)
-    return {simt_fn<HD>(d.num_q_heads / d.num_kv_heads), reinterpret_cast<const void*>(decode_merge_kernel<float, HD>)};
-  const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<__nv_bfloat16, HD>);
-  switch (d.num_kv_heads) {
-    case 1: return {mma_fn<HD, 1>(gs), merge};
-    case 2: return {mma_fn<HD, 2>(gs), merge};
-    case 4: return {mma_fn<HD, 4>(gs), merge};
-    default: return {mma_fn<HD, 8>(gs), merge};
+template <typename T, int HD>
+Fns fns_for(int hkv, int gs) {
+  const void* merge = reinterpret_cast<const void*>(decode_merge_kernel<T, HD>);
+  switch (hkv) {
+    case 1: return {main_fn<T, HD, 1>(gs), merge};
+    case 2: return {main_fn<T, HD, 2>(gs), merge};
+    case 4: return {main_fn<T, HD, 4>(gs), merge};
+    default: return {main_fn<T, HD, 8>(gs), merge};
   }
 }
 
-Fns get_fns(const pa_cache_desc& d, int gs) { return d.head_dim == 128 ? fns_for<128>(d, gs) : fns_for<64>(d, gs); }
+Fns get_fns(const pa_cache_desc& d, int gs) {
+  const int hkv = d.num_kv_heads;
+  if (d.dtype == PA_BF16)
+    return d.head_dim == 128 ? fns_for<__nv_bfloat16, 128>(hkv, gs) : fns_for<__nv_bfloat16, 64>(hkv, gs);
+  return d.head_dim == 128 ? fns_for<float, 128>(hkv, gs) : fns_for<float, 64>(hkv, gs);
+}
 
 // Bytes of a ring stage: a chunk's rows of K and V, and a request's queries.
 size_t q4_stage_bytes(const pa_cache_desc& d, const DecodePlan& pl) {
@@ -1160,26 +1068,19 @@ size_t q4_stage_bytes(const pa_cache_desc& d, const DecodePlan& pl) {
 
 int q4_groups(const pa_cache_desc& d) { return d.dtype == PA_BF16 ? 2 : 1; }
 
-int heads_padded(int G) { return G <= 2 ? G : G <= 4 ? 4 : 8; }
-
 }  // namespace
 
 cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ctx, int max_ctas, DecodePlan* out) {
   DeviceInfo di;
   cudaError_t e = current_device_info(&di);
   if (e != cudaSuccess) return e;
-  const int G = d.num_q_heads / d.num_kv_heads;
   DecodePlan pl;
   pl.nw = d.num_kv_heads * q4_groups(d);  // consumer warps
-  // fp32's CUDA cores are slow enough for 16 tokens to be a chunk: short requests
-  // then spread over twice the CTAs (one of 5-64 tokens, 16 q-heads over 8 of 128
-  // dims: 10.7 -> 8.5 us; long batches within 5%)
-  pl.tokens_per_chunk = d.dtype == PA_BF16 ? kTok : kHalf;
+  pl.tokens_per_chunk = kTok;
   pl.row_pitch = q4_row_bytes(d, gs);
   pl.chunk_bytes = pl.tokens_per_chunk * pl.row_pitch;
   // behind the ring: barriers, chunk descriptors, the batch's prefix sums, and
-  // what the CUDA-core consumer (fp32) keeps in shared memory
-  const bool simt = d.dtype != PA_BF16;
+  // the part that is handed over
   size_t off = 0;
   auto place = [&](size_t bytes) {
     const size_t at = off;
@@ -1190,19 +1091,15 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   pl.off_meta = place(kMaxStages * 16);
   pl.off_abort = place(16);
   pl.off_cs = place(static_cast<size_t>(kInlinePlanMax + 1 + 32) * 4);
-  pl.off_p = place(simt ? static_cast<size_t>(pl.nw) * kHalf * heads_padded(G) * 4 : 0);
-  pl.off_alpha = place(simt ? static_cast<size_t>(pl.nw) * 8 * 4 : 0);
-  // statistics, then the scaled queries
-  pl.off_ml = place(simt ? static_cast<size_t>(pl.nw) * (16 + heads_padded(G) * d.head_dim) * 4
-                         : static_cast<size_t>(d.num_q_heads) * (d.head_dim + 4) * 4);  // or the handed-over part
+  pl.off_ml = place(static_cast<size_t>(d.num_q_heads) * (d.head_dim + 4) * 4);
   // The ring takes what is left of a CTA's share of the SM's shared memory with
-  // 16 consumer warps on an SM: four or more chunks.
+  // 8 kv-heads on an SM: four or more chunks (of fp32, with many q-heads, two).
   const size_t fixed = align_up(off, 128), stage = q4_stage_bytes(d, pl);
-  const size_t share = static_cast<size_t>(di.max_smem_optin) * std::min(pl.nw, 16) / 16 - 1024;
+  const size_t share = static_cast<size_t>(di.max_smem_optin) * d.num_kv_heads / 8 - 1024;
   const size_t room = share > fixed ? (share - fixed) / stage : 0;
   pl.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(2, room)));
   const uint32_t ring = static_cast<uint32_t>(pl.stages * stage);  // the ring comes first
-  for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_p, &pl.off_alpha, &pl.off_ml})
+  for (uint32_t* o : {&pl.off_bar, &pl.off_meta, &pl.off_abort, &pl.off_cs, &pl.off_ml})
     *o += ring;
   pl.smem_bytes = ring + fixed;
   if (pl.smem_bytes > static_cast<size_t>(di.max_smem_optin)) return cudaErrorInvalidValue;
@@ -1219,16 +1116,13 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   // tokens by clusters of 8 13.7 (15.6), 37 of 64-512 by 4 13.3 (14.6), 64 by 2
   // 16.0 (17.5), 100 of 64-256 by one CTA each 15.0 (18.4), 4 of 5-64 7.6 (8.6).
   // Longer parts: 64 of 300-2000 33.8 (27.2).  Too few: 2 of 1000 by 8 12.1 (9.0),
-  // 4 of 256 by one 12.3 (8.8).  fp32's CUDA cores take a chunk four to eight
-  // times as long: 4 of 256 tokens of 64 dims by one 18.9 (8.0).
+  // 4 of 256 by one 12.3 (8.8).
   if (batch >= 1 && batch <= kInlinePlanMax && n >= batch) {
     const int64_t work = static_cast<int64_t>(max_ctx) * d.head_dim;
-    const int alone = simt ? kAloneTokensF32 : kAloneTokens;
     const int64_t most = std::min<int64_t>({kMaxCluster, n / batch, chunks_upper / batch});
-    int c = simt || work <= alone * 128 ? 1 : static_cast<int>(most);
-    for (; c >= 1; --c) {
-      const bool fills = !simt && 5 * static_cast<int64_t>(batch) * c >= 2 * di.sm_count;
-      if (work > (fills ? c * kPartTokens : c == 1 ? alone : 0) * 128) continue;
+    for (int c = work <= kAloneTokens * 128 ? 1 : static_cast<int>(most); c >= 1; --c) {
+      const bool fills = 5 * static_cast<int64_t>(batch) * c >= 2 * di.sm_count;
+      if (work > (fills ? c * kPartTokens : c == 1 ? kAloneTokens : 0) * 128) continue;
       int fit = batch;
       if (c > 1) {
         e = ctas_per_sm(di, get_fns(d, gs).main, (pl.nw + 1) * 32, pl.smem_bytes, &fit, c);
@@ -1259,7 +1153,6 @@ cudaError_t launch_decode_q4(const pa_cache_desc& d, int gs, const DecodePlan& p
   while ((1 << p.log2gs) < gs) ++p.log2gs;
   p.groups = q4_groups(d);
   p.cluster = pl.cluster;
-  p.off_q = pl.off_ml + pl.nw * 16 * 4;
   p.off_hand = pl.off_ml;
   void* args[] = {&p};
   return launch_decode_kernels(f.main, f.merge, pl, p.k, args, s);
