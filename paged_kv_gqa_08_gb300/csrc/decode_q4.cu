@@ -46,7 +46,7 @@ struct Q4Params {
   KParams k;
   int32_t stages;       // ring depth
   int32_t stage_bytes;  // K rows, V rows, queries
-  int32_t groups;       // consumer groups: 2 (tensor cores) or 1
+  int32_t groups;       // consumer groups: 2 (bf16) or 1 (fp32)
   int32_t cluster;      // CTAs of each request; 0: the CTAs share the batch's chunks evenly
   uint32_t off_hand;    // [Hq][HD + 4] fp32: the part that one group hands to the other, or a CTA to its cluster
   int32_t codes, pars;  // bytes of the two parts of a row
@@ -150,10 +150,13 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // the integer pipe (two cycles each); 309 with K and V decoded to float16 in
 // registers, 228 with raw codes loaded as words and paired by byte permutes.
 //
-// fp32 queries and outputs: queries, p s and p as two float16 numbers each, the
-// rounded value and what it lacks (22 bits in all), so twice the products; those of
-// O are added up in fp32 every 16 tokens (a tensor core's additions cut off).  One
-// consumer group, whose warps may have 168 registers.
+// fp32 queries and outputs.  Queries and p s are two float16 numbers each, multiples
+// of 2^-11 and 2^-23 of their bounds (p s: of the largest among a head's 16 tokens,
+// for each group), so that every sum of products with codes is exact; the two sums
+// and those of 16 tokens are added in fp32.  The second terms and the softmax sum are
+// fp32 multiply-adds of the lanes: the terms cancel to a fifth or less, and what a
+// tensor core's additions cut off (1e-7 of the largest) would show.  One consumer
+// group, whose warps may have 168 registers.
 //
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
 // [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
@@ -277,10 +280,14 @@ PA_DEVINL void ldsm4_trans(uint32_t (&r)[4], uint32_t a) {
                : "r"(a));
 }
 
-// Two numbers as float16 numbers, and what these lack.
-PA_DEVINL void split_f16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_f16x2(x, y);
-  lo = pack_f16x2(x - f16_lo(hi), y - f16_lo(hi >> 16));
+// x = hi + lo + less than 2^-12 of kGrid: hi a multiple of kGrid, lo of 2^-12
+// kGrid, both float16 numbers where |x| <= 2^11 kGrid.
+template <int kLog2Grid>
+PA_DEVINL void split(float x, float& hi, float& lo) {
+  constexpr float m = 1.5f * (1 << 23), g = kLog2Grid < 0 ? 1.f / (1 << -kLog2Grid) : 1.f * (1 << kLog2Grid);
+  hi = __fsub_rn(__fadd_rn(x, m * g), m * g);
+  const float rest = x - hi;
+  lo = __fsub_rn(__fadd_rn(rest, m * g * 0x1p-12f), m * g * 0x1p-12f);
 }
 
 template <typename T, int HD, int NG, int HKV>
@@ -316,15 +323,17 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, smem0 + p.k.off_abort, p.k.err); };
 
   uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
-  uint32_t qm = 0u;    // 2^-10 (16 sum q, sum q) over the dims of group tq; fp32: 2^-2, with ...
-  [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // what qf lacks
-  [[maybe_unused]] uint32_t qm_lo = 0u;            // what qm lacks (up to two groups: with the lanes tq + 2 or tq + 1)
+  [[maybe_unused]] uint32_t qm = 0u;               // 2^-10 (16 sum q, sum q) over the dims of group tq
+  [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // fp32: what qf lacks,
+  [[maybe_unused]] float q_sum[NG][2];             // and 2^-10 times the sums, for heads 2 tq and 2 tq + 1
+  // fp32: this lane's share of the sums over the tokens of p and of p m
+  [[maybe_unused]] float l_sum[2] = {0.f, 0.f}, pm_sum[NG][2];
   float o[MB][4];
   // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
   // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
   float om[4] = {0.f, 0.f, 0.f, 0.f};
   // The largest s with the exponent of the largest seen, twice (0: none above 0
-  // yet).  With that exponent's bits x, E = max(x - 21, -15).
+  // yet).  With that exponent's bits x, E = max(x - 21, -15).  (Not for fp32.)
   uint32_t s_most = 0u;
   float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone)
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
@@ -371,10 +380,11 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         // 2^-E of the largest magnitude's exponent E, and 2^E
         const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
         const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
-        qm = qm_lo = 0u;
+        qm = 0u;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float sum = 0.f;
+          [[maybe_unused]] float sum_l = 0.f;  // (apart: the sum of the first parts is all but exact)
 #pragma unroll
           for (int i = g * PG; i < (g + 1) * PG; ++i) {
             float (&q)[8] = qv[i];
@@ -382,13 +392,14 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
             // as they are rounded: the second term's sum has to be that of the first's queries
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float x = q[e] * down * 256.f;
-              q[e] = __half2float(__float2half_rn(x));
-              sum += q[e];
+              const float x = q[e] * down * 256.f;  // below 2^9
               if constexpr (kF32) {
-                l[e] = __half2float(__float2half_rn(x - q[e]));
-                sum += l[e];
+                split<-2>(x, q[e], l[e]);
+                sum_l += l[e];
+              } else {
+                q[e] = __half2float(__float2half_rn(x));
               }
+              sum += q[e];
             }
             qf[2 * i][0] = pack_f16x2(q[0], q[4]);
             qf[2 * i][1] = pack_f16x2(q[1], q[5]);
@@ -404,10 +415,11 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           if constexpr (kF32) {
-            const float r = sum * 0x1p-10f, rh = __half2float(__float2half_rn(r));
-            const float rl = __half2float(__float2half_rn(r - rh));
-            if (tq == g) qm = pack_f16x2(rh * 16.f, rh);
-            if (NG == 4 ? tq == g : tq == g + NG) (NG == 4 ? qm_lo : qm) = pack_f16x2(rl * 16.f, rl);
+            sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 1);
+            sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 2);
+            sum += sum_l;
+            q_sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * tq) * 0x1p-18f;
+            q_sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4) * 0x1p-18f;
           } else {
             const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
             if (tq == g) qm = pack_f16x2(r * 16.f, r);
@@ -422,6 +434,9 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         m[0] = m[1] = 0.f;
         limit = -INFINITY;
         om[0] = om[1] = om[2] = om[3] = 0.f;
+        l_sum[0] = l_sum[1] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) pm_sum[g][0] = pm_sum[g][1] = 0.f;
         s_most = 0u;
       }
       if (flags & kNew) {
@@ -437,25 +452,21 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const uint32_t half = st + hf * kHalf * R;
-      uint32_t par[2][NG], pm[2];  // parameters of tokens gq, gq + 8; of their group tq
+      uint32_t par[2][NG];  // parameters of tokens gq, gq + 8
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        lds_words<NG>(par[u], half + u * 8 * R + kp_at);
-        pm[u] = par[u][0];  // (any where there is no group tq: its queries' sum is 0)
-        if constexpr (NG == 2) pm[u] = (tq & 1) ? par[u][1] : par[u][0];
-        if constexpr (NG == 4)
-          pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
-      }
-      float sc[4], d[4];
-      mma_f16_k8(sc, pm[0], pm[1], qm);
-      if constexpr (kF32) {
-        if constexpr (NG == 4) {
-          mma_f16_k8(d, pm[0], pm[1], qm_lo);
+      for (int u = 0; u < 2; ++u) lds_words<NG>(par[u], half + u * 8 * R + kp_at);
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, d[4];
+      [[maybe_unused]] float dl[4];  // fp32: of the lower parts of the queries
+      if constexpr (!kF32) {
+        uint32_t pm[2];  // of their group tq (any where there is none: its queries' sum is 0)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[e] += d[e];
+        for (int u = 0; u < 2; ++u) {
+          pm[u] = par[u][0];
+          if constexpr (NG == 2) pm[u] = (tq & 1) ? par[u][1] : par[u][0];
+          if constexpr (NG == 4)
+            pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[e] *= 0x1p-8f;
+        mma_f16_k8(sc, pm[0], pm[1], qm);
       }
       uint32_t w[4];  // of two pieces: the words of tokens gq and gq + 8
 #pragma unroll
@@ -465,13 +476,23 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
         if (i % PG == 0) d[0] = d[1] = d[2] = d[3] = 0.f;
         if constexpr (kF32) {
-          mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), ql[2 * i][0], ql[2 * i][1]);
-          mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), ql[2 * i + 1][0], ql[2 * i + 1][1]);
+          if (i % PG == 0) dl[0] = dl[1] = dl[2] = dl[3] = 0.f;
+          mma_f16(dl, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), ql[2 * i][0], ql[2 * i][1]);
+          mma_f16(dl, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), ql[2 * i + 1][0], ql[2 * i + 1][1]);
         }
         mma_f16(d, raw_hi(w0), raw_hi(w1), raw_hi(y0), raw_hi(y1), qf[2 * i][0], qf[2 * i][1]);
         mma_f16(d, raw_lo(w0), raw_lo(w1), raw_lo(y0), raw_lo(y1), qf[2 * i + 1][0], qf[2 * i + 1][1]);
         if (i % PG == PG - 1) {
           const float s0 = f16_lo(par[0][i / PG]), s1 = f16_lo(par[1][i / PG]);
+          if constexpr (kF32) {
+            const float m0 = fmaf(16.f, s0, f16_lo(par[0][i / PG] >> 16));
+            const float m1 = fmaf(16.f, s1, f16_lo(par[1][i / PG] >> 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              d[e] += dl[e];
+              sc[e] = fmaf(e < 2 ? m0 : m1, q_sum[i / PG][e & 1], sc[e]);
+            }
+          }
           sc[0] = fmaf(d[0], s0, sc[0]);
           sc[1] = fmaf(d[1], s0, sc[1]);
           sc[2] = fmaf(d[2], s1, sc[2]);
@@ -511,6 +532,15 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         om[1] *= a1;
         om[2] *= a0;
         om[3] *= a1;
+        if constexpr (kF32) {
+          l_sum[0] *= a0;
+          l_sum[1] *= a1;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            pm_sum[g][0] *= a0;
+            pm_sum[g][1] *= a1;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           o[j][0] *= a0;
@@ -531,20 +561,11 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
       limit = 8.f;
     }
     uint32_t pb[2][2];  // B fragments of the probabilities
-    [[maybe_unused]] uint32_t pl[2][2];  // fp32: of what these lack (t: the probabilities)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const float p0 = ex2_approx(t[hf][0]), p1 = ex2_approx(t[hf][1]);
       const float p2 = ex2_approx(t[hf][2]), p3 = ex2_approx(t[hf][3]);
       if constexpr (kF32) {
-        uint32_t hi[2], lo[2];
-        split_f16x2(p0, p1, hi[0], lo[0]);
-        split_f16x2(p2, p3, hi[1], lo[1]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          pb[hf][u] = movm_trans(hi[u]);
-          pl[hf][u] = movm_trans(lo[u]);
-        }
         t[hf][0] = p0, t[hf][1] = p1, t[hf][2] = p2, t[hf][3] = p3;
       } else {
         pb[hf][0] = movm_trans(pack_f16x2(p0, p1));
@@ -553,64 +574,89 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
     }
 
     // O^T += V^T P^T
-    uint32_t vm[4];  // row gq of the parameter piece: tokens 2 tq, 2 tq + 1 (+ 8, + 16, + 24)
-    ldsm4_trans(vm, st + vp_at);
-    if (flags & kRagged) {
-      // rows past the context meet probability 0 and must be finite
+    [[maybe_unused]] uint32_t vm[4];  // row gq of the parameter piece: tokens 2 tq, 2 tq + 1 (+ 8, + 16, + 24)
+    [[maybe_unused]] uint32_t vpar[2][2][NG];  // fp32: the parameters of tokens gq, gq + 8 (+ 16)
+    if constexpr (kF32) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int n = static_cast<int>((flags >> (u / 2 * 8)) & 255) - (u & 1) * 8;
-        vm[u] &= (2 * tq < n ? 0xFFFFu : 0u) | (2 * tq + 1 < n ? 0xFFFF0000u : 0u);
-      }
-    }
-    // A larger s than the scale was made for: scale anew (s is never negative, so
-    // its bits compare as integers).
-    const uint32_t top = __vmaxu2(__vmaxu2(vm[0], vm[1]), __vmaxu2(vm[2], vm[3])) & s_mask;
-    if (__any_sync(0xffffffffu, __vmaxu2(top, s_most) != s_most)) {
-      const uint32_t bits = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 10, 1u);
-      if (s_most != 0u) {
-        const float a = __uint_as_float((127u + max(s_most >> 26, 6u) - max(bits, 6u)) << 23);
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= a;
-      }
-      s_most = (((bits + 1) << 10) - 1) * 0x00010001u;
-    }
-    // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
-    const uint32_t s_scale = 36u * kExponent - max(s_most & 0x7C007C00u, 6u * kExponent);
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      [[maybe_unused]] float s_of[2][NG];  // fp32: 2^-E s of tokens gq and gq + 8
-      if constexpr (kF32) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pl[hf][0], pl[hf][1]);
-        mma_f16(d, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) om[e] += d[e];
-        const float scale = __uint_as_float((127u + 21 - max(s_most >> 26, 6u)) << 23);
-        const int n = static_cast<int>((flags >> (8 * hf)) & 255);
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          uint32_t par[NG];
-          lds_words<NG>(par, st + kChunk + (hf * kHalf + u * 8) * R + kp_at);
+          lds_words<NG>(vpar[hf][u], st + kChunk + (hf * kHalf + u * 8) * R + kp_at);
+          // rows past the context meet probability 0 and must be finite
+          const bool live = gq + u * 8 < static_cast<int>((flags >> (8 * hf)) & 255);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) s_of[u][g] = gq + u * 8 < n ? f16_lo(par[g]) * scale : 0.f;
+          for (int g = 0; g < NG; ++g)
+            if (!live) vpar[hf][u][g] = 0u;
         }
+    } else {
+      ldsm4_trans(vm, st + vp_at);
+      if (flags & kRagged) {
+        // rows past the context meet probability 0 and must be finite
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int n = static_cast<int>((flags >> (u / 2 * 8)) & 255) - (u & 1) * 8;
+          vm[u] &= (2 * tq < n ? 0xFFFFu : 0u) | (2 * tq + 1 < n ? 0xFFFF0000u : 0u);
+        }
+      }
+      // A larger s than the scale was made for: scale anew (s is never negative, so
+      // its bits compare as integers).
+      const uint32_t top = __vmaxu2(__vmaxu2(vm[0], vm[1]), __vmaxu2(vm[2], vm[3])) & s_mask;
+      if (__any_sync(0xffffffffu, __vmaxu2(top, s_most) != s_most)) {
+        const uint32_t bits = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 10, 1u);
+        if (s_most != 0u) {
+          const float a = __uint_as_float((127u + max(s_most >> 26, 6u) - max(bits, 6u)) << 23);
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] *= a;
+        }
+        s_most = (((bits + 1) << 10) - 1) * 0x00010001u;
+      }
+    }
+    // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
+    [[maybe_unused]] const uint32_t s_scale = 36u * kExponent - max(s_most & 0x7C007C00u, 6u * kExponent);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      if constexpr (kF32) {
+        l_sum[0] += t[hf][0] + t[hf][2];
+        l_sum[1] += t[hf][1] + t[hf][3];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float m = fmaf(16.f, f16_lo(vpar[hf][u][g]), f16_lo(vpar[hf][u][g] >> 16));
+            pm_sum[g][0] = fmaf(t[hf][2 * u], m, pm_sum[g][0]);
+            pm_sum[g][1] = fmaf(t[hf][2 * u + 1], m, pm_sum[g][1]);
+          }
       } else {
         mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
       }
       uint32_t x[4];  // of two pieces: half word gq of tokens 2 tq, 2 tq + 1 and of those 8 on
       uint32_t b0, b1;
       [[maybe_unused]] uint32_t l0, l1;
+      [[maybe_unused]] float undo[2];  // the powers of two that the products of heads 2 tq, 2 tq + 1 lack
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (i % 2 == 0) ldsm4_trans(x, st + kChunk + hf * kHalf * R + c_at[i / 2]);
         if (i % PG == 0 && kF32) {  // p s of the group
-          const float s0 = s_of[0][i / PG], s1 = s_of[1][i / PG];
-          split_f16x2(t[hf][0] * s0, t[hf][1] * s0, b0, l0);
-          split_f16x2(t[hf][2] * s1, t[hf][3] * s1, b1, l1);
-          b0 = movm_trans(b0), b1 = movm_trans(b1), l0 = movm_trans(l0), l1 = movm_trans(l1);
+          float x[4], hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = t[hf][e] * f16_lo(vpar[hf][e / 2][i / PG]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float most = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+            const uint32_t eb = max(__float_as_uint(most) >> 23, 20u);
+            const float scale = __uint_as_float((260u - eb) << 23);  // the largest becomes 2^6 .. 2^7
+            undo[e] = __uint_as_float((eb + 12u) << 23);             // with the codes' 2^-18
+            split<-4>(x[e] * scale, hi[e], lo[e]);
+            split<-4>(x[e + 2] * scale, hi[e + 2], lo[e + 2]);
+          }
+          b0 = movm_trans(pack_f16x2(hi[0], hi[1]));
+          b1 = movm_trans(pack_f16x2(hi[2], hi[3]));
+          l0 = movm_trans(pack_f16x2(lo[0], lo[1]));
+          l1 = movm_trans(pack_f16x2(lo[2], lo[3]));
         } else if (i % PG == 0) {
           const int from = s_lane + i / PG * 8;
           b0 = mul_f16x2(pb[hf][0], mul_f16x2(__shfl_sync(0xffffffffu, vm[2 * hf], from), s_scale));
@@ -619,15 +665,15 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         const uint32_t x0 = i % 2 == 0 ? x[0] : x[2], x1 = i % 2 == 0 ? x[1] : x[3];
         const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
         if constexpr (kF32) {
-          float d[2][4] = {};
-          mma_f16(d[0], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), l0, l1);
+          float d[4][4] = {};
           mma_f16(d[0], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
-          mma_f16(d[1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), l0, l1);
-          mma_f16(d[1], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
+          mma_f16(d[1], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), l0, l1);
+          mma_f16(d[2], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), b0, b1);
+          mma_f16(d[3], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), l0, l1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            o[2 * i][e] += d[0][e];
-            o[2 * i + 1][e] += d[1][e];
+            o[2 * i][e] = fmaf(d[0][e] + d[1][e], undo[e & 1], o[2 * i][e]);
+            o[2 * i + 1][e] = fmaf(d[2][e] + d[3][e], undo[e & 1] * 16.f, o[2 * i + 1][e]);
           }
         } else {
           mma_f16(o[2 * i], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
@@ -645,15 +691,29 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
 
     if (flags & (kLast | kYield)) {
       float l[2] = {om[2], om[3]};  // the softmax sums
+      if constexpr (kF32) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l_sum[e] += __shfl_xor_sync(0xffffffffu, l_sum[e], k);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) pm_sum[g][e] += __shfl_xor_sync(0xffffffffu, pm_sum[g][e], k);
+          }
+        l[0] = l_sum[0];
+        l[1] = l_sum[1];
+      }
       // the powers of two undone, the second term added
-      const float hi = __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23), lo = hi * 16.f;
+      const float hi = kF32 ? 1.f : __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23);
+      const float lo = kF32 ? 1.f : hi * 16.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float add[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
-                        __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
+          add[e] = kF32 ? pm_sum[g][e]
+                        : fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
+                               __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
 #pragma unroll
         for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
 #pragma unroll

@@ -435,12 +435,13 @@ def test_a_key_that_is_not_a_number_makes_its_heads_outputs_nan_however_they_are
         assert err <= (1e-5 if dtype == "f32" else 1e-2) * np.abs(ref).max()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gs", [32, 64, 128])
 @pytest.mark.parametrize("order", ["growing", "falling", "one"])
-def test_scales_that_change_along_the_context(gs, order):
+def test_scales_that_change_along_the_context(gs, order, dtype):
     """V's magnitude rises or falls by 2^40 along the context, or is 2^20 times the others' in one token that no query
     looks at: the powers of two that keep p s in float16's range follow the largest scale."""
-    c = Case("bf16", 4, 4, 128, gs, 16, [700, 90] * 8, seed=8)
+    c = Case(dtype, 4, 4, 128, gs, 16, [700, 90] * 8, seed=8)
     rng = np.random.default_rng(1)
     for b, L in enumerate(c.lens):
         slots = c.bt[b, np.arange(L) // 16].astype(np.int64) * 16 + np.arange(L) % 16
@@ -461,7 +462,10 @@ def test_scales_that_change_along_the_context(gs, order):
         c.vals[1][slots] = q4.values(u, sc, off, gs)
     ref = c.reference()
     for max_ctas in (0, 1, 2, 20):
-        c.check(c.decode(max_ctas), ref)
+        out = c.decode(max_ctas)
+        c.check(out, ref)
+        if dtype == "f32":      # small outputs, too
+            assert np.abs(out.double().cpu().numpy() - ref).max() <= 1e-5 * np.abs(ref).max()
 
 
 def test_two_streams_at_once_and_the_same_bits_every_time():
