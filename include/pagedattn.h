@@ -498,8 +498,9 @@ PA_API size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t gro
 /*
  * pa_decode_q4 -- pa_decode over a 4-bit cache.  Arguments, padding rows, flags
  * and the split over CTAs as pa_decode, but short requests (max_context_len up
- * to some thousand tokens) take a CTA, or in bf16 a cluster of up to 8 CTAs, each
- * where batch * CTAs fit the GPU and max_ctas.  q and out are device memory.
+ * to some thousand tokens) take a CTA or a cluster of up to 8 CTAs each, where
+ * batch * CTAs fit the GPU and max_ctas.  fp32 results are off by a few 2^-24 of
+ * the values' magnitude, as a plain fp32 evaluation's.  q and out are device memory.
  */
 PA_API pa_status pa_decode_q4(const pa_cache_desc* desc, int32_t group_size, const void* q, int32_t batch,
                               const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -1,7 +1,7 @@
 // Batched GQA decode attention over a 4-bit paged cache (sm_103a).
 //
-// The mathematics is decode.cu's with K and V rows that are decoded on the
-// way in (q4_common.cuh): the split of the keys over the CTAs, the partial
+// The mathematics is decode.cu's over the values that K and V rows of 4-bit codes
+// stand for (q4_common.cuh): the even split of the keys over the CTAs, the partial
 // results and their merge are the same code (decode_shared.cuh).  A chunk is
 // 32 tokens, two halves of 16 tokens of one page each; a producer warp copies
 // their rows of K and V as they are into a ring in shared memory (one run of
