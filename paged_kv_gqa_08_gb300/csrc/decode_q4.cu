@@ -161,7 +161,8 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
 // [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
 // when a score passes it by more).  p s is kept in float16's range by a power of
-// two 2^-E that follows the largest s seen.  Each rounding to float16 is 2^-11
+// two 2^-E that follows the largest s seen (a group whose s is more than 2^17 below
+// that has fewer bits in p s).  Each rounding to float16 is 2^-11
 // relative, finer than the bf16 of queries and outputs; sums and statistics are
 // fp32.
 // ---------------------------------------------------------------------------
