@@ -13,11 +13,12 @@ a staging cache of the descriptor's dtype and attends to that.
 from __future__ import annotations
 
 import dataclasses
+import math
 from typing import Optional
 
 import torch
 
-from . import (cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
+from . import (PA_ERR_ALIGN, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedAttnError, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
                pa_kv_read_q4, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
                pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step, pa_prefill_varlen, pa_prefill_workspace_size,
                pa_slot_mapping)
@@ -145,11 +146,50 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
     return bufs.out
 
 
+def _refuse(status: int, message: str):
+    raise PagedAttnError("run_step", status, message)
+
+
+def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
+                   k_norm_w):
+    """What the attention of a step over a 4-bit cache would refuse once the step's rows are written: refused before
+    anything is enqueued (the write's own checks come first in its call)."""
+    n = q.shape[0]
+    norm = q_norm_w is not None
+    if n and not 1 <= max_context_len <= max_pages_per_seq * desc.page_size:
+        _refuse(PA_ERR_SHAPE, "max_context_len is not within 1 .. max_pages_per_seq * page_size")
+    if not math.isfinite(scale) or (kind != "decode" and not scale > 0):
+        _refuse(PA_ERR_SHAPE, "the scale is not finite, or not positive where prefill needs it")
+    if any(t is not None and t.data_ptr() % 16 for t in (bufs.out, bufs.q_out if norm else q)):
+        _refuse(PA_ERR_ALIGN, "q or out is not 16-byte aligned")
+    ws = bufs.workspace
+    if kind == "decode":
+        need = pa_decode_q4_workspace_size(desc, bufs.group_size, batch, max_context_len, bufs.max_ctas) if batch else 0
+        if need and ws is None:
+            _refuse(PA_ERR_WORKSPACE, "the buffers have no decode workspace")
+    else:
+        st = bufs.staging
+        if st is None:
+            raise ValueError("the buffers were not allocated for a prefill step over a 4-bit cache")
+        if batch > st.block_tables.shape[0] or max_context_len > st.max_pages * desc.page_size:
+            raise ValueError("the step's batch or max_context_len is beyond what the buffers were allocated for")
+        if n and not (batch and 1 <= max_seqlen_q <= max_context_len):
+            _refuse(PA_ERR_SHAPE, "tokens without requests, or max_seqlen_q is not within 1 .. max_context_len")
+        need = (pa_prefill_workspace_size(st.desc, batch, max_seqlen_q, n, max_context_len)
+                if n and ws is not None else 0)
+    if need and ws.numel() * ws.element_size() < need:
+        _refuse(PA_ERR_WORKSPACE, "the buffers' workspace is smaller than this step needs")
+    if ws is not None and ws.data_ptr() % 256:
+        _refuse(PA_ERR_ALIGN, "the workspace is not 256-byte aligned")
+
+
 def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, scale,
                  max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps, rope_theta, stream):
     """The step over a 4-bit cache.  A prefill step whose metadata is flagged as bad (``pa_read_device_errors``)
     attends, where a page was skipped, to what the staging cache held there before."""
     n, batch, gs = q.shape[0], context_lens.shape[0], bufs.group_size
+    _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
+                   k_norm_w)
     if q_norm_w is not None:
         pa_prefill_qk_norm_rope_kv_write_q4(desc, gs, q, q.stride(0), k, k.stride(0), v, v.stride(0), n,
                                             cu_seqlens_q, batch, context_lens, block_tables, max_pages_per_seq,
@@ -165,8 +205,6 @@ def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_ta
                      max_context_len, scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
         return bufs.out
     st = bufs.staging
-    if batch > st.block_tables.shape[0] or max_context_len > st.max_pages * desc.page_size:
-        raise ValueError("the step's batch or max_context_len is beyond what the buffers were allocated for")
     row = desc.num_kv_heads * desc.head_dim
     pa_kv_read_q4(desc, gs, batch, st.cu_rows, None, context_lens, block_tables, max_pages_per_seq,
                   batch * st.max_pages * desc.page_size, k_cache, v_cache, st.k, row, st.v, row, stream)

@@ -212,3 +212,117 @@ def test_the_binding_refuses_caches_that_are_not_4_bit_rows():
         with pytest.raises(pa.PagedAttnError) as e:
             pa.pa_kv_write_q4(desc, 32, FAKE, 1024, FAKE, 1024, 1, FAKE, bad, bad)
         assert e.value.status == status
+
+
+@pytest.fixture
+def enqueued(monkeypatch):
+    """The calls of the library that a step makes, recorded in place of made: these tests need no GPU and touch none."""
+    from paged_kv_gqa_08_gb300 import step
+    calls = []
+    for name in [n for n in vars(step) if n.startswith("pa_") and not n.endswith("workspace_size")]:
+        monkeypatch.setattr(step, name, lambda *a, name=name, **k: calls.append(name))
+    monkeypatch.setattr(step, "pa_decode_q4_workspace_size", lambda *a: 4096)
+    monkeypatch.setattr(step, "pa_prefill_workspace_size", lambda *a: 4096)
+    return calls
+
+
+def _step_args(kind="prefill", **kw):
+    """Buffers and arguments of run_step over a 4-bit cache of two requests, in host memory."""
+    import torch
+    from paged_kv_gqa_08_gb300.step import alloc_step_buffers
+
+    desc = _desc(num_pages=8)
+    bufs = alloc_step_buffers(desc, kind, 6, 2, 64, "cpu", norm=True, max_seqlen_q=8, group_size=32)
+    base = torch.zeros(8192, dtype=torch.uint8)
+    at = -base.data_ptr() % 256
+    bufs.workspace = base[at: at + 4096]
+    n = 6 if kind == "prefill" else 2
+    cache = torch.zeros(8 * 16, 640, dtype=torch.uint8)
+    rows = torch.zeros(n, 8, 128, dtype=torch.bfloat16)
+    a = dict(desc=desc, kind=kind, bufs=bufs, q=torch.zeros(n, 16, 128, dtype=torch.bfloat16), k=rows, v=rows,
+             cu_seqlens_q=torch.tensor([0, n // 2, n], dtype=torch.int32),
+             context_lens=torch.tensor([20, 30], dtype=torch.int32),
+             block_tables=torch.zeros(2, 4, dtype=torch.int32), k_cache=cache, v_cache=cache, scale=0.1,
+             max_pages_per_seq=4, max_context_len=64, max_seqlen_q=8, q_norm_w=None, k_norm_w=None, eps=1e-6,
+             rope_theta=1e4)
+    a.update(kw)
+    return a
+
+
+def _past_the_tables(torch, a):
+    a["max_context_len"] = 65
+    if a["bufs"].staging is not None:
+        a["bufs"].staging.max_pages = 5
+
+
+def _misaligned(torch, like):
+    return torch.zeros(like.numel() + 8, dtype=like.dtype)[1: 1 + like.numel()].view(like.shape)
+
+
+def _small_workspace(torch, a):
+    a["bufs"].workspace = a["bufs"].workspace[:4095]
+
+
+def _odd_workspace(torch, a):
+    base = torch.zeros(8192, dtype=torch.uint8)
+    a["bufs"].workspace = base[16 - base.data_ptr() % 256 + 256:]
+
+
+@pytest.mark.parametrize("kind", ["prefill", "decode"])
+@pytest.mark.parametrize("spoil,status", [
+    (_past_the_tables, pa.PA_ERR_SHAPE),
+    (lambda torch, a: a.update(max_context_len=0), pa.PA_ERR_SHAPE),
+    (lambda torch, a: a.update(scale=float("nan")), pa.PA_ERR_SHAPE),
+    (lambda torch, a: a.update(q=_misaligned(torch, a["q"])), pa.PA_ERR_ALIGN),
+    (lambda torch, a: setattr(a["bufs"], "out", _misaligned(torch, a["bufs"].out)), pa.PA_ERR_ALIGN),
+    (_small_workspace, pa.PA_ERR_WORKSPACE), (_odd_workspace, pa.PA_ERR_ALIGN)])
+def test_a_step_is_refused_before_anything_is_enqueued(enqueued, kind, spoil, status):
+    torch = pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    a = _step_args(kind)
+    spoil(torch, a)
+    with pytest.raises(pa.PagedAttnError) as e:
+        run_step(**a)
+    assert e.value.status == status and not enqueued
+
+
+@pytest.mark.parametrize("kw,status", [(dict(max_seqlen_q=0), pa.PA_ERR_SHAPE), (dict(max_seqlen_q=65), pa.PA_ERR_SHAPE),
+                                       (dict(scale=0.0), pa.PA_ERR_SHAPE), (dict(scale=-1.0), pa.PA_ERR_SHAPE)])
+def test_a_prefill_step_is_refused_before_anything_is_enqueued(enqueued, kw, status):
+    pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    with pytest.raises(pa.PagedAttnError) as e:
+        run_step(**_step_args(**kw))
+    assert e.value.status == status and not enqueued
+
+
+def test_a_prefill_step_beyond_its_buffers_is_refused_before_anything_is_enqueued(enqueued):
+    pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    decode_bufs = _step_args()
+    decode_bufs["bufs"].staging = None
+    for a in (_step_args(max_context_len=65, max_pages_per_seq=5), decode_bufs):
+        with pytest.raises(ValueError):
+            run_step(**a)
+        assert not enqueued
+
+
+def test_steps_that_are_not_refused(enqueued):
+    torch = pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    w = torch.ones(128, dtype=torch.bfloat16)
+    run_step(**_step_args())
+    run_step(**_step_args("decode"))
+    assert enqueued[-1] == "pa_decode_q4"
+    wide = torch.zeros(6, 32, 128, dtype=torch.bfloat16)[:, :16]
+    run_step(**_step_args(q=wide, q_norm_w=w, k_norm_w=w))          # the norm takes rows of any stride
+    run_step(**_step_args(q=wide[:1], cu_seqlens_q=torch.tensor([0, 0, 1], dtype=torch.int32)))   # one row has none
+    run_step(**_step_args("decode", scale=-0.1))
+    a = _step_args()
+    a["bufs"].workspace = None                                      # prefill takes none, too
+    run_step(**a)
+    assert enqueued.count("pa_prefill_varlen") == 4 and enqueued.count("pa_decode_q4") == 2
