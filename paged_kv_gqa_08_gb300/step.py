@@ -156,6 +156,9 @@ def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_con
     anything is enqueued (the write's own checks come first in its call)."""
     n = q.shape[0]
     norm = q_norm_w is not None
+    width = desc.num_q_heads * desc.head_dim
+    if not norm and n and not (q[0].is_contiguous() and (n == 1 or q.stride(0) == width)):
+        _refuse(PA_ERR_SHAPE, "without norm weights attention reads q itself, so its rows must be packed")
     if n and not 1 <= max_context_len <= max_pages_per_seq * desc.page_size:
         _refuse(PA_ERR_SHAPE, "max_context_len is not within 1 .. max_pages_per_seq * page_size")
     if not math.isfinite(scale) or (kind != "decode" and not scale > 0):

@@ -249,6 +249,14 @@ def _step_args(kind="prefill", **kw):
     return a
 
 
+def _wide(torch, a):             # q's rows inside a fused projection
+    a["q"] = torch.zeros(a["q"].shape[0], 32, 128, dtype=torch.bfloat16)[:, :16]
+
+
+def _transposed(torch, a):
+    a["q"] = torch.zeros(a["q"].shape[0], 128, 16, dtype=torch.bfloat16).transpose(1, 2)
+
+
 def _past_the_tables(torch, a):
     a["max_context_len"] = 65
     if a["bufs"].staging is not None:
@@ -270,7 +278,7 @@ def _odd_workspace(torch, a):
 
 @pytest.mark.parametrize("kind", ["prefill", "decode"])
 @pytest.mark.parametrize("spoil,status", [
-    (_past_the_tables, pa.PA_ERR_SHAPE),
+    (_wide, pa.PA_ERR_SHAPE), (_transposed, pa.PA_ERR_SHAPE), (_past_the_tables, pa.PA_ERR_SHAPE),
     (lambda torch, a: a.update(max_context_len=0), pa.PA_ERR_SHAPE),
     (lambda torch, a: a.update(scale=float("nan")), pa.PA_ERR_SHAPE),
     (lambda torch, a: a.update(q=_misaligned(torch, a["q"])), pa.PA_ERR_ALIGN),
