@@ -18,7 +18,7 @@ from typing import Optional
 
 import torch
 
-from . import (PA_ERR_ALIGN, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedAttnError, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
+from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedAttnError, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
                pa_kv_read_q4, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
                pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step, pa_prefill_varlen, pa_prefill_workspace_size,
                pa_slot_mapping)
@@ -155,6 +155,8 @@ def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_con
     """What the attention of a step over a 4-bit cache would refuse once the step's rows are written: refused before
     anything is enqueued (the write's own checks come first in its call)."""
     n = q.shape[0]
+    if (q_norm_w is None) != (k_norm_w is None):
+        _refuse(PA_ERR_NULL, "one norm weight without the other")
     norm = q_norm_w is not None
     width = desc.num_q_heads * desc.head_dim
     if not norm and n and not (q[0].is_contiguous() and (n == 1 or q.stride(0) == width)):

@@ -278,6 +278,8 @@ def _odd_workspace(torch, a):
 
 @pytest.mark.parametrize("kind", ["prefill", "decode"])
 @pytest.mark.parametrize("spoil,status", [
+    (lambda torch, a: a.update(q_norm_w=torch.ones(128, dtype=torch.bfloat16)), pa.PA_ERR_NULL),
+    (lambda torch, a: a.update(k_norm_w=torch.ones(128, dtype=torch.bfloat16)), pa.PA_ERR_NULL),
     (_wide, pa.PA_ERR_SHAPE), (_transposed, pa.PA_ERR_SHAPE), (_past_the_tables, pa.PA_ERR_SHAPE),
     (lambda torch, a: a.update(max_context_len=0), pa.PA_ERR_SHAPE),
     (lambda torch, a: a.update(scale=float("nan")), pa.PA_ERR_SHAPE),
