@@ -117,6 +117,9 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
     """Run one step; returns ``bufs.out`` (the attention output of the new tokens)."""
     n = q.shape[0]
     batch = context_lens.shape[0]
+    for t in (bufs.positions, bufs.slots, bufs.out, bufs.q_out if q_norm_w is not None else None):
+        if t is not None and t.shape[0] < n:
+            raise ValueError(f"a step of {n} tokens in buffers for {t.shape[0]}")
     if bufs.group_size:
         return _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
                             scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps,

@@ -320,6 +320,23 @@ def test_a_prefill_step_beyond_its_buffers_is_refused_before_anything_is_enqueue
         assert not enqueued
 
 
+@pytest.mark.parametrize("kind", ["prefill", "decode"])
+@pytest.mark.parametrize("group_size", [32, 0])
+@pytest.mark.parametrize("short", ["positions", "slots", "out", "q_out"])
+def test_a_step_of_more_tokens_than_its_buffers_hold_is_refused(enqueued, kind, group_size, short):
+    torch = pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    w = torch.ones(128, dtype=torch.bfloat16)
+    a = _step_args(kind, q_norm_w=w, k_norm_w=w)
+    bufs = a["bufs"]
+    bufs.group_size = group_size
+    setattr(bufs, short, getattr(bufs, short)[: a["q"].shape[0] - 1])
+    with pytest.raises(ValueError):
+        run_step(**a)
+    assert not enqueued
+
+
 def test_steps_that_are_not_refused(enqueued):
     torch = pytest.importorskip("torch")
     from paged_kv_gqa_08_gb300.step import run_step
