@@ -1609,7 +1609,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const Merg
   const int g = r / kBM, row = r % kBM;
   const int t = row / m.G, gg = row - t * m.G;
   const int tok = (2 * qp + g) * m.TQ + t;
-  if (tok >= n) return;
+  // rows past the tile's last token (128 is no multiple of some group sizes) are the next tile's to write
+  if (t >= m.TQ || tok >= n) return;
   const int64_t slot_stride = static_cast<int64_t>(m.Hkv) * 2 * kBM;  // rows per slot
   const int64_t r0 = (static_cast<int64_t>(slot0) * m.Hkv + h) * 2 * kBM + r;
   float mx = -INFINITY;
