@@ -327,7 +327,9 @@ PA_API pa_status pa_decode_no_alloc(const pa_cache_desc* desc, const void* q, in
  *   scale            softmax scale (host), finite and > 0.
  *   out              [num_tokens, num_q_heads, head_dim] contiguous.
  * bf16 with head_dim 128 runs on the tcgen05 tensor cores; other cases on a
- * CUDA-core kernel.
+ * CUDA-core kernel.  Keys of a page that is out of range (PA_DEVERR_BAD_PAGE)
+ * are left out by the latter; the former takes them as rows of zeros (score 0,
+ * value 0).
  *   workspace        optional device buffer (256-byte aligned) of
  *                    workspace_bytes >= pa_prefill_workspace_size(...), used
  *                    only by the tensor-core path; owned by the caller, not

@@ -1035,6 +1035,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           fence_async_smem();
           __syncwarp();
         }
+        // rows that are not copied because their page is out of range are zero, too
+        const bool no_full = pf != kNoPage && y_full < 0, no_rem = pr != kNoPage && y_rem < 0;
+        if (__any_sync(0xffffffffu, (isv != 0) == vrole && (no_full || no_rem))) {
+          if ((isv != 0) == vrole) {
+            uint4* rows = reinterpret_cast<uint4*>(stage + half * kHalfBytes);
+            for (int c = 0; c < (no_full ? kBoxRows * 8 : 0); ++c) rows[box * kBoxRows * 8 + c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < (no_rem ? rem * 8 : 0); ++c) rows[nfull * kBoxRows * 8 + c] = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+          }
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
         __syncwarp();
         if ((isv != 0) == vrole) {
