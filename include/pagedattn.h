@@ -475,7 +475,8 @@ PA_API pa_status pa_prefill_qk_norm_rope_kv_write_q4(
  * (context_lens[b] == 0) and rows from cu_rows[batch] on are left as they are.
  * With cu_rows stepping by whole pages, k_out and v_out are a paged cache of
  * desc's dtype, request b's pages following each other from cu_rows[b] /
- * page_size: what pa_prefill_varlen attends to.
+ * page_size: what pa_prefill_varlen attends to, by the tables of
+ * pa_kv_read_q4_tables.
  *
  *   cu_rows          int32 [batch+1], 0 = cu[0] <= cu[1] <= ...
  *   starts           int32 [batch], each >= 0, or NULL: every request from token 0.
@@ -491,6 +492,22 @@ PA_API pa_status pa_kv_read_q4(const pa_cache_desc* desc, int32_t group_size, in
                                int32_t max_pages_per_seq, int64_t num_rows, const void* k_cache, const void* v_cache,
                                void* k_out, int64_t k_row_stride, void* v_out, int64_t v_row_stride,
                                pa_stream_t stream);
+
+/*
+ * pa_kv_read_q4_tables -- block tables of the paged cache that a pa_kv_read_q4
+ * of whole pages filled.  Entry j of request b is page cu_rows[b] / page_size +
+ * j where the 4-bit cache's table names a page of it as entry j, and -1 where it
+ * does not (no row of that page was read: k_out and v_out hold what they held
+ * before, so attention has to skip and flag it as over the table itself), where
+ * the request has no such page among its rows, and past the table's end.
+ *
+ *   cu_rows          as in pa_kv_read_q4, multiples of page_size.
+ *   block_tables     int32 [batch, max_pages_per_seq], the 4-bit cache's.
+ *   tables_out       int32 [batch, max_pages_out] out.
+ */
+PA_API pa_status pa_kv_read_q4_tables(const pa_cache_desc* desc, int32_t batch, const int32_t* cu_rows,
+                                      const int32_t* block_tables, int32_t max_pages_per_seq, int32_t* tables_out,
+                                      int32_t max_pages_out, pa_stream_t stream);
 
 /* Bytes of device workspace pa_decode_q4 and pa_decode_kv_write_q4 need; as
  * pa_decode_workspace_size. */

@@ -98,6 +98,7 @@ _SIGS = {
     "pa_prefill_qk_norm_rope_kv_write_q4": (_I32, [_DESC, _I32, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _I32, _VP,
                                                    _VP, _I32, _VP, _VP, _F32, _F32, _VP, _VP, _VP, _VP, _VP, _VP]),
     "pa_kv_read_q4": (_I32, [_DESC, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP]),
+    "pa_kv_read_q4_tables": (_I32, [_DESC, _I32, _VP, _VP, _I32, _VP, _I32, _VP]),
     "pa_decode_q4_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _I32]),
     "pa_decode_q4": (_I32, [_DESC, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _F32, _I32, _VP, _VP,
                             ctypes.c_size_t, _VP]),
@@ -390,6 +391,14 @@ def pa_kv_read_q4(desc, group_size, batch, cu_rows, starts, context_lens, block_
     _check("pa_kv_read_q4", lib.pa_kv_read_q4(
         desc, group_size, batch, cu, starts, ctx, bt, max_pages_per_seq, num_rows, kc, vc, ko, k_row_stride, vo,
         v_row_stride, st))
+
+
+def pa_kv_read_q4_tables(desc, batch, cu_rows, block_tables, max_pages_per_seq, tables_out, max_pages_out,
+                         stream=None):
+    """Block tables of the paged cache that a ``pa_kv_read_q4`` of whole pages filled: -1 where no page was read."""
+    _check("pa_kv_read_q4_tables", load_library().pa_kv_read_q4_tables(
+        desc, batch, _at(cu_rows), _at(block_tables), max_pages_per_seq, _at(tables_out), max_pages_out,
+        _stream(stream)))
 
 
 def pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas=0) -> int:

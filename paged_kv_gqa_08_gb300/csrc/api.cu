@@ -690,6 +690,30 @@ pa_status pa_kv_read_q4(const pa_cache_desc* desc, int32_t group_size, int32_t b
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+pa_status pa_kv_read_q4_tables(const pa_cache_desc* desc, int32_t batch, const int32_t* cu_rows,
+                               const int32_t* block_tables, int32_t max_pages_per_seq, int32_t* tables_out,
+                               int32_t max_pages_out, pa_stream_t stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (batch < 0 || max_pages_per_seq < 1 || max_pages_out < 1) return PA_ERR_SHAPE;
+  if (static_cast<int64_t>(batch) * max_pages_out >= int64_t(1) << 38) return PA_ERR_SHAPE;
+  if (batch == 0) return PA_OK;
+  if (!cu_rows || !block_tables || !tables_out) return PA_ERR_NULL;
+  Q4TablesParams p{};
+  p.cu = cu_rows;
+  p.bt = block_tables;
+  p.out = tables_out;
+  p.num_pages = desc->num_pages;
+  p.batch = batch;
+  p.maxp = max_pages_per_seq;
+  p.maxp_out = max_pages_out;
+  while ((1 << p.log2P) < desc->page_size) ++p.log2P;
+  unsigned int* err = nullptr;
+  if ((st = prepare(&err)) != PA_OK) return st;
+  cudaError_t e = launch_kv_read_tables(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t group_size, int32_t batch,
                                    int32_t max_context_len, int32_t max_ctas) {
   if (check_q4(desc, group_size) != PA_OK || batch < 1 || max_context_len < 1 || max_ctas < 0) return 0;

@@ -141,6 +141,15 @@ struct Q4ReadParams {
 };
 cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, Q4ReadParams p, cudaStream_t s);
 
+struct Q4TablesParams {
+  const int32_t* cu;
+  const int32_t* bt;
+  int32_t* out;
+  int64_t num_pages;
+  int32_t batch, maxp, maxp_out, log2P;
+};
+cudaError_t launch_kv_read_tables(const Q4TablesParams& p, cudaStream_t s);
+
 // ---------------------------------------------------------------------------
 // decode
 // ---------------------------------------------------------------------------

@@ -181,6 +181,22 @@ __global__ void __launch_bounds__(kQ4Threads) kv_read_q4_kernel(const Q4ReadPara
   }
 }
 
+// ---------------------------------------------------------------------------
+// block tables of the rows read back: a thread takes an entry
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kQ4Threads) kv_read_tables_kernel(const Q4TablesParams p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kQ4Threads + threadIdx.x;
+  if (i >= static_cast<int64_t>(p.batch) * p.maxp_out) return;
+  const int b = static_cast<int>(i / p.maxp_out), j = static_cast<int>(i - static_cast<int64_t>(b) * p.maxp_out);
+  const int first = p.cu[b], end = p.cu[b + 1];
+  int page = -1;
+  if (j < p.maxp && first >= 0 && first + (static_cast<int64_t>(j + 1) << p.log2P) <= end) {
+    const int src = p.bt[static_cast<int64_t>(b) * p.maxp + j];
+    if (src >= 0 && src < p.num_pages) page = (first >> p.log2P) + j;
+  }
+  p.out[i] = page;
+}
+
 template <typename T, int HD>
 const void* write_fn(int gs) {
   if constexpr (HD == 128)
@@ -211,6 +227,13 @@ cudaError_t launch_kv_write_q4(const pa_cache_desc& d, int gs, const Q4WritePara
   void* args[] = {const_cast<Q4WriteParams*>(&p)};
   e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kQ4Threads), args, 0, s);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_kv_read_tables(const Q4TablesParams& p, cudaStream_t s) {
+  const int64_t n = static_cast<int64_t>(p.batch) * p.maxp_out;
+  const int64_t blocks = (n + kQ4Threads - 1) / kQ4Threads;  // (below 2^31: the caller's check)
+  kv_read_tables_kernel<<<static_cast<unsigned>(blocks), kQ4Threads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read_q4(const pa_cache_desc& d, int gs, Q4ReadParams p, cudaStream_t s) {

@@ -19,7 +19,7 @@ from typing import Optional
 import torch
 
 from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedAttnError, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
-               pa_kv_read_q4, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
+               pa_kv_read_q4, pa_kv_read_q4_tables, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
                pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step, pa_prefill_varlen, pa_prefill_workspace_size,
                pa_slot_mapping)
 
@@ -27,7 +27,8 @@ from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedA
 @dataclasses.dataclass
 class Staging:
     """Where a prefill step over a 4-bit cache reads the contexts back to: a paged cache of the descriptor's dtype
-    in which request b has the ``max_pages`` pages from ``b * max_pages`` on."""
+    in which request b has the ``max_pages`` pages from ``b * max_pages`` on.  Each step writes its own block tables:
+    they leave out the pages that its read-back could not fill."""
     desc: object                       # the staging cache's descriptor
     max_pages: int
     cu_rows: torch.Tensor              # int32 [batch + 1]
@@ -88,7 +89,7 @@ def alloc_step_buffers(desc, kind: str, num_tokens: int, batch: int, max_context
         shape = (pages, P, desc.num_kv_heads, desc.head_dim)
         staging = Staging(cache_desc(desc.num_q_heads, desc.num_kv_heads, desc.head_dim, P, pages, dt), max_pages,
                           torch.arange(0, pages * P + 1, max_pages * P, dtype=torch.int32, device=device),
-                          torch.arange(pages, dtype=torch.int32, device=device).view(-1, max_pages),
+                          torch.empty(max(batch, 1), max_pages, dtype=torch.int32, device=device),
                           torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device))
     return StepBuffers(positions, slots, out, q_out, ws, max_ctas, group_size, staging)
 
@@ -193,8 +194,8 @@ def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_con
 
 def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, scale,
                  max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps, rope_theta, stream):
-    """The step over a 4-bit cache.  A prefill step whose metadata is flagged as bad (``pa_read_device_errors``)
-    attends, where a page was skipped, to what the staging cache held there before."""
+    """The step over a 4-bit cache.  What is skipped and flagged (``pa_read_device_errors``) is as over other caches: the
+    staging cache's block tables have no page where the 4-bit cache's name none of it."""
     n, batch, gs = q.shape[0], context_lens.shape[0], bufs.group_size
     _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
                    k_norm_w)
@@ -216,6 +217,7 @@ def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_ta
     row = desc.num_kv_heads * desc.head_dim
     pa_kv_read_q4(desc, gs, batch, st.cu_rows, None, context_lens, block_tables, max_pages_per_seq,
                   batch * st.max_pages * desc.page_size, k_cache, v_cache, st.k, row, st.v, row, stream)
+    pa_kv_read_q4_tables(desc, batch, st.cu_rows, block_tables, max_pages_per_seq, st.block_tables, st.max_pages, stream)
     pa_prefill_varlen(st.desc, q, cu_seqlens_q, batch, max_seqlen_q, n, st.k, st.v, st.block_tables, st.max_pages,
                       context_lens, max_context_len, scale, bufs.out, bufs.workspace, None, stream)
     return bufs.out

@@ -353,3 +353,16 @@ def test_steps_that_are_not_refused(enqueued):
     a["bufs"].workspace = None                                      # prefill takes none, too
     run_step(**a)
     assert enqueued.count("pa_prefill_varlen") == 4 and enqueued.count("pa_decode_q4") == 2
+
+
+def test_read_back_tables_refusals(lib):
+    def call(desc=None, batch=2, cu=FAKE, bt=FAKE, maxp=4, out=FAKE, maxp_out=4):
+        return lib.pa_kv_read_q4_tables(ctypes.byref(desc or _desc()), batch, cu, bt, maxp, out, maxp_out, None)
+
+    assert call(batch=0) == pa.PA_OK
+    assert call(desc=_desc(dtype=7)) == pa.PA_ERR_DTYPE
+    assert call(desc=_desc(page_size=24)) == pa.PA_ERR_UNSUPPORTED
+    for bad in (dict(batch=-1), dict(maxp=0), dict(maxp_out=0), dict(batch=1 << 20, maxp_out=1 << 20)):
+        assert call(**bad) == pa.PA_ERR_SHAPE
+    for bad in (dict(cu=None), dict(bt=None), dict(out=None)):
+        assert call(**bad) == pa.PA_ERR_NULL
