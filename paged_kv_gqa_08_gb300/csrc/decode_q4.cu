@@ -155,7 +155,10 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // for each group), so that every sum of products with codes is exact; the two sums
 // and those of 16 tokens are added in fp32.  The second terms and the softmax sum are
 // fp32 multiply-adds of the lanes: the terms cancel to a fifth or less, and what a
-// tensor core's additions cut off (1e-7 of the largest) would show.  One consumer
+// tensor core's additions cut off (1e-7 of the largest) would show.  For the same
+// reason the 16 tokens' p m join their p s u before either enters O: summed apart over
+// a share the two grow with its tokens, their difference with the root of these, and it
+// kept their rounding (2.9e-4 of the outputs at 20000 tokens; now 3e-6).  One consumer
 // group, whose warps may have 168 registers.
 //
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in
@@ -327,8 +330,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   [[maybe_unused]] uint32_t qm = 0u;               // 2^-10 (16 sum q, sum q) over the dims of group tq
   [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // fp32: what qf lacks,
   [[maybe_unused]] float q_sum[NG][2];             // and 2^-10 times the sums, for heads 2 tq and 2 tq + 1
-  // fp32: this lane's share of the sums over the tokens of p and of p m
-  [[maybe_unused]] float l_sum[2] = {0.f, 0.f}, pm_sum[NG][2];
+  [[maybe_unused]] float l_sum[2] = {0.f, 0.f};  // fp32: this lane's share of the sum over the tokens of p
   float o[MB][4];
   // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
   // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
@@ -436,8 +438,6 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         limit = -INFINITY;
         om[0] = om[1] = om[2] = om[3] = 0.f;
         l_sum[0] = l_sum[1] = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) pm_sum[g][0] = pm_sum[g][1] = 0.f;
         s_most = 0u;
       }
       if (flags & kNew) {
@@ -536,11 +536,6 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         if constexpr (kF32) {
           l_sum[0] *= a0;
           l_sum[1] *= a1;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            pm_sum[g][0] *= a0;
-            pm_sum[g][1] *= a1;
-          }
         }
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
@@ -621,26 +616,28 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
       if constexpr (kF32) {
         l_sum[0] += t[hf][0] + t[hf][2];
         l_sum[1] += t[hf][1] + t[hf][3];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float m = fmaf(16.f, f16_lo(vpar[hf][u][g]), f16_lo(vpar[hf][u][g] >> 16));
-            pm_sum[g][0] = fmaf(t[hf][2 * u], m, pm_sum[g][0]);
-            pm_sum[g][1] = fmaf(t[hf][2 * u + 1], m, pm_sum[g][1]);
-          }
       } else {
         mma_f16(om, vm[2 * hf], kOnes, vm[2 * hf + 1], kOnes, pb[hf][0], pb[hf][1]);
       }
       uint32_t x[4];  // of two pieces: half word gq of tokens 2 tq, 2 tq + 1 and of those 8 on
       uint32_t b0, b1;
       [[maybe_unused]] uint32_t l0, l1;
-      [[maybe_unused]] float undo[2];  // the powers of two that the products of heads 2 tq, 2 tq + 1 lack
+      [[maybe_unused]] float undo[2];  // the powers of two that the products of heads 2 tq, 2 tq + 1 lack,
+      [[maybe_unused]] float pm[2];    // and the sums of p m over the 16 tokens
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (i % 2 == 0) ldsm4_trans(x, st + kChunk + hf * kHalf * R + c_at[i / 2]);
-        if (i % PG == 0 && kF32) {  // p s of the group
-          float x[4], hi[4], lo[4];
+        if (i % PG == 0 && kF32) {  // p s and p m of the group
+          float x[4], hi[4], lo[4], m[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            m[u] = fmaf(16.f, f16_lo(vpar[hf][u][i / PG]), f16_lo(vpar[hf][u][i / PG] >> 16));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            pm[e] = fmaf(t[hf][2 + e], m[1], t[hf][e] * m[0]);
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) pm[e] += __shfl_xor_sync(0xffffffffu, pm[e], k);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = t[hf][e] * f16_lo(vpar[hf][e / 2][i / PG]);
 #pragma unroll
@@ -673,8 +670,8 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
           mma_f16(d[3], raw_lo(x0), raw_lo(y0), raw_lo(x1), raw_lo(y1), l0, l1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            o[2 * i][e] = fmaf(d[0][e] + d[1][e], undo[e & 1], o[2 * i][e]);
-            o[2 * i + 1][e] = fmaf(d[2][e] + d[3][e], undo[e & 1] * 16.f, o[2 * i + 1][e]);
+            o[2 * i][e] += fmaf(d[0][e] + d[1][e], undo[e & 1], pm[e & 1]);
+            o[2 * i + 1][e] += fmaf(d[2][e] + d[3][e], undo[e & 1] * 16.f, pm[e & 1]);
           }
         } else {
           mma_f16(o[2 * i], raw_hi(x0), raw_hi(y0), raw_hi(x1), raw_hi(y1), b0, b1);
@@ -696,29 +693,24 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l_sum[e] += __shfl_xor_sync(0xffffffffu, l_sum[e], k);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) pm_sum[g][e] += __shfl_xor_sync(0xffffffffu, pm_sum[g][e], k);
-          }
+          for (int e = 0; e < 2; ++e) l_sum[e] += __shfl_xor_sync(0xffffffffu, l_sum[e], k);
         l[0] = l_sum[0];
         l[1] = l_sum[1];
-      }
-      // the powers of two undone, the second term added
-      const float hi = kF32 ? 1.f : __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23);
-      const float lo = kF32 ? 1.f : hi * 16.f;
+      } else {
+        // the powers of two undone, the second term added
+        const float hi = __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23), lo = hi * 16.f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float add[2];
+        for (int g = 0; g < NG; ++g) {
+          float add[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          add[e] = kF32 ? pm_sum[g][e]
-                        : fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
-                               __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
+          for (int e = 0; e < 2; ++e)
+            add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
+                          __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
 #pragma unroll
-        for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
+          for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
+            for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
+        }
       }
       if (flags & kYield) {
         // hand this group's part over: once the previous one has been taken

@@ -1,0 +1,118 @@
+"""Decode over a 4-bit cache against float64, each output held to a bound of its own: what its rounding steps can do to
+it, whatever the rest of the batch holds.  Contexts that one CTA sums alone, queries and keys of unequal magnitude, keys
+that take nearly all the weight, tokens whose loss would show."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_gqa_08_gb300 as pa
+from oracle import q4_cache as q4
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("cuda_lib")]
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+
+
+class Batch:
+    """A decode batch over a 4-bit cache of given K and V rows: k[b], v[b] are fp32 [len, hkv, hd], q [batch, hq, hd]."""
+
+    def __init__(self, dtype, hkv, gs, P, q, k, v, scale=None, seed=0):
+        rng = np.random.default_rng(seed)
+        B, hq, hd = q.shape
+        self.dtype, self.gs, self.hq, self.hkv, self.hd, self.P = dtype, gs, hq, hkv, hd, P
+        self.lens = np.array([len(x) for x in k], np.int32)
+        npg = -(-self.lens // P)
+        self.pages, self.maxp = int(npg.sum()) + 1, int(npg.max())
+        self.bt = np.full((B, self.maxp), self.pages - 1, np.int32)
+        perm = rng.permutation(self.pages - 1)
+        at = np.concatenate([[0], np.cumsum(npg)])
+        self.slots = []
+        for b in range(B):
+            self.bt[b, : npg[b]] = perm[at[b]: at[b + 1]]
+            t = np.arange(self.lens[b])
+            self.slots.append(self.bt[b, t // P].astype(np.int64) * P + t % P)
+        self.desc = pa.cache_desc(hq, hkv, hd, P, self.pages, DT[dtype])
+        self.caches, self.vals = [], []
+        for x in (k, v):
+            cache = rng.integers(0, 256, (self.pages * P, q4.row_bytes(hkv, hd, gs))).astype(np.uint8)
+            vals = []
+            for b in range(B):
+                u, s, c = q4.quantise(np.asarray(x[b], np.float32), gs)
+                cache[self.slots[b]] = q4.pack_rows(u, s, c, self.slots[b])
+                m = np.repeat(16 * s.astype(np.float64) + c.astype(np.float64), gs, -1)
+                vals.append((q4.values(u, s, c, gs), m))    # the values, and of each what its code 0 stands for
+            self.caches.append(torch.from_numpy(cache).cuda())
+            self.vals.append(vals)
+        self.q = torch.from_numpy(np.asarray(q, np.float32)).to(DT[dtype]).cuda()
+        self.scale = hd ** -0.5 if scale is None else scale
+        self.ctx, self.btd = torch.from_numpy(self.lens).cuda(), torch.from_numpy(self.bt).cuda()
+
+    def decode(self, max_ctas=0):
+        longest = int(self.lens.max())
+        n = pa.pa_decode_q4_workspace_size(self.desc, self.gs, len(self.lens), longest, max_ctas)
+        out = torch.full_like(self.q, 7.0)
+        pa.pa_decode_q4(self.desc, self.gs, self.q, len(self.lens), *self.caches, self.btd, self.maxp, self.ctx,
+                        longest, self.scale, max_ctas, out, torch.empty(n, dtype=torch.uint8, device="cuda"))
+        return out.double().cpu().numpy()
+
+    def reference(self):
+        """Outputs in float64 and their bounds.
+
+        With p the weights (sum 1), v = s u + m a value, u = 2^-24.  Rounding to nearest errs to either side, so errors
+        of many terms add like their squares; eight times that is allowed, and what a few terms can do at most.
+
+        bf16: the output is rounded (2^-8 of it); p and p s are float16 (2^-11 each), the first in sum and products
+        alike: 2^-11 p (|v - o| + |s u|) a term.
+
+        fp32: the two sums of 16 tokens round a few times (16 u of p (|s u| + |m|)); o grows by one addition for every
+        16 tokens, each u / 2 of what it has come to (at most about the largest output of the head); a weight is off by
+        the exponential's 4 u and by its score's rounding, some 10 u: 64 u of sqrt(sum p^2) times the largest value."""
+        outs, bounds = [], []
+        q64 = self.q.double().cpu().numpy()
+        for b in range(len(self.lens)):
+            K, (V, M) = self.vals[0][b][0], self.vals[1][b]
+            G = self.hq // self.hkv
+            o, e = np.empty((self.hq, self.hd)), np.empty((self.hq, self.hd))
+            for h in range(self.hq):
+                v, m = V[:, h // G], M[:, h // G]
+                t = K[:, h // G] @ q64[b, h] * self.scale
+                p = np.exp(t - t.max())
+                p /= p.sum()
+                o[h] = p @ v
+                su = np.abs(v - m)
+                if self.dtype == "bf16":
+                    term = p[:, None] * (np.abs(v - o[h]) + su)
+                    e[h] = 2.0 ** -8 * (np.abs(o[h]) + np.sqrt((term ** 2).sum(0))) + 2.0 ** -18 * (p @ (su + np.abs(m)))
+                else:
+                    n = np.sqrt(-(-len(v) // 16))
+                    e[h] = U * (16 * (p @ (su + np.abs(m))) / n + 2 * n * np.abs(o[h]).max()
+                                + 64 * np.sqrt((p ** 2).sum()) * np.abs(v).max())
+            outs.append(o)
+            bounds.append(e)
+        return np.stack(outs), np.stack(bounds)
+
+    def check(self, *splits):
+        ref, bound = self.reference()
+        for max_ctas in splits:
+            ratio = np.abs(self.decode(max_ctas) - ref) / bound
+            assert np.isfinite(ratio).all()
+            worst = ratio.reshape(len(self.lens), -1).max(1)
+            assert worst.max() <= 1, (max_ctas, worst)
+        assert pa.pa_read_device_errors(reset=True) == 0
+
+
+def normal(rng, lens, hkv, hd):
+    return [rng.standard_normal((n, hkv, hd)).astype(np.float32) for n in lens]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,hd,gs,P", [(4, 4, 128, 32, 16), (8, 2, 128, 64, 64), (7, 1, 128, 128, 32),
+                                            (8, 4, 64, 32, 16), (5, 1, 64, 64, 128)])
+@pytest.mark.parametrize("lens", [[64, 1000, 1, 17], [4096, 33, 20000]])
+def test_every_output_is_within_its_own_bound(dtype, hq, hkv, hd, gs, P, lens):
+    """Values without a mean, so that outputs shrink as the context grows, summed by one CTA and by many."""
+    rng = np.random.default_rng(hq + hd + gs)
+    c = Batch(dtype, hkv, gs, P, rng.standard_normal((len(lens), hq, hd)), normal(rng, lens, hkv, hd),
+              normal(rng, lens, hkv, hd))
+    c.check(1, 0, 7)
