@@ -151,23 +151,25 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // registers, 228 with raw codes loaded as words and paired by byte permutes.
 //
 // fp32 queries and outputs.  Queries and p s are two float16 numbers each, multiples
-// of 2^-11 and 2^-23 of their bounds (p s: of the largest among a head's 16 tokens,
-// for each group), so that every sum of products with codes is exact; the two sums
-// and those of 16 tokens are added in fp32.  The second terms and the softmax sum are
-// fp32 multiply-adds of the lanes: the terms cancel to a fifth or less, and what a
-// tensor core's additions cut off (1e-7 of the largest) would show.  For the same
-// reason the 16 tokens' p m join their p s u before either enters O: summed apart over
-// a share the two grow with its tokens, their difference with the root of these, and it
-// kept their rounding (2.9e-4 of the outputs at 20000 tokens; now 3e-6).  One consumer
-// group, whose warps may have 168 registers.
+// of 2^-11 and 2^-23 of their bounds, so that every sum of products with codes is
+// exact; the two sums and those of 16 tokens are added in fp32.  The bounds are those
+// of a head's group of dims (p s: among 16 tokens): keys of one group may be far
+// smaller than another's, and a query that is large there must not coarsen the rest
+// (with one bound for a head, outputs were off by 1e-4 where queries of one group were
+// 2^10 times the others' and its keys as much smaller).  The second terms and the
+// softmax sum are fp32 multiply-adds of the lanes: the terms cancel to a fifth or less,
+// and what a tensor core's additions cut off (1e-7 of the largest) would show.  For the
+// same reason the 16 tokens' p m join their p s u before either enters O: summed apart
+// over a share the two grow with its tokens, their difference with the root of these,
+// and it kept their rounding (2.9e-4 of the outputs at 20000 tokens; now 3e-6).  One
+// consumer group, whose warps may have 168 registers.
 //
-// Ranges.  Queries are scaled by a power of two to a largest magnitude in
-// [1, 2).  Probabilities stay below 2^8 (their reference follows the maximum
-// when a score passes it by more).  p s is kept in float16's range by a power of
-// two 2^-E that follows the largest s seen (a group whose s is more than 2^17 below
-// that has fewer bits in p s).  Each rounding to float16 is 2^-11
-// relative, finer than the bf16 of queries and outputs; sums and statistics are
-// fp32.
+// Ranges.  Queries are scaled by a power of two to a largest magnitude in [2^8, 2^9)
+// (of the head; fp32: of each group).  Probabilities stay below 2^8 (their reference
+// follows the maximum when a score passes it by more).  p s is kept in float16's range
+// by a power of two 2^-E that follows the largest s seen (a group whose s is more than
+// 2^17 below that has fewer bits in p s).  Each rounding to float16 is 2^-11 relative,
+// finer than the bf16 of queries and outputs; sums and statistics are fp32.
 // ---------------------------------------------------------------------------
 PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -329,7 +331,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
   [[maybe_unused]] uint32_t qm = 0u;               // 2^-10 (16 sum q, sum q) over the dims of group tq
   [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // fp32: what qf lacks,
-  [[maybe_unused]] float q_sum[NG][2];             // and 2^-10 times the sums, for heads 2 tq and 2 tq + 1
+  [[maybe_unused]] float q_sum[NG][2];             // and the sums, times mult, for heads 2 tq and 2 tq + 1
   [[maybe_unused]] float l_sum[2] = {0.f, 0.f};  // fp32: this lane's share of the sum over the tokens of p
   float o[MB][4];
   // Sums over the tokens: [0..1] of p s or p c (row gq of the parameter piece),
@@ -338,7 +340,8 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   // The largest s with the exponent of the largest seen, twice (0: none above 0
   // yet).  With that exponent's bits x, E = max(x - 21, -15).  (Not for fp32.)
   uint32_t s_most = 0u;
-  float mult[2] = {0.f, 0.f};  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone)
+  // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone); fp32: of each group
+  float mult[kF32 ? NG : 1][2];
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
   float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
   uint32_t hand_phase = 0;     // parity of the handovers so far
@@ -356,7 +359,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
       if (flags & kFirst) {
         const uint32_t qrow = st + 2 * kChunk + (h * G + gq) * HD * sizeof(T);
         float qv[NP][8];  // eight dims of each piece
-        float mx = 0.f;
+        float mx[kF32 ? NG : 1] = {};
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint32_t w[8] = {};
@@ -375,14 +378,22 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
               qv[i][e] = v.x;
               qv[i][e + 1] = v.y;
             }
-            mx = fmaxf(mx, fmaxf(fabsf(qv[i][e]), fabsf(qv[i][e + 1])));
+            float& most = mx[kF32 ? i / PG : 0];
+            most = fmaxf(most, fmaxf(fabsf(qv[i][e]), fabsf(qv[i][e + 1])));
           }
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^-E of the largest magnitude's exponent E, and 2^E
-        const uint32_t eb = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-        const float down = __uint_as_float((254u - eb) << 23), up = __uint_as_float(eb << 23) * p.k.scale_log2;
+        // 2^-E of the largest magnitude's exponent E (fp32: of each group's), and 2^E
+        float down[kF32 ? NG : 1];
+#pragma unroll
+        for (int g = 0; g < (kF32 ? NG : 1); ++g) {
+          mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 1));
+          mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 2));
+          const uint32_t eb = min(max(__float_as_uint(mx[g]) >> 23, 1u), 253u);
+          down[g] = __uint_as_float((254u - eb) << 23);
+          const float up = __uint_as_float(eb << 23) * p.k.scale_log2;
+          mult[g][0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
+          mult[g][1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
+        }
         qm = 0u;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -395,7 +406,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
             // as they are rounded: the second term's sum has to be that of the first's queries
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float x = q[e] * down * 256.f;  // below 2^9
+              const float x = q[e] * down[kF32 ? g : 0] * 256.f;  // below 2^9
               if constexpr (kF32) {
                 split<-2>(x, q[e], l[e]);
                 sum_l += l[e];
@@ -421,15 +432,13 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
             sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 1);
             sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 2);
             sum += sum_l;
-            q_sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * tq) * 0x1p-18f;
-            q_sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4) * 0x1p-18f;
+            q_sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * tq) * 0x1p-18f * mult[g][0];
+            q_sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4) * 0x1p-18f * mult[g][1];
           } else {
             const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
             if (tq == g) qm = pack_f16x2(r * 16.f, r);
           }
         }
-        mult[0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
-        mult[1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
 #pragma unroll
         for (int j = 0; j < MB; ++j)
 #pragma unroll
@@ -492,16 +501,18 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
             for (int e = 0; e < 4; ++e) {
               d[e] += dl[e];
               sc[e] = fmaf(e < 2 ? m0 : m1, q_sum[i / PG][e & 1], sc[e]);
+              sc[e] = fmaf(d[e], (e < 2 ? s0 : s1) * mult[i / PG][e & 1], sc[e]);
             }
+          } else {
+            sc[0] = fmaf(d[0], s0, sc[0]);
+            sc[1] = fmaf(d[1], s0, sc[1]);
+            sc[2] = fmaf(d[2], s1, sc[2]);
+            sc[3] = fmaf(d[3], s1, sc[3]);
           }
-          sc[0] = fmaf(d[0], s0, sc[0]);
-          sc[1] = fmaf(d[1], s0, sc[1]);
-          sc[2] = fmaf(d[2], s1, sc[2]);
-          sc[3] = fmaf(d[3], s1, sc[3]);
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[hf][e] = fmaf(sc[e], mult[e & 1], -m[e & 1]);
+      for (int e = 0; e < 4; ++e) t[hf][e] = kF32 ? sc[e] - m[e & 1] : fmaf(sc[e], mult[0][e & 1], -m[e & 1]);
     }
 
     // softmax: exponents relative to a reference that only moves when a score

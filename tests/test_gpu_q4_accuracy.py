@@ -116,3 +116,18 @@ def test_every_output_is_within_its_own_bound(dtype, hq, hkv, hd, gs, P, lens):
     c = Batch(dtype, hkv, gs, P, rng.standard_normal((len(lens), hq, hd)), normal(rng, lens, hkv, hd),
               normal(rng, lens, hkv, hd))
     c.check(1, 0, 7)
+
+
+@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("gs", [32, 64])
+@pytest.mark.parametrize("ratio", [8, 11, 14])
+def test_groups_of_unequal_query_magnitude(dtype, gs, ratio):
+    """The queries of a head's first group are 2^ratio times the others', its keys as much smaller: every group counts
+    alike in a score."""
+    rng = np.random.default_rng(ratio)
+    lens = [500, 77, 3000]
+    a = np.full(128, 2.0 ** (-ratio / 2))
+    a[:gs] = 2.0 ** (ratio / 2)
+    k = [(x / a).astype(np.float32) for x in normal(rng, lens, 2, 128)]
+    c = Batch(dtype, 2, gs, 16, rng.standard_normal((3, 6, 128)) * a, k, normal(rng, lens, 2, 128))
+    c.check(1, 0)
