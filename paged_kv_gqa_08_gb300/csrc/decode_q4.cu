@@ -140,8 +140,9 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // subnormal float16 u * 2^-18 (2^-22), exact, one mask.  With m = 16 s + c the
 // value is s u + m, so
 //   S = sum over groups of s (sum q u) + m (sum q):  the sums of q u are scaled
-//       by s as they leave the tensor cores, the second term is one m16n8k8
-//       product of the parameter words (s, c) with (16 sum q, sum q);
+//       by s as they leave the tensor cores, the second term is one product of the
+//       parameter words (s, c) with (16 sum q, sum q), each sum as two float16
+//       numbers;
 //   O = sum over tokens of (p s) u + p m:  p s replaces p as the B operand, and
 //       the second term is one product of the transposed parameter piece, whose
 //       rows are its groups' s and c, with p.  The product's other eight rows
@@ -178,11 +179,12 @@ PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// d = A B with 8 columns of A.
-PA_DEVINL void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+// d = A (B0 + B1) with 8 columns of A.
+PA_DEVINL void mma_f16_twice(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %4, %5}, {%6, %7}, "
+      "{%8, %8, %8, %8};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+      : "r"(a0), "r"(a1), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held two to a lane.
@@ -329,7 +331,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, smem0 + p.k.off_abort, p.k.err); };
 
   uint32_t qf[MB][2];  // B fragments of the queries: 2^8 q where codes are at bits 6-9, 2^12 q where at 2-5
-  [[maybe_unused]] uint32_t qm = 0u;               // 2^-10 (16 sum q, sum q) over the dims of group tq
+  [[maybe_unused]] uint32_t qm[2] = {};            // 2^2 (16 sum q, sum q) over the dims of group tq, and what it lacks
   [[maybe_unused]] uint32_t ql[kF32 ? MB : 1][2];  // fp32: what qf lacks,
   [[maybe_unused]] float q_sum[NG][2];             // and the sums, times mult, for heads 2 tq and 2 tq + 1
   [[maybe_unused]] float l_sum[2] = {0.f, 0.f};  // fp32: this lane's share of the sum over the tokens of p
@@ -394,7 +396,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
           mult[g][0] = __shfl_sync(0xffffffffu, up, 8 * tq) * 1024.f;
           mult[g][1] = __shfl_sync(0xffffffffu, up, 8 * tq + 4) * 1024.f;
         }
-        qm = 0u;
+        qm[0] = qm[1] = 0u;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float sum = 0.f;
@@ -435,8 +437,12 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
             q_sum[g][0] = __shfl_sync(0xffffffffu, sum, 8 * tq) * 0x1p-18f * mult[g][0];
             q_sum[g][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4) * 0x1p-18f * mult[g][1];
           } else {
-            const float r = __half2float(__float2half_rn(sum * 0x1p-18f));
-            if (tq == g) qm = pack_f16x2(r * 16.f, r);
+            // (at most 2^10; the second term is as large as the first for keys with a mean)
+            const float r = __half2float(__float2half_rn(sum * 0x1p-6f)), rest = sum * 0x1p-6f - r;
+            if (tq == g) {
+              qm[0] = pack_f16x2(r * 16.f, r);
+              qm[1] = pack_f16x2(rest * 16.f, rest);
+            }
           }
         }
 #pragma unroll
@@ -476,7 +482,9 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
           if constexpr (NG == 4)
             pm[u] = (tq & 2) ? ((tq & 1) ? par[u][3] : par[u][2]) : ((tq & 1) ? par[u][1] : par[u][0]);
         }
-        mma_f16_k8(sc, pm[0], pm[1], qm);
+        mma_f16_twice(sc, pm[0], pm[1], qm[0], qm[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] *= 0x1p-12f;
       }
       uint32_t w[4];  // of two pieces: the words of tokens gq and gq + 8
 #pragma unroll

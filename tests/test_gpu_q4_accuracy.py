@@ -118,7 +118,7 @@ def test_every_output_is_within_its_own_bound(dtype, hq, hkv, hd, gs, P, lens):
     c.check(1, 0, 7)
 
 
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gs", [32, 64])
 @pytest.mark.parametrize("ratio", [8, 11, 14])
 def test_groups_of_unequal_query_magnitude(dtype, gs, ratio):
