@@ -518,8 +518,18 @@ PA_API size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t gro
  * pa_decode_q4 -- pa_decode over a 4-bit cache.  Arguments, padding rows, flags
  * and the split over CTAs as pa_decode, but short requests (max_context_len up
  * to some thousand tokens) take a CTA or a cluster of up to 8 CTAs each, where
- * batch * CTAs fit the GPU and max_ctas.  fp32 results are off by a few 2^-24 of
- * the values' magnitude, as a plain fp32 evaluation's.  q and out are device memory.
+ * batch * CTAs fit the GPU and max_ctas.  q and out are device memory.
+ *
+ * Accuracy, against the exact result for the values that the rows stand for.
+ * fp32: a few 2^-24 of the values' magnitude, as a plain fp32 evaluation's (some
+ * 10 of them where one CTA adds 20000 tokens up; measured 3e-6 of outputs whose
+ * values have no mean).  bf16: the output's rounding, and the float16 roundings
+ * (2^-11 each) of a token's weight p and of p s; weights below 2^-32 of a
+ * share's largest count as 0, and where p s is less than 2^-25 of the largest
+ * weight times the largest s that the share of the request holds (or s less
+ * than 2^-18 of that) it has fewer bits: values so far below others of the same
+ * kv-head, attended to or not, lose accuracy relative to their own size (about
+ * 1% at s of 2^-22 of the largest, a third at 2^-26).
  */
 PA_API pa_status pa_decode_q4(const pa_cache_desc* desc, int32_t group_size, const void* q, int32_t batch,
                               const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -166,10 +166,11 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 // consumer group, whose warps may have 168 registers.
 //
 // Ranges.  Queries are scaled by a power of two to a largest magnitude in [2^8, 2^9)
-// (of the head; fp32: of each group).  Probabilities stay below 2^8 (their reference
-// follows the maximum when a score passes it by more).  p s is kept in float16's range
-// by a power of two 2^-E that follows the largest s seen (a group whose s is more than
-// 2^17 below that has fewer bits in p s).  Each rounding to float16 is 2^-11 relative,
+// (of the head; fp32: of each group).  A head's largest probability lies between 2^7 and
+// 2^11 (their reference follows the maximum when a score passes it by more).  p s is kept
+// in float16's range by a power of two 2^-E that follows the largest s seen in the share:
+// s has all its bits down to 2^-18 of that, p s while weight times s is at least 2^-25 of
+// the largest weight times the largest s.  Each rounding to float16 is 2^-11 relative,
 // finer than the bf16 of queries and outputs; sums and statistics are fp32.
 // ---------------------------------------------------------------------------
 PA_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -208,6 +209,10 @@ PA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 PA_DEVINL float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w & 0xFFFFu))); }
 
+// A head's largest probability is 2^7 at first and at most 2^11, and s at most 2^5, so
+// that p s is a float16.  Probabilities down to 2^-21 of the largest have all of its
+// bits, and 2^20 tokens lose no more than 2^-12 of their weight to those below 2^-32.
+constexpr float kFirstMost = 7.f, kMost = 11.f;
 constexpr uint32_t kOnes = 0x3C003C00u;      // 1 twice
 constexpr uint32_t kExponent = 0x04000400u;  // the lowest exponent bit of a float16, twice
 
@@ -340,12 +345,12 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
   // [2..3] of p (the softmax sums of heads 2 tq, 2 tq + 1).
   float om[4] = {0.f, 0.f, 0.f, 0.f};
   // The largest s with the exponent of the largest seen, twice (0: none above 0
-  // yet).  With that exponent's bits x, E = max(x - 21, -15).  (Not for fp32.)
+  // yet).  With that exponent's bits x, E = max(x - 19, -15).  (Not for fp32.)
   uint32_t s_most = 0u;
   // score scale of heads 2 tq, 2 tq + 1 (base 2, the powers of two undone); fp32: of each group
   float mult[kF32 ? NG : 1][2];
   float m[2] = {0.f, 0.f};     // the exponents' reference of the two heads
-  float limit = -INFINITY;     // scores more than this above the reference move it: any at first, then 2^8
+  float limit = -INFINITY;     // scores above the reference by more than this move it: any at first, then kMost
   uint32_t hand_phase = 0;     // parity of the handovers so far
   Ring ring;
   if (group) ring.next(p.stages);  // group g takes stages g, g + 2, ... of the ring
@@ -523,8 +528,8 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
       for (int e = 0; e < 4; ++e) t[hf][e] = kF32 ? sc[e] - m[e & 1] : fmaf(sc[e], mult[0][e & 1], -m[e & 1]);
     }
 
-    // softmax: exponents relative to a reference that only moves when a score
-    // passes it by more than 2^8 (probabilities stay below 2^8: a float16)
+    // softmax: exponents relative to a reference that lies kFirstMost below the first
+    // maximum and moves up to kFirstMost below a score that passes it by more than kMost
     if (flags & kRagged) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -542,11 +547,11 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, k));
       }
       if (limit == -INFINITY) {  // the first scores: O and l are zero
-        if (d0 == -INFINITY) d0 = 0.f;
-        if (d1 == -INFINITY) d1 = 0.f;
+        d0 = d0 == -INFINITY ? 0.f : d0 - kFirstMost;
+        d1 = d1 == -INFINITY ? 0.f : d1 - kFirstMost;
       } else {
-        d0 = fmaxf(d0, 0.f);
-        d1 = fmaxf(d1, 0.f);
+        d0 = fmaxf(d0 - kFirstMost, 0.f);
+        d1 = fmaxf(d1 - kFirstMost, 0.f);
         const float a0 = ex2_approx(-d0), a1 = ex2_approx(-d1);
         om[0] *= a0;
         om[1] *= a1;
@@ -573,7 +578,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         t[hf][2] -= d0;
         t[hf][3] -= d1;
       }
-      limit = 8.f;
+      limit = kMost;
     }
     uint32_t pb[2][2];  // B fragments of the probabilities
 #pragma unroll
@@ -619,7 +624,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
       if (__any_sync(0xffffffffu, __vmaxu2(top, s_most) != s_most)) {
         const uint32_t bits = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 10, 1u);
         if (s_most != 0u) {
-          const float a = __uint_as_float((127u + max(s_most >> 26, 6u) - max(bits, 6u)) << 23);
+          const float a = __uint_as_float((127u + max(s_most >> 26, 4u) - max(bits, 4u)) << 23);
 #pragma unroll
           for (int j = 0; j < MB; ++j)
 #pragma unroll
@@ -628,8 +633,8 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         s_most = (((bits + 1) << 10) - 1) * 0x00010001u;
       }
     }
-    // 2^-E: the largest s becomes 2^6 .. 2^7 (less where that would need more than 2^15)
-    [[maybe_unused]] const uint32_t s_scale = 36u * kExponent - max(s_most & 0x7C007C00u, 6u * kExponent);
+    // 2^-E: the largest s becomes 2^4 .. 2^5 (less where that would need more than 2^15)
+    [[maybe_unused]] const uint32_t s_scale = 34u * kExponent - max(s_most & 0x7C007C00u, 4u * kExponent);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       if constexpr (kF32) {
@@ -717,7 +722,7 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         l[1] = l_sum[1];
       } else {
         // the powers of two undone, the second term added
-        const float hi = __uint_as_float((127u + 18 - 21 + max(s_most >> 26, 6u)) << 23), lo = hi * 16.f;
+        const float hi = __uint_as_float((127u + 18 - 19 + max(s_most >> 26, 4u)) << 23), lo = hi * 16.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float add[2];

@@ -131,3 +131,31 @@ def test_groups_of_unequal_query_magnitude(dtype, gs, ratio):
     k = [(x / a).astype(np.float32) for x in normal(rng, lens, 2, 128)]
     c = Batch(dtype, 2, gs, 16, rng.standard_normal((3, 6, 128)) * a, k, normal(rng, lens, 2, 128))
     c.check(1, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_keys_far_below_the_largest_score_still_add_up(dtype):
+    """One key's weight is 2^25 times each other's, of which there are 200000: together they hold half a percent."""
+    n, hd = 200000, 64
+    k, v = np.zeros((n, 1, hd), np.float32), np.ones((n, 1, hd), np.float32)
+    k[1000], v[1000] = 25.2 * np.log(2) / 8, 0.0
+    c = Batch(dtype, 1, 64, 256, np.ones((1, 4, hd)), [k], [v])
+    c.check(1, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [True, False])
+def test_values_far_below_the_largest_scale(dtype, first):
+    """One token's values are 2^18 times the others', its weight next to nothing: the others' outputs keep their bits."""
+    rng = np.random.default_rng(3)
+    lens = [2000, 300]
+    q = rng.standard_normal((2, 4, 128))
+    k, v = normal(rng, lens, 2, 128), normal(rng, lens, 2, 128)
+    for b in range(2):
+        at = 0 if first else lens[b] // 2
+        v[b] = v[b] * np.float32(2.0 ** -8)
+        v[b][at] *= np.float32(2.0 ** 18)
+        for h in range(2):
+            k[b][at, h] = -60 * q[b, 2 * h: 2 * h + 2].sum(0) / 128      # scores of -100 and below
+    c = Batch(dtype, 2, 64, 16, q, k, v, scale=0.18)
+    c.check(1, 0)
