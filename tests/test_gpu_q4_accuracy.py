@@ -159,3 +159,24 @@ def test_values_far_below_the_largest_scale(dtype, first):
             k[b][at, h] = -60 * q[b, 2 * h: 2 * h + 2].sum(0) / 128      # scores of -100 and below
     c = Batch(dtype, 2, 64, 16, q, k, v, scale=0.18)
     c.check(1, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,hd,gs,P", [(16, 8, 128, 32, 16), (8, 2, 128, 128, 64), (6, 2, 64, 64, 16)])
+@pytest.mark.parametrize("lens,splits", [([20011, 1, 9000], (0, 1, 2, 31)), ([700, 33, 1000, 0, 65] * 5, (0, 1, 3, 24)),
+                                         ([1000, 300, 31] * 50, (0, 7, 152))])
+def test_every_chunk_counts_once(dtype, hq, hkv, hd, gs, P, lens, splits):
+    """One token of every 32 has a value of 40 in a dim of its own (as many dims as the head has, in turn): a chunk lost
+    or taken twice changes some dim's output by a good part of it, whatever the rest of the batch holds."""
+    if max(lens) > 5000 and hkv == 8 and dtype == "f32":
+        lens = [5011, 1, 3000]
+    rng = np.random.default_rng(hd + gs)
+    live = [n for n in lens if n]
+    k, v = normal(rng, live, hkv, hd), normal(rng, live, hkv, hd)
+    for b, n in enumerate(live):
+        k[b] *= np.float32(0.3)
+        v[b] *= np.float32(0.1)
+        for i in range(0, -(-n // 32)):
+            v[b][min(n - 1, 32 * i + int(rng.integers(32))), :, i % hd] += np.float32(40)
+    c = Batch(dtype, hkv, gs, P, rng.standard_normal((len(live), hq, hd)), k, v)
+    c.check(*splits)
