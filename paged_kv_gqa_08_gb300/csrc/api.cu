@@ -210,6 +210,7 @@ pa_status norm_rope_params(const pa_cache_desc* desc, const void* q, int64_t q_r
   p.hkv = desc->num_kv_heads;
   for (int i = 0; i < desc->head_dim / 2; ++i) {
     const double f = pow(static_cast<double>(rope_theta), -2.0 * i / desc->head_dim);
+    p.inv_freq[i] = f;
     p.inv_freq_hi[i] = static_cast<float>(f);
     p.inv_freq_lo[i] = static_cast<float>(f - static_cast<double>(p.inv_freq_hi[i]));
   }

@@ -156,21 +156,34 @@ PA_DEVINL void two_sum(float a, float b, float& s, float& e) {
   e = (a - (s - bb)) + (b - bb);
 }
 
-// Sine and cosine of pos * (fh + fl), rounded to fp32 from about 2^-35 of their
-// value (0.06% of them differ from the rounded double result, by one ulp; for
-// positions up to 140000).  The angle is a float pair, reduced by multiples of
-// pi/2 in three floats (p - k C1 is exact: both are multiples of the result's
-// last place); the Taylor series' first correction (-r^3/6, r^4/24) is a float
-// pair too, the rest of either series too small to need one.
-PA_DEVINL void sincos_pair(int pos, float fh, float fl, float& sn, float& cs) {
-  const float pf = static_cast<float>(pos);
-  const float p = __fmul_rn(pf, fh), lo = fmaf(pf, fl, fmaf(pf, fh, -p));
-  const float k = rintf(p * 0.636619772f);
-  const float h = __fmul_rn(k, -4.37113883e-8f), l = fmaf(k, -1.71512451e-15f, fmaf(k, -4.37113883e-8f, -h));
-  float s1, e1, s2, e2, r, rl;
-  two_sum(fmaf(-k, 1.57079637f, p), lo, s1, e1);
-  two_sum(s1, -h, s2, e2);
-  two_sum(s2, (e1 + e2) - l, r, rl);
+// Sine and cosine of pos * f, f = fh + fl but for 2^-49 of itself, rounded to fp32
+// from about 2^-35 of their value (0.06% of them differ from the rounded double
+// result, by one ulp).  The angle is a float pair, reduced by multiples of pi/2 in
+// three floats (p - k C1 is exact: both are multiples of the result's last place).
+// From position 2^17 on, where the pair's 2^-49 of the angle would begin to show (and
+// 2^24, where a float no longer holds every position), angle and reduction are in 64
+// bits.  The Taylor series' first correction (-r^3/6, r^4/24) is a float pair too, the
+// rest of either series too small to need one.
+PA_DEVINL void sincos_pair(int pos, float fh, float fl, double f, float& sn, float& cs) {
+  float r, rl;
+  int q;
+  if (pos < 1 << 17) {
+    const float pf = static_cast<float>(pos);
+    const float p = __fmul_rn(pf, fh), lo = fmaf(pf, fl, fmaf(pf, fh, -p));
+    const float k = rintf(p * 0.636619772f);
+    const float h = __fmul_rn(k, -4.37113883e-8f), l = fmaf(k, -1.71512451e-15f, fmaf(k, -4.37113883e-8f, -h));
+    float s1, e1, s2, e2;
+    two_sum(fmaf(-k, 1.57079637f, p), lo, s1, e1);
+    two_sum(s1, -h, s2, e2);
+    two_sum(s2, (e1 + e2) - l, r, rl);
+    q = static_cast<int>(k);
+  } else {
+    const double a = pos * f, k = rint(a * 0.63661977236758134);
+    const double d = fma(-k, 6.123233995736766e-17, fma(-k, 1.5707963267948966, a));
+    r = static_cast<float>(d);
+    rl = static_cast<float>(d - r);
+    q = static_cast<int>(k);
+  }
   const float z = __fmul_rn(r, r), zl = fmaf(r, r, -z);
   // sin: r - r^3 / 6 + ...
   const float a = __fmul_rn(r, z), al = fmaf(r, zl, fmaf(r, z, -a));
@@ -188,7 +201,6 @@ PA_DEVINL void sincos_pair(int pos, float fh, float fl, float& sn, float& cs) {
   s = fmaf(-0.5f, z, 1.f);
   const float c = s + w;
   const float C = c + ((w - (c - s)) + (fmaf(-0.5f, z, 1.f - s) + fmaf(-0.5f, z2, wl + tail)));
-  const int q = static_cast<int>(k);
   sn = (q & 1) ? C : S;
   cs = (q & 1) ? S : C;
   if (q & 2) sn = -sn;
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
         const float r = reduce_angle(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x]);
         __sincosf(r, &sv, &cv);
       } else {
-        sincos_pair(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x], sv, cv);
+        sincos_pair(pos, p.inv_freq_hi[threadIdx.x], p.inv_freq_lo[threadIdx.x], p.inv_freq[threadIdx.x], sv, cv);
       }
       cs_s[threadIdx.x] = cv;
       sn_s[threadIdx.x] = sv;

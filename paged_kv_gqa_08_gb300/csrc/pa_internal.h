@@ -86,8 +86,9 @@ struct NormRopeParams {
   float eps;
   int32_t hq, hkv;
   // theta^(-2i/head_dim), computed on the host in double and passed as a
-  // float plus the float nearest to the remainder
+  // float plus the float nearest to the remainder, and as it is
   float inv_freq_hi[64], inv_freq_lo[64];
+  double inv_freq[64];
   // positions == nullptr: each token's position and slot come from the varlen
   // metadata (as pa_slot_mapping computes them), optionally written out
   const int32_t* cu;

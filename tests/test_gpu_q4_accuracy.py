@@ -180,3 +180,31 @@ def test_every_chunk_counts_once(dtype, hq, hkv, hd, gs, P, lens, splits):
             v[b][min(n - 1, 32 * i + int(rng.integers(32))), :, i % hd] += np.float32(40)
     c = Batch(dtype, hkv, gs, P, rng.standard_normal((len(live), hq, hd)), k, v)
     c.check(*splits)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_rotary_angles_at_any_position(dtype, hd):
+    """Positions up to the largest that an int32 holds.  A sine or cosine that rounds to its other neighbour moves a value
+    by an ulp of its pair's size (2^-23, bf16 2^-7); the angle in 64 bits is off by two roundings, 2^-52 of it each."""
+    from test_gpu_q4_cache import plain_norm_rope
+
+    dt = DT[dtype]
+    far = [131071, 131072, 140001, 200003, (1 << 20) + 3, (1 << 24) - 1, (1 << 24) + 1, (1 << 24) + 3, (1 << 27) + 5,
+           (1 << 30) + 77, (1 << 31) - 1]
+    n, heads = len(far), 4
+    desc = pa.cache_desc(heads, heads, hd, 16, 4, dt)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = torch.randn(n, heads, hd, generator=g, device="cuda").to(dt), torch.ones(hd, dtype=dt, device="cuda")
+    pos = torch.tensor(far, dtype=torch.int32, device="cuda")
+    slots = torch.arange(n, dtype=torch.int64, device="cuda")
+    out, row = torch.zeros_like(x), heads * hd
+    caches = [torch.zeros(4 * 16, pa.pa_q4_row_bytes(desc, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pa.pa_qk_norm_rope_kv_write_q4(desc, 64, x, row, x, row, x, row, n, pos, w, w, 1e-6, 1e4, slots, out, *caches)
+    got, want = out.double(), plain_norm_rope(x, w, pos, 1e-6, 1e4).double()
+    h = hd // 2
+    size = torch.hypot(want[..., :h], want[..., h:])
+    size = torch.cat([size, size], -1)
+    bound = size * ((2.0 ** -7 if dtype == "bf16" else 2.0 ** -22) + 2.0 ** -51 * pos.double()[:, None, None])
+    worst = ((got - want).abs() / bound).amax((1, 2))
+    assert (worst <= 1).all(), dict(zip(far, worst.tolist()))
