@@ -24,9 +24,10 @@ constexpr int kTok = 32;        // tokens per chunk
 constexpr int kHalf = 16;       // tokens of a half chunk (a page holds whole halves)
 constexpr int kMaxStages = 8;   // ring depth, at most
 constexpr int kMaxCluster = 8;  // CTAs of a cluster that shares a request, at most
-// Tokens of 128 dims (of 64 twice as many) of a request that a CTA takes, alone or
-// with its cluster, where a CTA or a cluster per request comes to at least 2/5 of
-// the SMs; and that a CTA alone takes in any batch.
+// Tokens of 128 dims (of 64 twice as many; fp32, which takes a token about half as
+// fast, half as many) of a request that a CTA takes, alone or with its cluster, where
+// a CTA or a cluster per request comes to at least 2/5 of the SMs; and that a CTA
+// alone takes in any batch.
 constexpr int kPartTokens = 256, kAloneTokens = 64;
 
 // A chunk in the ring, as the producer describes it to the consumers: its
@@ -1189,13 +1190,17 @@ cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_ct
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
   // Short requests that fit the GPU at once: a CTA or a cluster each and no merge
   // kernel, 2 to 4 us of such a call; against them the GPU's other SMs.  With 32
-  // q-heads over 8 of 128 dims, in us (the even split): 16 requests of 300-1000
-  // tokens by clusters of 8 13.7 (15.6), 37 of 64-512 by 4 13.3 (14.6), 64 by 2
-  // 16.0 (17.5), 100 of 64-256 by one CTA each 15.0 (18.4), 4 of 5-64 7.6 (8.6).
-  // Longer parts: 64 of 300-2000 33.8 (27.2).  Too few: 2 of 1000 by 8 12.1 (9.0),
-  // 4 of 256 by one 12.3 (8.8).
+  // q-heads over 8 of 128 dims, groups of 32, in us (the even split), bf16: 16
+  // requests of 300-1000 tokens by clusters of 6 14.9 (16.5), 37 of 64-512 by 3 14.6
+  // (15.9), 64 of 100-512 by 2 16.9 (18.3), 100 of 64-256 by one CTA each 15.8 (19.3),
+  // 4 of 5-64 8.1 (8.8).  Longer parts: 64 of 300-2000 by 2 36.9 (28.3).  Too few: 2 of
+  // 301-905 by 8 12.8 (11.2), 4 of 100-256 by one 13.1 (9.3).  fp32, the same: 23.4
+  // (20.6), 23.9 (19.9), 29.7 (25.1), 28.6 (24.7), 10.5 (10.2); at half the length, 16
+  // over 8 heads of 64 dims: 16 of 300-1000 by 6 13.8 (14.6), 64 of 100-512 by 2 16.4
+  // (16.6), 152 of 64-256 by one 17.0 (20.8), 4 of 5-64 7.1 (8.1); 64 of 300-1000 by 2
+  // 26.3 (21.9).
   if (batch >= 1 && batch <= kInlinePlanMax && n >= batch) {
-    const int64_t work = static_cast<int64_t>(max_ctx) * d.head_dim;
+    const int64_t work = static_cast<int64_t>(max_ctx) * d.head_dim * (d.dtype == PA_BF16 ? 1 : 2);
     const int64_t most = std::min<int64_t>({kMaxCluster, n / batch, chunks_upper / batch});
     for (int c = work <= kAloneTokens * 128 ? 1 : static_cast<int>(most); c >= 1; --c) {
       const bool fills = 5 * static_cast<int64_t>(batch) * c >= 2 * di.sm_count;
