@@ -713,7 +713,7 @@ def main():
     tok_s = whole_job_rate(wl.batch, ms, world)
     dec_bytes = step_bytes
     achieved = dec_bytes / (attn_ms * 1e-3) / 1e9
-    traffic = profiled_traffic("decode_qwen3_0p6b", ["decode.cu", "pa_common.cuh"])
+    traffic = profiled_traffic("decode_qwen3_0p6b", ["decode.cu", "decode_shared.cuh", "pa_common.cuh"])
     e2e_ms, h2d, d2h, e2e_same = time_e2e(d, max(20, args.steps // 5), args.warmup, world)
     e2e_step_ms = e2e_ms / max(20, args.steps // 5)
     from paged_kv_gqa_08_gb300 import pa_decode_plan_info

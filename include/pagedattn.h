@@ -151,7 +151,9 @@ PA_API pa_status pa_kv_write(const pa_cache_desc* desc, const void* k, int64_t k
  *
  *   q                [num_tokens, num_q_heads, head_dim] rows at q_row_stride.
  *   k, v             rows at k_row_stride / v_row_stride (as pa_kv_write).
- *   positions        int32 [num_tokens], absolute positions (pa_slot_mapping).
+ *   positions        int32 [num_tokens], absolute positions (pa_slot_mapping),
+ *                    below 2^24; the rotation angle is within a few 1e-7 of the
+ *                    exact one up to position 131072.
  *   q_norm_w, k_norm_w  [head_dim] weights in the cache dtype.
  *   eps, rope_theta  RMSNorm epsilon and rotary base (host).
  *   q_out            [num_tokens, num_q_heads, head_dim] contiguous output; it
@@ -411,8 +413,9 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
  * 16 + u is (x - c) / s rounded half to even and clamped to 16..31 (s = 0:
  * u = 0).  The quotients are products with the fp32 numbers nearest to 1/15
  * and 1/s; every step rounds to fp32.  A value so comes back within s / 2 plus
- * the rounding of s and c (2^-11 of 31 s and of |c|).  A group with a NaN or an
- * infinity comes back as NaN.
+ * the rounding of s and c (2^-11 of 31 s and of |c|, and 2^-25 of 32 where float16
+ * numbers are subnormal: groups of values below 2^-10 or so lose accuracy, below
+ * 2^-20 all of it).  A group with a NaN or an infinity comes back as NaN.
  *
  * Layout.  [num_pages, page_size] rows of pa_q4_row_bytes() bytes: head h's
  * codes at byte h * head_dim / 2, two bytes for four consecutive dims (dim 0 in
@@ -423,6 +426,9 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
  * in slot t lies at piece j XOR (t mod the block's pieces).  Whole pages can be
  * copied; a row keeps its meaning only at the same offset in its page, modulo 8.
  * Caches must be 16-byte aligned and need no initialisation.
+ *
+ * pa_decode_no_alloc and pa_prefill_step have no 4-bit form: prefill is a write,
+ * pa_kv_read_q4 and pa_prefill_varlen.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of one token's row of a 4-bit K or V cache (a multiple of 16), or 0

@@ -8,7 +8,7 @@
 // rows where the halves follow each other in a page), and one consumer warp
 // per kv-head takes its head's part.
 //
-// Bound by HBM at its floor.  Measured (16-bit queries, 8 kv-heads of 128 dims; the
+// The floor is HBM's; the kernel does not reach it over a call's life.  Measured (16-bit queries, 8 kv-heads of 128 dims; the
 // call with its merge, replayed from a graph): 256 requests of 128-2048 tokens,
 // groups of 32, 70.7 us for 347 MB; 64 of 1024-8192, groups of 64, 66.2 us for
 // 355 MB; 8 of 32768, groups of 128, 55.9 us for 285 MB: 4.9 to 5.4 TB/s of a

@@ -179,7 +179,9 @@ PA_DEVINL void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// 2^x on the special-function unit (PTX ex2.approx; x <= 0 here).
+// 2^x on the special-function unit (PTX ex2.approx, results below 2^-126 as 0; x is
+// at most 0 in decode.cu and the merges, at most 11 in decode_q4.cu).  exp2f gives the
+// same bits wherever the result is no subnormal.
 PA_DEVINL float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -289,11 +289,14 @@ __host__ __device__ constexpr int nr_stage_bytes(int hq, int hkv, int hd, int e)
 // (quantising k from the rotation's registers and v apart took 3240 instructions
 // a token instead of 2900).  A code moves by a whole step when its value crosses
 // a border by an ulp, so here the norm and the rotation are the plain formulas,
-// operation by operation in fp32: squares rounded and added in a fixed order
-// (32 elements apart, then pairwise), products and sums of the rotation rounded
-// each, sines and cosines rounded from a float pair (3138 instructions a token;
-// 16384 tokens 63.3 us, 60.8 with the plain caches' arithmetic).  A lane's pairs
-// lie so that it holds the elements that are added first.
+// operation by operation in fp32: squares rounded and added, products and sums of
+// the rotation rounded each, sines and cosines rounded from more than fp32 (3138
+// instructions a token with angles of float pairs alone: 16384 tokens 63.3 us then,
+// 63.9 now; 60.8 with the plain caches' arithmetic).  The order in which the squares
+// are added (32 elements apart, then neighbours in pairs) is no more exact than
+// another; it is the interface's, stated in its header, so that a row's codes can be
+// worked out elsewhere bit for bit.  A lane's pairs lie so that it holds the elements
+// that are added first.
 template <typename T, int HD, int GS>
 __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     norm_rope_kv_write_kernel(const NormRopeParams p) {
@@ -420,9 +423,10 @@ __global__ void __launch_bounds__(kNrThreads, GS ? kNrCtasPerSmQ4 : 0)
     if (i + 1 < n_mine) token_meta(i + 1, pos_next, slot_next);  // the next token's, one token ahead
     const bool slot_ok = slot >= 0 && slot < p.num_slots;
     if (!slot_ok && slot != -1 && threadIdx.x == 0) raise_flag(p.err, PA_DEVERR_BAD_SLOT);
-    // cos / sin of the token's HD/2 pair indices, one thread per pair: the
-    // angle pos * theta^(-2i/HD) formed and reduced modulo 2*pi in two-float
-    // arithmetic, then evaluated by the special-function unit
+    // cos / sin of the token's HD/2 pair indices, one thread per pair, of the
+    // angle pos * theta^(-2i/HD) formed in two-float arithmetic: reduced modulo
+    // 2*pi and evaluated by the special-function unit, or (4-bit rows) reduced
+    // modulo pi/2 and evaluated by sincos_pair's series
     if (threadIdx.x < HD / 2) {
       float sv, cv;
       if constexpr (GS == 0) {

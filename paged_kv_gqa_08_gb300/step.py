@@ -115,7 +115,8 @@ def write_rows(desc, k_rows, v_rows, cu_rows, lens, block_tables, max_pages_per_
 def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_lens, block_tables,
              k_cache, v_cache, scale: float, max_pages_per_seq: int, max_context_len: int, max_seqlen_q: int,
              q_norm_w=None, k_norm_w=None, eps: float = 0.0, rope_theta: float = 0.0, stream=None):
-    """Run one step; returns ``bufs.out`` (the attention output of the new tokens)."""
+    """Run one step; returns ``bufs.out`` (the attention output of the new tokens).  A step beyond its buffers is a
+    ``ValueError``; over a 4-bit cache whatever is refused is refused before anything is enqueued."""
     n = q.shape[0]
     batch = context_lens.shape[0]
     for t in (bufs.positions, bufs.slots, bufs.out, bufs.q_out if q_norm_w is not None else None):
