@@ -10,8 +10,8 @@
 //
 // The floor is HBM's; the kernel does not reach it over a call's life.  Measured (16-bit queries, 8 kv-heads of 128 dims; the
 // call with its merge, replayed from a graph): 256 requests of 128-2048 tokens,
-// groups of 32, 70.7 us for 347 MB; 64 of 1024-8192, groups of 64, 66.2 us for
-// 355 MB; 8 of 32768, groups of 128, 55.9 us for 285 MB: 4.9 to 5.4 TB/s of a
+// groups of 32, 71.0 us for 347 MB; 64 of 1024-8192, groups of 64, 66.1 us for
+// 355 MB; 8 of 32768, groups of 128, 55.3 us for 285 MB: 4.9 to 5.4 TB/s of a
 // copy's 6.7.  Of these the start (plan, page look-up, first chunk) takes 6 to 7
 // and the merge 2 to 4 us.
 #include "decode_shared.cuh"
@@ -148,9 +148,10 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 //       the second term is one product of the transposed parameter piece, whose
 //       rows are its groups' s and c, with p.  The product's other eight rows
 //       are ones: the softmax sum.
-// 16 tokens of a head take 197 instructions with groups of 128, 109 of them on
-// the integer pipe (two cycles each); 309 with K and V decoded to float16 in
-// registers, 228 with raw codes loaded as words and paired by byte permutes.
+// 16 tokens of a head take 206 instructions with groups of 128, 111 of them on
+// the integer pipe (two cycles each), 253 with groups of 32 (fp32: 383 and 709);
+// 309 with K and V decoded to float16 in registers, 228 with raw codes loaded as
+// words and paired by byte permutes.
 //
 // fp32 queries and outputs.  Queries and p s are two float16 numbers each, multiples
 // of 2^-11 and 2^-23 of their bounds, so that every sum of products with codes is

@@ -262,7 +262,8 @@ PA_DEVINL void map_token(const NormRopeParams& p, int64_t t, bool report, int& p
 constexpr int kNrThreads = 128;
 constexpr int kNrCtasPerSm = 8;
 // 4-bit rows take more registers: 80 without recomputing values, so 5 CTAs
-// (16384 tokens of 16 q- and 8 kv-heads: 63.3 us; 4 and 6 CTAs 68.4 and 66.1 us).
+// (16384 tokens of 16 q- and 8 kv-heads: 63.9 us; 4 and 6 CTAs 68.4 and 66.1 us
+// where 5 took 63.3).
 constexpr int kNrCtasPerSmQ4 = 5;
 constexpr int kNrMaxPerCta = 2048;
 
@@ -290,9 +291,9 @@ __host__ __device__ constexpr int nr_stage_bytes(int hq, int hkv, int hd, int e)
 // a token instead of 2900).  A code moves by a whole step when its value crosses
 // a border by an ulp, so here the norm and the rotation are the plain formulas,
 // operation by operation in fp32: squares rounded and added, products and sums of
-// the rotation rounded each, sines and cosines rounded from more than fp32 (3138
-// instructions a token with angles of float pairs alone: 16384 tokens 63.3 us then,
-// 63.9 now; 60.8 with the plain caches' arithmetic).  The order in which the squares
+// the rotation rounded each, sines and cosines rounded from more than fp32 (3189
+// instructions a token: 16384 tokens 63.9 us; 3138 and 62.4 with angles of float pairs
+// alone, 60.8 with the plain caches' arithmetic).  The order in which the squares
 // are added (32 elements apart, then neighbours in pairs) is no more exact than
 // another; it is the interface's, stated in its header, so that a row's codes can be
 // worked out elsewhere bit for bit.  A lane's pairs lie so that it holds the elements
