@@ -529,8 +529,9 @@ PA_API size_t pa_decode_q4_workspace_size(const pa_cache_desc* desc, int32_t gro
  * Accuracy, against the exact result for the values that the rows stand for.
  * fp32: a few 2^-24 of the values' magnitude, as a plain fp32 evaluation's (some
  * 10 of them where one CTA adds 20000 tokens up; measured 3e-6 of outputs whose
- * values have no mean).  bf16: the output's rounding, and the float16 roundings
- * (2^-11 each) of a token's weight p and of p s; weights below 2^-32 of a
+ * values have no mean, 7e-6 at 100000).  bf16: the output's rounding (measured: 0.18
+ * to 0.2% rms to 100000 tokens a CTA), and the float16 roundings (2^-11 each) of a
+ * token's weight p and of p s; weights below 2^-32 of a
  * share's largest count as 0, and where p s is less than 2^-25 of the largest
  * weight times the largest s that the share of the request holds (or s less
  * than 2^-18 of that) it has fewer bits: values so far below others of the same

@@ -8,12 +8,12 @@
 // rows where the halves follow each other in a page), and one consumer warp
 // per kv-head takes its head's part.
 //
-// The floor is HBM's; the kernel does not reach it over a call's life.  Measured (16-bit queries, 8 kv-heads of 128 dims; the
-// call with its merge, replayed from a graph): 256 requests of 128-2048 tokens,
-// groups of 32, 71.0 us for 347 MB; 64 of 1024-8192, groups of 64, 66.1 us for
-// 355 MB; 8 of 32768, groups of 128, 55.3 us for 285 MB: 4.9 to 5.4 TB/s of a
-// copy's 6.7.  Of these the start (plan, page look-up, first chunk) takes 6 to 7
-// and the merge 2 to 4 us.
+// The floor is HBM's; over a call's life the kernel does not reach it.  Measured
+// (16-bit queries, 8 kv-heads of 128 dims; the call with its merge, replayed from a
+// graph): 256 requests of 128-2048 tokens, groups of 32, 72.3 us for 347 MB; 64 of
+// 1024-8192, groups of 64, 67.1 us for 355 MB; 8 of 32768, groups of 128, 56.2 us for
+// 285 MB: 4.8 to 5.3 TB/s of a copy's 6.7.  Of these the start (plan, page look-up,
+// first chunk) takes 6 to 7 and the merge 2 to 4 us.
 #include "decode_shared.cuh"
 #include "q4_common.cuh"
 
@@ -42,6 +42,9 @@ constexpr uint32_t kWhole = 1u << 20;  // the share holds the whole request
 constexpr uint32_t kRagged = 1u << 21; // a half has fewer than 16 tokens
 constexpr uint32_t kNew = 1u << 22;    // the request's new token is the last one
 constexpr uint32_t kEnd = 1u << 23;    // no chunk: the CTA's work is done
+constexpr uint32_t kSettle = 1u << 24; // every kSettleChunks-th of a consumer group's chunks of the request
+
+constexpr int kSettleChunks = 8;  // bf16: chunks whose second term is summed apart
 
 struct Q4Params {
   KParams k;
@@ -147,9 +150,13 @@ PA_DEVINL float partial_lse(float m, float l) { return l > 0.f ? m + log2f(l) : 
 //   O = sum over tokens of (p s) u + p m:  p s replaces p as the B operand, and
 //       the second term is one product of the transposed parameter piece, whose
 //       rows are its groups' s and c, with p.  The product's other eight rows
-//       are ones: the softmax sum.
-// 16 tokens of a head take 206 instructions with groups of 128, 111 of them on
-// the integer pipe (two cycles each), 253 with groups of 32 (fp32: 383 and 709);
+//       are ones: the softmax sum.  Every 256 tokens of a group of consumers
+//       (kSettle) the second term joins O: apart, the two sums grow with the tokens,
+//       what the tensor cores cut off of them with the square, and it stays when the
+//       two all but cancel (4% of outputs whose values have no mean at 100000
+//       tokens; together 0.2%, the output's rounding; at 2048 and below no change).
+// 16 tokens of a head take 212 instructions with groups of 128, 113 of them on
+// the integer pipe (two cycles each), 256 with groups of 32 (fp32: 383 and 709);
 // 309 with K and V decoded to float16 in registers, 228 with raw codes loaded as
 // words and paired by byte permutes.
 //
@@ -713,6 +720,23 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
     __syncwarp();
     if (lane == 0) bar_arrive(empty(s));
 
+    if (!kF32 && (flags & (kLast | kYield | kSettle))) {
+      // the second term joins the first, in the first's powers of two
+      const float hi = __uint_as_float((127u - 18 + 19 - max(s_most >> 26, 4u)) << 23), lo = hi * 0.0625f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float add[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
+                        __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
+#pragma unroll
+        for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] = fmaf(add[i & 1], (j & 1) ? lo : hi, o[j][i]);
+      }
+      om[0] = om[1] = 0.f;
+    }
     if (flags & (kLast | kYield)) {
       float l[2] = {om[2], om[3]};  // the softmax sums
       if constexpr (kF32) {
@@ -723,20 +747,12 @@ PA_DEVINL void consume(const Q4Params& p, unsigned char* smem, int h, int group)
         l[0] = l_sum[0];
         l[1] = l_sum[1];
       } else {
-        // the powers of two undone, the second term added
+        // the powers of two undone
         const float hi = __uint_as_float((127u + 18 - 19 + max(s_most >> 26, 4u)) << 23), lo = hi * 16.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float add[2];
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            add[e] = fmaf(16.f, __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g),
-                          __shfl_sync(0xffffffffu, om[e], s_lane + 8 * g + 4));
-#pragma unroll
-          for (int j = g * 2 * PG; j < (g + 1) * 2 * PG; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = fmaf(o[j][i], (j & 1) ? lo : hi, add[i & 1]);
-        }
+          for (int i = 0; i < 4; ++i) o[j][i] *= (j & 1) ? lo : hi;
       }
       if (flags & kYield) {
         // hand this group's part over: once the previous one has been taken
@@ -934,7 +950,8 @@ PA_DEVINL void produce(const Q4Params& p, unsigned char* smem, uint64_t* full, u
       flags = (x < xa + p.groups ? kFirst : 0u) | (x == xb - 1 ? kLast : 0u) |
               (p.groups == 2 && x == xb - 2 ? kYield : 0u) | (p.groups == 1 || xb - xa == 1 ? kSolo : 0u) |
               (cb0 >= x0 && cb1 <= x1 && p.cluster <= 1 ? kWhole : 0u) |
-              (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) | (new_slot >= 0 ? kNew : 0u);
+              (n[0] != kHalf || n[1] != kHalf ? kRagged : 0u) | (new_slot >= 0 ? kNew : 0u) |
+              ((x - xa) / p.groups % kSettleChunks == kSettleChunks - 1 ? kSettle : 0u);
     }
     b = __shfl_sync(0xffffffffu, my_b, nvalid - 1);
     for (int u = 0; u < nvalid; ++u, ring.next(p.stages)) {

@@ -63,7 +63,10 @@ class Batch:
         of many terms add like their squares; eight times that is allowed, and what a few terms can do at most.
 
         bf16: the output is rounded (2^-8 of it); p and p s are float16 (2^-11 each), the first in sum and products
-        alike: 2^-11 p (|v - o| + |s u|) a term.
+        alike: 2^-11 p (|v - o| + |s u|) a term.  The products' sums are fp32 numbers that the tensor cores may cut off
+        (2^-23 of a sum for every 16 tokens, to one side): for the output and the softmax sum, which grow evenly, half of
+        that on the average and half as many terms in each of two sums, 2^-24 of the output for every 16 tokens; and of
+        p s u, summed over 512 tokens before the rest joins, U * 64 of its sum.
 
         fp32: the two sums of 16 tokens round a few times (16 u of p (|s u| + |m|)); o grows by one addition for every
         16 tokens, each u / 2 of what it has come to (at most about the largest output of the head); a weight is off by
@@ -83,7 +86,8 @@ class Batch:
                 su = np.abs(v - m)
                 if self.dtype == "bf16":
                     term = p[:, None] * (np.abs(v - o[h]) + su)
-                    e[h] = 2.0 ** -8 * (np.abs(o[h]) + np.sqrt((term ** 2).sum(0))) + 2.0 ** -18 * (p @ (su + np.abs(m)))
+                    e[h] = 2.0 ** -8 * (np.abs(o[h]) + np.sqrt((term ** 2).sum(0))) + U * (
+                        -(-len(v) // 16) * np.abs(o[h]) + 64 * (p @ (su + np.abs(m))))
                 else:
                     n = np.sqrt(-(-len(v) // 16))
                     e[h] = U * (16 * (p @ (su + np.abs(m))) / n + 2 * n * np.abs(o[h]).max()
@@ -116,6 +120,17 @@ def test_every_output_is_within_its_own_bound(dtype, hq, hkv, hd, gs, P, lens):
     c = Batch(dtype, hkv, gs, P, rng.standard_normal((len(lens), hq, hd)), normal(rng, lens, hkv, hd),
               normal(rng, lens, hkv, hd))
     c.check(1, 0, 7)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hd,gs", [(4, 128, 32), (3, 128, 64), (8, 128, 128), (2, 64, 32), (1, 64, 64)])
+@pytest.mark.parametrize("mean", [0.0, 2.0])
+def test_a_share_of_a_hundred_thousand_tokens(dtype, hq, hd, gs, mean):
+    rng = np.random.default_rng(hd + gs)
+    lens = [100000, 40007]
+    v = [x + np.float32(mean) for x in normal(rng, lens, 1, hd)]
+    c = Batch(dtype, 1, gs, 64, rng.standard_normal((2, hq, hd)), normal(rng, lens, 1, hd), v)
+    c.check(1, 0)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
