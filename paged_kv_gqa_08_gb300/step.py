@@ -134,6 +134,7 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
                         rope_theta, scale, bufs.q_out, k_cache, v_cache, bufs.positions, bufs.slots, bufs.out,
                         bufs.workspace, stream=stream)
         return bufs.out
+    _check_queries(desc, q, q_norm_w, k_norm_w)
     if q_norm_w is not None:
         # slot mapping, norm, rotary and KV write in one kernel
         pa_prefill_qk_norm_rope_kv_write(desc, q, q.stride(0), k, k.stride(0), v, v.stride(0), n, cu_seqlens_q,
@@ -155,17 +156,22 @@ def _refuse(status: int, message: str):
     raise PagedAttnError("run_step", status, message)
 
 
+def _check_queries(desc, q, q_norm_w, k_norm_w):
+    """Both norm weights or neither; without them attention reads q itself, so its rows have to be packed."""
+    if (q_norm_w is None) != (k_norm_w is None):
+        _refuse(PA_ERR_NULL, "one norm weight without the other")
+    n = q.shape[0]
+    if q_norm_w is None and n and not (q[0].is_contiguous() and
+                                       (n == 1 or q.stride(0) == desc.num_q_heads * desc.head_dim)):
+        _refuse(PA_ERR_SHAPE, "without norm weights attention reads q itself, so its rows must be packed")
+
+
 def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
                    k_norm_w):
     """What the attention of a step over a 4-bit cache would refuse once the step's rows are written: refused before
     anything is enqueued (the write's own checks come first in its call)."""
-    n = q.shape[0]
-    if (q_norm_w is None) != (k_norm_w is None):
-        _refuse(PA_ERR_NULL, "one norm weight without the other")
-    norm = q_norm_w is not None
-    width = desc.num_q_heads * desc.head_dim
-    if not norm and n and not (q[0].is_contiguous() and (n == 1 or q.stride(0) == width)):
-        _refuse(PA_ERR_SHAPE, "without norm weights attention reads q itself, so its rows must be packed")
+    n, norm = q.shape[0], q_norm_w is not None
+    _check_queries(desc, q, q_norm_w, k_norm_w)
     if n and not 1 <= max_context_len <= max_pages_per_seq * desc.page_size:
         _refuse(PA_ERR_SHAPE, "max_context_len is not within 1 .. max_pages_per_seq * page_size")
     if not math.isfinite(scale) or (kind != "decode" and not scale > 0):

@@ -297,6 +297,22 @@ def test_a_step_is_refused_before_anything_is_enqueued(enqueued, kind, spoil, st
     assert e.value.status == status and not enqueued
 
 
+@pytest.mark.parametrize("spoil,status", [
+    (lambda torch, a: a.update(q_norm_w=torch.ones(128, dtype=torch.bfloat16)), pa.PA_ERR_NULL),
+    (lambda torch, a: a.update(k_norm_w=torch.ones(128, dtype=torch.bfloat16)), pa.PA_ERR_NULL),
+    (_wide, pa.PA_ERR_SHAPE), (_transposed, pa.PA_ERR_SHAPE)])
+def test_a_decode_step_over_rows_of_the_dtype_looks_at_its_queries_first(enqueued, spoil, status):
+    torch = pytest.importorskip("torch")
+    from paged_kv_gqa_08_gb300.step import run_step
+
+    a = _step_args("decode")
+    a["bufs"].group_size = 0
+    spoil(torch, a)
+    with pytest.raises(pa.PagedAttnError) as e:
+        run_step(**a)
+    assert e.value.status == status and not enqueued
+
+
 @pytest.mark.parametrize("kw,status", [(dict(max_seqlen_q=0), pa.PA_ERR_SHAPE), (dict(max_seqlen_q=65), pa.PA_ERR_SHAPE),
                                        (dict(scale=0.0), pa.PA_ERR_SHAPE), (dict(scale=-1.0), pa.PA_ERR_SHAPE)])
 def test_a_prefill_step_is_refused_before_anything_is_enqueued(enqueued, kw, status):
