@@ -400,6 +400,47 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
                                         int64_t num_tokens, int32_t max_context_len);
 
 /* ---------------------------------------------------------------------------
+ * Attention over a sliding window and the first tokens ("sinks").  The calls
+ * below stand beside their namesakes above: a query at position p attends to
+ * the keys j <= p of its request with p - window < j or j < num_sinks.  The
+ * window counts the query's own token, so window = 1 leaves it and the sinks;
+ * with window + num_sinks >= context_lens[b] the result is the namesake's.
+ *
+ *   window           >= 1 (host).
+ *   num_sinks        >= 0 (host).
+ *
+ * Keys that no query of the call attends to are not read, and neither are the
+ * block-table entries of pages that hold only such keys: those pages may belong
+ * to other requests, their entries may be -1.  Of the rows in one page (or one
+ * 128-key tile of prefill) those not attended to may hold anything, NaN
+ * included.  Lengths, padding rows, flags and refusals are the namesakes'.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace pa_decode_window and pa_decode_kv_write_window need;
+ * as pa_decode_workspace_size (at most that size). */
+PA_API size_t pa_decode_window_workspace_size(const pa_cache_desc* desc, int32_t window, int32_t num_sinks,
+                                              int32_t batch, int32_t max_context_len, int32_t max_ctas);
+
+/* pa_decode over the window and the sinks. */
+PA_API pa_status pa_decode_window(const pa_cache_desc* desc, int32_t window, int32_t num_sinks, const void* q,
+                                  int32_t batch, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int32_t max_pages_per_seq,
+                                  const int32_t* context_lens, int32_t max_context_len, float scale,
+                                  int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes,
+                                  pa_stream_t stream);
+
+/* pa_decode_kv_write over the window and the sinks: the new row is stored at
+ * position context_lens[b] - 1 and attended to.  Equal to pa_slot_mapping +
+ * pa_kv_write + pa_decode_window, bit for bit. */
+PA_API pa_status pa_decode_kv_write_window(const pa_cache_desc* desc, int32_t window, int32_t num_sinks,
+                                           const void* q, const void* k_new, int64_t k_row_stride,
+                                           const void* v_new, int64_t v_row_stride, int32_t batch, void* k_cache,
+                                           void* v_cache, const int32_t* block_tables, int32_t max_pages_per_seq,
+                                           const int32_t* context_lens, int32_t max_context_len, float scale,
+                                           int32_t max_ctas, int64_t* slot_mapping, void* out, void* workspace,
+                                           size_t workspace_bytes, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * A cache held in 4 bits.  The calls below stand beside their namesakes above:
  * desc describes the heads, the pages and the type of q, k, v rows and outputs
  * (fp32 or bf16); k_cache and v_cache hold 4-bit rows instead, and group_size

@@ -104,6 +104,11 @@ _SIGS = {
                             ctypes.c_size_t, _VP]),
     "pa_decode_kv_write_q4": (_I32, [_DESC, _I32, _VP, _VP, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _I32, _VP, _I32,
                                      _F32, _I32, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "pa_decode_window_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _I32, _I32]),
+    "pa_decode_window": (_I32, [_DESC, _I32, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _F32, _I32, _VP, _VP,
+                                ctypes.c_size_t, _VP]),
+    "pa_decode_kv_write_window": (_I32, [_DESC, _I32, _I32, _VP, _VP, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _I32, _VP,
+                                         _I32, _F32, _I32, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "pa_validate_metadata": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP]),
     "pa_selftest_bounded_wait": (_I32, [_I32, _VP]),
     "pa_read_device_errors": (_I32, [ctypes.POINTER(ctypes.c_uint32), _I32]),
@@ -430,6 +435,35 @@ def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row
     _check("pa_decode_kv_write_q4", lib.pa_decode_kv_write_q4(
         desc, group_size, q, k, k_row_stride, v, v_row_stride, batch, kc, vc, bt, max_pages_per_seq, ctx,
         max_context_len, scale, max_ctas, slots, out, ws, workspace_bytes, st))
+
+
+def _bytes_of(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        return workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return workspace_bytes
+
+
+def pa_decode_window_workspace_size(desc, window, num_sinks, batch, max_context_len, max_ctas=0) -> int:
+    return int(load_library().pa_decode_window_workspace_size(desc, window, num_sinks, batch, max_context_len,
+                                                              max_ctas))
+
+
+def pa_decode_window(desc, window, num_sinks, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq,
+                     context_lens, max_context_len, scale, max_ctas, out, workspace, workspace_bytes=None,
+                     stream=None):
+    _check("pa_decode_window", load_library().pa_decode_window(
+        desc, window, num_sinks, _at(q), batch, _at(k_cache), _at(v_cache), _at(block_tables), max_pages_per_seq,
+        _at(context_lens), max_context_len, scale, max_ctas, _at(out), _at(workspace),
+        _bytes_of(workspace, workspace_bytes), _stream(stream)))
+
+
+def pa_decode_kv_write_window(desc, window, num_sinks, q, k_new, k_row_stride, v_new, v_row_stride, batch, k_cache,
+                              v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas,
+                              slot_mapping, out, workspace, workspace_bytes=None, stream=None):
+    _check("pa_decode_kv_write_window", load_library().pa_decode_kv_write_window(
+        desc, window, num_sinks, _at(q), _at(k_new), k_row_stride, _at(v_new), v_row_stride, batch, _at(k_cache),
+        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
+        _at(slot_mapping), _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,

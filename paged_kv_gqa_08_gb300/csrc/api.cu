@@ -23,7 +23,8 @@ unsigned int* g_err_word[kMaxDevices];
 thread_local int g_last_cuda_error = 0;
 
 bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
 
 pa_status check_desc(const pa_cache_desc* d) {
   if (!d) return PA_ERR_NULL;
@@ -39,24 +40,15 @@ pa_status check_desc(const pa_cache_desc* d) {
   return PA_OK;
 }
 
-int64_t row_elems(const pa_cache_desc* d) { return static_cast<int64_t>(d->num_kv_heads) * d->head_dim; }
-
-// A row stride (elements) is usable when it covers the row and keeps 16-byte alignment.
 bool stride_ok(const pa_cache_desc* d, int64_t stride, int64_t min_elems) {
   return stride >= min_elems && (stride * elem_bytes(d->dtype)) % 16 == 0;
 }
 
-// Called by every entry point once its arguments are validated, before it
-// launches anything: fetches the device error word and clears a launch error
-// left pending by earlier, unrelated CUDA calls, so that the error checked
-// after our own launches is ours.
 pa_status prepare(unsigned int** err) {
   (void)cudaGetLastError();
   cudaError_t e = device_error_word(err);
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
-
-}  // namespace
 
 pa_status cuda_fail(cudaError_t e) {
   g_last_cuda_error = static_cast<int>(e);

@@ -50,7 +50,64 @@ struct KParams {
   const char* v_new;
   int64_t k_new_stride, v_new_stride;  // bytes
   int64_t* slot_out;                   // optional: the slot written for request b
+  // A range of each request's keys left out (the kRange kernels).  Without
+  // groups: the keys between the first `sinks` and the last `window`.  With
+  // them: the first prefix_lens[g] keys of the requests cu_groups[g] ..
+  // cu_groups[g + 1] - 1, which another kernel attends to.
+  int32_t window, sinks;
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  int32_t n_groups, max_prefix;
 };
+
+// Keys [lo, hi) of a request that a kRange kernel leaves out; hi = -1 when the
+// group's prefix is no prefix of its context.
+struct Hole {
+  int lo, hi;
+};
+
+// The group that request b is in (the last that starts at or before it), or -1.
+PA_DEVINL int group_of(const int32_t* cu_groups, int n_groups, int b) {
+  int lo = 0, hi = n_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu_groups[mid] <= b) lo = mid; else hi = mid - 1;
+  }
+  return cu_groups[lo] <= b && b < cu_groups[lo + 1] ? lo : -1;
+}
+
+PA_DEVINL Hole hole_of(const KParams& p, int b, int L) {
+  if (p.cu_groups != nullptr) {
+    const int g = group_of(p.cu_groups, p.n_groups, b);
+    const int pre = g < 0 ? 0 : p.prefix_lens[g];
+    return Hole{0, pre < 0 || pre > L || pre > p.max_prefix ? -1 : pre};
+  }
+  const int lo = min(p.sinks, L);
+  return Hole{lo, max(lo, L - p.window)};
+}
+
+// Chunks before the range and chunks wholly inside it (L: the context).
+PA_DEVINL int chunks_before_hole(Hole h, int log2T) { return (h.lo + (1 << log2T) - 1) >> log2T; }
+PA_DEVINL int chunks_in_hole(Hole h, int L, int log2T) {
+  const int end = h.hi >= L ? (L + (1 << log2T) - 1) >> log2T : h.hi >> log2T;
+  return max(0, end - chunks_before_hole(h, log2T));
+}
+
+// Chunks of request b, or 0 with *bad set when its lengths are inconsistent
+// (length 0 is a padding row: nothing is read, stored or written for it).
+template <bool kRange>
+PA_DEVINL int chunks_of(const KParams& p, int b, int cap, bool* bad) {
+  const int L = p.ctx[b];
+  *bad = L < 0 || L > cap;
+  if (L < 1 || L > cap) return 0;
+  const int n = (L + (1 << p.log2T) - 1) >> p.log2T;
+  if constexpr (kRange) {
+    const Hole h = hole_of(p, b, L);
+    *bad = h.hi < 0;
+    return h.hi < 0 ? 0 : n - chunks_in_hole(h, L, p.log2T);
+  }
+  return n;
+}
 
 // First request whose chunks extend past chunk x0 (cs: the prefix sums).
 __device__ __forceinline__ int first_request(const int32_t* cs, int B, int64_t x0) {
@@ -65,12 +122,12 @@ __device__ __forceinline__ int first_request(const int32_t* cs, int B, int64_t x
 // ---------------------------------------------------------------------------
 // plan: chunk prefix sums and each CTA's first request
 // ---------------------------------------------------------------------------
+template <bool kRange>
 __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const KParams p) {
   __shared__ int32_t warp_tot[kPlanThreads / 32];
   __shared__ int32_t carry;
   pdl_trigger();  // the decode kernel may start launching; it waits for this plan
   const int tid = threadIdx.x;
-  const int T = 1 << p.log2T;
   const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
   if (tid == 0) carry = 0;
   cta_sync();
@@ -78,14 +135,10 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const KParams
     const int b = base + tid;
     int cnt = 0;
     if (b < p.B) {
-      const int L = p.ctx[b];
-      if (L >= 1 && L <= cap) {
-        cnt = (L + T - 1) >> p.log2T;
-      } else {
-        // length 0 is a padding row: nothing is read, stored or written for it
-        if (L != 0) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
-        if (p.k_new != nullptr && p.slot_out) p.slot_out[b] = -1;
-      }
+      bool bad;
+      cnt = chunks_of<kRange>(p, b, cap, &bad);
+      if (bad) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
+      if (cnt == 0 && p.k_new != nullptr && p.slot_out) p.slot_out[b] = -1;
     }
     int x = cnt;
 #pragma unroll
@@ -124,21 +177,18 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const KParams
 // CTA, then each thread writes its run's prefix sums.  CTA 0 also does the
 // plan kernel's side work: it flags bad lengths and marks the slots of rows it
 // skips.  (The merge kernel works the sums out for itself.)
+template <bool kRange = false>
 __device__ __forceinline__ void plan_in_cta(const KParams& p, int32_t* cs_s, int32_t* warp_tot, bool first) {
   const int nthr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int T = 1 << p.log2T;
   const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
   const int per = (p.B + nthr - 1) / nthr;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
-    const int L = p.ctx[b];
-    int cnt = 0;
-    if (L >= 1 && L <= cap) {
-      cnt = (L + T - 1) >> p.log2T;
-    } else if (first) {
-      // length 0 is a padding row: nothing is read, stored or written for it
-      if (L != 0) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
+    bool bad;
+    const int cnt = chunks_of<kRange>(p, b, cap, &bad);
+    if (first && cnt == 0) {
+      if (bad) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
       if (p.k_new != nullptr && p.slot_out) p.slot_out[b] = -1;
     }
     cs_s[b + 1] = cnt;
@@ -195,7 +245,7 @@ PA_DEVINL float ex2_approx(float x) {
 // together, the first ones with their log-sum-exps'; the warps' sums meet in
 // shared memory and are added in a fixed order.
 // ---------------------------------------------------------------------------
-template <typename T, int HD>
+template <typename T, int HD, bool kRange = false>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KParams p) {
   constexpr int EL = HD / 32;  // elements per lane
   constexpr int NWARP = kMergeThreads / 32;
@@ -216,8 +266,8 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
     const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
     int below = 0;
     for (int i = lane; i < p.B; i += 32) {
-      const int L = p.ctx[i];
-      const int n = L >= 1 && L <= cap ? (L + (1 << p.log2T) - 1) >> p.log2T : 0;
+      bool bad;
+      const int n = chunks_of<kRange>(p, i, cap, &bad);
       NC += n;
       below += i < b ? n : 0;
       cb1 += i <= b ? n : 0;
@@ -469,6 +519,7 @@ inline KParams decode_params(const pa_cache_desc& d, const DecodePlan& pl, const
 
 // Launches a planned decode: main_fn (whose arguments are main_args) between
 // the plan kernel, where one is needed, and the merge.
+template <bool kRange = false>
 inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_fn, const DecodePlan& pl, KParams& p,
                                          void** main_args, cudaStream_t s) {
   // (plan ->) decode -> merge.  Up to kInlinePlanMax requests every decode CTA
@@ -487,7 +538,7 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
   } else if (p.inline_plan) {
     e = cudaLaunchKernel(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), main_args, pl.smem_bytes, s);
   } else {
-    decode_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    decode_plan_kernel<kRange><<<1, kPlanThreads, 0, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_after_previous(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), pl.smem_bytes, s, main_args);

@@ -36,6 +36,19 @@ pa_status check_decode_args(const pa_cache_desc* d, const void* q, int32_t batch
                             const int32_t* context_lens, int32_t max_context_len, float scale, int32_t max_ctas,
                             const void* out);
 
+// The checks that entry points share: the descriptor; a row stride (elements)
+// that covers the row and keeps 16-byte alignment; an address.
+pa_status check_desc(const pa_cache_desc* d);
+inline int64_t row_elems(const pa_cache_desc* d) { return static_cast<int64_t>(d->num_kv_heads) * d->head_dim; }
+bool stride_ok(const pa_cache_desc* d, int64_t stride, int64_t min_elems);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Called by every entry point once its arguments are validated, before it
+// launches anything: fetches the device error word and clears a launch error
+// left pending by earlier, unrelated CUDA calls, so that the error checked
+// after our own launches is ours.
+pa_status prepare(unsigned int** err);
+
 inline int elem_bytes(int dtype) { return dtype == PA_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------------------
@@ -191,9 +204,16 @@ struct DecodeArgs {
   const void* v_new = nullptr;
   int64_t k_new_stride_bytes = 0, v_new_stride_bytes = 0;
   int64_t* slot_out = nullptr;
+  // keys left out of the context (launch_decode_window)
+  int32_t window = 0, sinks = 0;
 };
 cudaError_t launch_decode(const pa_cache_desc& d, const DecodePlan& plan, const DecodeArgs& a,
                           cudaStream_t s);
+// The same over the first `sinks` and the last `window` keys of each request.
+cudaError_t plan_decode_window(const pa_cache_desc& d, int batch, int max_context_len, int window, int sinks,
+                               int max_ctas, DecodePlan* out);
+cudaError_t launch_decode_window(const pa_cache_desc& d, const DecodePlan& plan, const DecodeArgs& a,
+                                 cudaStream_t s);
 // The same over a 4-bit cache with groups of gs dims.
 cudaError_t plan_decode_q4(const pa_cache_desc& d, int gs, int batch, int max_context_len, int max_ctas,
                            DecodePlan* out);
