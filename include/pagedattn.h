@@ -440,6 +440,60 @@ PA_API pa_status pa_decode_kv_write_window(const pa_cache_desc* desc, int32_t wi
                                            int32_t max_ctas, int64_t* slot_mapping, void* out, void* workspace,
                                            size_t workspace_bytes, pa_stream_t stream);
 
+/* pa_prefill_varlen over the window and the sinks; the workspace's size is
+ * pa_prefill_workspace_size. */
+PA_API pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t window, int32_t num_sinks,
+                                          const void* q, const int32_t* cu_seqlens_q, int32_t batch,
+                                          int32_t max_seqlen_q, int64_t num_tokens, const void* k_cache,
+                                          const void* v_cache, const int32_t* block_tables,
+                                          int32_t max_pages_per_seq, const int32_t* context_lens,
+                                          int32_t max_context_len, float scale, void* out, void* workspace,
+                                          size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_decode_shared_prefix -- pa_decode for groups of requests whose first tokens
+ * are the same (what the block manager's prefix sharing makes: leading entries
+ * of their block tables that name the same pages).  The result is pa_decode's;
+ * a group's prefix is read once for all its requests, not once for each.
+ *
+ *   num_groups       groups (host); 0: every request stands alone.
+ *   cu_groups        int32 [num_groups+1], 0 <= cu[0] <= cu[1] <= ... <= batch:
+ *                    group g is requests cu[g] .. cu[g+1]-1.  Requests in no
+ *                    group stand alone.
+ *   prefix_lens      int32 [num_groups], tokens that all requests of the group
+ *                    share, each in [0, max_prefix_len]; 0: none.  They are read
+ *                    through the table of the group's first live request of at
+ *                    least that many tokens; the others' first tokens are not
+ *                    looked at.  A prefix may end inside a page: each request's
+ *                    own page then holds its own tokens from there on.
+ *   max_prefix_len   host upper bound on prefix_lens (0: none is shared).
+ *   scale            finite and > 0.
+ *   other arguments  as pa_decode.  max_ctas bounds the partitions of the
+ *                    prefixes' keys and those of the requests' own keys.
+ *   workspace        >= pa_decode_shared_prefix_workspace_size(...) bytes.
+ * A request shorter than its group's prefix, or of a group whose prefix_lens is
+ * out of range, is skipped (its output untouched) and flagged
+ * PA_DEVERR_BAD_LENGTH; padding rows (context_lens[b] == 0) inside a group are
+ * skipped silently.  Launches: the kernel over the prefixes, the decode kernel
+ * over the requests' own tokens (starting as the former's CTAs end) and the
+ * merge.  bf16 with head_dim 128 needs num_pages * page_size < 2^31 (else
+ * PA_ERR_UNSUPPORTED), and takes a page of the prefix that is out of range
+ * (PA_DEVERR_BAD_PAGE) as rows of zeros, like pa_prefill_varlen.
+ */
+PA_API pa_status pa_decode_shared_prefix(const pa_cache_desc* desc, int32_t num_groups, const int32_t* cu_groups,
+                                         const int32_t* prefix_lens, int32_t max_prefix_len, const void* q,
+                                         int32_t batch, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, int32_t max_pages_per_seq,
+                                         const int32_t* context_lens, int32_t max_context_len, float scale,
+                                         int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes,
+                                         pa_stream_t stream);
+
+/* Bytes of device workspace pa_decode_shared_prefix needs; as
+ * pa_decode_workspace_size. */
+PA_API size_t pa_decode_shared_prefix_workspace_size(const pa_cache_desc* desc, int32_t num_groups, int32_t batch,
+                                                     int32_t max_prefix_len, int32_t max_context_len,
+                                                     int32_t max_ctas);
+
 /* ---------------------------------------------------------------------------
  * A cache held in 4 bits.  The calls below stand beside their namesakes above:
  * desc describes the heads, the pages and the type of q, k, v rows and outputs

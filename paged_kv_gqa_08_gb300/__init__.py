@@ -109,6 +109,11 @@ _SIGS = {
                                 ctypes.c_size_t, _VP]),
     "pa_decode_kv_write_window": (_I32, [_DESC, _I32, _I32, _VP, _VP, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _I32, _VP,
                                          _I32, _F32, _I32, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "pa_prefill_varlen_window": (_I32, [_DESC, _I32, _I32, _VP, _VP, _I32, _I32, _I64, _VP, _VP, _VP, _I32, _VP, _I32,
+                                        _F32, _VP, _VP, ctypes.c_size_t, _VP]),
+    "pa_decode_shared_prefix_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _I32, _I32]),
+    "pa_decode_shared_prefix": (_I32, [_DESC, _I32, _VP, _VP, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _F32,
+                                       _I32, _VP, _VP, ctypes.c_size_t, _VP]),
     "pa_validate_metadata": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP]),
     "pa_selftest_bounded_wait": (_I32, [_I32, _VP]),
     "pa_read_device_errors": (_I32, [ctypes.POINTER(ctypes.c_uint32), _I32]),
@@ -464,6 +469,30 @@ def pa_decode_kv_write_window(desc, window, num_sinks, q, k_new, k_row_stride, v
         desc, window, num_sinks, _at(q), _at(k_new), k_row_stride, _at(v_new), v_row_stride, batch, _at(k_cache),
         _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
         _at(slot_mapping), _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+
+
+def pa_prefill_varlen_window(desc, window, num_sinks, q, cu_seqlens_q, batch, max_seqlen_q, num_tokens, k_cache,
+                             v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len, scale, out,
+                             workspace=None, workspace_bytes=None, stream=None):
+    _check("pa_prefill_varlen_window", load_library().pa_prefill_varlen_window(
+        desc, window, num_sinks, _at(q), _at(cu_seqlens_q), batch, max_seqlen_q, num_tokens, _at(k_cache),
+        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, _at(out),
+        _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+
+
+def pa_decode_shared_prefix_workspace_size(desc, num_groups, batch, max_prefix_len, max_context_len,
+                                           max_ctas=0) -> int:
+    return int(load_library().pa_decode_shared_prefix_workspace_size(desc, num_groups, batch, max_prefix_len,
+                                                                     max_context_len, max_ctas))
+
+
+def pa_decode_shared_prefix(desc, num_groups, cu_groups, prefix_lens, max_prefix_len, q, batch, k_cache, v_cache,
+                            block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas, out,
+                            workspace, workspace_bytes=None, stream=None):
+    _check("pa_decode_shared_prefix", load_library().pa_decode_shared_prefix(
+        desc, num_groups, _at(cu_groups), _at(prefix_lens), max_prefix_len, _at(q), batch, _at(k_cache),
+        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
+        _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,

@@ -237,6 +237,28 @@ pa_status prefill_norm_params(const pa_cache_desc* desc, const void* q, int64_t 
   return PA_OK;
 }
 
+// The descriptor and group size of a 4-bit cache.
+pa_status check_q4(const pa_cache_desc* d, int32_t group_size) {
+  pa_status st = check_desc(d);
+  if (st != PA_OK) return st;
+  if (group_size != 32 && group_size != 64 && group_size != 128) return PA_ERR_UNSUPPORTED;
+  if (group_size > d->head_dim) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// pa_decode_q4's and pa_decode_kv_write_q4's plan, once their arguments are checked.
+pa_status plan_q4(const pa_cache_desc* desc, int32_t gs, int32_t batch, int32_t max_context_len, int32_t max_ctas,
+                  const void* workspace, size_t workspace_bytes, DecodePlan* pl) {
+  if (!workspace) return PA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_ALIGN;
+  cudaError_t e = plan_decode_q4(*desc, gs, batch, max_context_len, max_ctas, pl);
+  if (e == cudaErrorInvalidValue) return PA_ERR_UNSUPPORTED;
+  if (e != cudaSuccess) return cuda_fail(e);
+  return workspace_bytes < pl->ws_bytes ? PA_ERR_WORKSPACE : PA_OK;
+}
+
+}  // namespace
+
 // Checks of pa_prefill_varlen's arguments and its launch arguments, the error
 // word left to the caller; a->num_tokens == 0 when there is nothing to do.
 pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* cu_seqlens_q, int32_t batch,
@@ -280,31 +302,10 @@ pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* 
   return PA_OK;
 }
 
-// The descriptor and group size of a 4-bit cache.
-pa_status check_q4(const pa_cache_desc* d, int32_t group_size) {
-  pa_status st = check_desc(d);
-  if (st != PA_OK) return st;
-  if (group_size != 32 && group_size != 64 && group_size != 128) return PA_ERR_UNSUPPORTED;
-  if (group_size > d->head_dim) return PA_ERR_UNSUPPORTED;
-  return PA_OK;
-}
-
-// pa_decode_q4's and pa_decode_kv_write_q4's plan, once their arguments are checked.
-pa_status plan_q4(const pa_cache_desc* desc, int32_t gs, int32_t batch, int32_t max_context_len, int32_t max_ctas,
-                  const void* workspace, size_t workspace_bytes, DecodePlan* pl) {
-  if (!workspace) return PA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_ALIGN;
-  cudaError_t e = plan_decode_q4(*desc, gs, batch, max_context_len, max_ctas, pl);
-  if (e == cudaErrorInvalidValue) return PA_ERR_UNSUPPORTED;
-  if (e != cudaSuccess) return cuda_fail(e);
-  return workspace_bytes < pl->ws_bytes ? PA_ERR_WORKSPACE : PA_OK;
-}
-
 cudaError_t launch_prefill(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
   return d.dtype == PA_BF16 && d.head_dim == 128 ? launch_prefill_tc(d, a, s) : launch_prefill_simt(d, a, s);
 }
 
-}  // namespace
 }  // namespace pa
 
 using namespace pa;

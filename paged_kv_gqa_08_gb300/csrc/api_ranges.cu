@@ -110,4 +110,78 @@ pa_status pa_decode_kv_write_window(const pa_cache_desc* desc, int32_t window, i
   return decode_window(desc, a, max_ctas, workspace_bytes, stream);
 }
 
+pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t window, int32_t num_sinks, const void* q,
+                                   const int32_t* cu_seqlens_q, int32_t batch, int32_t max_seqlen_q,
+                                   int64_t num_tokens, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int32_t max_pages_per_seq,
+                                   const int32_t* context_lens, int32_t max_context_len, float scale, void* out,
+                                   void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if ((st = check_window(window, num_sinks)) != PA_OK) return st;
+  PrefillArgs a;
+  st = prefill_args(desc, q, cu_seqlens_q, batch, max_seqlen_q, num_tokens, k_cache, v_cache, block_tables,
+                    max_pages_per_seq, context_lens, max_context_len, scale, out, workspace, workspace_bytes, &a);
+  if (st != PA_OK || a.num_tokens == 0) return st;
+  // a window of the whole context sees what no window sees
+  if (static_cast<int64_t>(window) + num_sinks < max_context_len) {
+    a.window = window;
+    a.sinks = num_sinks;
+  }
+  if ((st = prepare(&a.err)) != PA_OK) return st;
+  cudaError_t e = launch_prefill(*desc, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+size_t pa_decode_shared_prefix_workspace_size(const pa_cache_desc* desc, int32_t num_groups, int32_t batch,
+                                              int32_t max_prefix_len, int32_t max_context_len, int32_t max_ctas) {
+  if (check_desc(desc) != PA_OK || num_groups < 0 || batch < 1 || max_prefix_len < 0 || max_context_len < 1 ||
+      max_ctas < 0)
+    return 0;
+  SharedPlan pl;
+  if (plan_shared(*desc, num_groups, batch, max_prefix_len, max_context_len, max_ctas, &pl) != cudaSuccess) return 0;
+  return pl.ws_bytes;
+}
+
+pa_status pa_decode_shared_prefix(const pa_cache_desc* desc, int32_t num_groups, const int32_t* cu_groups,
+                                  const int32_t* prefix_lens, int32_t max_prefix_len, const void* q, int32_t batch,
+                                  const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                  int32_t max_pages_per_seq, const int32_t* context_lens, int32_t max_context_len,
+                                  float scale, int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes,
+                                  pa_stream_t stream) {
+  pa_status st = check_decode_args(desc, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens,
+                                   max_context_len, scale, max_ctas, out);
+  if (st != PA_OK) return st;
+  if (num_groups < 0 || max_prefix_len < 0) return PA_ERR_SHAPE;
+  if (batch == 0) return PA_OK;
+  if (max_prefix_len > max_context_len) return PA_ERR_SHAPE;
+  if (!(scale > 0.f)) return PA_ERR_SHAPE;  // the tensor-core kernel takes the maximum before it scales
+  if (num_groups > 0 && (!cu_groups || !prefix_lens)) return PA_ERR_NULL;
+  if ((st = check_workspace(workspace)) != PA_OK) return st;
+  SharedPlan pl;
+  cudaError_t e = plan_shared(*desc, num_groups, batch, max_prefix_len, max_context_len, max_ctas, &pl);
+  if (e == cudaErrorInvalidValue) return PA_ERR_UNSUPPORTED;
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (workspace_bytes < pl.ws_bytes) return PA_ERR_WORKSPACE;
+  SharedArgs a{};
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_groups = cu_groups;
+  a.prefix_lens = prefix_lens;
+  a.out = out;
+  a.workspace = workspace;
+  a.n_groups = num_groups;
+  a.max_prefix = max_prefix_len;
+  a.batch = batch;
+  a.max_pages = max_pages_per_seq;
+  a.max_context_len = max_context_len;
+  a.scale = scale;
+  if ((st = prepare(&a.err)) != PA_OK) return st;
+  e = launch_shared(*desc, pl, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 }  // extern "C"

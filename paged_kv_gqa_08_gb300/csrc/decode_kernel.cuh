@@ -372,7 +372,13 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
   const int NC = cs[p.B];
   const int x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / p.n_ctas);
   const int x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / p.n_ctas);
-  if (x0 >= x1) return;
+  // With groups the grid starts beside the kernel over their prefixes, whose
+  // output only the merge reads: each CTA's last act is to wait for it.
+  const bool beside = kRange && p.cu_groups != nullptr;
+  if (x0 >= x1) {
+    if (beside) pdl_wait();
+    return;
+  }
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
   uint64_t* empty = full + kStages;
@@ -505,6 +511,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
       for (int it = max(0, issued - kStages); it < issued; ++it)
         drain_wait(&full[it % kStages], (it / kStages) & 1);
     }
+    if (beside) pdl_wait();
     return;
   }
 

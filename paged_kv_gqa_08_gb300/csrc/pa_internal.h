@@ -262,6 +262,7 @@ struct PrefillArgs {
   // output, so the planner may start beside it (and waits for it before it
   // exits, which the attention kernel's wait on the planner then covers).
   bool planner_beside_write = false;
+  int32_t window = 0, sinks = 0;  // window > 0: only the last `window` and the first `sinks` keys are seen
 };
 // Workspace layout of the planned tensor-core prefill (byte offsets, each
 // 256-aligned); ws_bytes == 0 when the call cannot be planned.
@@ -272,10 +273,58 @@ struct PrefillPlan {
 };
 cudaError_t plan_prefill(const pa_cache_desc& d, int32_t batch, int32_t max_seqlen_q, int64_t num_tokens,
                          int32_t max_context_len, PrefillPlan* out);
+// Checks of pa_prefill_varlen's arguments and its launch arguments, the error
+// word left to the caller; a->num_tokens == 0 when there is nothing to do.
+pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* cu_seqlens_q, int32_t batch,
+                       int32_t max_seqlen_q, int64_t num_tokens, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int32_t max_pages_per_seq, const int32_t* context_lens,
+                       int32_t max_context_len, float scale, void* out, void* workspace, size_t workspace_bytes,
+                       PrefillArgs* a);
+// The kernel below that takes this type and head_dim.
+cudaError_t launch_prefill(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
 // CUDA-core kernel (any supported dtype / head_dim).
 cudaError_t launch_prefill_simt(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
 // tcgen05 tensor-core kernel (bf16, head_dim 128).
 cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// decode for groups of requests that share a prefix
+// ---------------------------------------------------------------------------
+struct SharedArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  void* out;
+  void* workspace;
+  unsigned int* err;
+  int32_t n_groups, max_prefix;
+  int32_t batch, max_pages, max_context_len;
+  float scale;
+};
+// The groups as the kernels over the prefixes cut them (prefix_plan.cuh).
+struct PrefixShape {
+  const int32_t* cu;
+  const int32_t* pre;
+  const int32_t* ctx;
+  int32_t n_groups, B, max_prefix, cap_ctx;
+  int32_t TQ, Hkv;              // requests per q-tile, kv-heads
+  int32_t cost_pair, cost_one;  // cost of a key tile of a unit of two q-tiles, and of one
+};
+struct SharedPlan {
+  DecodePlan suffix;  // the requests' own keys
+  int32_t prefix_ctas = 0, TQ = 0, cost_pair = 0, cost_one = 0;
+  size_t off_lse = 0, off_o = 0, ws_bytes = 0;  // the suffix's workspace comes first
+};
+PrefixShape prefix_shape(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl);
+cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max_prefix, int max_context_len,
+                        int max_ctas, SharedPlan* out);
+cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const SharedArgs& a, cudaStream_t s);
+// The prefixes' part in bf16 with head_dim 128 (tcgen05).
+cudaError_t launch_prefix_tc(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // metadata validation

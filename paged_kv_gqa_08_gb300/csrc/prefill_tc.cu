@@ -68,6 +68,7 @@
 #include <type_traits>
 
 #include "pa_common.cuh"
+#include "prefix_plan.cuh"
 
 namespace pa {
 namespace {
@@ -111,6 +112,11 @@ constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(k
                               ((uint32_t)(kBM >> 4) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);  // B (= V) is MN-major
 
+// What the rows of an item see: all keys up to their own (chunked prefill); of
+// those the last `window` and the first `sinks`; or, alike for all rows, the keys
+// of a prefix that a group of decode requests shares.
+enum Mode { kCausal, kWindow, kPrefix };
+
 struct TcParams {
   CUtensorMap tm_q;    // q      [num_tokens, Hq, 128], box {64, G, TQ}
   CUtensorMap tm_k16;  // k_cache rows, box {64, 16}
@@ -137,6 +143,8 @@ struct TcParams {
   int32_t* counter;  // next item to hand out (zeroed by the planner)
   float* o_part;    // [slot][Hkv][2 q-tiles][128 rows][128]
   float* lse_part;  // [slot][Hkv][2 q-tiles][128 rows]
+  int32_t window, sinks;  // kWindow
+  PrefixShape prefix;     // kPrefix: the groups, whose parts' rows are laid out as prefix_plan.cuh says
 };
 
 // ---------------------------------------------------------------------------
@@ -272,13 +280,43 @@ struct Item {
   int32_t rows[2];  // live tokens of that q-tile
   int32_t pos0[2];  // position of its first token
   int32_t kv_len;   // keys the pair needs (last token's position + 1)
-  int32_t pad[5];
+  // kWindow: no row of the pair sees keys [gap_lo, gap_hi); an item's key tiles
+  // count the `skip` tiles from tile `before` on, wholly inside, out
+  int32_t before, skip, gap_lo, gap_hi;
+  int32_t part_row;  // kPrefix: the part's row of the unit's first token
 };
 static_assert(sizeof(Item) == 96, "two items fit their shared-memory slot");
+
+// kWindow: the gap in the keys that a q-tile pair whose first token sits at
+// position p0 sees, and the 128-key tiles wholly inside it.
+struct Gap {
+  int lo, hi, before, skip;
+};
+PA_DEVINL Gap window_gap(int p0, int window, int sinks) {
+  Gap g;
+  g.hi = max(0, p0 - window + 1);
+  g.lo = min(sinks, g.hi);
+  g.before = (g.lo + kBN - 1) / kBN;
+  g.skip = max(0, g.hi / kBN - g.before);
+  return g;
+}
+
+// The key tile that an item's tile j is.
+template <Mode kMode>
+PA_DEVINL int key_tile(const Item& it, int j) {
+  return kMode == kWindow && j >= it.before ? j + it.skip : j;
+}
+
+// Row 0 .. 15 of the 16-row box at key k0 that some row of the pair sees, as bits.
+PA_DEVINL uint32_t seen_rows(const Item& it, int k0) {
+  auto below = [&](int k) { return (1u << min(max(k - k0, 0), 16)) - 1; };
+  return below(it.kv_len) & ~(below(it.gap_hi) & ~below(it.gap_lo));
+}
 
 // The work of pair qp of request b for kv-head h over key tiles [j_lo, j_hi).
 // False when there is none (a padding row, an empty range, a pair without
 // rows) or the request's lengths are inconsistent (flagged).
+template <Mode kMode>
 PA_DEVINL bool make_item(const TcParams& p, int b, int qp, int h, int j_lo, int j_hi, int slot, Item& it) {
   const int s0 = p.cu[b], s1 = p.cu[b + 1];
   const int n = s1 - s0;
@@ -298,6 +336,17 @@ PA_DEVINL bool make_item(const TcParams& p, int b, int qp, int h, int j_lo, int 
     rows[g] = g < nq ? min(p.TQ, n - qt * p.TQ) : 0;
     pos0[g] = L - n + qt * p.TQ;
     ntg[g] = g < nq ? (pos0[g] + rows[g] + kBN - 1) / kBN : 0;
+  }
+  it.before = it.skip = it.gap_lo = it.gap_hi = it.part_row = 0;
+  if constexpr (kMode == kWindow) {
+    const Gap gap = window_gap(pos0[0], p.window, p.sinks);
+    it.before = gap.before;
+    it.skip = gap.skip;
+    it.gap_lo = gap.lo;
+    it.gap_hi = gap.hi;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (g < nq) ntg[g] -= gap.skip;
   }
   j_hi = min(j_hi, ntg[nq - 1]);
   const int nt = j_hi - j_lo;
@@ -332,6 +381,31 @@ PA_DEVINL bool make_item(const TcParams& p, int b, int qp, int h, int j_lo, int 
     }
   }
   return true;
+}
+
+// kPrefix: key tiles [w.j_lo, w.j_hi) of a unit of CTA c's share.
+PA_DEVINL void make_prefix_item(const TcParams& p, const PrefixWork& w, int c, Item& it) {
+  it.valid = 1;
+  it.b = w.rep;
+  it.h = w.h;
+  it.qp = w.qp;
+  it.j_lo = w.j_lo;
+  it.nt = w.j_hi - w.j_lo;
+  it.slot = 0;
+  it.s0 = w.s0;
+  it.nq = (2 * w.qp + 1) * p.TQ < w.n ? 2 : 1;
+  it.split = it.nq == 1;
+  it.kv_len = w.prefix;
+  it.before = it.skip = it.gap_lo = it.gap_hi = 0;
+  it.part_row = prefix_part_row(w.s0, w.n, w.h, c, p.Hq, p.G);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int qt = it.split ? 0 : g;
+    it.c[g] = it.split ? (it.nt + 1 - g) / 2 : it.nt;
+    it.qt[g] = qt;
+    it.rows[g] = min(p.TQ, w.n - (2 * w.qp + qt) * p.TQ);
+    it.pos0[g] = w.prefix - 1;  // every row sees the whole prefix
+  }
 }
 
 // Wait (lane 0) for work item i, copy it to every lane and release its slot.
@@ -522,13 +596,14 @@ struct SoftmaxArgs {
   float* o_part;
   float* lse_part;
   unsigned int* err;
-  int32_t Hq, Hkv, G, TQ;
+  int32_t Hq, Hkv, G, TQ, window, sinks;
   float scale_log2;
 };
 
 // The two softmax warpgroups (warps 0-7).  A function of its own, entered
 // after the warpgroups' register rebalance, so that it is compiled for the
 // larger register budget.
+template <Mode kMode>
 __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* smem, uint32_t tmem, int warp,
                                           int lane) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -572,10 +647,11 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
     const int c = g ? c1 : c0;
     const int p0 = g ? it.pos0[1] : it.pos0[0];
     const int qtg = g ? it.qt[1] : it.qt[0];
-    const int pos_r = p0 + t_r;
+    const int pos_r = kMode == kPrefix ? p0 : p0 + t_r;
     const bool live = row < p.TQ * p.G && t_r < (g ? it.rows[1] : it.rows[0]);
     const int j_lo = it.j_lo, split = it.split, slot = it.slot, hh_kv = it.h;
     const int it_qp = it.qp, it_s0 = it.s0;
+    [[maybe_unused]] const int before = it.before, skip = it.skip, part_row = it.part_row;
     float m_used = -INFINITY, l = 0.f;
     for (int s = 0; s < c; ++s) {
       ok = mbar_wait_bounded(&s_full[g], sc & 1, abort_flag, p.err);
@@ -585,8 +661,12 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         break;
       }
       tc_fence_after();
-      const int key0 = (j_lo + (split ? 2 * s + g : s)) * kBN;
-      const bool need_mask = key0 + kBN - 1 > p0;
+      int tile = j_lo + (split ? 2 * s + g : s);
+      if (kMode == kWindow && tile >= before) tile += skip;
+      const int key0 = tile * kBN;
+      // (kWindow: the last row's window may start behind the tile's first key)
+      const bool need_mask = key0 + kBN - 1 > p0 ||
+                             (kMode == kWindow && key0 <= p0 + p.TQ - 1 - p.window && key0 + kBN > p.sinks);
       // One TMEM round trip per tile: all 128 scores of the row are loaded
       // (four loads, one wait), the row max is taken over the raw scores (the
       // scale is positive, so it commutes with the max) with eight independent
@@ -599,7 +679,8 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
       if (need_mask) {
 #pragma unroll
         for (int e = 0; e < 128; ++e)
-          if (key0 + e > pos_r) x[e] = __float_as_uint(-INFINITY);
+          if (key0 + e > pos_r || (kMode == kWindow && key0 + e <= pos_r - p.window && key0 + e >= p.sinks))
+            x[e] = __float_as_uint(-INFINITY);
       }
       float mx;
       {
@@ -669,7 +750,12 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
     pc[0] += c0;
     pc[1] += c1;
     const int qt = 2 * it_qp + qtg;  // q-tile index in the request
-    const int64_t prow = ((static_cast<int64_t>(slot) * p.Hkv + hh_kv) * 2 + qtg) * kBM + row;
+    // a part's row (kPrefix: packed rows, of which only live ones exist)
+    const int64_t prow = kMode == kPrefix
+                             ? static_cast<int64_t>(part_row) + qt * p.TQ * p.G + row
+                             : ((static_cast<int64_t>(slot) * p.Hkv + hh_kv) * 2 + qtg) * kBM + row;
+    const bool to_part = slot >= 0 && (kMode != kPrefix || live);
+    const bool to_out = live && kMode != kPrefix;
     char* dst = p.out + ((static_cast<int64_t>(it_s0) + qt * p.TQ + t_r) * p.Hq + hh_kv * p.G + gg) * 256;
     if (!split) {
       // ------------- pair mode epilogue: this group's q-tile -------------
@@ -694,9 +780,9 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         if (p.tm_o != nullptr && slot < 0 && __all_sync(0xffffffffu, live))
           store_rows_tma(o, inv, stage, p.tm_o, hh_kv * p.G, it_s0 + qt * p.TQ + wq * 32 / p.G, lane, tma_pending);
         else
-          store_cols<0>(o, inv, slot >= 0, live, p.o_part + prow * 128, dst, p.out32);
-        if (slot >= 0) p.lse_part[prow] = l > 0.f ? m_used + __log2f(l) : -INFINITY;
-      } else if (slot >= 0) {
+          store_cols<0>(o, inv, to_part, to_out, p.o_part + prow * 128, dst, p.out32);
+        if (to_part) p.lse_part[prow] = l > 0.f ? m_used + __log2f(l) : -INFINITY;
+      } else if (to_part) {
         p.lse_part[prow] = -INFINITY;  // no key tile of this part reaches the q-tile
       }
     } else if (g == 1) {
@@ -751,7 +837,7 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a0);
         }
-        store_cols<0>(o, 1.f, slot >= 0, live, p.o_part + prow * 128 + 32 * q, dst + 64 * q, p.out32);
+        store_cols<0>(o, 1.f, to_part, to_out, p.o_part + prow * 128 + 32 * q, dst + 64 * q, p.out32);
       }
       tc_fence_before();
       __syncwarp();
@@ -760,7 +846,7 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         mbar_arrive(&o_free[0]);
         if (two) mbar_arrive(&o_free[1]);
       }
-      if (slot >= 0) p.lse_part[prow] = lsum > 0.f ? mm + __log2f(lsum) : -INFINITY;
+      if (to_part) p.lse_part[prow] = lsum > 0.f ? mm + __log2f(lsum) : -INFINITY;
       ++ms;
     }
   }
@@ -768,12 +854,13 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
   if (tma_pending && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ TcParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (p.units) {
+  if (p.units || kMode == kPrefix) {
     pdl_trigger();  // the merge kernel may start launching; it waits for this grid
   } else {
     // one pair per CTA: a pair without rows leaves at once (the same for every thread)
@@ -860,8 +947,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     sa.Hkv = p.Hkv;
     sa.G = p.G;
     sa.TQ = p.TQ;
+    sa.window = p.window;
+    sa.sinks = p.sinks;
     sa.scale_log2 = p.scale_log2;
-    softmax_role(sa, smem, tmem, warp, lane);
+    softmax_role<kMode>(sa, smem, tmem, warp, lane);
     tc_fence_before();
     cta_sync();  // pairs with the other warpgroup's barrier before the TMEM is freed
     return;
@@ -872,6 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     // Planned launch: items k = unit * Hkv + kv-head are taken from a shared
     // counter, so a CTA that finishes early takes the next one (the units are
     // listed longest first).  Otherwise the CTA's own pair is its one item.
+    // A shared prefix: the CTA's share of the groups' key tiles, unit by unit.
+    PrefixShare share;
+    if constexpr (kMode == kPrefix) share = prefix_share(p.prefix, blockIdx.x, gridDim.x);
     if (lane == 0) {
       if (p.units) pdl_wait();  // the planner's unit list and counter are ready
       const int total = p.units ? *p.n_units * p.Hkv : 1;
@@ -896,9 +988,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           }
           if (!okg) break;
         }
-        const int k = p.units ? atomicAdd(p.counter, 1) : k_own++;
-        const bool last = k >= total;
-        if (!last) {
+        bool last;
+        int k = 0;
+        if constexpr (kMode == kPrefix) {
+          PrefixWork w;
+          last = !next_prefix_work(p.prefix, share, w);
+          if (!last) make_prefix_item(p, w, blockIdx.x, it);
+        } else {
+          k = p.units ? atomicAdd(p.counter, 1) : k_own++;
+          last = k >= total;
+        }
+        if (kMode != kPrefix && !last) {
           int b, qp, h, jl, jh, sl;
           if (p.units) {
             const int u = k / p.Hkv;
@@ -917,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             jh = 1 << 30;
             sl = -1;
           }
-          if (!make_item(p, b, qp, h, jl, jh, sl, it)) continue;
+          if (!make_item<kMode>(p, b, qp, h, jl, jh, sl, it)) continue;
         }
         const int s = pub & 1;
         // the slot frees when every role has taken the item two back: poll
@@ -967,8 +1067,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       const int x = it.h * 128 + half * 64;
       // Block-table entries of tile t: lane `box` reads the page of its 16-row
       // box, lanes 0-3 the page of a ragged end.
+      // (kWindow: of its box, whichever of the box's rows are seen.)
       auto load_pages = [&](int t, int& pg_full, int& pg_rem) {
-        const int t0 = (it.j_lo + t) * kBN;
+        const int t0 = key_tile<kMode>(it, it.j_lo + t) * kBN;
+        if constexpr (kMode == kWindow) {
+          const int k0 = t0 + box * kBoxRows;
+          pg_full = seen_rows(it, k0) ? p.bt[bt_row + (k0 >> p.log2P)] : kNoPage;
+          pg_rem = kNoPage;
+          return;
+        }
         const int valid = min(kBN, it.kv_len - t0);
         const int nfull = valid / kBoxRows, rem = valid % kBoxRows;
         pg_full = box < nfull ? p.bt[bt_row + ((t0 + box * kBoxRows) >> p.log2P)] : kNoPage;
@@ -1000,9 +1107,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         const int pf = pf_next, pr = pr_next;
         if (t + 1 < it.nt) load_pages(t + 1, pf_next, pr_next);  // one tile ahead
         const int st = kc & 1;
-        const int t0 = (it.j_lo + t) * kBN;
+        const int t0 = key_tile<kMode>(it, it.j_lo + t) * kBN;
         const int valid = min(kBN, it.kv_len - t0);
         const int nfull = valid / kBoxRows, rem = valid % kBoxRows;
+        const uint32_t seen = kMode == kWindow ? seen_rows(it, t0 + box * kBoxRows) : 0xffffu;
         int y_full = -1, y_rem = -1;
         if (pf != kNoPage) {
           if (pf >= 0 && pf < p.num_pages) y_full = (pf << p.log2P) + ((t0 + box * kBoxRows) & (p.P - 1));
@@ -1012,7 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           if (pr >= 0 && pr < p.num_pages) y_rem = (pr << p.log2P) + ((t0 + nfull * kBoxRows) & (p.P - 1));
           else raise_flag(p.err, PA_DEVERR_BAD_PAGE);
         }
-        const uint32_t mine = (y_full >= 0 ? kBoxRows * 128 : 0) + (y_rem >= 0 ? rem * 128 : 0);
+        const uint32_t mine = (y_full >= 0 ? (kMode == kWindow ? __popc(seen) : kBoxRows) * 128 : 0) + (y_rem >= 0 ? rem * 128 : 0);
         uint32_t bytes = (isv != 0) == vrole ? mine : 0;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
@@ -1023,7 +1131,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           break;
         }
         unsigned char* stage = smem + (vrole ? kOffV : kOffK) + st * kTileBytes;
-        if (vrole && valid < kBN) {
+        if (kMode == kWindow) {
+          // the rows that no query sees are not copied, and zero where they meet a probability of 0
+          if (vrole && __any_sync(0xffffffffu, seen != 0xffffu)) {
+            for (int c = lane; c < kBN * 16; c += 32) {
+              const int r = c >> 4, ch = c & 15, key = t0 + r;
+              if (key >= it.kv_len || (key >= it.gap_lo && key < it.gap_hi))
+                *reinterpret_cast<uint4*>(stage + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+        } else if (vrole && valid < kBN) {
           // a ragged tile: zero the rows it leaves unloaded (they may hold
           // another request's values), before the copies are counted
           const int chunks = (kBN - valid) * 16;
@@ -1050,7 +1170,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         __syncwarp();
         if ((isv != 0) == vrole) {
           unsigned char* dst = stage + half * kHalfBytes;
-          if (y_full >= 0) tma_load_2d(dst + box * kBoxRows * 128, m16, x, y_full, &full[st]);
+          if (kMode == kWindow && y_full >= 0 && seen != 0xffffu) {
+            for (uint32_t left = seen; left; left &= left - 1) {
+              const int r = __ffs(left) - 1;
+              tma_load_2d(dst + (box * kBoxRows + r) * 128, m1, x, y_full + r, &full[st]);
+            }
+          } else if (y_full >= 0) {
+            tma_load_2d(dst + box * kBoxRows * 128, m16, x, y_full, &full[st]);
+          }
           if (y_rem >= 0)
             for (int r = 0; r < rem; ++r) tma_load_2d(dst + (nfull * kBoxRows + r) * 128, m1, x, y_rem + r, &full[st]);
         }
@@ -1250,6 +1377,7 @@ struct PlanParams {
   int64_t num_tokens;
   int64_t kv_block_tokens;  // context tokens whose K and V fill a third of L2 (0: order by cost alone)
   int32_t B, TQ, Hkv, n_sm, max_seqlen_q, cap_ctx, pair_cap, slot_cap, split_cap;
+  int32_t window, sinks;  // kWindow
 };
 
 // Exclusive prefix sum over the CTA (blockDim.x a multiple of 32, <= 1024).
@@ -1323,7 +1451,7 @@ PA_DEVINL int order_bucket(int len, int nq, int part, int blk, bool blocked) {
 
 // A pair of nt key tiles cut into `parts` ranges: the first nt % parts ranges
 // hold one tile more than the others (lengths base + 1 and base).
-template <bool kScore>
+template <bool kScore, Mode kMode>
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PlanParams q) {
   extern __shared__ int plan_dyn[];  // candidate scoring: see plan_dyn_bytes
   __shared__ unsigned long long sh_scan[32];
@@ -1357,17 +1485,20 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PlanPa
       else
         np = ((n + q.TQ - 1) / q.TQ + 1) / 2;
     }
+    // context tokens that the request's rows read
+    const unsigned long long keys =
+        kMode == kWindow ? min(static_cast<long long>(L), static_cast<long long>(n) + q.window + q.sinks) : L;
     unsigned long long tot, tot_l;
     const unsigned long long off = carry + block_scan_excl<unsigned long long>(np, sh_scan, &tot);
     const unsigned long long l_before =
-        carry_l + block_scan_excl<unsigned long long>(np > 0 ? static_cast<unsigned long long>(L) : 0ull, sh_scan,
-                                                      &tot_l);
+        carry_l + block_scan_excl<unsigned long long>(np > 0 ? keys : 0ull, sh_scan, &tot_l);
     const int blk = q.kv_block_tokens > 0
                         ? static_cast<int>(min(l_before / static_cast<unsigned long long>(q.kv_block_tokens),
                                                static_cast<unsigned long long>(kMaxKvBlocks - 1)))
                         : 0;
     for (int k = 0; k < np; ++k) {
-      const int nt = (L - n + min((2 * k + 2) * q.TQ, n) + kBN - 1) / kBN;
+      int nt = (L - n + min((2 * k + 2) * q.TQ, n) + kBN - 1) / kBN;
+      if constexpr (kMode == kWindow) nt -= window_gap(L - n + 2 * k * q.TQ, q.window, q.sinks).skip;
       const int4 pr = make_int4(b, k, nt, ((2 * k + 1) * q.TQ < n ? 2 : 1) | (blk << 8));
       if (off + k < static_cast<unsigned long long>(q.pair_cap)) q.pairs[off + k] = pr;
       if (off + k < kPlanSmemPairs) sh_pairs[off + k] = pr;
@@ -1737,25 +1868,60 @@ cudaError_t plan_prefill(const pa_cache_desc& d, int32_t batch, int32_t max_seql
   return cudaSuccess;
 }
 
-cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
-  if (a.num_tokens == 0 || a.batch == 0) return cudaSuccess;
+namespace {
+
+// The kernels' attributes on the current device, set once.
+template <Mode kMode>
+cudaError_t prepare_kernels() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    // The warpgroups' register rebalance assumes the launch allocation; a
+    // build with another register count would make the softmax warpgroups
+    // wait for registers that are never released, so it is not launched.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<kMode>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    e = cudaFuncSetAttribute(prefill_tc_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if constexpr (kMode != kPrefix) {
+      int n_sm = 0;
+      if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(prefill_plan_kernel<true, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(plan_dyn_bytes(n_sm)));
+      if (e != cudaSuccess) return e;
+    }
+    done[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+// The tensor maps of q, of the cache and (with out) of the output rows, and
+// what else of the kernel's parameters is the descriptor's.
+cudaError_t cache_params(const pa_cache_desc& d, const void* q, int64_t q_rows, const void* k_cache,
+                         const void* v_cache, void* out, TcParams& p) {
   // TMA coordinates are 32-bit: the cache rows must be addressable.
   if (d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  TcParams p;
   memset(&p, 0, sizeof(p));
   const int G = d.num_q_heads / d.num_kv_heads;
   const int TQ = kBM / G;
   {
-    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d.num_q_heads), static_cast<cuuint64_t>(a.num_tokens)};
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d.num_q_heads), static_cast<cuuint64_t>(q_rows)};
     const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(d.num_q_heads) * 256};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(TQ)};
-    if (!encode(fn, &p.tm_q, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode(fn, &p.tm_q, q, 3, dims, strides, box)) return cudaErrorInvalidValue;
     // output rows by TMA when a softmax warp's 32 rows are whole tokens
-    if ((G & (G - 1)) == 0) {
+    if (out != nullptr && (G & (G - 1)) == 0) {
       const cuuint32_t obox[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(32 / G)};
-      if (!encode(fn, &p.tm_o, a.out, 3, dims, strides, obox)) return cudaErrorInvalidValue;
+      if (!encode(fn, &p.tm_o, out, 3, dims, strides, obox)) return cudaErrorInvalidValue;
       p.o_tma = 1;
     }
   }
@@ -1764,20 +1930,13 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
                                 static_cast<cuuint64_t>(d.num_pages) * d.page_size};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.num_kv_heads) * 256};
     const cuuint32_t box16[2] = {64, kBoxRows}, box1[2] = {64, 1};
-    if (!encode(fn, &p.tm_k16, a.k_cache, 2, dims, strides, box16) ||
-        !encode(fn, &p.tm_k1, a.k_cache, 2, dims, strides, box1) ||
-        !encode(fn, &p.tm_v16, a.v_cache, 2, dims, strides, box16) ||
-        !encode(fn, &p.tm_v1, a.v_cache, 2, dims, strides, box1))
+    if (!encode(fn, &p.tm_k16, k_cache, 2, dims, strides, box16) ||
+        !encode(fn, &p.tm_k1, k_cache, 2, dims, strides, box1) ||
+        !encode(fn, &p.tm_v16, v_cache, 2, dims, strides, box16) ||
+        !encode(fn, &p.tm_v1, v_cache, 2, dims, strides, box1))
       return cudaErrorInvalidValue;
   }
-  p.cu = a.cu_seqlens_q;
-  p.bt = a.block_tables;
-  p.ctx = a.context_lens;
-  p.out = static_cast<char*>(a.out);
-  p.err = a.err;
   p.num_pages = d.num_pages;
-  p.num_tokens = a.num_tokens;
-  p.B = a.batch;
   p.Hq = d.num_q_heads;
   p.Hkv = d.num_kv_heads;
   p.G = G;
@@ -1785,46 +1944,39 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
   p.P = d.page_size;
   p.log2P = 0;
   while ((1 << p.log2P) < d.page_size) ++p.log2P;
+  return cudaSuccess;
+}
+
+template <Mode kMode>
+cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
+  if (a.num_tokens == 0 || a.batch == 0) return cudaSuccess;
+  TcParams p;
+  cudaError_t e = cache_params(d, a.q, a.num_tokens, a.k_cache, a.v_cache, a.out, p);
+  if (e != cudaSuccess) return e;
+  const int TQ = p.TQ;
+  p.cu = a.cu_seqlens_q;
+  p.bt = a.block_tables;
+  p.ctx = a.context_lens;
+  p.out = static_cast<char*>(a.out);
+  p.err = a.err;
+  p.num_tokens = a.num_tokens;
+  p.B = a.batch;
   p.maxp = a.max_pages;
   p.max_ctx = a.max_context_len;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-
-  {
-    static std::mutex mu;
-    static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev]) {
-      // The warpgroups' register rebalance assumes the launch allocation; a
-      // build with another register count would make the softmax warpgroups
-      // wait for registers that are never released, so it is not launched.
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, prefill_tc_kernel);
-      if (e != cudaSuccess) return e;
-      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-      e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-      if (e != cudaSuccess) return e;
-      int n_sm = 0;
-      if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(prefill_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(plan_dyn_bytes(n_sm)));
-      if (e != cudaSuccess) return e;
-      done[dev] = true;
-    }
-  }
+  p.window = a.window;
+  p.sinks = a.sinks;
+  if ((e = prepare_kernels<kMode>()) != cudaSuccess) return e;
   if (!a.workspace) {
     const int qtiles = (a.max_seqlen_q + TQ - 1) / TQ;
     const dim3 grid((qtiles + 1) / 2, d.num_kv_heads, a.batch);
-    prefill_tc_kernel<<<grid, kThreads, kSmemBytes, s>>>(p);
+    prefill_tc_kernel<kMode><<<grid, kThreads, kSmemBytes, s>>>(p);
     return cudaGetLastError();
   }
 
   // planned launch: planner -> attention units -> merge of split pairs
   PrefillPlan pl;
-  cudaError_t e = plan_prefill(d, a.batch, a.max_seqlen_q, a.num_tokens, a.max_context_len, &pl);
+  e = plan_prefill(d, a.batch, a.max_seqlen_q, a.num_tokens, a.max_context_len, &pl);
   if (e != cudaSuccess) return e;
   if (pl.ws_bytes == 0 || a.workspace_bytes < pl.ws_bytes) return cudaErrorInvalidValue;
   char* ws = static_cast<char*>(a.workspace);
@@ -1848,6 +2000,8 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
     const int64_t kv_per_token = static_cast<int64_t>(d.num_kv_heads) * 128 * 2 * 2;
     q.kv_block_tokens = di.l2_bytes > 0 ? std::max<int64_t>(1, di.l2_bytes / 3 / kv_per_token) : 0;
   }
+  q.window = a.window;
+  q.sinks = a.sinks;
   q.max_seqlen_q = a.max_seqlen_q;
   q.cap_ctx = static_cast<int32_t>(std::min<int64_t>(a.max_context_len, int64_t(a.max_pages) << p.log2P));
   q.pair_cap = pl.pair_cap;
@@ -1861,8 +2015,8 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
   // planner is a wait on both.  Otherwise it starts after the previous kernel.
   {
     void* args[] = {&q};
-    const void* fn = q.slot_cap > 1 ? reinterpret_cast<const void*>(prefill_plan_kernel<true>)
-                                    : reinterpret_cast<const void*>(prefill_plan_kernel<false>);
+    const void* fn = q.slot_cap > 1 ? reinterpret_cast<const void*>(prefill_plan_kernel<true, kMode>)
+                                    : reinterpret_cast<const void*>(prefill_plan_kernel<false, kMode>);
     const size_t dyn = q.slot_cap > 1 ? plan_dyn_bytes(pl.n_sm) : 0;
     if (a.planner_beside_write)
       e = launch_after_previous(fn, dim3(1), dim3(kPlanThreads), dyn, s, args);
@@ -1882,7 +2036,7 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
     const int64_t items = static_cast<int64_t>(pl.pair_cap + pl.run_slot_cap) * d.num_kv_heads;
     const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(pl.n_sm, items));
     void* args[] = {&p};
-    e = launch_after_previous(reinterpret_cast<const void*>(prefill_tc_kernel), dim3(ctas), dim3(kThreads),
+    e = launch_after_previous(reinterpret_cast<const void*>(prefill_tc_kernel<kMode>), dim3(ctas), dim3(kThreads),
                               kSmemBytes, s, args);
     if (e != cudaSuccess) return e;
   }
@@ -1897,7 +2051,7 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
     m.out = p.out;
     m.Hq = d.num_q_heads;
     m.Hkv = d.num_kv_heads;
-    m.G = G;
+    m.G = p.G;
     m.TQ = TQ;
     void* args[] = {&m};
     e = launch_after_previous(reinterpret_cast<const void*>(prefill_merge_kernel),
@@ -1906,6 +2060,32 @@ cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cuda
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
+  return a.window > 0 ? launch_tc<kWindow>(d, a, s) : launch_tc<kCausal>(d, a, s);
+}
+
+cudaError_t launch_prefix_tc(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl, cudaStream_t s) {
+  TcParams p;
+  cudaError_t e = cache_params(d, a.q, a.batch, a.k_cache, a.v_cache, nullptr, p);
+  if (e != cudaSuccess) return e;
+  char* ws = static_cast<char*>(a.workspace);
+  p.bt = a.block_tables;
+  p.ctx = a.context_lens;
+  p.err = a.err;
+  p.num_tokens = a.batch;
+  p.maxp = a.max_pages;
+  p.max_ctx = a.max_context_len;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.prefix = prefix_shape(d, a, pl);
+  p.lse_part = reinterpret_cast<float*>(ws + pl.off_lse);
+  p.o_part = reinterpret_cast<float*>(ws + pl.off_o);
+  if ((e = prepare_kernels<kPrefix>()) != cudaSuccess) return e;
+  prefill_tc_kernel<kPrefix><<<pl.prefix_ctas, kThreads, kSmemBytes, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace pa
