@@ -94,6 +94,7 @@ typedef void* pa_stream_t;
 #define PA_DEVERR_BAD_PAGE 0x2u     /* a block-table entry outside [0, num_pages) was skipped */
 #define PA_DEVERR_BAD_LENGTH 0x4u   /* a context / chunk length was inconsistent; request skipped */
 #define PA_DEVERR_TIMEOUT 0x8u      /* a bounded wait on an async copy gave up; output invalid */
+#define PA_DEVERR_NO_PAGES 0x10u    /* pa_extend_tables: a request got no pages, the pool has too few */
 
 /*
  * pa_slot_mapping -- positions and physical slots of each request's new tokens.
@@ -493,6 +494,107 @@ PA_API pa_status pa_decode_shared_prefix(const pa_cache_desc* desc, int32_t num_
 PA_API size_t pa_decode_shared_prefix_workspace_size(const pa_cache_desc* desc, int32_t num_groups, int32_t batch,
                                                      int32_t max_prefix_len, int32_t max_context_len,
                                                      int32_t max_ctas);
+
+/* ---------------------------------------------------------------------------
+ * Block tables built on the GPU: the block manager's page rules (at the end of
+ * this file) as device calls, so that a step needs no host copy of the lengths
+ * and can be captured in a graph.  A user of these keeps, in device memory,
+ *
+ *   block_tables     int32 [batch, max_pages_per_seq].
+ *   free_pages       int32 [num_pages], a ring of free pages, first in, first
+ *                    out.  pool_state, int64 {taken, returned}, counts the pages
+ *                    taken from it and put into it since the start: the next one
+ *                    out is free_pages[taken % num_pages], and returned - taken
+ *                    pages are free.  A new pool of all pages holds 0, 1, ... and
+ *                    {0, num_pages}.
+ *   ref_counts       int32 [num_pages], the rows that hold each page (0: free).
+ *                    NULL where every page has one holder: then no page may
+ *                    occur twice in the tables.
+ *
+ * pool_state_out may be pool_state, and context_lens_out context_lens; no
+ * other arrays may overlap.  Pages are handed out and put back in the order of
+ * the rows, the same in every run.  num_pages must be below 2^31.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * pa_extend_tables -- pages, positions and slots for each request's next tokens
+ * (nano-vLLM learning note, BlockManager.allocate and may_append listings;
+ * prepare_prefill / prepare_decode listings for positions and slots).
+ *
+ * Request b has context_lens[b] tokens in ceil(context_lens[b] / page_size)
+ * pages of its table and gets new_tokens[b] more: the pages that takes come from
+ * the ring, requests in order, and are written behind its last entry.
+ *
+ *   new_tokens       int32 [batch], each >= 0.
+ *   context_lens     int32 [batch], the tokens before these (0: a new request, or
+ *                    a padding row where it gets none).
+ *   max_tokens       rows of positions and slot_mapping (host).
+ *   cu_seqlens_q     int32 [batch+1] out: the new tokens' rows, as
+ *                    pa_slot_mapping and prefill take them.
+ *   context_lens_out int32 [batch] out: the tokens with the new ones.
+ *   positions, slot_mapping  int32 / int64 [max_tokens] out, as pa_slot_mapping;
+ *                    rows behind the last token get position 0 and slot -1 (a
+ *                    step of a fixed number of rows stores nothing for them).
+ *   ref_counts       set to 1 for each page handed out (optional).
+ *   pool_state_out   int64 [2] out.
+ * A request gets all it asks for or nothing (cu_seqlens_q shows no rows for it,
+ * its length stays).  It gets nothing when it takes a page and the pages asked
+ * for up to and with it are more than are free (PA_DEVERR_NO_PAGES), when the
+ * tokens asked for up to and with it are more than max_tokens, or when its table
+ * is too short or a length negative (PA_DEVERR_BAD_LENGTH both; the latter counts
+ * as asking for nothing).  A bad entry of the ring or of a row's last page gives -1
+ * and PA_DEVERR_BAD_PAGE, a pool_state that is none counts as empty
+ * (PA_DEVERR_BAD_LENGTH).
+ */
+PA_API pa_status pa_extend_tables(const pa_cache_desc* desc, int32_t batch, const int32_t* new_tokens,
+                                  const int32_t* context_lens, int32_t* block_tables, int32_t max_pages_per_seq,
+                                  const int32_t* free_pages, const int64_t* pool_state, int64_t max_tokens,
+                                  int32_t* cu_seqlens_q, int32_t* context_lens_out, int32_t* positions,
+                                  int64_t* slot_mapping, int32_t* ref_counts, int64_t* pool_state_out,
+                                  pa_stream_t stream);
+
+/*
+ * pa_share_pages -- rows that begin with another row's pages (prefix sharing, a
+ * branch of a running request): the first num_shared_pages[b] entries of row
+ * parents[b] become those of row b, and each page counts one holder more.
+ *
+ *   parents          int32 [batch]; negative: the row is left as it is.  A parent
+ *                    must itself be left as it is in this call.
+ *   num_shared_pages int32 [batch].
+ * The row's own entries there are overwritten (release them before).  Entries of
+ * -1 are copied.  The row's length is the caller's to set, e.g. to
+ * num_shared_pages[b] * page_size, where pa_extend_tables then goes on.  Rows with
+ * a bad parent or count are skipped (PA_DEVERR_BAD_LENGTH).
+ */
+PA_API pa_status pa_share_pages(const pa_cache_desc* desc, int32_t batch, const int32_t* parents,
+                                const int32_t* num_shared_pages, int32_t* block_tables, int32_t max_pages_per_seq,
+                                int32_t* ref_counts, pa_stream_t stream);
+
+/*
+ * pa_release_pages -- hand back entries first_pages[b] .. end_pages[b]-1 of each
+ * row (nano-vLLM learning note, BlockManager.deallocate listing): they become
+ * -1, and a page that no row holds any longer goes into the ring, rows in order,
+ * each from its last entry down (a page handed back by several entries at the
+ * place of the last of them).  Entries that are -1 already are passed over.
+ *
+ *   first_pages, end_pages  int32 [batch], 0 <= first, end <= max_pages_per_seq;
+ *                    end <= first: none.  Rows out of these bounds are skipped
+ *                    (PA_DEVERR_BAD_LENGTH).
+ * A page that nobody held is flagged (PA_DEVERR_BAD_PAGE) and not put into the
+ * ring.  Up to 32768 rows and 2^30 table entries (else PA_ERR_UNSUPPORTED).
+ */
+PA_API pa_status pa_release_pages(const pa_cache_desc* desc, int32_t batch, const int32_t* first_pages,
+                                  const int32_t* end_pages, int32_t* block_tables, int32_t max_pages_per_seq,
+                                  int32_t* ref_counts, int32_t* free_pages, const int64_t* pool_state,
+                                  int64_t* pool_state_out, pa_stream_t stream);
+
+/* pa_release_pages of the pages that a sliding window with sinks has left: those
+ * whose tokens no token from position context_lens[b] on sees.  Entries behind
+ * them stay where they are, so that positions still find their pages. */
+PA_API pa_status pa_release_window_pages(const pa_cache_desc* desc, int32_t window, int32_t num_sinks, int32_t batch,
+                                         const int32_t* context_lens, int32_t* block_tables,
+                                         int32_t max_pages_per_seq, int32_t* ref_counts, int32_t* free_pages,
+                                         const int64_t* pool_state, int64_t* pool_state_out, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * A cache held in 4 bits.  The calls below stand beside their namesakes above:

@@ -36,6 +36,7 @@ PA_DEVERR_BAD_SLOT = 0x1
 PA_DEVERR_BAD_PAGE = 0x2
 PA_DEVERR_BAD_LENGTH = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_NO_PAGES = 0x10
 
 
 class PagedAttnError(RuntimeError):
@@ -114,6 +115,10 @@ _SIGS = {
     "pa_decode_shared_prefix_workspace_size": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _I32, _I32]),
     "pa_decode_shared_prefix": (_I32, [_DESC, _I32, _VP, _VP, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _VP, _I32, _F32,
                                        _I32, _VP, _VP, ctypes.c_size_t, _VP]),
+    "pa_extend_tables": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "pa_share_pages": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _VP, _VP]),
+    "pa_release_pages": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
+    "pa_release_window_pages": (_I32, [_DESC, _I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
     "pa_validate_metadata": (_I32, [_DESC, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP]),
     "pa_selftest_bounded_wait": (_I32, [_I32, _VP]),
     "pa_read_device_errors": (_I32, [ctypes.POINTER(ctypes.c_uint32), _I32]),
@@ -493,6 +498,35 @@ def pa_decode_shared_prefix(desc, num_groups, cu_groups, prefix_lens, max_prefix
         desc, num_groups, _at(cu_groups), _at(prefix_lens), max_prefix_len, _at(q), batch, _at(k_cache),
         _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
         _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+
+
+def pa_extend_tables(desc, batch, new_tokens, context_lens, block_tables, max_pages_per_seq, free_pages, pool_state,
+                     max_tokens, cu_seqlens_q, context_lens_out, positions, slot_mapping, ref_counts, pool_state_out,
+                     stream=None):
+    _check("pa_extend_tables", load_library().pa_extend_tables(
+        desc, batch, _at(new_tokens), _at(context_lens), _at(block_tables), max_pages_per_seq, _at(free_pages),
+        _at(pool_state), max_tokens, _at(cu_seqlens_q), _at(context_lens_out), _at(positions), _at(slot_mapping),
+        _at(ref_counts), _at(pool_state_out), _stream(stream)))
+
+
+def pa_share_pages(desc, batch, parents, num_shared_pages, block_tables, max_pages_per_seq, ref_counts, stream=None):
+    _check("pa_share_pages", load_library().pa_share_pages(
+        desc, batch, _at(parents), _at(num_shared_pages), _at(block_tables), max_pages_per_seq, _at(ref_counts),
+        _stream(stream)))
+
+
+def pa_release_pages(desc, batch, first_pages, end_pages, block_tables, max_pages_per_seq, ref_counts, free_pages,
+                     pool_state, pool_state_out, stream=None):
+    _check("pa_release_pages", load_library().pa_release_pages(
+        desc, batch, _at(first_pages), _at(end_pages), _at(block_tables), max_pages_per_seq, _at(ref_counts),
+        _at(free_pages), _at(pool_state), _at(pool_state_out), _stream(stream)))
+
+
+def pa_release_window_pages(desc, window, num_sinks, batch, context_lens, block_tables, max_pages_per_seq, ref_counts,
+                            free_pages, pool_state, pool_state_out, stream=None):
+    _check("pa_release_window_pages", load_library().pa_release_window_pages(
+        desc, window, num_sinks, batch, _at(context_lens), _at(block_tables), max_pages_per_seq, _at(ref_counts),
+        _at(free_pages), _at(pool_state), _at(pool_state_out), _stream(stream)))
 
 
 def pa_validate_metadata(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq,

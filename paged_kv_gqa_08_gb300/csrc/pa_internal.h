@@ -327,6 +327,49 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
 cudaError_t launch_prefix_tc(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// block tables
+// ---------------------------------------------------------------------------
+struct ExtendParams {
+  const int32_t* new_tokens;
+  const int32_t* ctx;
+  int32_t* bt;
+  const int32_t* ring;
+  const int64_t* pool;
+  int32_t* cu;
+  int32_t* ctx_out;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* refs;
+  int64_t* pool_out;
+  unsigned int* err;
+  int64_t num_pages, max_tokens;
+  int32_t batch, maxp, log2P;
+};
+struct ShareParams {
+  const int32_t* parents;
+  const int32_t* num_pages_shared;
+  int32_t* bt;
+  int32_t* refs;
+  unsigned int* err;
+  int64_t num_pages;
+  int32_t batch, maxp;
+};
+struct ReleaseParams {
+  const int32_t* first;
+  const int32_t* end;
+  const int32_t* ctx;  // or: the pages that no token from position ctx[b] on sees
+  int32_t window, sinks;
+  int32_t* bt;
+  int32_t* refs;
+  int32_t* ring;
+  const int64_t* pool;
+  int64_t* pool_out;
+  unsigned int* err;
+  int64_t num_pages;
+  int32_t batch, maxp, log2P;
+};
+
+// ---------------------------------------------------------------------------
 // metadata validation
 // ---------------------------------------------------------------------------
 struct ValidateArgs {
