@@ -375,6 +375,8 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
   // With groups the grid starts beside the kernel over their prefixes, whose
   // output only the merge reads: each CTA's last act is to wait for it.
   const bool beside = kRange && p.cu_groups != nullptr;
+  if (beside && p.inline_plan && c == 0)  // the sums, for that merge
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) p.cs[b] = cs[b];
   if (x0 >= x1) {
     if (beside) pdl_wait();
     return;

@@ -41,10 +41,12 @@ namespace {
 // request: the CTAs that had tiles of its unit of the prefix, then the CTAs that
 // had chunks of its own keys.  merge_w warps per (request, q-head), each with a
 // run of the parts, as decode_merge_kernel.  Which parts there are follows from
-// the lengths and is worked out while the grid before still runs.
+// the sums that the CTAs 0 of both grids leave: with every warp working them out
+// from the lengths, a batch of 128 requests spent 40 us here.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads)
-    shared_merge_kernel(const KParams p, const PrefixShape s, const float* o_pre, const float* lse_pre, int max_ctas) {
+    shared_merge_kernel(const KParams p, const PrefixShape s, const int64_t* costs, const float* o_pre,
+                        const float* lse_pre, int max_ctas) {
   constexpr int EL = HD / 32;
   constexpr int NWARP = kMergeThreads / 32;
   __shared__ float red[NWARP][32][EL + 1];
@@ -55,71 +57,37 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int b = active ? static_cast<int>(u / p.Hq) : 0;
   const int hq = active ? static_cast<int>(u - static_cast<int64_t>(b) * p.Hq) : 0;
   const int G = p.Hq / p.Hkv, h = hq / G;
-
-  // the prefix's parts: CTAs f0 .. f0 + np - 1 of ctas
   const int g = group_of(s.cu, s.n_groups, b);
-  int64_t total = 0, base = 0;
-  for (int i = lane; i < s.n_groups; i += 32) {
-    const int64_t cost = prefix_group(s, i).cost;
-    total += cost;
-    base += i < g ? cost : 0;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    base += __shfl_xor_sync(0xffffffffu, base, o);
-  }
-  const int ctas = prefix_ctas(s, total, max_ctas);
-  int f0 = 0, np = 0;
   PrefixGroup gr{};
-  PrefixUnit unit{};
   if (active && g >= 0) gr = prefix_group(s, g);
+  {
+    const int L = p.ctx[b];
+    const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
+    active = active && L >= 1 && L <= cap && hole_of(p, b, L).hi >= 0;  // its lengths are consistent
+  }
+  pdl_wait();  // the parts and sums of both grids are written
+  const int NC = p.cs[p.B], cb0 = p.cs[b], cb1 = p.cs[b + 1];
+  const int64_t total = costs[s.n_groups];
+  // the prefix's parts: np CTAs from f0 on
+  int f0 = 0, np = 0;
   if (gr.cost > 0) {
-    unit = prefix_unit(s, gr, base, h, (b - gr.s0) / s.TQ / 2);
+    const int ctas = prefix_ctas(s, total, max_ctas);
+    const PrefixUnit unit = prefix_unit(s, gr, costs[g], h, (b - gr.s0) / s.TQ / 2);
     f0 = prefix_cta_of(unit.start, total, ctas);
     np = prefix_cta_of(unit.start + static_cast<int64_t>(gr.nt - 1) * unit.cost, total, ctas) - f0 + 1;
   }
-  // the request's own: CTAs c0 .. c0 + ns - 1 of p.n_ctas
-  int NC = 0, cb0 = 0, cb1 = 0;
-  bool ok = false;  // its lengths are consistent
-  const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
-  if (active) {
-    const int L = p.ctx[b];
-    ok = L >= 1 && L <= cap && hole_of(p, b, L).hi >= 0;
-  }
-  if (p.inline_plan) {
-    int below = 0;
-    for (int i = lane; i < p.B; i += 32) {
-      bool bad;
-      const int n = chunks_of<true>(p, i, cap, &bad);
-      NC += n;
-      below += i < b ? n : 0;
-      cb1 += i <= b ? n : 0;
-    }
-    NC = __reduce_add_sync(0xffffffffu, NC);
-    cb0 = __reduce_add_sync(0xffffffffu, below);
-    cb1 = __reduce_add_sync(0xffffffffu, cb1);
-    pdl_wait();  // the parts of both grids are written
-  } else {
-    pdl_wait();
-    NC = p.cs[p.B];
-    cb0 = p.cs[b];
-    cb1 = p.cs[b + 1];
-  }
+  // the request's own: ns CTAs from c0 on
   int c0 = 0, ns = 0;
   if (cb1 > cb0) {
     c0 = static_cast<int>(((static_cast<int64_t>(cb0) + 1) * p.n_ctas + NC - 1) / NC) - 1;
     ns = static_cast<int>((static_cast<int64_t>(cb1) * p.n_ctas + NC - 1) / NC) - c0;
   }
   // without a prefix a single CTA's result is the output already
-  active = active && ok && (np > 0 || ns > 1);
+  active = active && (np > 0 || ns > 1);
   const int parts = np + ns;
-  // a CTA between the ends may have had no tile (no chunk) and left no part
+  // with more CTAs than chunks, a CTA between the ends may have had none and left no part
   auto has = [&](int k) {
-    if (k < np) {
-      const int64_t c = f0 + k;
-      return prefix_tile_at(unit, gr.nt, total * c / ctas) < prefix_tile_at(unit, gr.nt, total * (c + 1) / ctas);
-    }
+    if (k < np || NC >= p.n_ctas) return true;
     const int64_t c = c0 + k - np;
     return c * NC / p.n_ctas < (c + 1) * NC / p.n_ctas;
   };
@@ -153,20 +121,25 @@ __global__ void __launch_bounds__(kMergeThreads)
       }
     };
     load(k_begin);
-    float M = -INFINITY;
-    for (int k = lane; k < parts; k += 32)
+    // the first 32 parts' log-sum-exps stay in the lanes
+    const float lse_mine = lane < parts && has(lane) ? lse_of(lane) : -INFINITY;
+    float M = lse_mine;
+    for (int k = lane + 32; k < parts; k += 32)
       if (has(k)) M = fmaxf(M, lse_of(k));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M != -INFINITY) {
+      const float w_first = exp2f(lse_mine - M);
       for (int k0 = k_begin; k0 < k_end; k0 += 8) {
         if (k0 != k_begin) load(k0);
         const int k = k0 + lane;
-        const float w_mine = lane < 8 && k < k_end && has(k) ? exp2f(lse_of(k) - M) : 0.f;
+        float w_mine = 0.f;
+        if (parts > 32 && lane < 8 && k < k_end && has(k)) w_mine = exp2f(lse_of(k) - M);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float w = __shfl_sync(0xffffffffu, w_mine, i);
-          if (w != 0.f) {  // (an idle CTA wrote no part)
+          const float w = parts > 32 ? __shfl_sync(0xffffffffu, w_mine, i)
+                                     : __shfl_sync(0xffffffffu, w_first, (k0 + i) & 31);
+          if (k0 + i < k_end && w != 0.f) {  // (an idle CTA wrote no part)
 #pragma unroll
             for (int e = 0; e < EL; ++e) acc[e] += w * v[i][e];
             wsum += w;
@@ -212,6 +185,7 @@ struct PrefixSimtParams {
   float* o_part;
   float* lse_part;
   unsigned int* err;
+  int64_t* costs;
   PrefixShape shape;
   int64_t num_pages;
   int32_t Hq, G, maxp, log2P;
@@ -243,7 +217,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const PrefixS
   const int64_t row_bytes = static_cast<int64_t>(p.shape.Hkv) * HD * E;
   pdl_trigger();  // the decode kernel over the requests' own keys may start
   PrefixShare share;
-  if (warp == 0) share = prefix_share(p.shape, blockIdx.x, gridDim.x);
+  if (warp == 0) share = prefix_share(p.shape, blockIdx.x, gridDim.x, p.costs);
   for (;;) {
     if (tid == 0) {
       PrefixWork w;
@@ -419,6 +393,7 @@ cudaError_t launch_prefix_simt(const pa_cache_desc& d, const SharedArgs& a, cons
   p.lse_part = reinterpret_cast<float*>(ws + pl.off_lse);
   p.err = a.err;
   p.shape = prefix_shape(d, a, pl);
+  p.costs = reinterpret_cast<int64_t*>(ws + pl.off_costs);
   p.num_pages = d.num_pages;
   p.Hq = d.num_q_heads;
   p.G = d.num_q_heads / d.num_kv_heads;
@@ -468,7 +443,8 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
     if (rows >= int64_t(1) << 31) return cudaErrorInvalidValue;
     // TMA coordinates are 32-bit: the cache rows must be addressable
     if (tc && d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    pl.off_lse = pl.ws_bytes;
+    pl.off_costs = pl.ws_bytes;
+    pl.off_lse = align_up(pl.off_costs + (static_cast<size_t>(n_groups) + 1) * 8, 256);
     pl.off_o = align_up(pl.off_lse + static_cast<size_t>(rows) * 4, 256);
     pl.ws_bytes = align_up(pl.off_o + static_cast<size_t>(rows) * d.head_dim * 4, 256);
   }
@@ -519,15 +495,18 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   // plan kernel's sums, which it waits for), and waits for it before it ends.
   e = launch_after_previous(f.main, dim3(pl.suffix.n_ctas), dim3(threads), pl.suffix.smem_bytes, s, args);
   if (e != cudaSuccess) return e;
-  // warps per (request, q-head): about one per 8 parts of a request when all are equally long
-  const int per_req = (pl.suffix.n_ctas + pl.prefix_ctas) / std::max(1, std::min(p.B, d.num_kv_heads));
-  p.merge_w = per_req >= 32 ? 4 : per_req >= 16 ? 2 : 1;
+  // warps per (request, q-head): about one per 8 parts (the CTAs of a kv-head's
+  // one group, and of a request when all are equally long), where there are few
+  const int parts = pl.prefix_ctas / d.num_kv_heads + pl.suffix.n_ctas / std::max(1, p.B);
+  const bool few = static_cast<int64_t>(p.B) * p.Hq < 2048;
+  p.merge_w = few && parts >= 24 ? 4 : few && parts >= 12 ? 2 : 1;
   PrefixShape shape = prefix_shape(d, a, pl);
   char* ws = static_cast<char*>(a.workspace);
+  const int64_t* costs = reinterpret_cast<const int64_t*>(ws + pl.off_costs);
   const float* o_pre = reinterpret_cast<const float*>(ws + pl.off_o);
   const float* lse_pre = reinterpret_cast<const float*>(ws + pl.off_lse);
   int max_ctas = pl.prefix_ctas;
-  void* margs[] = {&p, &shape, &o_pre, &lse_pre, &max_ctas};
+  void* margs[] = {&p, &shape, &costs, &o_pre, &lse_pre, &max_ctas};
   const int64_t items = static_cast<int64_t>(p.B) * p.Hq;
   const int per_cta = kMergeThreads / 32 / p.merge_w;
   const void* merge =

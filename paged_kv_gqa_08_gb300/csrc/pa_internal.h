@@ -317,7 +317,7 @@ struct PrefixShape {
 struct SharedPlan {
   DecodePlan suffix;  // the requests' own keys
   int32_t prefix_ctas = 0, TQ = 0, cost_pair = 0, cost_one = 0;
-  size_t off_lse = 0, off_o = 0, ws_bytes = 0;  // the suffix's workspace comes first
+  size_t off_costs = 0, off_lse = 0, off_o = 0, ws_bytes = 0;  // the suffix's workspace comes first
 };
 PrefixShape prefix_shape(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl);
 cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max_prefix, int max_context_len,

@@ -145,6 +145,7 @@ struct TcParams {
   float* lse_part;  // [slot][Hkv][2 q-tiles][128 rows]
   int32_t window, sinks;  // kWindow
   PrefixShape prefix;     // kPrefix: the groups, whose parts' rows are laid out as prefix_plan.cuh says
+  int64_t* prefix_costs;  // kPrefix: where each group starts on the line, for the merge
 };
 
 // ---------------------------------------------------------------------------
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     // listed longest first).  Otherwise the CTA's own pair is its one item.
     // A shared prefix: the CTA's share of the groups' key tiles, unit by unit.
     PrefixShare share;
-    if constexpr (kMode == kPrefix) share = prefix_share(p.prefix, blockIdx.x, gridDim.x);
+    if constexpr (kMode == kPrefix) share = prefix_share(p.prefix, blockIdx.x, gridDim.x, p.prefix_costs);
     if (lane == 0) {
       if (p.units) pdl_wait();  // the planner's unit list and counter are ready
       const int total = p.units ? *p.n_units * p.Hkv : 1;
@@ -2081,6 +2082,7 @@ cudaError_t launch_prefix_tc(const pa_cache_desc& d, const SharedArgs& a, const 
   p.max_ctx = a.max_context_len;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.prefix = prefix_shape(d, a, pl);
+  p.prefix_costs = reinterpret_cast<int64_t*>(ws + pl.off_costs);
   p.lse_part = reinterpret_cast<float*>(ws + pl.off_lse);
   p.o_part = reinterpret_cast<float*>(ws + pl.off_o);
   if ((e = prepare_kernels<kPrefix>()) != cudaSuccess) return e;

@@ -58,7 +58,8 @@ PA_DEVINL PrefixGroup prefix_group(const PrefixShape& s, int g) {
   return r;
 }
 
-// CTAs that take a share of a line of this length: as many as get two tiles each.
+// CTAs that take a share of a line of this length: as many as get two tiles
+// each, so that every CTA between the ends of a unit has a tile of it.
 PA_DEVINL int prefix_ctas(const PrefixShape& s, int64_t total, int max_ctas) {
   return static_cast<int>(min(static_cast<int64_t>(max_ctas), max(total / (2 * s.cost_one), int64_t(1))));
 }
@@ -74,8 +75,9 @@ struct PrefixShare {
   int g;
 };
 
-// CTA c's share, found by one warp (all lanes).
-PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas) {
+// CTA c's share, found by one warp (all lanes); CTA 0 also writes where each
+// group starts, and the line's length, to costs[0 .. n_groups] for the merge.
+PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, int64_t* costs) {
   const int lane = threadIdx.x & 31;
   int64_t total = 0;
   for (int g = lane; g < s.n_groups; g += 32) total += prefix_group(s, g).cost;
@@ -98,15 +100,17 @@ PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas) {
       if (lane >= o) incl += y;
     }
     incl += carry;
+    if (c == 0 && g < s.n_groups) costs[g] = incl - cost;
     const unsigned past = __ballot_sync(0xffffffffu, incl > r.x);
-    if (past) {
+    if (past && r.g == s.n_groups) {
       const int first = __ffs(past) - 1;
       r.g = g0 + first;
       r.base = __shfl_sync(0xffffffffu, incl - cost, first);
-      break;
+      if (c != 0) break;
     }
     carry = __shfl_sync(0xffffffffu, incl, 31);
   }
+  if (c == 0 && lane == 0) costs[s.n_groups] = total;
   return r;
 }
 
