@@ -447,6 +447,11 @@ def pa_decode_kv_write_q4(desc, group_size, q, k_new, k_row_stride, v_new, v_row
         max_context_len, scale, max_ctas, slots, out, ws, workspace_bytes, st))
 
 
+def _addresses(*tensors):
+    """The addresses of ``tensors``: the calls are short, so the usual case takes the fewest steps."""
+    return [t.data_ptr() if t.__class__ is _Tensor else _at(t) for t in tensors]
+
+
 def _bytes_of(workspace, workspace_bytes):
     if workspace_bytes is None:
         return workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -461,28 +466,30 @@ def pa_decode_window_workspace_size(desc, window, num_sinks, batch, max_context_
 def pa_decode_window(desc, window, num_sinks, q, batch, k_cache, v_cache, block_tables, max_pages_per_seq,
                      context_lens, max_context_len, scale, max_ctas, out, workspace, workspace_bytes=None,
                      stream=None):
+    q, kc, vc, bt, ctx, o, ws = _addresses(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
     _check("pa_decode_window", load_library().pa_decode_window(
-        desc, window, num_sinks, _at(q), batch, _at(k_cache), _at(v_cache), _at(block_tables), max_pages_per_seq,
-        _at(context_lens), max_context_len, scale, max_ctas, _at(out), _at(workspace),
+        desc, window, num_sinks, q, batch, kc, vc, bt, max_pages_per_seq, ctx, max_context_len, scale, max_ctas, o, ws,
         _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_decode_kv_write_window(desc, window, num_sinks, q, k_new, k_row_stride, v_new, v_row_stride, batch, k_cache,
                               v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas,
                               slot_mapping, out, workspace, workspace_bytes=None, stream=None):
+    q, k, v, kc, vc, bt, ctx, slots, o, ws = _addresses(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens,
+                                                        slot_mapping, out, workspace)
     _check("pa_decode_kv_write_window", load_library().pa_decode_kv_write_window(
-        desc, window, num_sinks, _at(q), _at(k_new), k_row_stride, _at(v_new), v_row_stride, batch, _at(k_cache),
-        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
-        _at(slot_mapping), _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+        desc, window, num_sinks, q, k, k_row_stride, v, v_row_stride, batch, kc, vc, bt, max_pages_per_seq, ctx,
+        max_context_len, scale, max_ctas, slots, o, ws, _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_prefill_varlen_window(desc, window, num_sinks, q, cu_seqlens_q, batch, max_seqlen_q, num_tokens, k_cache,
                              v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len, scale, out,
                              workspace=None, workspace_bytes=None, stream=None):
+    q, cu, kc, vc, bt, ctx, o, ws = _addresses(q, cu_seqlens_q, k_cache, v_cache, block_tables, context_lens, out,
+                                               workspace)
     _check("pa_prefill_varlen_window", load_library().pa_prefill_varlen_window(
-        desc, window, num_sinks, _at(q), _at(cu_seqlens_q), batch, max_seqlen_q, num_tokens, _at(k_cache),
-        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, _at(out),
-        _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+        desc, window, num_sinks, q, cu, batch, max_seqlen_q, num_tokens, kc, vc, bt, max_pages_per_seq, ctx,
+        max_context_len, scale, o, ws, _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_decode_shared_prefix_workspace_size(desc, num_groups, batch, max_prefix_len, max_context_len,
@@ -494,19 +501,22 @@ def pa_decode_shared_prefix_workspace_size(desc, num_groups, batch, max_prefix_l
 def pa_decode_shared_prefix(desc, num_groups, cu_groups, prefix_lens, max_prefix_len, q, batch, k_cache, v_cache,
                             block_tables, max_pages_per_seq, context_lens, max_context_len, scale, max_ctas, out,
                             workspace, workspace_bytes=None, stream=None):
+    cu, pre, q, kc, vc, bt, ctx, o, ws = _addresses(cu_groups, prefix_lens, q, k_cache, v_cache, block_tables,
+                                                    context_lens, out, workspace)
     _check("pa_decode_shared_prefix", load_library().pa_decode_shared_prefix(
-        desc, num_groups, _at(cu_groups), _at(prefix_lens), max_prefix_len, _at(q), batch, _at(k_cache),
-        _at(v_cache), _at(block_tables), max_pages_per_seq, _at(context_lens), max_context_len, scale, max_ctas,
-        _at(out), _at(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream)))
+        desc, num_groups, cu, pre, max_prefix_len, q, batch, kc, vc, bt, max_pages_per_seq, ctx, max_context_len, scale,
+        max_ctas, o, ws, _bytes_of(workspace, workspace_bytes), _stream(stream)))
 
 
 def pa_extend_tables(desc, batch, new_tokens, context_lens, block_tables, max_pages_per_seq, free_pages, pool_state,
                      max_tokens, cu_seqlens_q, context_lens_out, positions, slot_mapping, ref_counts, pool_state_out,
                      stream=None):
+    new, ctx, bt, ring, pool, cu, ctx_out, pos, slots, refs, pool_out = _addresses(
+        new_tokens, context_lens, block_tables, free_pages, pool_state, cu_seqlens_q, context_lens_out, positions,
+        slot_mapping, ref_counts, pool_state_out)
     _check("pa_extend_tables", load_library().pa_extend_tables(
-        desc, batch, _at(new_tokens), _at(context_lens), _at(block_tables), max_pages_per_seq, _at(free_pages),
-        _at(pool_state), max_tokens, _at(cu_seqlens_q), _at(context_lens_out), _at(positions), _at(slot_mapping),
-        _at(ref_counts), _at(pool_state_out), _stream(stream)))
+        desc, batch, new, ctx, bt, max_pages_per_seq, ring, pool, max_tokens, cu, ctx_out, pos, slots, refs, pool_out,
+        _stream(stream)))
 
 
 def pa_share_pages(desc, batch, parents, num_shared_pages, block_tables, max_pages_per_seq, ref_counts, stream=None):
@@ -517,9 +527,10 @@ def pa_share_pages(desc, batch, parents, num_shared_pages, block_tables, max_pag
 
 def pa_release_pages(desc, batch, first_pages, end_pages, block_tables, max_pages_per_seq, ref_counts, free_pages,
                      pool_state, pool_state_out, stream=None):
+    first, end, bt, refs, ring, pool, pool_out = _addresses(first_pages, end_pages, block_tables, ref_counts, free_pages,
+                                                            pool_state, pool_state_out)
     _check("pa_release_pages", load_library().pa_release_pages(
-        desc, batch, _at(first_pages), _at(end_pages), _at(block_tables), max_pages_per_seq, _at(ref_counts),
-        _at(free_pages), _at(pool_state), _at(pool_state_out), _stream(stream)))
+        desc, batch, first, end, bt, max_pages_per_seq, refs, ring, pool, pool_out, _stream(stream)))
 
 
 def pa_release_window_pages(desc, window, num_sinks, batch, context_lens, block_tables, max_pages_per_seq, ref_counts,

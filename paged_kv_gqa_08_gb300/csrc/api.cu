@@ -303,7 +303,8 @@ pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* 
 }
 
 cudaError_t launch_prefill(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
-  return d.dtype == PA_BF16 && d.head_dim == 128 ? launch_prefill_tc(d, a, s) : launch_prefill_simt(d, a, s);
+  if (d.dtype == PA_BF16 && d.head_dim == 128) return launch_prefill_tc(d, a, s);
+  return a.window > 0 ? launch_prefill_window_tile(d, a, s) : launch_prefill_simt(d, a, s);
 }
 
 }  // namespace pa

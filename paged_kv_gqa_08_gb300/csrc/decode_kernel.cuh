@@ -359,8 +359,23 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
   const int NW = p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int32_t* cs;  // [B+1] chunk prefix sums
-  if (p.inline_plan) {
+  const int32_t* cs;  // [B+1] chunk prefix sums (of the CTA's own request: [2])
+  const int cs0 = kRange && p.per_request ? c : 0;  // the request that they start with
+  if (kRange && p.per_request) {
+    int32_t* cs_s = reinterpret_cast<int32_t*>(smem + p.off_cs);
+    const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
+    bool bad;
+    const int n = chunks_of<kRange>(p, c, cap, &bad);
+    if (threadIdx.x == 0) {
+      if (bad) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
+      if (n == 0 && p.k_new != nullptr && p.slot_out) p.slot_out[c] = -1;
+      cs_s[0] = 0;
+      cs_s[1] = n;
+    }
+    if (n == 0) return;
+    cta_sync();
+    cs = cs_s;
+  } else if (p.inline_plan) {
     int32_t* cs_s = reinterpret_cast<int32_t*>(smem + p.off_cs);
     plan_in_cta<kRange>(p, cs_s, cs_s + kInlinePlanMax + 1, c == 0);
     cs = cs_s;
@@ -369,9 +384,11 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
     cs = p.cs;
   }
   pdl_trigger();  // the merge kernel may start launching; it waits for this grid
-  const int NC = cs[p.B];
-  const int x0 = static_cast<int>((static_cast<int64_t>(c) * NC) / p.n_ctas);
-  const int x1 = static_cast<int>((static_cast<int64_t>(c + 1) * NC) / p.n_ctas);
+  const bool alone = kRange && p.per_request;
+  const int NC = cs[alone ? 1 : p.B];
+  const int n_ctas = alone ? 1 : sharing_ctas<kRange>(p, NC), share = alone ? 0 : kRange ? min(c, n_ctas) : c;
+  const int x0 = static_cast<int>((static_cast<int64_t>(share) * NC) / n_ctas);
+  const int x1 = kRange && share == n_ctas ? x0 : static_cast<int>((static_cast<int64_t>(share + 1) * NC) / n_ctas);
   // With groups the grid starts beside the kernel over their prefixes, whose
   // output only the merge reads: each CTA's last act is to wait for it.
   const bool beside = kRange && p.cu_groups != nullptr;
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
     // ------------------------------ producer ------------------------------
     const uint64_t pol = l2_policy_evict_first();
     const int tok = 1 << p.log2T;
-    int b = p.inline_plan ? first_request(cs, p.B, x0) : p.cta_seq[c];
+    int b = kRange && p.per_request ? c : p.inline_plan ? first_request(cs, p.B, x0) : p.cta_seq[c];
     int issued = 0;
     bool aborted = false;
     for (int xg = x0; xg < x1 && !aborted; xg += 32) {
@@ -411,8 +428,8 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
       int my_b = b, n = 0, flags = 0, new_slot = -1;
       long long off = 0;
       if (lane < nvalid) {
-        while (my_b < p.B - 1 && cs[my_b + 1] <= x) ++my_b;
-        const int cb0 = cs[my_b], cb1 = cs[my_b + 1];
+        while (my_b < p.B - 1 && cs[my_b - cs0 + 1] <= x) ++my_b;
+        const int cb0 = cs[my_b - cs0], cb1 = cs[my_b - cs0 + 1];
         const int jc = x - cb0;
         const int L = p.ctx[my_b];
         int t0 = jc << p.log2T;
@@ -803,7 +820,8 @@ cudaError_t plan_decode_keys(const pa_cache_desc& d, int batch, int max_keys, in
   const int64_t chunks_upper =
       static_cast<int64_t>(batch) *
       ((static_cast<int64_t>(max_keys) + pl.tokens_per_chunk - 1) / pl.tokens_per_chunk + extra_chunks);
-  int64_t n = static_cast<int64_t>(occ) * di.sm_count;
+  pl.slots = occ * di.sm_count;
+  int64_t n = pl.slots;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);
   n = std::min<int64_t>(n, std::max<int64_t>(1, chunks_upper));
   pl.n_ctas = static_cast<int>(std::max<int64_t>(1, n));

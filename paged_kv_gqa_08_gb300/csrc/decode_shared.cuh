@@ -58,6 +58,7 @@ struct KParams {
   const int32_t* cu_groups;
   const int32_t* prefix_lens;
   int32_t n_groups, max_prefix;
+  int32_t per_request;  // a CTA for each request, whole (no merge)
 };
 
 // Keys [lo, hi) of a request that a kRange kernel leaves out; hi = -1 when the
@@ -91,6 +92,14 @@ PA_DEVINL int chunks_before_hole(Hole h, int log2T) { return (h.lo + (1 << log2T
 PA_DEVINL int chunks_in_hole(Hole h, int L, int log2T) {
   const int end = h.hi >= L ? (L + (1 << log2T) - 1) >> log2T : h.hi >> log2T;
   return max(0, end - chunks_before_hole(h, log2T));
+}
+
+// CTAs that share NC chunks.  The kRange kernels leave CTAs without one idle
+// behind the others, so that few chunks are at work on the SMs that the kernel
+// before frees first, and no CTA between two others is without a part.
+template <bool kRange>
+PA_DEVINL int sharing_ctas(const KParams& p, int NC) {
+  return kRange ? min(p.n_ctas, max(NC, 1)) : p.n_ctas;
 }
 
 // Chunks of request b, or 0 with *bad set when its lengths are inconsistent
@@ -166,9 +175,9 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const KParams
   }
   if (tid == 0) p.cs[0] = 0;
   cta_sync();
-  const int NC = carry;
-  for (int c = tid; c < p.n_ctas; c += kPlanThreads)
-    p.cta_seq[c] = first_request(p.cs, p.B, (static_cast<int64_t>(c) * NC) / p.n_ctas);
+  const int NC = carry, n_ctas = sharing_ctas<kRange>(p, NC);
+  for (int c = tid; c < n_ctas; c += kPlanThreads)
+    p.cta_seq[c] = first_request(p.cs, p.B, (static_cast<int64_t>(c) * NC) / n_ctas);
 }
 
 // The plan kernel's prefix sums, computed by every thread of a decode CTA into
@@ -283,17 +292,18 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
     cb1 = p.cs[b + 1];
   }
   if (cb1 <= cb0) active = false;
+  const int n_ctas = sharing_ctas<kRange>(p, NC);
   if (active) {
-    c0 = static_cast<int>(((static_cast<int64_t>(cb0) + 1) * p.n_ctas + NC - 1) / NC) - 1;
-    const int c1 = static_cast<int>(((static_cast<int64_t>(cb1)) * p.n_ctas + NC - 1) / NC) - 1;
+    c0 = static_cast<int>(((static_cast<int64_t>(cb0) + 1) * n_ctas + NC - 1) / NC) - 1;
+    const int c1 = static_cast<int>(((static_cast<int64_t>(cb1)) * n_ctas + NC - 1) / NC) - 1;
     parts = c1 - c0 + 1;
     active = c0 != c1;  // one CTA wrote the request whole
   }
   // With more CTAs than chunks some CTAs between c0 and c1 own no chunk and
   // wrote no partial: only CTAs with a non-empty range take part.  With at
   // least as many chunks as CTAs every CTA has a range.
-  const bool all_busy = NC >= p.n_ctas;
-  auto start = [&](int c) { return (static_cast<int64_t>(c) * NC) / p.n_ctas; };
+  const bool all_busy = NC >= n_ctas;
+  auto start = [&](int c) { return (static_cast<int64_t>(c) * NC) / n_ctas; };
   auto busy = [&](int cc) { return all_busy || start(cc) < start(cc + 1); };
   auto lse_of = [&](int k) { return p.lse_part[(static_cast<int64_t>(c0 + k) + b) * p.Hq + hq]; };
   float acc[EL];
@@ -506,7 +516,8 @@ inline KParams decode_params(const pa_cache_desc& d, const DecodePlan& pl, const
   p.off_ml = pl.off_ml;
   p.off_abort = pl.off_abort;
   p.off_cs = pl.off_cs;
-  p.inline_plan = a.batch <= kInlinePlanMax ? 1 : 0;
+  p.per_request = pl.per_request ? 1 : 0;
+  p.inline_plan = a.batch <= kInlinePlanMax || pl.per_request ? 1 : 0;
   p.p_row = pl.p_row;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.k_new = static_cast<const char*>(a.k_new);
@@ -536,7 +547,7 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
     cfg.numAttrs = 1;
     e = cudaLaunchKernelExC(&cfg, main_fn, main_args);
   } else if (p.inline_plan) {
-    e = cudaLaunchKernel(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), main_args, pl.smem_bytes, s);
+    e = cudaLaunchKernel(main_fn, dim3(pl.per_request ? p.B : pl.n_ctas), dim3((pl.nw + 1) * 32), main_args, pl.smem_bytes, s);
   } else {
     decode_plan_kernel<kRange><<<1, kPlanThreads, 0, s>>>(p);
     e = cudaGetLastError();
@@ -544,7 +555,7 @@ inline cudaError_t launch_decode_kernels(const void* main_fn, const void* merge_
     e = launch_after_previous(main_fn, dim3(pl.n_ctas), dim3((pl.nw + 1) * 32), pl.smem_bytes, s, main_args);
   }
   if (e != cudaSuccess) return e;
-  if (pl.n_ctas > 1 && pl.cluster == 0) {
+  if (pl.n_ctas > 1 && pl.cluster == 0 && !pl.per_request) {
     // warps per (request, q-head): about one per 8 partials of a request when
     // the requests are equally long (CTAs per request / 8), at most 4
     const int per_req = pl.n_ctas / std::max(1, p.B);

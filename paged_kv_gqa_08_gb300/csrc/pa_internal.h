@@ -174,6 +174,8 @@ struct DecodePlan {
   int row_pitch = 0;     // shared-memory bytes per token row of a chunk
   int stages = 0;
   int n_ctas = 0;        // partitions of the key space
+  int slots = 0;         // CTAs that fit the GPU at once
+  bool per_request = false;  // a window: a CTA for each request, whole
   int cluster = 0;       // 4-bit caches: CTAs of each request, a cluster (0: CTAs share the batch's keys evenly)
   size_t smem_bytes = 0;
   // workspace layout (byte offsets)
@@ -284,6 +286,8 @@ pa_status prefill_args(const pa_cache_desc* desc, const void* q, const int32_t* 
 cudaError_t launch_prefill(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
 // CUDA-core kernel (any supported dtype / head_dim).
 cudaError_t launch_prefill_simt(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
+// Over a window, for the types that the latter kernel does not take.
+cudaError_t launch_prefill_window_tile(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
 // tcgen05 tensor-core kernel (bf16, head_dim 128).
 cudaError_t launch_prefill_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s);
 
@@ -325,6 +329,10 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
 cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const SharedArgs& a, cudaStream_t s);
 // The prefixes' part in bf16 with head_dim 128 (tcgen05).
 cudaError_t launch_prefix_tc(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl, cudaStream_t s);
+
+// The same for the other types, and the rows that a CTA of it takes.
+cudaError_t launch_prefix_tile(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl, cudaStream_t s);
+int prefix_tile_rows(const pa_cache_desc& d);
 
 // ---------------------------------------------------------------------------
 // block tables

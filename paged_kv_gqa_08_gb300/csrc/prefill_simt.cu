@@ -30,7 +30,6 @@ struct SimtParams {
   int64_t num_pages;
   int64_t num_tokens;
   int32_t B, Hq, Hkv, P, maxp, max_ctx;
-  int32_t window, sinks;  // window > 0: the keys between are not seen
   float scale_log2;
 };
 
@@ -87,8 +86,7 @@ __global__ void __launch_bounds__(128) prefill_simt_kernel(const SimtParams p) {
   }
   float m = -INFINITY, l = 0.f;
   const int32_t* row = p.bt + static_cast<int64_t>(b) * p.maxp;
-  const int gap_hi = p.window > 0 ? max(0, pos - p.window + 1) : 0, gap_lo = min(p.sinks, gap_hi);
-  for (int j = gap_lo > 0 ? 0 : gap_hi; j <= pos; j = j + 1 == gap_lo ? gap_hi : j + 1) {
+  for (int j = 0; j <= pos; ++j) {
     const int page = row[j / p.P];
     if (page < 0 || page >= p.num_pages) {
       if (lane == 0) raise_flag(p.err, PA_DEVERR_BAD_PAGE);
@@ -134,8 +132,6 @@ cudaError_t launch_prefill_simt(const pa_cache_desc& d, const PrefillArgs& a, cu
   p.P = d.page_size;
   p.maxp = a.max_pages;
   p.max_ctx = a.max_context_len;
-  p.window = a.window;
-  p.sinks = a.sinks;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   const dim3 grid(static_cast<unsigned>(a.num_tokens), (d.num_q_heads + 3) / 4);
   if (d.dtype == PA_BF16) {

@@ -890,6 +890,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc) + 1;
 
+  // A shared prefix: the CTA's share of the groups' key tiles, worked out beside the setup.
+  [[maybe_unused]] PrefixShare share;
+  [[maybe_unused]] PrefixWork work;
+  [[maybe_unused]] bool has_work = false;
+  if constexpr (kMode == kPrefix) {
+    if (warp == kSchedWarp) {
+      share = prefix_share(p.prefix, blockIdx.x, gridDim.x, p.prefix_costs);
+      if (lane == 0) has_work = next_prefix_work(p.prefix, share, work);
+    }
+  }
+
   // V rows past the last key of a tile meet a probability of 0 in the PV
   // products, so they must hold finite values: both V stages start zeroed and
   // the V producer zeroes the rows a ragged tile leaves unloaded.
@@ -962,9 +973,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     // Planned launch: items k = unit * Hkv + kv-head are taken from a shared
     // counter, so a CTA that finishes early takes the next one (the units are
     // listed longest first).  Otherwise the CTA's own pair is its one item.
-    // A shared prefix: the CTA's share of the groups' key tiles, unit by unit.
-    PrefixShare share;
-    if constexpr (kMode == kPrefix) share = prefix_share(p.prefix, blockIdx.x, gridDim.x, p.prefix_costs);
     if (lane == 0) {
       if (p.units) pdl_wait();  // the planner's unit list and counter are ready
       const int total = p.units ? *p.n_units * p.Hkv : 1;
@@ -992,9 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         bool last;
         int k = 0;
         if constexpr (kMode == kPrefix) {
-          PrefixWork w;
-          last = !next_prefix_work(p.prefix, share, w);
-          if (!last) make_prefix_item(p, w, blockIdx.x, it);
+          if (pub > 0) has_work = next_prefix_work(p.prefix, share, work);
+          last = !has_work;
+          if (!last) make_prefix_item(p, work, blockIdx.x, it);
         } else {
           k = p.units ? atomicAdd(p.counter, 1) : k_own++;
           last = k >= total;
@@ -1968,7 +1976,27 @@ cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t
   p.window = a.window;
   p.sinks = a.sinks;
   if ((e = prepare_kernels<kMode>()) != cudaSuccess) return e;
-  if (!a.workspace) {
+  bool planned = a.workspace != nullptr;
+  if (kMode == kWindow && planned) {
+    // A window bounds a pair's key tiles T, and with them what splitting can gain:
+    // while the pairs fill w <= 4 waves of CTAs, the last of them T (ceil(w) - w) of a
+    // tile's time; planner and merge cost about 12 tiles' (20 where they overlap
+    // other waves).  Measured, us (planned, unplanned; new tokens, window, q- / kv-heads):
+    //   33, 64, 16/8 (T 4, w 0.05)    22.2  13.5     128, 2048, 16/8 (T 19, w 0.05)  30.4  38.4
+    //   512, 2048, 40/8 (T 19, 0.58)  55.8  42.3     512, 8192, 40/8 (T 67, 0.58)  110.0 117.2
+    //   2048, 8192, 16/8 (T 67, 0.84) 128.7 114.0    2048, 8192, 40/8 (T 67, 2.16) 322.0 348.0
+    //   2048, 512, 40/8 (T 7, 2.16)    85.0  68.2    8192, 64, 40/8 (T 3, w 8.6)   122.5 148.5
+    const int64_t reach = static_cast<int64_t>(2 * TQ) + a.window + kBN - 2;  // keys of a pair's rows, unaligned
+    const int64_t T = std::min<int64_t>((static_cast<int64_t>(a.max_context_len) + kBN - 1) / kBN,
+                                        reach / kBN + 1 + (static_cast<int64_t>(a.sinks) + kBN - 1) / kBN);
+    const int64_t qp = ((a.max_seqlen_q + TQ - 1) / TQ + 1) / 2;
+    const int64_t pairs = std::min<int64_t>(a.batch * qp, a.num_tokens / (2 * TQ) + a.batch);
+    DeviceInfo di;
+    if ((e = current_device_info(&di)) != cudaSuccess) return e;
+    const double w = static_cast<double>(pairs * d.num_kv_heads) / di.sm_count;
+    if (w <= 4 && T * (ceil(w) - w) <= (w <= 1 ? 12 : 20) && a.batch <= 65535) planned = false;
+  }
+  if (!planned) {
     const int qtiles = (a.max_seqlen_q + TQ - 1) / TQ;
     const dim3 grid((qtiles + 1) / 2, d.num_kv_heads, a.batch);
     prefill_tc_kernel<kMode><<<grid, kThreads, kSmemBytes, s>>>(p);

@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(kTabThreads) release_pages_kernel(const Releas
 }
 
 cudaError_t launch_cluster(const void* fn, int ctas, size_t smem, cudaStream_t s, void** args) {
+  if (ctas == 1) return cudaLaunchKernel(fn, dim3(1), dim3(kTabThreads), args, smem, s);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTabThreads);
@@ -333,10 +334,8 @@ cudaError_t launch_cluster(const void* fn, int ctas, size_t smem, cudaStream_t s
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  if (ctas > 1) {
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-  }
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

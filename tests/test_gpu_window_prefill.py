@@ -112,22 +112,45 @@ def test_random_batches(cuda_lib, seed):
     run(c, new, c.randn(sum(new), G * Hkv, 128), window, sinks, what=f"{lens} {new} {G} {Hkv} {window} {sinks}")
 
 
-@pytest.mark.parametrize("dt,hd", [(BF16, 128), (F32, 64)])
+@pytest.mark.parametrize("dt,hd", [(BF16, 128), (BF16, 64), (F32, 64), (F32, 128)])
 def test_a_window_of_everything_is_plain_prefill(cuda_lib, dt, hd):
+    """The same bits where the same kernel runs; elsewhere two roundings of the same result."""
     lens, new = [700, 300, 1], [500, 1, 1]
     c = Paged(lens, 8, 2, hd, 16, dt, seed=1)
     q = c.randn(502, 8, hd)
     cu = torch.tensor([0, 500, 501, 502], dtype=torch.int32, device="cuda")
     full = torch.zeros_like(q)
     pa.pa_prefill_varlen(c.desc, q, cu, 3, 500, 502, c.k, c.v, c.bt, c.maxp, c.ctx, 700, 0.1, full)
-    for window, sinks in ((700, 0), (1 << 30, 1 << 30), ((1 << 31) - 1, 5), (300, 400)):
+    for window, sinks in ((700, 0), (1 << 30, 1 << 30), ((1 << 31) - 1, 5), ((1 << 31) - 1, (1 << 31) - 1), (300, 400)):
         out = prefill(c, new, q, window, sinks, 0.1, False)
-        assert torch.equal(out.view(torch.uint8), full.view(torch.uint8))
+        if (dt, hd) == (BF16, 128):
+            assert torch.equal(out.view(torch.uint8), full.view(torch.uint8))
+        compare(c, new, q, out, window, sinks, 0.1)
     # longer than the longest context, shorter than the bound that is given for it: the windowed kernel
     out = torch.zeros_like(q)
     pa.pa_prefill_varlen_window(c.desc, 701, 0, q, cu, 3, 500, 502, c.k, c.v, c.bt, c.maxp, c.ctx, c.maxp * 16, 0.1,
                                 out)
-    assert torch.equal(out.view(torch.uint8), full.view(torch.uint8))
+    if (dt, hd) == (BF16, 128):
+        assert torch.equal(out.view(torch.uint8), full.view(torch.uint8))
+    compare(c, new, q, out, 701, 0, 0.1)
+
+
+@pytest.mark.parametrize("dt,hd", [(BF16, 64), (F32, 64), (F32, 128)])
+def test_bad_pages_of_the_other_types_are_left_out(cuda_lib, dt, hd):
+    lens, new, window, sinks = [300, 300], [64, 64], 100, 4
+    c = Paged(lens, 4, 2, hd, 16, dt, seed=1)
+    q = c.randn(128, 4, hd)
+    c.bt[0, 5] = 1 << 30   # between the sinks and the window: not looked at
+    out = prefill(c, new, q, window, sinks, 0.1, True)
+    compare(c, new, q, out, window, sinks, 0.1)
+    assert pa.pa_read_device_errors(reset=True) == 0
+    c.bt[1, 15] = -3       # in the window of some rows: keys 240 to 255 are left out
+    out = prefill(c, new, q, window, sinks, 0.1, True)
+    assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_PAGE
+    p, j = torch.arange(236, 300, device="cuda")[:, None], torch.arange(300, device="cuda")
+    seen = (j <= p) & ((j > p - window) | (j < sinks)) & ~((j >= 240) & (j < 256))
+    o, bound = attend(q[64:], c.K[1], c.V[1], seen, 0.1, dt)
+    check(out[64:], o, bound)
 
 
 def test_bad_pages(cuda_lib):
