@@ -123,12 +123,8 @@ pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t window, in
   st = prefill_args(desc, q, cu_seqlens_q, batch, max_seqlen_q, num_tokens, k_cache, v_cache, block_tables,
                     max_pages_per_seq, context_lens, max_context_len, scale, out, workspace, workspace_bytes, &a);
   if (st != PA_OK || a.num_tokens == 0) return st;
-  // a window of the whole context sees what no window sees (the kernel for the
-  // other types takes it all the same: it is the faster one)
-  if (static_cast<int64_t>(window) + num_sinks < max_context_len || desc->dtype != PA_BF16 || desc->head_dim != 128) {
-    a.window = window;
-    a.sinks = num_sinks;
-  }
+  a.window = window;
+  a.sinks = num_sinks;
   if ((st = prepare(&a.err)) != PA_OK) return st;
   cudaError_t e = launch_prefill(*desc, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);

@@ -390,12 +390,14 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
   const int x0 = static_cast<int>((static_cast<int64_t>(share) * NC) / n_ctas);
   const int x1 = kRange && share == n_ctas ? x0 : static_cast<int>((static_cast<int64_t>(share + 1) * NC) / n_ctas);
   // With groups the grid starts beside the kernel over their prefixes, whose
-  // output only the merge reads: each CTA's last act is to wait for it.
-  const bool beside = kRange && p.cu_groups != nullptr;
+  // output only the merge reads: the last CTA waits for it before it ends, and
+  // with it the grid, while the others leave their SMs to the next ones.
+  const bool beside = kRange && p.cu_groups != nullptr && !p.through_rep;
   if (beside && p.inline_plan && c == 0)  // the sums, for that merge
     for (int b = threadIdx.x; b <= p.B; b += blockDim.x) p.cs[b] = cs[b];
+  const bool waits = beside && c == static_cast<int>(gridDim.x) - 1;
   if (x0 >= x1) {
-    if (beside) pdl_wait();
+    if (waits) pdl_wait();
     return;
   }
 
@@ -434,13 +436,25 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
         const int L = p.ctx[my_b];
         int t0 = jc << p.log2T;
         [[maybe_unused]] Hole hole{0, 0};
+        int end = L, table = my_b;
         if constexpr (kRange) {
           hole = hole_of(p, my_b, L);
-          const int before = chunks_before_hole(hole, p.log2T);
-          if (jc >= before) t0 += chunks_in_hole(hole, L, p.log2T) << p.log2T;
+          if (p.through_rep) {
+            const int pre_chunks = (hole.hi + tok - 1) >> p.log2T;
+            if (jc < pre_chunks) {  // of the prefix
+              const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
+              table = prefix_owner(p, my_b, hole.hi, cap);
+              end = hole.hi;
+              hole.hi = 0;
+            } else {
+              t0 = (jc - pre_chunks + (hole.hi >> p.log2T)) << p.log2T;
+            }
+          } else if (jc >= chunks_before_hole(hole, p.log2T)) {
+            t0 += chunks_in_hole(hole, L, p.log2T) << p.log2T;
+          }
         }
-        n = min(tok, L - t0);
-        const int page = p.bt[static_cast<int64_t>(my_b) * p.maxp + (t0 >> p.log2P)];
+        n = min(tok, end - t0);
+        const int page = p.bt[static_cast<int64_t>(table) * p.maxp + (t0 >> p.log2P)];
         if (page < 0 || page >= p.num_pages) {
           raise_flag(p.err, PA_DEVERR_BAD_PAGE);
           n = 0;
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
           const int a = min(max(hole.lo - t0, 0), n), z = min(max(hole.hi - t0, 0), n);
           if (z > a) flags |= a << 8 | z << 16;
           // the keys before the range are another kernel's: this share is a part however whole it is
-          if (p.cu_groups != nullptr && hole.hi > 0) flags &= ~4;
+          if (beside && hole.hi > 0) flags &= ~4;
         }
         if (p.k_new != nullptr && (flags & 8) && n >= 1)
           new_slot = static_cast<int>(off / p.row_bytes) + n - 1;  // position context_len - 1
@@ -530,7 +544,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
       for (int it = max(0, issued - kStages); it < issued; ++it)
         drain_wait(&full[it % kStages], (it / kStages) & 1);
     }
-    if (beside) pdl_wait();
+    if (waits) pdl_wait();
     return;
   }
 

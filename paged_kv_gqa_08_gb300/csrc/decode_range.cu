@@ -6,6 +6,8 @@
 // chunks at its two ends are not copied (tensor-core consumers) and have
 // probability 0.  Bytes per request: min(L, sinks + window) K and V rows; HBM
 // bound like the kernel over all keys.
+#include <cmath>
+
 #include "decode_kernel.cuh"
 #include "prefix_plan.cuh"
 
@@ -59,7 +61,7 @@ namespace {
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads)
     shared_merge_kernel(const KParams p, const PrefixShape s, const int64_t* costs, const float* o_pre,
-                        const float* lse_pre, int max_ctas) {
+                        const float* lse_pre) {
   constexpr int EL = HD / 32;
   constexpr int NWARP = kMergeThreads / 32;
   __shared__ float red[NWARP][32][EL + 1];
@@ -84,7 +86,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   // the prefix's parts: np CTAs from f0 on
   int f0 = 0, np = 0;
   if (gr.cost > 0) {
-    const int ctas = prefix_ctas(s, total, max_ctas);
+    const int ctas = static_cast<int>(costs[s.n_groups + 1]);
     const PrefixUnit unit = prefix_unit(s, gr, costs[g], h, (b - gr.s0) / s.TQ / 2);
     f0 = prefix_cta_of(unit.start, total, ctas);
     np = prefix_cta_of(unit.start + static_cast<int64_t>(gr.nt - 1) * unit.cost, total, ctas) - f0 + 1;
@@ -99,9 +101,9 @@ __global__ void __launch_bounds__(kMergeThreads)
   // without a prefix a single CTA's result is the output already
   active = active && (np > 0 || ns > 1);
   const int parts = np + ns;
-  const int64_t pre_row = np > 0 ? prefix_part_row(gr.s0, gr.n, h, f0, p.Hq, G) + (b - gr.s0) * G + hq - h * G : 0;
+  const int64_t pre_row = np > 0 ? prefix_part_row(s, gr.s0, gr.n, h, f0, p.Hq, G) + (b - gr.s0) * G + hq - h * G : 0;
   const int64_t own_row = static_cast<int64_t>(c0 + b) * p.Hq + hq;
-  auto row_of = [&](int k) { return k < np ? pre_row + static_cast<int64_t>(k) * kPrefixPartRows
+  auto row_of = [&](int k) { return k < np ? pre_row + static_cast<int64_t>(k) * s.unit_rows
                                            : own_row + static_cast<int64_t>(k - np) * p.Hq; };
   auto lse_of = [&](int k) { return k < np ? lse_pre[row_of(k)] : p.lse_part[row_of(k)]; };
   float acc[EL];
@@ -197,6 +199,8 @@ PrefixShape prefix_shape(const pa_cache_desc& d, const SharedArgs& a, const Shar
   s.Hkv = d.num_kv_heads;
   s.cost_pair = pl.cost_pair;
   s.cost_one = pl.cost_one;
+  s.min_share = pl.min_share;
+  s.unit_rows = pl.unit_rows;
   return s;
 }
 
@@ -213,17 +217,37 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
     if ((e = current_device_info(&di)) != cudaSuccess) return e;
     const int G = d.num_q_heads / d.num_kv_heads;
     const bool tc = prefix_on_tcgen05(d);
-    pl.prefix_ctas = max_ctas > 0 ? std::min(max_ctas, di.sm_count) : di.sm_count;
-    pl.TQ = (tc ? 128 : prefix_tile_rows(d) / 2) / G;
+    pl.unit_rows = tc ? 256 : prefix_tile_rows(d);
+    pl.TQ = pl.unit_rows / 2 / G;
     // a tile of one q-tile alone takes about 0.7 of the time that one of two takes
     pl.cost_pair = tc ? 10 : 1;
     pl.cost_one = tc ? 7 : 1;
-    const int64_t rows = static_cast<int64_t>(batch) * d.num_q_heads + static_cast<int64_t>(pl.prefix_ctas) * 256;
+    pl.min_share = tc ? 14 : 1;
+    const int most = di.sm_count * (tc ? 1 : 2);
+    pl.prefix_ctas = max_ctas > 0 ? std::min(max_ctas, most) : most;
+    // Few keys in all (by the bounds): one decode over prefixes and own keys reads
+    // a prefix once for each request, but spares a kernel and the larger merge.
+    // Estimates, us, beyond what both cost; measured, us (each, once; q- / kv-heads
+    // of dims, requests / groups, prefix):
+    //   bf16 16/8 of 128   4/1  1024  12.8 19.0    16/1  1024  19.2 19.3    64/1   256  19.5 23.0
+    //                     64/1  1024  44.9 25.2    24/3  4096  62.0 27.9   128/7   256  31.5 26.9
+    //   bf16 16/8 of 64    4/1  1024  11.3 13.1    16/1  1024  14.9 14.0    24/3  4096  33.5 20.6
+    //   fp32 16/4 of 128  16/1  1024  19.0 35.4    16/1  4096  39.3 41.2    16/1 16384 123.1 115.4
+    const double row = 2.0 * d.num_kv_heads * d.head_dim * elem_bytes(d.dtype);
+    const double each_us = batch * static_cast<double>(max_prefix) * row / 6.0e6;
+    const double units = std::ceil(static_cast<double>(batch) / n_groups * G / pl.unit_rows) * n_groups * d.num_kv_heads;
+    const double tile_us = tc ? 2 : d.dtype == PA_BF16 ? 2.8 : d.head_dim == 64 ? 14 : 24;  // 128 keys of a unit
+    const double once_us = (tc ? 7 + 0.09 * batch : 4) + std::ceil(units * ((max_prefix + 127) / 128) / most) * tile_us;
+    pl.through_rep = each_us < once_us;
+    if (pl.through_rep) pl.prefix_ctas = 0;
+  }
+  if (pl.prefix_ctas > 0) {
+    const int64_t rows = static_cast<int64_t>(batch) * d.num_q_heads + static_cast<int64_t>(pl.prefix_ctas) * pl.unit_rows;
     if (rows >= int64_t(1) << 31) return cudaErrorInvalidValue;
     // TMA coordinates are 32-bit: the cache rows must be addressable
-    if (tc && d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (prefix_on_tcgen05(d) && d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     pl.off_costs = pl.ws_bytes;
-    pl.off_lse = align_up(pl.off_costs + (static_cast<size_t>(n_groups) + 1) * 8, 256);
+    pl.off_lse = align_up(pl.off_costs + (static_cast<size_t>(n_groups) + 2) * 8, 256);
     pl.off_o = align_up(pl.off_lse + static_cast<size_t>(rows) * 4, 256);
     pl.ws_bytes = align_up(pl.off_o + static_cast<size_t>(rows) * d.head_dim * 4, 256);
   }
@@ -245,7 +269,7 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   da.max_pages = a.max_pages;
   da.max_context_len = a.max_context_len;
   da.scale = a.scale;
-  if (pl.prefix_ctas == 0) return launch_decode(d, pl.suffix, da, s);
+  if (pl.prefix_ctas == 0 && !pl.through_rep) return launch_decode(d, pl.suffix, da, s);
   const Fns f = get_fns<true>(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
   if (!f.main) return cudaErrorInvalidValue;
   KParams p = decode_params(d, pl.suffix, da, d.num_kv_heads * d.head_dim * elem_bytes(d.dtype));
@@ -254,6 +278,10 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   p.prefix_lens = a.prefix_lens;
   p.n_groups = a.n_groups;
   p.max_prefix = a.max_prefix;
+  if (pl.through_rep) {
+    p.through_rep = 1;
+    return launch_decode_kernels<true>(f.main, f.merge, pl.suffix, p, args, s);
+  }
   cudaError_t e = prefix_on_tcgen05(d) ? launch_prefix_tc(d, a, pl, s) : launch_prefix_tile(d, a, pl, s);
   if (e != cudaSuccess) return e;
   const int threads = (pl.suffix.nw + 1) * 32;
@@ -275,8 +303,7 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   const int64_t* costs = reinterpret_cast<const int64_t*>(ws + pl.off_costs);
   const float* o_pre = reinterpret_cast<const float*>(ws + pl.off_o);
   const float* lse_pre = reinterpret_cast<const float*>(ws + pl.off_lse);
-  int max_ctas = pl.prefix_ctas;
-  void* margs[] = {&p, &shape, &costs, &o_pre, &lse_pre, &max_ctas};
+  void* margs[] = {&p, &shape, &costs, &o_pre, &lse_pre};
   const int64_t items = static_cast<int64_t>(p.B) * p.Hq;
   const int per_cta = kMergeThreads / 32 / p.merge_w;
   const void* merge =

@@ -53,11 +53,12 @@ struct KParams {
   // A range of each request's keys left out (the kRange kernels).  Without
   // groups: the keys between the first `sinks` and the last `window`.  With
   // them: the first prefix_lens[g] keys of the requests cu_groups[g] ..
-  // cu_groups[g + 1] - 1, which another kernel attends to.
+  // cu_groups[g + 1] - 1, which another kernel attends to -- or, with
+  // through_rep, this one, by the table of the group's first request.
   int32_t window, sinks;
   const int32_t* cu_groups;
   const int32_t* prefix_lens;
-  int32_t n_groups, max_prefix;
+  int32_t n_groups, max_prefix, through_rep;
   int32_t per_request;  // a CTA for each request, whole (no merge)
 };
 
@@ -87,6 +88,15 @@ PA_DEVINL Hole hole_of(const KParams& p, int b, int L) {
   return Hole{lo, max(lo, L - p.window)};
 }
 
+// The request whose table names the prefix of b's group: the first live one that
+// is as long (b itself is, where b's lengths are consistent).
+PA_DEVINL int prefix_owner(const KParams& p, int b, int prefix, int cap) {
+  const int g = group_of(p.cu_groups, p.n_groups, b);
+  for (int r = max(p.cu_groups[g], 0); r < b; ++r)
+    if (p.ctx[r] >= prefix && p.ctx[r] <= cap) return r;
+  return b;
+}
+
 // Chunks before the range and chunks wholly inside it (L: the context).
 PA_DEVINL int chunks_before_hole(Hole h, int log2T) { return (h.lo + (1 << log2T) - 1) >> log2T; }
 PA_DEVINL int chunks_in_hole(Hole h, int L, int log2T) {
@@ -113,7 +123,10 @@ PA_DEVINL int chunks_of(const KParams& p, int b, int cap, bool* bad) {
   if constexpr (kRange) {
     const Hole h = hole_of(p, b, L);
     *bad = h.hi < 0;
-    return h.hi < 0 ? 0 : n - chunks_in_hole(h, L, p.log2T);
+    if (h.hi < 0) return 0;
+    // a prefix and the own keys in chunks of their own, the one at the seam in both
+    if (p.through_rep) return ((h.hi + (1 << p.log2T) - 1) >> p.log2T) + (L > h.hi ? n - (h.hi >> p.log2T) : 0);
+    return n - chunks_in_hole(h, L, p.log2T);
   }
   return n;
 }

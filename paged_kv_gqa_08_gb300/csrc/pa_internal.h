@@ -317,10 +317,13 @@ struct PrefixShape {
   int32_t n_groups, B, max_prefix, cap_ctx;
   int32_t TQ, Hkv;              // requests per q-tile, kv-heads
   int32_t cost_pair, cost_one;  // cost of a key tile of a unit of two q-tiles, and of one
+  int32_t min_share;            // of a CTA, at least cost_pair
+  int32_t unit_rows;            // rows of a unit, at most
 };
 struct SharedPlan {
   DecodePlan suffix;  // the requests' own keys
-  int32_t prefix_ctas = 0, TQ = 0, cost_pair = 0, cost_one = 0;
+  bool through_rep = false;  // one decode over prefixes and own keys
+  int32_t prefix_ctas = 0, TQ = 0, cost_pair = 0, cost_one = 0, min_share = 0, unit_rows = 0;
   size_t off_costs = 0, off_lse = 0, off_o = 0, ws_bytes = 0;  // the suffix's workspace comes first
 };
 PrefixShape prefix_shape(const pa_cache_desc& d, const SharedArgs& a, const SharedPlan& pl);

@@ -398,7 +398,7 @@ PA_DEVINL void make_prefix_item(const TcParams& p, const PrefixWork& w, int c, I
   it.split = it.nq == 1;
   it.kv_len = w.prefix;
   it.before = it.skip = it.gap_lo = it.gap_hi = 0;
-  it.part_row = prefix_part_row(w.s0, w.n, w.h, c, p.Hq, p.G);
+  it.part_row = prefix_part_row(p.prefix, w.s0, w.n, w.h, c, p.Hq, p.G);
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const int qt = it.split ? 0 : g;

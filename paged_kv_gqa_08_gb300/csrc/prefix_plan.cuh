@@ -13,20 +13,19 @@
 //
 // A unit cut over CTAs leaves a part (O / l and the base-2 log-sum-exp of each
 // row) per CTA.  Parts are packed: CTA c's part of the rows of kv-head h of a
-// group starts at row cu[g] Hq + h n G + 256 c, row (request, q-head) in order;
-// a unit has at most 256 rows, so parts never overlap, and B Hq + 256 CTAs rows
-// hold them all.
+// group starts at row cu[g] Hq + h n G + R c, row (request, q-head) in order; a
+// unit has at most R rows, so parts never overlap, and B Hq + R CTAs rows hold
+// them all.
 #pragma once
 
 #include "pa_common.cuh"
 
 namespace pa {
 
-constexpr int kPrefixTile = 128;      // keys per tile
-constexpr int kPrefixPartRows = 256;  // rows of a unit, at most
+constexpr int kPrefixTile = 128;  // keys per tile
 
-PA_DEVINL int32_t prefix_part_row(int s0, int n, int h, int c, int Hq, int G) {
-  return s0 * Hq + h * n * G + c * kPrefixPartRows;
+PA_DEVINL int32_t prefix_part_row(const PrefixShape& s, int s0, int n, int h, int c, int Hq, int G) {
+  return s0 * Hq + h * n * G + c * s.unit_rows;
 }
 
 struct PrefixGroup {
@@ -58,10 +57,14 @@ PA_DEVINL PrefixGroup prefix_group(const PrefixShape& s, int g) {
   return r;
 }
 
-// CTAs that take a share of a line of this length: as many as get two tiles
-// each, so that every CTA between the ends of a unit has a tile of it.
+// CTAs that take a share of a line of this length: as many as get min_share
+// of it, at least the cost of a tile, so that every CTA between the ends of a
+// unit has a tile of it.  (Fewer, with SMs left to the decode kernel over the
+// requests' own keys from the start, was no faster: 64 -> 67 us for 96 requests
+// in 3 groups, 96 -> 98 us for 128 behind 32768 keys.  A decode CTA streams 50
+// GB/s at most, hardly more than its part of HBM's rate when all SMs stream.)
 PA_DEVINL int prefix_ctas(const PrefixShape& s, int64_t total, int max_ctas) {
-  return static_cast<int>(min(static_cast<int64_t>(max_ctas), max(total / (2 * s.cost_one), int64_t(1))));
+  return static_cast<int>(min(static_cast<int64_t>(max_ctas), max(total / s.min_share, int64_t(1))));
 }
 
 // The CTA that place x of the line belongs to.
@@ -76,7 +79,8 @@ struct PrefixShare {
 };
 
 // CTA c's share, found by one warp (all lanes); CTA 0 also writes where each
-// group starts, and the line's length, to costs[0 .. n_groups] for the merge.
+// group starts, the line's length and the number of CTAs to costs[0 .. n_groups + 1]
+// for the merge.
 PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, int64_t* costs) {
   const int lane = threadIdx.x & 31;
   int64_t total = 0;
@@ -110,7 +114,10 @@ PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, in
     }
     carry = __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (c == 0 && lane == 0) costs[s.n_groups] = total;
+  if (c == 0 && lane == 0) {
+    costs[s.n_groups] = total;
+    costs[s.n_groups + 1] = ctas;
+  }
   return r;
 }
 

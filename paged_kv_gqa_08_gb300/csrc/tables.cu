@@ -23,6 +23,7 @@ namespace pa {
 namespace {
 
 constexpr int kTabThreads = 512;  // also the requests per pass of the prefix sums
+constexpr int kTabAhead = 4;       // look-ups that a thread has in flight
 constexpr int kTabCluster = 8;
 constexpr int kMaxReleaseRows = 32768;  // their prefix sums are in shared memory
 
@@ -135,19 +136,30 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Extend
       }
       p.bt[static_cast<int64_t>(b0 + i) * p.maxp + held + (k - s_page[i])] = page;
     }
-    for (int64_t t = static_cast<int64_t>(rank) * kTabThreads + tid; t < got_total.y;
-         t += static_cast<int64_t>(R) * kTabThreads) {
-      const int i = last_at_or_below(s_tok, rows, static_cast<int>(t));
-      const int pos = s_len[i] + static_cast<int>(t - s_tok[i]);
-      const int held = (static_cast<int64_t>(s_len[i]) + (1 << p.log2P) - 1) >> p.log2P, at = pos >> p.log2P;
-      const int page = at < held ? p.bt[static_cast<int64_t>(b0 + i) * p.maxp + at] : page_at(s_page[i] + at - held);
-      int64_t slot = -1;
-      if (page >= 0 && page < p.num_pages)
-        slot = (static_cast<int64_t>(page) << p.log2P) + (pos & ((1 << p.log2P) - 1));
-      else
-        raise_flag(p.err, PA_DEVERR_BAD_PAGE);
-      p.positions[tokens + t] = pos;
-      p.slots[tokens + t] = slot;
+    const int64_t step = static_cast<int64_t>(R) * kTabThreads;
+    for (int64_t t0 = static_cast<int64_t>(rank) * kTabThreads + tid; t0 < got_total.y; t0 += kTabAhead * step) {
+      int pos[kTabAhead], page[kTabAhead];
+#pragma unroll
+      for (int u = 0; u < kTabAhead; ++u) {
+        const int64_t t = t0 + u * step;
+        if (t >= got_total.y) break;
+        const int i = last_at_or_below(s_tok, rows, static_cast<int>(t));
+        pos[u] = s_len[i] + static_cast<int>(t - s_tok[i]);
+        const int held = (static_cast<int64_t>(s_len[i]) + (1 << p.log2P) - 1) >> p.log2P, at = pos[u] >> p.log2P;
+        page[u] = at < held ? p.bt[static_cast<int64_t>(b0 + i) * p.maxp + at] : page_at(s_page[i] + at - held);
+      }
+#pragma unroll
+      for (int u = 0; u < kTabAhead; ++u) {
+        const int64_t t = t0 + u * step;
+        if (t >= got_total.y) break;
+        int64_t slot = -1;
+        if (page[u] >= 0 && page[u] < p.num_pages)
+          slot = (static_cast<int64_t>(page[u]) << p.log2P) + (pos[u] & ((1 << p.log2P) - 1));
+        else
+          raise_flag(p.err, PA_DEVERR_BAD_PAGE);
+        p.positions[tokens + t] = pos[u];
+        p.slots[tokens + t] = slot;
+      }
     }
     pages_asked += total.x;
     tokens_asked += total.y;
@@ -244,21 +256,42 @@ __global__ void __launch_bounds__(kTabThreads) release_pages_kernel(const Releas
   }
   if (tid == 0) s_sums[p.batch] = n_all;
   cta_sync();
+  // this CTA's entries, and of those this thread's: [lo, hi), in order
   const int e0 = static_cast<int>(static_cast<int64_t>(n_all) * rank / R);
   const int e1 = static_cast<int>(static_cast<int64_t>(n_all) * (rank + 1) / R);
+  const int per = (e1 - e0 + kTabThreads - 1) / kTabThreads;
+  const int lo = min(e1, e0 + tid * per), hi = min(e1, lo + per);
+  auto end_of = [&](int b) {
+    return p.ctx ? static_cast<int>(min(max(static_cast<int64_t>(p.ctx[b]) + 1 - p.window, int64_t(0)) >> p.log2P,
+                                        static_cast<int64_t>(p.maxp)))
+                 : p.end[b];
+  };
   auto entry = [&](int e) {  // the place of entry e in the tables
     const int b = last_at_or_below(s_sums, p.batch, e);
-    const int end = p.ctx ? static_cast<int>(min(max(static_cast<int64_t>(p.ctx[b]) + 1 - p.window, int64_t(0)) >> p.log2P,
-                                                 static_cast<int64_t>(p.maxp)))
-                          : p.end[b];
-    return p.bt + static_cast<int64_t>(b) * p.maxp + end - 1 - (e - s_sums[b]);
+    return p.bt + static_cast<int64_t>(b) * p.maxp + end_of(b) - 1 - (e - s_sums[b]);
   };
   auto valid = [&](int page) { return page >= 0 && page < p.num_pages; };
+  // A thread's first entries stay in registers from step to step, with their
+  // look-ups in flight together; the others are looked up again.
+  int32_t* place_of[kTabAhead];
+  int page_of[kTabAhead];
+#pragma unroll
+  for (int u = 0; u < kTabAhead; ++u) place_of[u] = lo + u < hi ? entry(lo + u) : nullptr;
+#pragma unroll
+  for (int u = 0; u < kTabAhead; ++u) page_of[u] = place_of[u] ? *place_of[u] : -1;
+  auto for_entries = [&](auto&& f) {  // f(entry, page, place)
+#pragma unroll
+    for (int u = 0; u < kTabAhead; ++u)
+      if (place_of[u]) f(lo + u, page_of[u], place_of[u]);
+    for (int e = lo + kTabAhead; e < hi; ++e) {
+      int32_t* place = entry(e);
+      f(e, *place, place);
+    }
+  };
   // 1. the counts
-  for (int e = e0 + tid; e < e1; e += kTabThreads) {
-    const int page = *entry(e);
+  for_entries([&](int, int page, int32_t*) {
     if (page >= p.num_pages) raise_flag(p.err, PA_DEVERR_BAD_PAGE);
-    if (!valid(page) || !p.refs) continue;
+    if (!valid(page) || !p.refs) return;
     const int old = atomicSub(&p.refs[page], 1);
     if (old == 1) {
       atomicAdd(&p.refs[page], kReturned);
@@ -266,27 +299,31 @@ __global__ void __launch_bounds__(kTabThreads) release_pages_kernel(const Releas
       atomicAdd(&p.refs[page], 1);
       raise_flag(p.err, PA_DEVERR_BAD_PAGE);
     }
-  }
+  });
   if (p.refs) {
     cluster_barrier(R);
     // 2. the last entry of each page that nobody holds any longer
-    for (int e = e0 + tid; e < e1; e += kTabThreads) {
-      const int page = *entry(e);
+    for_entries([&](int e, int page, int32_t*) {
       if (valid(page) && __ldcg(&p.refs[page]) <= kReturned) atomicMin(&p.refs[page], kReturned - 1 - e);
-    }
+    });
   }
   cluster_barrier(R);
-  // 3. how many of this CTA's entries return a page, and where in the ring
+  // 3. how many of this thread's entries return a page, and where in the ring
   auto returns = [&](int e, int page) {
     return valid(page) && (!p.refs || __ldcg(&p.refs[page]) == kReturned - 1 - e);
   };
   int mine = 0;
-  for (int e = e0 + tid; e < e1; e += kTabThreads) mine += returns(e, *entry(e));
+  uint32_t out_of = 0;  // those kept in registers
+  for_entries([&](int e, int page, int32_t*) {
+    const bool out = returns(e, page);
+    mine += out;
+    if (e - lo < kTabAhead) out_of |= static_cast<uint32_t>(out) << (e - lo);
+  });
   longlong2 total;
-  scan2(make_longlong2(mine, 0), sh, &total);
+  const int64_t before = scan2(make_longlong2(mine, 0), sh, &total).x;
   if (tid == 0) s_count = static_cast<int>(total.x);
   cluster_barrier(R);
-  int64_t at = 0, all = 0;
+  int64_t at = before, all = 0;
   for (int r = 0; r < R; ++r) {
     int n = s_count;
     if (R > 1) {
@@ -297,25 +334,17 @@ __global__ void __launch_bounds__(kTabThreads) release_pages_kernel(const Releas
     at += r < rank ? n : 0;
     all += n;
   }
-  for (int x = e0; x < e1; x += kTabThreads) {
-    const int e = x + tid;
-    int page = -1;
-    int32_t* place = nullptr;
-    bool out = false;
-    if (e < e1) {
-      place = entry(e);
-      page = *place;
-      out = returns(e, page);
-    }
-    const int64_t k = at + scan2(make_longlong2(out, 0), sh, &total).x;
-    if (out) {
-      if (k < room) p.ring[(returned + k) % p.num_pages] = page;
+  int64_t to = (returned + at) % p.num_pages;
+  for_entries([&](int e, int page, int32_t* place) {
+    if (e - lo < kTabAhead ? (out_of >> (e - lo)) & 1 : returns(e, page)) {
+      if (at < room) p.ring[to] = page;
       else raise_flag(p.err, PA_DEVERR_BAD_LENGTH);  // more pages than there are
       if (p.refs) p.refs[page] = 0;
+      ++at;
+      if (++to == p.num_pages) to = 0;
     }
-    if (place) *place = -1;
-    at += total.x;
-  }
+    *place = -1;
+  });
   if (rank == 0 && tid == 0) {
     p.pool_out[0] = taken;
     p.pool_out[1] = returned + min(all, room);

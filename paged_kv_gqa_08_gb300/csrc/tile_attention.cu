@@ -10,7 +10,7 @@
 // room for one, and two CTAs an SM instead), with an online softmax in base 2:
 //   bf16   16 rows a warp, S = Q K^T and O += P V as mma.sync m16n8k16 with fp32
 //          sums, K and V fragments by ldmatrix from swizzled rows.
-//   fp32   8 rows a warp, a lane two keys of the tile for the scores (packed
+//   fp32   up to 8 rows a warp (few rows: a fourth of them each), a lane two keys of the tile for the scores (packed
 //          fp32 pairs) and head_dim / 32 dims for the output: fp32 throughout,
 //          bound by the fp32 pipe and the shared-memory loads that feed it.
 // Rows that no query sees are zero in shared memory and have probability 0; they
@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "prefix_plan.cuh"
@@ -183,7 +184,9 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
   using Gm = TileGeom<T, HD>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = smem_u32(smem);
-  const int row0 = warp * Gm::kWarpRows;
+  // rows of this warp: 16, or (fp32) up to 8, evenly over the warps
+  const int nr = Gm::kMma ? Gm::kWarpRows : (it.rows + 3) >> 2;
+  const int row0 = warp * nr;
   const bool busy = row0 < it.rows;  // the warp has rows
   const TileOut<T, HD, kPrefix> out{p, it, part_row};
   auto seen = [&](int pos, int key) {
@@ -243,7 +246,7 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
           make_float4(v.x * p.scale_log2, v.y * p.scale_log2, v.z * p.scale_log2, v.w * p.scale_log2);
     }
   }
-  const int pos_min = pos_of(row0), pos_max = pos_of(min(it.rows, row0 + Gm::kWarpRows) - 1);
+  const int pos_min = pos_of(row0), pos_max = pos_of(min(it.rows, row0 + nr) - 1);
 
   for (int j = list.first; j < list.end; ++j) {
     const int k0 = list.key0(j), n = j - list.first;
@@ -341,66 +344,73 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
           }
         }
       } else {
-        const float* qs = reinterpret_cast<const float*>(smem + Gm::kOffQ) + row0 * HD;
-        float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + row0 * kTileKeys;
-        const float* kf = reinterpret_cast<const float*>(smem + (kst - smem0));
-        const float* vf = reinterpret_cast<const float*>(smem + (vst - smem0));
-        float2 acc[R][2];
+        // (for 2, 4 or 8 rows, so that few rows cost little and the sums stay in registers)
+        auto tile_rows = [&](auto rows_c) {
+          constexpr int NR = decltype(rows_c)::value;
+          const float* qs = reinterpret_cast<const float*>(smem + Gm::kOffQ) + row0 * HD;
+          float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + row0 * kTileKeys;
+          const float* kf = reinterpret_cast<const float*>(smem + (kst - smem0));
+          const float* vf = reinterpret_cast<const float*>(smem + (vst - smem0));
+          float2 acc[NR][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
+          for (int r = 0; r < NR; ++r) acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
 #pragma unroll 2
-        for (int d = 0; d < HD; d += 4) {
-          const float4 ka = *reinterpret_cast<const float4*>(kf + lane * (HD + 4) + d);
-          const float4 kb = *reinterpret_cast<const float4*>(kf + (lane + 32) * (HD + 4) + d);
+          for (int d = 0; d < HD; d += 4) {
+            const float4 ka = *reinterpret_cast<const float4*>(kf + lane * (HD + 4) + d);
+            const float4 kb = *reinterpret_cast<const float4*>(kf + (lane + 32) * (HD + 4) + d);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float4 qv = *reinterpret_cast<const float4*>(qs + r * HD + d);
-            acc[r][0] = ffma2(make_float2(qv.x, qv.y), make_float2(ka.x, ka.y), acc[r][0]);
-            acc[r][0] = ffma2(make_float2(qv.z, qv.w), make_float2(ka.z, ka.w), acc[r][0]);
-            acc[r][1] = ffma2(make_float2(qv.x, qv.y), make_float2(kb.x, kb.y), acc[r][1]);
-            acc[r][1] = ffma2(make_float2(qv.z, qv.w), make_float2(kb.z, kb.w), acc[r][1]);
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float s0 = acc[r][0].x + acc[r][0].y, s1 = acc[r][1].x + acc[r][1].y;
-          if (mask) {
-            const int ka = k0 + lane, kb = ka + 32;
-            if (!seen(pos[r], ka) || (bad && !live_key(ka))) s0 = -INFINITY;
-            if (!seen(pos[r], kb) || (bad && !live_key(kb))) s1 = -INFINITY;
-          }
-          float mx = fmaxf(s0, s1);
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const float m_new = fmaxf(m[r], mx), m_use = m_new == -INFINITY ? 0.f : m_new;
-          const float alpha = tile_ex2(m[r] - m_use);
-          m[r] = m_new;
-          const float p0 = tile_ex2(s0 - m_use), p1 = tile_ex2(s1 - m_use);
-          l[r] = l[r] * alpha + (p0 + p1);  // this lane's share of the sum
-          ps[r * kTileKeys + lane] = p0;
-          ps[r * kTileKeys + lane + 32] = p1;
-#pragma unroll
-          for (int e = 0; e < DL; ++e) o1[r][e] *= alpha;
-        }
-        __syncwarp();
-#pragma unroll 2
-        for (int k = 0; k < kTileKeys; k += 4) {
-          float v[4][DL];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < DL; e += 2) {
-              const float2 w = *reinterpret_cast<const float2*>(vf + (k + u) * HD + lane * DL + e);
-              v[u][e] = w.x, v[u][e + 1] = w.y;
+            for (int r = 0; r < NR; ++r) {
+              const float4 qv = *reinterpret_cast<const float4*>(qs + r * HD + d);
+              acc[r][0] = ffma2(make_float2(qv.x, qv.y), make_float2(ka.x, ka.y), acc[r][0]);
+              acc[r][0] = ffma2(make_float2(qv.z, qv.w), make_float2(ka.z, ka.w), acc[r][0]);
+              acc[r][1] = ffma2(make_float2(qv.x, qv.y), make_float2(kb.x, kb.y), acc[r][1]);
+              acc[r][1] = ffma2(make_float2(qv.z, qv.w), make_float2(kb.z, kb.w), acc[r][1]);
             }
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float4 pv = *reinterpret_cast<const float4*>(ps + r * kTileKeys + k);
-#pragma unroll
-            for (int e = 0; e < DL; ++e)
-              o1[r][e] = fmaf(pv.w, v[3][e], fmaf(pv.z, v[2][e], fmaf(pv.y, v[1][e], fmaf(pv.x, v[0][e], o1[r][e]))));
           }
-        }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float s0 = acc[r][0].x + acc[r][0].y, s1 = acc[r][1].x + acc[r][1].y;
+            if (mask) {
+              const int ka = k0 + lane, kb = ka + 32;
+              if (!seen(pos[r], ka) || (bad && !live_key(ka))) s0 = -INFINITY;
+              if (!seen(pos[r], kb) || (bad && !live_key(kb))) s1 = -INFINITY;
+            }
+            float mx = fmaxf(s0, s1);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m_new = fmaxf(m[r], mx), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = tile_ex2(m[r] - m_use);
+            m[r] = m_new;
+            const float p0 = tile_ex2(s0 - m_use), p1 = tile_ex2(s1 - m_use);
+            l[r] = l[r] * alpha + (p0 + p1);  // this lane's share of the sum
+            ps[r * kTileKeys + lane] = p0;
+            ps[r * kTileKeys + lane + 32] = p1;
+#pragma unroll
+            for (int e = 0; e < DL; ++e) o1[r][e] *= alpha;
+          }
+          __syncwarp();
+#pragma unroll 2
+          for (int k = 0; k < kTileKeys; k += 4) {
+            float v[4][DL];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < DL; e += 2) {
+                const float2 w = *reinterpret_cast<const float2*>(vf + (k + u) * HD + lane * DL + e);
+                v[u][e] = w.x, v[u][e + 1] = w.y;
+              }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float4 pv = *reinterpret_cast<const float4*>(ps + r * kTileKeys + k);
+#pragma unroll
+              for (int e = 0; e < DL; ++e)
+                o1[r][e] = fmaf(pv.w, v[3][e], fmaf(pv.z, v[2][e], fmaf(pv.y, v[1][e], fmaf(pv.x, v[0][e], o1[r][e]))));
+            }
+          }
+        };
+        if (nr <= 2) tile_rows(std::integral_constant<int, 2>{});
+        else if (nr <= 4) tile_rows(std::integral_constant<int, 4>{});
+        else tile_rows(std::integral_constant<int, 8>{});
       }
     }
     cta_sync();  // the stage may be filled again
@@ -427,7 +437,7 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
     for (int r = 0; r < R; ++r) {
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-      if (row0 + r >= it.rows) continue;
+      if (r >= nr || row0 + r >= it.rows) continue;
       const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
 #pragma unroll
       for (int e = 0; e < DL; e += 2) out.store2(row0 + r, lane * DL + e, o1[r][e] * inv, o1[r][e + 1] * inv);
@@ -508,7 +518,7 @@ __global__ void __launch_bounds__(kTileThreads) prefix_tile_kernel(const TilePar
     list.before = list.skip = 0;
     list.end = min(w.j_hi * kSub, (w.prefix + kTileKeys - 1) / kTileKeys);
     // (every warp has copied `work` by the barriers of its tiles, before it is written again)
-    tile_run<T, HD, true>(p, it, list, prefix_part_row(w.s0, w.n, w.h, blockIdx.x, p.Hq, p.G) + t0 * p.G, tile_smem);
+    tile_run<T, HD, true>(p, it, list, prefix_part_row(p.shape, w.s0, w.n, w.h, blockIdx.x, p.Hq, p.G) + t0 * p.G, tile_smem);
   }
 }
 

@@ -16,10 +16,14 @@ class Groups(Paged):
     """Requests of `groups` = [(prefix, [own tokens, ...]), ...] (None: a padding row), the prefix's whole pages
     shared, its last tokens copied; what the calls may not look at is left out or poisoned."""
 
-    def __init__(self, groups, Hq, Hkv, hd, P, dt, seed):
+    def __init__(self, groups, Hq, Hkv, hd, P, dt, seed, wide=False):
         lens = [0 if o is None else pre + o for pre, own in groups for o in own]
         super().__init__(lens, Hq, Hkv, hd, P, dt, seed)
         self.groups = groups
+        if wide:  # tables, and so bounds, of a million tokens and more: the kernel over the prefixes, whatever is shared
+            self.bt = torch.nn.functional.pad(self.bt, (0, 65536 - self.maxp), value=-1)
+            self.maxp = 65536
+        self.wide = wide
         self.cu = torch.tensor([0] + list(torch.tensor([len(o) for _, o in groups]).cumsum(0)), dtype=torch.int32,
                                device="cuda")
         self.pre = torch.tensor([p for p, _ in groups], dtype=torch.int32, device="cuda")
@@ -40,8 +44,8 @@ class Groups(Paged):
 
     def call(self, q, scale, max_ctas=0, out=None, max_ctx=None, max_pre=None):
         B, ng = len(self.lens), len(self.groups)
-        mx = max_ctx or max(max(self.lens), 1)
-        mp = max_pre if max_pre is not None else int(self.pre.max())
+        mx = max_ctx or (65536 * self.P if self.wide else max(max(self.lens), 1))
+        mp = max_pre if max_pre is not None else mx if self.wide else int(self.pre.max())
         nbytes = pa.pa_decode_shared_prefix_workspace_size(self.desc, ng, B, mp, mx, max_ctas)
         assert nbytes > 0
         ws = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
@@ -76,8 +80,9 @@ GROUPS = {
 
 @pytest.mark.parametrize("dt,Hq,Hkv,hd", HEADS)
 @pytest.mark.parametrize("name", GROUPS)
-def test_against_plain(cuda_lib, dt, Hq, Hkv, hd, name):
-    c = Groups(GROUPS[name], Hq, Hkv, hd, 16 if name != "ragged" else 64, dt, seed=Hq)
+@pytest.mark.parametrize("wide", [False, True])
+def test_against_plain(cuda_lib, dt, Hq, Hkv, hd, name, wide):
+    c = Groups(GROUPS[name], Hq, Hkv, hd, 16 if name != "ragged" else 64, dt, Hq, wide)
     q = c.randn(len(c.lens), Hq, hd)
     for max_ctas in (0, 1, 5):
         out = c.call(q, hd ** -0.5, max_ctas)
@@ -96,9 +101,10 @@ def test_long_prefix(cuda_lib, dt, Hq, Hkv, hd):
 
 
 @pytest.mark.parametrize("dt,hd", [(BF16, 128), (F32, 64)])
-def test_batches_planned_before_the_kernel(cuda_lib, dt, hd):
+@pytest.mark.parametrize("wide", [False, True])
+def test_batches_planned_before_the_kernel(cuda_lib, dt, hd, wide):
     groups = [(64 + i % 100, [(i * k) % 40 for k in range(1, 9)]) for i in range(70)]
-    c = Groups(groups, 4, 2, hd, 16, dt, seed=1)
+    c = Groups(groups, 4, 2, hd, 16, dt, 1, wide)
     assert len(c.lens) > 512
     q = c.randn(len(c.lens), 4, hd)
     c.compare(q, c.call(q, 0.1), 0.1)
@@ -106,7 +112,8 @@ def test_batches_planned_before_the_kernel(cuda_lib, dt, hd):
 
 
 @pytest.mark.parametrize("seed", range(10))
-def test_random_groups(cuda_lib, seed):
+@pytest.mark.parametrize("wide", [False, True])
+def test_random_groups(cuda_lib, seed, wide):
     r = random.Random(seed)
     groups = []
     for _ in range(r.randint(1, 12)):
@@ -114,7 +121,7 @@ def test_random_groups(cuda_lib, seed):
         pre = r.choice([0, 1, 127, 128, 129, int(2 ** r.uniform(0, 12))])
         groups.append((pre, [1 if o == 0 and pre == 0 else o for o in own]))
     G, Hkv = r.randint(1, 8), r.choice([1, 2, 4, 8])
-    c = Groups(groups, G * Hkv, Hkv, 128, r.choice([16, 64, 256]), BF16, seed)
+    c = Groups(groups, G * Hkv, Hkv, 128, r.choice([16, 64, 256]), BF16, seed, wide)
     q = c.randn(len(c.lens), G * Hkv, 128)
     c.compare(q, c.call(q, 0.1, r.choice([0, 0, 7])), 0.1, f"{groups} {G} {Hkv}")
     assert pa.pa_read_device_errors(reset=True) == 0
@@ -142,9 +149,11 @@ def test_no_groups_is_plain_decode(cuda_lib, dt, hd):
     assert pa.pa_read_device_errors(reset=True) == 0
 
 
-def test_bad_lengths_and_pages(cuda_lib):
-    c = Groups([(256, [4, 40, 8]), (64, [9, 9])], 4, 2, 128, 16, BF16, seed=1)
-    q = c.randn(5, 4, 128)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dt,hd", [(BF16, 128), (BF16, 64), (F32, 128)])
+def test_bad_lengths_and_pages(cuda_lib, dt, hd, wide):
+    c = Groups([(256, [4, 40, 8]), (64, [9, 9])], 4, 2, hd, 16, dt, 1, wide)
+    q = c.randn(5, 4, hd)
     c.ctx[1] = 255                      # shorter than its group's prefix
     out = c.call(q, 0.1, out=torch.full_like(q, 3.0))
     assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_LENGTH
@@ -153,9 +162,9 @@ def test_bad_lengths_and_pages(cuda_lib):
     out[1] = NAN
     c.compare(q, out, 0.1)
     c.lens[1], c.ctx[1] = 296, 296
-    for bad in (-1, 300):               # out of range: the group's requests are skipped
+    for bad in (-1, 1 << 30):               # out of range: the group's requests are skipped
         c.pre[1] = bad
-        out = c.call(q, 0.1, out=torch.full_like(q, 3.0), max_pre=256)
+        out = c.call(q, 0.1, out=torch.full_like(q, 3.0), max_pre=None if wide else 256)
         assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_LENGTH
         assert (out[3:] == 3.0).all()
         keep, c.lens[3], c.lens[4] = c.lens[3:], -1, -1
@@ -163,21 +172,28 @@ def test_bad_lengths_and_pages(cuda_lib):
         c.compare(q, out, 0.1)
         c.lens[3:] = keep
     c.pre[1] = 64
-    c.bt[0, 3] = c.num_pages            # a page of the first group's prefix: rows of zeros
+    c.bt[0, 3] = c.num_pages            # a page of the first group's prefix
     out = c.call(q, 0.1)
     assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_PAGE
-    for b in range(3):
-        c.K[b][48:64], c.V[b][48:64] = 0, 0
-    c.compare(q, out, 0.1)
+    for b in range(5):
+        seen = torch.ones(1, c.lens[b], dtype=torch.bool, device="cuda")
+        if b < 3 and wide and (dt, hd) == (BF16, 128):
+            c.K[b][48:64], c.V[b][48:64] = 0, 0
+        elif b < 3:                     # the other kernels leave its keys out
+            seen[:, 48:64] = False
+        o, bound = attend(q[b: b + 1], c.K[b], c.V[b], seen, 0.1, dt)
+        check(out[b: b + 1], o, bound, f"request {b}")
 
 
-def test_graph_and_stream(cuda_lib):
-    c = Groups([(500, [30, 20, 10]), (100, [200, 300])], 8, 4, 128, 16, BF16, seed=2)
+@pytest.mark.parametrize("wide", [False, True])
+def test_graph_and_stream(cuda_lib, wide):
+    c = Groups([(500, [30, 20, 10]), (100, [200, 300])], 8, 4, 128, 16, BF16, 2, wide)
+    most = 65536 * 16 if wide else 530
     q = c.randn(5, 8, 128)
     out = torch.full_like(q, NAN)
-    ws = torch.empty(pa.pa_decode_shared_prefix_workspace_size(c.desc, 2, 5, 530, 530), dtype=torch.uint8,
+    ws = torch.empty(pa.pa_decode_shared_prefix_workspace_size(c.desc, 2, 5, most, most), dtype=torch.uint8,
                      device="cuda")
-    args = (c.desc, 2, c.cu, c.pre, 530, q, 5, c.k, c.v, c.bt, c.maxp, c.ctx, 530, 0.1, 0, out, ws)
+    args = (c.desc, 2, c.cu, c.pre, most, q, 5, c.k, c.v, c.bt, c.maxp, c.ctx, most, 0.1, 0, out, ws)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     pa.pa_decode_shared_prefix(*args, stream=side)
