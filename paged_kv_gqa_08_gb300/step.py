@@ -9,6 +9,10 @@ and sequences calls; every value is computed by libpagedattn's kernels.
 Buffers allocated with a ``group_size`` step over a 4-bit cache: the writes
 quantise, decode attends to the codes, and prefill reads the contexts back into
 a staging cache of the descriptor's dtype and attends to that.
+
+A step with a ``window`` attends to the last ``window`` tokens and the first
+``num_sinks``; a decode step with ``cu_groups`` reads the prefix that the requests
+of a group share once for all of them.
 """
 from __future__ import annotations
 
@@ -18,10 +22,12 @@ from typing import Optional
 
 import torch
 
-from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_WORKSPACE, PagedAttnError, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_workspace_size,
-               pa_kv_read_q4, pa_kv_read_q4_tables, pa_kv_write, pa_kv_write_q4, pa_prefill_qk_norm_rope_kv_write,
-               pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step, pa_prefill_varlen, pa_prefill_workspace_size,
-               pa_slot_mapping)
+from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PagedAttnError, cache_desc,
+               pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_shared_prefix,
+               pa_decode_shared_prefix_workspace_size, pa_decode_window, pa_decode_window_workspace_size,
+               pa_decode_workspace_size, pa_kv_read_q4, pa_kv_read_q4_tables, pa_kv_write, pa_kv_write_q4,
+               pa_prefill_qk_norm_rope_kv_write, pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step,
+               pa_prefill_varlen, pa_prefill_varlen_window, pa_prefill_workspace_size, pa_slot_mapping)
 
 
 @dataclasses.dataclass
@@ -55,12 +61,15 @@ def torch_dtype(desc) -> torch.dtype:
 
 def alloc_step_buffers(desc, kind: str, num_tokens: int, batch: int, max_context_len: int, device,
                        norm: bool = False, max_ctas: int = 0, max_seqlen_q: Optional[int] = None,
-                       plan_prefill: bool = True, group_size: int = 0) -> StepBuffers:
+                       plan_prefill: bool = True, group_size: int = 0, window: int = 0, num_sinks: int = 0,
+                       num_groups: int = 0, max_prefix_len: int = 0) -> StepBuffers:
     """Buffers of one step.  A prefill step gets the planned-launch workspace
     unless ``plan_prefill`` is False (or the shape is never planned); it is
     sized for chunks up to ``max_seqlen_q`` tokens (default: ``num_tokens``).
     ``group_size`` (32, 64 or 128) is that of a 4-bit cache; a prefill step over
-    one gets a staging cache for ``batch`` contexts of ``max_context_len``."""
+    one gets a staging cache for ``batch`` contexts of ``max_context_len``.
+    ``window`` and ``num_sinks``, or ``num_groups`` and ``max_prefix_len``, are those
+    that a decode step will be run with."""
     dt = torch_dtype(desc)
     n = max(num_tokens, 1)
     positions = torch.empty(n, dtype=torch.int32, device=device)
@@ -69,9 +78,19 @@ def alloc_step_buffers(desc, kind: str, num_tokens: int, batch: int, max_context
     q_out = torch.empty_like(out) if norm else None
     ws = None
     if kind == "decode":
-        fn = "pa_decode_q4_workspace_size" if group_size else "pa_decode_workspace_size"
-        nbytes = (pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas) if group_size
-                  else pa_decode_workspace_size(desc, batch, max_context_len, max_ctas))
+        if group_size:
+            fn = "pa_decode_q4_workspace_size"
+            nbytes = pa_decode_q4_workspace_size(desc, group_size, batch, max_context_len, max_ctas)
+        elif window:
+            fn = "pa_decode_window_workspace_size"
+            nbytes = pa_decode_window_workspace_size(desc, window, num_sinks, batch, max_context_len, max_ctas)
+        elif num_groups:
+            fn = "pa_decode_shared_prefix_workspace_size"
+            nbytes = pa_decode_shared_prefix_workspace_size(desc, num_groups, batch, max_prefix_len, max_context_len,
+                                                            max_ctas)
+        else:
+            fn = "pa_decode_workspace_size"
+            nbytes = pa_decode_workspace_size(desc, batch, max_context_len, max_ctas)
         if nbytes == 0:
             raise RuntimeError(fn + " returned 0 (unsupported shape or no device)")
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -114,14 +133,24 @@ def write_rows(desc, k_rows, v_rows, cu_rows, lens, block_tables, max_pages_per_
 
 def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_lens, block_tables,
              k_cache, v_cache, scale: float, max_pages_per_seq: int, max_context_len: int, max_seqlen_q: int,
-             q_norm_w=None, k_norm_w=None, eps: float = 0.0, rope_theta: float = 0.0, stream=None):
+             q_norm_w=None, k_norm_w=None, eps: float = 0.0, rope_theta: float = 0.0, stream=None, window: int = 0,
+             num_sinks: int = 0, cu_groups=None, prefix_lens=None, max_prefix_len: int = 0):
     """Run one step; returns ``bufs.out`` (the attention output of the new tokens).  A step beyond its buffers is a
-    ``ValueError``; over a 4-bit cache whatever is refused is refused before anything is enqueued."""
+    ``ValueError``; over a 4-bit cache, with a window and with groups whatever is refused is refused before anything is
+    enqueued.
+
+    ``window`` > 0: the tokens attended to are those of ``pa_decode_window`` and ``pa_prefill_varlen_window``.
+    ``cu_groups`` and ``prefix_lens`` (up to ``max_prefix_len``): the groups of ``pa_decode_shared_prefix``, for decode
+    steps.  One or the other, and not over a 4-bit cache."""
     n = q.shape[0]
     batch = context_lens.shape[0]
     for t in (bufs.positions, bufs.slots, bufs.out, bufs.q_out if q_norm_w is not None else None):
         if t is not None and t.shape[0] < n:
             raise ValueError(f"a step of {n} tokens in buffers for {t.shape[0]}")
+    if window or cu_groups is not None:
+        return _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
+                               scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps,
+                               rope_theta, stream, window, num_sinks, cu_groups, prefix_lens, max_prefix_len)
     if bufs.group_size:
         return _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
                             scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps,
@@ -135,20 +164,80 @@ def run_step(desc, kind: str, bufs: StepBuffers, q, k, v, cu_seqlens_q, context_
                         bufs.workspace, stream=stream)
         return bufs.out
     _check_queries(desc, q, q_norm_w, k_norm_w)
+    qa = _write_step(desc, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
+                     max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, stream)
+    pa_decode(desc, qa, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len,
+              scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
+    return bufs.out
+
+
+def _write_step(desc, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, max_pages_per_seq,
+                q_norm_w, k_norm_w, eps, rope_theta, stream):
+    """The step's K/V rows into the cache; returns the queries that attention takes."""
+    n, batch = q.shape[0], context_lens.shape[0]
     if q_norm_w is not None:
         # slot mapping, norm, rotary and KV write in one kernel
         pa_prefill_qk_norm_rope_kv_write(desc, q, q.stride(0), k, k.stride(0), v, v.stride(0), n, cu_seqlens_q,
                                          batch, context_lens, block_tables, max_pages_per_seq, q_norm_w, k_norm_w,
                                          eps, rope_theta, bufs.q_out, k_cache, v_cache, bufs.positions, bufs.slots,
                                          stream)
-        qa = bufs.q_out
+        return bufs.q_out
+    pa_slot_mapping(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq, n, bufs.positions,
+                    bufs.slots, stream)
+    pa_kv_write(desc, k, k.stride(0), v, v.stride(0), n, bufs.slots, k_cache, v_cache, stream)
+    return q
+
+
+def _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, scale,
+                    max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w, k_norm_w, eps, rope_theta, stream,
+                    window, num_sinks, cu_groups, prefix_lens, max_prefix_len):
+    """A step over a window, or with groups that share a prefix."""
+    n, batch = q.shape[0], context_lens.shape[0]
+    if window and cu_groups is not None:
+        _refuse(PA_ERR_UNSUPPORTED, "a window and shared prefixes in one step")
+    if bufs.group_size:
+        _refuse(PA_ERR_UNSUPPORTED, "a 4-bit cache has no windowed and no shared-prefix attention")
+    if cu_groups is not None and kind != "decode":
+        _refuse(PA_ERR_UNSUPPORTED, "shared prefixes are a decode step's")
+    if window < 0 or (window and num_sinks < 0):
+        _refuse(PA_ERR_SHAPE, "a window is at least 1, the sinks at least 0")
+    groups = 0
+    if cu_groups is not None:
+        groups = cu_groups.shape[0] - 1
+        if prefix_lens is None:
+            _refuse(PA_ERR_NULL, "groups without prefix lengths")
+        if groups < 0 or prefix_lens.shape[0] < groups or not 0 <= max_prefix_len <= max_context_len:
+            _refuse(PA_ERR_SHAPE, "cu_groups, prefix_lens or max_prefix_len out of range")
+    _check_queries(desc, q, q_norm_w, k_norm_w)
+
+    def need():
+        if not (n and batch):
+            return 0
+        if kind != "decode":
+            return (pa_prefill_workspace_size(desc, batch, max_seqlen_q, n, max_context_len)
+                    if bufs.workspace is not None else 0)
+        nbytes = (pa_decode_window_workspace_size(desc, window, num_sinks, batch, max_context_len, bufs.max_ctas)
+                  if window else pa_decode_shared_prefix_workspace_size(desc, groups, batch, max_prefix_len,
+                                                                        max_context_len, bufs.max_ctas))
+        if nbytes == 0:
+            _refuse(PA_ERR_UNSUPPORTED, "decode does not take this descriptor, or there is no device")
+        return nbytes
+
+    _check_attention(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q,
+                     q_norm_w is not None, need, positive_scale=groups > 0)
+    qa = _write_step(desc, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
+                     max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, stream)
+    if kind != "decode":
+        pa_prefill_varlen_window(desc, window, num_sinks, qa, cu_seqlens_q, batch, max_seqlen_q, n, k_cache, v_cache,
+                                 block_tables, max_pages_per_seq, context_lens, max_context_len, scale, bufs.out,
+                                 bufs.workspace, None, stream)
+    elif window:
+        pa_decode_window(desc, window, num_sinks, qa, batch, k_cache, v_cache, block_tables, max_pages_per_seq,
+                         context_lens, max_context_len, scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
     else:
-        pa_slot_mapping(desc, batch, cu_seqlens_q, context_lens, block_tables, max_pages_per_seq, n, bufs.positions,
-                        bufs.slots, stream)
-        pa_kv_write(desc, k, k.stride(0), v, v.stride(0), n, bufs.slots, k_cache, v_cache, stream)
-        qa = q
-    pa_decode(desc, qa, batch, k_cache, v_cache, block_tables, max_pages_per_seq, context_lens, max_context_len,
-              scale, bufs.max_ctas, bufs.out, bufs.workspace, None, stream)
+        pa_decode_shared_prefix(desc, groups, cu_groups, prefix_lens, max_prefix_len, qa, batch, k_cache, v_cache,
+                                block_tables, max_pages_per_seq, context_lens, max_context_len, scale, bufs.max_ctas,
+                                bufs.out, bufs.workspace, None, stream)
     return bufs.out
 
 
@@ -170,29 +259,42 @@ def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_con
                    k_norm_w):
     """What the attention of a step over a 4-bit cache would refuse once the step's rows are written: refused before
     anything is enqueued (the write's own checks come first in its call)."""
-    n, norm = q.shape[0], q_norm_w is not None
+    n = q.shape[0]
     _check_queries(desc, q, q_norm_w, k_norm_w)
-    if n and not 1 <= max_context_len <= max_pages_per_seq * desc.page_size:
-        _refuse(PA_ERR_SHAPE, "max_context_len is not within 1 .. max_pages_per_seq * page_size")
-    if not math.isfinite(scale) or (kind != "decode" and not scale > 0):
-        _refuse(PA_ERR_SHAPE, "the scale is not finite, or not positive where prefill needs it")
-    if any(t is not None and t.data_ptr() % 16 for t in (bufs.out, bufs.q_out if norm else q)):
-        _refuse(PA_ERR_ALIGN, "q or out is not 16-byte aligned")
-    ws = bufs.workspace
-    if kind == "decode":
-        need = pa_decode_q4_workspace_size(desc, bufs.group_size, batch, max_context_len, bufs.max_ctas) if batch else 0
-        if need and ws is None:
-            _refuse(PA_ERR_WORKSPACE, "the buffers have no decode workspace")
-    else:
+
+    def need():
+        if kind == "decode":
+            return (pa_decode_q4_workspace_size(desc, bufs.group_size, batch, max_context_len, bufs.max_ctas)
+                    if batch else 0)
         st = bufs.staging
         if st is None:
             raise ValueError("the buffers were not allocated for a prefill step over a 4-bit cache")
         if batch > st.block_tables.shape[0] or max_context_len > st.max_pages * desc.page_size:
             raise ValueError("the step's batch or max_context_len is beyond what the buffers were allocated for")
-        if n and not (batch and 1 <= max_seqlen_q <= max_context_len):
-            _refuse(PA_ERR_SHAPE, "tokens without requests, or max_seqlen_q is not within 1 .. max_context_len")
-        need = (pa_prefill_workspace_size(st.desc, batch, max_seqlen_q, n, max_context_len)
-                if n and ws is not None else 0)
+        return (pa_prefill_workspace_size(st.desc, batch, max_seqlen_q, n, max_context_len)
+                if n and bufs.workspace is not None else 0)
+
+    _check_attention(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q,
+                     q_norm_w is not None, need)
+
+
+def _check_attention(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, norm, need,
+                     positive_scale=False):
+    """What attention refuses once the step's rows are written: bounds, scale, alignment, and a workspace of less than
+    ``need()`` bytes."""
+    n = q.shape[0]
+    if n and not 1 <= max_context_len <= max_pages_per_seq * desc.page_size:
+        _refuse(PA_ERR_SHAPE, "max_context_len is not within 1 .. max_pages_per_seq * page_size")
+    if not math.isfinite(scale) or ((kind != "decode" or positive_scale) and not scale > 0):
+        _refuse(PA_ERR_SHAPE, "the scale is not finite, or not positive where prefill or a shared prefix needs it")
+    if any(t is not None and t.data_ptr() % 16 for t in (bufs.out, bufs.q_out if norm else q)):
+        _refuse(PA_ERR_ALIGN, "q or out is not 16-byte aligned")
+    ws, need = bufs.workspace, need()
+    if kind == "decode":
+        if need and ws is None:
+            _refuse(PA_ERR_WORKSPACE, "the buffers have no decode workspace")
+    elif n and not (batch and 1 <= max_seqlen_q <= max_context_len):
+        _refuse(PA_ERR_SHAPE, "tokens without requests, or max_seqlen_q is not within 1 .. max_context_len")
     if need and ws.numel() * ws.element_size() < need:
         _refuse(PA_ERR_WORKSPACE, "the buffers' workspace is smaller than this step needs")
     if ws is not None and ws.data_ptr() % 256:
