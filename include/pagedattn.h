@@ -412,9 +412,11 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
  *
  * Keys that no query of the call attends to are not read, and neither are the
  * block-table entries of pages that hold only such keys: those pages may belong
- * to other requests, their entries may be -1.  Of the rows in one page (or one
- * 128-key tile of prefill) those not attended to may hold anything, NaN
- * included.  Lengths, padding rows, flags and refusals are the namesakes'.
+ * to other requests, their entries may be -1; the tokens in other pages that no
+ * query attends to may hold anything, NaN included.  (The values that some
+ * query of a prefill chunk attends to must be finite, as in the namesake, where
+ * the chunk's later tokens must: its other rows multiply them by 0.)  Lengths,
+ * padding rows, flags and refusals are the namesakes'.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace pa_decode_window and pa_decode_kv_write_window need;

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kTabThreads) extend_tables_kernel(const Extend
   __shared__ longlong2 sh[kTabThreads / 32];
   __shared__ int32_t s_len[kTabThreads], s_tok[kTabThreads], s_page[kTabThreads];
   const int tid = threadIdx.x, rank = blockIdx.x, R = gridDim.x;
-  const int64_t cap = static_cast<int64_t>(p.maxp) << p.log2P;
+  const int64_t cap = min(static_cast<int64_t>(p.maxp) << p.log2P, static_cast<int64_t>(0x7fffffff));
   const int64_t taken = p.pool[0], returned = p.pool[1];
   int64_t free_pages = returned - taken;
   if (taken < 0 || free_pages < 0 || free_pages > p.num_pages) {

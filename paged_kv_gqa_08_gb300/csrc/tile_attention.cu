@@ -60,7 +60,7 @@ struct TileParams {
   const int32_t* ctx;
   char* out;
   int64_t num_tokens;
-  int32_t max_ctx, window, sinks;
+  int32_t max_ctx, window, sinks, q_tiles;
   // shared prefixes
   PrefixShape shape;
   int64_t* costs;
@@ -446,13 +446,13 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
   }
 }
 
-// Chunked prefill: CTA = (q-tile, kv-head, request).
+// Chunked prefill: CTA = (q-tile of a request, kv-head).
 template <typename T, int HD>
 __global__ void __launch_bounds__(kTileThreads) window_tile_kernel(const TileParams p) {
   extern __shared__ __align__(128) unsigned char tile_smem[];
-  const int b = blockIdx.z, TQ = TileGeom<T, HD>::kRows / p.G;
+  const int b = blockIdx.x / p.q_tiles, TQ = TileGeom<T, HD>::kRows / p.G;
   const int s0 = p.cu[b], s1 = p.cu[b + 1], n = s1 - s0, L = p.ctx[b];
-  const int t0 = blockIdx.x * TQ;
+  const int t0 = (blockIdx.x - b * p.q_tiles) * TQ;
   if (L == 0 && s0 >= 0 && s1 <= p.num_tokens) return;  // a padding row
   const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
   if (s0 < 0 || s1 > p.num_tokens || n < 0 || L < n || L > cap) {
@@ -560,7 +560,10 @@ cudaError_t launch_window(const pa_cache_desc& d, const PrefillArgs& a, cudaStre
   p.window = a.window;
   p.sinks = a.sinks;
   const int TQ = TileGeom<T, HD>::kRows / p.G;
-  const dim3 grid((a.max_seqlen_q + TQ - 1) / TQ, d.num_kv_heads, a.batch);
+  p.q_tiles = (a.max_seqlen_q + TQ - 1) / TQ;
+  const int64_t tiles = static_cast<int64_t>(p.q_tiles) * a.batch;
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles), d.num_kv_heads);
   return launch_tile<T, HD>(reinterpret_cast<const void*>(window_tile_kernel<T, HD>), grid, p, s);
 }
 
@@ -583,7 +586,6 @@ int prefix_tile_rows(const pa_cache_desc& d) {
 
 cudaError_t launch_prefill_window_tile(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t s) {
   if (a.num_tokens == 0 || a.batch == 0) return cudaSuccess;
-  if (a.batch > 65535) return cudaErrorInvalidValue;
   if (d.dtype == PA_BF16) return launch_window<__nv_bfloat16, 64>(d, a, s);
   return d.head_dim == 128 ? launch_window<float, 128>(d, a, s) : launch_window<float, 64>(d, a, s);
 }
