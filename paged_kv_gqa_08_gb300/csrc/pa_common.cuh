@@ -151,6 +151,10 @@ PA_DEVINL void cta_sync() {
 PA_DEVINL void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// (counts a warp in without waiting for the others)
+PA_DEVINL void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 
 // ----------------------------------------------------------------------------
 // packed fp32x2 arithmetic

@@ -175,6 +175,12 @@ PA_DEVINL void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, i
                : "memory");
 }
 
+// Brings a tensor map to where the copy engine reads it: a kernel's first copies
+// else wait for theirs.
+PA_DEVINL void tma_prefetch_map(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
+
 PA_DEVINL void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 PA_DEVINL void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 PA_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -890,26 +896,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc) + 1;
 
-  // A shared prefix: the CTA's share of the groups' key tiles, worked out beside the setup.
-  [[maybe_unused]] PrefixShare share;
-  [[maybe_unused]] PrefixWork work;
-  [[maybe_unused]] bool has_work = false;
-  if constexpr (kMode == kPrefix) {
-    if (warp == kSchedWarp) {
-      share = prefix_share(p.prefix, blockIdx.x, gridDim.x, p.prefix_costs);
-      if (lane == 0) has_work = next_prefix_work(p.prefix, share, work);
-    }
+  if (warp == kVWarp && lane < (p.o_tma ? 6 : 5)) {
+    const CUtensorMap* maps[6] = {&p.tm_q, &p.tm_k16, &p.tm_v16, &p.tm_k1, &p.tm_v1, &p.tm_o};
+    tma_prefetch_map(maps[lane]);
   }
 
-  // V rows past the last key of a tile meet a probability of 0 in the PV
-  // products, so they must hold finite values: both V stages start zeroed and
-  // the V producer zeroes the rows a ragged tile leaves unloaded.
-  {
+  if constexpr (kMode == kCausal) {
+    // V rows past the last key of a tile meet a probability of 0 in the PV
+    // products, so they must hold finite values: both V stages start zeroed and
+    // the V producer zeroes the rows a ragged tile leaves unloaded.  (The other
+    // modes leave it to the producer: every row of a tile is copied or zeroed.)
     const uint4 z = make_uint4(0, 0, 0, 0);
     for (int i = threadIdx.x; i < 2 * kTileBytes / 16; i += kThreads)
       reinterpret_cast<uint4*>(smem + kOffV)[i] = z;
+    fence_async_smem();
   }
-  fence_async_smem();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
@@ -938,8 +939,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // A shared prefix: the scheduler works out the CTA's share of the groups' key
+  // tiles meanwhile.  It waits for the setup, the others do not wait for it.
+  [[maybe_unused]] PrefixShare share;
+  [[maybe_unused]] PrefixWork work;
+  [[maybe_unused]] bool has_work = false;
   tc_fence_before();
-  cta_sync();
+  if constexpr (kMode == kPrefix) {
+    if (warp == kSchedWarp) {
+      share = prefix_share(p.prefix, blockIdx.x, gridDim.x, p.prefix_costs);
+      if (lane == 0) has_work = next_prefix_work(p.prefix, share, work);
+      __syncwarp();
+      named_bar_sync(2, kThreads);
+    } else {
+      __syncwarp();
+      named_bar_sync(1, kThreads - 32);
+      named_bar_arrive(2, kThreads);
+    }
+  } else {
+    cta_sync();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 

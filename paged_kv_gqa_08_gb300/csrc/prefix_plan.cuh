@@ -24,6 +24,11 @@ namespace pa {
 
 constexpr int kPrefixTile = 128;  // keys per tile
 
+// a / b for a >= 0, b > 0: mostly small numbers, whose division is far shorter.
+PA_DEVINL int64_t div_small(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 PA_DEVINL int32_t prefix_part_row(const PrefixShape& s, int s0, int n, int h, int c, int Hq, int G) {
   return s0 * Hq + h * n * G + c * s.unit_rows;
 }
@@ -64,12 +69,12 @@ PA_DEVINL PrefixGroup prefix_group(const PrefixShape& s, int g) {
 // in 3 groups, 96 -> 98 us for 128 behind 32768 keys.  A decode CTA streams 50
 // GB/s at most, hardly more than its part of HBM's rate when all SMs stream.)
 PA_DEVINL int prefix_ctas(const PrefixShape& s, int64_t total, int max_ctas) {
-  return static_cast<int>(min(static_cast<int64_t>(max_ctas), max(total / s.min_share, int64_t(1))));
+  return static_cast<int>(min(static_cast<int64_t>(max_ctas), max(div_small(total, s.min_share), int64_t(1))));
 }
 
 // The CTA that place x of the line belongs to.
 PA_DEVINL int prefix_cta_of(int64_t x, int64_t total, int ctas) {
-  return static_cast<int>(((x + 1) * ctas + total - 1) / total) - 1;
+  return static_cast<int>(div_small((x + 1) * ctas + total - 1, total)) - 1;
 }
 
 struct PrefixShare {
@@ -90,8 +95,8 @@ PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, in
   PrefixShare r{0, 0, 0, s.n_groups};
   const int ctas = prefix_ctas(s, total, max_ctas);
   if (c < ctas && total > 0) {
-    r.x = total * c / ctas;
-    r.x1 = total * (c + 1) / ctas;
+    r.x = div_small(total * c, ctas);
+    r.x1 = div_small(total * (c + 1), ctas);
   }
   int64_t carry = 0;
   for (int g0 = 0; g0 < s.n_groups; g0 += 32) {
@@ -136,7 +141,7 @@ PA_DEVINL PrefixUnit prefix_unit(const PrefixShape& s, const PrefixGroup& gr, in
 
 // Tiles [lo, hi) of a unit that start in [x0, x1) of the line.
 PA_DEVINL int prefix_tile_at(const PrefixUnit& u, int nt, int64_t x) {
-  return x <= u.start ? 0 : static_cast<int>(min(static_cast<int64_t>(nt), (x - u.start + u.cost - 1) / u.cost));
+  return x <= u.start ? 0 : static_cast<int>(min(static_cast<int64_t>(nt), div_small(x - u.start + u.cost - 1, u.cost)));
 }
 
 struct PrefixWork {
@@ -154,9 +159,9 @@ PA_DEVINL bool next_prefix_work(const PrefixShape& s, PrefixShare& sh, PrefixWor
       ++sh.g;
       continue;
     }
-    const int h = static_cast<int>(rel / gr.head_cost);
+    const int h = static_cast<int>(div_small(rel, gr.head_cost));
     const int64_t y = rel - h * gr.head_cost;
-    const int qp = static_cast<int>(min(static_cast<int64_t>(gr.pairs), y / (static_cast<int64_t>(gr.nt) * s.cost_pair)));
+    const int qp = static_cast<int>(min(static_cast<int64_t>(gr.pairs), div_small(y, static_cast<int64_t>(gr.nt) * s.cost_pair)));
     const PrefixUnit u = prefix_unit(s, gr, sh.base, h, qp);
     const int j_lo = prefix_tile_at(u, gr.nt, sh.x), j_hi = prefix_tile_at(u, gr.nt, sh.x1);
     sh.x = u.start + static_cast<int64_t>(gr.nt) * u.cost;
