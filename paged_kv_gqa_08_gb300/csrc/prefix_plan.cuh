@@ -81,6 +81,7 @@ struct PrefixShare {
   int64_t x, x1;  // what is left of the share
   int64_t base;   // where group g starts
   int g;
+  PrefixGroup gr;  // group g, once looked up
 };
 
 // CTA c's share, found by one warp (all lanes); CTA 0 also writes where each
@@ -88,11 +89,16 @@ struct PrefixShare {
 // for the merge.
 PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, int64_t* costs) {
   const int lane = threadIdx.x & 31;
+  PrefixShare r{0, 0, 0, s.n_groups, {}};
   int64_t total = 0;
-  for (int g = lane; g < s.n_groups; g += 32) total += prefix_group(s, g).cost;
+  for (int g = lane; g < s.n_groups; g += 32) {
+    const PrefixGroup gr = prefix_group(s, g);
+    if (g < 32) r.gr = gr;  // the lane's first one is used again
+    total += gr.cost;
+  }
+  PrefixGroup mine = r.gr;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  PrefixShare r{0, 0, 0, s.n_groups};
   const int ctas = prefix_ctas(s, total, max_ctas);
   if (c < ctas && total > 0) {
     r.x = div_small(total * c, ctas);
@@ -101,20 +107,26 @@ PA_DEVINL PrefixShare prefix_share(const PrefixShape& s, int c, int max_ctas, in
   int64_t carry = 0;
   for (int g0 = 0; g0 < s.n_groups; g0 += 32) {
     const int g = g0 + lane;
-    const int64_t cost = g < s.n_groups ? prefix_group(s, g).cost : 0;
-    int64_t incl = cost;
+    if (g0 > 0) {
+      mine.cost = 0;
+      if (g < s.n_groups) mine = prefix_group(s, g);
+    }
+    int64_t incl = mine.cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     incl += carry;
-    if (c == 0 && g < s.n_groups) costs[g] = incl - cost;
+    if (c == 0 && g < s.n_groups) costs[g] = incl - mine.cost;
     const unsigned past = __ballot_sync(0xffffffffu, incl > r.x);
     if (past && r.g == s.n_groups) {
       const int first = __ffs(past) - 1;
+      auto from = [&](auto v) { return __shfl_sync(0xffffffffu, v, first); };
       r.g = g0 + first;
-      r.base = __shfl_sync(0xffffffffu, incl - cost, first);
+      r.base = from(incl - mine.cost);
+      r.gr = PrefixGroup{from(mine.s0),  from(mine.n),   from(mine.prefix),    from(mine.nt),  from(mine.rep),
+                         from(mine.pairs), from(mine.one), from(mine.head_cost), from(mine.cost)};
       if (c != 0) break;
     }
     carry = __shfl_sync(0xffffffffu, incl, 31);
@@ -152,11 +164,11 @@ struct PrefixWork {
 // The share's next unit with tiles in it (one thread); false at the end.
 PA_DEVINL bool next_prefix_work(const PrefixShape& s, PrefixShare& sh, PrefixWork& w) {
   while (sh.x < sh.x1 && sh.g < s.n_groups) {
-    const PrefixGroup gr = prefix_group(s, sh.g);
+    const PrefixGroup& gr = sh.gr;
     const int64_t rel = sh.x - sh.base;
     if (rel >= gr.cost) {
       sh.base += gr.cost;
-      ++sh.g;
+      if (++sh.g < s.n_groups) sh.gr = prefix_group(s, sh.g);
       continue;
     }
     const int h = static_cast<int>(div_small(rel, gr.head_cost));
