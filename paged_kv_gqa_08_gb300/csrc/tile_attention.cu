@@ -6,13 +6,17 @@
 // A CTA has up to 64 rows (bf16; fp32 32) of one kv-head: tokens x the G q-heads
 // that share it, so that a K/V tile in shared memory serves them all.  It goes
 // through the tiles of 64 keys that some row sees, copied 16 bytes at a time
-// (cp.async, the next tile while this one is at work; fp32 rows of 128 dims have
-// room for one, and two CTAs an SM instead), with an online softmax in base 2:
+// (cp.async; bf16: the next tile while this one is at work; fp32: one tile, and
+// more CTAs an SM instead -- 1200 tokens of 32 q-heads over 8 of 128 dims: 521 us
+// with one stage and two CTAs, 670 with two stages and one CTA; 4 requests of 100
+// to 300 tokens over 900 to 1500, 16 over 4 heads of 64 dims: 127 and 176), with
+// an online softmax in base 2:
 //   bf16   16 rows a warp, S = Q K^T and O += P V as mma.sync m16n8k16 with fp32
 //          sums, K and V fragments by ldmatrix from swizzled rows.
 //   fp32   up to 8 rows a warp (few rows: a fourth of them each), a lane two keys of the tile for the scores (packed
-//          fp32 pairs) and head_dim / 32 dims for the output: fp32 throughout,
-//          bound by the fp32 pipe and the shared-memory loads that feed it.
+//          fp32 pairs) and head_dim / 32 dims for the output: fp32 throughout;
+//          the fp32 pipe is busy 44% of the time with 8 warps an SM, what its
+//          shared memory holds.
 // Rows that no query sees are zero in shared memory and have probability 0; they
 // are not read, and neither are table entries of pages that hold only such rows.
 // Keys of a page that is out of range are left out.
@@ -38,7 +42,7 @@ struct TileGeom {
   static constexpr int kPitch = kMma ? HD * 2 : (HD + 4) * 4;  // bytes of a K row (fp32: lanes' rows in different banks)
   static constexpr int kVPitch = HD * static_cast<int>(sizeof(T));
   static constexpr int kStage = kTileKeys * (kPitch + kVPitch);
-  static constexpr int kStages = !kMma && HD == 128 ? 1 : 2;
+  static constexpr int kStages = kMma ? 2 : 1;
   static constexpr int kOffQ = kStages * kStage;                         // fp32: the rows' queries, scaled
   static constexpr int kOffP = kOffQ + (kMma ? 0 : kRows * HD * 4);      // fp32: probabilities
   static constexpr int kOffWork = kOffP + (kMma ? 0 : kRows * kTileKeys * 4);
@@ -354,7 +358,7 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
           float2 acc[NR][2];
 #pragma unroll
           for (int r = 0; r < NR; ++r) acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
           for (int d = 0; d < HD; d += 4) {
             const float4 ka = *reinterpret_cast<const float4*>(kf + lane * (HD + 4) + d);
             const float4 kb = *reinterpret_cast<const float4*>(kf + (lane + 32) * (HD + 4) + d);
@@ -389,16 +393,20 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
             for (int e = 0; e < DL; ++e) o1[r][e] *= alpha;
           }
           __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
           for (int k = 0; k < kTileKeys; k += 4) {
             float v[4][DL];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int e = 0; e < DL; e += 2) {
-                const float2 w = *reinterpret_cast<const float2*>(vf + (k + u) * HD + lane * DL + e);
-                v[u][e] = w.x, v[u][e + 1] = w.y;
+            for (int u = 0; u < 4; ++u) {
+              const float* src = vf + (k + u) * HD + lane * DL;
+              if constexpr (DL == 4) {
+                const float4 w = *reinterpret_cast<const float4*>(src);
+                v[u][0] = w.x, v[u][1] = w.y, v[u][2] = w.z, v[u][3] = w.w;
+              } else {
+                const float2 w = *reinterpret_cast<const float2*>(src);
+                v[u][0] = w.x, v[u][1] = w.y;
               }
+            }
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               const float4 pv = *reinterpret_cast<const float4*>(ps + r * kTileKeys + k);
