@@ -5,7 +5,7 @@
 namespace pa {
 
 cudaError_t plan_decode(const pa_cache_desc& d, int batch, int max_ctx, int max_ctas, DecodePlan* out) {
-  return plan_decode_keys<false>(d, batch, max_ctx, 0, max_ctas, out);
+  return plan_decode_keys<false>(d, batch, max_ctx, max_ctx, 0, max_ctas, out);
 }
 
 cudaError_t launch_decode(const pa_cache_desc& d, const DecodePlan& pl, const DecodeArgs& a, cudaStream_t s) {

@@ -318,7 +318,8 @@ PA_DEVINL void mma_consumer(const KParams& p, unsigned char* smem, uint64_t* ful
           float* dst = p.o_part + (slot * p.Hq + hq) * 128 + 2 * tq;
 #pragma unroll
           for (int j = 0; j < 16; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
-          if (tq == 0) p.lse_part[slot * p.Hq + hq] = l > 0.f ? m_run + log2f(l) : -INFINITY;
+          // (kRange: a sum that is no number stays one for the merge)
+          if (tq == 0) p.lse_part[slot * p.Hq + hq] = (kRange ? l != 0.f : l > 0.f) ? m_run + log2f(l) : -INFINITY;
         }
       }
       __syncwarp();
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
             for (int r = 0; r < NPR; r += 2)
               *reinterpret_cast<float4*>(dst + 2 * r) =
                   make_float4(o[g][r].x * inv, o[g][r].y * inv, o[g][r + 1].x * inv, o[g][r + 1].y * inv);
-            if (j == 0) p.lse_part[slot * p.Hq + hq] = lg > 0.f ? mg + log2f(lg) : -INFINITY;
+            if (j == 0) p.lse_part[slot * p.Hq + hq] = (kRange ? lg != 0.f : lg > 0.f) ? mg + log2f(lg) : -INFINITY;
           }
         }
       }
@@ -786,10 +787,10 @@ Fns get_fns(int dtype, int hd, int G) {
 
 bool uses_mma(int dtype, int hd, int /*G*/) { return dtype == PA_BF16 && hd == 128; }
 
-// The plan of a batch whose requests have up to `max_keys` keys to attend to, in
-// up to `extra_chunks` chunks more than those would fill.
+// The plan of a batch whose requests have up to max_ctx keys, of which up to
+// max_keys, in up to `extra` chunks more than those would fill, are attended to.
 template <bool kRange>
-cudaError_t plan_decode_keys(const pa_cache_desc& d, int batch, int max_keys, int extra_chunks, int max_ctas,
+cudaError_t plan_decode_keys(const pa_cache_desc& d, int batch, int max_ctx, int max_keys, int extra, int max_ctas,
                              DecodePlan* out) {
   DeviceInfo di;
   cudaError_t e = current_device_info(&di);
@@ -831,9 +832,8 @@ cudaError_t plan_decode_keys(const pa_cache_desc& d, int batch, int max_keys, in
   int occ = 0;
   e = ctas_per_sm(di, f.main, (pl.nw + 1) * 32, pl.smem_bytes, &occ);
   if (e != cudaSuccess) return e;
-  const int64_t chunks_upper =
-      static_cast<int64_t>(batch) *
-      ((static_cast<int64_t>(max_keys) + pl.tokens_per_chunk - 1) / pl.tokens_per_chunk + extra_chunks);
+  const int64_t T = pl.tokens_per_chunk;
+  const int64_t chunks_upper = batch * std::min((max_ctx + T - 1) / T, (max_keys + T - 1) / T + extra);
   pl.slots = occ * di.sm_count;
   int64_t n = pl.slots;
   if (max_ctas > 0) n = std::min<int64_t>(n, max_ctas);

@@ -12,12 +12,13 @@
 #include "prefix_plan.cuh"
 
 namespace pa {
+
 cudaError_t plan_decode_window(const pa_cache_desc& d, int batch, int max_ctx, int window, int sinks, int max_ctas,
                                DecodePlan* out) {
   const int64_t keys = static_cast<int64_t>(window) + sinks;
   if (keys >= max_ctx) return plan_decode(d, batch, max_ctx, max_ctas, out);  // nothing is left out
   // the sinks' last chunk and the window's first may both be partly filled
-  cudaError_t e = plan_decode_keys<true>(d, batch, static_cast<int>(keys), 2, max_ctas, out);
+  cudaError_t e = plan_decode_keys<true>(d, batch, max_ctx, static_cast<int>(keys), 2, max_ctas, out);
   if (e != cudaSuccess) return e;
   // A CTA for each request saves the merge and the sums over the batch.  It pays
   // where a request has few keys, or where the requests about fill the CTAs that
@@ -133,10 +134,16 @@ __global__ void __launch_bounds__(kMergeThreads)
     load(k_begin);
     // the first 32 parts' log-sum-exps stay in the lanes
     const float lse_mine = lane < parts ? lse_of(lane) : -INFINITY;
-    float M = lse_mine;
-    for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, lse_of(k));
+    float M = fmaxf(lse_mine, -INFINITY);
+    bool nan = lse_mine != lse_mine;
+    for (int k = lane + 32; k < parts; k += 32) {
+      const float x = lse_of(k);
+      M = fmaxf(M, x);
+      nan |= x != x;
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = merge_maximum(M, nan);
     if (M != -INFINITY) {
       const float w_first = exp2f(lse_mine - M);
       for (int k0 = k_begin; k0 < k_end; k0 += 8) {
@@ -208,7 +215,7 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
                         SharedPlan* out) {
   SharedPlan pl;
   const bool shared = n_groups > 0 && max_prefix > 0;
-  cudaError_t e = shared ? plan_decode_keys<true>(d, batch, max_ctx, 0, max_ctas, &pl.suffix)
+  cudaError_t e = shared ? plan_decode_keys<true>(d, batch, max_ctx, max_ctx, 0, max_ctas, &pl.suffix)
                          : plan_decode(d, batch, max_ctx, max_ctas, &pl.suffix);
   if (e != cudaSuccess) return e;
   pl.ws_bytes = align_up(pl.suffix.ws_bytes, 256);
@@ -239,13 +246,11 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
     const double tile_us = tc ? 2 : d.dtype == PA_BF16 ? 2.8 : d.head_dim == 64 ? 14 : 24;  // 128 keys of a unit
     const double once_us = (tc ? 7 + 0.09 * batch : 4) + std::ceil(units * ((max_prefix + 127) / 128) / most) * tile_us;
     pl.through_rep = each_us < once_us;
-    if (pl.through_rep) pl.prefix_ctas = 0;
-  }
-  if (pl.prefix_ctas > 0) {
+    // (the parts' room is in the size either way: a workspace for the largest bounds serves smaller ones)
     const int64_t rows = static_cast<int64_t>(batch) * d.num_q_heads + static_cast<int64_t>(pl.prefix_ctas) * pl.unit_rows;
     if (rows >= int64_t(1) << 31) return cudaErrorInvalidValue;
     // TMA coordinates are 32-bit: the cache rows must be addressable
-    if (prefix_on_tcgen05(d) && d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (tc && d.num_pages * d.page_size >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     pl.off_costs = pl.ws_bytes;
     pl.off_lse = align_up(pl.off_costs + (static_cast<size_t>(n_groups) + 2) * 8, 256);
     pl.off_o = align_up(pl.off_lse + static_cast<size_t>(rows) * 4, 256);
@@ -269,7 +274,7 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   da.max_pages = a.max_pages;
   da.max_context_len = a.max_context_len;
   da.scale = a.scale;
-  if (pl.prefix_ctas == 0 && !pl.through_rep) return launch_decode(d, pl.suffix, da, s);
+  if (pl.prefix_ctas == 0) return launch_decode(d, pl.suffix, da, s);
   const Fns f = get_fns<true>(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
   if (!f.main) return cudaErrorInvalidValue;
   KParams p = decode_params(d, pl.suffix, da, d.num_kv_heads * d.head_dim * elem_bytes(d.dtype));

@@ -260,6 +260,12 @@ PA_DEVINL float ex2_approx(float x) {
   return y;
 }
 
+// The largest log-sum-exp of the parts of a whole warp, M without those that are
+// no numbers (nan): never -inf where there are such, so that they reach the output.
+PA_DEVINL float merge_maximum(float M, bool nan) {
+  return __any_sync(0xffffffffu, nan) && M == -INFINITY ? 0.f : M;
+}
+
 // ---------------------------------------------------------------------------
 // log-sum-exp merge of the partials of requests cut across CTAs.  merge_w
 // warps per (request, q-head): each takes a contiguous range of the partials,
@@ -346,10 +352,16 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
     };
     load(k_begin);
     float M = -INFINITY;
+    [[maybe_unused]] bool nan = false;
     for (int k = lane; k < parts; k += 32)
-      if (busy(c0 + k)) M = fmaxf(M, lse_of(k));
+      if (busy(c0 + k)) {
+        const float x = lse_of(k);
+        M = fmaxf(M, x);
+        nan |= x != x;
+      }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if constexpr (kRange) M = merge_maximum(M, nan);
     if (M != -INFINITY) {
       for (int k0 = k_begin; k0 < k_end; k0 += 8) {
         if (k0 != k_begin) load(k0);

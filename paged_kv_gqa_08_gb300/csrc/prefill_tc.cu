@@ -788,7 +788,7 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
           store_rows_tma(o, inv, stage, p.tm_o, hh_kv * p.G, it_s0 + qt * p.TQ + wq * 32 / p.G, lane, tma_pending);
         else
           store_cols<0>(o, inv, to_part, to_out, p.o_part + prow * 128, dst, p.out32);
-        if (to_part) p.lse_part[prow] = l > 0.f ? m_used + __log2f(l) : -INFINITY;
+        if (to_part) p.lse_part[prow] = (kMode == kCausal ? l > 0.f : l != 0.f) ? m_used + __log2f(l) : -INFINITY;
       } else if (to_part) {
         p.lse_part[prow] = -INFINITY;  // no key tile of this part reaches the q-tile
       }
@@ -853,7 +853,8 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         mbar_arrive(&o_free[0]);
         if (two) mbar_arrive(&o_free[1]);
       }
-      if (to_part) p.lse_part[prow] = lsum > 0.f ? mm + __log2f(lsum) : -INFINITY;
+      if (to_part)
+        p.lse_part[prow] = (kMode == kCausal ? lsum > 0.f : lsum != 0.f) ? mm + __log2f(lsum) : -INFINITY;
       ++ms;
     }
   }

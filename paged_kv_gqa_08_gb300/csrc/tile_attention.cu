@@ -178,7 +178,7 @@ struct TileOut {
       *reinterpret_cast<float2*>(p.out + e * 4) = make_float2(a, b);
   }
   PA_DEVINL void store_lse(int r, float m, float l) const {
-    if constexpr (kPrefix) p.lse_part[row(r)] = l > 0.f ? m + log2f(l) : -INFINITY;
+    if constexpr (kPrefix) p.lse_part[row(r)] = l != 0.f ? m + log2f(l) : -INFINITY;
   }
 };
 

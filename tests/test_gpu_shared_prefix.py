@@ -221,3 +221,19 @@ def test_the_same_bits_every_time(cuda_lib):
     first = c.call(q, 0.1)
     for _ in range(20):
         assert torch.equal(c.call(q, 0.1), first)
+
+
+@pytest.mark.parametrize("dt,hd", [(BF16, 128), (F32, 64)])
+def test_a_workspace_for_the_largest_bounds_serves_smaller_ones(cuda_lib, dt, hd):
+    desc = pa.cache_desc(32, 8, hd, 16, 1000, dt)
+    sizes = [(g, b, p, c) for g in (0, 1, 3, 8, 64) for b in (1, 2, 8, 64) for p in (0, 1, 128, 4000, 40000)
+             for c in (40000, 80000) if g <= b]
+    need = {k: pa.pa_decode_shared_prefix_workspace_size(desc, *k) for k in sizes}
+    for k in sizes:
+        assert 0 < need[k] <= need[(64, 64, 40000, 80000)]
+        assert all(need[k] <= need[m] for m in sizes if all(x <= y for x, y in zip(k, m)))
+    for window, sinks in ((1, 0), (15, 1), (99, 0), (98, 1), (64, 30)):  # at most that of plain decode
+        for b in (1, 3, 100):
+            for mx in (1, 17, 100, 5000):
+                assert (pa.pa_decode_window_workspace_size(desc, window, sinks, b, mx) <=
+                        pa.pa_decode_workspace_size(desc, b, mx))
