@@ -700,11 +700,24 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
       for (int q = 0; q < 4; ++q) tmem_ld32_async(tmem + lane_off + colS + 32 * q, x + 32 * q);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_wait_ld32(x + 32 * q);
-      if (need_mask) {
+      if (kMode == kWindow && need_mask) {
+        // the row's keys of the tile as bits: below its end, and below the sinks'
+        // or not below its window's start (half the instructions of comparing keys)
+        const int end = pos_r + 1 - key0, start = pos_r + 1 - p.window - key0, sinks = p.sinks - key0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          auto below = [&](int n) {
+            return static_cast<uint32_t>((1ull << min(max(n - 32 * q, 0), 32)) - 1);
+          };
+          const uint32_t bits = below(end) & (~below(start) | below(sinks));
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((bits >> e) & 1)) x[32 * q + e] = __float_as_uint(-INFINITY);
+        }
+      } else if (need_mask) {
 #pragma unroll
         for (int e = 0; e < 128; ++e)
-          if (key0 + e > pos_r || (kMode == kWindow && key0 + e <= pos_r - p.window && key0 + e >= p.sinks))
-            x[e] = __float_as_uint(-INFINITY);
+          if (key0 + e > pos_r) x[e] = __float_as_uint(-INFINITY);
       }
       float mx;
       {
