@@ -28,11 +28,11 @@
 //
 // Two more modes of the same kernel:
 //   kWindow  a row sees the keys j of (its position - window, its position] and
-//            the first `sinks`.  A pair's key tiles leave out those between the
-//            sinks and its first row's window; the rows at the ends of that gap
-//            which no row of the pair sees are not copied (single-row boxes where
-//            a 16-row box is cut) and zero; inside a tile the scores outside a
-//            row's own window are masked.  A window bounds a pair's tiles, so that
+//            the first `sinks`.  A pair's key tiles leave out the 16-row
+//            boxes between the sinks and its first row's window and close up; the
+//            rows at the ends of that gap which no row of the pair sees are not
+//            copied (single-row boxes where a box is cut) and zero; inside a tile
+//            the scores outside a row's own window are masked.  A window bounds a pair's tiles, so that
 //            most batches run unplanned (the rule at launch_tc, with both sides'
 //            times).  8 x 2048 new tokens, window 2048, 16 / 8 heads: 252 us, 1100
 //            TFLOP/s of the pairs that are seen (18 tiles a pair for 2064 keys a row).
@@ -304,31 +304,36 @@ struct Item {
   int32_t rows[2];  // live tokens of that q-tile
   int32_t pos0[2];  // position of its first token
   int32_t kv_len;   // keys the pair needs (last token's position + 1)
-  // kWindow: no row of the pair sees keys [gap_lo, gap_hi); an item's key tiles
-  // count the `skip` tiles from tile `before` on, wholly inside, out
+  // kWindow: no row of the pair sees keys [gap_lo, gap_hi); key tiles are of the
+  // keys with the `skip` ones from key `before` on, wholly inside, left out
   int32_t before, skip, gap_lo, gap_hi;
   int32_t part_row;  // kPrefix: the part's row of the unit's first token
 };
 static_assert(sizeof(Item) == 96, "two items fit their shared-memory slot");
 
 // kWindow: the gap in the keys that a q-tile pair whose first token sits at
-// position p0 sees, and the 128-key tiles wholly inside it.
+// position p0 sees (and keys from `end` on, no more), and the 16-row boxes wholly
+// inside it (as keys): what is left closes up, so that the sinks may share a tile
+// with the window's first keys.  Of the boxes that would only have lengthened the
+// last tile's empty end, the gap keeps as many: an end at a tile's own leaves fewer
+// tiles to mask (8 x 2048 tokens, window 2048: 242 us, all left out 252).
 struct Gap {
   int lo, hi, before, skip;
 };
-PA_DEVINL Gap window_gap(int p0, int window, int sinks) {
+PA_DEVINL Gap window_gap(int p0, int end, int window, int sinks) {
   Gap g;
   g.hi = max(0, p0 - window + 1);
   g.lo = min(sinks, g.hi);
-  g.before = (g.lo + kBN - 1) / kBN;
-  g.skip = max(0, g.hi / kBN - g.before);
+  g.before = (g.lo + kBoxRows - 1) / kBoxRows * kBoxRows;
+  g.skip = max(0, g.hi / kBoxRows * kBoxRows - g.before);
+  g.skip = max(0, g.skip - (kBN - 1 - (end - g.skip + kBN - 1) % kBN) / kBoxRows * kBoxRows);
   return g;
 }
 
-// The key tile that an item's tile j is.
+// The key that is key v of an item's tiles.
 template <Mode kMode>
-PA_DEVINL int key_tile(const Item& it, int j) {
-  return kMode == kWindow && j >= it.before ? j + it.skip : j;
+PA_DEVINL int key_of(const Item& it, int v) {
+  return kMode == kWindow && v >= it.before ? v + it.skip : v;
 }
 
 // Row 0 .. 15 of the 16-row box at key k0 that some row of the pair sees, as bits.
@@ -363,14 +368,14 @@ PA_DEVINL bool make_item(const TcParams& p, int b, int qp, int h, int j_lo, int 
   }
   it.before = it.skip = it.gap_lo = it.gap_hi = it.part_row = 0;
   if constexpr (kMode == kWindow) {
-    const Gap gap = window_gap(pos0[0], p.window, p.sinks);
+    const Gap gap = window_gap(pos0[0], pos0[nq - 1] + rows[nq - 1], p.window, p.sinks);
     it.before = gap.before;
     it.skip = gap.skip;
     it.gap_lo = gap.lo;
     it.gap_hi = gap.hi;
 #pragma unroll
     for (int g = 0; g < 2; ++g)
-      if (g < nq) ntg[g] -= gap.skip;
+      if (g < nq) ntg[g] = (pos0[g] + rows[g] - gap.skip + kBN - 1) / kBN;
   }
   j_hi = min(j_hi, ntg[nq - 1]);
   const int nt = j_hi - j_lo;
@@ -675,7 +680,7 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
     const bool live = row < p.TQ * p.G && t_r < (g ? it.rows[1] : it.rows[0]);
     const int j_lo = it.j_lo, split = it.split, slot = it.slot, hh_kv = it.h;
     const int it_qp = it.qp, it_s0 = it.s0;
-    [[maybe_unused]] const int before = it.before, skip = it.skip, part_row = it.part_row;
+    [[maybe_unused]] const int skip = it.skip, part_row = it.part_row;
     float m_used = -INFINITY, l = 0.f;
     for (int s = 0; s < c; ++s) {
       ok = mbar_wait_bounded(&s_full[g], sc & 1, abort_flag, p.err);
@@ -685,12 +690,14 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         break;
       }
       tc_fence_after();
-      int tile = j_lo + (split ? 2 * s + g : s);
-      if (kMode == kWindow && tile >= before) tile += skip;
-      const int key0 = tile * kBN;
+      // the tile's first key; kWindow: without the keys that the tiles leave out,
+      // like the rows' positions here (a sink lies before those, a window's key after)
+      const int key0 = (j_lo + (split ? 2 * s + g : s)) * kBN;
       // (kWindow: the last row's window may start behind the tile's first key)
-      const bool need_mask = key0 + kBN - 1 > p0 ||
-                             (kMode == kWindow && key0 <= p0 + p.TQ - 1 - p.window && key0 + kBN > p.sinks);
+      const bool need_mask = kMode == kWindow
+                                 ? key0 + kBN - 1 > p0 - skip ||
+                                       (key0 <= p0 + p.TQ - 1 - p.window - skip && key0 + kBN > p.sinks)
+                                 : key0 + kBN - 1 > p0;
       // One TMEM round trip per tile: all 128 scores of the row are loaded
       // (four loads, one wait), the row max is taken over the raw scores (the
       // scale is positive, so it commutes with the max) with eight independent
@@ -703,7 +710,7 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
       if (kMode == kWindow && need_mask) {
         // the row's keys of the tile as bits: below its end, and below the sinks'
         // or not below its window's start (half the instructions of comparing keys)
-        const int end = pos_r + 1 - key0, start = pos_r + 1 - p.window - key0, sinks = p.sinks - key0;
+        const int end = pos_r + 1 - skip - key0, start = max(end, 0) - p.window, sinks = p.sinks - key0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           auto below = [&](int n) {
@@ -1128,9 +1135,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       // box, lanes 0-3 the page of a ragged end.
       // (kWindow: of its box, whichever of the box's rows are seen.)
       auto load_pages = [&](int t, int& pg_full, int& pg_rem) {
-        const int t0 = key_tile<kMode>(it, it.j_lo + t) * kBN;
+        const int t0 = (it.j_lo + t) * kBN;
         if constexpr (kMode == kWindow) {
-          const int k0 = t0 + box * kBoxRows;
+          const int k0 = key_of<kMode>(it, t0 + box * kBoxRows);
           pg_full = seen_rows(it, k0) ? p.bt[bt_row + (k0 >> p.log2P)] : kNoPage;
           pg_rem = kNoPage;
           return;
@@ -1166,13 +1173,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         const int pf = pf_next, pr = pr_next;
         if (t + 1 < it.nt) load_pages(t + 1, pf_next, pr_next);  // one tile ahead
         const int st = kc & 1;
-        const int t0 = key_tile<kMode>(it, it.j_lo + t) * kBN;
+        const int t0 = (it.j_lo + t) * kBN;
         const int valid = min(kBN, it.kv_len - t0);
         const int nfull = valid / kBoxRows, rem = valid % kBoxRows;
-        const uint32_t seen = kMode == kWindow ? seen_rows(it, t0 + box * kBoxRows) : 0xffffu;
+        const int k_box = key_of<kMode>(it, t0 + box * kBoxRows);
+        const uint32_t seen = kMode == kWindow ? seen_rows(it, k_box) : 0xffffu;
         int y_full = -1, y_rem = -1;
         if (pf != kNoPage) {
-          if (pf >= 0 && pf < p.num_pages) y_full = (pf << p.log2P) + ((t0 + box * kBoxRows) & (p.P - 1));
+          if (pf >= 0 && pf < p.num_pages) y_full = (pf << p.log2P) + (k_box & (p.P - 1));
           else raise_flag(p.err, PA_DEVERR_BAD_PAGE);
         }
         if (pr != kNoPage) {
@@ -1194,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           // the rows that no query sees are not copied, and zero where they meet a probability of 0
           if (vrole && __any_sync(0xffffffffu, seen != 0xffffu)) {
             for (int c = lane; c < kBN * 16; c += 32) {
-              const int r = c >> 4, ch = c & 15, key = t0 + r;
+              const int r = c >> 4, ch = c & 15, key = key_of<kMode>(it, t0 + r);
               if (key >= it.kv_len || (key >= it.gap_lo && key < it.gap_hi))
                 *reinterpret_cast<uint4*>(stage + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
@@ -1556,8 +1564,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PlanPa
                                                static_cast<unsigned long long>(kMaxKvBlocks - 1)))
                         : 0;
     for (int k = 0; k < np; ++k) {
-      int nt = (L - n + min((2 * k + 2) * q.TQ, n) + kBN - 1) / kBN;
-      if constexpr (kMode == kWindow) nt -= window_gap(L - n + 2 * k * q.TQ, q.window, q.sinks).skip;
+      int end = L - n + min((2 * k + 2) * q.TQ, n);
+      if constexpr (kMode == kWindow) end -= window_gap(L - n + 2 * k * q.TQ, end, q.window, q.sinks).skip;
+      const int nt = (end + kBN - 1) / kBN;
       const int4 pr = make_int4(b, k, nt, ((2 * k + 1) * q.TQ < n ? 2 : 1) | (blk << 8));
       if (off + k < static_cast<unsigned long long>(q.pair_cap)) q.pairs[off + k] = pr;
       if (off + k < kPlanSmemPairs) sh_pairs[off + k] = pr;
@@ -2036,9 +2045,10 @@ cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t
     //   512, 2048, 40/8 (T 19, 0.58)  55.8  42.3     512, 8192, 40/8 (T 67, 0.58)  110.0 117.2
     //   2048, 8192, 16/8 (T 67, 0.84) 128.7 114.0    2048, 8192, 40/8 (T 67, 2.16) 322.0 348.0
     //   2048, 512, 40/8 (T 7, 2.16)    85.0  68.2    8192, 64, 40/8 (T 3, w 8.6)   122.5 148.5
-    const int64_t reach = static_cast<int64_t>(2 * TQ) + a.window + kBN - 2;  // keys of a pair's rows, unaligned
-    const int64_t T = std::min<int64_t>((static_cast<int64_t>(a.max_context_len) + kBN - 1) / kBN,
-                                        reach / kBN + 1 + (static_cast<int64_t>(a.sinks) + kBN - 1) / kBN);
+    // (the keys that a pair's rows see, in whole boxes at the gap's ends)
+    const int64_t reach = std::min<int64_t>(
+        a.max_context_len, static_cast<int64_t>(2 * TQ) + a.window + a.sinks + 2 * (kBoxRows - 1));
+    const int64_t T = (reach + kBN - 1) / kBN;
     const int64_t qp = ((a.max_seqlen_q + TQ - 1) / TQ + 1) / 2;
     const int64_t pairs = std::min<int64_t>(a.batch * qp, a.num_tokens / (2 * TQ) + a.batch);
     DeviceInfo di;
