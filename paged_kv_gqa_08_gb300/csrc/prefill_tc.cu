@@ -32,10 +32,12 @@
 //            boxes between the sinks and its first row's window and close up; the
 //            rows at the ends of that gap which no row of the pair sees are not
 //            copied (single-row boxes where a box is cut) and zero; inside a tile
-//            the scores outside a row's own window are masked.  A window bounds a pair's tiles, so that
-//            most batches run unplanned (the rule at launch_tc, with both sides'
-//            times).  8 x 2048 new tokens, window 2048, 16 / 8 heads: 252 us, 1100
-//            TFLOP/s of the pairs that are seen (18 tiles a pair for 2064 keys a row).
+//            the scores outside a row's own window are masked.  A window bounds a
+//            pair's tiles, so that most batches run unplanned (the rule at
+//            launch_tc, with both sides' times): a CTA that ends takes over a block
+//            that has not started.  8 x 2048 new tokens, window 2048, 16 / 8 heads:
+//            235 us, 1180 TFLOP/s of the pairs that are seen (18 tiles a pair for
+//            2064 keys a row).
 //   kPrefix  the rows are the queries of a group of decode requests, all of which
 //            see the same keys.  Each CTA has a share of the tiles of all groups
 //            (prefix_plan.cuh), which its scheduler warp finds beside the setup;
@@ -112,15 +114,16 @@ constexpr int kOffK = kOffQ + 2 * kTileBytes;     // two K stages
 constexpr int kOffV = kOffK + 2 * kTileBytes;     // two V stages
 constexpr int kStageBytes = 32 * 128;             // a softmax warp's 32 rows x 128 bytes on their way out
 constexpr int kOffStage = kOffV + 2 * kTileBytes; // eight softmax warps' output staging (1024-aligned)
-constexpr int kOffBar = kOffStage + 8 * kStageBytes;  // 26 mbarriers
+constexpr int kOffBar = kOffStage + 8 * kStageBytes;  // 27 mbarriers
 // indices of the mbarriers in their table (pairs are [2], one per stage or group)
 constexpr int kBarItemFull = 0, kBarItemEmpty = 2, kBarQFull = 4, kBarQEmpty = 5, kBarKFull = 6, kBarKEmpty = 8,
               kBarVFull = 10, kBarVEmpty = 12, kBarSFull = 14, kBarPFull = 16, kBarPvDone = 18, kBarOFree = 20,
-              kBarMlFull = 22, kBarMlEmpty = 23, kBarMmaDone = 24, kBarSchedGo = 25;
+              kBarMlFull = 22, kBarMlEmpty = 23, kBarMmaDone = 24, kBarSchedGo = 25, kBarTaken = 26;
 constexpr int kOffItem = kOffBar + 256;           // two work items
 constexpr int kOffMl = kOffItem + 256;            // 128 (max, sum) rows handed between the softmax groups
 constexpr int kOffMisc = kOffMl + 128 * 8;        // TMEM base address, abort flag
-constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + slack to align the base to 1024
+constexpr int kOffTaken = kOffMisc + 16;          // kWindow: the answer to a request for another CTA's block
+constexpr int kSmemBytes = kOffTaken + 16 + 1024;  // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "within the 227 KB a CTA may use");
 static_assert(kOffStage % 1024 == 0, "128-byte-swizzled staging starts on a 1024-byte boundary");
 
@@ -201,6 +204,34 @@ PA_DEVINL void tma_prefetch_map(const CUtensorMap* tm) {
 PA_DEVINL void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 PA_DEVINL void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 PA_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Asks for a block of the grid that has not started yet, to run it in this CTA
+// (the hardware then does not launch it): 16 bytes in shared memory, counted on an
+// mbarrier.  After an answer of "none left" no more may be asked.
+PA_DEVINL void ask_block(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The block that was given, or false when none is left.
+PA_DEVINL bool given_block(const void* answer, int3& block) {
+  uint32_t ok, x, y, z;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "ld.shared.b128 a, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, a;\n\t}"
+      : "=&r"(ok), "=&r"(x), "=&r"(y), "=&r"(z)
+      : "r"(smem_u32(answer))
+      : "memory");
+  block = make_int3(static_cast<int>(x), static_cast<int>(y), static_cast<int>(z));
+  return ok != 0;
+}
 
 PA_DEVINL void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -968,6 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     mbar_init(ml_empty, 4);
     mbar_init(mma_done, 1);
     mbar_init(sched_go, 1);
+    mbar_init(bars + kBarTaken, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -1029,11 +1061,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     // ------------------------------- work scheduler -------------------------------
     // Planned launch: items k = unit * Hkv + kv-head are taken from a shared
     // counter, so a CTA that finishes early takes the next one (the units are
-    // listed longest first).  Otherwise the CTA's own pair is its one item.
+    // listed longest first).  Otherwise the CTA's own pair is its one item;
+    // kWindow: its first, then those of CTAs that have not started, so that the next
+    // pair's copies and products begin under this one's end and no further CTA
+    // sets up.  8 x 2048 new tokens, window 64: 64 us for 70 planned.
     if (lane == 0) {
       if (p.units) pdl_wait();  // the planner's unit list and counter are ready
       const int total = p.units ? *p.n_units * p.Hkv : 1;
       int pub = 0, k_own = 0;
+      [[maybe_unused]] int3 block = make_int3(blockIdx.x, blockIdx.y, blockIdx.z);
+      [[maybe_unused]] unsigned char* taken = smem + kOffTaken;
+      [[maybe_unused]] int asked = -1;  // blocks asked for (the first is the CTA's own)
       for (;;) {
         Item it;
         it.valid = 0;
@@ -1060,6 +1098,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           if (pub > 0) has_work = next_prefix_work(p.prefix, share, work);
           last = !has_work;
           if (!last) make_prefix_item(p, work, blockIdx.x, it);
+        } else if (kMode == kWindow && !p.units) {
+          last = false;
+          if (++asked > 0) {
+            mbar_arrive_expect_tx(bars + kBarTaken, 16);
+            ask_block(taken, bars + kBarTaken);
+            if (!mbar_wait_bounded(bars + kBarTaken, (asked - 1) & 1, abort_flag, p.err)) {
+              drain(bars + kBarTaken, (asked - 1) & 1);  // the answer may still be landing
+              break;
+            }
+            last = !given_block(taken, block);
+            fence_async_smem();  // the answer is read before the next one is written
+          }
         } else {
           k = p.units ? atomicAdd(p.counter, 1) : k_own++;
           last = k >= total;
@@ -1076,9 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             jh = static_cast<int>(static_cast<uint32_t>(ud.z) >> 16);
             sl = ud.w;
           } else {
-            b = blockIdx.z;
-            h = blockIdx.y;
-            qp = blockIdx.x;
+            b = kMode == kWindow ? block.z : blockIdx.z;
+            h = kMode == kWindow ? block.y : blockIdx.y;
+            qp = kMode == kWindow ? block.x : blockIdx.x;
             jl = 0;
             jh = 1 << 30;
             sl = -1;
@@ -2038,13 +2088,17 @@ cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t
   bool planned = a.workspace != nullptr;
   if (kMode == kWindow && planned) {
     // A window bounds a pair's key tiles T, and with them what splitting can gain:
-    // while the pairs fill w <= 4 waves of CTAs, the last of them T (ceil(w) - w) of a
-    // tile's time; planner and merge cost about 12 tiles' (20 where they overlap
-    // other waves).  Measured, us (planned, unplanned; new tokens, window, q- / kv-heads):
-    //   33, 64, 16/8 (T 4, w 0.05)    22.2  13.5     128, 2048, 16/8 (T 19, w 0.05)  30.4  38.4
-    //   512, 2048, 40/8 (T 19, 0.58)  55.8  42.3     512, 8192, 40/8 (T 67, 0.58)  110.0 117.2
-    //   2048, 8192, 16/8 (T 67, 0.84) 128.7 114.0    2048, 8192, 40/8 (T 67, 2.16) 322.0 348.0
-    //   2048, 512, 40/8 (T 7, 2.16)    85.0  68.2    8192, 64, 40/8 (T 3, w 8.6)   122.5 148.5
+    // while the pairs fill w <= 1.5 waves of CTAs, the last of them T (ceil(w) - w) of a
+    // tile's time; planner and merge cost about 12 tiles' (20 where they overlap other
+    // waves).  In more waves the CTAs take each other's blocks and whole pairs balance
+    // well, unless a CTA meets many blocks without rows (e, about 1 us each).  Measured,
+    // us (planned, unplanned; requests x new tokens, window, q- / kv-heads):
+    //   1 x 33, 64, 16/8 (T 4, w 0.05)        22.2  13.5     8 x 2048, 64, 16/8 (w 6.7)   70.2  64.4
+    //   1 x 512, 2048, 16/8 (T 18, w 0.21)    32.5  38.0     8 x 2048, 2048, 16/8 (w 6.7)  245   238
+    //   1 x 512, 8192, 40/8 (T 66, w 0.58)     109   115     1 x 8192, 512, 40/8 (w 8.6)   144   130
+    //   8 x 1..512, 8192, 16/8 (T 66, w 1.26)  169   195     1 x 8192, 8192, 16/8 (w 3.4)  468   440
+    //   1 x 8192, 8192, 8/1 (T 66, w 1.68)     298   220     8 x 2048, 8192, 16/8 (w 6.7)  784   802
+    //   8 x 512, 8192, 16/8 (T 66, w 1.68)     245   228     32 x 1..512, 512, 40/8 (w 11, e 7.6)  163  174
     // (the keys that a pair's rows see, in whole boxes at the gap's ends)
     const int64_t reach = std::min<int64_t>(
         a.max_context_len, static_cast<int64_t>(2 * TQ) + a.window + a.sinks + 2 * (kBoxRows - 1));
@@ -2054,7 +2108,8 @@ cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t
     DeviceInfo di;
     if ((e = current_device_info(&di)) != cudaSuccess) return e;
     const double w = static_cast<double>(pairs * d.num_kv_heads) / di.sm_count;
-    if (w <= 4 && T * (ceil(w) - w) <= (w <= 1 ? 12 : 20) && a.batch <= 65535) planned = false;
+    const double e_sm = static_cast<double>((a.batch * qp - pairs) * d.num_kv_heads) / di.sm_count;
+    planned = a.batch > 65535 || e_sm > 4 || (w <= 1.5 && T * (ceil(w) - w) > (w <= 1 ? 12 : 20));
   }
   if (!planned) {
     const int qtiles = (a.max_seqlen_q + TQ - 1) / TQ;
