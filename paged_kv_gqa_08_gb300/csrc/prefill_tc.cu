@@ -768,7 +768,9 @@ __device__ __noinline__ void softmax_role(const SoftmaxArgs p, unsigned char* sm
         for (int e = 0; e < 4; ++e) m8[e] = fmaxf(m8[e], m8[e + 4]);
         mx = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])) * p.scale_log2;
       }
-      if (__any_sync(0xffffffffu, mx > m_used + 8.f)) {
+      // (Not kCausal: rows that hold no token have scores with what the stages held
+      // before; they have no say, so that a row's result does not depend on those.)
+      if (__any_sync(0xffffffffu, (kMode == kCausal || live) && mx > m_used + 8.f)) {
         const float m_new = fmaxf(m_used, mx);
         const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
         if (s > 0) {

@@ -195,3 +195,39 @@ def test_graph_and_stream(cuda_lib):
     compare(c, new, q, out, window, sinks, 0.1)
     assert torch.isnan(out[350:].float()).all()
     assert pa.pa_read_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("B,new,Hq,Hkv", [(24, 1300, 10, 2), (90, 2300, 16, 8), (300, 70, 8, 8)])
+def test_many_blocks_without_rows(cuda_lib, B, new, Hq, Hkv):
+    """A few long chunks between requests of one token: most of a grid has no rows, the rest fills several waves of
+    CTAs, with and without a plan, on two streams at once and replayed."""
+    r = random.Random(B)
+    news = [new if b % 11 == 3 else r.choice([1, 1, 2, 40]) for b in range(B)]
+    lens = [n + r.randint(0, 400) for n in news]
+    lens[5] = 0
+    c = Paged(lens, Hq, Hkv, 128, 16, BF16, seed=B)
+    q = c.randn(sum(news), Hq, 128)
+    run(c, news, q, 90, 5)
+    want = prefill(c, news, q, 90, 5, 0.088, False)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(prefill(c, news, q, 90, 5, 0.088, False))
+    torch.cuda.synchronize()
+    cu = torch.tensor([0] + list(torch.tensor(news).cumsum(0)), dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, NAN)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pa.pa_prefill_varlen_window(c.desc, 90, 5, q, cu, B, max(news), sum(news), c.k, c.v, c.bt, c.maxp, c.ctx,
+                                    max(lens), 0.088, out)
+    for _ in range(3):
+        out.fill_(NAN)
+        g.replay()
+        torch.cuda.synchronize()
+        outs.append(out.clone())
+    for o in outs:
+        assert torch.equal(o.view(torch.uint8), want.view(torch.uint8))
+    assert pa.pa_read_device_errors(reset=True) == 0
