@@ -1,6 +1,6 @@
 // How the attention of decode requests to prefixes that they share is cut over
 // the CTAs of one launch, for the kernels that compute it (prefill_tc.cu,
-// shared_prefix.cu) and the merge.
+// tile_attention.cu) and the merge.
 //
 // Group g is requests cu[g] .. cu[g+1]-1, whose first pre[g] keys are the same.
 // For every kv-head its queries are n * G rows (n requests, G q-heads), cut into
