@@ -113,3 +113,32 @@ def test_hundreds_of_thousands_of_keys(cuda_lib, dt, Hq, Hkv, hd):
     out = prefill(w, [1, 1], q, 200003, 77, 0.1, False)
     compare(w, 200003, 77, q, out, 0.1)
     assert pa.pa_read_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("dt,hd", [(BF16, 128), (BF16, 64), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("G", [1, 3, 4, 5])
+def test_results_repeat_whatever_ran_before(cuda_lib, dt, hd, G):
+    """The same bits again after calls that leave huge values, infinities and NaN in every SM's memory."""
+    Hkv, Hq = 2, 2 * G
+    own, new, window, sinks = [1, 40, 200, 7, 90], [70, 1, 129, 300, 20], 100, 5
+    c = Paged([400, 130, 600, 300, 333], Hq, Hkv, hd, 16, dt, seed=G)
+    q = c.randn(sum(new), Hq, hd)
+    g = [Groups([(777, own), (130, own[:3])], Hq, Hkv, hd, 16, dt, G, wide) for wide in (False, True)]
+    gq = c.randn(8, Hq, hd)
+    w = Paged([900] * 40, Hq, Hkv, hd, 16, dt, seed=9)  # as many pairs and requests as reach all SMs
+    bad = [x.clone() for x in (w.k, w.v)]
+
+    def calls():
+        return [prefill(c, new, q, window, sinks, 0.1, plan) for plan in (False, True)] + \
+            [x.call(gq, 0.1) for x in g] + [decode(c, window, sinks, q[:5], 0.1)]
+
+    want = calls()
+    for value in (3e4, -3e4, INF, NAN):
+        for x in bad:
+            x.fill_(value)
+        w.k, w.v = bad
+        for n in (1, 200):
+            prefill(w, [n] * 40, torch.full((40 * n, Hq, hd), value, dtype=dt, device="cuda"), 512, 0, 0.1, False)
+        for i, (a, b) in enumerate(zip(calls(), want)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), f"call {i} after {value}"
+    assert pa.pa_read_device_errors(reset=True) == 0
