@@ -348,11 +348,12 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
           }
         }
       } else {
-        // (for 2, 4 or 8 rows, so that few rows cost little and the sums stay in registers)
+        // (for 2, 4 or 8 rows, so that few rows cost little and the sums stay in registers; those past
+        // nr are the next warps', worked out here under this warp's mask and kept apart from theirs)
         auto tile_rows = [&](auto rows_c) {
           constexpr int NR = decltype(rows_c)::value;
           const float* qs = reinterpret_cast<const float*>(smem + Gm::kOffQ) + row0 * HD;
-          float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + row0 * kTileKeys;
+          float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + warp * Gm::kWarpRows * kTileKeys;
           const float* kf = reinterpret_cast<const float*>(smem + (kst - smem0));
           const float* vf = reinterpret_cast<const float*>(smem + (vst - smem0));
           float2 acc[NR][2];
