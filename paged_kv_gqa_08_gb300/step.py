@@ -224,7 +224,7 @@ def _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block
         return nbytes
 
     _check_attention(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q,
-                     q_norm_w is not None, need, positive_scale=groups > 0)
+                     q_norm_w is not None, need, positive_scale=cu_groups is not None)
     qa = _write_step(desc, bufs, q, k, v, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache,
                      max_pages_per_seq, q_norm_w, k_norm_w, eps, rope_theta, stream)
     if kind != "decode":
