@@ -331,9 +331,9 @@ def pa_q4_row_bytes(desc, group_size) -> int:
     return int(load_library().pa_q4_row_bytes(desc, group_size))
 
 
-def _q4_caches(fn, desc, group_size, k_cache, v_cache):
-    """A 4-bit cache given as a tensor is contiguous uint8 on the current device and holds every row of the
-    descriptor: a cache of the dtype's rows, or one allocated for another group size, is refused here."""
+def _q4_cache_shapes(fn, desc, group_size, k_cache, v_cache):
+    """A 4-bit cache given as a tensor is contiguous uint8 and holds every row of the descriptor: a cache of the dtype's
+    rows, or one allocated for another group size, is refused here."""
     need = desc.num_pages * desc.page_size * load_library().pa_q4_row_bytes(desc, group_size)
     for t in (k_cache, v_cache):
         if not isinstance(t, torch.Tensor):
@@ -342,7 +342,14 @@ def _q4_caches(fn, desc, group_size, k_cache, v_cache):
             raise PagedAttnError(fn, PA_ERR_DTYPE, f"a 4-bit cache is a uint8 tensor, not {t.dtype}")
         if t.numel() < need or not t.is_contiguous():
             raise PagedAttnError(fn, PA_ERR_SHAPE, f"a 4-bit cache is contiguous and has at least {need} bytes")
-        if (_current_device is None and not _find_cuda()) or t.get_device() != _current_device():
+
+
+def _q4_caches(fn, desc, group_size, k_cache, v_cache):
+    """Those checks, and that a cache given as a tensor is on the current device."""
+    _q4_cache_shapes(fn, desc, group_size, k_cache, v_cache)
+    for t in (k_cache, v_cache):
+        if isinstance(t, torch.Tensor) and ((_current_device is None and not _find_cuda()) or
+                                            t.get_device() != _current_device()):
             raise PagedAttnError(fn, PA_ERR_UNSUPPORTED, f"the cache is on {t.device}, not on the current CUDA device")
 
 

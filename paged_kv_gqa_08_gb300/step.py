@@ -22,8 +22,8 @@ from typing import Optional
 
 import torch
 
-from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PagedAttnError, cache_desc,
-               pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_shared_prefix,
+from . import (PA_ERR_ALIGN, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PagedAttnError, _at,
+               _q4_cache_shapes, cache_desc, pa_decode, pa_decode_q4, pa_decode_q4_workspace_size, pa_decode_shared_prefix,
                pa_decode_shared_prefix_workspace_size, pa_decode_window, pa_decode_window_workspace_size,
                pa_decode_workspace_size, pa_kv_read_q4, pa_kv_read_q4_tables, pa_kv_write, pa_kv_write_q4,
                pa_prefill_qk_norm_rope_kv_write, pa_prefill_qk_norm_rope_kv_write_q4, pa_prefill_step,
@@ -209,6 +209,8 @@ def _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block
         if groups < 0 or prefix_lens.shape[0] < groups or not 0 <= max_prefix_len <= max_context_len:
             _refuse(PA_ERR_SHAPE, "cu_groups, prefix_lens or max_prefix_len out of range")
     _check_queries(desc, q, q_norm_w, k_norm_w)
+    if q_norm_w is None:
+        _check_rows(desc, bufs, n, k, v, k_cache, v_cache)
 
     def need():
         if not (n and batch):
@@ -255,12 +257,32 @@ def _check_queries(desc, q, q_norm_w, k_norm_w):
         _refuse(PA_ERR_SHAPE, "without norm weights attention reads q itself, so its rows must be packed")
 
 
-def _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
-                   k_norm_w):
+def _check_rows(desc, bufs, n, k, v, k_cache, v_cache):
+    """What the write of a step's rows as they are (no norm weights) refuses, once their slots are enqueued."""
+    if not n:
+        return
+    if not all(map(_at, (k, v, k_cache, v_cache))):
+        _refuse(PA_ERR_NULL, "k, v or a cache is missing")
+    if min(k.stride(0), v.stride(0)) < desc.num_kv_heads * desc.head_dim:
+        _refuse(PA_ERR_SHAPE, "the rows of k or v overlap")
+    size = torch_dtype(desc).itemsize
+    if any(t.stride(0) * size % 16 for t in (k, v)) or any(_at(t) % 16 for t in (k, v, k_cache, v_cache)):
+        _refuse(PA_ERR_ALIGN, "k, v, the stride of their rows or a cache is not 16-byte aligned")
+    if bufs.group_size:
+        _q4_cache_shapes("run_step", desc, bufs.group_size, k_cache, v_cache)
+        for t in (k_cache, v_cache):
+            if isinstance(t, torch.Tensor) and t.device != bufs.slots.device:
+                _refuse(PA_ERR_UNSUPPORTED, f"a cache on {t.device}, buffers on {bufs.slots.device}")
+
+
+def _check_step_q4(desc, kind, bufs, q, k, v, k_cache, v_cache, batch, scale, max_pages_per_seq, max_context_len,
+                   max_seqlen_q, q_norm_w, k_norm_w):
     """What the attention of a step over a 4-bit cache would refuse once the step's rows are written: refused before
-    anything is enqueued (the write's own checks come first in its call)."""
+    anything is enqueued (with norm weights the write's own checks come first in its call)."""
     n = q.shape[0]
     _check_queries(desc, q, q_norm_w, k_norm_w)
+    if q_norm_w is None:
+        _check_rows(desc, bufs, n, k, v, k_cache, v_cache)
 
     def need():
         if kind == "decode":
@@ -306,8 +328,8 @@ def _run_step_q4(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block_ta
     """The step over a 4-bit cache.  What is skipped and flagged (``pa_read_device_errors``) is as over other caches: the
     staging cache's block tables have no page where the 4-bit cache's name none of it."""
     n, batch, gs = q.shape[0], context_lens.shape[0], bufs.group_size
-    _check_step_q4(desc, kind, bufs, q, batch, scale, max_pages_per_seq, max_context_len, max_seqlen_q, q_norm_w,
-                   k_norm_w)
+    _check_step_q4(desc, kind, bufs, q, k, v, k_cache, v_cache, batch, scale, max_pages_per_seq, max_context_len,
+                   max_seqlen_q, q_norm_w, k_norm_w)
     if q_norm_w is not None:
         pa_prefill_qk_norm_rope_kv_write_q4(desc, gs, q, q.stride(0), k, k.stride(0), v, v.stride(0), n,
                                             cu_seqlens_q, batch, context_lens, block_tables, max_pages_per_seq,
