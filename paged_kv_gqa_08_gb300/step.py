@@ -199,8 +199,8 @@ def _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block
         _refuse(PA_ERR_UNSUPPORTED, "a 4-bit cache has no windowed and no shared-prefix attention")
     if cu_groups is not None and kind != "decode":
         _refuse(PA_ERR_UNSUPPORTED, "shared prefixes are a decode step's")
-    if window < 0 or (window and num_sinks < 0):
-        _refuse(PA_ERR_SHAPE, "a window is at least 1, the sinks at least 0")
+    if not 0 <= window < 2 ** 31 or (window and not 0 <= num_sinks < 2 ** 31):
+        _refuse(PA_ERR_SHAPE, "a window is at least 1, the sinks at least 0, and both are below 2^31")
     groups = 0
     if cu_groups is not None:
         groups = cu_groups.shape[0] - 1

@@ -64,3 +64,9 @@ def test_caches_that_hold_no_4_bit_rows_are_refused_first(enqueued, kind):  # no
     for bad, status in ((torch.zeros(8, 16, 8, 128, dtype=torch.bfloat16), pa.PA_ERR_DTYPE),
                         (torch.zeros(8 * 16, 544, dtype=torch.uint8), pa.PA_ERR_SHAPE)):
         refused(enqueued, status, q4_args(kind, v_cache=bad))
+
+
+@pytest.mark.parametrize("kind", ["prefill", "decode"])
+@pytest.mark.parametrize("window,sinks", [(1 << 31, 4), ((1 << 32) + 16, 4), (16, 1 << 31), (16, (1 << 32) + 1)])
+def test_windows_beyond_32_bits_are_refused_first(enqueued, kind, window, sinks):  # noqa: F811
+    refused(enqueued, pa.PA_ERR_SHAPE, _step_args(kind, window=window, num_sinks=sinks))
