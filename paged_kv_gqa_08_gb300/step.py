@@ -201,6 +201,9 @@ def _run_step_range(desc, kind, bufs, q, k, v, cu_seqlens_q, context_lens, block
         _refuse(PA_ERR_UNSUPPORTED, "shared prefixes are a decode step's")
     if not 0 <= window < 2 ** 31 or (window and not 0 <= num_sinks < 2 ** 31):
         _refuse(PA_ERR_SHAPE, "a window is at least 1, the sinks at least 0, and both are below 2^31")
+    if (kind != "decode" and n and torch_dtype(desc) is torch.bfloat16 and desc.head_dim == 128
+            and desc.num_pages * desc.page_size >= 2 ** 31):
+        _refuse(PA_ERR_UNSUPPORTED, "prefill in bf16 with head_dim 128 takes a cache of less than 2^31 rows")
     groups = 0
     if cu_groups is not None:
         groups = cu_groups.shape[0] - 1

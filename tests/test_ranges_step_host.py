@@ -70,3 +70,9 @@ def test_caches_that_hold_no_4_bit_rows_are_refused_first(enqueued, kind):  # no
 @pytest.mark.parametrize("window,sinks", [(1 << 31, 4), ((1 << 32) + 16, 4), (16, 1 << 31), (16, (1 << 32) + 1)])
 def test_windows_beyond_32_bits_are_refused_first(enqueued, kind, window, sinks):  # noqa: F811
     refused(enqueued, pa.PA_ERR_SHAPE, _step_args(kind, window=window, num_sinks=sinks))
+
+
+def test_a_prefill_step_over_a_cache_that_its_kernel_does_not_take_is_refused_first(enqueued):  # noqa: F811
+    a = _step_args("prefill", window=16)
+    a["desc"].num_pages = 1 << 27
+    refused(enqueued, pa.PA_ERR_UNSUPPORTED, a)
