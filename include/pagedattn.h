@@ -444,7 +444,8 @@ PA_API pa_status pa_decode_kv_write_window(const pa_cache_desc* desc, int32_t wi
                                            size_t workspace_bytes, pa_stream_t stream);
 
 /* pa_prefill_varlen over the window and the sinks; the workspace's size is
- * pa_prefill_workspace_size. */
+ * pa_prefill_workspace_size.  A chunk of more than max_seqlen_q tokens is skipped
+ * and flagged (PA_DEVERR_BAD_LENGTH), with a workspace or without. */
 PA_API pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t window, int32_t num_sinks,
                                           const void* q, const int32_t* cu_seqlens_q, int32_t batch,
                                           int32_t max_seqlen_q, int64_t num_tokens, const void* k_cache,

@@ -163,7 +163,7 @@ struct TcParams {
   int32_t* counter;  // next item to hand out (zeroed by the planner)
   float* o_part;    // [slot][Hkv][2 q-tiles][128 rows][128]
   float* lse_part;  // [slot][Hkv][2 q-tiles][128 rows]
-  int32_t window, sinks;  // kWindow
+  int32_t window, sinks, max_q;  // kWindow
   PrefixShape prefix;     // kPrefix: the groups, whose parts' rows are laid out as prefix_plan.cuh says
   int64_t* prefix_costs;  // kPrefix: where each group starts on the line, for the merge
 };
@@ -383,7 +383,8 @@ PA_DEVINL bool make_item(const TcParams& p, int b, int qp, int h, int j_lo, int 
   const int L = p.ctx[b];
   if (L == 0 && s0 >= 0 && s1 <= p.num_tokens) return false;  // a padding row
   const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
-  if (s0 < 0 || s1 > p.num_tokens || n < 0 || L < n || L > cap) {
+  // (the planner, too, leaves out chunks beyond the bound that the grid is made for)
+  if (s0 < 0 || s1 > p.num_tokens || n < 0 || (kMode == kWindow && n > p.max_q) || L < n || L > cap) {
     raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
     return false;
   }
@@ -2086,6 +2087,7 @@ cudaError_t launch_tc(const pa_cache_desc& d, const PrefillArgs& a, cudaStream_t
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.window = a.window;
   p.sinks = a.sinks;
+  p.max_q = a.max_seqlen_q;
   if ((e = prepare_kernels<kMode>()) != cudaSuccess) return e;
   bool planned = a.workspace != nullptr;
   if (kMode == kWindow && planned) {

@@ -64,7 +64,7 @@ struct TileParams {
   const int32_t* ctx;
   char* out;
   int64_t num_tokens;
-  int32_t max_ctx, window, sinks, q_tiles;
+  int32_t max_ctx, max_q, window, sinks, q_tiles;
   // shared prefixes
   PrefixShape shape;
   int64_t* costs;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kTileThreads) window_tile_kernel(const TilePar
   const int t0 = (blockIdx.x - b * p.q_tiles) * TQ;
   if (L == 0 && s0 >= 0 && s1 <= p.num_tokens) return;  // a padding row
   const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_ctx), static_cast<int64_t>(p.maxp) << p.log2P));
-  if (s0 < 0 || s1 > p.num_tokens || n < 0 || L < n || L > cap) {
+  if (s0 < 0 || s1 > p.num_tokens || n < 0 || n > p.max_q || L < n || L > cap) {
     if (threadIdx.x == 0) raise_flag(p.err, PA_DEVERR_BAD_LENGTH);
     return;
   }
@@ -566,6 +566,7 @@ cudaError_t launch_window(const pa_cache_desc& d, const PrefillArgs& a, cudaStre
   p.out = static_cast<char*>(a.out);
   p.num_tokens = a.num_tokens;
   p.max_ctx = a.max_context_len;
+  p.max_q = a.max_seqlen_q;
   p.window = a.window;
   p.sinks = a.sinks;
   const int TQ = TileGeom<T, HD>::kRows / p.G;
