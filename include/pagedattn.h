@@ -416,7 +416,10 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
  * query attends to may hold anything, NaN included.  (The values that some
  * query of a prefill chunk attends to must be finite, as in the namesake, where
  * the chunk's later tokens must: its other rows multiply them by 0.)  Lengths,
- * padding rows, flags and refusals are the namesakes'.
+ * padding rows, flags and refusals are the namesakes'.  Where a score of a key that
+ * is attended to is no number, so is the row's result, whatever the bounds; so in
+ * pa_decode_shared_prefix.  (pa_decode and pa_prefill_varlen leave out what a
+ * CTA worked out of such a score where several share a row's keys.)
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace pa_decode_window and pa_decode_kv_write_window need;

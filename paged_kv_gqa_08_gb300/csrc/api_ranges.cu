@@ -47,6 +47,7 @@ DecodeArgs decode_args(const void* q, int32_t batch, const void* k_cache, const 
   a.max_pages = max_pages_per_seq;
   a.max_context_len = max_context_len;
   a.scale = scale;
+  a.keep_nan = true;  // whatever the bounds leave out
   return a;
 }
 

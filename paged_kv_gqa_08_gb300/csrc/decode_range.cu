@@ -279,6 +279,7 @@ cudaError_t launch_shared(const pa_cache_desc& d, const SharedPlan& pl, const Sh
   da.max_pages = a.max_pages;
   da.max_context_len = a.max_context_len;
   da.scale = a.scale;
+  da.keep_nan = true;
   if (pl.prefix_ctas == 0) return launch_decode(d, pl.suffix, da, s);
   const Fns f = get_fns<true>(d.dtype, d.head_dim, d.num_q_heads / d.num_kv_heads);
   if (!f.main) return cudaErrorInvalidValue;

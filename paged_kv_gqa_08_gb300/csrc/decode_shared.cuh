@@ -60,6 +60,10 @@ struct KParams {
   const int32_t* prefix_lens;
   int32_t n_groups, max_prefix, through_rep;
   int32_t per_request;  // a CTA for each request, whole (no merge)
+  // A part whose sum is no number (NaN among its scores) reaches the output: always
+  // in the kRange kernels, and where they would be launched but that the bounds leave
+  // nothing out.  (pa_decode's merge takes such a part for one without keys.)
+  int32_t keep_nan;
 };
 
 // Keys [lo, hi) of a request that a kRange kernel leaves out; hi = -1 when the
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
     };
     load(k_begin);
     float M = -INFINITY;
-    [[maybe_unused]] bool nan = false;
+    bool nan = false;
     for (int k = lane; k < parts; k += 32)
       if (busy(c0 + k)) {
         const float x = lse_of(k);
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
       }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if constexpr (kRange) M = merge_maximum(M, nan);
+    if (kRange || p.keep_nan) M = merge_maximum(M, nan);
     if (M != -INFINITY) {
       for (int k0 = k_begin; k0 < k_end; k0 += 8) {
         if (k0 != k_begin) load(k0);
@@ -542,6 +546,7 @@ inline KParams decode_params(const pa_cache_desc& d, const DecodePlan& pl, const
   p.off_abort = pl.off_abort;
   p.off_cs = pl.off_cs;
   p.per_request = pl.per_request ? 1 : 0;
+  p.keep_nan = a.keep_nan ? 1 : 0;
   p.inline_plan = a.batch <= kInlinePlanMax || pl.per_request ? 1 : 0;
   p.p_row = pl.p_row;
   p.scale_log2 = a.scale * 1.4426950408889634f;
