@@ -482,10 +482,12 @@ PA_API pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t win
  * out of range, is skipped (its output untouched) and flagged
  * PA_DEVERR_BAD_LENGTH; padding rows (context_lens[b] == 0) inside a group are
  * skipped silently.  Keys of a page of the prefix that is out of range are left
- * out or taken as rows of zeros (PA_DEVERR_BAD_PAGE).  Launches: the kernel over
- * the prefixes, the decode kernel over the requests' own tokens (starting as the
- * former's CTAs end) and the merge; where the bounds leave so little to share
- * that this takes longer, the decode kernel over both and its merge.  bf16 with
+ * out (PA_DEVERR_BAD_PAGE); only the tensor-core kernel over the prefixes (bf16,
+ * head_dim 128) takes them as rows of zeros, as in pa_prefill_varlen.  Launches:
+ * the kernel over the prefixes, the decode kernel over the requests' own tokens
+ * (up to 512 requests: starting as the former's CTAs end) and the merge; where the
+ * bounds leave so little to share that this takes longer, the decode kernel over
+ * both and its merge (for every type, keys of such pages left out).  bf16 with
  * head_dim 128 needs num_pages * page_size < 2^31 (else PA_ERR_UNSUPPORTED).
  */
 PA_API pa_status pa_decode_shared_prefix(const pa_cache_desc* desc, int32_t num_groups, const int32_t* cu_groups,
