@@ -419,7 +419,9 @@ PA_API size_t pa_prefill_workspace_size(const pa_cache_desc* desc, int32_t batch
  * padding rows, flags and refusals are the namesakes'.  Where a score of a key that
  * is attended to is no number, so is the row's result, whatever the bounds; so in
  * pa_decode_shared_prefix.  (pa_decode and pa_prefill_varlen leave out what a
- * CTA worked out of such a score where several share a row's keys.)
+ * CTA worked out of such a score where several share a row's keys.)  Both
+ * take contexts of up to 2^31 - 128 tokens; a longer one is skipped and flagged
+ * (PA_DEVERR_BAD_LENGTH).
  * ------------------------------------------------------------------------- */
 
 /* Bytes of device workspace pa_decode_window and pa_decode_kv_write_window need;

@@ -12,6 +12,10 @@ pa_status check_window(int32_t window, int32_t num_sinks) {
   return window < 1 || num_sinks < 0 ? PA_ERR_SHAPE : PA_OK;
 }
 
+// The bound on the contexts that the kernels take: they round lengths up to tiles of
+// up to 128 keys in 32 bits.  (Longer contexts are skipped and flagged.)
+int32_t most_keys(int32_t max_context_len) { return max_context_len < 0x7fffff80 ? max_context_len : 0x7fffff80; }
+
 pa_status check_workspace(const void* workspace) {
   if (!workspace) return PA_ERR_WORKSPACE;
   return (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ? PA_ERR_ALIGN : PA_OK;
@@ -45,7 +49,7 @@ DecodeArgs decode_args(const void* q, int32_t batch, const void* k_cache, const 
   a.workspace = workspace;
   a.batch = batch;
   a.max_pages = max_pages_per_seq;
-  a.max_context_len = max_context_len;
+  a.max_context_len = most_keys(max_context_len);
   a.scale = scale;
   a.keep_nan = true;  // whatever the bounds leave out
   return a;
@@ -63,7 +67,8 @@ size_t pa_decode_window_workspace_size(const pa_cache_desc* desc, int32_t window
   if (check_desc(desc) != PA_OK || check_window(window, num_sinks) != PA_OK) return 0;
   if (batch < 1 || max_context_len < 1 || max_ctas < 0) return 0;
   DecodePlan pl;
-  if (plan_decode_window(*desc, batch, max_context_len, window, num_sinks, max_ctas, &pl) != cudaSuccess) return 0;
+  if (plan_decode_window(*desc, batch, most_keys(max_context_len), window, num_sinks, max_ctas, &pl) != cudaSuccess)
+    return 0;
   return pl.ws_bytes;
 }
 
@@ -124,6 +129,7 @@ pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t window, in
   st = prefill_args(desc, q, cu_seqlens_q, batch, max_seqlen_q, num_tokens, k_cache, v_cache, block_tables,
                     max_pages_per_seq, context_lens, max_context_len, scale, out, workspace, workspace_bytes, &a);
   if (st != PA_OK || a.num_tokens == 0) return st;
+  a.max_context_len = most_keys(max_context_len);
   a.window = window;
   a.sinks = num_sinks;
   if ((st = prepare(&a.err)) != PA_OK) return st;
@@ -175,7 +181,7 @@ pa_status pa_decode_shared_prefix(const pa_cache_desc* desc, int32_t num_groups,
   a.max_prefix = max_prefix_len;
   a.batch = batch;
   a.max_pages = max_pages_per_seq;
-  a.max_context_len = max_context_len;
+  a.max_context_len = most_keys(max_context_len);
   a.scale = scale;
   if ((st = prepare(&a.err)) != PA_OK) return st;
   e = launch_shared(*desc, pl, a, static_cast<cudaStream_t>(stream));

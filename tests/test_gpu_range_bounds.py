@@ -74,3 +74,53 @@ def test_scores_that_are_no_numbers_reach_the_output_whatever_the_bounds(cuda_li
                               dt)
             check(out[b: b + 1], o, bound, f"{name}, request {b}")
     assert pa.pa_read_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("dt,hd", [(BF16, 128), (BF16, 64), (F32, 64), (F32, 128)])
+def test_the_longest_contexts(cuda_lib, dt, hd):
+    """Windows at the end of 2^31 - 128 tokens, whose pages are mostly the same ones; a longer context is skipped."""
+    P, window, sinks, most = 1 << 20, 100, 5, 2 ** 31 - 1
+    lens = [2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1, 2 ** 31 - 200, 300]
+    maxp = 2 ** 31 // P
+    desc = pa.cache_desc(2, 1, hd, P, 3, dt)
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    k, v = (torch.full((3, P, 1, hd), NAN, dtype=dt, device="cuda") for _ in range(2))
+    for x in (k, v):   # the tails of page 1, the heads of pages 0 (the last requests' own) and 2 (everyone's sinks)
+        x[1, -1024:] = torch.randn(1024, 1, hd, generator=g, device="cuda").to(dt)
+        x[0, :1024] = torch.randn(1024, 1, hd, generator=g, device="cuda").to(dt)
+        x[2, :sinks] = torch.randn(sinks, 1, hd, generator=g, device="cuda").to(dt)
+    bt = torch.full((5, maxp), -1, dtype=torch.int32, device="cuda")
+    bt[:, 0], bt[:, -1], bt[4, 0] = 2, 1, 0
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    new = [3, 3, 3, 70, 3]
+    n = sum(new)
+    cu = torch.tensor([0] + list(torch.tensor(new).cumsum(0)), dtype=torch.int32, device="cuda")
+    q = torch.randn(n, 2, hd, generator=g, device="cuda").to(dt)
+
+    def keys(b, x):  # the sinks and the last 300 tokens, with their positions
+        L = lens[b]
+        if L == 300:
+            return x[0, :300], torch.arange(300, device="cuda")
+        j = torch.cat([torch.arange(sinks, device="cuda"), torch.arange(L - 300, L, device="cuda")])
+        return torch.cat([x[2, :sinks], x[1, j[sinks:] % P]]), j
+
+    def compare(b, rows, out, qs):
+        p = torch.arange(lens[b] - rows, lens[b], device="cuda")[:, None]
+        (K, j), V = keys(b, k), keys(b, v)[0]
+        o, bound = attend(qs, K, V, (j <= p) & ((j > p - window) | (j < sinks)), 0.1, dt)
+        check(out, o, bound, f"request {b}")
+
+    out = torch.full_like(q, NAN)
+    pa.pa_prefill_varlen_window(desc, window, sinks, q, cu, 5, 70, n, k, v, bt, maxp, ctx, most, 0.1, out)
+    assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_LENGTH
+    assert torch.isnan(out[3:9].float()).all()
+    for b in (0, 3, 4):
+        compare(b, new[b], out[cu[b]: cu[b + 1]], q[cu[b]: cu[b + 1]])
+    ws = torch.full((pa.pa_decode_window_workspace_size(desc, window, sinks, 5, most),), 255, dtype=torch.uint8,
+                    device="cuda")
+    out = torch.full_like(q[:5], NAN)
+    pa.pa_decode_window(desc, window, sinks, q[:5], 5, k, v, bt, maxp, ctx, most, 0.1, 0, out, ws)
+    assert pa.pa_read_device_errors(reset=True) == pa.PA_DEVERR_BAD_LENGTH
+    assert torch.isnan(out[1:3].float()).all()
+    for b in (0, 3, 4):
+        compare(b, 1, out[b: b + 1], q[b: b + 1])
