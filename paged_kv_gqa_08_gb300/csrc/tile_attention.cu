@@ -13,10 +13,10 @@
 // an online softmax in base 2:
 //   bf16   16 rows a warp, S = Q K^T and O += P V as mma.sync m16n8k16 with fp32
 //          sums, K and V fragments by ldmatrix from swizzled rows.
-//   fp32   up to 8 rows a warp (few rows: a fourth of them each), a lane two keys of the tile for the scores (packed
-//          fp32 pairs) and head_dim / 32 dims for the output: fp32 throughout;
-//          the fp32 pipe is busy 44% of the time with 8 warps an SM, what its
-//          shared memory holds.
+//   fp32   8 rows a warp (4 or 2 where that leaves no row over), a lane two keys of
+//          the tile for the scores (packed fp32 pairs) and head_dim / 32 dims for
+//          the output: fp32 throughout; with 128 dims the fp32 pipe is busy 44% of
+//          the time with 8 warps an SM, what its shared memory holds.
 // Rows that no query sees are zero in shared memory and have probability 0; they
 // are not read, and neither are table entries of pages that hold only such rows.
 // Keys of a page that is out of range are left out.
@@ -188,8 +188,8 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
   using Gm = TileGeom<T, HD>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = smem_u32(smem);
-  // rows of this warp: 16, or (fp32) up to 8, evenly over the warps
-  const int nr = Gm::kMma ? Gm::kWarpRows : (it.rows + 3) >> 2;
+  // rows of this warp: 16, or (fp32) 2, 4 or 8, as many as its loops work on: a row is one warp's
+  const int nr = Gm::kMma ? Gm::kWarpRows : it.rows <= 8 ? 2 : it.rows <= 16 ? 4 : 8;
   const int row0 = warp * nr;
   const bool busy = row0 < it.rows;  // the warp has rows
   const TileOut<T, HD, kPrefix> out{p, it, part_row};
@@ -348,12 +348,11 @@ PA_DEVINL void tile_run(const TileParams& p, const TileItem& it, const TileList&
           }
         }
       } else {
-        // (for 2, 4 or 8 rows, so that few rows cost little and the sums stay in registers; those past
-        // nr are the next warps', worked out here under this warp's mask and kept apart from theirs)
+        // (for 2, 4 or 8 rows, so that few rows cost little and the sums stay in registers)
         auto tile_rows = [&](auto rows_c) {
           constexpr int NR = decltype(rows_c)::value;
           const float* qs = reinterpret_cast<const float*>(smem + Gm::kOffQ) + row0 * HD;
-          float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + warp * Gm::kWarpRows * kTileKeys;
+          float* ps = reinterpret_cast<float*>(smem + Gm::kOffP) + row0 * kTileKeys;
           const float* kf = reinterpret_cast<const float*>(smem + (kst - smem0));
           const float* vf = reinterpret_cast<const float*>(smem + (vst - smem0));
           float2 acc[NR][2];
