@@ -574,7 +574,9 @@ PA_API pa_status pa_extend_tables(const pa_cache_desc* desc, int32_t batch, cons
  *   num_shared_pages int32 [batch].
  * The row's own entries there are overwritten (release them before).  Entries of
  * -1 are copied.  The row's length is the caller's to set, e.g. to
- * num_shared_pages[b] * page_size, where pa_extend_tables then goes on.  Rows with
+ * num_shared_pages[b] * page_size, where pa_extend_tables then goes on.  A page
+ * that is only partly filled is not shared: its holders would store their next
+ * tokens over each other's.  Rows with
  * a bad parent or count are skipped (PA_DEVERR_BAD_LENGTH).
  */
 PA_API pa_status pa_share_pages(const pa_cache_desc* desc, int32_t batch, const int32_t* parents,
@@ -601,7 +603,9 @@ PA_API pa_status pa_release_pages(const pa_cache_desc* desc, int32_t batch, cons
 
 /* pa_release_pages of the pages that a sliding window with sinks has left: those
  * whose tokens no token from position context_lens[b] on sees.  Entries behind
- * them stay where they are, so that positions still find their pages. */
+ * them stay where they are, so that positions still find their pages.  Every call
+ * looks at all entries from the sinks to the window: after each of a batch's
+ * steps most are -1 already, 4 bytes each to read. */
 PA_API pa_status pa_release_window_pages(const pa_cache_desc* desc, int32_t window, int32_t num_sinks, int32_t batch,
                                          const int32_t* context_lens, int32_t* block_tables,
                                          int32_t max_pages_per_seq, int32_t* ref_counts, int32_t* free_pages,
