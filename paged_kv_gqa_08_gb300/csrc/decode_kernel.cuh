@@ -318,8 +318,8 @@ PA_DEVINL void mma_consumer(const KParams& p, unsigned char* smem, uint64_t* ful
           float* dst = p.o_part + (slot * p.Hq + hq) * 128 + 2 * tq;
 #pragma unroll
           for (int j = 0; j < 16; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][0] * inv, o[j][1] * inv);
-          // (a sum that is no number may stay one for the merge)
-          if (tq == 0) p.lse_part[slot * p.Hq + hq] = (kRange || p.keep_nan ? l != 0.f : l > 0.f) ? m_run + log2f(l) : -INFINITY;
+          // (kRange: a sum that is no number stays one for the merge)
+          if (tq == 0) p.lse_part[slot * p.Hq + hq] = (kRange ? l != 0.f : l > 0.f) ? m_run + log2f(l) : -INFINITY;
         }
       }
       __syncwarp();
@@ -745,8 +745,7 @@ __global__ void __launch_bounds__(9 * 32) __maxnreg__((G <= 4 && !kUseMma<T, HD,
             for (int r = 0; r < NPR; r += 2)
               *reinterpret_cast<float4*>(dst + 2 * r) =
                   make_float4(o[g][r].x * inv, o[g][r].y * inv, o[g][r + 1].x * inv, o[g][r + 1].y * inv);
-            if (j == 0)
-              p.lse_part[slot * p.Hq + hq] = (kRange || p.keep_nan ? lg != 0.f : lg > 0.f) ? mg + log2f(lg) : -INFINITY;
+            if (j == 0) p.lse_part[slot * p.Hq + hq] = (kRange ? lg != 0.f : lg > 0.f) ? mg + log2f(lg) : -INFINITY;
           }
         }
       }

@@ -60,10 +60,6 @@ struct KParams {
   const int32_t* prefix_lens;
   int32_t n_groups, max_prefix, through_rep;
   int32_t per_request;  // a CTA for each request, whole (no merge)
-  // A part whose sum is no number (NaN among its scores) reaches the output: always
-  // in the kRange kernels, and where they would be launched but that the bounds leave
-  // nothing out.  (pa_decode's merge takes such a part for one without keys.)
-  int32_t keep_nan;
 };
 
 // Keys [lo, hi) of a request that a kRange kernel leaves out; hi = -1 when the
@@ -276,8 +272,13 @@ PA_DEVINL float merge_maximum(float M, bool nan) {
 // a lane owns HD/32 elements of the head, eight partials' loads are in flight
 // together, the first ones with their log-sum-exps'; the warps' sums meet in
 // shared memory and are added in a fixed order.
+//
+// A part with NaN among its scores reaches the output with kRange (its log-sum-exp
+// is NaN, too) and with kKeepNan: the plain kernel's parts, for the calls over
+// ranges of keys whose bounds leave nothing out.  (pa_decode takes such a part for
+// one without keys.)
 // ---------------------------------------------------------------------------
-template <typename T, int HD, bool kRange = false>
+template <typename T, int HD, bool kRange = false, bool kKeepNan = false>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KParams p) {
   constexpr int EL = HD / 32;  // elements per lane
   constexpr int NWARP = kMergeThreads / 32;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
     };
     load(k_begin);
     float M = -INFINITY;
-    bool nan = false;
+    [[maybe_unused]] bool nan = false;
     for (int k = lane; k < parts; k += 32)
       if (busy(c0 + k)) {
         const float x = lse_of(k);
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
       }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (kRange || p.keep_nan) M = merge_maximum(M, nan);
+    if constexpr (kRange) M = merge_maximum(M, nan);
+    if constexpr (kKeepNan) M = M == -INFINITY ? 0.f : M;
     if (M != -INFINITY) {
       for (int k0 = k_begin; k0 < k_end; k0 += 8) {
         if (k0 != k_begin) load(k0);
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const KPara
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float w = __shfl_sync(0xffffffffu, w_mine, i);
-          if (w != 0.f) {  // (an idle CTA wrote no partial)
+          // (an idle CTA wrote no partial; one of scores that are no numbers has weight 0, and NaN for its output)
+          if (w != 0.f || (kKeepNan && k0 + i < k_end && busy(c0 + k0 + i))) {
 #pragma unroll
             for (int e = 0; e < EL; ++e) acc[e] += w * v[i][e];
             wsum += w;
@@ -546,7 +549,6 @@ inline KParams decode_params(const pa_cache_desc& d, const DecodePlan& pl, const
   p.off_abort = pl.off_abort;
   p.off_cs = pl.off_cs;
   p.per_request = pl.per_request ? 1 : 0;
-  p.keep_nan = a.keep_nan ? 1 : 0;
   p.inline_plan = a.batch <= kInlinePlanMax || pl.per_request ? 1 : 0;
   p.p_row = pl.p_row;
   p.scale_log2 = a.scale * 1.4426950408889634f;

@@ -208,7 +208,7 @@ struct DecodeArgs {
   int64_t* slot_out = nullptr;
   // keys left out of the context (launch_decode_window)
   int32_t window = 0, sinks = 0;
-  bool keep_nan = false;  // parts whose sums are no numbers reach the output (KParams::keep_nan)
+  bool keep_nan = false;  // launch_decode: parts with scores that are no numbers reach the output
 };
 cudaError_t launch_decode(const pa_cache_desc& d, const DecodePlan& plan, const DecodeArgs& a,
                           cudaStream_t s);
