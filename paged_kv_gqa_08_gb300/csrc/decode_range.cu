@@ -30,6 +30,13 @@ cudaError_t plan_decode_window(const pa_cache_desc& d, int batch, int max_ctx, i
   //   64               7.8 -> 8.9       8.0 -> 9.7        14.5 -> 10.5        38.1 -> 38.2 (32: 10.3 -> 10.2)
   //   256              7.9 -> 23.9      9.0 -> 24.8       27.9 -> 25.7       104.7 -> 103.8
   // and fp32 (16 / 4 heads), slower by the key: 16 keys 6.8 -> 6.2, 64 keys 7.0 -> 14.0, 128 x 64 15.0 -> 15.5.
+  // With 64 dims two CTAs fit an SM (16 / 8 heads, bf16; 16 / 4, fp32):
+  //   bf16  16 keys  1 request 6.0 -> 4.4   128: 9.6 -> 5.7   600: 19.0 -> 13.4
+  //         64               7.1 -> 7.1       12.3 -> 8.9       27.9 -> 23.5
+  //         256              7.3 -> 16.8      20.6 -> 19.0      300: 34.3 -> 29.1
+  //   fp32  16 keys          7.1 -> 5.0        9.5 -> 6.1       18.2 -> 7.8
+  //         64               6.9 -> 9.1       12.0 -> 10.5      27.7 -> 18.0
+  //         256              7.3 -> 25.3      20.2 -> 27.0      300: 35.5 -> 30.8
   const int few = d.dtype == PA_F32 ? 16 : 32;
   out->per_request = (keys <= few || (keys <= 2 * few && batch >= 32) ||
                       (keys <= 256 && 3 * static_cast<int64_t>(batch) >= 2 * out->slots && batch <= out->slots)) &&
@@ -245,6 +252,9 @@ cudaError_t plan_shared(const pa_cache_desc& d, int n_groups, int batch, int max
     //                     64/1  1024  44.9 25.2    24/3  4096  62.0 27.9   128/7   256  31.5 26.9
     //   bf16 16/8 of 64    4/1  1024  11.3 13.1    16/1  1024  14.9 14.0    24/3  4096  33.5 20.6
     //   fp32 16/4 of 128  16/1  1024  19.0 35.4    16/1  4096  39.3 41.2    16/1 16384 123.1 115.4
+    // Of 55 more in 64 dims and fp32 (16/8, 32/8, 16/4; 4 to 128 requests in 1 to 7
+    // groups behind 256 to 16384 tokens) the rule takes one that is slower by more
+    // than 15% twice: bf16 16/8 of 64, 16/1 512 13.3 11.4; 32/8 of 64, 64/1 256 18.3 14.5.
     const double row = 2.0 * d.num_kv_heads * d.head_dim * elem_bytes(d.dtype);
     const double each_us = batch * static_cast<double>(max_prefix) * row / 6.0e6;
     const double units = std::ceil(static_cast<double>(batch) / n_groups * G / pl.unit_rows) * n_groups * d.num_kv_heads;
