@@ -475,7 +475,8 @@ PA_API pa_status pa_prefill_varlen_window(const pa_cache_desc* desc, int32_t win
  *                    least that many tokens; the others' first tokens are not
  *                    looked at.  A prefix may end inside a page: each request's
  *                    own page then holds its own tokens from there on.
- *   max_prefix_len   host upper bound on prefix_lens (0: none is shared).
+ *   max_prefix_len   host upper bound on prefix_lens (0: none is shared), at most
+ *                    max_context_len.
  *   scale            finite and > 0.
  *   other arguments  as pa_decode.  max_ctas bounds the partitions of the
  *                    prefixes' keys and those of the requests' own keys.
