@@ -15,7 +15,7 @@
 //          sums, K and V fragments by ldmatrix from swizzled rows.
 //   fp32   8 rows a warp (4 or 2 where that leaves no row over), a lane two keys of
 //          the tile for the scores (packed fp32 pairs) and head_dim / 32 dims for
-//          the output: fp32 throughout; with 128 dims the fp32 pipe is busy 44% of
+//          the output: fp32 throughout; with 128 dims the fp32 pipe is busy 43% of
 //          the time with 8 warps an SM, what its shared memory holds.
 // Rows that no query sees are zero in shared memory and have probability 0; they
 // are not read, and neither are table entries of pages that hold only such rows.
